@@ -73,7 +73,17 @@ typedef enum tria_dtype {
   /* q8_0 (ggml Q8_0 values, stored planar): int8 codes [row][head_dim] in the
    * data plane plus fp16 block scales [row][head_dim/32] in the scale plane;
    * value = scale of its 32-wide block x code ([Doc] §4 "--cache-type-k q8_0"). */
-  TRIA_Q8_0 = 2
+  TRIA_Q8_0 = 2,
+  /* q4_0 (ggml Q4_0 values, stored planar): 4-bit codes [row][head_dim/2]
+   * bytes in the data plane - byte j of a 32-wide block's 16 bytes holds the
+   * code of its dim j in the low half and of dim j + 16 in the high half -
+   * plus fp16 block scales [row][head_dim/32] in the scale plane; value =
+   * scale of its block x (code - 8). Cache planes only; keys of this type are
+   * scored by the fp32 scorer and evicted by the staged kernels. */
+  TRIA_Q4_0 = 3,
+  /* bfloat16: projections, queries and attention outputs (tria_rotate,
+   * tria_append_qkv, tria_attend); not a type of the cache. */
+  TRIA_BF16 = 4
 } tria_dtype;
 
 /* Calibration statistics of one model ([Doc] §2 "Calibration file (.tria)":
@@ -128,17 +138,17 @@ typedef struct tria_stats tria_stats;  /* opaque, device resident, immutable aft
  * seq_row0[s]; KV head g of it (one segment) starts at row
  * seq_row0[s] + g * capacity[s]. Row r of every plane is at byte offset
  * r * (row bytes of that plane). Row bytes: f32 4*hd, f16 2*hd, q8_0 data hd,
- * q8_0 scales hd/16; pos 4. Segments must not overlap. */
+ * q4_0 data hd/2, q8_0 / q4_0 scales hd/16; pos 4. Segments must not overlap. */
 typedef struct tria_layer_cache {
   int32_t n_seqs;             /* 1 .. TRIA_MAX_SEQS */
   int32_t n_kv_heads;
   int32_t head_dim;
-  tria_dtype k_type;          /* F32, F16 or Q8_0 */
-  tria_dtype v_type;          /* F32, F16 or Q8_0 */
+  tria_dtype k_type;          /* F32, F16, Q8_0 or Q4_0 */
+  tria_dtype v_type;          /* F32, F16, Q8_0 or Q4_0 */
   void* k;                    /* device, 16-byte aligned, rotated keys */
-  void* k_scale;              /* device, q8_0 keys only (else NULL) */
+  void* k_scale;              /* device, q8_0 / q4_0 keys only (else NULL) */
   void* v;                    /* device, 16-byte aligned */
-  void* v_scale;              /* device, q8_0 values only (else NULL) */
+  void* v_scale;              /* device, q8_0 / q4_0 values only (else NULL) */
   int32_t* pos;               /* device [rows] absolute token positions (moved with the rows) */
   int32_t* n_live;            /* device [n_seqs] live rows per sequence (all its KV heads);
                                  read at the start, set to the budget by compaction */
@@ -408,14 +418,14 @@ tria_status tria_shared_select(const float* combined, const tria_layer_cache* ca
  * n_live back.
  *   k_new        device, rows of k_type laid out [n_seqs][n_kv_heads][n_tokens]
  *                (row bytes as in the cache), 16-byte aligned
- *   k_scale_new  device, q8_0 keys only (else NULL): scale rows, same layout,
- *                2-byte aligned
+ *   k_scale_new  device, q8_0 / q4_0 keys only (else NULL): scale rows, same
+ *                layout, 2-byte aligned
  *   v_new, v_scale_new  likewise for the values
  *   pos_new      device int32 [n_seqs][n_tokens]: absolute positions, written
  *                to the new row of every KV head
  *   ws           a workspace of this cache (only its control words are used)
  * Host errors: TRIA_ERR_INVALID_ARG (null or misaligned pointer, n_tokens < 0,
- * a scale plane given for a non-q8_0 type or missing for q8_0),
+ * a scale plane given for a type without one or missing for q8_0 / q4_0),
  * TRIA_ERR_WORKSPACE. Device errors (tria_device_status): TRIA_ERR_DEVICE_ARG
  * when n_live is outside [0, capacity], TRIA_ERR_CAPACITY when n_live +
  * n_tokens > capacity; that sequence is left unchanged. n_tokens = 0 does
@@ -537,6 +547,165 @@ tria_status tria_calib_accumulate(const void* q, tria_dtype q_type, int32_t n_to
                                   int32_t head_dim, int32_t nonrot_dim, double* acc, void* stream);
 tria_status tria_calib_finish(const double* acc, int64_t n_tokens, int32_t n_q_heads, int32_t head_dim,
                               int32_t nonrot_dim, float* q_mean, float* q_abs, float* q_nonrot, void* stream);
+
+/* ---- Making the cache's rows and reading them --------------------------
+ * What a decode loop runs on both sides of the pass, per layer:
+ *   tria_append_qkv  the new tokens' projections: per-head norm and rotation
+ *                    of queries and keys, keys and values into the cache in
+ *                    its own types
+ *   tria_attend      the new tokens' attention over the cache as it stands,
+ *                    per-head rows and positions after evictions included
+ *   tria_evict       when the schedule says so
+ * tria_rotate is the norm and rotation alone. The rotation's frequencies are
+ * those that tria_load_stats takes as omega (tria_rope_frequencies), so that
+ * a model with a scaled rotation is scored with the rotation it runs. */
+
+/* Where the two members of rotary pair f < rot/2 lie in a head (rot =
+ * head_dim - nonrot_dim; the last nonrot_dim dims are never rotated). */
+typedef enum tria_rope_layout {
+  TRIA_ROPE_HALF = 0,          /* (f, f + rot/2): what the scorer reads */
+  TRIA_ROPE_INTERLEAVED = 1,   /* (2f, 2f + 1) */
+  /* read as (2f, 2f + 1), written as (f, f + rot/2): the same permutation of
+   * queries and keys, so logits do not change, and the cache's keys are in
+   * the order that the scorer reads */
+  TRIA_ROPE_INTERLEAVED_TO_HALF = 2
+} tria_rope_layout;
+
+/* How the frequencies theta^(-2f/rot) change for contexts longer than the
+ * model was trained on (orig_ctx tokens). */
+typedef enum tria_rope_scaling {
+  TRIA_ROPE_PLAIN = 0,
+  TRIA_ROPE_LINEAR = 1,  /* w / factor */
+  TRIA_ROPE_NTK = 2,     /* theta * factor^(rot / (rot - 2)) */
+  /* YaRN: unscaled above `high` turns over orig_ctx (0: 32), w / factor below
+   * `low` turns (0: 1), a linear ramp over the pair index between; rotated
+   * dims times mscale (0: 0.1 ln(factor) + 1) */
+  TRIA_ROPE_YARN = 3,
+  /* by wavelength: unscaled above `high` turns over orig_ctx (0: 4), w /
+   * factor below `low` (0: 1), blended linearly in the turns between */
+  TRIA_ROPE_BANDS = 4
+} tria_rope_scaling;
+
+typedef struct tria_rope_desc {
+  int32_t head_dim;          /* a multiple of 32, at most 256 */
+  int32_t nonrot_dim;        /* head_dim - nonrot_dim a multiple of 16 */
+  int32_t layout;            /* tria_rope_layout */
+  int32_t scaling;           /* tria_rope_scaling */
+  double theta;              /* > 1; not used when omega is given */
+  const double* omega;       /* host [rot/2] optional frequencies (TRIA_ROPE_PLAIN only) */
+  double factor;             /* >= 1 (every scaling but PLAIN) */
+  int64_t orig_ctx;          /* YARN, BANDS */
+  double low, high;          /* turns; 0: the default of the scaling */
+  double mscale;             /* factor on the rotated dims; 0: the default (1, or YaRN's) */
+} tria_rope_desc;
+
+typedef struct tria_rope tria_rope;   /* opaque, device resident, immutable after load */
+
+/* The scaled frequencies omega_out[rot/2] and the factor on the rotated dims.
+ * Host only. Errors as tria_load_rope. */
+tria_status tria_rope_frequencies(const tria_rope_desc* desc, double* omega_out, double* mscale_out);
+
+/* Builds the rotation on the device (allocates with cudaMalloc; synchronous).
+ * TRIA_ERR_UNSUPPORTED: head_dim outside the gate or rotary dims not a
+ * multiple of 16; TRIA_ERR_INVALID_ARG: bad layout, scaling, theta, factor,
+ * orig_ctx, low / high, mscale. *out is NULL on error. */
+tria_status tria_load_rope(const tria_rope_desc* desc, tria_rope** out);
+void tria_free_rope(tria_rope* rope);
+
+/* Heads of a batch of tokens: token t's n_heads heads of head_dim values lie
+ * consecutively at x + t * x_stride values, so that slices of a joint
+ * projection need no copy. Pointers 16-byte aligned, strides at least
+ * n_heads * head_dim and multiples of 16 bytes. out may be x (same stride);
+ * other overlaps are not allowed. */
+typedef struct tria_heads {
+  const void* x;             /* device */
+  void* out;                 /* device */
+  const float* norm;         /* device [head_dim], 16-byte aligned: y = x / sqrt(mean(x^2) + eps) * norm
+                                before the rotation; NULL: no norm */
+  int32_t n_heads;
+  int32_t pad;
+  int64_t x_stride, out_stride;
+} tria_heads;
+
+/* Norm and rotation of one or two sets of heads (queries and keys) in one
+ * pass. pos: device int32 [n_tokens] absolute positions. type: F32, F16 or
+ * BF16, of x and out; computed in fp32, rounded once. n_tokens = 0 does
+ * nothing. */
+tria_status tria_rotate(const tria_rope* rope, tria_dtype type, const tria_heads* parts, int32_t n_parts,
+                        int32_t n_tokens, const int32_t* pos, double eps, void* stream);
+
+/* One layer's projections of new tokens. Tokens tok0[s] .. tok0[s + 1] - 1
+ * (host int32 [n_seqs + 1], tok0[0] = 0, not descending) are sequence s's, in
+ * order; a sequence may have none. q / k / v as in tria_heads. */
+typedef struct tria_qkv {
+  tria_dtype type;           /* F32, F16 or BF16: q, k, v, q_out, k_held, v_held */
+  int32_t n_q_heads;         /* 0: no queries */
+  const void* q;
+  const void* k;             /* the cache's n_kv_heads heads */
+  const void* v;
+  void* q_out;               /* may be q (same stride) */
+  void* k_held;              /* optional: the values that the cache now holds for the new tokens, */
+  void* v_held;              /*   [n_tokens][n_kv_heads][head_dim], 16-byte aligned; NULL: not written */
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const float* q_norm;       /* as tria_heads.norm */
+  const float* k_norm;
+  double eps;
+  const int32_t* pos;        /* device [n_tokens] absolute positions */
+  const int32_t* tok0;       /* host [n_seqs + 1] */
+  const int32_t* n_before;   /* optional device [n_seqs]: live rows before the call, in the place of n_live
+                                (a step that is taken again, rejected draft tokens written over) */
+} tria_qkv;
+
+/* Norm and rotation of queries and keys, and the new rows behind the live
+ * ones: keys (rotated) and values quantised to the cache's types, positions,
+ * n_live = rows before + new rows, in one kernel.
+ *   q8_0: d = max |x| / 127, code = x / d rounded half away from zero
+ *   q4_0: d = m / -8 with m the first value of largest modulus, code =
+ *         min(15, floor(x / d + 8.5)); scales are stored as fp16(d)
+ * The host errors are INVALID_ARG, UNSUPPORTED (type), WORKSPACE (ws: a
+ * workspace of this cache, only its control words are used); device errors as
+ * tria_append, and a sequence with one is left unchanged (its queries are
+ * still rotated). rope: the cache's head_dim. Rows' positions must keep
+ * ascending. */
+tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_cache* cache, const tria_qkv* qkv, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Attention of new tokens over one layer's cache: query head h reads KV head
+ * h / (n_q_heads / n_kv_heads) of its sequence (at most 8 query heads per KV
+ * head). Token t at position p sees row r < n_live when pos[r] <= p and,
+ * with a window, p - pos[r] < window or r < sink:
+ *   out = sum_r softmax_r(scale q . K_r) V_r,   lse = ln sum_r exp(scale q . K_r)
+ * A token that sees no row gets out = 0 and lse = -inf. Rows that a token
+ * does not see never count, whatever they hold. Positions must ascend
+ * strictly with the rows of a segment (as appends and passes leave them). */
+typedef struct tria_attention {
+  tria_dtype type;           /* F32, F16 or BF16: q and out */
+  int32_t n_q_heads;
+  const void* q;             /* device, rotated queries: token t's heads at q + t * q_stride values */
+  void* out;                 /* device, likewise */
+  float* lse;                /* device [n_tokens][n_q_heads], optional */
+  int64_t q_stride, out_stride;   /* values; multiples of 16 bytes */
+  const int32_t* pos;        /* device [n_tokens] absolute positions */
+  const int32_t* tok0;       /* host [n_seqs + 1], as tria_qkv.tok0 */
+  double scale;              /* 0: 1 / sqrt(head_dim) */
+  int32_t window;            /* 0: no window */
+  int32_t sink;              /* first rows that stay visible outside the window */
+} tria_attention;
+
+/* Workspace bytes of tria_attend for these shapes (0 on invalid input). The
+ * workspace is zeroed once (tria_workspace_init) and not shared with other
+ * calls that overlap on the GPU, nor with the pass's workspace. */
+size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0);
+
+/* fp32 queries and caches with an fp32 plane are computed in fp32. Otherwise
+ * the products run on the tensor cores in fp16 with fp32 sums: queries as
+ * fp16 (bf16 ones scaled by a power of two first, which is undone), weights
+ * as fp16, statistics in fp32. Host errors: INVALID_ARG, UNSUPPORTED (type,
+ * group), WORKSPACE. Device errors (tria_device_status on ws):
+ * TRIA_ERR_DEVICE_ARG when n_live is outside [0, capacity]; that sequence's
+ * outputs are not written. */
+tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* attention, void* ws, size_t ws_bytes,
+                        void* stream);
 
 const char* tria_status_string(tria_status status);
 int32_t tria_version(void);

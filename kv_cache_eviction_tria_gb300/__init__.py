@@ -19,8 +19,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtria.so")
 
 TRIA_MAX_SEQS = 128
-F32, F16, Q8_0 = 0, 1, 2
-DTYPES = {"f32": F32, "f16": F16, "q8_0": Q8_0}
+F32, F16, Q8_0, Q4_0, BF16 = range(5)
+DTYPES = {"f32": F32, "f16": F16, "q8_0": Q8_0, "q4_0": Q4_0}   # types of the cache's planes
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1, "interleaved_to_half": 2}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 STATUS = {
     0: "TRIA_OK", 1: "TRIA_ERR_INVALID_ARG", 2: "TRIA_ERR_UNSUPPORTED", 3: "TRIA_ERR_BUDGET",
@@ -42,6 +44,8 @@ EXPORTS = (
     "tria_seq_prefill", "tria_seq_decode", "tria_schedule_plan", "tria_schedule_passed",
     "tria_shared_combine", "tria_shared_select",
     "tria_status_string", "tria_version", "tria_workspace_score_offset",
+    "tria_rope_frequencies", "tria_load_rope", "tria_free_rope", "tria_rotate", "tria_append_qkv",
+    "tria_attend_workspace_size", "tria_attend",
 )
 
 
@@ -98,6 +102,40 @@ class _SeqState(ctypes.Structure):
         ("capacity", ctypes.c_int64), ("rows", ctypes.c_int64), ("counted", ctypes.c_int64),
         ("prompt_rows", ctypes.c_int64), ("next_pos", ctypes.c_int64), ("decode_steps", ctypes.c_int64),
         ("passes", ctypes.c_int64), ("due", ctypes.c_int32), ("pad", ctypes.c_int32),
+    ]
+
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("nonrot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+        ("scaling", ctypes.c_int32), ("theta", ctypes.c_double), ("omega", ctypes.POINTER(ctypes.c_double)),
+        ("factor", ctypes.c_double), ("orig_ctx", ctypes.c_int64), ("low", ctypes.c_double),
+        ("high", ctypes.c_double), ("mscale", ctypes.c_double),
+    ]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("norm", ctypes.c_void_p), ("n_heads", ctypes.c_int32),
+        ("pad", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+    ]
+
+
+class _Qkv(ctypes.Structure):
+    _fields_ = [
+        ("type", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_held", ctypes.c_void_p), ("v_held", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+        ("eps", ctypes.c_double), ("pos", ctypes.c_void_p), ("tok0", ctypes.c_void_p), ("n_before", ctypes.c_void_p),
+    ]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [
+        ("type", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("pos", ctypes.c_void_p),
+        ("tok0", ctypes.c_void_p), ("scale", ctypes.c_double), ("window", ctypes.c_int32), ("sink", ctypes.c_int32),
     ]
 
 
@@ -185,6 +223,21 @@ def load_library(path: str | None = None):
     lib.tria_schedule_plan.restype = i32
     lib.tria_schedule_passed.argtypes = [sch_p, st_p, i32]
     lib.tria_schedule_passed.restype = i32
+    lib.tria_rope_frequencies.argtypes = [ctypes.POINTER(_RopeDesc), ctypes.POINTER(ctypes.c_double),
+                                          ctypes.POINTER(ctypes.c_double)]
+    lib.tria_rope_frequencies.restype = i32
+    lib.tria_load_rope.argtypes = [ctypes.POINTER(_RopeDesc), ctypes.POINTER(vp)]
+    lib.tria_load_rope.restype = i32
+    lib.tria_free_rope.argtypes = [vp]
+    lib.tria_free_rope.restype = None
+    lib.tria_rotate.argtypes = [vp, i32, ctypes.POINTER(_Heads), i32, i32, vp, ctypes.c_double, vp]
+    lib.tria_rotate.restype = i32
+    lib.tria_append_qkv.argtypes = [vp, ctypes.POINTER(_LayerCache), ctypes.POINTER(_Qkv), vp, sz, vp]
+    lib.tria_append_qkv.restype = i32
+    lib.tria_attend_workspace_size.argtypes = [ctypes.POINTER(_LayerCache), i32, vp]
+    lib.tria_attend_workspace_size.restype = sz
+    lib.tria_attend.argtypes = [ctypes.POINTER(_LayerCache), ctypes.POINTER(_Attention), vp, sz, vp]
+    lib.tria_attend.restype = i32
     lib.tria_status_string.argtypes = [i32]
     lib.tria_status_string.restype = ctypes.c_char_p
     lib.tria_workspace_score_offset.argtypes = [ctypes.POINTER(_LayerCache)]
@@ -573,6 +626,194 @@ def shared_select(combined, cache: LayerCache, policy: Policy, keep_out, *, ws, 
                                              wp, wb, _stream_handle(stream)), "tria_shared_select")
 
 
+# --------------------------------------------------------------------------- rows in, rows out
+
+def _rope_desc(head_dim, theta, nonrot_dim, layout, scaling, omega, factor, orig_ctx, low, high, mscale):
+    om_arr, om_p = _host_array(omega, np.float64, ctypes.c_double)
+    if om_arr is not None and om_arr.size != (head_dim - nonrot_dim) // 2:
+        raise ValueError("omega must hold (head_dim - nonrot_dim) / 2 frequencies")
+    desc = _RopeDesc(int(head_dim), int(nonrot_dim), ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], float(theta), om_p,
+                     float(factor), int(orig_ctx), float(low), float(high), float(mscale))
+    return desc, om_arr
+
+
+def rope_frequencies(*, head_dim: int, theta: float = 0.0, nonrot_dim: int = 0, layout: str = "half",
+                     scaling: str = "none", omega=None, factor: float = 1.0, orig_ctx: int = 0, low: float = 0.0,
+                     high: float = 0.0, mscale: float = 0.0):
+    """tria_rope_frequencies: (omega float64 [rot/2] as Stats takes it, the factor on the rotated dims). Host only."""
+    desc, _keep = _rope_desc(head_dim, theta, nonrot_dim, layout, scaling, omega, factor, orig_ctx, low, high, mscale)
+    out = np.zeros(max((head_dim - nonrot_dim) // 2, 1), np.float64)
+    m = ctypes.c_double()
+    _check(load_library().tria_rope_frequencies(ctypes.byref(desc), out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)),
+                                                ctypes.byref(m)), "tria_rope_frequencies")
+    return out, m.value
+
+
+class Rope:
+    """Device-resident rotation (``tria_load_rope``); arguments as rope_frequencies."""
+
+    def __init__(self, *, head_dim: int, theta: float = 0.0, nonrot_dim: int = 0, layout: str = "half",
+                 scaling: str = "none", omega=None, factor: float = 1.0, orig_ctx: int = 0, low: float = 0.0,
+                 high: float = 0.0, mscale: float = 0.0):
+        self.handle = ctypes.c_void_p()
+        desc, _keep = _rope_desc(head_dim, theta, nonrot_dim, layout, scaling, omega, factor, orig_ctx, low, high, mscale)
+        handle = ctypes.c_void_p()
+        _check(load_library().tria_load_rope(ctypes.byref(desc), ctypes.byref(handle)), "tria_load_rope")
+        self.handle = handle
+        self.head_dim, self.nonrot_dim = int(head_dim), int(nonrot_dim)
+
+    def close(self):
+        if self.handle:
+            load_library().tria_free_rope(self.handle)
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_ACT = None
+
+
+def _act_type(t) -> int:
+    global _ACT
+    if _ACT is None:
+        import torch
+        _ACT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    if t.dtype not in _ACT:
+        raise ValueError("activations must be float32, float16 or bfloat16")
+    return _ACT[t.dtype]
+
+
+def _rows3(t, name: str, n_tokens: int, head_dim: int, like=None):
+    """(address, values between tokens) of [tokens][heads][head_dim], heads of a token consecutive."""
+    sh, sd = t.shape, t.stride()
+    if len(sh) != 3 or sh[0] != n_tokens or sh[2] != head_dim or (like is not None and t.dtype != like):
+        raise ValueError(f"{name} must be [{n_tokens}][heads][{head_dim}] of the call's type")
+    if not t.is_cuda:
+        raise ValueError("device argument must be a CUDA tensor")
+    if n_tokens and (sd[2] != 1 or (sh[1] > 1 and sd[1] != head_dim)):
+        raise ValueError(f"{name}: the heads of a token must be consecutive")
+    return t.data_ptr(), sd[0] if n_tokens > 1 else max(sd[0], sh[1] * head_dim)
+
+
+def _pos32(pos, n_tokens: int) -> int:
+    if pos.numel() != n_tokens or pos.dtype.itemsize != 4 or pos.is_floating_point() or not pos.is_contiguous() or not pos.is_cuda:
+        raise ValueError(f"pos must be a contiguous int32 CUDA tensor of {n_tokens} positions")
+    return pos.data_ptr()
+
+
+def _vec32(t, n: int, name: str):
+    if t is None:
+        return None
+    if t.numel() != n or t.dtype.itemsize != 4 or not t.is_floating_point() or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} values")
+    return t.data_ptr()
+
+
+def _tokens0(tok0, n_seqs: int, n_tokens: int):
+    """Host token offsets [n_seqs + 1]; None: the same number of tokens for every sequence."""
+    if tok0 is None:
+        if n_tokens % n_seqs:
+            raise ValueError("tok0 is needed when the sequences' tokens differ")
+        return np.arange(n_seqs + 1, dtype=np.int32) * (n_tokens // n_seqs)
+    if not (isinstance(tok0, np.ndarray) and tok0.dtype == np.int32 and tok0.flags.c_contiguous):
+        tok0 = np.ascontiguousarray(np.asarray(tok0, dtype=np.int32))
+    if tok0.size != n_seqs + 1 or int(tok0[-1]) != n_tokens:
+        raise ValueError("tok0 must hold n_seqs + 1 offsets, the last one the number of tokens")
+    return tok0
+
+
+def rotate(rope: Rope, parts, pos, *, eps: float = 1e-6, stream=None):
+    """tria_rotate: per-head norm and rotation of one or two sets of heads. parts: [(x, out, norm or None)],
+    x / out [tokens][heads][head_dim] (slices of a joint projection are fine), norm float32 [head_dim];
+    pos int32 [tokens]."""
+    n = pos.numel()
+    structs = (_Heads * len(parts))()
+    kind = parts[0][0].dtype
+    for h, (x, out, norm) in zip(structs, parts):
+        h.x, h.x_stride = _rows3(x, "x", n, rope.head_dim, kind)
+        h.out, h.out_stride = _rows3(out, "out", n, rope.head_dim, kind)
+        if x.shape[1] != out.shape[1]:
+            raise ValueError("x and out must have the same heads")
+        h.norm, h.n_heads = _vec32(norm, rope.head_dim, "norm"), x.shape[1]
+    _check(load_library().tria_rotate(rope.handle, _act_type(parts[0][0]), structs, len(parts), n, _pos32(pos, n),
+                                      float(eps), _stream_handle(stream)), "tria_rotate")
+
+
+def append_qkv(rope: Rope, cache: LayerCache, q, k, v, pos, *, ws, q_out=None, tok0=None, n_before=None, q_norm=None,
+               k_norm=None, eps: float = 1e-6, k_held=None, v_held=None, stream=None):
+    """tria_append_qkv: norm and rotation of queries and keys, the new tokens' rows into the cache in its types,
+    n_live = rows before + new rows. q (or None) / k / v [tokens][heads][head_dim], pos int32 [tokens], tok0 host
+    offsets of the sequences' tokens (None: equally many each), n_before int32 [n_seqs] live rows before the call
+    (None: n_live); k_held / v_held receive the values that the cache now holds for the tokens."""
+    n, hd, n_seqs = pos.numel(), cache.head_dim, len(cache.seq_row0)
+    kind = k.dtype
+    a = _Qkv()
+    a.type = _act_type(k)
+    a.k, a.k_stride = _rows3(k, "k", n, hd, kind)
+    a.v, a.v_stride = _rows3(v, "v", n, hd, kind)
+    if k.shape[1] != cache.n_kv_heads or v.shape[1] != cache.n_kv_heads:
+        raise ValueError("k and v must have the cache's KV heads")
+    if q is not None:
+        if q_out is None or q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        a.q, a.q_stride = _rows3(q, "q", n, hd, kind)
+        a.q_out, a.q_out_stride = _rows3(q_out, "q_out", n, hd, kind)
+        a.n_q_heads = q.shape[1]
+    for name, t in (("k_held", k_held), ("v_held", v_held)):
+        if t is not None:
+            if not t.is_contiguous() or t.shape != k.shape:
+                raise ValueError(f"{name} must be contiguous [tokens][n_kv_heads][head_dim]")
+            setattr(a, name, _rows3(t, name, n, hd, kind)[0])
+    a.q_norm, a.k_norm, a.eps = _vec32(q_norm, hd, "q_norm"), _vec32(k_norm, hd, "k_norm"), float(eps)
+    a.pos = _pos32(pos, n)
+    tok0 = _tokens0(tok0, n_seqs, n)
+    a.tok0 = tok0.ctypes.data
+    if n_before is not None:
+        a.n_before = _pos32(n_before, n_seqs)
+    c = cache.c_struct()
+    wp, wb = _ws(ws)
+    _check(load_library().tria_append_qkv(rope.handle, ctypes.byref(c), ctypes.byref(a), wp, wb, _stream_handle(stream)),
+           "tria_append_qkv")
+
+
+def attend_workspace_size(cache: LayerCache, n_q_heads: int, tok0) -> int:
+    """tria_attend_workspace_size: tok0 host offsets of the sequences' tokens, or the tokens of every sequence."""
+    n_seqs = len(cache.seq_row0)
+    if np.ndim(tok0) == 0:
+        tok0 = np.arange(n_seqs + 1, dtype=np.int32) * int(tok0)
+    tok0 = _tokens0(tok0, n_seqs, int(tok0[-1]))
+    c = cache.c_struct()
+    n = load_library().tria_attend_workspace_size(ctypes.byref(c), n_q_heads, tok0.ctypes.data)
+    if n == 0:
+        raise TriaError(ERR_INVALID_ARG, "tria_attend_workspace_size")
+    return n
+
+
+def attend(cache: LayerCache, q, out, pos, *, ws, tok0=None, lse=None, scale: float = 0.0, window: int = 0, sink: int = 0,
+           stream=None):
+    """tria_attend: attention of new tokens over the cache. q / out [tokens][n_q_heads][head_dim], pos int32
+    [tokens], tok0 host offsets of the sequences' tokens (None: equally many each), lse float32
+    [tokens][n_q_heads] or None; scale 0: 1 / sqrt(head_dim); window 0: none; sink first rows stay visible."""
+    n, hd, n_seqs = pos.numel(), cache.head_dim, len(cache.seq_row0)
+    a = _Attention()
+    a.type, a.n_q_heads = _act_type(q), q.shape[1]
+    a.q, a.q_stride = _rows3(q, "q", n, hd)
+    a.out, a.out_stride = _rows3(out, "out", n, hd, q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    a.lse = _vec32(lse, n * q.shape[1], "lse")
+    a.pos = _pos32(pos, n)
+    tok0 = _tokens0(tok0, n_seqs, n)
+    a.tok0, a.scale, a.window, a.sink = tok0.ctypes.data, float(scale), int(window), int(sink)
+    c = cache.c_struct()
+    wp, wb = _ws(ws)
+    _check(load_library().tria_attend(ctypes.byref(c), ctypes.byref(a), wp, wb, _stream_handle(stream)), "tria_attend")
+
+
 # --------------------------------------------------------------------------- decode-loop lifecycle
 
 def append(cache: LayerCache, k_new, v_new, pos_new, *, ws, k_scale_new=None, v_scale_new=None, stream=None):
@@ -582,9 +823,9 @@ def append(cache: LayerCache, k_new, v_new, pos_new, *, ws, k_scale_new=None, v_
     if pos_new.dim() != 2 or pos_new.shape[0] != n_seqs or pos_new.dtype.itemsize != 4:
         raise ValueError("pos_new must be int32 [n_seqs][n_tokens]")
     n_tokens = int(pos_new.shape[-1])
-    row_bytes = {F32: 4, F16: 2, Q8_0: 1}
+    half_bytes = {F32: 8, F16: 4, Q8_0: 2, Q4_0: 1}
     for name, t, dt in (("k_new", k_new, cache.k_type), ("v_new", v_new, cache.v_type)):
-        want = n_seqs * cache.n_kv_heads * n_tokens * cache.head_dim * row_bytes[dt]
+        want = n_seqs * cache.n_kv_heads * n_tokens * cache.head_dim * half_bytes[dt] // 2
         if t is None or not t.is_contiguous() or t.numel() * t.element_size() != want:
             raise ValueError(f"{name} must be contiguous [n_seqs][n_kv_heads][n_tokens][head_dim] rows of the cache type")
     c = cache.c_struct()

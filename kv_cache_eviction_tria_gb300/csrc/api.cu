@@ -21,13 +21,17 @@ int row_bytes(tria_dtype t, int hd) {
     case TRIA_F32: return 4 * hd;
     case TRIA_F16: return 2 * hd;
     case TRIA_Q8_0: return hd;
+    case TRIA_Q4_0: return hd / 2;
+    case TRIA_BF16: break;   // not a type of the cache
   }
   return 0;
 }
 
-int scale_row_bytes(tria_dtype t, int hd) { return t == TRIA_Q8_0 ? hd / 16 : 0; }
+bool has_scales(int t) { return t == TRIA_Q8_0 || t == TRIA_Q4_0; }
 
-bool dtype_ok(int t) { return t == TRIA_F32 || t == TRIA_F16 || t == TRIA_Q8_0; }
+int scale_row_bytes(tria_dtype t, int hd) { return has_scales(t) ? hd / 16 : 0; }
+
+bool dtype_ok(int t) { return t == TRIA_F32 || t == TRIA_F16 || t == TRIA_Q8_0 || t == TRIA_Q4_0; }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -293,8 +297,8 @@ tria_status check_cache(const tria_layer_cache* c) {
   if (!c->k || !c->v || !c->pos || !c->n_live || !c->seq_row0 || !c->capacity) return TRIA_ERR_INVALID_ARG;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->pos, 4) || !aligned(c->n_live, 4))
     return TRIA_ERR_INVALID_ARG;
-  if ((c->k_type == TRIA_Q8_0) != (c->k_scale != nullptr)) return TRIA_ERR_INVALID_ARG;
-  if ((c->v_type == TRIA_Q8_0) != (c->v_scale != nullptr)) return TRIA_ERR_INVALID_ARG;
+  if (has_scales(c->k_type) != (c->k_scale != nullptr)) return TRIA_ERR_INVALID_ARG;
+  if (has_scales(c->v_type) != (c->v_scale != nullptr)) return TRIA_ERR_INVALID_ARG;
   if (c->k_scale && !aligned(c->k_scale, 16)) return TRIA_ERR_INVALID_ARG;
   if (c->v_scale && !aligned(c->v_scale, 16)) return TRIA_ERR_INVALID_ARG;
   // segments of different sequences must not overlap
@@ -487,8 +491,8 @@ extern "C" tria_status tria_append(const tria_layer_cache* cache, const void* k_
   if (n_tokens == 0) return TRIA_OK;
   if (!k_new || !v_new || !pos_new) return TRIA_ERR_INVALID_ARG;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(pos_new, 4)) return TRIA_ERR_INVALID_ARG;
-  if ((cache->k_type == TRIA_Q8_0) != (k_scale_new != nullptr)) return TRIA_ERR_INVALID_ARG;
-  if ((cache->v_type == TRIA_Q8_0) != (v_scale_new != nullptr)) return TRIA_ERR_INVALID_ARG;
+  if (has_scales(cache->k_type) != (k_scale_new != nullptr)) return TRIA_ERR_INVALID_ARG;
+  if (has_scales(cache->v_type) != (v_scale_new != nullptr)) return TRIA_ERR_INVALID_ARG;
   if ((k_scale_new && !aligned(k_scale_new, 2)) || (v_scale_new && !aligned(v_scale_new, 2)))
     return TRIA_ERR_INVALID_ARG;
   const Layout L = make_layout(cache, 0);

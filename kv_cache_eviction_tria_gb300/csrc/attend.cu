@@ -1,0 +1,378 @@
+// Attention over the cache (tria_attend): argument checks, the split of the
+// sequences between the kernels, and the fp32 kernel.
+//
+//   out(t, h) = sum_r softmax_r(scale q(t, h) . K_r) V_r   over the rows r of
+//   KV head h / G that token t sees: r < n_live, pos_r <= p_t and, with a
+//   window, p_t - pos_r < window or r < sink.
+//
+// Positions ascend with the rows, so a token sees a prefix (the sink) and one
+// run of rows; only those are read.
+//
+// The fp32 kernel (k_attend_plain) takes fp32 queries or fp32 planes of the
+// cache, where results are held to fp32 accuracy, and head_dims that the
+// tensor-core kernels are not built for. A CTA handles a unit of up to 8
+// columns (token x head of one KV head's group) or one part of its rows; each
+// warp walks 32-row tiles with its own running maximum and sum: logits with a
+// lane per row, the weighted sum with a lane per dim, tiles dequantised to
+// fp32 in shared memory. The FMAs of 8 columns bound it (16 per value read),
+// not memory.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "attend_internal.cuh"
+
+namespace tria {
+
+namespace {
+
+constexpr int kCols = 8;
+constexpr int kPlainWarps = 4;
+
+// value e of row `row` of a plane, as fp32
+__device__ __forceinline__ float plane_value(const uint8_t* data, const uint8_t* scale, int type, int64_t row, int hd, int e) {
+  switch (type) {
+    case TRIA_F32: return reinterpret_cast<const float*>(data)[row * hd + e];
+    case TRIA_F16: return __half2float(reinterpret_cast<const __half*>(data)[row * hd + e]);
+    case TRIA_Q8_0:
+      return (float)reinterpret_cast<const int8_t*>(data)[row * hd + e] *
+             __half2float(reinterpret_cast<const __half*>(scale)[row * (hd / 32) + e / 32]);
+  }
+  const int b = data[row * (hd / 2) + (e / 32) * 16 + (e & 15)];
+  const int c = (e & 16) ? b >> 4 : b & 15;
+  return (float)(c - 8) * __half2float(reinterpret_cast<const __half*>(scale)[row * (hd / 32) + e / 32]);
+}
+
+__global__ void __launch_bounds__(kPlainWarps * 32) k_attend_plain(const __grid_constant__ AttendArgs A) {
+  extern __shared__ float smem[];
+  const int hd = A.hd, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ts = hd + 1;
+  float* s_q = smem;                                           // [kCols][hd]
+  float* s_p = s_q + kCols * hd + warp * kCols * 32;           // [kCols][32] of this warp
+  float* s_tile = s_q + kCols * hd + kPlainWarps * kCols * 32 + warp * 32 * ts;   // [32][hd + 1]
+  __shared__ float s_m[kPlainWarps][kCols], s_l[kPlainWarps][kCols];
+  __shared__ int s_last;
+
+  const int part = blockIdx.x % A.split, y = blockIdx.x / A.split;
+  const int g = y % A.n_kv, unit = y / A.n_kv;
+  int lo_s = 0, hi_s = A.n_seqs - 1;
+  while (lo_s < hi_s) {
+    const int mid = (lo_s + hi_s + 1) >> 1;
+    if (A.seq[mid].unit0 <= unit) lo_s = mid; else hi_s = mid - 1;
+  }
+  const AttendSeq& S = A.seq[lo_s];
+  const int c0 = (unit - S.unit0) * kCols, ncol = min(kCols, S.t * A.G - c0);
+  const int n = *((volatile const int32_t*)(A.n_live + lo_s));
+  if (n < 0 || n > S.cap) {
+    if (threadIdx.x == 0) report(A.ctrl, TRIA_ERR_DEVICE_ARG, (uint32_t)lo_s);
+    return;
+  }
+  const int64_t row0 = S.row0 + (int64_t)g * S.cap;
+  const int32_t* rpos = A.cpos + row0;
+  int pcol[kCols];
+  int pmin = INT32_MAX, pmax = INT32_MIN;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    pcol[c] = c < ncol ? A.pos[S.tok0 + (c0 + c) / A.G] : INT32_MIN;
+    if (c < ncol) {
+      pmin = min(pmin, pcol[c]);
+      pmax = max(pmax, pcol[c]);
+    }
+  }
+  const int hi = rows_upto(rpos, n, pmax);
+  const int lo = A.window > 0 ? rows_upto(rpos, hi, (int64_t)pmin - A.window) : 0;
+  const int sr = min(A.sink, lo);
+  const int R = sr + hi - lo;
+  const int v0 = (int)((int64_t)part * R / A.split), v1 = (int)((int64_t)(part + 1) * R / A.split);
+
+  for (int i = threadIdx.x; i < kCols * hd; i += blockDim.x) {
+    const int c = i / hd, e = i - c * hd;
+    float x = 0.f;
+    if (c < ncol) {
+      const int col = c0 + c;
+      x = act_load(A.q, A.type, (int64_t)(S.tok0 + col / A.G) * A.q_stride + (int64_t)(g * A.G + col % A.G) * hd + e) * A.scale;
+    }
+    s_q[i] = x;
+  }
+  __syncthreads();
+
+  float m[kCols], l[kCols], o[kCols][8];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    m[c] = -INFINITY;
+    l[c] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[c][j] = 0.f;
+  }
+  for (int v = v0 + warp * 32; v < v1; v += kPlainWarps * 32) {
+    const int rows = min(32, v1 - v);
+    auto row_of = [&](int i) { return i < sr ? i : lo + i - sr; };
+    for (int r = 0; r < rows; ++r)
+      for (int e = lane; e < hd; e += 32) s_tile[r * ts + e] = plane_value(A.k, A.ks, A.k_type, row0 + row_of(v + r), hd, e);
+    __syncwarp();
+    float x[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) x[c] = 0.f;
+    const float* kr = s_tile + min(lane, rows - 1) * ts;
+    for (int e = 0; e < hd; ++e) {
+      const float kv = kr[e];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) x[c] = fmaf(s_q[c * hd + e], kv, x[c]);
+    }
+    const int my = row_of(v + min(lane, rows - 1));
+    const int p = rpos[my];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      const bool see = lane < rows && p <= pcol[c] && (A.window <= 0 || (int64_t)pcol[c] - p < A.window || my < A.sink);
+      float xc = see ? x[c] : -INFINITY, top = xc;
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const float mn = fmaxf(m[c], top);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float a = expf(m[c] - base), w = see ? expf(xc - base) : 0.f;
+      m[c] = mn;
+      float sum = w;
+#pragma unroll
+      for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      l[c] = l[c] * a + sum;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[c][j] *= a;
+      s_p[c * 32 + lane] = w;
+    }
+    __syncwarp();
+    for (int r = 0; r < rows; ++r)
+      for (int e = lane; e < hd; e += 32) s_tile[r * ts + e] = plane_value(A.v, A.vs, A.v_type, row0 + row_of(v + r), hd, e);
+    __syncwarp();
+    for (int r = 0; r < rows; ++r) {
+      float w[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) w[c] = s_p[c * 32 + r];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j * 32 >= hd) break;
+        const float x2 = s_tile[r * ts + j * 32 + lane];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)   // a hidden row's values never count, whatever they are
+          if (w[c] != 0.f) o[c][j] = fmaf(w[c], x2, o[c][j]);
+      }
+    }
+    __syncwarp();
+  }
+  // the warps' results, merged in warp order
+  if (lane == 0) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      s_m[warp][c] = m[c];
+      s_l[warp][c] = l[c];
+    }
+  }
+  __syncthreads();
+  float* s_o = smem + kCols * hd + kPlainWarps * kCols * 32;   // [kCols][hd]
+  float mt[kCols], lt[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    mt[c] = s_m[0][c];
+#pragma unroll
+    for (int w = 1; w < kPlainWarps; ++w) mt[c] = fmaxf(mt[c], s_m[w][c]);
+    const float base = mt[c] == -INFINITY ? 0.f : mt[c];
+    lt[c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPlainWarps; ++w) lt[c] += s_l[w][c] * expf(s_m[w][c] - base);
+  }
+  for (int w = 0; w < kPlainWarps; ++w) {
+    if (warp == w) {
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const float a = expf(m[c] - (mt[c] == -INFINITY ? 0.f : mt[c]));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j * 32 < hd) {
+            float* d = s_o + c * hd + j * 32 + lane;
+            *d = (w ? *d : 0.f) + o[c][j] * a;
+          }
+      }
+    }
+    __syncthreads();
+  }
+  auto write = [&](int c, int e, float val, float top, float sum) {
+    const int col = c0 + c, tok = S.tok0 + col / A.G, head = g * A.G + col % A.G;
+    act_store(A.out, A.type, (int64_t)tok * A.out_stride + (int64_t)head * hd + e, sum > 0.f || sum != sum ? val / sum : 0.f);
+    if (e == 0 && A.lse) A.lse[(int64_t)tok * A.nq + head] = top + logf(sum);
+  };
+  if (A.split == 1) {
+    for (int i = threadIdx.x; i < ncol * hd; i += blockDim.x) {
+      const int c = i / hd;
+      float top = mt[0], sum = lt[0];
+#pragma unroll
+      for (int k = 1; k < kCols; ++k)
+        if (c == k) {
+          top = mt[k];
+          sum = lt[k];
+        }
+      write(c, i - c * hd, s_o[i], top, sum);
+    }
+    return;
+  }
+  // a part of the unit: the last of its CTAs to arrive merges the parts in order
+  const int pstride = kCols * (hd + 2);
+  float* slot = A.part + ((int64_t)y * A.split + part) * pstride;
+  for (int i = threadIdx.x; i < kCols * hd; i += blockDim.x) slot[2 * kCols + i] = s_o[i];
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      slot[c] = mt[c];
+      slot[kCols + c] = lt[c];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(&A.count[y], 1u) == (uint32_t)A.split - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last) return;
+  const float* parts = A.part + (int64_t)y * A.split * pstride;
+  for (int i = threadIdx.x; i < ncol * hd; i += blockDim.x) {
+    const int c = i / hd;
+    float top = -INFINITY, sum = 0.f, val = 0.f;
+    for (int k = 0; k < A.split; ++k) top = fmaxf(top, __ldcg(parts + k * pstride + c));
+    const float base = top == -INFINITY ? 0.f : top;
+    for (int k = 0; k < A.split; ++k) {
+      const float a = expf(__ldcg(parts + k * pstride + c) - base);
+      sum = fmaf(__ldcg(parts + k * pstride + kCols + c), a, sum);
+      val = fmaf(__ldcg(parts + k * pstride + 2 * kCols + i), a, val);
+    }
+    write(c, i - c * hd, val, top, sum);
+  }
+  if (threadIdx.x == 0) A.count[y] = 0u;
+}
+
+// Parts of a unit: enough CTAs for the GPU, none under 128 rows of the
+// capacity.
+int plain_split(int64_t units, int cap_max) {
+  const int64_t want = (2 * 152 + units - 1) / std::max<int64_t>(units, 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)(cap_max + 127) / 128, 64}));
+}
+
+}  // namespace
+
+cudaError_t launch_attend_plain(AttendArgs& A, cudaStream_t st) {
+  const int64_t grid = (int64_t)A.units * A.n_kv * A.split;
+  if (grid == 0) return cudaSuccess;
+  const int smem = (kCols * A.hd + kPlainWarps * kCols * 32 + kPlainWarps * 32 * (A.hd + 1)) * (int)sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(k_attend_plain, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  k_attend_plain<<<(unsigned)grid, kPlainWarps * 32, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
+}  // namespace tria
+
+using namespace tria;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct AttendLayout {
+  size_t count, part, total;
+  int units, split;
+};
+
+AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0) {
+  AttendLayout L{};
+  int64_t units = 0;
+  int cap_max = 0;
+  for (int s = 0; s < c->n_seqs; ++s) {
+    units += ((int64_t)(tok0[s + 1] - tok0[s]) * G + kCols - 1) / kCols;
+    cap_max = std::max(cap_max, c->capacity[s]);
+  }
+  L.units = (int)units;
+  L.split = plain_split(units * c->n_kv_heads, cap_max);
+  L.count = up256(sizeof(Ctrl));
+  L.part = up256(L.count + sizeof(uint32_t) * (size_t)(units * c->n_kv_heads));
+  L.total = L.part + (L.split > 1 ? sizeof(float) * (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0);
+  L.total = up256(L.total);
+  return L;
+}
+
+tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const int32_t* tok0) {
+  tria_status r;
+  if ((r = check_cache(c)) != TRIA_OK) return r;
+  if (!tok0 || n_q_heads < 1) return TRIA_ERR_INVALID_ARG;
+  if (n_q_heads % c->n_kv_heads != 0 || n_q_heads / c->n_kv_heads > TRIA_MAX_GROUP) return TRIA_ERR_UNSUPPORTED;
+  return check_tokens(tok0, c->n_seqs);
+}
+
+}  // namespace
+
+extern "C" size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0) {
+  if (check_attend_shape(cache, n_q_heads, tok0) != TRIA_OK) return 0;
+  return attend_layout(cache, n_q_heads / cache->n_kv_heads, tok0).total;
+}
+
+extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* a, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  tria_status r;
+  if (!a) return TRIA_ERR_INVALID_ARG;
+  if ((r = check_attend_shape(cache, a->n_q_heads, a->tok0)) != TRIA_OK) return r;
+  if (!act_ok(a->type)) return TRIA_ERR_UNSUPPORTED;
+  if (a->window < 0 || a->sink < 0 || !(a->scale >= 0.0) || !isfinite(a->scale)) return TRIA_ERR_INVALID_ARG;
+  const int hd = cache->head_dim, nq = a->n_q_heads, n_tokens = a->tok0[cache->n_seqs];
+  const int size = a->type == TRIA_F32 ? 4 : 2;
+  if (n_tokens > 0) {
+    if (!a->q || !a->out || !a->pos || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->pos, 4) ||
+        (a->lse && !aligned(a->lse, 4)))
+      return TRIA_ERR_INVALID_ARG;
+    if (a->q_stride < (int64_t)nq * hd || a->out_stride < (int64_t)nq * hd || (a->q_stride * size) % 16 != 0 ||
+        (a->out_stride * size) % 16 != 0)
+      return TRIA_ERR_INVALID_ARG;
+  }
+  const int G = nq / cache->n_kv_heads;
+  const AttendLayout L = attend_layout(cache, G, a->tok0);
+  if (!ws || !aligned(ws, 256) || ws_bytes < L.total) return TRIA_ERR_WORKSPACE;
+  if (n_tokens == 0) return TRIA_OK;
+  AttendArgs A;
+  memset(&A, 0, sizeof(A));
+  A.q = a->q;
+  A.out = a->out;
+  A.lse = a->lse;
+  A.pos = a->pos;
+  A.q_stride = a->q_stride;
+  A.out_stride = a->out_stride;
+  A.k = (const uint8_t*)cache->k;
+  A.ks = (const uint8_t*)cache->k_scale;
+  A.v = (const uint8_t*)cache->v;
+  A.vs = (const uint8_t*)cache->v_scale;
+  A.cpos = cache->pos;
+  A.n_live = cache->n_live;
+  A.ctrl = (Ctrl*)ws;
+  A.count = (uint32_t*)((uint8_t*)ws + L.count);
+  A.part = (float*)((uint8_t*)ws + L.part);
+  A.n_seqs = cache->n_seqs;
+  A.n_kv = cache->n_kv_heads;
+  A.G = G;
+  A.hd = hd;
+  A.nq = nq;
+  A.type = a->type;
+  A.k_type = cache->k_type;
+  A.v_type = cache->v_type;
+  A.window = a->window;
+  A.sink = a->sink;
+  A.scale = (float)(a->scale != 0.0 ? a->scale : 1.0 / sqrt((double)hd));
+  int units = 0;
+  for (int s = 0; s < cache->n_seqs; ++s) {
+    A.seq[s].row0 = cache->seq_row0[s];
+    A.seq[s].cap = cache->capacity[s];
+    A.seq[s].tok0 = a->tok0[s];
+    A.seq[s].t = a->tok0[s + 1] - a->tok0[s];
+    A.seq[s].unit0 = units;
+    units += (A.seq[s].t * G + kCols - 1) / kCols;
+  }
+  A.units = units;
+  A.split = L.split;
+  return launch_attend_plain(A, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+}

@@ -1,0 +1,635 @@
+// Rotary positions with the per-head norm of queries and keys in the same
+// pass, alone (tria_rotate) or written into the cache in its own format
+// (tria_append_qkv).
+//
+// A head x of head_dim values, rot = head_dim - nonrot_dim of them rotated:
+//   y = x / sqrt(mean(x^2) + eps) * norm                  (when a norm is given)
+//   (a, b) -> m (a cos t - b sin t, a sin t + b cos t),   t = w_f * position
+// for pair f < rot/2 at (f, f + rot/2) or (2f, 2f + 1); m and w_f come from
+// the long-context scaling. Phases are taken as in the scorer: w_f / 2 pi as a
+// 64-bit fraction of a turn, so that position x turn mod 2^64 is the exact
+// fractional turn at any position and no floating-point range reduction is
+// needed.
+//
+// Layout: a lane owns 8 pairs of a head (16 values), head_dim / 16 lanes make
+// a head and a warp takes 32 / (lanes per head, rounded up to a power of two)
+// heads at once, so that both members of a pair sit in one lane, loads and
+// stores are 16 bytes wide and the norm is a shuffle reduction. A warp keeps
+// its lanes' sines and cosines over all the heads of a token that it handles:
+// sincospif costs about as much as moving ten heads.
+// Keys on their way into the cache go through shared memory once, because
+// their quantisation blocks (32 consecutive dims) do not line up with the
+// pairs. The kernels are bound by memory for prompts and by launch latency for
+// single tokens.
+#include <cuda_bf16.h>
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "attend_internal.cuh"
+
+namespace tria {
+
+namespace {
+
+constexpr int kRopeWarps = 8;
+constexpr int kPartDirect = 0, kPartKey = 1, kPartValue = 2;
+
+struct RopePart {
+  const void* x;
+  void* out;             // direct: rotated heads; key / value: the held values (may be NULL)
+  const float* norm;
+  int64_t x_stride, out_stride;   // values between tokens
+  int32_t heads;
+  int32_t groups;        // warps' worth of heads per token
+  int32_t kind;
+};
+
+struct RopeArgs {
+  RopePart part[3];
+  int32_t n_parts, n_tokens, groups;   // groups: of all parts, per token
+  int32_t per_warp;                    // groups a warp handles
+  int32_t hd, rot, layout, lanes;      // lanes: per head, a power of two
+  float eps, mscale;
+  const unsigned long long* turns;
+  const int32_t* pos;
+  // cache (append only)
+  uint8_t* k;
+  uint8_t* ks;
+  uint8_t* v;
+  uint8_t* vs;
+  int32_t* cpos;
+  int32_t* n_live;
+  const int32_t* n_before;
+  Ctrl* ctrl;
+  int32_t n_seqs, n_kv, k_type, v_type;
+  int64_t row0[kMaxSeqs];
+  int32_t cap[kMaxSeqs];
+  int32_t tok0[kMaxSeqs + 1];
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float* x) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__half>(const __half* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* x);
+template <>
+__device__ __forceinline__ void store8<float>(float* p, const float* x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <>
+__device__ __forceinline__ void store8<__half>(__half* p, const float* x) {
+  uint4 u;
+  __half2* h = reinterpret_cast<__half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = u;
+}
+template <>
+__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* x) {
+  uint4 u;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = u;
+}
+
+// 16 consecutive values (dims e0 .. e0 + 15) of a head into cache row `row` of
+// a plane; the lane next to it (lane ^ 1) holds the other half of the 32-wide
+// block. x becomes the values that the plane now stands for. All lanes of the
+// warp call it (`on`: this lane has values to store).
+__device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_t* scale, int64_t row, int hd, int e0,
+                                       bool on) {
+  if (type == TRIA_F32) {
+    if (on) {
+      float* d = reinterpret_cast<float*>(data) + row * hd + e0;
+      store8<float>(d, x);
+      store8<float>(d + 8, x + 8);
+    }
+    return;
+  }
+  if (type == TRIA_F16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __half2float(__float2half_rn(x[i]));
+    if (on) {
+      __half* d = reinterpret_cast<__half*>(data) + row * hd + e0;
+      store8<__half>(d, x);
+      store8<__half>(d + 8, x + 8);
+    }
+    return;
+  }
+  __half* sc = reinterpret_cast<__half*>(scale) + row * (hd / 32) + e0 / 32;
+  if (type == TRIA_Q8_0) {
+    float am = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) am = fmaxf(am, fabsf(x[i]));
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    const float d = __fdiv_rn(am, 127.f);
+    const __half dh = __float2half_rn(d);
+    const float ds = __half2float(dh);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float c = d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(x[i], d)), -127.f), 127.f) : 0.f;
+      w[i >> 2] |= ((uint32_t)(int)c & 255u) << (8 * (i & 3));
+      x[i] = c * ds;
+    }
+    if (on) {
+      *reinterpret_cast<uint4*>(data + row * hd + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (!(e0 & 16)) *sc = dh;
+    }
+    return;
+  }
+  // q4_0: scale = m / -8 with m the first value of largest modulus
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i)
+    if (fabsf(x[i]) > fabsf(m)) m = x[i];
+  const float other = __shfl_xor_sync(0xffffffffu, m, 1);
+  const bool upper = (e0 & 16) != 0;
+  const float lo = upper ? other : m, hi = upper ? m : other;
+  m = fabsf(hi) > fabsf(lo) ? hi : lo;
+  const float d = m * -0.125f;
+  const __half dh = __float2half_rn(d + 0.f);   // an all-zero block's scale is +0
+  const float ds = __half2float(dh);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float c = d != 0.f ? fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[i], d), 8.5f)), 0.f), 15.f) : 8.f;
+    w[i >> 2] |= (uint32_t)(int)c << (8 * (i & 3));
+    x[i] = (c - 8.f) * ds;
+  }
+  // byte j of a block: code j low, code j + 16 high; the lower lane writes bytes 0..7
+  const uint32_t r0 = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[2], 1);
+  const uint32_t r1 = __shfl_xor_sync(0xffffffffu, upper ? w[1] : w[3], 1);
+  uint2 o;
+  o.x = upper ? (r0 | (w[2] << 4)) : (w[0] | (r0 << 4));
+  o.y = upper ? (r1 | (w[3] << 4)) : (w[1] | (r1 << 4));
+  if (on) {
+    *reinterpret_cast<uint2*>(data + row * (hd / 2) + (e0 / 32) * 16 + (upper ? 8 : 0)) = o;
+    if (!upper) *sc = dh;
+  }
+}
+
+__device__ __forceinline__ uint32_t qkv_error(int n, int t, int cap) {
+  if (n < 0 || n > cap) return TRIA_ERR_DEVICE_ARG;
+  if ((int64_t)n + t > cap) return TRIA_ERR_CAPACITY;
+  return 0u;
+}
+
+template <typename T, bool kCache>
+__global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant__ RopeArgs A) {
+  extern __shared__ float s_key[];    // kCache: [warps][heads per warp][head_dim + 4]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hpw = 32 / A.lanes;                   // heads a warp takes at once
+  const int sub = lane / A.lanes, p = lane % A.lanes;
+  const bool on_dim = 16 * p < A.hd;
+  const int half = A.rot / 2, f0 = 8 * p;
+  const bool rotary = f0 < half;
+  const int warps_per_token = (A.groups + A.per_warp - 1) / A.per_warp;
+  const int64_t total = (int64_t)A.n_tokens * warps_per_token;
+  for (int64_t u = (int64_t)blockIdx.x * kRopeWarps + warp; u < total; u += (int64_t)gridDim.x * kRopeWarps) {
+    const int tok = (int)(u / warps_per_token);
+    const int g0 = (int)(u - (int64_t)tok * warps_per_token) * A.per_warp;
+    const int g1 = min(A.groups, g0 + A.per_warp);
+    const int position = A.pos[tok];
+    int seq = 0, row = 0;
+    bool row_ok = false;
+    if constexpr (kCache) {
+      int lo = 0, hi = A.n_seqs - 1;              // the last sequence whose first token is <= tok
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (A.tok0[mid] <= tok) lo = mid; else hi = mid - 1;
+      }
+      seq = lo;
+      const int t = A.tok0[seq + 1] - A.tok0[seq];
+      const int n = A.n_before ? A.n_before[seq] : *((volatile const int32_t*)(A.n_live + seq));
+      row_ok = qkv_error(n, t, A.cap[seq]) == 0u;
+      row = n + (tok - A.tok0[seq]);
+    }
+    float cs[8], sn[8];
+    bool have = false;
+    for (int g = g0; g < g1; ++g) {
+      int gi = g, pi = 0;
+      while (gi >= A.part[pi].groups) gi -= A.part[pi++].groups;
+      const RopePart& Q = A.part[pi];
+      const int head = gi * hpw + sub;
+      const bool on = on_dim && head < Q.heads;
+      const T* src = reinterpret_cast<const T*>(Q.x) + (int64_t)tok * Q.x_stride + (int64_t)head * A.hd;
+      float a[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a[i] = 0.f;
+      if (kCache && Q.kind == kPartValue) {
+        if (on) {
+          load8<T>(src + 16 * p, a);
+          load8<T>(src + 16 * p + 8, a + 8);
+        }
+        const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
+        hold16(a, A.v_type, A.v, A.vs, r, A.hd, 16 * p, on && row_ok);
+        if (on && row_ok && Q.out) {
+          T* o = reinterpret_cast<T*>(Q.out) + ((int64_t)tok * Q.heads + head) * A.hd + 16 * p;
+          store8<T>(o, a);
+          store8<T>(o + 8, a + 8);
+        }
+        continue;
+      }
+      // where the lane's pairs lie: a[0..7] the first members, a[8..15] the second ones
+      const bool inter = A.layout != TRIA_ROPE_HALF;
+      const int ea = inter ? 16 * p : (rotary ? f0 : f0 + half);
+      const int eb = inter ? 16 * p + 8 : ea + (rotary ? half : (A.hd - A.rot) / 2);
+      if (on) {
+        load8<T>(src + ea, a);
+        load8<T>(src + eb, a + 8);
+      }
+      if (Q.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(a[i], a[i], ss);
+        for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss / (float)A.hd + A.eps);
+        if (on) {
+          float w[16];
+          load8<float>(Q.norm + ea, w);
+          load8<float>(Q.norm + eb, w + 8);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) a[i] = a[i] * r * w[i];
+        }
+      } else {
+        __syncwarp();   // every lane has its values before any writes in place
+      }
+      const bool turn = rotary;
+      if (turn) {
+        if (!have) {
+          const unsigned long long x = (unsigned long long)(long long)position;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sincospif((float)(int)((A.turns[f0 + i] * x) >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+            sn[i] *= A.mscale;
+            cs[i] *= A.mscale;
+          }
+          have = true;
+        }
+        if (inter) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float re = a[2 * i], im = a[2 * i + 1];
+            a[2 * i] = re * cs[i] - im * sn[i];
+            a[2 * i + 1] = re * sn[i] + im * cs[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float re = a[i], im = a[8 + i];
+            a[i] = re * cs[i] - im * sn[i];
+            a[8 + i] = re * sn[i] + im * cs[i];
+          }
+        }
+      }
+      int oa = ea, ob = eb;
+      if (A.layout == TRIA_ROPE_INTERLEAVED_TO_HALF && rotary) {
+        float b[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          b[i] = a[2 * i];
+          b[8 + i] = a[2 * i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a[i] = b[i];
+        oa = f0;
+        ob = f0 + half;
+      }
+      if (!kCache || Q.kind == kPartDirect) {
+        if (on) {
+          T* o = reinterpret_cast<T*>(Q.out) + (int64_t)tok * Q.out_stride + (int64_t)head * A.hd;
+          store8<T>(o + oa, a);
+          store8<T>(o + ob, a + 8);
+        }
+        continue;
+      }
+      // a key on its way into the cache: to consecutive dims through shared memory
+      float* buf = s_key + (warp * hpw + sub) * (A.hd + 4);
+      __syncwarp();
+      if (on) {
+        store8<float>(buf + oa, a);
+        store8<float>(buf + ob, a + 8);
+      }
+      __syncwarp();
+      if (on) {
+        load8<float>(buf + 16 * p, a);
+        load8<float>(buf + 16 * p + 8, a + 8);
+      }
+      const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
+      hold16(a, A.k_type, A.k, A.ks, r, A.hd, 16 * p, on && row_ok);
+      if (on && row_ok) {
+        if (p == 0) A.cpos[r] = position;
+        if (Q.out) {
+          T* o = reinterpret_cast<T*>(Q.out) + ((int64_t)tok * Q.heads + head) * A.hd + 16 * p;
+          store8<T>(o, a);
+          store8<T>(o + 8, a + 8);
+        }
+      }
+    }
+  }
+  if constexpr (kCache) {
+    // n_live changes once nothing reads it any more: at once when the rows
+    // before the call are the caller's, else by the last CTA to finish
+    bool mine = blockIdx.x == 0;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    if (!A.n_before) {
+      __threadfence();
+      mine = atomicAdd(&A.ctrl->append_ticket, 1u) == gridDim.x - 1;
+      __threadfence();
+    }
+    if (!mine) return;
+    for (int s = 0; s < A.n_seqs; ++s) {
+      const int t = A.tok0[s + 1] - A.tok0[s];
+      const int n = A.n_before ? A.n_before[s] : *((volatile const int32_t*)(A.n_live + s));
+      const uint32_t e = qkv_error(n, t, A.cap[s]);
+      if (e)
+        report(A.ctrl, e, (uint32_t)s);
+      else
+        A.n_live[s] = n + t;
+    }
+    if (!A.n_before) atomicExch(&A.ctrl->append_ticket, 0u);
+  }
+}
+
+int ceil_pow2(int x) {
+  int p = 1;
+  while (p < x) p <<= 1;
+  return p;
+}
+
+template <typename T, bool kCache>
+cudaError_t launch_rope_t(const RopeArgs& A, cudaStream_t st) {
+  const int64_t wpt = (A.groups + A.per_warp - 1) / A.per_warp;
+  const int64_t want = ((int64_t)A.n_tokens * wpt + kRopeWarps - 1) / kRopeWarps;
+  const int grid = (int)std::min<int64_t>(std::max<int64_t>(want, 1), 16 * 152);
+  const int smem = kCache ? kRopeWarps * (32 / A.lanes) * (A.hd + 4) * (int)sizeof(float) : 0;
+  k_rope<T, kCache><<<grid, kRopeWarps * 32, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <bool kCache>
+cudaError_t launch_rope(const RopeArgs& A, int type, cudaStream_t st) {
+  if (type == TRIA_F32) return launch_rope_t<float, kCache>(A, st);
+  if (type == TRIA_F16) return launch_rope_t<__half, kCache>(A, st);
+  return launch_rope_t<__nv_bfloat16, kCache>(A, st);
+}
+
+// Work of a warp: one group of heads while the groups do not fill the GPU
+// (a single token then takes one short step on as many SMs as it has groups),
+// else as many groups of a token as leave about 64 warps for each SM, so that
+// the sines and cosines are shared.
+void finish_args(RopeArgs& A, const tria_rope* rope) {
+  A.hd = rope->head_dim;
+  A.rot = rope->head_dim - rope->nonrot_dim;
+  A.layout = rope->layout;
+  A.turns = rope->turns;
+  A.mscale = (float)rope->mscale;
+  A.lanes = ceil_pow2(A.hd / 16);
+  const int hpw = 32 / A.lanes;
+  A.groups = 0;
+  for (int i = 0; i < A.n_parts; ++i) {
+    A.part[i].groups = (A.part[i].heads + hpw - 1) / hpw;
+    A.groups += A.part[i].groups;
+  }
+  const int64_t total = (int64_t)A.n_tokens * A.groups;
+  A.per_warp = (int)std::min<int64_t>(std::max<int64_t>(total / (64 * 152), 1), A.groups);
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+int act_size(int type) { return type == TRIA_F32 ? 4 : 2; }
+
+tria_status check_heads(const void* x, int64_t stride, int heads, int hd, int type) {
+  if (!x || !aligned(x, 16) || heads < 1) return TRIA_ERR_INVALID_ARG;
+  if (stride < (int64_t)heads * hd || (stride * act_size(type)) % 16 != 0) return TRIA_ERR_INVALID_ARG;
+  return TRIA_OK;
+}
+
+tria_status check_rope_desc(const tria_rope_desc* d) {
+  if (!d) return TRIA_ERR_INVALID_ARG;
+  const int hd = d->head_dim, nr = d->nonrot_dim;
+  if (hd <= 0 || hd > TRIA_MAX_HEAD_DIM || hd % 32 != 0) return TRIA_ERR_UNSUPPORTED;
+  if (nr < 0 || nr >= hd) return TRIA_ERR_INVALID_ARG;
+  if ((hd - nr) % 16 != 0) return TRIA_ERR_UNSUPPORTED;
+  if (d->layout < TRIA_ROPE_HALF || d->layout > TRIA_ROPE_INTERLEAVED_TO_HALF) return TRIA_ERR_INVALID_ARG;
+  if (d->scaling < TRIA_ROPE_PLAIN || d->scaling > TRIA_ROPE_BANDS) return TRIA_ERR_INVALID_ARG;
+  if (d->omega) {
+    if (d->scaling != TRIA_ROPE_PLAIN) return TRIA_ERR_INVALID_ARG;
+  } else if (!(d->theta > 1.0) || !isfinite(d->theta)) {
+    return TRIA_ERR_INVALID_ARG;
+  }
+  if (d->scaling != TRIA_ROPE_PLAIN && (!(d->factor >= 1.0) || !isfinite(d->factor))) return TRIA_ERR_INVALID_ARG;
+  if ((d->scaling == TRIA_ROPE_YARN || d->scaling == TRIA_ROPE_BANDS) && d->orig_ctx < 1) return TRIA_ERR_INVALID_ARG;
+  if (!(d->mscale >= 0.0) || !isfinite(d->mscale)) return TRIA_ERR_INVALID_ARG;
+  const double hi = d->high == 0.0 ? (d->scaling == TRIA_ROPE_YARN ? 32.0 : 4.0) : d->high;
+  const double lo = d->low == 0.0 ? 1.0 : d->low;
+  if ((d->scaling == TRIA_ROPE_YARN || d->scaling == TRIA_ROPE_BANDS) && !(lo > 0.0 && hi > lo && isfinite(hi)))
+    return TRIA_ERR_INVALID_ARG;
+  if (d->omega)
+    for (int f = 0; f < (hd - nr) / 2; ++f)
+      if (!isfinite(d->omega[f])) return TRIA_ERR_INVALID_ARG;
+  return TRIA_OK;
+}
+
+void frequencies(const tria_rope_desc* d, double* w, double* mscale) {
+  const int rot = d->head_dim - d->nonrot_dim, n = rot / 2;
+  *mscale = d->mscale != 0.0 ? d->mscale : (d->scaling == TRIA_ROPE_YARN ? 0.1 * log(d->factor) + 1.0 : 1.0);
+  if (d->omega) {
+    for (int f = 0; f < n; ++f) w[f] = d->omega[f];
+    return;
+  }
+  double theta = d->theta;
+  if (d->scaling == TRIA_ROPE_NTK && rot > 2) theta *= pow(d->factor, (double)rot / (rot - 2));
+  const double two_pi = 2.0 * 3.14159265358979323846;
+  const double low = d->low == 0.0 ? 1.0 : d->low;
+  const double high = d->high == 0.0 ? (d->scaling == TRIA_ROPE_YARN ? 32.0 : 4.0) : d->high;
+  // pair index (real-valued) that turns `turns` times over the original context
+  auto pair_of = [&](double turns) { return rot * log((double)d->orig_ctx / (turns * two_pi)) / (2.0 * log(theta)); };
+  double lo = 0.0, hi = 0.0;
+  if (d->scaling == TRIA_ROPE_YARN) {
+    lo = std::max(floor(pair_of(high)), 0.0);
+    hi = std::min(ceil(pair_of(low)), (double)(rot - 1));
+  }
+  for (int f = 0; f < n; ++f) {
+    const double base = pow(theta, -2.0 * f / rot);
+    double keep = 1.0;      // share of the unscaled frequency
+    switch (d->scaling) {
+      case TRIA_ROPE_LINEAR: keep = 0.0; break;
+      case TRIA_ROPE_YARN: keep = 1.0 - std::min(std::max((f - lo) / std::max(hi - lo, 0.001), 0.0), 1.0); break;
+      case TRIA_ROPE_BANDS:
+        keep = std::min(std::max(((double)d->orig_ctx * base / two_pi - low) / (high - low), 0.0), 1.0);
+        break;
+      default: break;
+    }
+    const bool scaled = d->scaling != TRIA_ROPE_PLAIN && d->scaling != TRIA_ROPE_NTK;
+    w[f] = scaled ? base / d->factor * (1.0 - keep) + base * keep : base;
+  }
+}
+
+}  // namespace
+
+}  // namespace tria
+
+using namespace tria;
+
+extern "C" tria_status tria_rope_frequencies(const tria_rope_desc* desc, double* omega_out, double* mscale_out) {
+  const tria_status r = check_rope_desc(desc);
+  if (r != TRIA_OK) return r;
+  if (!omega_out || !mscale_out) return TRIA_ERR_INVALID_ARG;
+  frequencies(desc, omega_out, mscale_out);
+  return TRIA_OK;
+}
+
+extern "C" tria_status tria_load_rope(const tria_rope_desc* desc, tria_rope** out) {
+  if (!out) return TRIA_ERR_INVALID_ARG;
+  *out = nullptr;
+  const tria_status r = check_rope_desc(desc);
+  if (r != TRIA_OK) return r;
+  const int n = (desc->head_dim - desc->nonrot_dim) / 2;
+  double w[TRIA_MAX_HEAD_DIM / 2];
+  unsigned long long turns[TRIA_MAX_HEAD_DIM / 2];
+  double mscale;
+  frequencies(desc, w, &mscale);
+  for (int f = 0; f < n; ++f) {
+    double t = w[f] / (2.0 * 3.14159265358979323846);
+    t -= floor(t);
+    const double scaled = ldexp(t, 64);
+    turns[f] = scaled >= 18446744073709551615.0 ? 0ull : (unsigned long long)scaled;
+  }
+  tria_rope* h = new (std::nothrow) tria_rope;
+  if (!h) return TRIA_ERR_CUDA;
+  h->head_dim = desc->head_dim;
+  h->nonrot_dim = desc->nonrot_dim;
+  h->layout = desc->layout;
+  h->mscale = mscale;
+  h->turns = nullptr;
+  if (cudaMalloc((void**)&h->turns, sizeof(unsigned long long) * n) != cudaSuccess ||
+      cudaMemcpy(h->turns, turns, sizeof(unsigned long long) * n, cudaMemcpyHostToDevice) != cudaSuccess) {
+    if (h->turns) cudaFree(h->turns);
+    delete h;
+    return TRIA_ERR_CUDA;
+  }
+  *out = h;
+  return TRIA_OK;
+}
+
+extern "C" void tria_free_rope(tria_rope* rope) {
+  if (!rope) return;
+  cudaFree(rope->turns);
+  delete rope;
+}
+
+extern "C" tria_status tria_rotate(const tria_rope* rope, tria_dtype type, const tria_heads* parts, int32_t n_parts,
+                                   int32_t n_tokens, const int32_t* pos, double eps, void* stream) {
+  if (!rope || !parts || n_parts < 1 || n_parts > 2 || n_tokens < 0 || !(eps >= 0.0)) return TRIA_ERR_INVALID_ARG;
+  if (!act_ok(type)) return TRIA_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return TRIA_OK;
+  if (!pos || !aligned(pos, 4)) return TRIA_ERR_INVALID_ARG;
+  RopeArgs A;
+  memset(&A, 0, sizeof(A));
+  for (int i = 0; i < n_parts; ++i) {
+    const tria_heads& h = parts[i];
+    tria_status r;
+    if ((r = check_heads(h.x, h.x_stride, h.n_heads, rope->head_dim, type)) != TRIA_OK) return r;
+    if ((r = check_heads(h.out, h.out_stride, h.n_heads, rope->head_dim, type)) != TRIA_OK) return r;
+    if (h.norm && !aligned(h.norm, 16)) return TRIA_ERR_INVALID_ARG;
+    A.part[i] = RopePart{h.x, h.out, h.norm, h.x_stride, h.out_stride, h.n_heads, 0, kPartDirect};
+  }
+  A.n_parts = n_parts;
+  A.n_tokens = n_tokens;
+  A.eps = (float)eps;
+  A.pos = pos;
+  finish_args(A, rope);
+  return launch_rope<false>(A, type, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+}
+
+extern "C" tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_cache* cache, const tria_qkv* a,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  tria_status r;
+  if (!rope || !a) return TRIA_ERR_INVALID_ARG;
+  if ((r = check_cache(cache)) != TRIA_OK) return r;
+  if (rope->head_dim != cache->head_dim) return TRIA_ERR_INVALID_ARG;
+  if (!act_ok(a->type)) return TRIA_ERR_UNSUPPORTED;
+  if (!a->tok0 || a->n_q_heads < 0 || !(a->eps >= 0.0)) return TRIA_ERR_INVALID_ARG;
+  if ((r = check_tokens(a->tok0, cache->n_seqs)) != TRIA_OK) return r;
+  if (!ws || !aligned(ws, 256) || ws_bytes < sizeof(Ctrl)) return TRIA_ERR_WORKSPACE;
+  const int n_tokens = a->tok0[cache->n_seqs];
+  const int32_t* n_before = a->n_before == cache->n_live ? nullptr : a->n_before;
+  if (n_before && !aligned(n_before, 4)) return TRIA_ERR_INVALID_ARG;
+  if (n_tokens == 0 && !n_before) return TRIA_OK;
+  const int hd = cache->head_dim;
+  RopeArgs A;
+  memset(&A, 0, sizeof(A));
+  if (n_tokens > 0) {
+    if (!a->pos || !aligned(a->pos, 4)) return TRIA_ERR_INVALID_ARG;
+    if ((r = check_heads(a->k, a->k_stride, cache->n_kv_heads, hd, a->type)) != TRIA_OK) return r;
+    if ((r = check_heads(a->v, a->v_stride, cache->n_kv_heads, hd, a->type)) != TRIA_OK) return r;
+    if (a->n_q_heads > 0) {
+      if ((r = check_heads(a->q, a->q_stride, a->n_q_heads, hd, a->type)) != TRIA_OK) return r;
+      if ((r = check_heads(a->q_out, a->q_out_stride, a->n_q_heads, hd, a->type)) != TRIA_OK) return r;
+    }
+    if ((a->q_norm && !aligned(a->q_norm, 16)) || (a->k_norm && !aligned(a->k_norm, 16))) return TRIA_ERR_INVALID_ARG;
+    if ((a->k_held && !aligned(a->k_held, 16)) || (a->v_held && !aligned(a->v_held, 16))) return TRIA_ERR_INVALID_ARG;
+  }
+  const int kv = cache->n_kv_heads;
+  if (a->n_q_heads > 0)
+    A.part[A.n_parts++] = RopePart{a->q, a->q_out, a->q_norm, a->q_stride, a->q_out_stride, a->n_q_heads, 0, kPartDirect};
+  A.part[A.n_parts++] = RopePart{a->k, a->k_held, a->k_norm, a->k_stride, 0, kv, 0, kPartKey};
+  A.part[A.n_parts++] = RopePart{a->v, a->v_held, nullptr, a->v_stride, 0, kv, 0, kPartValue};
+  A.n_tokens = n_tokens;
+  A.eps = (float)a->eps;
+  A.pos = a->pos;
+  A.k = (uint8_t*)cache->k;
+  A.ks = (uint8_t*)cache->k_scale;
+  A.v = (uint8_t*)cache->v;
+  A.vs = (uint8_t*)cache->v_scale;
+  A.cpos = cache->pos;
+  A.n_live = cache->n_live;
+  A.n_before = n_before;
+  A.ctrl = (Ctrl*)ws;
+  A.n_seqs = cache->n_seqs;
+  A.n_kv = kv;
+  A.k_type = cache->k_type;
+  A.v_type = cache->v_type;
+  for (int s = 0; s < cache->n_seqs; ++s) {
+    A.row0[s] = cache->seq_row0[s];
+    A.cap[s] = cache->capacity[s];
+  }
+  for (int s = 0; s <= cache->n_seqs; ++s) A.tok0[s] = a->tok0[s];
+  finish_args(A, rope);
+  return launch_rope<true>(A, a->type, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+}

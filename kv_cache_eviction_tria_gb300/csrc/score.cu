@@ -107,6 +107,31 @@ struct Loader<TRIA_Q8_0, PPT> {
   }
 };
 
+// q4_0: byte j of a 32-wide block holds dim j in its low half, dim j + 16 in
+// its high half; PPT consecutive dims from a multiple of PPT share one half
+template <int PPT>
+struct Loader<TRIA_Q4_0, PPT> {
+  static __device__ __forceinline__ void half(const uint8_t* row, int e0, float2* x) {
+    const uint8_t* b = row + (e0 >> 5) * 16 + (e0 & 15);
+    const int shift = (e0 & 16) ? 4 : 0;
+    uint32_t u[PPT / 4];
+    if constexpr (PPT == 8) {
+      const uint2 w = *reinterpret_cast<const uint2*>(b);
+      u[0] = w.x;
+      u[1] = w.y;
+    } else {
+      u[0] = *reinterpret_cast<const uint32_t*>(b);
+    }
+#pragma unroll
+    for (int j = 0; j < PPT / 4; ++j) {
+      const uint32_t c = (u[j] >> shift) & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        x[2 * j + i] = make_float2((float)((int)((c >> (16 * i)) & 15u) - 8), (float)((int)((c >> (16 * i + 8)) & 15u) - 8));
+    }
+  }
+};
+
 // Transposed reduction of NV partial sums over the TPR lanes of a row group:
 // each step with more than one value left sends half of them to the partner
 // lane and keeps the other half; once a lane carries one value the rest is a
@@ -146,9 +171,9 @@ struct HeadReduce {
 // Compile-time shape of the row batch a lane accumulates before one reduction.
 template <int KT, int G, int TPR, int PPT>
 struct Batch {
-  static constexpr int kElem = KT == TRIA_F32 ? 4 : (KT == TRIA_F16 ? 2 : 1);
+  static constexpr int kElem2 = KT == TRIA_F32 ? 8 : (KT == TRIA_F16 ? 4 : (KT == TRIA_Q8_0 ? 2 : 1));   // bytes of 2 dims
   static constexpr int kRowsPerStep = 32 / TPR;
-  static constexpr int kRbMax = kElem * 2 * TPR * PPT;   // key bytes of the widest row
+  static constexpr int kRbMax = kElem2 * TPR * PPT;   // key bytes of the widest row
   static constexpr int kPieceRows = (kPieceBytes / kRbMax) > 64 ? 64 : (kPieceBytes / kRbMax);
   static constexpr int kSteps = (kPieceRows / kRowsPerStep) > 0 ? (kPieceRows / kRowsPerStep) : 1;
   static constexpr int kTarget = TPR / G > 0 ? TPR / G : 1;   // NV = TPR: no butterfly duplicates
@@ -425,7 +450,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) k_score(const __grid_constan
           const uint8_t* row = buf + (size_t)rr * P.k_rb;
           Loader<KT, PPT>::half(row, e_re, kr);
           Loader<KT, PPT>::half(row, e_im, ki);
-          if constexpr (KT == TRIA_Q8_0) {
+          if constexpr (KT == TRIA_Q8_0 || KT == TRIA_Q4_0) {
             const __half* sc = reinterpret_cast<const __half*>(P.ks + (size_t)(grow + rr) * P.ks_rb);
             const float d1 = __half2float(sc[e_re >> 5]);
             const float d2 = __half2float(sc[e_im >> 5]);
@@ -776,6 +801,7 @@ cudaError_t launch_score(const Pass& P, cudaStream_t st) {
     case TRIA_F32: return launch_score_k<TRIA_F32>(P, st);
     case TRIA_F16: return launch_score_k<TRIA_F16>(P, st);
     case TRIA_Q8_0: return launch_score_k<TRIA_Q8_0>(P, st);
+    case TRIA_Q4_0: return launch_score_k<TRIA_Q4_0>(P, st);
   }
   return cudaErrorInvalidValue;
 }
