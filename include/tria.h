@@ -676,7 +676,8 @@ tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_cache* cache
  * with a window, p - pos[r] < window or r < sink:
  *   out = sum_r softmax_r(scale q . K_r) V_r,   lse = ln sum_r exp(scale q . K_r)
  * A token that sees no row gets out = 0 and lse = -inf. Rows that a token
- * does not see never count, whatever they hold. Positions must ascend
+ * does not see never count, whatever they hold (one that sees a row with a
+ * non-finite scale has no defined result). Positions must ascend
  * strictly with the rows of a segment (as appends and passes leave them). */
 typedef struct tria_attention {
   tria_dtype type;           /* F32, F16 or BF16: q and out */

@@ -258,7 +258,7 @@ int plain_split(int64_t units, int cap_max) {
 
 }  // namespace
 
-cudaError_t launch_attend_plain(AttendArgs& A, cudaStream_t st) {
+cudaError_t launch_attend_plain(const AttendArgs& A, cudaStream_t st) {
   const int64_t grid = (int64_t)A.units * A.n_kv * A.split;
   if (grid == 0) return cudaSuccess;
   const int smem = (kCols * A.hd + kPlainWarps * kCols * 32 + kPlainWarps * 32 * (A.hd + 1)) * (int)sizeof(float);
@@ -277,26 +277,65 @@ namespace {
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Which kernel a sequence of t tokens takes.
+enum { kPathNone, kPathPlain, kPathStep };
+
+bool tensor_types(const tria_layer_cache* c, int type) {
+  return type != TRIA_F32 && c->k_type != TRIA_F32 && c->v_type != TRIA_F32 &&
+         (c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256);
+}
+
+constexpr int kStepCols = 16;
+
+int path_of(bool tensor, int t, int G) {
+  if (t == 0) return kPathNone;
+  return tensor && t * G <= kStepCols ? kPathStep : kPathPlain;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 152;
+  return sms;
+}
+
+// The kernels of a call run one after the other and share the arrival counters
+// and the space of the partial results. The layout covers every type of
+// queries.
 struct AttendLayout {
   size_t count, part, total;
-  int units, split;
+  int units, split, sms;
 };
 
 AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0) {
   AttendLayout L{};
   int64_t units = 0;
-  int cap_max = 0;
+  int cap_max = 0, cols = 0;
   for (int s = 0; s < c->n_seqs; ++s) {
-    units += ((int64_t)(tok0[s + 1] - tok0[s]) * G + kCols - 1) / kCols;
+    const int64_t x = (int64_t)(tok0[s + 1] - tok0[s]) * G;
+    units += (x + kCols - 1) / kCols;
+    if (x <= kStepCols) cols = std::max(cols, (int)x);
     cap_max = std::max(cap_max, c->capacity[s]);
   }
+  L.sms = sm_count();
   L.units = (int)units;
   L.split = plain_split(units * c->n_kv_heads, cap_max);
   L.count = up256(sizeof(Ctrl));
-  L.part = up256(L.count + sizeof(uint32_t) * (size_t)(units * c->n_kv_heads));
-  L.total = L.part + (L.split > 1 ? sizeof(float) * (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0);
-  L.total = up256(L.total);
+  L.part = up256(L.count + sizeof(uint32_t) * (size_t)(std::max<int64_t>(units, c->n_seqs) * c->n_kv_heads));
+  const size_t plain = L.split > 1 ? (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0;
+  const size_t step = (size_t)L.sms * 2 * (cols <= 8 ? 8 : 16) * (c->head_dim + 2);
+  L.total = up256(L.part + sizeof(float) * std::max(plain, step));
   return L;
+}
+
+cudaError_t launch_step(const AttendArgs& A, int cols, int workers, cudaStream_t st) {
+  using Fn = cudaError_t (*)(const AttendArgs&, int, int, cudaStream_t);
+  static constexpr Fn fn[3][3] = {
+      {launch_attend_step_f16_f16, launch_attend_step_f16_q8, launch_attend_step_f16_q4},
+      {launch_attend_step_q8_f16, launch_attend_step_q8_q8, launch_attend_step_q8_q4},
+      {launch_attend_step_q4_f16, launch_attend_step_q4_q8, launch_attend_step_q4_q4}};
+  static_assert(TRIA_F16 == 1 && TRIA_Q8_0 == 2 && TRIA_Q4_0 == 3, "table order");
+  return fn[A.k_type - 1][A.v_type - 1](A, cols, workers, st);
 }
 
 tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const int32_t* tok0) {
@@ -363,16 +402,40 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   A.window = a->window;
   A.sink = a->sink;
   A.scale = (float)(a->scale != 0.0 ? a->scale : 1.0 / sqrt((double)hd));
-  int units = 0;
+  const bool tensor = tensor_types(cache, a->type);
+  int units = 0, cols = 0;
+  bool plain = false, step = false;
   for (int s = 0; s < cache->n_seqs; ++s) {
     A.seq[s].row0 = cache->seq_row0[s];
     A.seq[s].cap = cache->capacity[s];
     A.seq[s].tok0 = a->tok0[s];
-    A.seq[s].t = a->tok0[s + 1] - a->tok0[s];
-    A.seq[s].unit0 = units;
-    units += (A.seq[s].t * G + kCols - 1) / kCols;
+    const int t = a->tok0[s + 1] - a->tok0[s], path = path_of(tensor, t, G);
+    plain = plain || path == kPathPlain;
+    if (path == kPathStep) {
+      step = true;
+      cols = std::max(cols, t * G);
+    }
   }
-  A.units = units;
-  A.split = L.split;
-  return launch_attend_plain(A, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+  // each kernel sees the sequences it takes, the others without tokens
+  auto take = [&](int path) {
+    units = 0;
+    for (int s = 0; s < cache->n_seqs; ++s) {
+      const int t = a->tok0[s + 1] - a->tok0[s];
+      A.seq[s].t = path_of(tensor, t, G) == path ? t : 0;
+      A.seq[s].unit0 = units;
+      units += (A.seq[s].t * G + kCols - 1) / kCols;
+    }
+    A.units = units;
+  };
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (step) {
+    take(kPathStep);
+    if (launch_step(A, cols, L.sms, st) != cudaSuccess) return TRIA_ERR_CUDA;
+  }
+  if (plain) {
+    take(kPathPlain);
+    A.split = L.split;
+    if (launch_attend_plain(A, st) != cudaSuccess) return TRIA_ERR_CUDA;
+  }
+  return TRIA_OK;
 }

@@ -60,8 +60,18 @@ struct AttendArgs {
   AttendSeq seq[kMaxSeqs];
 };
 
-// A call's sequences that one kernel takes; the launcher fills unit0 / units.
-cudaError_t launch_attend_plain(AttendArgs& A, cudaStream_t st);     // attend.cu
+// attend.cu
+cudaError_t launch_attend_plain(const AttendArgs& A, cudaStream_t st);
+// attend_step_*.cu: up to 16 columns (tokens x group) a sequence, one CTA per worker
+cudaError_t launch_attend_step_f16_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_f16_q8(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_f16_q4(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_q8_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_q8_q8(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_q8_q4(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_q4_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_q4_q8(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+cudaError_t launch_attend_step_q4_q4(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 
 __device__ __forceinline__ float act_load(const void* p, int type, int64_t i) {
   if (type == TRIA_F32) return reinterpret_cast<const float*>(p)[i];

@@ -1,0 +1,692 @@
+// Attention of a few new tokens over the cache (decode steps): a stream over
+// the visible rows, with the query columns of a KV head (token x head, up to 8
+// or 16) as one side of tensor-core products.
+//
+//   S = Q K^T    m16n8k16, M = columns, N = 8 rows, K = 16 dims
+//   O^T = V^T P  m16n8k16, M = 16 dims, N = 8 columns, K = 16 rows
+//
+// S leaves a thread with rows 2t, 2t + 1 of column gid, which is the B fragment
+// of the second product, so weights never leave their registers. fp16 rows are
+// read with ldmatrix; 8- and 4-bit codes become fp16 exactly by bit
+// insertion (1024 + code, minus the offset), with the dims of a step in the
+// order in which the codes lie in a word (the queries are loaded in the same
+// order). Key scales multiply the fp32 sum of each 32-wide block; value scales
+// multiply the fp32 weight before its one rounding to fp16, so that an
+// 8- or 4-bit cache costs no rounding that an fp16 one does not have.
+//
+// Weights are kept relative to M = max logit + E - 14, E the exponent of the
+// largest value scale so far: weight x scale then reaches up to 2^14 in fp16
+// whatever the size of the values, and the common factor cancels in O / l.
+//
+// Each warp streams its own tiles through a ring of cp.async stages without
+// block-wide barriers (padded rows: no bank conflicts). The tiles of all
+// units (sequence x KV head) are one list, cut into equal runs, one per CTA:
+// the live rows are known on the device alone, and ragged batches stay
+// balanced. A CTA's warps join through shared memory, CTAs that share a unit
+// through the workspace, the last one to arrive merging the parts in order.
+#pragma once
+
+#include <type_traits>
+
+#include "attend_internal.cuh"
+
+namespace tria {
+
+constexpr int kStepSmem = 220 * 1024;
+
+// TR: rows of a tile; SB: bytes of a stage
+template <int KT, int VT, int HD, int NT>
+struct StepShape {
+  static constexpr bool kKq = KT != TRIA_F16, kVq = VT != TRIA_F16;
+  static constexpr int kRb = KT == TRIA_F16 ? 2 * HD : (KT == TRIA_Q8_0 ? HD : HD / 2);
+  static constexpr int vRb = VT == TRIA_F16 ? 2 * HD : (VT == TRIA_Q8_0 ? HD : HD / 2);
+  static constexpr int kStride = kRb + 16, vStride = vRb + 16;
+  static constexpr int scRb = HD / 16;                     // block scales of a row
+  static constexpr int TR = (KT == TRIA_Q4_0 && VT == TRIA_Q4_0) ? 32 : 16;
+  static constexpr int oV = TR * kStride, oKs = oV + TR * vStride, oVs = oKs + (kKq ? TR * scRb : 0),
+                       oPos = oVs + (kVq ? TR * scRb : 0);
+  static constexpr int SB = (oPos + TR * 4 + 15) & ~15;
+  static constexpr int kStages = 3;
+  static constexpr int kOut = (HD * 8 * NT + 16 * NT) * 4;  // a warp's result in its stages
+  static constexpr int fit = kStepSmem / (SB * kStages);
+  static constexpr int kWarps = fit >= 12 ? 12 : (fit >= 8 ? 8 : 4);
+  static constexpr int kArea = SB * kStages;
+  static_assert(kArea >= kOut, "a warp's result fits its stages");
+  static_assert(kArea * kWarps <= kStepSmem, "stages fit shared memory");
+};
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// Codes of a word (q8_0: bytes 0 / 2 and 1 / 3; q4_0: the low halves of bytes
+// 0 / 2 and 1 / 3, then the high halves) as fp16 pairs, exactly: 0x6400 | u is
+// 1024 + u, and 1024 + 16 u for a code in the high half of a byte.
+__device__ __forceinline__ void q8_pairs(uint32_t w, uint32_t* h) {
+  h[0] = h2_sub((w & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);          // - 1152
+  h[1] = h2_sub(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+}
+__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t* h) {
+  const uint32_t u = w >> 8;
+  h[0] = h2_sub((w & 0x000F000Fu) | 0x64006400u, 0x64086408u);          // - 1032
+  h[1] = h2_sub((u & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+  h[2] = h2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);   // / 16 - 72
+  h[3] = h2_fma((u & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+}
+
+template <int KT, int VT, int HD, int NT>
+__global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
+    k_attend_step(const __grid_constant__ AttendArgs A) {
+  using H = StepShape<KT, VT, HD, NT>;
+  constexpr int TR = H::TR, NB = HD / 32, NG = TR / 8;     // blocks of a row, 8-row groups of a tile
+  constexpr int kWarps = H::kWarps, kStages = H::kStages, kCol = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_first[kMaxSeqs + 1];                    // first tile of each sequence's units
+  __shared__ int s_scan[40];
+  __shared__ int s_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
+
+  // ---- the tile list: units of a sequence have equally many tiles
+  auto span_of = [&](int s) {                              // positions between the sequence's tokens
+    int lo = INT32_MAX, hi = INT32_MIN;
+    for (int i = 0; i < A.seq[s].t; ++i) {
+      const int p = A.pos[A.seq[s].tok0 + i];
+      lo = min(lo, p);
+      hi = max(hi, p);
+    }
+    return (int64_t)hi - lo;
+  };
+  auto tiles_of = [&](int s, int n) {                      // tiles that a unit of sequence s may need
+    if (A.window <= 0) return max(1, (n + TR - 1) / TR);
+    const int64_t reach = min((int64_t)n, A.window + span_of(s));
+    return max(1, (min(A.sink, n) + TR - 1) / TR + (int)((reach + TR - 1) / TR));
+  };
+  {
+    int cnt = 0;
+    if ((int)threadIdx.x < A.n_seqs) {
+      const int s = threadIdx.x, n = *((volatile const int32_t*)(A.n_live + s));
+      if (A.seq[s].t > 0) {
+        if (n < 0 || n > A.seq[s].cap) {
+          if (blockIdx.x == 0) report(A.ctrl, TRIA_ERR_DEVICE_ARG, (uint32_t)s);
+        } else {
+          cnt = tiles_of(s, n) * A.n_kv;
+        }
+      }
+    }
+    int tot;
+    const int before = block_exclusive_scan(cnt, &tot, s_scan);
+    if ((int)threadIdx.x < A.n_seqs) s_first[threadIdx.x] = before;
+    if (threadIdx.x == 0) s_first[A.n_seqs] = tot;
+    __syncthreads();
+  }
+  const int64_t total = s_first[A.n_seqs];
+  if (total == 0) return;
+  const int64_t workers = min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps);
+  if ((int64_t)blockIdx.x >= workers) return;
+  auto start_of = [&](int64_t i) { return i * total / workers; };
+  const int64_t end = start_of(blockIdx.x + 1);
+  int64_t at = start_of(blockIdx.x);
+  const int64_t begin = at;
+
+  uint8_t* area = smem + warp * H::kArea;
+  const uint32_t area_u = smem_u32(area);
+
+  while (at < end) {
+    // ---- the unit
+    int lo_s = 0, hi_s = A.n_seqs - 1;
+    while (lo_s < hi_s) {
+      const int mid = (lo_s + hi_s + 1) >> 1;
+      if (s_first[mid] <= at) lo_s = mid; else hi_s = mid - 1;
+    }
+    const int s = lo_s;
+    const AttendSeq& S = A.seq[s];
+    const int per = (s_first[s + 1] - s_first[s]) / A.n_kv;
+    const int g = (int)((at - s_first[s]) / per);
+    const int64_t u0 = s_first[s] + (int64_t)g * per, u1 = u0 + per;   // the unit's tiles in the list
+    const int j0 = (int)(at - u0), j1 = (int)(min(end, u1) - u0);      // those of this CTA
+    const int n = *((volatile const int32_t*)(A.n_live + s));
+    const int64_t row0 = S.row0 + (int64_t)g * S.cap;
+    const int32_t* rpos = A.cpos + row0;
+    const int ncol = S.t * A.G;
+    int pmin = INT32_MAX, pmax = INT32_MIN;
+    for (int i = 0; i < S.t; ++i) {
+      const int p = A.pos[S.tok0 + i];
+      pmin = min(pmin, p);
+      pmax = max(pmax, p);
+    }
+    const bool newest = n == 0 || rpos[n - 1] <= pmin;     // every row is old enough for every token
+    int lo = 0, hi = n;
+    if (A.window > 0) {
+      hi = rows_upto(rpos, n, pmax);
+      lo = (int)max((int64_t)0, hi - (A.window + (int64_t)pmax - pmin));
+    }
+    const int sr = min(A.sink, lo), nt_sink = (sr + TR - 1) / TR;
+    const bool need_pos = A.window > 0 || !newest;
+    auto tile_row = [&](int j, int& rows) {                // first row and rows of tile j (rows <= 0: none)
+      if (j < nt_sink) {
+        rows = min(TR, sr - j * TR);
+        return j * TR;
+      }
+      const int r = lo + (j - nt_sink) * TR;
+      rows = min(TR, hi - r);
+      return r;
+    };
+    auto issue = [&](int j, int st) {
+      int rows;
+      const int r = tile_row(j, rows);
+      if (rows <= 0) return;
+      uint8_t* d = area + st * H::SB;
+      const uint8_t* ks = A.k + (row0 + r) * H::kRb;
+      const uint8_t* vsrc = A.v + (row0 + r) * H::vRb;
+      constexpr int kc = H::kRb / 16, vc = H::vRb / 16;    // 16-byte pieces of a row
+#pragma unroll
+      for (int i = 0; i < (TR * kc + 31) / 32; ++i) {
+        const int x = i * 32 + lane, rr = x / kc, c = x - rr * kc;
+        if (rr < rows) cp_async16(d + rr * H::kStride + c * 16, ks + rr * H::kRb + c * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < (TR * vc + 31) / 32; ++i) {
+        const int x = i * 32 + lane, rr = x / vc, c = x - rr * vc;
+        if (rr < rows) cp_async16(d + H::oV + rr * H::vStride + c * 16, vsrc + rr * H::vRb + c * 16);
+      }
+      auto copy_scales = [&](uint8_t* dst, const uint8_t* src) {
+        if constexpr (H::scRb == 16) cp_async16(dst, src);
+        else if constexpr (H::scRb == 8) cp_async8(dst, src);
+        else cp_async4(dst, src);
+      };
+      if (lane < rows) {
+        if constexpr (H::kKq) copy_scales(d + H::oKs + lane * H::scRb, A.ks + (row0 + r + lane) * H::scRb);
+        if constexpr (H::kVq) copy_scales(d + H::oVs + lane * H::scRb, A.vs + (row0 + r + lane) * H::scRb);
+        if (need_pos) cp_async4(d + H::oPos + lane * 4, rpos + r + lane);
+      }
+    };
+    // this warp's tiles: j0 + warp, + kWarps, ...
+    const int mine = j1 - j0 > warp ? (j1 - j0 - warp + kWarps - 1) / kWarps : 0;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < mine) issue(j0 + warp + i * kWarps, i);
+      cp_async_commit();
+    }
+
+    // ---- queries: A fragments, columns gid and gid + 8; qf: their exponent
+    uint32_t qa[NB * 2][2 * NT];                           // [step][column half * 2 ... k low, k high]
+    float qf[NT];
+    int pq[NT];
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      const int col = gid + 8 * h;
+      const bool on = col < ncol;
+      const int tok = S.tok0 + (on ? col / A.G : 0);
+      const int64_t qoff = (int64_t)tok * A.q_stride + (int64_t)(g * A.G + (on ? col % A.G : 0)) * HD;
+      pq[h] = on ? A.pos[tok] : INT32_MIN;
+      float x[NB][8];
+      float am = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        // dims of the thread: fp16 keys 2t, 2t+1, 8+2t, 9+2t (+16); codes 4t .. 4t+3 (+16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          int e;
+          if constexpr (H::kKq) e = 4 * t4 + (i & 3) + 16 * (i >> 2);
+          else e = 2 * t4 + (i & 1) + 8 * ((i >> 1) & 1) + 16 * (i >> 2);
+          x[b][i] = on ? act_load(A.q, A.type, qoff + 32 * b + e) : 0.f;
+          am = fmaxf(am, fabsf(x[b][i]));
+        }
+      }
+      qf[h] = A.scale * 1.4426950408889634f;
+      float f = 1.f;
+      if (A.type != TRIA_F16) {
+        // bf16's range into fp16's: times a power of two, undone in the logits
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        const int ex = (int)((__float_as_uint(am) >> 23) & 255u) - 127;
+        if (ex > -120 && ex < 120) {
+          f = __uint_as_float((uint32_t)(127 - ex) << 23);
+          qf[h] *= __uint_as_float((uint32_t)(127 + ex) << 23);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float* y = &x[b][4 * k];
+          if constexpr (H::kKq) {
+            qa[2 * b + k][2 * h] = pack_h2(y[0] * f, y[2] * f);
+            qa[2 * b + k][2 * h + 1] = pack_h2(y[1] * f, y[3] * f);
+          } else {
+            qa[2 * b + k][2 * h] = pack_h2(y[0] * f, y[1] * f);
+            qa[2 * b + k][2 * h + 1] = pack_h2(y[2] * f, y[3] * f);
+          }
+        }
+    }
+    auto qfrag = [&](int st, uint32_t* a) {
+      a[0] = qa[st][0];
+      a[2] = qa[st][1];
+      a[1] = NT == 2 ? qa[st][2 * NT - 2] : 0u;
+      a[3] = NT == 2 ? qa[st][2 * NT - 1] : 0u;
+    };
+
+    float M[NT], l[NT];
+    float o[HD / 16][NT][4];
+    int E = H::kVq ? -24 : 0;                              // exponent of the largest value scale so far
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      M[h] = -INFINITY;
+      l[h] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+      for (int h = 0; h < NT; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][h][c] = 0.f;
+
+    auto tile = [&](auto masked_c, uint32_t base, int r, int rows) {
+      constexpr bool kMasked = decltype(masked_c)::value;
+      // logits
+      float sc[NG][2 * NT];
+#pragma unroll
+      for (int gq = 0; gq < NG; ++gq) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (!H::kKq) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            uint32_t kf[4], a[4];
+            ldsm4(kf, base + (gq * 8 + (lane & 7)) * H::kStride + b * 64 + (lane >> 3) * 16);
+            qfrag(2 * b, a);
+            mma16816(acc, a, kf[0], kf[1]);
+            qfrag(2 * b + 1, a);
+            mma16816(acc, a, kf[2], kf[3]);
+          }
+        } else {
+          // scales of rows 2t, 2t + 1
+          const __half* kss = reinterpret_cast<const __half*>(area + (base - area_u) + H::oKs) + (gq * 8 + 2 * t4) * (H::scRb / 2);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t h[4], a[4];
+            if constexpr (KT == TRIA_Q8_0) {
+              const uint32_t w = base + (gq * 8 + gid) * H::kStride + b * 32 + t4 * 4;
+              q8_pairs(lds32(w), h);
+              q8_pairs(lds32(w + 16), h + 2);
+            } else {
+              q4_pairs(lds32(base + (gq * 8 + gid) * H::kStride + b * 16 + t4 * 4), h);
+            }
+            qfrag(2 * b, a);
+            mma16816(c, a, h[0], h[1]);
+            qfrag(2 * b + 1, a);
+            mma16816(c, a, h[2], h[3]);
+            const float s0 = __half2float(kss[b]), s1 = __half2float(kss[b + H::scRb / 2]);
+            acc[0] = fmaf(c[0], s0, acc[0]);
+            acc[1] = fmaf(c[1], s1, acc[1]);
+            if constexpr (NT == 2) {
+              acc[2] = fmaf(c[2], s0, acc[2]);
+              acc[3] = fmaf(c[3], s1, acc[3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+          sc[gq][2 * h] = acc[2 * h] * qf[h];
+          sc[gq][2 * h + 1] = acc[2 * h + 1] * qf[h];
+        }
+      }
+      const int32_t* tp = reinterpret_cast<const int32_t*>(area + (base - area_u) + H::oPos);
+      auto sees = [&](int row, int p) {                    // row of the tile, position of the query
+        if (row >= rows) return false;
+        if (!need_pos) return true;
+        const int q = tp[row];
+        return q <= p && (A.window <= 0 || (int64_t)p - q < A.window || r + row < A.sink);
+      };
+      if constexpr (kMasked) {
+#pragma unroll
+        for (int gq = 0; gq < NG; ++gq)
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (!sees(gq * 8 + 2 * t4 + c, pq[h])) sc[gq][2 * h + c] = -INFINITY;
+      }
+      // largest value scale
+      int En = E;
+      if constexpr (H::kVq) {
+        float big = 0.f;
+        const __half2* vss = reinterpret_cast<const __half2*>(area + (base - area_u) + H::oVs);
+        // all scales of the tile, spread over the lanes: TR * NB / 2 pairs
+#pragma unroll
+        for (int i = 0; i < (TR * NB / 2 + 31) / 32; ++i) {
+          const int x = i * 32 + lane;
+          bool on = x < TR * NB / 2;
+          if constexpr (kMasked) {                         // rows that some token sees
+            const int row = 2 * x / NB;
+            on = on && row < rows &&
+                 (!need_pos || (tp[row] <= pmax && (A.window <= 0 || (int64_t)pmin - tp[row] < A.window || r + row < A.sink)));
+          }
+          if (on) {
+            const float2 f = __half22float2(__habs2(vss[x]));
+            if (f.x <= 65504.f) big = fmaxf(big, f.x);
+            if (f.y <= 65504.f) big = fmaxf(big, f.y);
+          }
+        }
+        // the exponent above the largest one (its bits order like integers)
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+        En = max(E, min((int)(bits >> 23) - 126, 17));
+      }
+      // running reference
+      float Mn[NT];
+      bool grow = En != E;
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int gq = 0; gq < NG; ++gq) top = fmaxf(top, fmaxf(sc[gq][2 * h], sc[gq][2 * h + 1]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        Mn[h] = fmaxf(M[h] + (float)(En - E), top + (float)(En - 14));
+        grow = grow || Mn[h] > M[h];
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+          const float a = M[h] == -INFINITY ? 0.f : exp2_approx(M[h] - Mn[h]);
+          l[h] *= a;
+          M[h] = Mn[h];
+          // the accumulator's columns are 2t, 2t + 1
+          const float a0 = __shfl_sync(0xffffffffu, a, 8 * t4), a1 = __shfl_sync(0xffffffffu, a, 8 * t4 + 4);
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            o[i][h][0] *= a0;
+            o[i][h][1] *= a1;
+            o[i][h][2] *= a0;
+            o[i][h][3] *= a1;
+          }
+        }
+        E = En;
+      }
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+        const float mb = M[h] == -INFINITY ? 0.f : M[h];
+#pragma unroll
+        for (int gq = 0; gq < NG; ++gq)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float w = exp2_approx(sc[gq][2 * h + c] - mb);
+            sc[gq][2 * h + c] = w;
+            l[h] += w;
+          }
+      }
+      // weighted sum
+      if constexpr (!H::kVq) {
+#pragma unroll
+        for (int k = 0; k < TR / 16; ++k) {
+          uint32_t pb[NT][2];
+#pragma unroll
+          for (int h = 0; h < NT; ++h) {
+            pb[h][0] = pack_h2(sc[2 * k][2 * h], sc[2 * k][2 * h + 1]);
+            pb[h][1] = pack_h2(sc[2 * k + 1][2 * h], sc[2 * k + 1][2 * h + 1]);
+          }
+          const uint32_t va = base + H::oV + (k * 16 + (lane & 7) + ((lane >> 4) << 3)) * H::vStride + ((lane >> 3) & 1) * 16;
+          if constexpr (!kMasked) {
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+              uint32_t vf[4];
+              ldsm4t(vf, va + i * 32);
+#pragma unroll
+              for (int h = 0; h < NT; ++h) mma16816(o[i][h], vf, pb[h][0], pb[h][1]);
+            }
+          } else {
+            // token by token, rows that it does not see as zeros
+            for (int tk = 0; tk < S.t; ++tk) {
+              const int p = A.pos[S.tok0 + tk], rr = k * 16 + 2 * t4;
+              const uint32_t m0 = (sees(rr, p) ? 0xFFFFu : 0u) | (sees(rr + 1, p) ? 0xFFFF0000u : 0u);
+              const uint32_t m1 = (sees(rr + 8, p) ? 0xFFFFu : 0u) | (sees(rr + 9, p) ? 0xFFFF0000u : 0u);
+#pragma unroll
+              for (int i = 0; i < HD / 16; ++i) {
+                uint32_t vf[4];
+                ldsm4t(vf, va + i * 32);
+                vf[0] &= m0;
+                vf[1] &= m0;
+                vf[2] &= m1;
+                vf[3] &= m1;
+#pragma unroll
+                for (int h = 0; h < NT; ++h) {
+                  // junk that this token sees stays out of the other columns
+                  float c[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(c, vf, pb[h][0], pb[h][1]);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    if ((2 * t4 + (x & 1) + 8 * h) / A.G == tk) o[i][h][x] += c[x];
+                }
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < TR / 16; ++k) {
+          const __half* v0 = reinterpret_cast<const __half*>(area + (base - area_u) + H::oVs) + (k * 16 + 2 * t4) * (H::scRb / 2);
+          const uint32_t vr = base + H::oV + (k * 16 + 2 * t4) * H::vStride;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            uint32_t pb[NT][2];
+            float s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = __half2float(v0[b + ((i & 1) + 8 * (i >> 1)) * (H::scRb / 2)]);
+#pragma unroll
+            for (int h = 0; h < NT; ++h) {
+              float x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float w = sc[2 * k + (i >> 1)][2 * h + (i & 1)];
+                x[i] = kMasked && w == 0.f ? 0.f : w * s[i];   // a hidden row's scale never counts
+              }
+              pb[h][0] = pack_h2(x[0], x[1]);
+              pb[h][1] = pack_h2(x[2], x[3]);
+            }
+            uint32_t f0[4], f1[4];                         // rows 2t, 2t+1 and 2t+8, 2t+9 of four dims
+            if constexpr (VT == TRIA_Q8_0) {
+              const uint32_t w = vr + b * 32 + gid * 4;
+              const uint32_t w0 = lds32(w), w1 = lds32(w + H::vStride), w2 = lds32(w + 8 * H::vStride), w3 = lds32(w + 9 * H::vStride);
+              q8_pairs(__byte_perm(w0, w1, 0x5410), f0);
+              q8_pairs(__byte_perm(w0, w1, 0x7632), f0 + 2);
+              q8_pairs(__byte_perm(w2, w3, 0x5410), f1);
+              q8_pairs(__byte_perm(w2, w3, 0x7632), f1 + 2);
+            } else {
+              const uint32_t w = vr + b * 16 + gid * 2;
+              q4_pairs(lds16(w) | (lds16(w + H::vStride) << 16), f0);
+              q4_pairs(lds16(w + 8 * H::vStride) | (lds16(w + 9 * H::vStride) << 16), f1);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t vf[4] = {f0[2 * i], f0[2 * i + 1], f1[2 * i], f1[2 * i + 1]};
+#pragma unroll
+              for (int h = 0; h < NT; ++h) mma16816(o[2 * b + i][h], vf, pb[h][0], pb[h][1]);
+            }
+          }
+        }
+      }
+    };
+
+    for (int i = 0; i < mine; ++i) {
+      if (i + kStages - 1 < mine) issue(j0 + warp + (i + kStages - 1) * kWarps, (i + kStages - 1) % kStages);
+      cp_async_commit();
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      int rows;
+      const int r = tile_row(j0 + warp + i * kWarps, rows);
+      const uint32_t base = area_u + (i % kStages) * H::SB;
+      if (rows > 0) {
+        bool masked = rows < TR, skip = false;
+        if (need_pos) {
+          const int32_t* tp = reinterpret_cast<const int32_t*>(area + (i % kStages) * H::SB + H::oPos);
+          const int64_t first = tp[0], last = tp[rows - 1];
+          const bool in_sink = r + rows <= A.sink;
+          skip = first > pmax || (A.window > 0 && pmin - last >= A.window && r >= A.sink);
+          masked = masked || last > pmin || (A.window > 0 && pmax - first >= A.window && !in_sink);
+        }
+        if (!skip) {
+          if (masked) tile(std::true_type{}, base, r, rows);
+          else tile(std::false_type{}, base, r, rows);
+        }
+      }
+      __syncwarp();
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+
+    // ---- join the warps: M, l per column, O [column][dim]
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+    float* res = reinterpret_cast<float*>(area);
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      if (t4 == 0) {
+        res[gid + 8 * h] = M[h];
+        res[kCol + gid + 8 * h] = l[h];
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          int d;                                           // the dim of the accumulator's row
+          if constexpr (VT == TRIA_F16) d = 16 * i + gid + 8 * (c >> 1);
+          else if constexpr (VT == TRIA_Q8_0) d = 32 * (i >> 1) + 4 * gid + 2 * (i & 1) + (c >> 1);
+          else d = 32 * (i >> 1) + 16 * (i & 1) + 2 * gid + (c >> 1);
+          res[2 * kCol + (2 * t4 + (c & 1) + 8 * h) * HD + d] = o[i][h][c];
+        }
+    }
+    __syncthreads();
+    const bool whole = j0 == 0 && j1 == per;
+    const bool late = begin > u0;                          // the CTA's run starts inside the unit
+    float* slot = A.part + ((int64_t)blockIdx.x * 2 + (late ? 0 : 1)) * (kCol * (HD + 2));
+    auto write = [&](int col, int d, float val, float top, float sum) {
+      const int tok = S.tok0 + col / A.G, head = g * A.G + col % A.G;
+      act_store(A.out, A.type, (int64_t)tok * A.out_stride + (int64_t)head * HD + d, sum == 0.f ? 0.f : val / sum);
+      if (d == 0 && A.lse) A.lse[(int64_t)tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    };
+    for (int i = threadIdx.x; i < ncol * HD; i += kWarps * 32) {
+      const int col = i / HD, d = i - col * HD;
+      float top = -INFINITY, sum = 0.f, val = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, reinterpret_cast<const float*>(smem + w * H::kArea)[col]);
+      const float tb = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* x = reinterpret_cast<const float*>(smem + w * H::kArea);
+        const float f = exp2_approx(x[col] - tb);
+        sum = fmaf(x[kCol + col], f, sum);
+        val = fmaf(x[2 * kCol + i], f, val);
+      }
+      if (whole) {
+        write(col, d, val, top, sum);
+      } else {
+        slot[2 * kCol + i] = val;
+        if (d == 0) {
+          slot[col] = top;
+          slot[kCol + col] = sum;
+        }
+      }
+    }
+    __syncthreads();
+    if (!whole) {
+      // the CTAs of the unit: those whose runs meet [u0, u1)
+      const int64_t c0 = ((u0 + 1) * workers - 1) / total, c1 = (u1 * workers - 1) / total;
+      uint32_t* count = A.count + (int64_t)s * A.n_kv + g;
+      if (threadIdx.x == 0) {
+        __threadfence();
+        s_flag = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_flag) {
+        for (int i = threadIdx.x; i < ncol * HD; i += kWarps * 32) {
+          const int col = i / HD;
+          float top = -INFINITY, sum = 0.f, val = 0.f;
+          auto part_of = [&](int64_t c) { return A.part + (c * 2 + (start_of(c) > u0 ? 0 : 1)) * (kCol * (HD + 2)); };
+          for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part_of(c) + col));
+          const float tb = top == -INFINITY ? 0.f : top;
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float* x = part_of(c);
+            const float f = exp2_approx(__ldcg(x + col) - tb);
+            sum = fmaf(__ldcg(x + kCol + col), f, sum);
+            val = fmaf(__ldcg(x + 2 * kCol + i), f, val);
+          }
+          write(col, i - col * HD, val, top, sum);
+        }
+        if (threadIdx.x == 0) *count = 0u;
+      }
+      __syncthreads();
+    }
+    at = min(end, u1);
+  }
+}
+
+template <int KT, int VT, int HD, int NT>
+cudaError_t launch_attend_step_t(const AttendArgs& A, int workers, cudaStream_t st) {
+  using H = StepShape<KT, VT, HD, NT>;
+  auto kern = k_attend_step<KT, VT, HD, NT>;
+  const int smem = H::kArea * H::kWarps;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<workers, H::kWarps * 32, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <int KT, int VT>
+cudaError_t launch_attend_step_kv(const AttendArgs& A, int cols, int workers, cudaStream_t st) {
+  const bool one = cols <= 8;
+  switch (A.hd) {
+    case 64: return one ? launch_attend_step_t<KT, VT, 64, 1>(A, workers, st) : launch_attend_step_t<KT, VT, 64, 2>(A, workers, st);
+    case 128: return one ? launch_attend_step_t<KT, VT, 128, 1>(A, workers, st) : launch_attend_step_t<KT, VT, 128, 2>(A, workers, st);
+    case 256: return one ? launch_attend_step_t<KT, VT, 256, 1>(A, workers, st) : launch_attend_step_t<KT, VT, 256, 2>(A, workers, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace tria

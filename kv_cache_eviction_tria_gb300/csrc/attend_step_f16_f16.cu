@@ -1,0 +1,10 @@
+// Attention of decode steps over f16 keys and f16 values.
+#include "attend_step.cuh"
+
+namespace tria {
+
+cudaError_t launch_attend_step_f16_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st) {
+  return launch_attend_step_kv<TRIA_F16, TRIA_F16>(A, cols, workers, st);
+}
+
+}  // namespace tria

@@ -117,12 +117,21 @@ def check_attend(got, got_lse, want, kind, tensor, rows, hd, q_exact=True, k_exa
     rel = np.expm1(2 * dS) + (rows / 32 + 64) * U24 + (2 * U16 if tensor else 0.0)
     tol = rel[..., None] * sum_abs + (rows * U24 * vmax)[..., None] * (1.0 if tensor else 0.0)
     tol = tol + HALF_STEP[kind] * (np.abs(out) + tol) + 2.0 ** -24
-    blown = ~np.isfinite(out)                 # a token that sees a junk row has no finite value
-    assert np.array_equal(blown, ~np.isfinite(got))
+    # A token that sees a junk row has no finite value. Over quantised keys it has no defined one either: a block's
+    # sum of codes times an infinite scale is an infinity of the sum's sign, possibly -inf (weight 0), where the sum
+    # of products has infinities of both signs.
+    blown = ~np.isfinite(out)
+    if k_exact:
+        assert np.array_equal(blown, ~np.isfinite(got))
+    else:
+        assert np.isfinite(got[~blown]).all()
     bad = np.where(blown, False, np.abs(got - out) > tol)
     assert not bad.any(), f"{bad.sum()} of {bad.size} outputs off, worst {np.max(np.abs(got - out) / tol):.2f} tolerances"
     if got_lse is not None:
         seen = np.isfinite(lse)
-        assert np.array_equal(seen, np.isfinite(got_lse)) and np.array_equal(got_lse == -np.inf, lse == -np.inf)
+        if k_exact:
+            assert np.array_equal(seen, np.isfinite(got_lse)) and np.array_equal(got_lse == -np.inf, lse == -np.inf)
+        else:
+            assert np.isfinite(got_lse[seen]).all() and np.all(got_lse[lse == -np.inf] == -np.inf)
         tl = dS + (rows / 32 + 64) * U24 + U24 * 4 * np.abs(np.where(seen, lse, 0))
         assert np.all(np.abs(got_lse - lse)[seen] <= tl[seen]), np.max((np.abs(got_lse - lse) / tl)[seen])
