@@ -278,7 +278,7 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Which kernel a sequence of t tokens takes.
-enum { kPathNone, kPathPlain, kPathStep };
+enum { kPathNone, kPathPlain, kPathStep, kPathPrompt };
 
 bool tensor_types(const tria_layer_cache* c, int type) {
   return type != TRIA_F32 && c->k_type != TRIA_F32 && c->v_type != TRIA_F32 &&
@@ -289,7 +289,8 @@ constexpr int kStepCols = 16;
 
 int path_of(bool tensor, int t, int G) {
   if (t == 0) return kPathNone;
-  return tensor && t * G <= kStepCols ? kPathStep : kPathPlain;
+  if (!tensor) return kPathPlain;
+  return t * G <= kStepCols ? kPathStep : kPathPrompt;
 }
 
 int sm_count() {
@@ -304,17 +305,36 @@ int sm_count() {
 // queries.
 struct AttendLayout {
   size_t count, part, total;
-  int units, split, sms;
+  int units, split, prompt_split, sms;
 };
+
+// Parts of a unit of a prompt: as many as make the last wave of CTAs (one per
+// SM) full, each part costing a share of a fixed start and of the merge; none
+// under 512 rows of the capacity.
+int prompt_split(int64_t units, int cap_max, int sms) {
+  if (units == 0) return 1;
+  int best = 1;
+  double least = 1e30;
+  for (int k = 1; k <= 16 && (k == 1 || (int64_t)k * 512 <= cap_max); ++k) {
+    if (k > 1 && units * k > 2 * sms) break;
+    const double t = (double)((units * k + sms - 1) / sms) / k + 0.02 * k;
+    if (t < least - 1e-9) {
+      least = t;
+      best = k;
+    }
+  }
+  return best;
+}
 
 AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0) {
   AttendLayout L{};
-  int64_t units = 0;
+  int64_t units = 0, prompts = 0;
   int cap_max = 0, cols = 0;
   for (int s = 0; s < c->n_seqs; ++s) {
     const int64_t x = (int64_t)(tok0[s + 1] - tok0[s]) * G;
     units += (x + kCols - 1) / kCols;
     if (x <= kStepCols) cols = std::max(cols, (int)x);
+    else prompts += (x + prompt_cols(c->head_dim) - 1) / prompt_cols(c->head_dim);
     cap_max = std::max(cap_max, c->capacity[s]);
   }
   L.sms = sm_count();
@@ -324,7 +344,10 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   L.part = up256(L.count + sizeof(uint32_t) * (size_t)(std::max<int64_t>(units, c->n_seqs) * c->n_kv_heads));
   const size_t plain = L.split > 1 ? (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0;
   const size_t step = (size_t)L.sms * 2 * (cols <= 8 ? 8 : 16) * (c->head_dim + 2);
-  L.total = up256(L.part + sizeof(float) * std::max(plain, step));
+  L.prompt_split = prompt_split(prompts * c->n_kv_heads, cap_max, L.sms);
+  const size_t prompt = L.prompt_split > 1
+      ? (size_t)(prompts * c->n_kv_heads) * L.prompt_split * prompt_cols(c->head_dim) * (c->head_dim + 2) : 0;
+  L.total = up256(L.part + sizeof(float) * std::max(std::max(plain, step), prompt));
   return L;
 }
 
@@ -336,6 +359,15 @@ cudaError_t launch_step(const AttendArgs& A, int cols, int workers, cudaStream_t
       {launch_attend_step_q4_f16, launch_attend_step_q4_q8, launch_attend_step_q4_q4}};
   static_assert(TRIA_F16 == 1 && TRIA_Q8_0 == 2 && TRIA_Q4_0 == 3, "table order");
   return fn[A.k_type - 1][A.v_type - 1](A, cols, workers, st);
+}
+
+cudaError_t launch_prompt(const AttendArgs& A, cudaStream_t st) {
+  using Fn = cudaError_t (*)(const AttendArgs&, cudaStream_t);
+  static constexpr Fn fn[3][3] = {
+      {launch_attend_prompt_f16_f16, launch_attend_prompt_f16_q8, launch_attend_prompt_f16_q4},
+      {launch_attend_prompt_q8_f16, launch_attend_prompt_q8_q8, launch_attend_prompt_q8_q4},
+      {launch_attend_prompt_q4_f16, launch_attend_prompt_q4_q8, launch_attend_prompt_q4_q4}};
+  return fn[A.k_type - 1][A.v_type - 1](A, st);
 }
 
 tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const int32_t* tok0) {
@@ -404,13 +436,14 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   A.scale = (float)(a->scale != 0.0 ? a->scale : 1.0 / sqrt((double)hd));
   const bool tensor = tensor_types(cache, a->type);
   int units = 0, cols = 0;
-  bool plain = false, step = false;
+  bool plain = false, step = false, prompt = false;
   for (int s = 0; s < cache->n_seqs; ++s) {
     A.seq[s].row0 = cache->seq_row0[s];
     A.seq[s].cap = cache->capacity[s];
     A.seq[s].tok0 = a->tok0[s];
     const int t = a->tok0[s + 1] - a->tok0[s], path = path_of(tensor, t, G);
     plain = plain || path == kPathPlain;
+    prompt = prompt || path == kPathPrompt;
     if (path == kPathStep) {
       step = true;
       cols = std::max(cols, t * G);
@@ -418,12 +451,13 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   }
   // each kernel sees the sequences it takes, the others without tokens
   auto take = [&](int path) {
+    const int per = path == kPathPrompt ? prompt_cols(hd) : kCols;
     units = 0;
     for (int s = 0; s < cache->n_seqs; ++s) {
       const int t = a->tok0[s + 1] - a->tok0[s];
       A.seq[s].t = path_of(tensor, t, G) == path ? t : 0;
       A.seq[s].unit0 = units;
-      units += (A.seq[s].t * G + kCols - 1) / kCols;
+      units += (A.seq[s].t * G + per - 1) / per;
     }
     A.units = units;
   };
@@ -431,6 +465,11 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   if (step) {
     take(kPathStep);
     if (launch_step(A, cols, L.sms, st) != cudaSuccess) return TRIA_ERR_CUDA;
+  }
+  if (prompt) {
+    take(kPathPrompt);
+    A.split = L.prompt_split;
+    if (launch_prompt(A, st) != cudaSuccess) return TRIA_ERR_CUDA;
   }
   if (plain) {
     take(kPathPlain);

@@ -72,6 +72,17 @@ cudaError_t launch_attend_step_q8_q4(const AttendArgs& A, int cols, int workers,
 cudaError_t launch_attend_step_q4_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 cudaError_t launch_attend_step_q4_q8(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 cudaError_t launch_attend_step_q4_q4(const AttendArgs& A, int cols, int workers, cudaStream_t st);
+// attend_prompt_*.cu: units of prompt_cols(hd) columns
+inline int prompt_cols(int hd) { return hd == 256 ? 128 : 256; }
+cudaError_t launch_attend_prompt_f16_f16(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_f16_q8(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_f16_q4(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_q8_f16(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_q8_q8(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_q8_q4(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_q4_f16(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_q4_q8(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt_q4_q4(const AttendArgs& A, cudaStream_t st);
 
 __device__ __forceinline__ float act_load(const void* p, int type, int64_t i) {
   if (type == TRIA_F32) return reinterpret_cast<const float*>(p)[i];

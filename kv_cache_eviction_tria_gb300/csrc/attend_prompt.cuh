@@ -1,0 +1,806 @@
+// Attention of many new tokens over the cache (prompts and their chunks) on
+// the fifth-generation tensor cores.
+//
+//   S = Q K^T (128 x BN, fp32 in TMEM), P = 2^(scale S - M) (fp16, written over
+//   S in TMEM), O += P V (128 x head_dim, fp32 in TMEM), l = sum of P
+//
+// A tile's 128 rows are (token, head) pairs of one KV head's group, so that a
+// key tile is read once for the whole group. Per CTA (one per SM): two such
+// tiles with a softmax warpgroup each (one tile and two score buffers at
+// head_dim 256, where two outputs would fill TMEM), so that the tensor cores
+// work on one tile while the other is in its softmax; a warpgroup that fills a
+// ring of key and value tiles; one thread that issues the products. What
+// bounds it is the tensor cores' rate together with one exponential per score.
+//
+// A thread owns a row of S: maximum and sum need no shuffles. The reference M
+// moves only when a row's maximum has grown by more than 2^8 (kLazy), since
+// until then P stays inside fp16 (it is kept 2^-kShift below its limit) and
+// the common factor cancels in O / l: rescaling O costs a pass over TMEM and is
+// rare this way.
+//
+// fp16 rows come by cp.async, 8- and 4-bit ones are rounded to fp16 once
+// (code x scale) on their way into the 128-byte-swizzled tiles: a copy engine
+// could not convert them, and rows past the last live one have to become
+// zeros. In tiles that some token does not see whole, a value row that holds
+// an infinity or NaN is replaced by zeros and the tokens that do see it get
+// NaN, so that hidden junk never meets a weight of zero.
+#pragma once
+
+#include <type_traits>
+
+#include "attend_internal.cuh"
+
+namespace tria {
+
+template <int HD>
+struct PromptShape {
+  static constexpr int QT = HD == 256 ? 1 : 2;             // tiles of 128 rows per CTA
+  static constexpr int BN = HD == 256 ? 64 : 128;          // rows of a key / value tile
+  static constexpr int kQ = 128 * HD * 2;                  // bytes of a query tile
+  static constexpr int kStage = BN * HD * 2;
+  static constexpr int kStages = HD == 64 ? 8 : 5;
+  static constexpr int oQ = 0, oRing = QT * kQ;
+  static constexpr int oPos = oRing + kStages * kStage;    // positions of a tile's rows, 4 tiles
+  static constexpr int oBar = oPos + 4 * BN * 4;           // barriers, then PromptShared
+  static constexpr int kSmem = oBar + 512;
+  static constexpr int cS = 0, cO = 256;                   // TMEM columns: two score buffers, outputs
+  static_assert(cO + QT * HD <= 512, "TMEM");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct PromptShared {
+  uint32_t junk[8][4];                                     // rows of a value tile that held junk, by stage
+  uint32_t tmem, abort;
+  int32_t pmin, pmax, hi, last;
+};
+constexpr int kPromptBars = 2 * 8 + 2 + 2 + 3;
+static_assert(kPromptBars * 8 + sizeof(PromptShared) <= 512, "barriers and shared state");
+
+constexpr int kPromptThreads = 512;
+constexpr float kLazy = 8.f, kShift = 5.f;
+
+// ---- PTX -------------------------------------------------------------------
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define TRIA_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define TRIA_S8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : TRIA_R8(r, 0), TRIA_R8(r, 8), TRIA_R8(r, 16), TRIA_R8(r, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::TRIA_S8(r, 0),
+      TRIA_S8(r, 8), TRIA_S8(r, 16), TRIA_S8(r, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::TRIA_S8(r, 0),
+      TRIA_S8(r, 8), "r"(addr)
+      : "memory");
+}
+// keeps uses of loaded registers behind the wait for them
+#define TRIA_P8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7])
+__device__ __forceinline__ void tc_pin(uint32_t* r) {
+  asm volatile("" : TRIA_P8(r, 0), TRIA_P8(r, 8));
+  asm volatile("" : TRIA_P8(r, 16), TRIA_P8(r, 24));
+}
+#undef TRIA_P8
+#undef TRIA_R8
+#undef TRIA_S8
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 128-byte-swizzled tile descriptors: rows of 128 bytes in groups of eight
+// (1024 bytes). K-major operands step 32 bytes per 16 dims inside a row; the
+// values (dims contiguous, rows along K) step 2048 bytes per 16 rows and
+// `blocks` bytes from one 64-dim block to the next.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t block_bytes) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(block_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// fp16 operands, fp32 result, M = 128
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ uint32_t swz(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
+
+__device__ __forceinline__ bool junk_h2(uint32_t w) {     // an infinity or NaN in a pair of fp16
+  return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Rows r .. r + rows of a plane into a tile of fp16 in shared memory (zeros
+// past `rows`), by the 128 threads of the loading warpgroup. Quantised rows
+// are fetched into registers ahead of their turn.
+template <int T, int HD, int BN>
+struct TileLoader {
+  static constexpr bool kQ = T != TRIA_F16;
+  static constexpr int kUnits = T == TRIA_F16 ? BN * HD / 8 / 128 : (T == TRIA_Q8_0 ? BN * HD / 16 / 128 : BN * HD / 32 / 128);
+  uint4 u[kQ ? kUnits : 1];
+  uint32_t s[kQ ? kUnits : 1];     // the unit's scale, twice
+
+  __device__ __forceinline__ void fetch(const uint8_t* data, const uint8_t* scale, int64_t row, int rows, int tid) {
+    if constexpr (kQ) {
+      constexpr int per = T == TRIA_Q8_0 ? HD / 16 : HD / 32;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int x = i * 128 + tid, r = x / per, c = x - r * per;
+        u[i] = make_uint4(0, 0, 0, 0);
+        s[i] = 0;
+        if (r < rows) {
+          u[i] = *reinterpret_cast<const uint4*>(data + ((row + r) * per + c) * 16);
+          const uint32_t h = reinterpret_cast<const uint16_t*>(scale)[(row + r) * (HD / 32) + (T == TRIA_Q8_0 ? c / 2 : c)];
+          s[i] = h | (h << 16);
+        }
+      }
+    }
+  }
+  // fp16: starts the copies (commit and wait are the caller's)
+  __device__ __forceinline__ void copy(uint8_t* tile, const uint8_t* data, int64_t row, int rows, int tid) {
+    constexpr int per = HD / 8;
+#pragma unroll 8
+    for (int i = 0; i < kUnits; ++i) {
+      const int x = i * 128 + tid, r = x / per, c = x - r * per;
+      const uint32_t dst = smem_u32(tile) + (c >> 3) * (BN * 128) + swz(r, c & 7);
+      const uint8_t* src = data + ((row + (r < rows ? r : 0)) * per + c) * 16;
+      const int bytes = r < rows ? 16 : 0;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    }
+  }
+  // values with junk become zeros and their rows are marked
+  __device__ __forceinline__ void clean(uint8_t* tile, uint32_t* marks, int tid) {
+    constexpr int per = HD / 8;
+    for (int i = 0; i < kUnits; ++i) {
+      const int x = i * 128 + tid, r = x / per, c = x - r * per;
+      uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * (BN * 128) + swz(r, c & 7));
+      const uint4 v = *p;
+      if (junk_h2(v.x) || junk_h2(v.y) || junk_h2(v.z) || junk_h2(v.w)) {
+        *p = make_uint4(0, 0, 0, 0);
+        atomicOr(&marks[r >> 5], 1u << (r & 31));
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* tile, bool cleaned, uint32_t* marks, int tid) {
+    constexpr int per = T == TRIA_Q8_0 ? HD / 16 : HD / 32;
+#pragma unroll
+    for (int i = 0; i < (kQ ? kUnits : 0); ++i) {
+      const int x = i * 128 + tid, r = x / per, c = x - r * per;
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      uint32_t sc = s[i];
+      auto mul = [&](uint32_t a) {
+        uint32_t d;
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(sc));
+        return d;
+      };
+      auto sub = [&](uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+      };
+      if (cleaned && junk_h2(sc)) {
+        sc = 0;
+        atomicOr(&marks[r >> 5], 1u << (r & 31));
+      }
+      if constexpr (T == TRIA_Q8_0) {
+        uint32_t h[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t b = w[k] ^ 0x80808080u;           // 0x64, code + 128: 1152 + code
+          h[2 * k] = mul(sub(__byte_perm(b, 0x64646464u, 0x4140), 0x64806480u));
+          h[2 * k + 1] = mul(sub(__byte_perm(b, 0x64646464u, 0x4342), 0x64806480u));
+        }
+        uint8_t* blk = tile + (c >> 2) * (BN * 128);
+        *reinterpret_cast<uint4*>(blk + swz(r, (2 * c) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(blk + swz(r, (2 * c + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
+      } else {
+        uint8_t* blk = tile + (c >> 1) * (BN * 128);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {             // dims 0..15 in the low halves, 16..31 in the high ones
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t b = (half ? w[k] >> 4 : w[k]) & 0x0F0F0F0Fu;
+            h[2 * k] = mul(sub(__byte_perm(b, 0x64646464u, 0x4140), 0x64086408u));
+            h[2 * k + 1] = mul(sub(__byte_perm(b, 0x64646464u, 0x4342), 0x64086408u));
+          }
+          const int c0 = 4 * (c & 1) + 2 * half;
+          *reinterpret_cast<uint4*>(blk + swz(r, c0)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(blk + swz(r, c0 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+    }
+  }
+};
+
+template <int KT, int VT, int HD>
+__global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __grid_constant__ AttendArgs A) {
+  using H = PromptShape<HD>;
+  constexpr int QT = H::QT, BN = H::BN, ST = H::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
+  // full: a tile is in the ring; empty: its products are done; s: scores; p:
+  // weights; q: queries; o: outputs; x: every product
+  uint64_t *b_full = bar, *b_empty = bar + ST, *b_s = bar + 2 * ST, *b_p = b_s + 2, *b_q = b_p + 2, *b_o = b_q + 1, *b_x = b_o + 1;
+  int32_t* s_pos = reinterpret_cast<int32_t*>(smem + H::oPos);
+  PromptShared& X = *reinterpret_cast<PromptShared*>(smem + H::oBar + kPromptBars * 8);
+  volatile uint32_t* s_abort = &X.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
+
+  // ---- the unit: QT x 128 columns (token x head) of one KV head; late tokens first
+  const int part = blockIdx.x % A.split;
+  const int y = A.units * A.n_kv - 1 - (int)(blockIdx.x / A.split);
+  const int unit = y / A.n_kv, g = y - unit * A.n_kv;
+  int s = 0;
+  {
+    int hi_s = A.n_seqs - 1;
+    while (s < hi_s) {
+      const int mid = (s + hi_s + 1) >> 1;
+      if (A.seq[mid].unit0 <= unit) s = mid; else hi_s = mid - 1;
+    }
+  }
+  const AttendSeq& S = A.seq[s];
+  const int n = *((volatile const int32_t*)(A.n_live + s));
+  if (n < 0 || n > S.cap) {
+    if (threadIdx.x == 0) report(A.ctrl, TRIA_ERR_DEVICE_ARG, (uint32_t)s);
+    return;
+  }
+  if (smem_u32(smem) & 1023u) {                            // the swizzled tiles need it
+    if (threadIdx.x == 0) report(A.ctrl, TRIA_ERR_CUDA, (uint32_t)s);
+    return;
+  }
+  const int c0 = (unit - S.unit0) * (QT * 128), ncol = min(QT * 128, S.t * A.G - c0);
+  const int tok_a = c0 / A.G, tok_b = (c0 + ncol - 1) / A.G;   // its tokens (of the sequence)
+  const int64_t row0 = S.row0 + (int64_t)g * S.cap;
+  const int32_t* rpos = A.cpos + row0;
+  if (threadIdx.x == 0) {
+    X.pmin = INT32_MAX;
+    X.pmax = INT32_MIN;
+    X.abort = 0;
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&b_full[i], 128);
+      mbar_init(&b_empty[i], 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b_s[i], 1);
+      mbar_init(&b_p[i], 128);
+    }
+    mbar_init(b_q, QT * 128);
+    mbar_init(b_o, 1);
+    mbar_init(b_x, 1);
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&X.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncthreads();
+  for (int i = tok_a + (int)threadIdx.x; i <= tok_b; i += kPromptThreads) {
+    const int p = A.pos[S.tok0 + i];
+    atomicMin(&X.pmin, p);
+    atomicMax(&X.pmax, p);
+  }
+  __syncthreads();
+  const int pmin = X.pmin, pmax = X.pmax;
+  if (warp == 0) {
+    // rows up to the newest token: where the rows behind it are the later
+    // tokens', else by a search in 32 parts
+    const int h = n - (S.t - 1 - tok_b);
+    const bool there = h >= 0 && (h == 0 || rpos[h - 1] <= pmax) && (h == n || rpos[h] > pmax);
+    int lo = 0, hi = n;                                    // rows < lo are <= pmax, rows >= hi are not
+    if (there) {
+      lo = hi = h;
+    } else {
+      while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int r = min(hi, lo + (lane + 1) * step) - 1;   // last row of this lane's share
+        const unsigned ok = __ballot_sync(0xffffffffu, rpos[r] <= pmax);
+        const int k = __popc(ok);                          // whole shares at or below pmax
+        lo = min(hi, lo + k * step);
+        if (k < 32) hi = min(hi, lo + step - 1 < lo ? lo : lo + step - 1);
+      }
+    }
+    if (lane == 0) X.hi = lo;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int hi = X.hi;
+  const int lo = A.window > 0 ? (int)max((int64_t)0, hi - (A.window + (int64_t)pmax - pmin)) : 0;
+  const int sr = min(A.sink, lo), nt_sink = (sr + BN - 1) / BN;
+  const int nt_all = nt_sink + (hi - lo + BN - 1) / BN;
+  const int ta = (int)((int64_t)part * nt_all / A.split), nt = (int)((int64_t)(part + 1) * nt_all / A.split) - ta;
+  const bool need_pos = A.window > 0 || (hi > 0 && rpos[hi - 1] > pmin);
+  auto tile_row = [&](int i, int& rows) {
+    const int j = ta + i;
+    if (j < nt_sink) {
+      rows = min(BN, sr - j * BN);
+      return j * BN;
+    }
+    const int r = lo + (j - nt_sink) * BN;
+    rows = min(BN, hi - r);
+    return r;
+  };
+  const uint32_t tmem = X.tmem;
+  // a bounded wait; after one gave up nobody waits any more
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    for (int it = 0; it < (1 << 22); ++it) {
+      if (mbar_try_wait(b, parity)) return true;
+      if (*s_abort) return false;
+    }
+    *s_abort = 1;
+    report(A.ctrl, TRIA_ERR_TIMEOUT, (uint32_t)s);
+    return false;
+  };
+
+  if (wg == 3) {
+    // ---- products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 12 && nt > 0) {
+      const uint32_t ring = smem_u32(smem + H::oRing), q0 = smem_u32(smem + H::oQ);
+      const bool one = lane == 0;
+      auto scores = [&](int q, int buf, int st) {
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          tc_mma_ss(tmem + H::cS + buf * 128, tile_desc(q0 + q * H::kQ + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
+                    tile_desc(ring + st * H::kStage + (k >> 2) * (BN * 128) + (k & 3) * 32, 16), mma_desc(BN, false), k > 0);
+      };
+      auto sums = [&](int q, int buf, int st, bool acc) {
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          tc_mma_ts(tmem + H::cO + q * HD, tmem + H::cS + buf * 128 + k * 8,
+                    tile_desc(ring + st * H::kStage + k * 2048, BN * 128), mma_desc(HD, true), acc || k > 0);
+      };
+      bool ok = wait(b_q, 0) && wait(&b_full[0], 0);
+      tc_fence_after();
+      if (ok && one) {
+#pragma unroll
+        for (int q = 0; q < QT; ++q) {
+          scores(q, q, 0);
+          tc_commit(&b_s[q]);
+        }
+        tc_commit(&b_empty[0]);
+      }
+      __syncwarp();
+      for (int i = 0; ok && i < nt; ++i) {
+        const int ev = 2 * i + 1, ek = 2 * i + 2;          // ring entries of V(i), K(i + 1)
+        const bool more = i + 1 < nt;
+        if constexpr (QT == 2) {
+          ok = wait(&b_full[ev % ST], (ev / ST) & 1) && (!more || wait(&b_full[ek % ST], (ek / ST) & 1));
+          for (int q = 0; q < 2 && ok; ++q) {
+            ok = wait(&b_p[q], i & 1);
+            tc_fence_after();
+            if (ok && one) {
+              sums(q, q, ev % ST, i > 0);
+              if (more) {
+                scores(q, q, ek % ST);
+                tc_commit(&b_s[q]);
+              }
+            }
+            __syncwarp();
+          }
+          if (ok && one) {
+            tc_commit(&b_empty[ev % ST]);
+            if (more) tc_commit(&b_empty[ek % ST]);
+            else tc_commit(b_o);
+          }
+        } else {
+          if (more) {
+            ok = wait(&b_full[ek % ST], (ek / ST) & 1);
+            tc_fence_after();
+            if (ok && one) {
+              scores(0, (i + 1) & 1, ek % ST);
+              tc_commit(&b_s[(i + 1) & 1]);
+              tc_commit(&b_empty[ek % ST]);
+            }
+            __syncwarp();
+          }
+          ok = ok && wait(&b_full[ev % ST], (ev / ST) & 1) && wait(&b_p[i & 1], (i >> 1) & 1);
+          tc_fence_after();
+          if (ok && one) {
+            sums(0, i & 1, ev % ST, i > 0);
+            tc_commit(&b_empty[ev % ST]);
+            tc_commit(b_o);
+          }
+        }
+        __syncwarp();
+      }
+      // nothing may be running when the accumulators are given back
+      if (one) tc_commit(b_x);
+      for (int it = 0; it < (1 << 22) && !mbar_try_wait(b_x, 0); ++it) {
+      }
+    }
+  } else if (wg == 2) {
+    // ---- key and value tiles
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    const int tid = threadIdx.x - 256;
+    constexpr bool kKq = KT != TRIA_F16, kVq = VT != TRIA_F16;
+    TileLoader<KT, HD, BN> lk;
+    TileLoader<VT, HD, BN> lv;
+    auto stage = [&](int e) { return smem + H::oRing + (e % ST) * H::kStage; };
+    auto free_stage = [&](int e) { return e < ST || wait(&b_empty[e % ST], ((e / ST) - 1) & 1); };
+    auto full = [&](int e) {
+      fence_proxy_async_smem();
+      mbar_arrive(&b_full[e % ST]);
+    };
+    auto whole = [&](int i) {                              // every token sees every row of tile i
+      int rows;
+      const int r = tile_row(i, rows);
+      if (rows < BN) return false;
+      if (!need_pos) return true;
+      const int32_t* tp = s_pos + (i & 3) * BN;
+      return tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window || r + BN <= A.sink);
+    };
+    // positions and marks go with the value tile, which stays until the weights are used
+    int next_pos = 0;                                      // of this thread's row of the tile to come
+    auto fetch_pos = [&](int i) {
+      int rows;
+      const int r = tile_row(i, rows);
+      next_pos = need_pos && i < nt && tid < BN && tid < rows ? rpos[r + tid] : INT32_MAX;
+    };
+    fetch_pos(0);
+    auto side = [&](int i) {
+      const int e = 2 * i + 1;
+      if (need_pos && tid < BN) s_pos[(i & 3) * BN + tid] = next_pos;
+      fetch_pos(i + 1);
+      if (tid < 4) X.junk[e % ST][tid] = 0;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    };
+    auto finish_v = [&](int i) {
+      if (!whole(i)) lv.clean(stage(2 * i + 1), X.junk[(2 * i + 1) % ST], tid);
+      full(2 * i + 1);
+    };
+    int rows;
+    bool ok = true;
+    if (kKq && nt > 0) {
+      const int r = tile_row(0, rows);
+      lk.fetch(A.k, A.ks, row0 + r, rows, tid);
+    }
+    for (int i = 0; ok && i < nt; ++i) {
+      const int r = tile_row(i, rows), ek = 2 * i, ev = 2 * i + 1;
+      if constexpr (kVq) lv.fetch(A.v, A.vs, row0 + r, rows, tid);
+      ok = free_stage(ek);
+      if (!ok) break;
+      if constexpr (kKq) {
+        lk.store(stage(ek), false, nullptr, tid);
+        full(ek);
+        if (i + 1 < nt) {
+          int rows2;
+          const int r2 = tile_row(i + 1, rows2);
+          lk.fetch(A.k, A.ks, row0 + r2, rows2, tid);
+        }
+      } else {
+        lk.copy(stage(ek), A.k, row0 + r, rows, tid);
+        cp_async_commit();
+        if constexpr (!kVq) {
+          if (i > 0) {                                     // the value tile before it has arrived
+            cp_async_wait<1>();
+            finish_v(i - 1);
+          }
+        }
+      }
+      ok = free_stage(ev);
+      if (!ok) break;
+      side(i);
+      if constexpr (kVq) {
+        lv.store(stage(ev), !whole(i), X.junk[ev % ST], tid);
+        full(ev);
+        if constexpr (!kKq) {
+          cp_async_wait<0>();
+          full(ek);
+        }
+      } else {
+        lv.copy(stage(ev), A.v, row0 + r, rows, tid);
+        cp_async_commit();
+        if constexpr (!kKq) {
+          cp_async_wait<1>();
+          full(ek);
+        } else {
+          cp_async_wait<0>();
+          finish_v(i);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if constexpr (!kKq && !kVq) {
+      if (ok && nt > 0) finish_v(nt - 1);
+    }
+  } else if (wg < QT) {
+    // ---- softmax: a thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    const int q = wg, m = threadIdx.x & 127, col = c0 + q * 128 + m;
+    const bool on = q * 128 + m < ncol;
+    const int tl = on ? col / A.G : tok_a;
+    const int64_t tok = S.tok0 + tl;
+    const int head = g * A.G + (on ? col - tl * A.G : 0);
+    const int p = on ? A.pos[tok] : INT32_MIN;
+    float sl = A.scale * 1.4426950408889634f;
+    {
+      // the row's queries as fp16; bf16 ones times a power of two, undone in the logits
+      const int64_t off = tok * A.q_stride + (int64_t)head * HD;
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(A.q) + off);
+      uint8_t* dst = smem + H::oQ + q * H::kQ;
+      float f = 1.f;
+      if (A.type == TRIA_BF16 && on) {
+        uint32_t am = 0;
+        for (int c = 0; c < HD / 8; ++c) {
+          const uint4 v = src[c];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) am = max(am, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+        }
+        const int ex = (int)(am >> 7) - 127;
+        if (ex > -120 && ex < 120) {
+          f = __uint_as_float((uint32_t)(127 - ex) << 23);
+          sl *= __uint_as_float((uint32_t)(127 + ex) << 23);
+        }
+      }
+      for (int c = 0; c < HD / 8; ++c) {
+        uint4 v = on ? src[c] : make_uint4(0, 0, 0, 0);
+        if (A.type == TRIA_BF16) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + swz(m, c & 7)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(b_q);
+    }
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = lane_base + H::cO + q * HD;
+    float M = -INFINITY, l = 0.f;
+    bool poison = false, ok = true;
+    for (int i = 0; i < nt; ++i) {
+      const int buf = QT == 2 ? q : (i & 1);
+      ok = wait(&b_s[buf], QT == 2 ? (i & 1) : ((i >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t ts = lane_base + H::cS + buf * 128;
+      uint32_t x[BN];
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) tc_ld32(x + c, ts + c);
+      int rows;
+      const int r = tile_row(i, rows);
+      bool masked = rows < BN;
+      const int ev = 2 * i + 1;
+      if (need_pos || masked) {
+        ok = wait(&b_full[ev % ST], (ev / ST) & 1);        // positions and marks are there
+        if (!ok) break;
+      }
+      const int32_t* tp = s_pos + (i & 3) * BN;
+      if (need_pos)
+        masked = masked || tp[BN - 1] > pmin || (A.window > 0 && (int64_t)pmax - tp[0] >= A.window && r + BN > A.sink);
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) tc_pin(x + c);
+      if (masked) {
+        const uint32_t* jm = X.junk[ev % ST];
+#pragma unroll
+        for (int c = 0; c < BN; ++c) {
+          bool see = c < rows;
+          if (need_pos) {
+            const int pr = tp[c];
+            see = see && pr <= p && (A.window <= 0 || (int64_t)p - pr < A.window || r + c < A.sink);
+          }
+          if (!see) x[c] = 0xFF800000u;                    // -inf
+          else if ((jm[c >> 5] >> (c & 31)) & 1u) poison = true;
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < BN; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+      top = top * sl - kShift;
+      const bool move = top > M + kLazy || M == -INFINITY;
+      if (__any_sync(0xffffffffu, move && top > -INFINITY)) {
+        float a = 1.f;
+        if (move && top > -INFINITY) {
+          a = exp2_fast(M - top);
+          M = top;
+          l *= a;
+        }
+        if (i > 0) {
+          if constexpr (QT == 1) {                         // the sums of the tile before are still running
+            ok = wait(b_o, (i - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            tc_ld32(o, to + c);
+            tc_wait_ld();
+            tc_pin(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            tc_st32(to + c, o);
+          }
+        }
+      }
+      const float mb = M == -INFINITY ? 0.f : M;
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float a = exp2_fast(fmaf(__uint_as_float(x[c + 2 * k]), sl, -mb));
+          const float b = exp2_fast(fmaf(__uint_as_float(x[c + 2 * k + 1]), sl, -mb));
+          l0 += a;
+          l1 += b;
+          const __half2 h = __floats2half2_rn(a, b);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        tc_st16(ts + c / 2, w);
+      }
+      l += l0 + l1;
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&b_p[buf]);
+    }
+    // ---- results
+    if (ok && nt > 0) {
+      if constexpr (QT == 2) ok = wait(b_o, 0);
+      else ok = (nt < 2 || wait(b_o, (nt - 2) & 1)) && wait(b_o, (nt - 1) & 1);
+      tc_fence_after();
+    }
+    if (ok) {
+      const bool split = A.split > 1;
+      float* slot = A.part + ((int64_t)y * A.split + part) * (QT * 128) * (HD + 2) + (q * 128 + m);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tc_ld32(o, to + c);
+          tc_wait_ld();
+          tc_pin(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+        if (poison) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0x7FC00000u;
+        }
+        if (split) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) slot[(int64_t)(2 + c + k) * (QT * 128)] = __uint_as_float(o[k]);
+        } else if (on) {
+          uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD + c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = __uint_as_float(o[8 * k + 2 * e]) * inv, b = __uint_as_float(o[8 * k + 2 * e + 1]) * inv;
+              if (A.type == TRIA_F16) {
+                const __half2 h = __floats2half2_rn(a, b);
+                w[e] = *reinterpret_cast<const uint32_t*>(&h);
+              } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                w[e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            }
+            d[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (split) {
+        slot[0] = M;
+        slot[QT * 128] = l;
+      } else if (on && A.lse) {
+        A.lse[tok * A.nq + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+    if (A.split > 1) {
+      // the last CTA of the unit to arrive merges the parts in order
+      asm volatile("bar.sync 2, %0;" ::"n"(QT * 128) : "memory");
+      if (threadIdx.x == 0) {
+        __threadfence();
+        X.last = atomicAdd(&A.count[y], 1u) == (uint32_t)A.split - 1;
+        __threadfence();
+        if (X.last) A.count[y] = 0u;
+      }
+      asm volatile("bar.sync 2, %0;" ::"n"(QT * 128) : "memory");
+      if (X.last && on) {
+        const int64_t stride = (int64_t)(QT * 128) * (HD + 2);
+        const float* x = A.part + (int64_t)y * A.split * stride + (q * 128 + m);
+        float top = -INFINITY, sum = 0.f;
+        for (int k = 0; k < A.split; ++k) top = fmaxf(top, __ldcg(x + k * stride));
+        const float tb = top == -INFINITY ? 0.f : top;
+        for (int k = 0; k < A.split; ++k) sum = fmaf(__ldcg(x + k * stride + QT * 128), exp2_fast(__ldcg(x + k * stride) - tb), sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int c = 0; c < HD; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = 0.f;
+          for (int k = 0; k < A.split; ++k) {
+            const float f = exp2_fast(__ldcg(x + k * stride) - tb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(__ldcg(x + k * stride + (int64_t)(2 + c + e) * (QT * 128)), f, v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) act_store(A.out, A.type, tok * A.out_stride + (int64_t)head * HD + c + e, v[e] * inv);
+        }
+        if (A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int KT, int VT, int HD>
+cudaError_t launch_attend_prompt_t(const AttendArgs& A, cudaStream_t st) {
+  using H = PromptShape<HD>;
+  auto kern = k_attend_prompt<KT, VT, HD>;
+  const int smem = H::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // the warpgroups' register shares (184, 184, 96, 48) are cut from the 128 a
+  // thread that the block starts with
+  cudaFuncAttributes attr;
+  const cudaError_t e2 = cudaFuncGetAttributes(&attr, kern);
+  if (e2 != cudaSuccess) return e2;
+  if (attr.numRegs != 128) return cudaErrorInvalidConfiguration;
+  const int64_t grid = (int64_t)A.units * A.n_kv * A.split;
+  kern<<<(unsigned)grid, kPromptThreads, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <int KT, int VT>
+cudaError_t launch_attend_prompt_kv(const AttendArgs& A, cudaStream_t st) {
+  switch (A.hd) {
+    case 64: return launch_attend_prompt_t<KT, VT, 64>(A, st);
+    case 128: return launch_attend_prompt_t<KT, VT, 128>(A, st);
+    case 256: return launch_attend_prompt_t<KT, VT, 256>(A, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace tria
