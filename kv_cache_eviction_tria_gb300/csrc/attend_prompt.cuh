@@ -18,14 +18,18 @@
 // the common factor cancels in O / l: rescaling O costs a pass over TMEM and is
 // rare this way.
 //
-// fp16 rows come by cp.async, 8- and 4-bit ones are rounded to fp16 once
-// (code x scale) on their way into the 128-byte-swizzled tiles: a copy engine
-// could not convert them, and rows past the last live one have to become
-// zeros. In tiles that some token does not see whole, a value row that holds
-// an infinity or NaN is replaced by zeros and the tokens that do see it get
-// NaN, so that hidden junk never meets a weight of zero.
+// fp16 rows come by TMA into 128-byte-swizzled tiles; 8- and 4-bit ones are
+// rounded to fp16 once (code x scale) by the loading warpgroup on their way
+// there. In tiles that some token does not see whole, value rows past the last
+// one become zeros, and one that holds an infinity or NaN is replaced by zeros
+// while the tokens that do see it get NaN, so that hidden junk never meets a
+// weight of zero.
 #pragma once
 
+#include <cuda.h>
+#include <string.h>
+
+#include <algorithm>
 #include <type_traits>
 
 #include "attend_internal.cuh"
@@ -53,10 +57,19 @@ struct PromptShared {
   uint32_t tmem, abort;
   int32_t pmin, pmax, hi, last;
 };
-constexpr int kPromptBars = 2 * 8 + 2 + 2 + 3;
+constexpr int kPromptBars = 2 * 8 + 2 + 2 + 4;
 static_assert(kPromptBars * 8 + sizeof(PromptShared) <= 512, "barriers and shared state");
 
 constexpr int kPromptThreads = 512;
+
+// Registers of a thread by warpgroup: conversions need more in the loading
+// one. The shares add up to the 4 x 128 that the block starts with.
+template <bool kConvert>
+struct PromptRegs {
+  static constexpr int kSoft = kConvert ? 168 : 192, kLoad = kConvert ? 112 : 72, kIssue = kConvert ? 64 : 56;
+  static_assert(2 * kSoft + kLoad + kIssue == 512, "register shares");
+};
+
 constexpr float kLazy = 8.f, kShift = 5.f;
 
 // ---- PTX -------------------------------------------------------------------
@@ -92,12 +105,10 @@ __device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
       : TRIA_R8(r, 0), TRIA_R8(r, 8), TRIA_R8(r, 16), TRIA_R8(r, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::TRIA_S8(r, 0),
-      TRIA_S8(r, 8), TRIA_S8(r, 16), TRIA_S8(r, 24), "r"(addr)
-      : "memory");
+__device__ __forceinline__ void tc_ld16(uint32_t* r, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : TRIA_R8(r, 0), TRIA_R8(r, 8)
+               : "r"(addr));
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -107,9 +118,10 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
 }
 // keeps uses of loaded registers behind the wait for them
 #define TRIA_P8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7])
+__device__ __forceinline__ void tc_pin16(uint32_t* r) { asm volatile("" : TRIA_P8(r, 0), TRIA_P8(r, 8)); }
 __device__ __forceinline__ void tc_pin(uint32_t* r) {
-  asm volatile("" : TRIA_P8(r, 0), TRIA_P8(r, 8));
-  asm volatile("" : TRIA_P8(r, 16), TRIA_P8(r, 24));
+  tc_pin16(r);
+  tc_pin16(r + 16);
 }
 #undef TRIA_P8
 #undef TRIA_R8
@@ -170,24 +182,28 @@ struct TileLoader {
       }
     }
   }
-  // fp16: starts the copies (commit and wait are the caller's)
-  __device__ __forceinline__ void copy(uint8_t* tile, const uint8_t* data, int64_t row, int rows, int tid) {
-    constexpr int per = HD / 8;
-#pragma unroll 8
-    for (int i = 0; i < kUnits; ++i) {
-      const int x = i * 128 + tid, r = x / per, c = x - r * per;
-      const uint32_t dst = smem_u32(tile) + (c >> 3) * (BN * 128) + swz(r, c & 7);
-      const uint8_t* src = data + ((row + (r < rows ? r : 0)) * per + c) * 16;
-      const int bytes = r < rows ? 16 : 0;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    }
+  // fp16: starts the copies of rows row .. row + BN, arriving on `bar`
+  static __device__ __forceinline__ void copy(uint8_t* tile, const CUtensorMap* map, int64_t row, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, BN * HD * 2);
+#pragma unroll
+    for (int c = 0; c < HD / 64; ++c)
+      asm volatile(
+          "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+              smem_u32(tile) + c * (BN * 128)),
+          "l"(map), "r"(c * 64), "r"((int)row), "r"(smem_u32(bar))
+          : "memory");
   }
-  // values with junk become zeros and their rows are marked
-  __device__ __forceinline__ void clean(uint8_t* tile, uint32_t* marks, int tid) {
+  // rows past `rows` and values with junk become zeros, the latter's rows are marked
+  __device__ __forceinline__ void clean(uint8_t* tile, int rows, uint32_t* marks, int tid) {
     constexpr int per = HD / 8;
+#pragma unroll 4
     for (int i = 0; i < kUnits; ++i) {
       const int x = i * 128 + tid, r = x / per, c = x - r * per;
       uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * (BN * 128) + swz(r, c & 7));
+      if (r >= rows) {
+        *p = make_uint4(0, 0, 0, 0);
+        continue;
+      }
       const uint4 v = *p;
       if (junk_h2(v.x) || junk_h2(v.y) || junk_h2(v.z) || junk_h2(v.w)) {
         *p = make_uint4(0, 0, 0, 0);
@@ -248,14 +264,18 @@ struct TileLoader {
 };
 
 template <int KT, int VT, int HD>
-__global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __grid_constant__ AttendArgs A) {
+__global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __grid_constant__ AttendArgs A,
+                                                                     const __grid_constant__ CUtensorMap map_k,
+                                                                     const __grid_constant__ CUtensorMap map_v) {
   using H = PromptShape<HD>;
+  using R = PromptRegs<KT != TRIA_F16 || VT != TRIA_F16>;
   constexpr int QT = H::QT, BN = H::BN, ST = H::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
   // full: a tile is in the ring; empty: its products are done; s: scores; p:
-  // weights; q: queries; o: outputs; x: every product
-  uint64_t *b_full = bar, *b_empty = bar + ST, *b_s = bar + 2 * ST, *b_p = b_s + 2, *b_q = b_p + 2, *b_o = b_q + 1, *b_x = b_o + 1;
+  // weights; q: queries; o: outputs; x: every product; raw: values that are
+  // looked through before their tile is full
+  uint64_t *b_full = bar, *b_empty = bar + ST, *b_s = bar + 2 * ST, *b_p = b_s + 2, *b_q = b_p + 2, *b_o = b_q + 1, *b_x = b_o + 1, *b_raw = b_x + 1;
   int32_t* s_pos = reinterpret_cast<int32_t*>(smem + H::oPos);
   PromptShared& X = *reinterpret_cast<PromptShared*>(smem + H::oBar + kPromptBars * 8);
   volatile uint32_t* s_abort = &X.abort;
@@ -293,7 +313,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     X.abort = 0;
 #pragma unroll
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&b_full[i], 128);
+      mbar_init(&b_full[i], 1);
       mbar_init(&b_empty[i], 1);
     }
 #pragma unroll
@@ -304,6 +324,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     mbar_init(b_q, QT * 128);
     mbar_init(b_o, 1);
     mbar_init(b_x, 1);
+    mbar_init(b_raw, 1);
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -371,7 +392,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
 
   if (wg == 3) {
     // ---- products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssue));
     if (warp == 12 && nt > 0) {
       const uint32_t ring = smem_u32(smem + H::oRing), q0 = smem_u32(smem + H::oQ);
       const bool one = lane == 0;
@@ -448,16 +469,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     }
   } else if (wg == 2) {
     // ---- key and value tiles
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLoad));
     const int tid = threadIdx.x - 256;
     constexpr bool kKq = KT != TRIA_F16, kVq = VT != TRIA_F16;
     TileLoader<KT, HD, BN> lk;
     TileLoader<VT, HD, BN> lv;
     auto stage = [&](int e) { return smem + H::oRing + (e % ST) * H::kStage; };
     auto free_stage = [&](int e) { return e < ST || wait(&b_empty[e % ST], ((e / ST) - 1) & 1); };
+    // the tile of entry e has been written by all threads
     auto full = [&](int e) {
       fence_proxy_async_smem();
-      mbar_arrive(&b_full[e % ST]);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (tid == 0) mbar_arrive(&b_full[e % ST]);
     };
     auto whole = [&](int i) {                              // every token sees every row of tile i
       int rows;
@@ -482,11 +505,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       if (tid < 4) X.junk[e % ST][tid] = 0;
       asm volatile("bar.sync 1, 128;" ::: "memory");
     };
-    auto finish_v = [&](int i) {
-      if (!whole(i)) lv.clean(stage(2 * i + 1), X.junk[(2 * i + 1) % ST], tid);
-      full(2 * i + 1);
-    };
-    int rows;
+    int rows, looked = 0;
     bool ok = true;
     if (kKq && nt > 0) {
       const int r = tile_row(0, rows);
@@ -506,50 +525,44 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
           lk.fetch(A.k, A.ks, row0 + r2, rows2, tid);
         }
       } else {
-        lk.copy(stage(ek), A.k, row0 + r, rows, tid);
-        cp_async_commit();
-        if constexpr (!kVq) {
-          if (i > 0) {                                     // the value tile before it has arrived
-            cp_async_wait<1>();
-            finish_v(i - 1);
-          }
-        }
+        // hidden keys, and those past the last row, only reach logits that the mask replaces
+        if (tid == 0) lk.copy(stage(ek), &map_k, row0 + r, &b_full[ek % ST]);
       }
       ok = free_stage(ev);
       if (!ok) break;
       side(i);
+      const bool all = whole(i);
       if constexpr (kVq) {
-        lv.store(stage(ev), !whole(i), X.junk[ev % ST], tid);
+        lv.store(stage(ev), !all, X.junk[ev % ST], tid);
         full(ev);
-        if constexpr (!kKq) {
-          cp_async_wait<0>();
-          full(ek);
-        }
+      } else if (all) {
+        if (tid == 0) lv.copy(stage(ev), &map_v, row0 + r, &b_full[ev % ST]);
       } else {
-        lv.copy(stage(ev), A.v, row0 + r, rows, tid);
-        cp_async_commit();
-        if constexpr (!kKq) {
-          cp_async_wait<1>();
-          full(ek);
-        } else {
-          cp_async_wait<0>();
-          finish_v(i);
-        }
+        if (tid == 0) lv.copy(stage(ev), &map_v, row0 + r, b_raw);
+        ok = wait(b_raw, looked & 1);
+        if (!ok) break;
+        ++looked;
+        lv.clean(stage(ev), rows, X.junk[ev % ST], tid);
+        full(ev);
       }
     }
-    cp_async_wait<0>();
-    if constexpr (!kKq && !kVq) {
-      if (ok && nt > 0) finish_v(nt - 1);
-    }
+    // copies still on their way when a wait gave up: those of whole tiles are
+    // waited for by their entries' parity
+    if (*s_abort && tid == 0)
+      for (int e = max(0, 2 * nt - ST); e < 2 * nt; ++e)
+        for (int it = 0; it < 1024 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
+        }
   } else if (wg < QT) {
     // ---- softmax: a thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoft));
     const int q = wg, m = threadIdx.x & 127, col = c0 + q * 128 + m;
     const bool on = q * 128 + m < ncol;
     const int tl = on ? col / A.G : tok_a;
     const int64_t tok = S.tok0 + tl;
     const int head = g * A.G + (on ? col - tl * A.G : 0);
     const int p = on ? A.pos[tok] : INT32_MIN;
+    // rows at or before it are outside the window
+    const int pold = A.window > 0 ? (int)max((int64_t)INT32_MIN, (int64_t)p - A.window) : INT32_MIN;
     float sl = A.scale * 1.4426950408889634f;
     {
       // the row's queries as fp16; bf16 ones times a power of two, undone in the logits
@@ -616,20 +629,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       for (int c = 0; c < BN; c += 32) tc_pin(x + c);
       if (masked) {
         const uint32_t* jm = X.junk[ev % ST];
+        const int first = r < A.sink ? A.sink - r : 0;     // rows of the tile before it are in the sink
 #pragma unroll
         for (int c = 0; c < BN; ++c) {
           bool see = c < rows;
           if (need_pos) {
             const int pr = tp[c];
-            see = see && pr <= p && (A.window <= 0 || (int64_t)p - pr < A.window || r + c < A.sink);
+            see = see && pr <= p && (pr > pold || c < first);
           }
           if (!see) x[c] = 0xFF800000u;                    // -inf
           else if ((jm[c >> 5] >> (c & 31)) & 1u) poison = true;
         }
       }
-      float top = -INFINITY;
+      float tops[4];
 #pragma unroll
-      for (int c = 0; c < BN; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+      for (int k = 0; k < 4; ++k) tops[k] = __uint_as_float(x[k]);
+#pragma unroll
+      for (int c = 4; c < BN - 4; c += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tops[k] = fmaxf(fmaxf(tops[k], __uint_as_float(x[c + k])), __uint_as_float(x[c + 4 + k]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], __uint_as_float(x[BN - 4 + k]));
+      float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       top = top * sl - kShift;
       const bool move = top > M + kLazy || M == -INFINITY;
       if (__any_sync(0xffffffffu, move && top > -INFINITY)) {
@@ -646,34 +668,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
             tc_fence_after();
           }
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            uint32_t o[32];
-            tc_ld32(o, to + c);
+          for (int c = 0; c < HD; c += 16) {
+            uint32_t o[16];
+            tc_ld16(o, to + c);
             tc_wait_ld();
-            tc_pin(o);
+            tc_pin16(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-            tc_st32(to + c, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            tc_st16(to + c, o);
           }
         }
       }
       const float mb = M == -INFINITY ? 0.f : M;
-      float l0 = 0.f, l1 = 0.f;
+      const float2 sl2 = make_float2(sl, sl), mb2 = make_float2(-mb, -mb);
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int c = 0; c < BN; c += 32) {
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const float a = exp2_fast(fmaf(__uint_as_float(x[c + 2 * k]), sl, -mb));
-          const float b = exp2_fast(fmaf(__uint_as_float(x[c + 2 * k + 1]), sl, -mb));
-          l0 += a;
-          l1 += b;
-          const __half2 h = __floats2half2_rn(a, b);
+          float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), sl2, mb2);
+          e.x = exp2_fast(e.x);
+          e.y = exp2_fast(e.y);
+          ls[k & 1] = __fadd2_rn(ls[k & 1], e);
+          const __half2 h = __floats2half2_rn(e.x, e.y);
           w[k] = *reinterpret_cast<const uint32_t*>(&h);
         }
         tc_st16(ts + c / 2, w);
       }
-      l += l0 + l1;
+      l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(&b_p[buf]);
@@ -775,6 +798,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
   }
 }
 
+// TMA view of an fp16 plane: boxes of 64 dims x `box` rows, 128-byte swizzle
+inline bool plane_map_f16(CUtensorMap* m, const void* base, int hd, int64_t rows, int box) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return (Encode)fn;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)hd * 2};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, steps[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int KT, int VT, int HD>
 cudaError_t launch_attend_prompt_t(const AttendArgs& A, cudaStream_t st) {
   using H = PromptShape<HD>;
@@ -782,14 +826,21 @@ cudaError_t launch_attend_prompt_t(const AttendArgs& A, cudaStream_t st) {
   const int smem = H::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // the warpgroups' register shares (184, 184, 96, 48) are cut from the 128 a
+  // the warpgroups' register shares (PromptRegs) are cut from the 128 a
   // thread that the block starts with
   cudaFuncAttributes attr;
   const cudaError_t e2 = cudaFuncGetAttributes(&attr, kern);
   if (e2 != cudaSuccess) return e2;
   if (attr.numRegs != 128) return cudaErrorInvalidConfiguration;
   const int64_t grid = (int64_t)A.units * A.n_kv * A.split;
-  kern<<<(unsigned)grid, kPromptThreads, smem, st>>>(A);
+  CUtensorMap mk, mv;
+  memset(&mk, 0, sizeof(mk));
+  memset(&mv, 0, sizeof(mv));
+  int64_t rows = 0;
+  for (int s = 0; s < A.n_seqs; ++s) rows = std::max(rows, A.seq[s].row0 + (int64_t)A.n_kv * A.seq[s].cap);
+  if ((KT == TRIA_F16 && !plane_map_f16(&mk, A.k, HD, rows, H::BN)) || (VT == TRIA_F16 && !plane_map_f16(&mv, A.v, HD, rows, H::BN)))
+    return cudaErrorInvalidValue;
+  kern<<<(unsigned)grid, kPromptThreads, smem, st>>>(A, mk, mv);
   return cudaGetLastError();
 }
 
