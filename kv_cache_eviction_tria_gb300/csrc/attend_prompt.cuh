@@ -6,8 +6,8 @@
 //
 // A tile's 128 rows are (token, head) pairs of one KV head's group, so that a
 // key tile is read once for the whole group. Per CTA (one per SM): two such
-// tiles with a softmax warpgroup each (one tile and two score buffers at
-// head_dim 256, where two outputs would fill TMEM), so that the tensor cores
+// tiles with a softmax warpgroup each (one tile at head_dim 256, where two
+// outputs would fill TMEM, with two score buffers), so that the tensor cores
 // work on one tile while the other is in its softmax; a warpgroup that fills a
 // ring of key and value tiles; one thread that issues the products. What
 // bounds it is the tensor cores' rate together with one exponential per score.
@@ -40,15 +40,19 @@ template <int HD>
 struct PromptShape {
   static constexpr int QT = HD == 256 ? 1 : 2;             // tiles of 128 rows per CTA
   static constexpr int BN = HD == 256 ? 64 : 128;          // rows of a key / value tile
+  static constexpr int NB = HD == 256 ? 2 : 1;             // score buffers of a tile
   static constexpr int kQ = 128 * HD * 2;                  // bytes of a query tile
   static constexpr int kStage = BN * HD * 2;
   static constexpr int kStages = HD == 64 ? 8 : 5;
-  static constexpr int oQ = 0, oRing = QT * kQ;
-  static constexpr int oPos = oRing + kStages * kStage;    // positions of a tile's rows, 4 tiles
-  static constexpr int oBar = oPos + 4 * BN * 4;           // barriers, then PromptShared
+  static constexpr int kPosTiles = 4;                      // positions are kept of the last tiles: a tile's value
+                                                           // stage is free once the fourth before it is done
+  static constexpr int oQ = 0, oRing = QT * kQ, oPos = oRing + kStages * kStage;
+  static constexpr int oBar = oPos + kPosTiles * BN * 4;   // barriers, then PromptShared
   static constexpr int kSmem = oBar + 512;
-  static constexpr int cS = 0, cO = 256;                   // TMEM columns: two score buffers, outputs
-  static_assert(cO + QT * HD <= 512, "TMEM");
+  // TMEM columns: score buffers, outputs
+  static constexpr int cO = 256;
+  static constexpr int cS(int q, int buf) { return (NB * q + buf) * BN; }
+  static_assert(QT * NB * BN <= cO && cO + QT * HD <= 512, "TMEM");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -57,16 +61,18 @@ struct PromptShared {
   uint32_t tmem, abort;
   int32_t pmin, pmax, hi, last;
 };
-constexpr int kPromptBars = 2 * 8 + 2 + 2 + 4;
+constexpr int kPromptBars = 2 * 8 + 4 + 4 + 2 + 2 + 3;
 static_assert(kPromptBars * 8 + sizeof(PromptShared) <= 512, "barriers and shared state");
 
 constexpr int kPromptThreads = 512;
 
-// Registers of a thread by warpgroup: conversions need more in the loading
-// one. The shares add up to the 4 x 128 that the block starts with.
-template <bool kConvert>
+// Registers of a thread by warpgroup: a row of 128 scores stays in them, and
+// conversions need more in the loading one. The shares add up to the 4 x 128
+// that the block starts with.
+template <int BN, bool kConvert>
 struct PromptRegs {
-  static constexpr int kSoft = kConvert ? 168 : 192, kLoad = kConvert ? 112 : 72, kIssue = kConvert ? 64 : 56;
+  static constexpr int kSoft = BN == 64 ? 152 : (kConvert ? 168 : 192), kLoad = BN == 64 ? 128 : (kConvert ? 112 : 72),
+                       kIssue = BN == 64 ? 80 : (kConvert ? 64 : 56);
   static_assert(2 * kSoft + kLoad + kIssue == 512, "register shares");
 };
 
@@ -87,6 +93,13 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// true in one lane of a converged warp (the compiler then knows that the branch
+// holds a single thread and keeps descriptors in uniform registers)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.b32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -268,14 +281,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
                                                                      const __grid_constant__ CUtensorMap map_k,
                                                                      const __grid_constant__ CUtensorMap map_v) {
   using H = PromptShape<HD>;
-  using R = PromptRegs<KT != TRIA_F16 || VT != TRIA_F16>;
-  constexpr int QT = H::QT, BN = H::BN, ST = H::kStages;
+  using R = PromptRegs<H::BN, KT != TRIA_F16 || VT != TRIA_F16>;
+  constexpr int QT = H::QT, BN = H::BN, NB = H::NB, ST = H::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
   // full: a tile is in the ring; empty: its products are done; s: scores; p:
-  // weights; q: queries; o: outputs; x: every product; raw: values that are
+  // weights; q: queries; o: sums; f: the last sums; x: every product; raw: values that are
   // looked through before their tile is full
-  uint64_t *b_full = bar, *b_empty = bar + ST, *b_s = bar + 2 * ST, *b_p = b_s + 2, *b_q = b_p + 2, *b_o = b_q + 1, *b_x = b_o + 1, *b_raw = b_x + 1;
+  uint64_t *b_full = bar, *b_empty = bar + ST, *b_s = bar + 2 * ST, *b_p = b_s + 4, *b_o = b_p + 4, *b_f = b_o + 2, *b_q = b_f + 2, *b_x = b_q + 1,
+           *b_raw = b_x + 1;
   int32_t* s_pos = reinterpret_cast<int32_t*>(smem + H::oPos);
   PromptShared& X = *reinterpret_cast<PromptShared*>(smem + H::oBar + kPromptBars * 8);
   volatile uint32_t* s_abort = &X.abort;
@@ -317,12 +331,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       mbar_init(&b_empty[i], 1);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&b_s[i], 1);
       mbar_init(&b_p[i], 128);
     }
     mbar_init(b_q, QT * 128);
-    mbar_init(b_o, 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b_o[i], 1);
+      mbar_init(&b_f[i], 1);
+    }
     mbar_init(b_x, 1);
     mbar_init(b_raw, 1);
     fence_mbar_init();
@@ -332,36 +350,100 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   __syncthreads();
-  for (int i = tok_a + (int)threadIdx.x; i <= tok_b; i += kPromptThreads) {
-    const int p = A.pos[S.tok0 + i];
-    atomicMin(&X.pmin, p);
-    atomicMax(&X.pmax, p);
-  }
-  __syncthreads();
-  const int pmin = X.pmin, pmax = X.pmax;
-  if (warp == 0) {
-    // rows up to the newest token: where the rows behind it are the later
-    // tokens', else by a search in 32 parts
-    const int h = n - (S.t - 1 - tok_b);
-    const bool there = h >= 0 && (h == 0 || rpos[h - 1] <= pmax) && (h == n || rpos[h] > pmax);
-    int lo = 0, hi = n;                                    // rows < lo are <= pmax, rows >= hi are not
-    if (there) {
-      lo = hi = h;
-    } else {
-      while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
-        const int r = min(hi, lo + (lane + 1) * step) - 1;   // last row of this lane's share
-        const unsigned ok = __ballot_sync(0xffffffffu, rpos[r] <= pmax);
-        const int k = __popc(ok);                          // whole shares at or below pmax
-        lo = min(hi, lo + k * step);
-        if (k < 32) hi = min(hi, lo + step - 1 < lo ? lo : lo + step - 1);
+  // ---- the softmax warpgroups fetch their queries; the loading one finds the rows
+  const uint32_t q_row = threadIdx.x & 127;                // a thread per row of the softmax
+  const int col = c0 + wg * 128 + (int)q_row;
+  const bool on = wg < QT && wg * 128 + (int)q_row < ncol;
+  const int tl = on ? col / A.G : tok_a;
+  const int64_t tok = S.tok0 + tl;
+  const int head = g * A.G + (on ? col - tl * A.G : 0);
+  float sl = A.scale * 1.4426950408889634f;
+  if (wg < QT) {
+    // as fp16; bf16 ones times a power of two, undone in the logits
+    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(A.q) + tok * A.q_stride + (int64_t)head * HD);
+    uint8_t* dst = smem + H::oQ + wg * H::kQ;
+    float f = 1.f;
+    constexpr int kPart = HD / 8 < 16 ? HD / 8 : 16;       // 16-byte pieces held at once
+    uint4 v[kPart];
+    if (A.type == TRIA_BF16) {
+      uint32_t am = 0;
+#pragma unroll 1
+      for (int c0q = 0; c0q < HD / 8; c0q += kPart) {
+#pragma unroll
+        for (int c = 0; c < kPart; ++c) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < kPart; ++c) {
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) am = max(am, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+        }
+      }
+      const int ex = (int)(am >> 7) - 127;
+      if (ex > -120 && ex < 120) {
+        f = __uint_as_float((uint32_t)(127 - ex) << 23);
+        sl *= __uint_as_float((uint32_t)(127 + ex) << 23);
       }
     }
-    if (lane == 0) X.hi = lo;
+#pragma unroll 1
+    for (int c0q = 0; c0q < HD / 8; c0q += kPart) {
+#pragma unroll
+      for (int c = 0; c < kPart; ++c) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < kPart; ++c) {
+        uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        if (A.type == TRIA_BF16) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        const int cc = c0q + c;
+        *reinterpret_cast<uint4*>(dst + (cc >> 3) * (128 * 128) + swz(q_row, cc & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(b_q);
+  } else if (wg == 2) {
+    int pl = INT32_MAX, ph = INT32_MIN;
+    for (int i = tok_a + (int)q_row; i <= tok_b; i += 128) {
+      const int p = A.pos[S.tok0 + i];
+      pl = min(pl, p);
+      ph = max(ph, p);
+    }
+    pl = __reduce_min_sync(0xffffffffu, pl);
+    ph = __reduce_max_sync(0xffffffffu, ph);
+    if (lane == 0) {
+      atomicMin(&X.pmin, pl);
+      atomicMax(&X.pmax, ph);
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp == 8) {
+      // rows up to the newest token: where the rows behind it are the later
+      // tokens', else by a search in 32 parts
+      const int pmax = *(volatile int32_t*)&X.pmax;
+      const int h = n - (S.t - 1 - tok_b);
+      const bool there = h >= 0 && (h == 0 || rpos[h - 1] <= pmax) && (h == n || rpos[h] > pmax);
+      int lo = 0, hi = n;                                  // rows < lo are <= pmax, rows >= hi are not
+      if (there) {
+        lo = hi = h;
+      } else {
+        while (lo < hi) {
+          const int step = (hi - lo + 31) / 32;
+          const int r = min(hi, lo + (lane + 1) * step) - 1;   // last row of this lane's share
+          const unsigned okm = __ballot_sync(0xffffffffu, rpos[r] <= pmax);
+          const int k = __popc(okm);                       // whole shares at or below pmax
+          lo = min(hi, lo + k * step);
+          if (k < 32) hi = min(hi, lo + step - 1);
+        }
+      }
+      if (lane == 0) X.hi = lo;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const int pmin = X.pmin, pmax = X.pmax;
   const int hi = X.hi;
   const int lo = A.window > 0 ? (int)max((int64_t)0, hi - (A.window + (int64_t)pmax - pmin)) : 0;
   const int sr = min(A.sink, lo), nt_sink = (sr + BN - 1) / BN;
@@ -394,82 +476,100 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     // ---- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssue));
     if (warp == 12 && nt > 0) {
-      const uint32_t ring = smem_u32(smem + H::oRing), q0 = smem_u32(smem + H::oQ);
-      const bool one = lane == 0;
-      auto scores = [&](int q, int buf, int st) {
+      // results of waits and addresses are the same in all lanes and kept in
+      // such a form (votes, a broadcast): operands of the products then live in
+      // uniform registers, without which issuing them was the bottleneck
+      auto wait_all = [&](uint64_t* b, uint32_t parity) {
+        for (int it = 0; it < (1 << 22); ++it) {
+          if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+          if (__any_sync(0xffffffffu, *s_abort != 0)) return false;
+        }
+        *s_abort = 1;
+        if (lane == 0) report(A.ctrl, TRIA_ERR_TIMEOUT, (uint32_t)s);
+        return false;
+      };
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t dq = tile_desc(smem_u32(smem + H::oQ), 16), dk = tile_desc(smem_u32(smem + H::oRing), 16),
+                     dv = tile_desc(smem_u32(smem + H::oRing), BN * 128);
+      auto scores = [&](int q, int i, int st) {            // address fields count 16 bytes
+        const uint64_t a = dq + (uint64_t)(q * (H::kQ / 16)), b = dk + (uint64_t)(st * (H::kStage / 16));
+        const uint32_t d = tm + H::cS(q, i % NB);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
-          tc_mma_ss(tmem + H::cS + buf * 128, tile_desc(q0 + q * H::kQ + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
-                    tile_desc(ring + st * H::kStage + (k >> 2) * (BN * 128) + (k & 3) * 32, 16), mma_desc(BN, false), k > 0);
+          tc_mma_ss(d, a + (uint64_t)((k >> 2) * (128 * 8) + (k & 3) * 2), b + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2),
+                    mma_desc(BN, false), k > 0);
+        tc_commit(&b_s[NB * q + i % NB]);
       };
-      auto sums = [&](int q, int buf, int st, bool acc) {
+      auto sums = [&](int q, int i, int st) {
+        const uint64_t b = dv + (uint64_t)(st * (H::kStage / 16));
+        const uint32_t d = tm + H::cO + q * HD, a = tm + H::cS(q, i % NB);
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          tc_mma_ts(tmem + H::cO + q * HD, tmem + H::cS + buf * 128 + k * 8,
-                    tile_desc(ring + st * H::kStage + k * 2048, BN * 128), mma_desc(HD, true), acc || k > 0);
+        for (int k = 0; k < BN / 16; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), i > 0 || k > 0);
+        tc_commit(&b_o[q]);
       };
-      bool ok = wait(b_q, 0) && wait(&b_full[0], 0);
+      bool ok = wait_all(b_q, 0) && wait_all(&b_full[0], 0);
       tc_fence_after();
-      if (ok && one) {
+      if (ok && elect_one()) {
 #pragma unroll
-        for (int q = 0; q < QT; ++q) {
-          scores(q, q, 0);
-          tc_commit(&b_s[q]);
-        }
+        for (int q = 0; q < QT; ++q) scores(q, 0, 0);
         tc_commit(&b_empty[0]);
       }
       __syncwarp();
+      int sv = 1 % ST, sk = 2 % ST, pv = 0, pk = 2 / ST & 1;   // ring stage and parity of V(i), K(i + 1)
       for (int i = 0; ok && i < nt; ++i) {
-        const int ev = 2 * i + 1, ek = 2 * i + 2;          // ring entries of V(i), K(i + 1)
         const bool more = i + 1 < nt;
-        if constexpr (QT == 2) {
-          ok = wait(&b_full[ev % ST], (ev / ST) & 1) && (!more || wait(&b_full[ek % ST], (ek / ST) & 1));
-          for (int q = 0; q < 2 && ok; ++q) {
-            ok = wait(&b_p[q], i & 1);
-            tc_fence_after();
-            if (ok && one) {
-              sums(q, q, ev % ST, i > 0);
-              if (more) {
-                scores(q, q, ek % ST);
-                tc_commit(&b_s[q]);
-              }
-            }
-            __syncwarp();
-          }
-          if (ok && one) {
-            tc_commit(&b_empty[ev % ST]);
-            if (more) tc_commit(&b_empty[ek % ST]);
-            else tc_commit(b_o);
-          }
-        } else {
+        if (more) ok = wait_all(&b_full[sk], pk);
+        if constexpr (NB == 2) {
+          // the other buffer's weights are those of tile i - 1, whose sums were issued before
           if (more) {
-            ok = wait(&b_full[ek % ST], (ek / ST) & 1);
             tc_fence_after();
-            if (ok && one) {
-              scores(0, (i + 1) & 1, ek % ST);
-              tc_commit(&b_s[(i + 1) & 1]);
-              tc_commit(&b_empty[ek % ST]);
+            if (ok && elect_one()) {
+#pragma unroll
+              for (int q = 0; q < QT; ++q) scores(q, i + 1, sk);
+              tc_commit(&b_empty[sk]);
             }
             __syncwarp();
-          }
-          ok = ok && wait(&b_full[ev % ST], (ev / ST) & 1) && wait(&b_p[i & 1], (i >> 1) & 1);
-          tc_fence_after();
-          if (ok && one) {
-            sums(0, i & 1, ev % ST, i > 0);
-            tc_commit(&b_empty[ev % ST]);
-            tc_commit(b_o);
           }
         }
+        ok = ok && wait_all(&b_full[sv], pv);
+#pragma unroll
+        for (int q = 0; q < QT; ++q) {
+          ok = ok && wait_all(&b_p[NB * q + i % NB], (i / NB) & 1);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            sums(q, i, sv);
+            // products run in the order of their issue: the scores overwrite weights that the sums have used
+            if (NB == 1 && more) scores(q, i + 1, sk);
+          }
+          __syncwarp();
+        }
+        if (ok && elect_one()) {
+          tc_commit(&b_empty[sv]);
+          if (NB == 1 && more) tc_commit(&b_empty[sk]);
+          if (!more)
+#pragma unroll
+            for (int q = 0; q < QT; ++q) tc_commit(&b_f[q]);
+        }
         __syncwarp();
+        sv += 2;
+        if (sv >= ST) {
+          sv -= ST;
+          pv ^= 1;
+        }
+        sk += 2;
+        if (sk >= ST) {
+          sk -= ST;
+          pk ^= 1;
+        }
       }
       // nothing may be running when the accumulators are given back
-      if (one) tc_commit(b_x);
+      if (elect_one()) tc_commit(b_x);
       for (int it = 0; it < (1 << 22) && !mbar_try_wait(b_x, 0); ++it) {
       }
     }
   } else if (wg == 2) {
     // ---- key and value tiles
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLoad));
+    if constexpr (R::kLoad < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLoad));
     const int tid = threadIdx.x - 256;
     constexpr bool kKq = KT != TRIA_F16, kVq = VT != TRIA_F16;
     TileLoader<KT, HD, BN> lk;
@@ -487,7 +587,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       const int r = tile_row(i, rows);
       if (rows < BN) return false;
       if (!need_pos) return true;
-      const int32_t* tp = s_pos + (i & 3) * BN;
+      const int32_t* tp = s_pos + (i % H::kPosTiles) * BN;
       return tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window || r + BN <= A.sink);
     };
     // positions and marks go with the value tile, which stays until the weights are used
@@ -500,7 +600,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     fetch_pos(0);
     auto side = [&](int i) {
       const int e = 2 * i + 1;
-      if (need_pos && tid < BN) s_pos[(i & 3) * BN + tid] = next_pos;
+      if (need_pos && tid < BN) s_pos[(i % H::kPosTiles) * BN + tid] = next_pos;
       fetch_pos(i + 1);
       if (tid < 4) X.junk[e % ST][tid] = 0;
       asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -555,61 +655,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
   } else if (wg < QT) {
     // ---- softmax: a thread per row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoft));
-    const int q = wg, m = threadIdx.x & 127, col = c0 + q * 128 + m;
-    const bool on = q * 128 + m < ncol;
-    const int tl = on ? col / A.G : tok_a;
-    const int64_t tok = S.tok0 + tl;
-    const int head = g * A.G + (on ? col - tl * A.G : 0);
+    const int q = wg, m = (int)q_row;
     const int p = on ? A.pos[tok] : INT32_MIN;
     // rows at or before it are outside the window
     const int pold = A.window > 0 ? (int)max((int64_t)INT32_MIN, (int64_t)p - A.window) : INT32_MIN;
-    float sl = A.scale * 1.4426950408889634f;
-    {
-      // the row's queries as fp16; bf16 ones times a power of two, undone in the logits
-      const int64_t off = tok * A.q_stride + (int64_t)head * HD;
-      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(A.q) + off);
-      uint8_t* dst = smem + H::oQ + q * H::kQ;
-      float f = 1.f;
-      if (A.type == TRIA_BF16 && on) {
-        uint32_t am = 0;
-        for (int c = 0; c < HD / 8; ++c) {
-          const uint4 v = src[c];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) am = max(am, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-        }
-        const int ex = (int)(am >> 7) - 127;
-        if (ex > -120 && ex < 120) {
-          f = __uint_as_float((uint32_t)(127 - ex) << 23);
-          sl *= __uint_as_float((uint32_t)(127 + ex) << 23);
-        }
-      }
-      for (int c = 0; c < HD / 8; ++c) {
-        uint4 v = on ? src[c] : make_uint4(0, 0, 0, 0);
-        if (A.type == TRIA_BF16) {
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 h = __floats2half2_rn(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + swz(m, c & 7)) = v;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(b_q);
-    }
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = lane_base + H::cO + q * HD;
     float M = -INFINITY, l = 0.f;
     bool poison = false, ok = true;
     for (int i = 0; i < nt; ++i) {
-      const int buf = QT == 2 ? q : (i & 1);
-      ok = wait(&b_s[buf], QT == 2 ? (i & 1) : ((i >> 1) & 1));
+      const int buf = NB * q + i % NB;
+      ok = wait(&b_s[buf], (i / NB) & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t ts = lane_base + H::cS + buf * 128;
+      const uint32_t ts = lane_base + H::cS(q, i % NB);
       uint32_t x[BN];
 #pragma unroll
       for (int c = 0; c < BN; c += 32) tc_ld32(x + c, ts + c);
@@ -621,25 +680,37 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         ok = wait(&b_full[ev % ST], (ev / ST) & 1);        // positions and marks are there
         if (!ok) break;
       }
-      const int32_t* tp = s_pos + (i & 3) * BN;
+      const int32_t* tp = s_pos + (i % H::kPosTiles) * BN;
       if (need_pos)
         masked = masked || tp[BN - 1] > pmin || (A.window > 0 && (int64_t)pmax - tp[0] >= A.window && r + BN > A.sink);
       tc_wait_ld();
 #pragma unroll
       for (int c = 0; c < BN; c += 32) tc_pin(x + c);
       if (masked) {
-        const uint32_t* jm = X.junk[ev % ST];
-        const int first = r < A.sink ? A.sink - r : 0;     // rows of the tile before it are in the sink
-#pragma unroll
-        for (int c = 0; c < BN; ++c) {
-          bool see = c < rows;
-          if (need_pos) {
-            const int pr = tp[c];
-            see = see && pr <= p && (pr > pold || c < first);
+        // the row's token sees columns [cl, ch) and, of the first rows, [0, cf)
+        int cl = 0, ch = rows, cf = 0;
+        if (need_pos) {
+          auto upto = [&](int pos) {                       // columns with a position <= pos
+            int a = 0, b = rows;
+            while (a < b) {
+              const int mid = (a + b) >> 1;
+              if (tp[mid] <= pos) a = mid + 1; else b = mid;
+            }
+            return a;
+          };
+          ch = upto(p);
+          if (A.window > 0) {
+            cl = min(ch, upto(pold));
+            cf = min(ch, max(0, A.sink - r));
           }
-          if (!see) x[c] = 0xFF800000u;                    // -inf
-          else if ((jm[c >> 5] >> (c & 31)) & 1u) poison = true;
         }
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          if (c >= ch || (c < cl && c >= cf)) x[c] = 0xFF800000u;   // -inf
+        const uint32_t* jm = X.junk[ev % ST];
+        if (jm[0] | jm[1] | jm[2] | jm[3])
+          for (int c = 0; c < rows; ++c)
+            if (((jm[c >> 5] >> (c & 31)) & 1u) && c < ch && (c >= cl || c < cf)) poison = true;
       }
       float tops[4];
 #pragma unroll
@@ -662,11 +733,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
           l *= a;
         }
         if (i > 0) {
-          if constexpr (QT == 1) {                         // the sums of the tile before are still running
-            ok = wait(b_o, (i - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-          }
+          ok = wait(&b_o[q], (i - 1) & 1);                 // the sums of the tile before may be running
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < HD; c += 16) {
             uint32_t o[16];
@@ -703,15 +772,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     }
     // ---- results
     if (ok && nt > 0) {
-      if constexpr (QT == 2) ok = wait(b_o, 0);
-      else ok = (nt < 2 || wait(b_o, (nt - 2) & 1)) && wait(b_o, (nt - 1) & 1);
+      ok = wait(&b_f[q], 0);
       tc_fence_after();
     }
     if (ok) {
       const bool split = A.split > 1;
       float* slot = A.part + ((int64_t)y * A.split + part) * (QT * 128) * (HD + 2) + (q * 128 + m);
       const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
+      // a row leaves through shared memory in one copy (padded rows: no bank
+      // conflicts), in the place of the queries: every score is done when
+      // b_f is, and with the last tile's sums everything is,
+      // whose rows reach past the queries into the ring
+      uint8_t* row_out = smem + H::oQ + (q * 128 + m) * (HD * 2 + 16);
+#pragma unroll 2
       for (int c = 0; c < HD; c += 32) {
         uint32_t o[32];
         if (nt > 0) {
@@ -729,8 +802,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         if (split) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) slot[(int64_t)(2 + c + k) * (QT * 128)] = __uint_as_float(o[k]);
-        } else if (on) {
-          uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD + c);
+        } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
@@ -745,9 +817,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
                 w[e] = *reinterpret_cast<const uint32_t*>(&h);
               }
             }
-            d[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(row_out + c * 2 + k * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+      }
+      if (!split && on) {
+        fence_proxy_async_smem();
+        bulk_s2g(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD, row_out, HD * 2);
+        bulk_commit();
+        bulk_wait_all();
       }
       if (split) {
         slot[0] = M;
