@@ -177,21 +177,18 @@ struct TileLoader {
   static constexpr bool kQ = T != TRIA_F16;
   static constexpr int kUnits = T == TRIA_F16 ? BN * HD / 8 / 128 : (T == TRIA_Q8_0 ? BN * HD / 16 / 128 : BN * HD / 32 / 128);
   uint4 u[kQ ? kUnits : 1];
-  uint32_t s[kQ ? kUnits : 1];     // the unit's scale, twice
+  uint32_t s[kQ ? kUnits : 1];     // the unit's scale (as loaded: nothing waits for it before its turn)
 
   __device__ __forceinline__ void fetch(const uint8_t* data, const uint8_t* scale, int64_t row, int rows, int tid) {
     if constexpr (kQ) {
       constexpr int per = T == TRIA_Q8_0 ? HD / 16 : HD / 32;
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const int x = i * 128 + tid, r = x / per, c = x - r * per;
-        u[i] = make_uint4(0, 0, 0, 0);
-        s[i] = 0;
-        if (r < rows) {
-          u[i] = *reinterpret_cast<const uint4*>(data + ((row + r) * per + c) * 16);
-          const uint32_t h = reinterpret_cast<const uint16_t*>(scale)[(row + r) * (HD / 32) + (T == TRIA_Q8_0 ? c / 2 : c)];
-          s[i] = h | (h << 16);
-        }
+        // (rows past the last one: a row that exists, its scale is replaced when stored)
+        const int x = i * 128 + tid, c = x % per;
+        const int64_t r = row + min(x / per, rows - 1);
+        u[i] = __ldg(reinterpret_cast<const uint4*>(data + (r * per + c) * 16));
+        s[i] = __ldg(reinterpret_cast<const uint16_t*>(scale) + r * (HD / 32) + (T == TRIA_Q8_0 ? c / 2 : c));
       }
     }
   }
@@ -224,13 +221,13 @@ struct TileLoader {
       }
     }
   }
-  __device__ __forceinline__ void store(uint8_t* tile, bool cleaned, uint32_t* marks, int tid) {
+  __device__ __forceinline__ void store(uint8_t* tile, int rows, bool cleaned, uint32_t* marks, int tid) {
     constexpr int per = T == TRIA_Q8_0 ? HD / 16 : HD / 32;
 #pragma unroll
     for (int i = 0; i < (kQ ? kUnits : 0); ++i) {
       const int x = i * 128 + tid, r = x / per, c = x - r * per;
       const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-      uint32_t sc = s[i];
+      uint32_t sc = r < rows ? s[i] | (s[i] << 16) : 0u;
       auto mul = [&](uint32_t a) {
         uint32_t d;
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(sc));
@@ -617,7 +614,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       ok = free_stage(ek);
       if (!ok) break;
       if constexpr (kKq) {
-        lk.store(stage(ek), false, nullptr, tid);
+        lk.store(stage(ek), rows, false, nullptr, tid);
         full(ek);
         if (i + 1 < nt) {
           int rows2;
@@ -633,7 +630,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       side(i);
       const bool all = whole(i);
       if constexpr (kVq) {
-        lv.store(stage(ev), !all, X.junk[ev % ST], tid);
+        lv.store(stage(ev), rows, !all, X.junk[ev % ST], tid);
         full(ev);
       } else if (all) {
         if (tid == 0) lv.copy(stage(ev), &map_v, row0 + r, &b_full[ev % ST]);
