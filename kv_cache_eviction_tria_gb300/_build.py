@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(ROOT, "_build", "tria")
 
 SOURCES = ["api.cu", "stats.cu", "score.cu", "select.cu", "compact.cu", "noalloc.cu", "calib.cu", "lifecycle.cu",
            "shared.cu", "pass_f16.cu", "pass_q8.cu", "rope.cu", "attend.cu"] + \
-          [f"attend_{p}_{k}_{v}.cu" for p in ("step", "prompt") for k in ("f16", "q8", "q4") for v in ("f16", "q8", "q4")]
+          ["attend_prompt.cu"] + [f"attend_step_{k}_{v}.cu" for k in ("f16", "q8", "q4") for v in ("f16", "q8", "q4")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

@@ -304,7 +304,7 @@ int sm_count() {
 // and the space of the partial results. The layout covers every type of
 // queries.
 struct AttendLayout {
-  size_t count, part, total;
+  size_t count, part, wide_k, wide_v, total;
   int units, split, prompt_split, sms;
 };
 
@@ -329,12 +329,16 @@ int prompt_split(int64_t units, int cap_max, int sms) {
 AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0) {
   AttendLayout L{};
   int64_t units = 0, prompts = 0;
+  int64_t wide = 0;    // rows of the prompts' sequences
   int cap_max = 0, cols = 0;
   for (int s = 0; s < c->n_seqs; ++s) {
     const int64_t x = (int64_t)(tok0[s + 1] - tok0[s]) * G;
     units += (x + kCols - 1) / kCols;
     if (x <= kStepCols) cols = std::max(cols, (int)x);
-    else prompts += (x + prompt_cols(c->head_dim) - 1) / prompt_cols(c->head_dim);
+    else {
+      prompts += (x + prompt_cols(c->head_dim) - 1) / prompt_cols(c->head_dim);
+      wide += (int64_t)c->n_kv_heads * c->capacity[s];
+    }
     cap_max = std::max(cap_max, c->capacity[s]);
   }
   L.sms = sm_count();
@@ -347,7 +351,11 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   L.prompt_split = prompt_split(prompts * c->n_kv_heads, cap_max, L.sms);
   const size_t prompt = L.prompt_split > 1
       ? (size_t)(prompts * c->n_kv_heads) * L.prompt_split * prompt_cols(c->head_dim) * (c->head_dim + 2) : 0;
-  L.total = up256(L.part + sizeof(float) * std::max(std::max(plain, step), prompt));
+  L.wide_k = up256(L.part + sizeof(float) * std::max(std::max(plain, step), prompt));
+  const size_t plane = up256((size_t)wide * c->head_dim * 2);
+  const bool tensor = tensor_types(c, TRIA_F16);
+  L.wide_v = L.wide_k + (tensor && c->k_type != TRIA_F16 ? plane : 0);
+  L.total = L.wide_v + (tensor && c->v_type != TRIA_F16 ? plane : 0);
   return L;
 }
 
@@ -359,15 +367,6 @@ cudaError_t launch_step(const AttendArgs& A, int cols, int workers, cudaStream_t
       {launch_attend_step_q4_f16, launch_attend_step_q4_q8, launch_attend_step_q4_q4}};
   static_assert(TRIA_F16 == 1 && TRIA_Q8_0 == 2 && TRIA_Q4_0 == 3, "table order");
   return fn[A.k_type - 1][A.v_type - 1](A, cols, workers, st);
-}
-
-cudaError_t launch_prompt(const AttendArgs& A, cudaStream_t st) {
-  using Fn = cudaError_t (*)(const AttendArgs&, cudaStream_t);
-  static constexpr Fn fn[3][3] = {
-      {launch_attend_prompt_f16_f16, launch_attend_prompt_f16_q8, launch_attend_prompt_f16_q4},
-      {launch_attend_prompt_q8_f16, launch_attend_prompt_q8_q8, launch_attend_prompt_q8_q4},
-      {launch_attend_prompt_q4_f16, launch_attend_prompt_q4_q8, launch_attend_prompt_q4_q4}};
-  return fn[A.k_type - 1][A.v_type - 1](A, st);
 }
 
 tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const int32_t* tok0) {
@@ -452,12 +451,15 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   // each kernel sees the sequences it takes, the others without tokens
   auto take = [&](int path) {
     const int per = path == kPathPrompt ? prompt_cols(hd) : kCols;
+    int64_t wide = 0;
     units = 0;
     for (int s = 0; s < cache->n_seqs; ++s) {
       const int t = a->tok0[s + 1] - a->tok0[s];
       A.seq[s].t = path_of(tensor, t, G) == path ? t : 0;
       A.seq[s].unit0 = units;
+      A.seq[s].wide0 = wide;
       units += (A.seq[s].t * G + per - 1) / per;
+      if (A.seq[s].t > 0) wide += (int64_t)cache->n_kv_heads * cache->capacity[s];
     }
     A.units = units;
   };
@@ -469,7 +471,9 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   if (prompt) {
     take(kPathPrompt);
     A.split = L.prompt_split;
-    if (launch_prompt(A, st) != cudaSuccess) return TRIA_ERR_CUDA;
+    if (cache->k_type != TRIA_F16) A.wide_k = (uint16_t*)((uint8_t*)ws + L.wide_k);
+    if (cache->v_type != TRIA_F16) A.wide_v = (uint16_t*)((uint8_t*)ws + L.wide_v);
+    if (launch_attend_prompt(A, st) != cudaSuccess) return TRIA_ERR_CUDA;
   }
   if (plain) {
     take(kPathPlain);

@@ -30,6 +30,7 @@ inline tria_status check_tokens(const int32_t* tok0, int n_seqs) {
 // One attention call, passed by value.
 struct AttendSeq {
   int64_t row0;
+  int64_t wide0;      // first of its rows in the widened planes
   int32_t cap;
   int32_t tok0;       // first token of the sequence in q / out / pos
   int32_t t;          // its tokens
@@ -51,6 +52,8 @@ struct AttendArgs {
   Ctrl* ctrl;
   uint32_t* count;     // arrivals per unit, zero between calls
   float* part;         // partial results of split units
+  uint16_t* wide_k;    // fp16 copies of quantised planes (prompts; NULL: none)
+  uint16_t* wide_v;
   int32_t n_seqs, n_kv, G, hd, nq;
   int32_t type, k_type, v_type;
   int32_t window, sink;
@@ -72,17 +75,9 @@ cudaError_t launch_attend_step_q8_q4(const AttendArgs& A, int cols, int workers,
 cudaError_t launch_attend_step_q4_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 cudaError_t launch_attend_step_q4_q8(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 cudaError_t launch_attend_step_q4_q4(const AttendArgs& A, int cols, int workers, cudaStream_t st);
-// attend_prompt_*.cu: units of prompt_cols(hd) columns
+// attend_prompt.cu: units of prompt_cols(hd) columns
 inline int prompt_cols(int hd) { return hd == 256 ? 128 : 256; }
-cudaError_t launch_attend_prompt_f16_f16(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_f16_q8(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_f16_q4(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_q8_f16(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_q8_q8(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_q8_q4(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_q4_f16(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_q4_q8(const AttendArgs& A, cudaStream_t st);
-cudaError_t launch_attend_prompt_q4_q4(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_prompt(const AttendArgs& A, cudaStream_t st);
 
 __device__ __forceinline__ float act_load(const void* p, int type, int64_t i) {
   if (type == TRIA_F32) return reinterpret_cast<const float*>(p)[i];

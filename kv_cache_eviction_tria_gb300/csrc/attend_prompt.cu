@@ -8,8 +8,8 @@
 // key tile is read once for the whole group. Per CTA (one per SM): two such
 // tiles with a softmax warpgroup each (one tile at head_dim 256, where two
 // outputs would fill TMEM, with two score buffers), so that the tensor cores
-// work on one tile while the other is in its softmax; a warpgroup that fills a
-// ring of key and value tiles; one thread that issues the products. What
+// work on one tile while the other is in its softmax; threads that keep a ring
+// of key and value tiles filled; one thread that issues the products. What
 // bounds it is the tensor cores' rate together with one exponential per score.
 //
 // A thread owns a row of S: maximum and sum need no shuffles. The reference M
@@ -18,14 +18,17 @@
 // the common factor cancels in O / l: rescaling O costs a pass over TMEM and is
 // rare this way.
 //
-// fp16 rows come by TMA into 128-byte-swizzled tiles; 8- and 4-bit ones are
-// rounded to fp16 once (code x scale) by the loading warpgroup on their way
-// there. In tiles that some token does not see whole, value rows past the last
-// one become zeros, and one that holds an infinity or NaN is replaced by zeros
+// Tiles come by TMA into 128-byte-swizzled shared memory, so the planes are
+// fp16: 8- and 4-bit rows are rounded to fp16 once (code x scale) into the
+// workspace first (k_widen), 128 rows of them being read again by every 256
+// columns. Converting them tile by tile on their way into shared memory, which
+// the products' operands already fill to its rate, held a pair of tiles at 2.3
+// (q4_0) and 3.2 us (q8_0) instead of 1.7.
+//
+// In tiles that some token does not see whole, value rows past the last one
+// become zeros, and one that holds an infinity or NaN is replaced by zeros
 // while the tokens that do see it get NaN, so that hidden junk never meets a
 // weight of zero.
-#pragma once
-
 #include <cuda.h>
 #include <string.h>
 
@@ -35,6 +38,8 @@
 #include "attend_internal.cuh"
 
 namespace tria {
+
+namespace {
 
 template <int HD>
 struct PromptShape {
@@ -64,17 +69,14 @@ struct PromptShared {
 constexpr int kPromptBars = 2 * 8 + 4 + 4 + 2 + 2 + 3;
 static_assert(kPromptBars * 8 + sizeof(PromptShared) <= 512, "barriers and shared state");
 
-constexpr int kPromptThreads = 512;
-
-// Registers of a thread by warpgroup: a row of 128 scores stays in them, and
-// conversions need more in the loading one. The shares add up to the 4 x 128
-// that the block starts with.
-template <int BN, bool kConvert>
-struct PromptRegs {
-  static constexpr int kSoft = BN == 64 ? 152 : (kConvert ? 168 : 192), kLoad = BN == 64 ? 128 : (kConvert ? 112 : 72),
-                       kIssue = BN == 64 ? 80 : (kConvert ? 64 : 56);
-  static_assert(2 * kSoft + kLoad + kIssue == 512, "register shares");
-};
+// two warpgroups of softmax; one whose first warp loads keys (the others only
+// find the rows); one of which three warps load and look through values and
+// the last issues the products
+constexpr int kPromptThreads = 512, kIssueWarp = 15, kLoadV = 96, kPromptRegs = 128;
+// registers of a thread in the softmax (a row of 128 scores stays in them) and
+// in the other warpgroups, cut from what the block starts with
+constexpr int kSoftRegs = 192, kOtherRegs = 64;
+static_assert(2 * kSoftRegs + 2 * kOtherRegs == 4 * kPromptRegs, "register shares");
 
 constexpr float kLazy = 8.f, kShift = 5.f;
 
@@ -169,116 +171,45 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Rows r .. r + rows of a plane into a tile of fp16 in shared memory (zeros
-// past `rows`), by the 128 threads of the loading warpgroup. Quantised rows
-// are fetched into registers ahead of their turn.
-template <int T, int HD, int BN>
-struct TileLoader {
-  static constexpr bool kQ = T != TRIA_F16;
-  static constexpr int kUnits = T == TRIA_F16 ? BN * HD / 8 / 128 : (T == TRIA_Q8_0 ? BN * HD / 16 / 128 : BN * HD / 32 / 128);
-  uint4 u[kQ ? kUnits : 1];
-  uint32_t s[kQ ? kUnits : 1];     // the unit's scale (as loaded: nothing waits for it before its turn)
+// Starts the copies of rows row .. row + BN of a plane into a tile, arriving on `bar`.
+template <int HD, int BN>
+__device__ __forceinline__ void copy_tile(uint8_t* tile, const CUtensorMap* map, int64_t row, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, BN * HD * 2);
+#pragma unroll
+  for (int c = 0; c < HD / 64; ++c)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(tile) + c * (BN * 128)),
+        "l"(map), "r"(c * 64), "r"((int)row), "r"(smem_u32(bar))
+        : "memory");
+}
 
-  __device__ __forceinline__ void fetch(const uint8_t* data, const uint8_t* scale, int64_t row, int rows, int tid) {
-    if constexpr (kQ) {
-      constexpr int per = T == TRIA_Q8_0 ? HD / 16 : HD / 32;
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        // (rows past the last one: a row that exists, its scale is replaced when stored)
-        const int x = i * 128 + tid, c = x % per;
-        const int64_t r = row + min(x / per, rows - 1);
-        u[i] = __ldg(reinterpret_cast<const uint4*>(data + (r * per + c) * 16));
-        s[i] = __ldg(reinterpret_cast<const uint16_t*>(scale) + r * (HD / 32) + (T == TRIA_Q8_0 ? c / 2 : c));
-      }
-    }
-  }
-  // fp16: starts the copies of rows row .. row + BN, arriving on `bar`
-  static __device__ __forceinline__ void copy(uint8_t* tile, const CUtensorMap* map, int64_t row, uint64_t* bar) {
-    mbar_arrive_expect_tx(bar, BN * HD * 2);
-#pragma unroll
-    for (int c = 0; c < HD / 64; ++c)
-      asm volatile(
-          "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-              smem_u32(tile) + c * (BN * 128)),
-          "l"(map), "r"(c * 64), "r"((int)row), "r"(smem_u32(bar))
-          : "memory");
-  }
-  // rows past `rows` and values with junk become zeros, the latter's rows are marked
-  __device__ __forceinline__ void clean(uint8_t* tile, int rows, uint32_t* marks, int tid) {
-    constexpr int per = HD / 8;
+// Values past `rows` and those with junk become zeros; the latter's rows are
+// marked. By kLoadV threads.
+template <int HD, int BN>
+__device__ __forceinline__ void clean_tile(uint8_t* tile, int rows, uint32_t* marks, int tid) {
+  constexpr int per = HD / 8;
 #pragma unroll 4
-    for (int i = 0; i < kUnits; ++i) {
-      const int x = i * 128 + tid, r = x / per, c = x - r * per;
-      uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * (BN * 128) + swz(r, c & 7));
-      if (r >= rows) {
-        *p = make_uint4(0, 0, 0, 0);
-        continue;
-      }
-      const uint4 v = *p;
-      if (junk_h2(v.x) || junk_h2(v.y) || junk_h2(v.z) || junk_h2(v.w)) {
-        *p = make_uint4(0, 0, 0, 0);
-        atomicOr(&marks[r >> 5], 1u << (r & 31));
-      }
+  for (int x = tid; x < BN * per; x += kLoadV) {
+    const int r = x / per, c = x - r * per;
+    uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * (BN * 128) + swz(r, c & 7));
+    if (r >= rows) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 v = *p;
+    if (junk_h2(v.x) || junk_h2(v.y) || junk_h2(v.z) || junk_h2(v.w)) {
+      *p = make_uint4(0, 0, 0, 0);
+      atomicOr(&marks[r >> 5], 1u << (r & 31));
     }
   }
-  __device__ __forceinline__ void store(uint8_t* tile, int rows, bool cleaned, uint32_t* marks, int tid) {
-    constexpr int per = T == TRIA_Q8_0 ? HD / 16 : HD / 32;
-#pragma unroll
-    for (int i = 0; i < (kQ ? kUnits : 0); ++i) {
-      const int x = i * 128 + tid, r = x / per, c = x - r * per;
-      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-      uint32_t sc = r < rows ? s[i] | (s[i] << 16) : 0u;
-      auto mul = [&](uint32_t a) {
-        uint32_t d;
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(sc));
-        return d;
-      };
-      auto sub = [&](uint32_t a, uint32_t b) {
-        uint32_t d;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-        return d;
-      };
-      if (cleaned && junk_h2(sc)) {
-        sc = 0;
-        atomicOr(&marks[r >> 5], 1u << (r & 31));
-      }
-      if constexpr (T == TRIA_Q8_0) {
-        uint32_t h[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t b = w[k] ^ 0x80808080u;           // 0x64, code + 128: 1152 + code
-          h[2 * k] = mul(sub(__byte_perm(b, 0x64646464u, 0x4140), 0x64806480u));
-          h[2 * k + 1] = mul(sub(__byte_perm(b, 0x64646464u, 0x4342), 0x64806480u));
-        }
-        uint8_t* blk = tile + (c >> 2) * (BN * 128);
-        *reinterpret_cast<uint4*>(blk + swz(r, (2 * c) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(blk + swz(r, (2 * c + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
-      } else {
-        uint8_t* blk = tile + (c >> 1) * (BN * 128);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {             // dims 0..15 in the low halves, 16..31 in the high ones
-          uint32_t h[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t b = (half ? w[k] >> 4 : w[k]) & 0x0F0F0F0Fu;
-            h[2 * k] = mul(sub(__byte_perm(b, 0x64646464u, 0x4140), 0x64086408u));
-            h[2 * k + 1] = mul(sub(__byte_perm(b, 0x64646464u, 0x4342), 0x64086408u));
-          }
-          const int c0 = 4 * (c & 1) + 2 * half;
-          *reinterpret_cast<uint4*>(blk + swz(r, c0)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(blk + swz(r, c0 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
-      }
-    }
-  }
-};
+}
 
-template <int KT, int VT, int HD>
+template <int HD>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __grid_constant__ AttendArgs A,
                                                                      const __grid_constant__ CUtensorMap map_k,
                                                                      const __grid_constant__ CUtensorMap map_v) {
   using H = PromptShape<HD>;
-  using R = PromptRegs<H::BN, KT != TRIA_F16 || VT != TRIA_F16>;
   constexpr int QT = H::QT, BN = H::BN, NB = H::NB, ST = H::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
@@ -316,7 +247,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
   }
   const int c0 = (unit - S.unit0) * (QT * 128), ncol = min(QT * 128, S.t * A.G - c0);
   const int tok_a = c0 / A.G, tok_b = (c0 + ncol - 1) / A.G;   // its tokens (of the sequence)
-  const int64_t row0 = S.row0 + (int64_t)g * S.cap;
+  const int64_t row0 = S.row0 + (int64_t)g * S.cap, seg0 = (int64_t)g * S.cap;
+  const int64_t key0 = seg0 + (A.wide_k ? S.wide0 : S.row0), value0 = seg0 + (A.wide_v ? S.wide0 : S.row0);
   const int32_t* rpos = A.cpos + row0;
   if (threadIdx.x == 0) {
     X.pmin = INT32_MAX;
@@ -342,7 +274,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     mbar_init(b_raw, 1);
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&X.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -469,10 +401,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     return false;
   };
 
-  if (wg == 3) {
+  if (wg >= 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kIssueWarp) {
     // ---- products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kIssue));
-    if (warp == 12 && nt > 0) {
+    if (nt > 0) {
       // results of waits and addresses are the same in all lanes and kept in
       // such a form (votes, a broadcast): operands of the products then live in
       // uniform registers, without which issuing them was the bottleneck
@@ -564,94 +496,76 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       for (int it = 0; it < (1 << 22) && !mbar_try_wait(b_x, 0); ++it) {
       }
     }
-  } else if (wg == 2) {
-    // ---- key and value tiles
-    if constexpr (R::kLoad < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLoad));
-    const int tid = threadIdx.x - 256;
-    constexpr bool kKq = KT != TRIA_F16, kVq = VT != TRIA_F16;
-    TileLoader<KT, HD, BN> lk;
-    TileLoader<VT, HD, BN> lv;
+  } else if (wg >= 2) {
+    // ---- key tiles (ring entries 2i) and value tiles (2i + 1)
+    const int tid = threadIdx.x & 127;
     auto stage = [&](int e) { return smem + H::oRing + (e % ST) * H::kStage; };
-    auto free_stage = [&](int e) { return e < ST || wait(&b_empty[e % ST], ((e / ST) - 1) & 1); };
-    // the tile of entry e has been written by all threads
-    auto full = [&](int e) {
-      fence_proxy_async_smem();
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (tid == 0) mbar_arrive(&b_full[e % ST]);
+    auto free_stage = [&](int e) {
+      if (e >= ST) wait(&b_empty[e % ST], ((e / ST) - 1) & 1);
     };
-    auto whole = [&](int i) {                              // every token sees every row of tile i
-      int rows;
-      const int r = tile_row(i, rows);
-      if (rows < BN) return false;
-      if (!need_pos) return true;
-      const int32_t* tp = s_pos + (i % H::kPosTiles) * BN;
-      return tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window || r + BN <= A.sink);
-    };
-    // positions and marks go with the value tile, which stays until the weights are used
-    int next_pos = 0;                                      // of this thread's row of the tile to come
-    auto fetch_pos = [&](int i) {
-      int rows;
-      const int r = tile_row(i, rows);
-      next_pos = need_pos && i < nt && tid < BN && tid < rows ? rpos[r + tid] : INT32_MAX;
-    };
-    fetch_pos(0);
-    auto side = [&](int i) {
-      const int e = 2 * i + 1;
-      if (need_pos && tid < BN) s_pos[(i % H::kPosTiles) * BN + tid] = next_pos;
-      fetch_pos(i + 1);
-      if (tid < 4) X.junk[e % ST][tid] = 0;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    };
-    int rows, looked = 0;
-    bool ok = true;
-    if (kKq && nt > 0) {
-      const int r = tile_row(0, rows);
-      lk.fetch(A.k, A.ks, row0 + r, rows, tid);
-    }
-    for (int i = 0; ok && i < nt; ++i) {
-      const int r = tile_row(i, rows), ek = 2 * i, ev = 2 * i + 1;
-      if constexpr (kVq) lv.fetch(A.v, A.vs, row0 + r, rows, tid);
-      ok = free_stage(ek);
-      if (!ok) break;
-      if constexpr (kKq) {
-        lk.store(stage(ek), rows, false, nullptr, tid);
-        full(ek);
-        if (i + 1 < nt) {
-          int rows2;
-          const int r2 = tile_row(i + 1, rows2);
-          lk.fetch(A.k, A.ks, row0 + r2, rows2, tid);
-        }
-      } else {
-        // hidden keys, and those past the last row, only reach logits that the mask replaces
-        if (tid == 0) lk.copy(stage(ek), &map_k, row0 + r, &b_full[ek % ST]);
-      }
-      ok = free_stage(ev);
-      if (!ok) break;
-      side(i);
-      const bool all = whole(i);
-      if constexpr (kVq) {
-        lv.store(stage(ev), rows, !all, X.junk[ev % ST], tid);
-        full(ev);
-      } else if (all) {
-        if (tid == 0) lv.copy(stage(ev), &map_v, row0 + r, &b_full[ev % ST]);
-      } else {
-        if (tid == 0) lv.copy(stage(ev), &map_v, row0 + r, b_raw);
-        ok = wait(b_raw, looked & 1);
-        if (!ok) break;
-        ++looked;
-        lv.clean(stage(ev), rows, X.junk[ev % ST], tid);
-        full(ev);
-      }
-    }
-    // copies still on their way when a wait gave up: those of whole tiles are
-    // waited for by their entries' parity
-    if (*s_abort && tid == 0)
-      for (int e = max(0, 2 * nt - ST); e < 2 * nt; ++e)
+    // after a wait gave up the loops run to their end without waiting (their
+    // threads meet at barriers), start no more copies, and wait, bounded, for
+    // those still on their way
+    auto go = [&] { return tid == 0 && !*s_abort; };
+    auto drain = [&](int first) {
+      if (!*s_abort || tid != 0) return;
+      for (int e = first; e < 2 * nt; e += 2)
         for (int it = 0; it < 1024 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
         }
+    };
+    int rows;
+    if (wg == 2) {
+      if (tid == 0) {
+        for (int i = 0; i < nt; ++i) {
+          // hidden keys, and those past the last row, only reach logits that the mask replaces
+          const int r = tile_row(i, rows), e = 2 * i;
+          free_stage(e);
+          if (go()) copy_tile<HD, BN>(stage(e), &map_k, key0 + r, &b_full[e % ST]);
+        }
+        drain(max(0, 2 * nt - ST) & ~1);
+      }
+    } else {
+      constexpr int kPos = (BN + kLoadV - 1) / kLoadV;
+      int next_pos[kPos];                                  // of this thread's rows of the tile to come
+      auto fetch_pos = [&](int i) {
+        int n_rows;
+        const int r = tile_row(i, n_rows);
+#pragma unroll
+        for (int k = 0; k < kPos; ++k) {
+          const int c = k * kLoadV + tid;
+          next_pos[k] = INT32_MAX;
+          if (need_pos && i < nt && c < n_rows) next_pos[k] = rpos[r + c];
+        }
+      };
+      fetch_pos(0);
+      int looked = 0;
+      for (int i = 0; i < nt; ++i) {
+        const int r = tile_row(i, rows), e = 2 * i + 1;
+        free_stage(e);
+        // positions and marks go with the value tile, which stays until the weights are used
+        const int32_t* tp = s_pos + (i % H::kPosTiles) * BN;
+#pragma unroll
+        for (int k = 0; k < kPos; ++k)
+          if (need_pos && k * kLoadV + tid < BN) s_pos[(i % H::kPosTiles) * BN + k * kLoadV + tid] = next_pos[k];
+        fetch_pos(i + 1);
+        if (tid < 4) X.junk[e % ST][tid] = 0;
+        asm volatile("bar.sync 3, %0;" ::"n"(kLoadV) : "memory");
+        const bool all = rows == BN && (!need_pos || (tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window ||
+                                                                            r + BN <= A.sink)));   // seen whole by every token
+        if (go()) copy_tile<HD, BN>(stage(e), &map_v, value0 + r, all ? &b_full[e % ST] : b_raw);
+        if (all) continue;
+        wait(b_raw, looked & 1);
+        ++looked;
+        clean_tile<HD, BN>(stage(e), rows, X.junk[e % ST], tid);
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 3, %0;" ::"n"(kLoadV) : "memory");
+        if (tid == 0) mbar_arrive(&b_full[e % ST]);
+      }
+      drain(max(1, 2 * nt - ST) | 1);
+    }
   } else if (wg < QT) {
     // ---- softmax: a thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoft));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int q = wg, m = (int)q_row;
     const int p = on ? A.pos[tok] : INT32_MIN;
     // rows at or before it are outside the window
@@ -867,14 +781,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
 // TMA view of an fp16 plane: boxes of 64 dims x `box` rows, 128-byte swizzle
-inline bool plane_map_f16(CUtensorMap* m, const void* base, int hd, int64_t rows, int box) {
+bool plane_map_f16(CUtensorMap* m, const void* base, int hd, int64_t rows, int box) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -894,37 +808,129 @@ inline bool plane_map_f16(CUtensorMap* m, const void* base, int hd, int64_t rows
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KT, int VT, int HD>
-cudaError_t launch_attend_prompt_t(const AttendArgs& A, cudaStream_t st) {
+// ---- quantised planes as fp16 ------------------------------------------------
+
+constexpr int kWidenRows = 64;   // rows of a block
+
+// Rows of the prompt's sequences as fp16 (code x scale, rounded once), eight
+// values a thread; rows that no token sees are left out. Bound by the fp16
+// rows' way to memory.
+template <int T>
+__device__ __forceinline__ void widen_rows(const uint8_t* data, const uint8_t* scale, uint16_t* out, int64_t src, int64_t dst, int rows,
+                                           int hd) {
+  const int per = hd / 8;
+#pragma unroll 4
+  for (int x = threadIdx.x; x < rows * per; x += blockDim.x) {
+    const int r = x / per, c = x - r * per;
+    const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(scale) + (src + r) * (hd / 32) + c / 4);
+    const uint32_t sc = h | (h << 16);
+    uint32_t o[4];
+    uint2 w;
+    if constexpr (T == TRIA_Q8_0) {
+      w = __ldg(reinterpret_cast<const uint2*>(data + (src + r) * hd + c * 8));
+      w.x ^= 0x80808080u;                                  // 0x64, code + 128: 1152 + code
+      w.y ^= 0x80808080u;
+    } else {
+      // dims 0..15 of a block in the low halves of its 16 bytes, 16..31 in the high ones
+      w = __ldg(reinterpret_cast<const uint2*>(data + (src + r) * (hd / 2) + (c / 4) * 16 + (c & 1) * 8));
+      if (c & 2) {
+        w.x >>= 4;
+        w.y >>= 4;
+      }
+      w.x &= 0x0F0F0F0Fu;
+      w.y &= 0x0F0F0F0Fu;
+    }
+    const uint32_t bias = T == TRIA_Q8_0 ? 0x64806480u : 0x64086408u;
+    const uint32_t b[4] = {__byte_perm(w.x, 0x64646464u, 0x4140), __byte_perm(w.x, 0x64646464u, 0x4342),
+                           __byte_perm(w.y, 0x64646464u, 0x4140), __byte_perm(w.y, 0x64646464u, 0x4342)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(b[k]), "r"(bias));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(o[k]), "r"(sc));
+    }
+    *reinterpret_cast<uint4*>(out + (dst + r) * hd + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+__global__ void __launch_bounds__(256) k_widen(const __grid_constant__ AttendArgs A, uint16_t* wide_k, uint16_t* wide_v) {
+  __shared__ int s_min;
+  const int g = blockIdx.y;
+  // blocks of a sequence follow those of the ones before it
+  int s = 0, b = blockIdx.x;
+  for (; s < A.n_seqs; ++s) {
+    const int nb = A.seq[s].t > 0 ? (A.seq[s].cap + kWidenRows - 1) / kWidenRows : 0;
+    if (b < nb) break;
+    b -= nb;
+  }
+  if (s == A.n_seqs) return;
+  const AttendSeq& S = A.seq[s];
+  const int n = *((volatile const int32_t*)(A.n_live + s)), r0 = b * kWidenRows;
+  if (n > S.cap || r0 >= n) return;
+  const int rows = min(kWidenRows, n - r0);
+  const int64_t seg0 = (int64_t)g * S.cap;
+  if (A.window > 0 && r0 >= A.sink) {
+    if (threadIdx.x == 0) s_min = INT32_MAX;
+    __syncthreads();
+    int p = INT32_MAX;
+    for (int i = threadIdx.x; i < S.t; i += blockDim.x) p = min(p, A.pos[S.tok0 + i]);
+    p = __reduce_min_sync(0xffffffffu, p);
+    if ((threadIdx.x & 31) == 0) atomicMin(&s_min, p);
+    __syncthreads();
+    if ((int64_t)s_min - A.cpos[S.row0 + seg0 + r0 + rows - 1] >= A.window) return;
+  }
+  const int64_t src = S.row0 + seg0 + r0, dst = S.wide0 + seg0 + r0;
+  if (blockIdx.z == 0) {
+    if (A.k_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0>(A.k, A.ks, wide_k, src, dst, rows, A.hd);
+    else if (A.k_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0>(A.k, A.ks, wide_k, src, dst, rows, A.hd);
+  } else {
+    if (A.v_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0>(A.v, A.vs, wide_v, src, dst, rows, A.hd);
+    else if (A.v_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0>(A.v, A.vs, wide_v, src, dst, rows, A.hd);
+  }
+}
+
+template <int HD>
+cudaError_t launch_prompt_hd(const AttendArgs& A, cudaStream_t st) {
   using H = PromptShape<HD>;
-  auto kern = k_attend_prompt<KT, VT, HD>;
-  const int smem = H::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern = k_attend_prompt<HD>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, H::kSmem);
   if (e != cudaSuccess) return e;
-  // the warpgroups' register shares (PromptRegs) are cut from the 128 a
-  // thread that the block starts with
+  // the warpgroups' register shares are cut from what the block starts with
   cudaFuncAttributes attr;
   const cudaError_t e2 = cudaFuncGetAttributes(&attr, kern);
   if (e2 != cudaSuccess) return e2;
-  if (attr.numRegs != 128) return cudaErrorInvalidConfiguration;
+  if (attr.numRegs != kPromptRegs) return cudaErrorInvalidConfiguration;
   const int64_t grid = (int64_t)A.units * A.n_kv * A.split;
   CUtensorMap mk, mv;
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));
-  int64_t rows = 0;
-  for (int s = 0; s < A.n_seqs; ++s) rows = std::max(rows, A.seq[s].row0 + (int64_t)A.n_kv * A.seq[s].cap);
-  if ((KT == TRIA_F16 && !plane_map_f16(&mk, A.k, HD, rows, H::BN)) || (VT == TRIA_F16 && !plane_map_f16(&mv, A.v, HD, rows, H::BN)))
+  int64_t rows = 0, wide = 0;
+  for (int s = 0; s < A.n_seqs; ++s) {
+    rows = std::max(rows, A.seq[s].row0 + (int64_t)A.n_kv * A.seq[s].cap);
+    wide = std::max(wide, A.seq[s].wide0 + (int64_t)A.n_kv * A.seq[s].cap);
+  }
+  if (!plane_map_f16(&mk, A.wide_k ? (const void*)A.wide_k : A.k, HD, A.wide_k ? wide : rows, H::BN) ||
+      !plane_map_f16(&mv, A.wide_v ? (const void*)A.wide_v : A.v, HD, A.wide_v ? wide : rows, H::BN))
     return cudaErrorInvalidValue;
-  kern<<<(unsigned)grid, kPromptThreads, smem, st>>>(A, mk, mv);
+  kern<<<(unsigned)grid, kPromptThreads, H::kSmem, st>>>(A, mk, mv);
   return cudaGetLastError();
 }
 
-template <int KT, int VT>
-cudaError_t launch_attend_prompt_kv(const AttendArgs& A, cudaStream_t st) {
+}  // namespace
+
+cudaError_t launch_attend_prompt(const AttendArgs& A, cudaStream_t st) {
+  if (A.wide_k || A.wide_v) {
+    int64_t blocks = 0;
+    for (int s = 0; s < A.n_seqs; ++s)
+      if (A.seq[s].t > 0) blocks += (A.seq[s].cap + kWidenRows - 1) / kWidenRows;
+    const dim3 grid((unsigned)blocks, A.n_kv, 2);
+    if (blocks > 0) k_widen<<<grid, 256, 0, st>>>(A, A.wide_k, A.wide_v);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   switch (A.hd) {
-    case 64: return launch_attend_prompt_t<KT, VT, 64>(A, st);
-    case 128: return launch_attend_prompt_t<KT, VT, 128>(A, st);
-    case 256: return launch_attend_prompt_t<KT, VT, 256>(A, st);
+    case 64: return launch_prompt_hd<64>(A, st);
+    case 128: return launch_prompt_hd<128>(A, st);
+    case 256: return launch_prompt_hd<256>(A, st);
   }
   return cudaErrorInvalidValue;
 }
