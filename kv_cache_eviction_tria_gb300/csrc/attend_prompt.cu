@@ -64,7 +64,7 @@ struct PromptShape {
 struct PromptShared {
   uint32_t junk[8][4];                                     // rows of a value tile that held junk, by stage
   uint32_t tmem, abort;
-  int32_t pmin, pmax, hi, last;
+  int32_t pmin, pmax, hi, pad;
 };
 constexpr int kPromptBars = 2 * 8 + 4 + 4 + 2 + 2 + 3;
 static_assert(kPromptBars * 8 + sizeof(PromptShared) <= 512, "barriers and shared state");
@@ -163,6 +163,15 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) { return (uint32_t)(
 
 __device__ __forceinline__ bool junk_h2(uint32_t w) {     // an infinity or NaN in a pair of fp16
   return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
+}
+
+__device__ __forceinline__ uint32_t pack_out(int type, float a, float b) {   // a pair of the output's type
+  if (type == TRIA_F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -718,16 +727,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = __uint_as_float(o[8 * k + 2 * e]) * inv, b = __uint_as_float(o[8 * k + 2 * e + 1]) * inv;
-              if (A.type == TRIA_F16) {
-                const __half2 h = __floats2half2_rn(a, b);
-                w[e] = *reinterpret_cast<const uint32_t*>(&h);
-              } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                w[e] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-            }
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_out(A.type, __uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
             *reinterpret_cast<uint4*>(row_out + c * 2 + k * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
@@ -743,39 +744,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         slot[QT * 128] = l;
       } else if (on && A.lse) {
         A.lse[tok * A.nq + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
-      }
-    }
-    if (A.split > 1) {
-      // the last CTA of the unit to arrive merges the parts in order
-      asm volatile("bar.sync 2, %0;" ::"n"(QT * 128) : "memory");
-      if (threadIdx.x == 0) {
-        __threadfence();
-        X.last = atomicAdd(&A.count[y], 1u) == (uint32_t)A.split - 1;
-        __threadfence();
-        if (X.last) A.count[y] = 0u;
-      }
-      asm volatile("bar.sync 2, %0;" ::"n"(QT * 128) : "memory");
-      if (X.last && on) {
-        const int64_t stride = (int64_t)(QT * 128) * (HD + 2);
-        const float* x = A.part + (int64_t)y * A.split * stride + (q * 128 + m);
-        float top = -INFINITY, sum = 0.f;
-        for (int k = 0; k < A.split; ++k) top = fmaxf(top, __ldcg(x + k * stride));
-        const float tb = top == -INFINITY ? 0.f : top;
-        for (int k = 0; k < A.split; ++k) sum = fmaf(__ldcg(x + k * stride + QT * 128), exp2_fast(__ldcg(x + k * stride) - tb), sum);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        for (int c = 0; c < HD; c += 8) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 0.f;
-          for (int k = 0; k < A.split; ++k) {
-            const float f = exp2_fast(__ldcg(x + k * stride) - tb);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(__ldcg(x + k * stride + (int64_t)(2 + c + e) * (QT * 128)), f, v[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) act_store(A.out, A.type, tok * A.out_stride + (int64_t)head * HD + c + e, v[e] * inv);
-        }
-        if (A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       }
     }
     tc_fence_before();
@@ -806,6 +774,51 @@ bool plane_map_f16(CUtensorMap* m, const void* base, int hd, int64_t rows, int b
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---- parts of split units ------------------------------------------------------
+
+constexpr int kJoinDims = 32;    // dims of a block
+
+// Merges the parts of a unit in order: a thread per column, 32 dims a block.
+// (One of the unit's own CTAs doing it alone took longer than all the parts.)
+template <int HD>
+__global__ void __launch_bounds__(PromptShape<HD>::QT * 128) k_join_parts(const __grid_constant__ AttendArgs A) {
+  constexpr int kCols = PromptShape<HD>::QT * 128;
+  const int y = blockIdx.x, unit = y / A.n_kv, g = y - unit * A.n_kv, d0 = blockIdx.y * kJoinDims, c = threadIdx.x;
+  int s = 0, hi_s = A.n_seqs - 1;
+  while (s < hi_s) {
+    const int mid = (s + hi_s + 1) >> 1;
+    if (A.seq[mid].unit0 <= unit) s = mid; else hi_s = mid - 1;
+  }
+  const AttendSeq& S = A.seq[s];
+  const int n = *((volatile const int32_t*)(A.n_live + s)), col = (unit - S.unit0) * kCols + c;
+  if (n < 0 || n > S.cap || col >= S.t * A.G) return;
+  const int64_t stride = (int64_t)kCols * (HD + 2), tok = S.tok0 + col / A.G;
+  const int head = g * A.G + col % A.G;
+  const float* x = A.part + (int64_t)y * A.split * stride + c;
+  float top = -INFINITY, sum = 0.f, v[kJoinDims];
+#pragma unroll
+  for (int e = 0; e < kJoinDims; ++e) v[e] = 0.f;
+  for (int k = 0; k < A.split; ++k) top = fmaxf(top, x[k * stride]);
+  const float tb = top == -INFINITY ? 0.f : top;
+  for (int k = 0; k < A.split; ++k) {
+    const float* p = x + k * stride;
+    const float f = exp2_fast(p[0] - tb);
+    sum = fmaf(p[kCols], f, sum);
+#pragma unroll
+    for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(p[(2 + d0 + e) * kCols], f, v[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD + d0);
+#pragma unroll
+  for (int q = 0; q < kJoinDims / 8; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack_out(A.type, v[8 * q + 2 * e] * inv, v[8 * q + 2 * e + 1] * inv);
+    o[q] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (d0 == 0 && A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ---- quantised planes as fp16 ------------------------------------------------
@@ -912,6 +925,11 @@ cudaError_t launch_prompt_hd(const AttendArgs& A, cudaStream_t st) {
       !plane_map_f16(&mv, A.wide_v ? (const void*)A.wide_v : A.v, HD, A.wide_v ? wide : rows, H::BN))
     return cudaErrorInvalidValue;
   kern<<<(unsigned)grid, kPromptThreads, H::kSmem, st>>>(A, mk, mv);
+  if (A.split > 1) {
+    const cudaError_t e3 = cudaGetLastError();
+    if (e3 != cudaSuccess) return e3;
+    k_join_parts<HD><<<dim3((unsigned)(A.units * A.n_kv), HD / kJoinDims), H::QT * 128, 0, st>>>(A);
+  }
   return cudaGetLastError();
 }
 
