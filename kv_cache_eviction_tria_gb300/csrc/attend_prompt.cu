@@ -64,7 +64,7 @@ struct PromptShape {
 struct PromptShared {
   uint32_t junk[8][4];                                     // rows of a value tile that held junk, by stage
   uint32_t tmem, abort;
-  int32_t pmin, pmax, hi, pad;
+  int32_t pmin, pmax, hi, need_pos;
 };
 constexpr int kPromptBars = 2 * 8 + 4 + 4 + 2 + 2 + 3;
 static_assert(kPromptBars * 8 + sizeof(PromptShared) <= 512, "barriers and shared state");
@@ -259,7 +259,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
   const int64_t row0 = S.row0 + (int64_t)g * S.cap, seg0 = (int64_t)g * S.cap;
   const int64_t key0 = seg0 + (A.wide_k ? S.wide0 : S.row0), value0 = seg0 + (A.wide_v ? S.wide0 : S.row0);
   const int32_t* rpos = A.cpos + row0;
-  if (threadIdx.x == 0) {
+  // loads that need nothing else are on their way before the set-up: a thread
+  // per row of the softmax, its queries; the loading warpgroup, the tokens'
+  // positions and those of the rows around the place where the newest of these
+  // tokens should be (behind it, the later tokens' rows)
+  const uint32_t q_row = threadIdx.x & 127;
+  const int col = c0 + wg * 128 + (int)q_row;
+  const bool on = wg < QT && wg * 128 + (int)q_row < ncol;
+  const int tl = on ? col / A.G : tok_a;
+  const int64_t tok = S.tok0 + tl;
+  const int head = g * A.G + (on ? col - tl * A.G : 0);
+  const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(A.q) + tok * A.q_stride + (int64_t)head * HD);
+  constexpr int kPart = HD / 8 < 16 ? HD / 8 : 16;         // 16-byte pieces held at once
+  uint4 v[kPart];
+  int pl = INT32_MAX, ph = INT32_MIN, before = 0, after = 0;
+  const int h = n - (S.t - 1 - tok_b);
+  if (wg < QT) {
+#pragma unroll
+    for (int c = 0; c < kPart; ++c) v[c] = on ? src[c] : make_uint4(0, 0, 0, 0);
+  } else if (wg == 2) {
+    if (h > 0) before = rpos[h - 1];
+    if (h >= 0 && h < n) after = rpos[h];
+    for (int i = tok_a + (int)q_row; i <= tok_b; i += 128) {
+      const int p = A.pos[S.tok0 + i];
+      pl = min(pl, p);
+      ph = max(ph, p);
+    }
+  }
+  if (threadIdx.x == 480) {                                // the issuing warp's first thread
     X.pmin = INT32_MAX;
     X.pmax = INT32_MIN;
     X.abort = 0;
@@ -288,27 +315,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   __syncthreads();
-  // ---- the softmax warpgroups fetch their queries; the loading one finds the rows
-  const uint32_t q_row = threadIdx.x & 127;                // a thread per row of the softmax
-  const int col = c0 + wg * 128 + (int)q_row;
-  const bool on = wg < QT && wg * 128 + (int)q_row < ncol;
-  const int tl = on ? col / A.G : tok_a;
-  const int64_t tok = S.tok0 + tl;
-  const int head = g * A.G + (on ? col - tl * A.G : 0);
+  // ---- queries into shared memory; the rows that these tokens see
   float sl = A.scale * 1.4426950408889634f;
   if (wg < QT) {
     // as fp16; bf16 ones times a power of two, undone in the logits
-    const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(A.q) + tok * A.q_stride + (int64_t)head * HD);
     uint8_t* dst = smem + H::oQ + wg * H::kQ;
     float f = 1.f;
-    constexpr int kPart = HD / 8 < 16 ? HD / 8 : 16;       // 16-byte pieces held at once
-    uint4 v[kPart];
     if (A.type == TRIA_BF16) {
       uint32_t am = 0;
 #pragma unroll 1
       for (int c0q = 0; c0q < HD / 8; c0q += kPart) {
 #pragma unroll
-        for (int c = 0; c < kPart; ++c) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < kPart; ++c)
+          if (c0q > 0) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < kPart; ++c) {
           const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
@@ -325,7 +344,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
 #pragma unroll 1
     for (int c0q = 0; c0q < HD / 8; c0q += kPart) {
 #pragma unroll
-      for (int c = 0; c < kPart; ++c) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < kPart; ++c)
+        if (HD / 8 > kPart) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int c = 0; c < kPart; ++c) {
         uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
@@ -343,12 +363,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     fence_proxy_async_smem();
     mbar_arrive(b_q);
   } else if (wg == 2) {
-    int pl = INT32_MAX, ph = INT32_MIN;
-    for (int i = tok_a + (int)q_row; i <= tok_b; i += 128) {
-      const int p = A.pos[S.tok0 + i];
-      pl = min(pl, p);
-      ph = max(ph, p);
-    }
     pl = __reduce_min_sync(0xffffffffu, pl);
     ph = __reduce_max_sync(0xffffffffu, ph);
     if (lane == 0) {
@@ -357,11 +371,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     if (warp == 8) {
-      // rows up to the newest token: where the rows behind it are the later
-      // tokens', else by a search in 32 parts
-      const int pmax = *(volatile int32_t*)&X.pmax;
-      const int h = n - (S.t - 1 - tok_b);
-      const bool there = h >= 0 && (h == 0 || rpos[h - 1] <= pmax) && (h == n || rpos[h] > pmax);
+      // rows up to the newest token; where it is not as expected, by a search in 32 parts
+      const int pmin = *(volatile int32_t*)&X.pmin, pmax = *(volatile int32_t*)&X.pmax;
+      const bool there = h >= 0 && (h == 0 || before <= pmax) && (h == n || after > pmax);
       int lo = 0, hi = n;                                  // rows < lo are <= pmax, rows >= hi are not
       if (there) {
         lo = hi = h;
@@ -375,7 +387,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
           if (k < 32) hi = min(hi, lo + step - 1);
         }
       }
-      if (lane == 0) X.hi = lo;
+      if (!there && lo > 0) before = rpos[lo - 1];
+      if (lane == 0) {
+        X.hi = lo;
+        X.need_pos = A.window > 0 || (lo > 0 && before > pmin);
+      }
     }
   }
   tc_fence_before();
@@ -387,7 +403,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
   const int sr = min(A.sink, lo), nt_sink = (sr + BN - 1) / BN;
   const int nt_all = nt_sink + (hi - lo + BN - 1) / BN;
   const int ta = (int)((int64_t)part * nt_all / A.split), nt = (int)((int64_t)(part + 1) * nt_all / A.split) - ta;
-  const bool need_pos = A.window > 0 || (hi > 0 && rpos[hi - 1] > pmin);
+  const bool need_pos = X.need_pos != 0;
   auto tile_row = [&](int i, int& rows) {
     const int j = ta + i;
     if (j < nt_sink) {
@@ -737,7 +753,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         fence_proxy_async_smem();
         bulk_s2g(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD, row_out, HD * 2);
         bulk_commit();
-        bulk_wait_all();
+        bulk_wait_read_all();
       }
       if (split) {
         slot[0] = M;
