@@ -13,11 +13,12 @@
 //
 // Layout: a lane owns 8 pairs of a head (16 values), head_dim / 16 lanes make
 // a head and a warp takes 32 / (lanes per head, rounded up to a power of two)
-// heads at once, so that both members of a pair sit in one lane, loads and
-// stores are 16 bytes wide and the norm is a shuffle reduction. A warp keeps
-// its lanes' sines and cosines over all the heads of a token that it handles:
-// sincospif costs about as much as moving ten heads.
-// Keys on their way into the cache go through shared memory once, because
+// heads at once, so that both members of a pair sit in one lane and the norm
+// is a shuffle reduction. A warp keeps its lanes' sines and cosines over the
+// heads of a token that it handles: they cost about as much as a head. Heads come through shared memory, up to a token's at once: with
+// loads into registers the bytes in flight (16 KB an SM) held the kernel at
+// 2.9 TB/s.
+// Keys on their way into the cache go through shared memory once more, because
 // their quantisation blocks (32 consecutive dims) do not line up with the
 // pairs. The kernels are bound by memory for prompts and by launch latency for
 // single tokens.
@@ -34,7 +35,8 @@ namespace tria {
 
 namespace {
 
-constexpr int kRopeWarps = 8;
+constexpr int kRopeWarps = 16;      // one CTA per SM
+constexpr int kRopeSmem = 226 * 1024, kRopeStageMax = 12288;   // bytes of heads that a warp handles at once
 constexpr int kPartDirect = 0, kPartKey = 1, kPartValue = 2;
 
 struct RopePart {
@@ -50,9 +52,9 @@ struct RopePart {
 struct RopeArgs {
   RopePart part[3];
   int32_t n_parts, n_tokens, groups;   // groups: of all parts, per token
-  int32_t per_warp;                    // groups a warp handles
+  int32_t per_warp, stage;             // groups a warp handles; bytes of its stage
   int32_t hd, rot, layout, lanes;      // lanes: per head, a power of two
-  float eps, mscale;
+  float eps, mscale, inv_hd;
   const unsigned long long* turns;
   const int32_t* pos;
   // cache (append only)
@@ -70,16 +72,13 @@ struct RopeArgs {
   int32_t tok0[kMaxSeqs + 1];
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* x) {
+// eight values as fp32
+__device__ __forceinline__ void load8(const float* p, float* x) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float* x) {
+__device__ __forceinline__ void load8(const __half* p, float* x) {
   const uint4 u = *reinterpret_cast<const uint4*>(p);
   const __half2* h = reinterpret_cast<const __half2*>(&u);
 #pragma unroll
@@ -89,8 +88,7 @@ __device__ __forceinline__ void load8<__half>(const __half* p, float* x) {
     x[2 * i + 1] = f.y;
   }
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
   const uint4 u = *reinterpret_cast<const uint4*>(p);
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -122,6 +120,70 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
   *reinterpret_cast<uint4*>(p) = u;
+}
+
+// Four codes as the bytes of a word, from floats to which kMagic = 1.5 x 2^23
+// has been added: rounding to integers happened in that sum, and the integer
+// lies in the low mantissa bits.
+constexpr float kMagic = 12582912.f;
+__device__ __forceinline__ uint32_t bytes_of(const float* m) {
+  const uint32_t lo = __byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// Codes of 16 values: round(x / d) away from zero (q8_0) and min(15, floor(x / d
+// + 8.5)) (q4_0) of the correctly rounded fp32 quotient, as kMagic + code. x
+// times the reciprocal is within 2^-22 of the quotient relative to it (at most
+// 128), so only within 2^-14 of a border between codes can the two differ, and
+// only then are the divisions made.
+__device__ __forceinline__ void codes_q8(const float* x, float d, float* m) {
+  const float inv = __frcp_rn(d);
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float q = x[i] * inv;
+    m[i] = q + kMagic;
+    far = fmaxf(far, fabsf(q - (m[i] - kMagic)));
+  }
+  if (far <= 0.5f - 0x1p-14f && d >= 0x1p-120f) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m[i] = (d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(x[i], d)), -127.f), 127.f) : 0.f) + kMagic;
+}
+__device__ __forceinline__ void codes_q4(const float* x, float d, float* m) {
+  const float inv = __frcp_rn(d);
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float q = __fadd_rn(__fmul_rn(x[i], inv), 8.5f) - 0.5f;   // floor(q + 0.5) is q rounded, but for borders
+    m[i] = q + kMagic;
+    far = fmaxf(far, fabsf(q - (m[i] - kMagic)));
+    m[i] = fminf(m[i], kMagic + 15.f);
+  }
+  if (far <= 0.5f - 0x1p-14f && fabsf(d) >= 0x1p-120f) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    m[i] = (d != 0.f ? fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[i], d), 8.5f)), 0.f), 15.f) : 8.f) + kMagic;
+}
+
+// cos and sin of 2 pi x / 2^32: the quadrant off the top bits, Taylor's series
+// on what is left (|r| <= pi / 4: 5e-10 and 2e-9 off).
+__device__ __forceinline__ void turn_cos_sin(uint32_t x, float& c, float& s) {
+  const uint32_t quad = (x + 0x20000000u) >> 30;
+  const float r = (float)(int)(x - (quad << 30)) * 1.46291807926715968e-9f;   // 2 pi / 2^32
+  const float z = r * r;
+  float ps = fmaf(z, 2.7557319224e-6f, -1.9841269841e-4f);
+  ps = fmaf(z, ps, 8.3333333333e-3f);
+  ps = fmaf(z, ps, -1.6666666667e-1f);
+  const float sr = fmaf(r * z, ps, r);
+  float pc = fmaf(z, -2.7557319224e-7f, 2.4801587302e-5f);
+  pc = fmaf(z, pc, -1.3888888889e-3f);
+  pc = fmaf(z, pc, 4.1666666667e-2f);
+  pc = fmaf(z, pc, -0.5f);
+  const float cr = fmaf(z, pc, 1.f);
+  const float a = (quad & 1u) ? sr : cr, b = (quad & 1u) ? cr : sr;
+  c = (quad == 1u || quad == 2u) ? -a : a;
+  s = (quad & 2u) ? -b : b;
 }
 
 // 16 consecutive values (dims e0 .. e0 + 15) of a head into cache row `row` of
@@ -157,13 +219,11 @@ __device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_
     const float d = __fdiv_rn(am, 127.f);
     const __half dh = __float2half_rn(d);
     const float ds = __half2float(dh);
-    uint32_t w[4] = {0, 0, 0, 0};
+    float m[16];
+    codes_q8(x, d, m);
+    const uint32_t w[4] = {bytes_of(m), bytes_of(m + 4), bytes_of(m + 8), bytes_of(m + 12)};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float c = d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(x[i], d)), -127.f), 127.f) : 0.f;
-      w[i >> 2] |= ((uint32_t)(int)c & 255u) << (8 * (i & 3));
-      x[i] = c * ds;
-    }
+    for (int i = 0; i < 16; ++i) x[i] = (m[i] - kMagic) * ds;
     if (on) {
       *reinterpret_cast<uint4*>(data + row * hd + e0) = make_uint4(w[0], w[1], w[2], w[3]);
       if (!(e0 & 16)) *sc = dh;
@@ -171,24 +231,32 @@ __device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_
     return;
   }
   // q4_0: scale = m / -8 with m the first value of largest modulus
-  float m = x[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i)
-    if (fabsf(x[i]) > fabsf(m)) m = x[i];
-  const float other = __shfl_xor_sync(0xffffffffu, m, 1);
   const bool upper = (e0 & 16) != 0;
-  const float lo = upper ? other : m, hi = upper ? m : other;
-  m = fabsf(hi) > fabsf(lo) ? hi : lo;
-  const float d = m * -0.125f;
+  float hi = x[0], lo = x[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) {
+    hi = fmaxf(hi, x[i]);
+    lo = fminf(lo, x[i]);
+  }
+  float big = hi > -lo ? hi : lo;
+  if (hi == -lo)                                // both signs: the first one of the lane's values
+#pragma unroll 1
+    for (int i = 15; i >= 0; --i) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k == i && fabsf(x[k]) == hi) big = x[k];
+    }
+  const float other = __shfl_xor_sync(0xffffffffu, big, 1);
+  const float first = upper ? other : big, second = upper ? big : other;
+  big = fabsf(second) > fabsf(first) ? second : first;
+  const float d = big * -0.125f;
   const __half dh = __float2half_rn(d + 0.f);   // an all-zero block's scale is +0
   const float ds = __half2float(dh);
-  uint32_t w[4] = {0, 0, 0, 0};
+  float m[16];
+  codes_q4(x, d, m);
+  const uint32_t w[4] = {bytes_of(m), bytes_of(m + 4), bytes_of(m + 8), bytes_of(m + 12)};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float c = d != 0.f ? fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[i], d), 8.5f)), 0.f), 15.f) : 8.f;
-    w[i >> 2] |= (uint32_t)(int)c << (8 * (i & 3));
-    x[i] = (c - 8.f) * ds;
-  }
+  for (int i = 0; i < 16; ++i) x[i] = (m[i] - kMagic - 8.f) * ds;
   // byte j of a block: code j low, code j + 16 high; the lower lane writes bytes 0..7
   const uint32_t r0 = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[2], 1);
   const uint32_t r1 = __shfl_xor_sync(0xffffffffu, upper ? w[1] : w[3], 1);
@@ -207,20 +275,75 @@ __device__ __forceinline__ uint32_t qkv_error(int n, int t, int cap) {
   return 0u;
 }
 
-template <typename T, bool kCache>
-__global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant__ RopeArgs A) {
-  extern __shared__ float s_key[];    // kCache: [warps][heads per warp][head_dim + 4]
+// A lane's eight pairs: first and second members, two pairs to a register pair
+// (packed fp32 arithmetic).
+struct Pairs {
+  float2 f[4], s[4];
+};
+template <int LAYOUT, typename T>
+__device__ __forceinline__ void load_pairs(const T* head, int ea, int eb, Pairs& v) {
+  float a[8], b[8];
+  load8(head + ea, a);
+  load8(head + eb, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (LAYOUT == TRIA_ROPE_HALF) {
+      v.f[i] = make_float2(a[2 * i], a[2 * i + 1]);
+      v.s[i] = make_float2(b[2 * i], b[2 * i + 1]);
+    } else {
+      const float* x = (i < 2 ? a : b) + (i & 1) * 4;
+      v.f[i] = make_float2(x[0], x[2]);
+      v.s[i] = make_float2(x[1], x[3]);
+    }
+  }
+}
+
+template <typename T, bool kCache, int LAYOUT>
+__global__ void __launch_bounds__(kRopeWarps * 32, 1) k_rope(const __grid_constant__ RopeArgs A) {
+  // per warp: a stage of heads; kCache: [heads of a group][head_dim + 4] floats
+  extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hpw = 32 / A.lanes;                   // heads a warp takes at once
   const int sub = lane / A.lanes, p = lane % A.lanes;
   const bool on_dim = 16 * p < A.hd;
   const int half = A.rot / 2, f0 = 8 * p;
   const bool rotary = f0 < half;
-  const int warps_per_token = (A.groups + A.per_warp - 1) / A.per_warp;
-  const int64_t total = (int64_t)A.n_tokens * warps_per_token;
-  for (int64_t u = (int64_t)blockIdx.x * kRopeWarps + warp; u < total; u += (int64_t)gridDim.x * kRopeWarps) {
-    const int tok = (int)(u / warps_per_token);
-    const int g0 = (int)(u - (int64_t)tok * warps_per_token) * A.per_warp;
+  constexpr bool kInter = LAYOUT != TRIA_ROPE_HALF;
+  const bool to_half = LAYOUT == TRIA_ROPE_INTERLEAVED_TO_HALF && rotary;
+  // this lane's two runs of eight values: the first members of its pairs at
+  // ea, the second ones at eb (consecutive where the pairs are interleaved)
+  const int ea = kInter ? 16 * p : (rotary ? f0 : f0 + half);
+  const int eb = kInter ? 16 * p + 8 : ea + (rotary ? half : (A.hd - A.rot) / 2);
+  const int oa = to_half ? f0 : ea, ob = to_half ? f0 + half : eb;
+  const int head_bytes = A.hd * (int)sizeof(T), group_bytes = hpw * head_bytes;
+  uint8_t* stage = smem + warp * A.stage;
+  float* key_buf = reinterpret_cast<float*>(smem + kRopeWarps * A.stage) + (warp * hpw + sub) * (A.hd + 4);
+  const uint32_t units_per_token = (A.groups + A.per_warp - 1) / A.per_warp;   // (their product fits: checked by the host)
+  const uint32_t total = (uint32_t)A.n_tokens * units_per_token, step = gridDim.x * kRopeWarps;
+  const uint32_t first = blockIdx.x * kRopeWarps + warp;
+
+  // starts the copies of a unit's heads into the stage, group after group
+  auto fetch = [&](uint32_t u) {
+    const int tok = (int)(u / units_per_token), g0 = (int)(u - (uint32_t)tok * units_per_token) * A.per_warp;
+    const int g1 = min(A.groups, g0 + A.per_warp);
+    int base = 0;
+    uint8_t* dst = stage;
+#pragma unroll 1
+    for (int pi = 0; pi < A.n_parts; ++pi) {
+      const RopePart& Q = A.part[pi];
+      const int ga = max(g0 - base, 0), ge = min(g1 - base, Q.groups);
+      base += Q.groups;
+      if (ga >= ge) continue;
+      const int bytes = (min(ge * hpw, Q.heads) - ga * hpw) * head_bytes;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(Q.x) + ((int64_t)tok * Q.x_stride + (int64_t)ga * hpw * A.hd) * (int)sizeof(T);
+      for (int i = lane * 16; i < bytes; i += 512) cp_async16(dst + i, src + i);
+      dst += (ge - ga) * group_bytes;
+    }
+  };
+  for (uint32_t u = first; u < total; u += step) {
+    fetch(u);
+    cp_async_commit();
+    const int tok = (int)(u / units_per_token), g0 = (int)(u - (uint32_t)tok * units_per_token) * A.per_warp;
     const int g1 = min(A.groups, g0 + A.per_warp);
     const int position = A.pos[tok];
     int seq = 0, row = 0;
@@ -237,142 +360,148 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
       row_ok = qkv_error(n, t, A.cap[seq]) == 0u;
       row = n + (tok - A.tok0[seq]);
     }
-    float cs[8], sn[8];
-    bool have = false;
-    for (int g = g0; g < g1; ++g) {
-      int gi = g, pi = 0;
-      while (gi >= A.part[pi].groups) gi -= A.part[pi++].groups;
+    float2 cs[4], sn[4], ns[4];                   // cosines, sines and their negatives of the pairs
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cs[i] = make_float2(1.f, 1.f);
+      sn[i] = make_float2(0.f, 0.f);
+      if (rotary) {
+        const unsigned long long x = (unsigned long long)(long long)position;
+        turn_cos_sin((uint32_t)((x * A.turns[f0 + 2 * i]) >> 32), cs[i].x, sn[i].x);
+        turn_cos_sin((uint32_t)((x * A.turns[f0 + 2 * i + 1]) >> 32), cs[i].y, sn[i].y);
+        cs[i] = make_float2(cs[i].x * A.mscale, cs[i].y * A.mscale);
+        sn[i] = make_float2(sn[i].x * A.mscale, sn[i].y * A.mscale);
+      }
+      ns[i] = make_float2(-sn[i].x, -sn[i].y);
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    const uint8_t* in = stage + sub * head_bytes;
+    int base = 0;
+#pragma unroll 1
+    for (int pi = 0; pi < A.n_parts; ++pi) {
       const RopePart& Q = A.part[pi];
-      const int head = gi * hpw + sub;
-      const bool on = on_dim && head < Q.heads;
-      const T* src = reinterpret_cast<const T*>(Q.x) + (int64_t)tok * Q.x_stride + (int64_t)head * A.hd;
-      float a[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) a[i] = 0.f;
+      const int ga = max(g0 - base, 0), ge = min(g1 - base, Q.groups);
+      base += Q.groups;
+      if (ga >= ge) continue;
+      int head = ga * hpw + sub;
+      T* out = reinterpret_cast<T*>(Q.out) + (int64_t)tok * Q.out_stride + (int64_t)head * A.hd;
       if (kCache && Q.kind == kPartValue) {
-        if (on) {
-          load8<T>(src + 16 * p, a);
-          load8<T>(src + 16 * p + 8, a + 8);
-        }
-        const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
-        hold16(a, A.v_type, A.v, A.vs, r, A.hd, 16 * p, on && row_ok);
-        if (on && row_ok && Q.out) {
-          T* o = reinterpret_cast<T*>(Q.out) + ((int64_t)tok * Q.heads + head) * A.hd + 16 * p;
-          store8<T>(o, a);
-          store8<T>(o + 8, a + 8);
+#pragma unroll 1
+        for (int gi = ga; gi < ge; ++gi, head += hpw, in += group_bytes, out += hpw * A.hd) {
+          const bool on = on_dim && head < Q.heads;
+          // (a lane past head_dim holds zeros; a whole head past the last one, junk
+          // that goes nowhere)
+          float a[16] = {};
+          if (on_dim) {
+            load8(reinterpret_cast<const T*>(in) + 16 * p, a);
+            load8(reinterpret_cast<const T*>(in) + 16 * p + 8, a + 8);
+          }
+          const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
+          hold16(a, A.v_type, A.v, A.vs, r, A.hd, 16 * p, on && row_ok);
+          if (on && row_ok && Q.out) {
+            store8<T>(out + 16 * p, a);
+            store8<T>(out + 16 * p + 8, a + 8);
+          }
         }
         continue;
       }
-      // where the lane's pairs lie: a[0..7] the first members, a[8..15] the second ones
-      const bool inter = A.layout != TRIA_ROPE_HALF;
-      const int ea = inter ? 16 * p : (rotary ? f0 : f0 + half);
-      const int eb = inter ? 16 * p + 8 : ea + (rotary ? half : (A.hd - A.rot) / 2);
-      if (on) {
-        load8<T>(src + ea, a);
-        load8<T>(src + eb, a + 8);
-      }
-      if (Q.norm) {
-        float ss = 0.f;
+      Pairs w;
+      if (Q.norm && on_dim) load_pairs<LAYOUT>(Q.norm, ea, eb, w);
+#pragma unroll 1
+      for (int gi = ga; gi < ge; ++gi, head += hpw, in += group_bytes, out += hpw * A.hd) {
+        const bool on = on_dim && head < Q.heads;
+        Pairs a = {};
+        if (on_dim) load_pairs<LAYOUT>(reinterpret_cast<const T*>(in), ea, eb, a);
+        if (Q.norm) {
+          float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(a[i], a[i], ss);
-        for (int o = 1; o < A.lanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = rsqrtf(ss / (float)A.hd + A.eps);
-        if (on) {
-          float w[16];
-          load8<float>(Q.norm + ea, w);
-          load8<float>(Q.norm + eb, w + 8);
+          for (int i = 0; i < 4; ++i) sq = __ffma2_rn(a.s[i], a.s[i], __ffma2_rn(a.f[i], a.f[i], sq));
+          float ss = sq.x + sq.y;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) a[i] = a[i] * r * w[i];
-        }
-      } else {
-        __syncwarp();   // every lane has its values before any writes in place
-      }
-      const bool turn = rotary;
-      if (turn) {
-        if (!have) {
-          const unsigned long long x = (unsigned long long)(long long)position;
+          for (int o = 1; o < 16; o <<= 1)
+            if (o < A.lanes) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float r = rsqrtf(ss * A.inv_hd + A.eps);
+          const float2 r2 = make_float2(r, r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            sincospif((float)(int)((A.turns[f0 + i] * x) >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-            sn[i] *= A.mscale;
-            cs[i] *= A.mscale;
-          }
-          have = true;
-        }
-        if (inter) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float re = a[2 * i], im = a[2 * i + 1];
-            a[2 * i] = re * cs[i] - im * sn[i];
-            a[2 * i + 1] = re * sn[i] + im * cs[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float re = a[i], im = a[8 + i];
-            a[i] = re * cs[i] - im * sn[i];
-            a[8 + i] = re * sn[i] + im * cs[i];
+          for (int i = 0; i < 4; ++i) {
+            a.f[i] = __fmul2_rn(__fmul2_rn(a.f[i], r2), w.f[i]);
+            a.s[i] = __fmul2_rn(__fmul2_rn(a.s[i], r2), w.s[i]);
           }
         }
-      }
-      int oa = ea, ob = eb;
-      if (A.layout == TRIA_ROPE_INTERLEAVED_TO_HALF && rotary) {
-        float b[16];
+        if (rotary) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          b[i] = a[2 * i];
-          b[8 + i] = a[2 * i + 1];
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = __ffma2_rn(a.f[i], cs[i], __fmul2_rn(a.s[i], ns[i]));
+            a.s[i] = __ffma2_rn(a.f[i], sn[i], __fmul2_rn(a.s[i], cs[i]));
+            a.f[i] = x;
+          }
         }
+        float b[16];                              // first members, then second ones (or pairs)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = b[i];
-        oa = f0;
-        ob = f0 + half;
-      }
-      if (!kCache || Q.kind == kPartDirect) {
-        if (on) {
-          T* o = reinterpret_cast<T*>(Q.out) + (int64_t)tok * Q.out_stride + (int64_t)head * A.hd;
-          store8<T>(o + oa, a);
-          store8<T>(o + ob, a + 8);
+        for (int i = 0; i < 4; ++i) {
+          if (LAYOUT == TRIA_ROPE_INTERLEAVED || (LAYOUT == TRIA_ROPE_INTERLEAVED_TO_HALF && !rotary)) {
+            b[4 * i] = a.f[i].x;
+            b[4 * i + 1] = a.s[i].x;
+            b[4 * i + 2] = a.f[i].y;
+            b[4 * i + 3] = a.s[i].y;
+          } else {
+            b[2 * i] = a.f[i].x;
+            b[2 * i + 1] = a.f[i].y;
+            b[8 + 2 * i] = a.s[i].x;
+            b[8 + 2 * i + 1] = a.s[i].y;
+          }
         }
-        continue;
-      }
-      // a key on its way into the cache: to consecutive dims through shared memory
-      float* buf = s_key + (warp * hpw + sub) * (A.hd + 4);
-      __syncwarp();
-      if (on) {
-        store8<float>(buf + oa, a);
-        store8<float>(buf + ob, a + 8);
-      }
-      __syncwarp();
-      if (on) {
-        load8<float>(buf + 16 * p, a);
-        load8<float>(buf + 16 * p + 8, a + 8);
-      }
-      const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
-      hold16(a, A.k_type, A.k, A.ks, r, A.hd, 16 * p, on && row_ok);
-      if (on && row_ok) {
-        if (p == 0) A.cpos[r] = position;
-        if (Q.out) {
-          T* o = reinterpret_cast<T*>(Q.out) + ((int64_t)tok * Q.heads + head) * A.hd + 16 * p;
-          store8<T>(o, a);
-          store8<T>(o + 8, a + 8);
+        if (!kCache || Q.kind == kPartDirect) {
+          if (on) {
+            store8<T>(out + oa, b);
+            store8<T>(out + ob, b + 8);
+          }
+          continue;
+        }
+        if constexpr (kCache) {
+          // a key on its way into the cache: to consecutive dims through shared memory
+          __syncwarp();
+          if (on) {
+            store8<float>(key_buf + oa, b);
+            store8<float>(key_buf + ob, b + 8);
+          }
+          __syncwarp();
+          if (on) {
+            load8(key_buf + 16 * p, b);
+            load8(key_buf + 16 * p + 8, b + 8);
+          }
+          const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
+          hold16(b, A.k_type, A.k, A.ks, r, A.hd, 16 * p, on && row_ok);
+          if (on && row_ok) {
+            if (p == 0) A.cpos[r] = position;
+            if (Q.out) {
+              store8<T>(out + 16 * p, b);
+              store8<T>(out + 16 * p + 8, b + 8);
+            }
+          }
         }
       }
     }
+    __syncwarp();                                 // the stage is free
   }
   if constexpr (kCache) {
     // n_live changes once nothing reads it any more: at once when the rows
     // before the call are the caller's, else by the last CTA to finish
-    bool mine = blockIdx.x == 0;
+    __shared__ int s_mine;
     __syncthreads();
-    if (threadIdx.x != 0) return;
-    if (!A.n_before) {
-      __threadfence();
-      mine = atomicAdd(&A.ctrl->append_ticket, 1u) == gridDim.x - 1;
-      __threadfence();
+    if (threadIdx.x == 0) {
+      s_mine = blockIdx.x == 0;
+      if (!A.n_before) {
+        __threadfence();
+        s_mine = atomicAdd(&A.ctrl->append_ticket, 1u) == gridDim.x - 1;
+        __threadfence();
+        if (s_mine) atomicExch(&A.ctrl->append_ticket, 0u);
+      }
     }
-    if (!mine) return;
-    for (int s = 0; s < A.n_seqs; ++s) {
+    __syncthreads();
+    if (!s_mine) return;
+    for (int s = threadIdx.x; s < A.n_seqs; s += blockDim.x) {
       const int t = A.tok0[s + 1] - A.tok0[s];
       const int n = A.n_before ? A.n_before[s] : *((volatile const int32_t*)(A.n_live + s));
       const uint32_t e = qkv_error(n, t, A.cap[s]);
@@ -381,7 +510,6 @@ __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant_
       else
         A.n_live[s] = n + t;
     }
-    if (!A.n_before) atomicExch(&A.ctrl->append_ticket, 0u);
   }
 }
 
@@ -391,14 +519,24 @@ int ceil_pow2(int x) {
   return p;
 }
 
+template <typename T, bool kCache, int LAYOUT>
+cudaError_t launch_rope_tl(const RopeArgs& A, cudaStream_t st) {
+  const int64_t upt = (A.groups + A.per_warp - 1) / A.per_warp;
+  const int64_t want = ((int64_t)A.n_tokens * upt + kRopeWarps - 1) / kRopeWarps;
+  const int grid = (int)std::min<int64_t>(std::max<int64_t>(want, 1), 152);
+  const int smem = kRopeWarps * (A.stage + (kCache ? (32 / A.lanes) * (A.hd + 4) * (int)sizeof(float) : 0));
+  auto kern = k_rope<T, kCache, LAYOUT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kRopeWarps * 32, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
 template <typename T, bool kCache>
 cudaError_t launch_rope_t(const RopeArgs& A, cudaStream_t st) {
-  const int64_t wpt = (A.groups + A.per_warp - 1) / A.per_warp;
-  const int64_t want = ((int64_t)A.n_tokens * wpt + kRopeWarps - 1) / kRopeWarps;
-  const int grid = (int)std::min<int64_t>(std::max<int64_t>(want, 1), 16 * 152);
-  const int smem = kCache ? kRopeWarps * (32 / A.lanes) * (A.hd + 4) * (int)sizeof(float) : 0;
-  k_rope<T, kCache><<<grid, kRopeWarps * 32, smem, st>>>(A);
-  return cudaGetLastError();
+  if (A.layout == TRIA_ROPE_HALF) return launch_rope_tl<T, kCache, TRIA_ROPE_HALF>(A, st);
+  if (A.layout == TRIA_ROPE_INTERLEAVED) return launch_rope_tl<T, kCache, TRIA_ROPE_INTERLEAVED>(A, st);
+  return launch_rope_tl<T, kCache, TRIA_ROPE_INTERLEAVED_TO_HALF>(A, st);
 }
 
 template <bool kCache>
@@ -408,28 +546,36 @@ cudaError_t launch_rope(const RopeArgs& A, int type, cudaStream_t st) {
   return launch_rope_t<__nv_bfloat16, kCache>(A, st);
 }
 
-// Work of a warp: one group of heads while the groups do not fill the GPU
-// (a single token then takes one short step on as many SMs as it has groups),
-// else as many groups of a token as leave about 64 warps for each SM, so that
-// the sines and cosines are shared.
-void finish_args(RopeArgs& A, const tria_rope* rope) {
+// Work of a warp at once: one group of heads while the groups do not fill the
+// GPU's warps (a single token then takes one short step in as many warps as it
+// has groups), else as many groups of a token as a stage holds, which share
+// the sines and cosines.
+void finish_args(RopeArgs& A, const tria_rope* rope, int type) {
   A.hd = rope->head_dim;
   A.rot = rope->head_dim - rope->nonrot_dim;
   A.layout = rope->layout;
   A.turns = rope->turns;
   A.mscale = (float)rope->mscale;
+  A.inv_hd = 1.f / (float)A.hd;
   A.lanes = ceil_pow2(A.hd / 16);
-  const int hpw = 32 / A.lanes;
+  const int hpw = 32 / A.lanes, group_bytes = hpw * A.hd * (type == TRIA_F32 ? 4 : 2);
   A.groups = 0;
   for (int i = 0; i < A.n_parts; ++i) {
     A.part[i].groups = (A.part[i].heads + hpw - 1) / hpw;
     A.groups += A.part[i].groups;
   }
   const int64_t total = (int64_t)A.n_tokens * A.groups;
-  A.per_warp = (int)std::min<int64_t>(std::max<int64_t>(total / (64 * 152), 1), A.groups);
+  // stages and the keys' buffers of all warps fill shared memory
+  const int room = (kRopeSmem / kRopeWarps - hpw * (A.hd + 4) * (int)sizeof(float)) & ~15;
+  const int most = std::min(std::min(room, kRopeStageMax) / group_bytes, A.groups);
+  A.per_warp = (int)std::min<int64_t>(std::max<int64_t>(total / (kRopeWarps * 152), 1), most);
+  A.stage = A.per_warp * group_bytes;
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// units of work are counted in 32 bits
+bool rope_fits(int64_t tokens, int64_t heads) { return tokens * (heads + 3) < ((int64_t)1 << 31); }
 
 int act_size(int type) { return type == TRIA_F32 ? 4 : 2; }
 
@@ -559,6 +705,7 @@ extern "C" tria_status tria_rotate(const tria_rope* rope, tria_dtype type, const
   if (!act_ok(type)) return TRIA_ERR_UNSUPPORTED;
   if (n_tokens == 0) return TRIA_OK;
   if (!pos || !aligned(pos, 4)) return TRIA_ERR_INVALID_ARG;
+  if (!rope_fits(n_tokens, (int64_t)parts[0].n_heads + (n_parts > 1 ? parts[1].n_heads : 0))) return TRIA_ERR_UNSUPPORTED;
   RopeArgs A;
   memset(&A, 0, sizeof(A));
   for (int i = 0; i < n_parts; ++i) {
@@ -573,7 +720,7 @@ extern "C" tria_status tria_rotate(const tria_rope* rope, tria_dtype type, const
   A.n_tokens = n_tokens;
   A.eps = (float)eps;
   A.pos = pos;
-  finish_args(A, rope);
+  finish_args(A, rope, type);
   return launch_rope<false>(A, type, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
 
@@ -591,6 +738,7 @@ extern "C" tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_c
   const int32_t* n_before = a->n_before == cache->n_live ? nullptr : a->n_before;
   if (n_before && !aligned(n_before, 4)) return TRIA_ERR_INVALID_ARG;
   if (n_tokens == 0 && !n_before) return TRIA_OK;
+  if (!rope_fits(n_tokens, (int64_t)a->n_q_heads + 2 * cache->n_kv_heads)) return TRIA_ERR_UNSUPPORTED;
   const int hd = cache->head_dim;
   RopeArgs A;
   memset(&A, 0, sizeof(A));
@@ -608,8 +756,9 @@ extern "C" tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_c
   const int kv = cache->n_kv_heads;
   if (a->n_q_heads > 0)
     A.part[A.n_parts++] = RopePart{a->q, a->q_out, a->q_norm, a->q_stride, a->q_out_stride, a->n_q_heads, 0, kPartDirect};
-  A.part[A.n_parts++] = RopePart{a->k, a->k_held, a->k_norm, a->k_stride, 0, kv, 0, kPartKey};
-  A.part[A.n_parts++] = RopePart{a->v, a->v_held, nullptr, a->v_stride, 0, kv, 0, kPartValue};
+  const int64_t held = (int64_t)kv * hd;
+  A.part[A.n_parts++] = RopePart{a->k, a->k_held, a->k_norm, a->k_stride, held, kv, 0, kPartKey};
+  A.part[A.n_parts++] = RopePart{a->v, a->v_held, nullptr, a->v_stride, held, kv, 0, kPartValue};
   A.n_tokens = n_tokens;
   A.eps = (float)a->eps;
   A.pos = a->pos;
@@ -630,6 +779,6 @@ extern "C" tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_c
     A.cap[s] = cache->capacity[s];
   }
   for (int s = 0; s <= cache->n_seqs; ++s) A.tok0[s] = a->tok0[s];
-  finish_args(A, rope);
+  finish_args(A, rope, a->type);
   return launch_rope<true>(A, a->type, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
