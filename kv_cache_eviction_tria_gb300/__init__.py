@@ -253,10 +253,22 @@ def _check(status: int, where: str):
         raise TriaError(status, where)
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """Address of torch's current stream on the current device."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        fast = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = (lambda: fast(torch.cuda.current_device())) if fast else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
 def _stream_handle(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(_current_stream())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -391,6 +403,26 @@ class LayerCache:
             _ptr(self.k), _ptr(self.k_scale), _ptr(self.v), _ptr(self.v_scale), _ptr(self.pos),
             _ptr(self.n_live), self.seq_row0.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)),
             self.capacity.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)))
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, "_made", None)
+        object.__setattr__(self, name, value)
+
+    def c_ref(self):
+        """A reference to the C struct, made anew only when a field or a plane's address has changed since the last
+        call (a decode step calls this for every layer)."""
+        ks, vs = self.k_scale, self.v_scale
+        at = (self.k if isinstance(self.k, int) else self.k.data_ptr(), self.v if isinstance(self.v, int) else self.v.data_ptr(),
+              self.pos if isinstance(self.pos, int) else self.pos.data_ptr(),
+              self.n_live if isinstance(self.n_live, int) else self.n_live.data_ptr(),
+              0 if ks is None else ks if isinstance(ks, int) else ks.data_ptr(),
+              0 if vs is None else vs if isinstance(vs, int) else vs.data_ptr())
+        made = self._made
+        if made is None or made[0] != at:
+            c = self.c_struct()
+            made = (at, c, ctypes.byref(c))
+            object.__setattr__(self, "_made", made)
+        return made[2]
 
 
 class Policy:
@@ -674,33 +706,39 @@ class Rope:
             pass
 
 
-_ACT = None
+_ACT, _INT32 = {}, ()       # torch's types, filled at the first call
 
 
 def _act_type(t) -> int:
-    global _ACT
-    if _ACT is None:
+    global _INT32
+    if not _ACT:
         import torch
-        _ACT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    if t.dtype not in _ACT:
+        _ACT.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+        _INT32 = (torch.int32,)
+    kind = _ACT.get(t.dtype)
+    if kind is None:
         raise ValueError("activations must be float32, float16 or bfloat16")
-    return _ACT[t.dtype]
+    return kind
 
 
 def _rows3(t, name: str, n_tokens: int, head_dim: int, like=None):
     """(address, values between tokens) of [tokens][heads][head_dim], heads of a token consecutive."""
-    sh, sd = t.shape, t.stride()
-    if len(sh) != 3 or sh[0] != n_tokens or sh[2] != head_dim or (like is not None and t.dtype != like):
+    try:
+        n, heads, hd = t.shape
+    except ValueError:
+        n = -1
+    if n != n_tokens or hd != head_dim or (like is not None and t.dtype is not like):
         raise ValueError(f"{name} must be [{n_tokens}][heads][{head_dim}] of the call's type")
     if not t.is_cuda:
         raise ValueError("device argument must be a CUDA tensor")
-    if n_tokens and (sd[2] != 1 or (sh[1] > 1 and sd[1] != head_dim)):
+    s0, s1, s2 = t.stride()
+    if n and (s2 != 1 or (heads > 1 and s1 != hd)):
         raise ValueError(f"{name}: the heads of a token must be consecutive")
-    return t.data_ptr(), sd[0] if n_tokens > 1 else max(sd[0], sh[1] * head_dim)
+    return t.data_ptr(), s0 if n > 1 else max(s0, heads * hd)
 
 
 def _pos32(pos, n_tokens: int) -> int:
-    if pos.numel() != n_tokens or pos.dtype.itemsize != 4 or pos.is_floating_point() or not pos.is_contiguous() or not pos.is_cuda:
+    if pos.numel() != n_tokens or pos.dtype not in _INT32 or not pos.is_contiguous() or not pos.is_cuda:
         raise ValueError(f"pos must be a contiguous int32 CUDA tensor of {n_tokens} positions")
     return pos.data_ptr()
 
@@ -708,7 +746,7 @@ def _pos32(pos, n_tokens: int) -> int:
 def _vec32(t, n: int, name: str):
     if t is None:
         return None
-    if t.numel() != n or t.dtype.itemsize != 4 or not t.is_floating_point() or not t.is_contiguous() or not t.is_cuda:
+    if t.numel() != n or _ACT.get(t.dtype) != F32 or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} values")
     return t.data_ptr()
 
@@ -721,7 +759,7 @@ def _tokens0(tok0, n_seqs: int, n_tokens: int):
         return np.arange(n_seqs + 1, dtype=np.int32) * (n_tokens // n_seqs)
     if not (isinstance(tok0, np.ndarray) and tok0.dtype == np.int32 and tok0.flags.c_contiguous):
         tok0 = np.ascontiguousarray(np.asarray(tok0, dtype=np.int32))
-    if tok0.size != n_seqs + 1 or int(tok0[-1]) != n_tokens:
+    if len(tok0) != n_seqs + 1 or tok0[n_seqs] != n_tokens:
         raise ValueError("tok0 must hold n_seqs + 1 offsets, the last one the number of tokens")
     return tok0
 
@@ -732,14 +770,14 @@ def rotate(rope: Rope, parts, pos, *, eps: float = 1e-6, stream=None):
     pos int32 [tokens]."""
     n = pos.numel()
     structs = (_Heads * len(parts))()
-    kind = parts[0][0].dtype
+    kind, act = parts[0][0].dtype, _act_type(parts[0][0])
     for h, (x, out, norm) in zip(structs, parts):
         h.x, h.x_stride = _rows3(x, "x", n, rope.head_dim, kind)
         h.out, h.out_stride = _rows3(out, "out", n, rope.head_dim, kind)
         if x.shape[1] != out.shape[1]:
             raise ValueError("x and out must have the same heads")
         h.norm, h.n_heads = _vec32(norm, rope.head_dim, "norm"), x.shape[1]
-    _check(load_library().tria_rotate(rope.handle, _act_type(parts[0][0]), structs, len(parts), n, _pos32(pos, n),
+    _check(load_library().tria_rotate(rope.handle, act, structs, len(parts), n, _pos32(pos, n),
                                       float(eps), _stream_handle(stream)), "tria_rotate")
 
 
@@ -774,10 +812,10 @@ def append_qkv(rope: Rope, cache: LayerCache, q, k, v, pos, *, ws, q_out=None, t
     a.tok0 = tok0.ctypes.data
     if n_before is not None:
         a.n_before = _pos32(n_before, n_seqs)
-    c = cache.c_struct()
     wp, wb = _ws(ws)
-    _check(load_library().tria_append_qkv(rope.handle, ctypes.byref(c), ctypes.byref(a), wp, wb, _stream_handle(stream)),
-           "tria_append_qkv")
+    st = load_library().tria_append_qkv(rope.handle, cache.c_ref(), ctypes.byref(a), wp, wb, _stream_handle(stream))
+    if st:
+        _check(st, "tria_append_qkv")
 
 
 def attend_workspace_size(cache: LayerCache, n_q_heads: int, tok0) -> int:
@@ -809,9 +847,10 @@ def attend(cache: LayerCache, q, out, pos, *, ws, tok0=None, lse=None, scale: fl
     a.pos = _pos32(pos, n)
     tok0 = _tokens0(tok0, n_seqs, n)
     a.tok0, a.scale, a.window, a.sink = tok0.ctypes.data, float(scale), int(window), int(sink)
-    c = cache.c_struct()
     wp, wb = _ws(ws)
-    _check(load_library().tria_attend(ctypes.byref(c), ctypes.byref(a), wp, wb, _stream_handle(stream)), "tria_attend")
+    st = load_library().tria_attend(cache.c_ref(), ctypes.byref(a), wp, wb, _stream_handle(stream))
+    if st:
+        _check(st, "tria_attend")
 
 
 # --------------------------------------------------------------------------- decode-loop lifecycle
