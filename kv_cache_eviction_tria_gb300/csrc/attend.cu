@@ -249,6 +249,45 @@ __global__ void __launch_bounds__(kPlainWarps * 32) k_attend_plain(const __grid_
   if (threadIdx.x == 0) A.count[y] = 0u;
 }
 
+// Rows besides the sink that some token of a sequence sees in each segment: a
+// warp per segment searches the positions in 32 parts (three rounds for 4096
+// candidates), since every CTA of the attention needs the count of every one.
+__global__ void __launch_bounds__(128) k_attend_span(const __grid_constant__ AttendArgs A, int32_t* span) {
+  const int u = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (u >= A.n_seqs * A.n_kv) return;
+  const int s = u / A.n_kv, g = u - s * A.n_kv;
+  const AttendSeq& S = A.seq[s];
+  const int n = *((volatile const int32_t*)(A.n_live + s));
+  if (S.t == 0 || n < 0 || n > S.cap) return;
+  const int32_t* rpos = A.cpos + S.row0 + (int64_t)g * S.cap;
+  int pl = INT32_MAX, ph = INT32_MIN;
+  for (int i = lane; i < S.t; i += 32) {
+    const int p = A.pos[S.tok0 + i];
+    pl = min(pl, p);
+    ph = max(ph, p);
+  }
+  const int last = n > 0 ? rpos[n - 1] : 0;
+  pl = __reduce_min_sync(0xffffffffu, pl);
+  ph = __reduce_max_sync(0xffffffffu, ph);
+  auto upto = [&](int lo, int hi, int64_t p) {   // rows with a position <= p, between lo and hi of them
+    while (lo < hi) {
+      const int step = (hi - lo + 31) / 32;
+      const int r = min(hi, lo + (lane + 1) * step) - 1;   // last row of this lane's share
+      const int k = __popc(__ballot_sync(0xffffffffu, rpos[r] <= p));
+      lo = min(hi, lo + k * step);
+      if (k < 32) hi = min(hi, lo + step - 1);
+    }
+    return lo;
+  };
+  const int hi = n == 0 || last <= ph ? n : upto(0, n, ph);
+  // positions ascend strictly, so at most window + (ph - pl) rows lie in reach
+  const int lo = upto((int)max((int64_t)0, hi - (A.window + (int64_t)ph - pl)), hi, (int64_t)pl - A.window);
+  if (lane == 0) {
+    span[2 * u] = lo;
+    span[2 * u + 1] = hi;
+  }
+}
+
 // Parts of a unit: enough CTAs for the GPU, none under 128 rows of the
 // capacity.
 int plain_split(int64_t units, int cap_max) {
@@ -265,6 +304,11 @@ cudaError_t launch_attend_plain(const AttendArgs& A, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(k_attend_plain, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   k_attend_plain<<<(unsigned)grid, kPlainWarps * 32, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attend_span(const AttendArgs& A, int32_t* span, cudaStream_t st) {
+  k_attend_span<<<(A.n_seqs * A.n_kv + 3) / 4, 128, 0, st>>>(A, span);
   return cudaGetLastError();
 }
 
@@ -304,7 +348,7 @@ int sm_count() {
 // and the space of the partial results. The layout covers every type of
 // queries.
 struct AttendLayout {
-  size_t count, part, wide_k, wide_v, total;
+  size_t count, span, part, wide_k, wide_v, total;
   int units, split, prompt_split, sms;
 };
 
@@ -345,7 +389,8 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   L.units = (int)units;
   L.split = plain_split(units * c->n_kv_heads, cap_max);
   L.count = up256(sizeof(Ctrl));
-  L.part = up256(L.count + sizeof(uint32_t) * (size_t)(std::max<int64_t>(units, c->n_seqs) * c->n_kv_heads));
+  L.span = up256(L.count + sizeof(uint32_t) * (size_t)(std::max<int64_t>(units, c->n_seqs) * c->n_kv_heads));
+  L.part = up256(L.span + 2 * sizeof(int32_t) * (size_t)c->n_seqs * c->n_kv_heads);
   const size_t plain = L.split > 1 ? (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0;
   const size_t step = (size_t)L.sms * 2 * (cols <= 8 ? 8 : 16) * (c->head_dim + 2);
   L.prompt_split = prompt_split(prompts * c->n_kv_heads, cap_max, L.sms);
@@ -466,6 +511,11 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   const cudaStream_t st = (cudaStream_t)stream;
   if (step) {
     take(kPathStep);
+    if (A.window > 0) {
+      int32_t* span = (int32_t*)((uint8_t*)ws + L.span);
+      if (launch_attend_span(A, span, st) != cudaSuccess) return TRIA_ERR_CUDA;
+      A.span = span;
+    }
     if (launch_step(A, cols, L.sms, st) != cudaSuccess) return TRIA_ERR_CUDA;
   }
   if (prompt) {

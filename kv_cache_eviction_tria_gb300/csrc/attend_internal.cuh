@@ -54,6 +54,7 @@ struct AttendArgs {
   float* part;         // partial results of split units
   uint16_t* wide_k;    // fp16 copies of quantised planes (prompts; NULL: none)
   uint16_t* wide_v;
+  const int32_t* span; // decode steps with a window: [sequence][KV head] {first, past the last} row that a token sees
   int32_t n_seqs, n_kv, G, hd, nq;
   int32_t type, k_type, v_type;
   int32_t window, sink;
@@ -65,6 +66,7 @@ struct AttendArgs {
 
 // attend.cu
 cudaError_t launch_attend_plain(const AttendArgs& A, cudaStream_t st);
+cudaError_t launch_attend_span(const AttendArgs& A, int32_t* span, cudaStream_t st);
 // attend_step_*.cu: up to 16 columns (tokens x group) a sequence, one CTA per worker
 cudaError_t launch_attend_step_f16_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 cudaError_t launch_attend_step_f16_q8(const AttendArgs& A, int cols, int workers, cudaStream_t st);

@@ -32,7 +32,7 @@
 
 namespace tria {
 
-constexpr int kStepSmem = 220 * 1024;
+constexpr int kStepSmem = 212 * 1024;   // stages; the unit tables need 13 KB more
 
 // TR: rows of a tile; SB: bytes of a stage
 template <int KT, int VT, int HD, int NT>
@@ -102,6 +102,26 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
+// Block scales of two neighbouring rows (NB halves each, side by side).
+template <int NB>
+__device__ __forceinline__ void load_scales(const uint8_t* p, float* a, float* b) {
+  __half2 h[NB];
+  if constexpr (NB == 2) {
+    *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NB / 4; ++i) reinterpret_cast<uint4*>(h)[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+#pragma unroll
+  for (int i = 0; i < NB / 2; ++i) {
+    const float2 x = __half22float2(h[i]), y = __half22float2(h[NB / 2 + i]);
+    a[2 * i] = x.x;
+    a[2 * i + 1] = x.y;
+    b[2 * i] = y.x;
+    b[2 * i + 1] = y.y;
+  }
+}
+
 // Codes of a word (q8_0: bytes 0 / 2 and 1 / 3; q4_0: the low halves of bytes
 // 0 / 2 and 1 / 3, then the high halves) as fp16 pairs, exactly: 0x6400 | u is
 // 1024 + u, and 1024 + 16 u for a code in the high half of a byte.
@@ -124,45 +144,52 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
   constexpr int TR = H::TR, NB = HD / 32, NG = TR / 8;     // blocks of a row, 8-row groups of a tile
   constexpr int kWarps = H::kWarps, kStages = H::kStages, kCol = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_first[kMaxSeqs + 1];                    // first tile of each sequence's units
+  __shared__ int s_first[kMaxSegments + 1];                // first tile of each unit
+  __shared__ int s_lo[kMaxSegments], s_hi[kMaxSegments];   // its rows besides the sink
   __shared__ int s_scan[40];
   __shared__ int s_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
 
-  // ---- the tile list: units of a sequence have equally many tiles
-  auto span_of = [&](int s) {                              // positions between the sequence's tokens
-    int lo = INT32_MAX, hi = INT32_MIN;
-    for (int i = 0; i < A.seq[s].t; ++i) {
-      const int p = A.pos[A.seq[s].tok0 + i];
-      lo = min(lo, p);
-      hi = max(hi, p);
-    }
-    return (int64_t)hi - lo;
-  };
-  auto tiles_of = [&](int s, int n) {                      // tiles that a unit of sequence s may need
-    if (A.window <= 0) return max(1, (n + TR - 1) / TR);
-    const int64_t reach = min((int64_t)n, A.window + span_of(s));
-    return max(1, (min(A.sink, n) + TR - 1) / TR + (int)((reach + TR - 1) / TR));
-  };
+  // ---- the tile list: every unit has a tile at least (a token without rows
+  // still gets its zeros), but those of sequences that take no part
+  const int n_units = A.n_seqs * A.n_kv;
+  constexpr int kPer = (kMaxSegments + kWarps * 32 - 1) / (kWarps * 32);   // units of a thread, consecutive
   {
-    int cnt = 0;
-    if ((int)threadIdx.x < A.n_seqs) {
-      const int s = threadIdx.x, n = *((volatile const int32_t*)(A.n_live + s));
-      if (A.seq[s].t > 0) {
-        if (n < 0 || n > A.seq[s].cap) {
-          if (blockIdx.x == 0) report(A.ctrl, TRIA_ERR_DEVICE_ARG, (uint32_t)s);
-        } else {
-          cnt = tiles_of(s, n) * A.n_kv;
-        }
+    int cnt[kPer], local = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      cnt[i] = 0;
+      const int u = (int)threadIdx.x * kPer + i;
+      if (u >= n_units) continue;
+      const int s = u / A.n_kv;
+      if (A.seq[s].t == 0) continue;
+      const int n = __ldg(A.n_live + s);
+      if (n < 0 || n > A.seq[s].cap) {
+        if (blockIdx.x == 0 && u == s * A.n_kv) report(A.ctrl, TRIA_ERR_DEVICE_ARG, (uint32_t)s);
+        continue;
       }
+      int lo = 0, hi = n;
+      if (A.window > 0) {
+        lo = A.span[2 * u];
+        hi = A.span[2 * u + 1];
+      }
+      s_lo[u] = lo;
+      s_hi[u] = hi;
+      cnt[i] = max(1, (min(A.sink, lo) + TR - 1) / TR + (hi - lo + TR - 1) / TR);
+      local += cnt[i];
     }
     int tot;
-    const int before = block_exclusive_scan(cnt, &tot, s_scan);
-    if ((int)threadIdx.x < A.n_seqs) s_first[threadIdx.x] = before;
-    if (threadIdx.x == 0) s_first[A.n_seqs] = tot;
+    int before = block_exclusive_scan(local, &tot, s_scan);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = (int)threadIdx.x * kPer + i;
+      if (u < n_units) s_first[u] = before;
+      before += cnt[i];
+    }
+    if (threadIdx.x == 0) s_first[n_units] = tot;
     __syncthreads();
   }
-  const int64_t total = s_first[A.n_seqs];
+  const int64_t total = s_first[n_units];
   if (total == 0) return;
   const int64_t workers = min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps);
   if ((int64_t)blockIdx.x >= workers) return;
@@ -176,35 +203,24 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
 
   while (at < end) {
     // ---- the unit
-    int lo_s = 0, hi_s = A.n_seqs - 1;
-    while (lo_s < hi_s) {
-      const int mid = (lo_s + hi_s + 1) >> 1;
-      if (s_first[mid] <= at) lo_s = mid; else hi_s = mid - 1;
+    int unit = 0;                                          // the last one that starts at or before `at`
+    {
+      int hi_u = n_units - 1;
+      while (unit < hi_u) {
+        const int mid = (unit + hi_u + 1) >> 1;
+        if (s_first[mid] <= at) unit = mid; else hi_u = mid - 1;
+      }
     }
-    const int s = lo_s;
+    const int s = unit / A.n_kv, g = unit - s * A.n_kv;
     const AttendSeq& S = A.seq[s];
-    const int per = (s_first[s + 1] - s_first[s]) / A.n_kv;
-    const int g = (int)((at - s_first[s]) / per);
-    const int64_t u0 = s_first[s] + (int64_t)g * per, u1 = u0 + per;   // the unit's tiles in the list
-    const int j0 = (int)(at - u0), j1 = (int)(min(end, u1) - u0);      // those of this CTA
-    const int n = *((volatile const int32_t*)(A.n_live + s));
+    const int64_t u0 = s_first[unit], u1 = s_first[unit + 1];          // the unit's tiles in the list
+    const int per = (int)(u1 - u0), j0 = (int)(at - u0), j1 = (int)(min(end, u1) - u0);   // those of this CTA
     const int64_t row0 = S.row0 + (int64_t)g * S.cap;
     const int32_t* rpos = A.cpos + row0;
     const int ncol = S.t * A.G;
-    int pmin = INT32_MAX, pmax = INT32_MIN;
-    for (int i = 0; i < S.t; ++i) {
-      const int p = A.pos[S.tok0 + i];
-      pmin = min(pmin, p);
-      pmax = max(pmax, p);
-    }
-    const bool newest = n == 0 || rpos[n - 1] <= pmin;     // every row is old enough for every token
-    int lo = 0, hi = n;
-    if (A.window > 0) {
-      hi = rows_upto(rpos, n, pmax);
-      lo = (int)max((int64_t)0, hi - (A.window + (int64_t)pmax - pmin));
-    }
+    const int lo = s_lo[unit], hi = s_hi[unit];
     const int sr = min(A.sink, lo), nt_sink = (sr + TR - 1) / TR;
-    const bool need_pos = A.window > 0 || !newest;
+    bool need_pos = true;                                  // until it is known that every token sees every row
     auto tile_row = [&](int j, int& rows) {                // first row and rows of tile j (rows <= 0: none)
       if (j < nt_sink) {
         rows = min(TR, sr - j * TR);
@@ -243,13 +259,22 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
         if (need_pos) cp_async4(d + H::oPos + lane * 4, rpos + r + lane);
       }
     };
-    // this warp's tiles: j0 + warp, + kWarps, ...
+    // this warp's tiles: j0 + warp, + kWarps, ...; the first are on their way
+    // before anything else is asked for
     const int mine = j1 - j0 > warp ? (j1 - j0 - warp + kWarps - 1) / kWarps : 0;
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
       if (i < mine) issue(j0 + warp + i * kWarps, i);
       cp_async_commit();
     }
+
+    int pmin = INT32_MAX, pmax = INT32_MIN;
+    for (int i = 0; i < S.t; ++i) {
+      const int p = A.pos[S.tok0 + i];
+      pmin = min(pmin, p);
+      pmax = max(pmax, p);
+    }
+    need_pos = A.window > 0 || (hi > 0 && rpos[hi - 1] > pmin);
 
     // ---- queries: A fragments, columns gid and gid + 8; qf: their exponent
     uint32_t qa[NB * 2][2 * NT];                           // [step][column half * 2 ... k low, k high]
@@ -264,18 +289,35 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       pq[h] = on ? A.pos[tok] : INT32_MIN;
       float x[NB][8];
       float am = 0.f;
+      const uint16_t* qp = reinterpret_cast<const uint16_t*>(A.q) + qoff;
+      uint32_t raw[NB][4];                                 // pairs of fp16 or bf16
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         // dims of the thread: fp16 keys 2t, 2t+1, 8+2t, 9+2t (+16); codes 4t .. 4t+3 (+16)
+        if constexpr (H::kKq) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          int e;
-          if constexpr (H::kKq) e = 4 * t4 + (i & 3) + 16 * (i >> 2);
-          else e = 2 * t4 + (i & 1) + 8 * ((i >> 1) & 1) + 16 * (i >> 2);
-          x[b][i] = on ? act_load(A.q, A.type, qoff + 32 * b + e) : 0.f;
-          am = fmaxf(am, fabsf(x[b][i]));
+          for (int k = 0; k < 2; ++k) {
+            const uint2 v = on ? *reinterpret_cast<const uint2*>(qp + 32 * b + 16 * k + 4 * t4) : make_uint2(0, 0);
+            raw[b][2 * k] = v.x;
+            raw[b][2 * k + 1] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            raw[b][k] = on ? *reinterpret_cast<const uint32_t*>(qp + 32 * b + 8 * k + 2 * t4) : 0u;
         }
       }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t w = raw[b][k];
+          const float2 f = A.type == TRIA_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
+                                              : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+          x[b][2 * k] = f.x;
+          x[b][2 * k + 1] = f.y;
+          am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
       qf[h] = A.scale * 1.4426950408889634f;
       float f = 1.f;
       if (A.type != TRIA_F16) {
@@ -343,7 +385,8 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
           }
         } else {
           // scales of rows 2t, 2t + 1
-          const __half* kss = reinterpret_cast<const __half*>(area + (base - area_u) + H::oKs) + (gq * 8 + 2 * t4) * (H::scRb / 2);
+          float ks0[NB], ks1[NB];
+          load_scales<NB>(area + (base - area_u) + H::oKs + (gq * 8 + 2 * t4) * H::scRb, ks0, ks1);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -359,7 +402,7 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
             mma16816(c, a, h[0], h[1]);
             qfrag(2 * b + 1, a);
             mma16816(c, a, h[2], h[3]);
-            const float s0 = __half2float(kss[b]), s1 = __half2float(kss[b + H::scRb / 2]);
+            const float s0 = ks0[b], s1 = ks1[b];
             acc[0] = fmaf(c[0], s0, acc[0]);
             acc[1] = fmaf(c[1], s1, acc[1]);
             if constexpr (NT == 2) {
@@ -507,14 +550,14 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       } else {
 #pragma unroll
         for (int k = 0; k < TR / 16; ++k) {
-          const __half* v0 = reinterpret_cast<const __half*>(area + (base - area_u) + H::oVs) + (k * 16 + 2 * t4) * (H::scRb / 2);
+          float vs0[NB], vs1[NB], vs2[NB], vs3[NB];        // of rows 2t, 2t + 1, 2t + 8, 2t + 9
+          load_scales<NB>(area + (base - area_u) + H::oVs + (k * 16 + 2 * t4) * H::scRb, vs0, vs1);
+          load_scales<NB>(area + (base - area_u) + H::oVs + (k * 16 + 8 + 2 * t4) * H::scRb, vs2, vs3);
           const uint32_t vr = base + H::oV + (k * 16 + 2 * t4) * H::vStride;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             uint32_t pb[NT][2];
-            float s[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = __half2float(v0[b + ((i & 1) + 8 * (i >> 1)) * (H::scRb / 2)]);
+            const float s[4] = {vs0[b], vs1[b], vs2[b], vs3[b]};
 #pragma unroll
             for (int h = 0; h < NT; ++h) {
               float x[4];
@@ -637,7 +680,7 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
     if (!whole) {
       // the CTAs of the unit: those whose runs meet [u0, u1)
       const int64_t c0 = ((u0 + 1) * workers - 1) / total, c1 = (u1 * workers - 1) / total;
-      uint32_t* count = A.count + (int64_t)s * A.n_kv + g;
+      uint32_t* count = A.count + unit;
       if (threadIdx.x == 0) {
         __threadfence();
         s_flag = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
@@ -648,14 +691,26 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
         for (int i = threadIdx.x; i < ncol * HD; i += kWarps * 32) {
           const int col = i / HD;
           float top = -INFINITY, sum = 0.f, val = 0.f;
-          auto part_of = [&](int64_t c) { return A.part + (c * 2 + (start_of(c) > u0 ? 0 : 1)) * (kCol * (HD + 2)); };
-          for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part_of(c) + col));
-          const float tb = top == -INFINITY ? 0.f : top;
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* x = part_of(c);
-            const float f = exp2_approx(__ldcg(x + col) - tb);
-            sum = fmaf(__ldcg(x + kCol + col), f, sum);
-            val = fmaf(__ldcg(x + 2 * kCol + i), f, val);
+          // every CTA but the first starts inside the unit; four parts' loads at a time
+          auto part_of = [&](int64_t c) { return A.part + (c * 2 + (c > c0 || start_of(c0) > u0 ? 0 : 1)) * (kCol * (HD + 2)); };
+          for (int64_t c = c0; c <= c1; c += 4) {
+            float m[4], l4[4], v4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float* x = part_of(min(c + k, c1));
+              m[k] = __ldcg(x + col);
+              l4[k] = __ldcg(x + kCol + col);
+              v4[k] = __ldcg(x + 2 * kCol + i);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (c + k > c1) break;
+              const float mn = fmaxf(top, m[k]), tb = mn == -INFINITY ? 0.f : mn;
+              const float f0 = exp2_approx(top - tb), f1 = exp2_approx(m[k] - tb);
+              sum = fmaf(sum, f0, l4[k] * f1);
+              val = fmaf(val, f0, v4[k] * f1);
+              top = mn;
+            }
           }
           write(col, i - col * HD, val, top, sum);
         }
