@@ -65,23 +65,18 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
+// (plain loads, so that constant offsets go into the instruction)
+__device__ __forceinline__ uint32_t get32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ uint32_t get16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -125,16 +120,39 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float* a, float* b
 // Codes of a word (q8_0: bytes 0 / 2 and 1 / 3; q4_0: the low halves of bytes
 // 0 / 2 and 1 / 3, then the high halves) as fp16 pairs, exactly: 0x6400 | u is
 // 1024 + u, and 1024 + 16 u for a code in the high half of a byte.
-__device__ __forceinline__ void q8_pairs(uint32_t w, uint32_t* h) {
-  h[0] = h2_sub((w & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);          // - 1152
-  h[1] = h2_sub(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+// The constants sit in registers that the compiler cannot see through: as
+// immediates, of which an instruction takes one, every masked insertion became
+// two.
+struct Magic {
+  uint32_t q8, one, low, inv, high;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x64806480;" : "=r"(q8));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(one));
+    asm volatile("mov.b32 %0, 0x64086408;" : "=r"(low));
+    asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(inv));
+    asm volatile("mov.b32 %0, 0xD480D480;" : "=r"(high));
+  }
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(b));
+  return d;
 }
-__device__ __forceinline__ void q4_pairs(uint32_t w, uint32_t* h) {
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(mask), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void q8_pairs(const Magic& m, uint32_t w, uint32_t* h) {
+  h[0] = h2_sub(and_xor(w, 0x00FF00FFu, m.q8), m.q8);                   // - 1152
+  h[1] = h2_sub(and_xor(w >> 8, 0x00FF00FFu, m.q8), m.q8);
+}
+__device__ __forceinline__ void q4_pairs(const Magic& m, uint32_t w, uint32_t* h) {
   const uint32_t u = w >> 8;
-  h[0] = h2_sub((w & 0x000F000Fu) | 0x64006400u, 0x64086408u);          // - 1032
-  h[1] = h2_sub((u & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-  h[2] = h2_fma((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);   // / 16 - 72
-  h[3] = h2_fma((u & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+  h[0] = h2_sub(and_or(w, 0x000F000Fu, m.one), m.low);                  // - 1032
+  h[1] = h2_sub(and_or(u, 0x000F000Fu, m.one), m.low);
+  h[2] = h2_fma(and_or(w, 0x00F000F0u, m.one), m.inv, m.high);          // / 16 - 72
+  h[3] = h2_fma(and_or(u, 0x00F000F0u, m.one), m.inv, m.high);
 }
 
 template <int KT, int VT, int HD, int NT>
@@ -198,8 +216,8 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
   int64_t at = start_of(blockIdx.x);
   const int64_t begin = at;
 
+  const Magic mg;
   uint8_t* area = smem + warp * H::kArea;
-  const uint32_t area_u = smem_u32(area);
 
   while (at < end) {
     // ---- the unit
@@ -366,8 +384,12 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[i][h][c] = 0.f;
 
-    auto tile = [&](auto masked_c, uint32_t base, int r, int rows) {
+    auto tile = [&](auto masked_c, const uint8_t* tile_p, int r, int rows) {
       constexpr bool kMasked = decltype(masked_c)::value;
+      const uint32_t base = smem_u32(tile_p);
+      // this thread's words: keys of rows gid, values of rows 2t, 2t + 1, 2t + 8, 2t + 9
+      const uint8_t* kp = tile_p + gid * H::kStride + t4 * 4;
+      const uint8_t* vp = tile_p + H::oV + 2 * t4 * H::vStride + gid * (VT == TRIA_Q8_0 ? 4 : 2);
       // logits
       float sc[NG][2 * NT];
 #pragma unroll
@@ -386,17 +408,16 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
         } else {
           // scales of rows 2t, 2t + 1
           float ks0[NB], ks1[NB];
-          load_scales<NB>(area + (base - area_u) + H::oKs + (gq * 8 + 2 * t4) * H::scRb, ks0, ks1);
+          load_scales<NB>(tile_p + H::oKs + (gq * 8 + 2 * t4) * H::scRb, ks0, ks1);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             float c[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t h[4], a[4];
             if constexpr (KT == TRIA_Q8_0) {
-              const uint32_t w = base + (gq * 8 + gid) * H::kStride + b * 32 + t4 * 4;
-              q8_pairs(lds32(w), h);
-              q8_pairs(lds32(w + 16), h + 2);
+              q8_pairs(mg, get32(kp + gq * 8 * H::kStride + b * 32), h);
+              q8_pairs(mg, get32(kp + gq * 8 * H::kStride + b * 32 + 16), h + 2);
             } else {
-              q4_pairs(lds32(base + (gq * 8 + gid) * H::kStride + b * 16 + t4 * 4), h);
+              q4_pairs(mg, get32(kp + gq * 8 * H::kStride + b * 16), h);
             }
             qfrag(2 * b, a);
             mma16816(c, a, h[0], h[1]);
@@ -417,7 +438,7 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
           sc[gq][2 * h + 1] = acc[2 * h + 1] * qf[h];
         }
       }
-      const int32_t* tp = reinterpret_cast<const int32_t*>(area + (base - area_u) + H::oPos);
+      const int32_t* tp = reinterpret_cast<const int32_t*>(tile_p + H::oPos);
       auto sees = [&](int row, int p) {                    // row of the tile, position of the query
         if (row >= rows) return false;
         if (!need_pos) return true;
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       int En = E;
       if constexpr (H::kVq) {
         float big = 0.f;
-        const __half2* vss = reinterpret_cast<const __half2*>(area + (base - area_u) + H::oVs);
+        const __half2* vss = reinterpret_cast<const __half2*>(tile_p + H::oVs);
         // all scales of the tile, spread over the lanes: TR * NB / 2 pairs
 #pragma unroll
         for (int i = 0; i < (TR * NB / 2 + 31) / 32; ++i) {
@@ -551,9 +572,9 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
 #pragma unroll
         for (int k = 0; k < TR / 16; ++k) {
           float vs0[NB], vs1[NB], vs2[NB], vs3[NB];        // of rows 2t, 2t + 1, 2t + 8, 2t + 9
-          load_scales<NB>(area + (base - area_u) + H::oVs + (k * 16 + 2 * t4) * H::scRb, vs0, vs1);
-          load_scales<NB>(area + (base - area_u) + H::oVs + (k * 16 + 8 + 2 * t4) * H::scRb, vs2, vs3);
-          const uint32_t vr = base + H::oV + (k * 16 + 2 * t4) * H::vStride;
+          load_scales<NB>(tile_p + H::oVs + (k * 16 + 2 * t4) * H::scRb, vs0, vs1);
+          load_scales<NB>(tile_p + H::oVs + (k * 16 + 8 + 2 * t4) * H::scRb, vs2, vs3);
+          const uint8_t* vr = vp + k * 16 * H::vStride;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             uint32_t pb[NT][2];
@@ -571,16 +592,16 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
             }
             uint32_t f0[4], f1[4];                         // rows 2t, 2t+1 and 2t+8, 2t+9 of four dims
             if constexpr (VT == TRIA_Q8_0) {
-              const uint32_t w = vr + b * 32 + gid * 4;
-              const uint32_t w0 = lds32(w), w1 = lds32(w + H::vStride), w2 = lds32(w + 8 * H::vStride), w3 = lds32(w + 9 * H::vStride);
-              q8_pairs(__byte_perm(w0, w1, 0x5410), f0);
-              q8_pairs(__byte_perm(w0, w1, 0x7632), f0 + 2);
-              q8_pairs(__byte_perm(w2, w3, 0x5410), f1);
-              q8_pairs(__byte_perm(w2, w3, 0x7632), f1 + 2);
+              const uint8_t* w = vr + b * 32;
+              const uint32_t w0 = get32(w), w1 = get32(w + H::vStride), w2 = get32(w + 8 * H::vStride), w3 = get32(w + 9 * H::vStride);
+              q8_pairs(mg, __byte_perm(w0, w1, 0x5410), f0);
+              q8_pairs(mg, __byte_perm(w0, w1, 0x7632), f0 + 2);
+              q8_pairs(mg, __byte_perm(w2, w3, 0x5410), f1);
+              q8_pairs(mg, __byte_perm(w2, w3, 0x7632), f1 + 2);
             } else {
-              const uint32_t w = vr + b * 16 + gid * 2;
-              q4_pairs(lds16(w) | (lds16(w + H::vStride) << 16), f0);
-              q4_pairs(lds16(w + 8 * H::vStride) | (lds16(w + 9 * H::vStride) << 16), f1);
+              const uint8_t* w = vr + b * 16;
+              q4_pairs(mg, __byte_perm(get16(w), get16(w + H::vStride), 0x5410), f0);
+              q4_pairs(mg, __byte_perm(get16(w + 8 * H::vStride), get16(w + 9 * H::vStride), 0x5410), f1);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -600,19 +621,19 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       __syncwarp();
       int rows;
       const int r = tile_row(j0 + warp + i * kWarps, rows);
-      const uint32_t base = area_u + (i % kStages) * H::SB;
+      const uint8_t* tile_p = area + (i % kStages) * H::SB;
       if (rows > 0) {
         bool masked = rows < TR, skip = false;
         if (need_pos) {
-          const int32_t* tp = reinterpret_cast<const int32_t*>(area + (i % kStages) * H::SB + H::oPos);
+          const int32_t* tp = reinterpret_cast<const int32_t*>(tile_p + H::oPos);
           const int64_t first = tp[0], last = tp[rows - 1];
           const bool in_sink = r + rows <= A.sink;
           skip = first > pmax || (A.window > 0 && pmin - last >= A.window && r >= A.sink);
           masked = masked || last > pmin || (A.window > 0 && pmax - first >= A.window && !in_sink);
         }
         if (!skip) {
-          if (masked) tile(std::true_type{}, base, r, rows);
-          else tile(std::false_type{}, base, r, rows);
+          if (masked) tile(std::true_type{}, tile_p, r, rows);
+          else tile(std::false_type{}, tile_p, r, rows);
         }
       }
       __syncwarp();
