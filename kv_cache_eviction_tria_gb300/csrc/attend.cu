@@ -392,7 +392,8 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   L.span = up256(L.count + sizeof(uint32_t) * (size_t)(std::max<int64_t>(units, c->n_seqs) * c->n_kv_heads));
   L.part = up256(L.span + 2 * sizeof(int32_t) * (size_t)c->n_seqs * c->n_kv_heads);
   const size_t plain = L.split > 1 ? (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0;
-  const size_t step = (size_t)L.sms * 2 * (cols <= 8 ? 8 : 16) * (c->head_dim + 2);
+  // a part a warp (at most 12 a CTA) and two a CTA
+  const size_t step = (size_t)L.sms * 14 * (cols <= 8 ? 8 : 16) * (c->head_dim + 2);
   L.prompt_split = prompt_split(prompts * c->n_kv_heads, cap_max, L.sms);
   const size_t prompt = L.prompt_split > 1
       ? (size_t)(prompts * c->n_kv_heads) * L.prompt_split * prompt_cols(c->head_dim) * (c->head_dim + 2) : 0;

@@ -18,12 +18,15 @@
 // largest value scale so far: weight x scale then reaches up to 2^14 in fp16
 // whatever the size of the values, and the common factor cancels in O / l.
 //
-// Each warp streams its own tiles through a ring of cp.async stages without
-// block-wide barriers (padded rows: no bank conflicts). The tiles of all
-// units (sequence x KV head) are one list, cut into equal runs, one per CTA:
-// the live rows are known on the device alone, and ragged batches stay
-// balanced. A CTA's warps join through shared memory, CTAs that share a unit
-// through the workspace, the last one to arrive merging the parts in order.
+// The tiles of all units (sequence x KV head) are one list, cut into equal
+// runs, one per warp, neighbouring ones in a CTA: the live rows are known on
+// the device alone, and ragged batches stay balanced. A warp streams its run
+// through a ring of cp.async stages (padded rows: no bank conflicts) from unit
+// to unit without stopping: a block that met at every unit's end ran 64
+// sequences of 1000 rows at 3.1 TB/s. A unit inside a run is written by its
+// warp; parts of a unit go to the workspace and are merged in order, those of
+// a CTA's warps when all have finished, those of several CTAs by the last one
+// to arrive.
 #pragma once
 
 #include <type_traits>
@@ -47,11 +50,11 @@ struct StepShape {
                        oPos = oVs + (kVq ? TR * scRb : 0);
   static constexpr int SB = (oPos + TR * 4 + 15) & ~15;
   static constexpr int kStages = 3;
-  static constexpr int kOut = (HD * 8 * NT + 16 * NT) * 4;  // a warp's result in its stages
   static constexpr int fit = kStepSmem / (SB * kStages);
   static constexpr int kWarps = fit >= 12 ? 12 : (fit >= 8 ? 8 : 4);
   static constexpr int kArea = SB * kStages;
-  static_assert(kArea >= kOut, "a warp's result fits its stages");
+  static constexpr int kOut = (HD * 8 * NT + 16 * NT) * 4;  // a warp's part of a unit, in its stages
+  static_assert(kArea >= kOut, "a warp's part fits its stages");
   static_assert(kArea * kWarps <= kStepSmem, "stages fit shared memory");
 };
 
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
   __shared__ int s_first[kMaxSegments + 1];                // first tile of each unit
   __shared__ int s_lo[kMaxSegments], s_hi[kMaxSegments];   // its rows besides the sink
   __shared__ int s_scan[40];
-  __shared__ int s_flag;
+  __shared__ int s_flag[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
 
   // ---- the tile list: every unit has a tile at least (a token without rows
@@ -212,87 +215,94 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
   const int64_t workers = min((int64_t)gridDim.x, (total + kWarps - 1) / kWarps);
   if ((int64_t)blockIdx.x >= workers) return;
   auto start_of = [&](int64_t i) { return i * total / workers; };
-  const int64_t end = start_of(blockIdx.x + 1);
-  int64_t at = start_of(blockIdx.x);
-  const int64_t begin = at;
+  const int64_t begin = start_of(blockIdx.x), end = start_of(blockIdx.x + 1);
+  auto warp_start = [&](int64_t w) { return begin + (end - begin) * w / kWarps; };
+  const int64_t wb = warp_start(warp), we = warp_start(warp + 1);   // this warp's run
+  auto unit_of = [&](int64_t tile) {                       // the last unit that starts at or before it
+    int u = 0, hi_u = n_units - 1;
+    while (u < hi_u) {
+      const int mid = (u + hi_u + 1) >> 1;
+      if (s_first[mid] <= tile) u = mid; else hi_u = mid - 1;
+    }
+    return u;
+  };
+  constexpr int kSlot = kCol * (HD + 2);                   // a part: M, l per column, O [column][dim]
 
   const Magic mg;
   uint8_t* area = smem + warp * H::kArea;
 
-  while (at < end) {
-    // ---- the unit
-    int unit = 0;                                          // the last one that starts at or before `at`
-    {
-      int hi_u = n_units - 1;
-      while (unit < hi_u) {
-        const int mid = (unit + hi_u + 1) >> 1;
-        if (s_first[mid] <= at) unit = mid; else hi_u = mid - 1;
-      }
+  // a tile's rows in its segment (rows <= 0: none)
+  auto tile_row = [&](int unit, int64_t tile, int& rows) {
+    const int j = (int)(tile - s_first[unit]), lo = s_lo[unit];
+    const int sr = min(A.sink, lo), nt_sink = (sr + TR - 1) / TR;
+    if (j < nt_sink) {
+      rows = min(TR, sr - j * TR);
+      return j * TR;
     }
+    const int r = lo + (j - nt_sink) * TR;
+    rows = min(TR, s_hi[unit] - r);
+    return r;
+  };
+  auto row_base = [&](int unit) {
+    const int s = unit / A.n_kv;
+    return A.seq[s].row0 + (int64_t)(unit - s * A.n_kv) * A.seq[s].cap;
+  };
+  int p_unit = wb < we ? unit_of(wb) : 0;                  // of the tile to fetch next
+  int64_t p_row0 = row_base(p_unit);
+  auto issue = [&](int64_t tile, int st) {
+    if (tile >= s_first[p_unit + 1]) {
+      do ++p_unit;
+      while (tile >= s_first[p_unit + 1]);
+      p_row0 = row_base(p_unit);
+    }
+    int rows;
+    const int r = tile_row(p_unit, tile, rows);
+    if (rows <= 0) return;
+    uint8_t* d = area + st * H::SB;
+    const uint8_t* ks = A.k + (p_row0 + r) * H::kRb;
+    const uint8_t* vsrc = A.v + (p_row0 + r) * H::vRb;
+    constexpr int kc = H::kRb / 16, vc = H::vRb / 16;      // 16-byte pieces of a row
+#pragma unroll
+    for (int i = 0; i < (TR * kc + 31) / 32; ++i) {
+      const int x = i * 32 + lane, rr = x / kc, c = x - rr * kc;
+      if (rr < rows) cp_async16(d + rr * H::kStride + c * 16, ks + rr * H::kRb + c * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < (TR * vc + 31) / 32; ++i) {
+      const int x = i * 32 + lane, rr = x / vc, c = x - rr * vc;
+      if (rr < rows) cp_async16(d + H::oV + rr * H::vStride + c * 16, vsrc + rr * H::vRb + c * 16);
+    }
+    auto copy_scales = [&](uint8_t* dst, const uint8_t* src) {
+      if constexpr (H::scRb == 16) cp_async16(dst, src);
+      else if constexpr (H::scRb == 8) cp_async8(dst, src);
+      else cp_async4(dst, src);
+    };
+    if (lane < rows) {
+      if constexpr (H::kKq) copy_scales(d + H::oKs + lane * H::scRb, A.ks + (p_row0 + r + lane) * H::scRb);
+      if constexpr (H::kVq) copy_scales(d + H::oVs + lane * H::scRb, A.vs + (p_row0 + r + lane) * H::scRb);
+      cp_async4(d + H::oPos + lane * 4, A.cpos + p_row0 + r + lane);
+    }
+  };
+  // the first tiles are on their way before anything else is asked for
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (wb + i < we) issue(wb + i, i);
+    cp_async_commit();
+  }
+
+  int st = 0;
+  int64_t at = wb;
+  for (int unit = p_unit < n_units && wb < we ? unit_of(wb) : n_units; at < we; ++unit) {
+    if (s_first[unit + 1] <= at) continue;                 // (a unit without tiles)
     const int s = unit / A.n_kv, g = unit - s * A.n_kv;
     const AttendSeq& S = A.seq[s];
-    const int64_t u0 = s_first[unit], u1 = s_first[unit + 1];          // the unit's tiles in the list
-    const int per = (int)(u1 - u0), j0 = (int)(at - u0), j1 = (int)(min(end, u1) - u0);   // those of this CTA
-    const int64_t row0 = S.row0 + (int64_t)g * S.cap;
-    const int32_t* rpos = A.cpos + row0;
     const int ncol = S.t * A.G;
-    const int lo = s_lo[unit], hi = s_hi[unit];
-    const int sr = min(A.sink, lo), nt_sink = (sr + TR - 1) / TR;
-    bool need_pos = true;                                  // until it is known that every token sees every row
-    auto tile_row = [&](int j, int& rows) {                // first row and rows of tile j (rows <= 0: none)
-      if (j < nt_sink) {
-        rows = min(TR, sr - j * TR);
-        return j * TR;
-      }
-      const int r = lo + (j - nt_sink) * TR;
-      rows = min(TR, hi - r);
-      return r;
-    };
-    auto issue = [&](int j, int st) {
-      int rows;
-      const int r = tile_row(j, rows);
-      if (rows <= 0) return;
-      uint8_t* d = area + st * H::SB;
-      const uint8_t* ks = A.k + (row0 + r) * H::kRb;
-      const uint8_t* vsrc = A.v + (row0 + r) * H::vRb;
-      constexpr int kc = H::kRb / 16, vc = H::vRb / 16;    // 16-byte pieces of a row
-#pragma unroll
-      for (int i = 0; i < (TR * kc + 31) / 32; ++i) {
-        const int x = i * 32 + lane, rr = x / kc, c = x - rr * kc;
-        if (rr < rows) cp_async16(d + rr * H::kStride + c * 16, ks + rr * H::kRb + c * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < (TR * vc + 31) / 32; ++i) {
-        const int x = i * 32 + lane, rr = x / vc, c = x - rr * vc;
-        if (rr < rows) cp_async16(d + H::oV + rr * H::vStride + c * 16, vsrc + rr * H::vRb + c * 16);
-      }
-      auto copy_scales = [&](uint8_t* dst, const uint8_t* src) {
-        if constexpr (H::scRb == 16) cp_async16(dst, src);
-        else if constexpr (H::scRb == 8) cp_async8(dst, src);
-        else cp_async4(dst, src);
-      };
-      if (lane < rows) {
-        if constexpr (H::kKq) copy_scales(d + H::oKs + lane * H::scRb, A.ks + (row0 + r + lane) * H::scRb);
-        if constexpr (H::kVq) copy_scales(d + H::oVs + lane * H::scRb, A.vs + (row0 + r + lane) * H::scRb);
-        if (need_pos) cp_async4(d + H::oPos + lane * 4, rpos + r + lane);
-      }
-    };
-    // this warp's tiles: j0 + warp, + kWarps, ...; the first are on their way
-    // before anything else is asked for
-    const int mine = j1 - j0 > warp ? (j1 - j0 - warp + kWarps - 1) / kWarps : 0;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < mine) issue(j0 + warp + i * kWarps, i);
-      cp_async_commit();
-    }
-
     int pmin = INT32_MAX, pmax = INT32_MIN;
     for (int i = 0; i < S.t; ++i) {
       const int p = A.pos[S.tok0 + i];
       pmin = min(pmin, p);
       pmax = max(pmax, p);
     }
-    need_pos = A.window > 0 || (hi > 0 && rpos[hi - 1] > pmin);
 
     // ---- queries: A fragments, columns gid and gid + 8; qf: their exponent
     uint32_t qa[NB * 2][2 * NT];                           // [step][column half * 2 ... k low, k high]
@@ -441,7 +451,6 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       const int32_t* tp = reinterpret_cast<const int32_t*>(tile_p + H::oPos);
       auto sees = [&](int row, int p) {                    // row of the tile, position of the query
         if (row >= rows) return false;
-        if (!need_pos) return true;
         const int q = tp[row];
         return q <= p && (A.window <= 0 || (int64_t)p - q < A.window || r + row < A.sink);
       };
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
           if constexpr (kMasked) {                         // rows that some token sees
             const int row = 2 * x / NB;
             on = on && row < rows &&
-                 (!need_pos || (tp[row] <= pmax && (A.window <= 0 || (int64_t)pmin - tp[row] < A.window || r + row < A.sink)));
+                 tp[row] <= pmax && (A.window <= 0 || (int64_t)pmin - tp[row] < A.window || r + row < A.sink);
           }
           if (on) {
             const float2 f = __half22float2(__habs2(vss[x]));
@@ -614,132 +623,214 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       }
     };
 
-    for (int i = 0; i < mine; ++i) {
-      if (i + kStages - 1 < mine) issue(j0 + warp + (i + kStages - 1) * kWarps, (i + kStages - 1) % kStages);
+    const int64_t last_tile = min(we, (int64_t)s_first[unit + 1]);
+    for (; at < last_tile; ++at) {
+      if (at + kStages - 1 < we) issue(at + kStages - 1, st == 0 ? kStages - 1 : st - 1);
       cp_async_commit();
       cp_async_wait<kStages - 1>();
       __syncwarp();
       int rows;
-      const int r = tile_row(j0 + warp + i * kWarps, rows);
-      const uint8_t* tile_p = area + (i % kStages) * H::SB;
+      const int r = tile_row(unit, at, rows);
+      const uint8_t* tile_p = area + st * H::SB;
       if (rows > 0) {
-        bool masked = rows < TR, skip = false;
-        if (need_pos) {
-          const int32_t* tp = reinterpret_cast<const int32_t*>(tile_p + H::oPos);
-          const int64_t first = tp[0], last = tp[rows - 1];
-          const bool in_sink = r + rows <= A.sink;
-          skip = first > pmax || (A.window > 0 && pmin - last >= A.window && r >= A.sink);
-          masked = masked || last > pmin || (A.window > 0 && pmax - first >= A.window && !in_sink);
-        }
+        const int32_t* tp = reinterpret_cast<const int32_t*>(tile_p + H::oPos);
+        const int first = tp[0], last = tp[rows - 1];
+        const bool skip = first > pmax || (A.window > 0 && (int64_t)pmin - last >= A.window && r >= A.sink);
+        const bool masked = rows < TR || last > pmin ||
+                            (A.window > 0 && (int64_t)pmax - first >= A.window && r + rows > A.sink);
         if (!skip) {
           if (masked) tile(std::true_type{}, tile_p, r, rows);
           else tile(std::false_type{}, tile_p, r, rows);
         }
       }
       __syncwarp();
+      st = st + 1 == kStages ? 0 : st + 1;
     }
-    cp_async_wait<0>();
-    __syncwarp();
 
-    // ---- join the warps: M, l per column, O [column][dim]
+    // ---- the unit's result, or this run's part of it
 #pragma unroll
     for (int h = 0; h < NT; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
-    float* res = reinterpret_cast<float*>(area);
-#pragma unroll
-    for (int h = 0; h < NT; ++h) {
-      if (t4 == 0) {
-        res[gid + 8 * h] = M[h];
-        res[kCol + gid + 8 * h] = l[h];
-      }
-#pragma unroll
-      for (int i = 0; i < HD / 16; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          int d;                                           // the dim of the accumulator's row
-          if constexpr (VT == TRIA_F16) d = 16 * i + gid + 8 * (c >> 1);
-          else if constexpr (VT == TRIA_Q8_0) d = 32 * (i >> 1) + 4 * gid + 2 * (i & 1) + (c >> 1);
-          else d = 32 * (i >> 1) + 16 * (i & 1) + 2 * gid + (c >> 1);
-          res[2 * kCol + (2 * t4 + (c & 1) + 8 * h) * HD + d] = o[i][h][c];
-        }
-    }
-    __syncthreads();
-    const bool whole = j0 == 0 && j1 == per;
-    const bool late = begin > u0;                          // the CTA's run starts inside the unit
-    float* slot = A.part + ((int64_t)blockIdx.x * 2 + (late ? 0 : 1)) * (kCol * (HD + 2));
-    auto write = [&](int col, int d, float val, float top, float sum) {
-      const int tok = S.tok0 + col / A.G, head = g * A.G + col % A.G;
-      act_store(A.out, A.type, (int64_t)tok * A.out_stride + (int64_t)head * HD + d, sum == 0.f ? 0.f : val / sum);
-      if (d == 0 && A.lse) A.lse[(int64_t)tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    auto dim_of = [&](int i, int c) {                      // the dim of an accumulator's row
+      if constexpr (VT == TRIA_F16) return 16 * i + gid + 8 * (c >> 1);
+      else if constexpr (VT == TRIA_Q8_0) return 32 * (i >> 1) + 4 * gid + 2 * (i & 1) + (c >> 1);
+      else return 32 * (i >> 1) + 16 * (i & 1) + 2 * gid + (c >> 1);
     };
-    for (int i = threadIdx.x; i < ncol * HD; i += kWarps * 32) {
-      const int col = i / HD, d = i - col * HD;
-      float top = -INFINITY, sum = 0.f, val = 0.f;
+    const bool early = s_first[unit] < wb;                 // it began in an earlier run
+    if (!early && s_first[unit + 1] <= we) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, reinterpret_cast<const float*>(smem + w * H::kArea)[col]);
+      for (int h = 0; h < NT; ++h) {
+        const int col = gid + 8 * h;
+        if (A.lse && t4 == 0 && col < ncol)
+          A.lse[(int64_t)(S.tok0 + col / A.G) * A.nq + g * A.G + col % A.G] =
+              l[h] == 0.f ? -INFINITY : (M[h] + log2f(l[h])) * 0.6931471805599453f;
+        const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {                      // columns 2t, 2t + 1
+          const float f = __shfl_sync(0xffffffffu, inv, 8 * t4 + 4 * e);
+          const int c2 = 2 * t4 + e + 8 * h;
+          if (c2 >= ncol) continue;
+          const int64_t to = (int64_t)(S.tok0 + c2 / A.G) * A.out_stride + (int64_t)(g * A.G + c2 % A.G) * HD;
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            act_store(A.out, A.type, to + dim_of(i, 0), o[i][h][e] * f);
+            act_store(A.out, A.type, to + dim_of(i, 2), o[i][h][2 + e] * f);
+          }
+        }
+      }
+    } else {
+      // the run's last unit: into its stages, which nothing uses any more
+      float* slot = at == we ? reinterpret_cast<float*>(area) : A.part + (int64_t)(blockIdx.x * kWarps + warp) * kSlot;
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+        if (t4 == 0) {
+          slot[gid + 8 * h] = M[h];
+          slot[kCol + gid + 8 * h] = l[h];
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) slot[2 * kCol + (2 * t4 + (c & 1) + 8 * h) * HD + dim_of(i, c)] = o[i][h][c];
+      }
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+
+  // ---- units that several runs share; a thread merges four dims of a column
+  auto add = [&](float4& v, float f, const float4& x) {
+    v.x = fmaf(x.x, f, v.x);
+    v.y = fmaf(x.y, f, v.y);
+    v.z = fmaf(x.z, f, v.z);
+    v.w = fmaf(x.w, f, v.w);
+  };
+  float* cta_parts = A.part + (int64_t)gridDim.x * kWarps * kSlot;
+  const int len = (int)(end - begin);
+  auto write = [&](int unit, int col, int d, const float4& val, float top, float sum) {
+    const int s = unit / A.n_kv, head = (unit - s * A.n_kv) * A.G + col % A.G;
+    const int64_t tok = A.seq[s].tok0 + col / A.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t w[2];
+    if (A.type == TRIA_F16) {
+      w[0] = pack_h2(val.x * inv, val.y * inv);
+      w[1] = pack_h2(val.z * inv, val.w * inv);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(val.x * inv, val.y * inv), b = __floats2bfloat162_rn(val.z * inv, val.w * inv);
+      w[0] = *reinterpret_cast<const uint32_t*>(&a);
+      w[1] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD + d) = make_uint2(w[0], w[1]);
+    if (d == 0 && A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  };
+  int open[2] = {-1, -1};                                  // units that reach into other CTAs: the first, the last
+  for (int unit = unit_of(begin); unit < n_units && s_first[unit] < end; ++unit) {
+    const int64_t u0 = s_first[unit], u1 = s_first[unit + 1];
+    if (u1 <= begin || u0 == u1) continue;
+    const bool inside = u0 >= begin && u1 <= end;
+    const int x0 = (int)(max(u0, begin) - begin), x1 = (int)(min(u1, end) - 1 - begin);
+    const int w0 = ((x0 + 1) * kWarps - 1) / len, w1 = ((x1 + 1) * kWarps - 1) / len;
+    if (inside && w0 == w1) continue;                      // written by its warp
+    // the runs that have tiles of it, and those of them whose last unit it is
+    // (their parts lie in their stages)
+    uint32_t have = 0, staged = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int e = len * (w + 1) / kWarps;
+      if (w < w0 || w > w1 || e == len * w / kWarps) continue;
+      have |= 1u << w;
+      if (e <= (int)(u1 - begin)) staged |= 1u << w;
+    }
+    const int which = u0 < begin ? 0 : 1;
+    if (!inside) open[which] = unit;
+    float* mine = cta_parts + ((int64_t)blockIdx.x * 2 + which) * kSlot;
+    for (int i = threadIdx.x; i < A.seq[unit / A.n_kv].t * A.G * (HD / 4); i += kWarps * 32) {
+      const int col = i / (HD / 4), d = 4 * (i - col * (HD / 4));
+      auto part = [&](int w) {
+        return (staged >> w) & 1u ? reinterpret_cast<const float*>(smem + w * H::kArea)
+                                  : A.part + (int64_t)(blockIdx.x * kWarps + w) * kSlot;
+      };
+      float top = -INFINITY, sum = 0.f;
+      float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if ((have >> w) & 1u) top = fmaxf(top, part(w)[col]);
       const float tb = top == -INFINITY ? 0.f : top;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* x = reinterpret_cast<const float*>(smem + w * H::kArea);
-        const float f = exp2_approx(x[col] - tb);
-        sum = fmaf(x[kCol + col], f, sum);
-        val = fmaf(x[2 * kCol + i], f, val);
-      }
-      if (whole) {
-        write(col, d, val, top, sum);
+      for (int w = 0; w < kWarps; ++w)
+        if ((have >> w) & 1u) {
+          const float* x = part(w);
+          const float f = exp2_approx(x[col] - tb);
+          sum = fmaf(x[kCol + col], f, sum);
+          add(val, f, *reinterpret_cast<const float4*>(x + 2 * kCol + col * HD + d));
+        }
+      if (inside) {
+        write(unit, col, d, val, top, sum);
       } else {
-        slot[2 * kCol + i] = val;
+        *reinterpret_cast<float4*>(mine + 2 * kCol + col * HD + d) = val;
         if (d == 0) {
-          slot[col] = top;
-          slot[kCol + col] = sum;
+          mine[col] = top;
+          mine[kCol + col] = sum;
         }
       }
     }
-    __syncthreads();
-    if (!whole) {
-      // the CTAs of the unit: those whose runs meet [u0, u1)
-      const int64_t c0 = ((u0 + 1) * workers - 1) / total, c1 = (u1 * workers - 1) / total;
-      uint32_t* count = A.count + unit;
-      if (threadIdx.x == 0) {
-        __threadfence();
-        s_flag = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_flag) {
-        for (int i = threadIdx.x; i < ncol * HD; i += kWarps * 32) {
-          const int col = i / HD;
-          float top = -INFINITY, sum = 0.f, val = 0.f;
-          // every CTA but the first starts inside the unit; four parts' loads at a time
-          auto part_of = [&](int64_t c) { return A.part + (c * 2 + (c > c0 || start_of(c0) > u0 ? 0 : 1)) * (kCol * (HD + 2)); };
-          for (int64_t c = c0; c <= c1; c += 4) {
-            float m[4], l4[4], v4[4];
+  }
+  __threadfence();
+  __syncthreads();
+  // the CTAs of a unit: those whose runs meet its tiles
+  auto cta_of = [&](int64_t tile) { return (int)(((tile + 1) * workers - 1) / total); };
+  if (threadIdx.x < 2) {
+    const int unit = threadIdx.x == 0 ? open[0] : open[1];
+    s_flag[threadIdx.x] = 0;
+    if (unit >= 0) {
+      const int others = cta_of(s_first[unit + 1] - 1) - cta_of(s_first[unit]);
+      s_flag[threadIdx.x] = atomicAdd(A.count + unit, 1u) == (uint32_t)others;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    if (!s_flag[which]) continue;
+    const int unit = which == 0 ? open[0] : open[1];
+    const int c0 = cta_of(s_first[unit]), c1 = cta_of(s_first[unit + 1] - 1);
+    for (int i = threadIdx.x; i < A.seq[unit / A.n_kv].t * A.G * (HD / 4); i += kWarps * 32) {
+      const int col = i / (HD / 4), d = 4 * (i - col * (HD / 4));
+      float top = -INFINITY, sum = 0.f;
+      float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = c0; c <= c1; c += 8) {                  // eight parts' loads at a time
+        float m[8], l8[8];
+        float4 v8[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float* x = part_of(min(c + k, c1));
-              m[k] = __ldcg(x + col);
-              l4[k] = __ldcg(x + kCol + col);
-              v4[k] = __ldcg(x + 2 * kCol + i);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (c + k > c1) break;
-              const float mn = fmaxf(top, m[k]), tb = mn == -INFINITY ? 0.f : mn;
-              const float f0 = exp2_approx(top - tb), f1 = exp2_approx(m[k] - tb);
-              sum = fmaf(sum, f0, l4[k] * f1);
-              val = fmaf(val, f0, v4[k] * f1);
-              top = mn;
-            }
+        for (int k = 0; k < 8; ++k) {
+          m[k] = -INFINITY;
+          l8[k] = 0.f;
+          v8[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c + k <= c1) {
+            const float* x = cta_parts + ((int64_t)(c + k) * 2 + (c + k > c0 ? 0 : 1)) * kSlot;   // only the first does not start inside
+            m[k] = __ldcg(x + col);
+            l8[k] = __ldcg(x + kCol + col);
+            v8[k] = __ldcg(reinterpret_cast<const float4*>(x + 2 * kCol + col * HD + d));
           }
-          write(col, i - col * HD, val, top, sum);
         }
-        if (threadIdx.x == 0) *count = 0u;
+        float mn = top;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mn = fmaxf(mn, m[k]);
+        const float tb = mn == -INFINITY ? 0.f : mn, f0 = exp2_approx(top - tb);
+        sum *= f0;
+        val = make_float4(val.x * f0, val.y * f0, val.z * f0, val.w * f0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = exp2_approx(m[k] - tb);
+          sum = fmaf(l8[k], f, sum);
+          add(val, f, v8[k]);
+        }
+        top = mn;
       }
-      __syncthreads();
+      write(unit, col, d, val, top, sum);
     }
-    at = min(end, u1);
+    if (threadIdx.x == 0) A.count[unit] = 0u;
   }
 }
 
