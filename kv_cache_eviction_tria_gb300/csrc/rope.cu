@@ -166,6 +166,19 @@ __device__ __forceinline__ void codes_q4(const float* x, float d, float* m) {
     m[i] = (d != 0.f ? fminf(fmaxf(floorf(__fadd_rn(__fdiv_rn(x[i], d), 8.5f)), 0.f), 15.f) : 8.f) + kMagic;
 }
 
+// The larger / smaller value, NaN when either is one (a block that holds a NaN
+// gets a NaN for its scale and reads as NaN, as an unquantised row would).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // cos and sin of 2 pi x / 2^32: the quadrant off the top bits, Taylor's series
 // on what is left (|r| <= pi / 4: 5e-10 and 2e-9 off).
 __device__ __forceinline__ void turn_cos_sin(uint32_t x, float& c, float& s) {
@@ -214,8 +227,8 @@ __device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_
   if (type == TRIA_Q8_0) {
     float am = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) am = fmaxf(am, fabsf(x[i]));
-    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    for (int i = 0; i < 16; ++i) am = max_nan(am, fabsf(x[i]));
+    am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, 1));
     const float d = __fdiv_rn(am, 127.f);
     const __half dh = __float2half_rn(d);
     const float ds = __half2float(dh);
@@ -235,8 +248,8 @@ __device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_
   float hi = x[0], lo = x[0];
 #pragma unroll
   for (int i = 1; i < 16; ++i) {
-    hi = fmaxf(hi, x[i]);
-    lo = fminf(lo, x[i]);
+    hi = max_nan(hi, x[i]);
+    lo = min_nan(lo, x[i]);
   }
   float big = hi > -lo ? hi : lo;
   if (hi == -lo)                                // both signs: the first one of the lane's values
@@ -248,7 +261,7 @@ __device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_
     }
   const float other = __shfl_xor_sync(0xffffffffu, big, 1);
   const float first = upper ? other : big, second = upper ? big : other;
-  big = fabsf(second) > fabsf(first) ? second : first;
+  big = fabsf(second) > fabsf(first) || second != second ? second : first;
   const float d = big * -0.125f;
   const __half dh = __float2half_rn(d + 0.f);   // an all-zero block's scale is +0
   const float ds = __half2float(dh);
@@ -713,6 +726,7 @@ extern "C" tria_status tria_rotate(const tria_rope* rope, tria_dtype type, const
     tria_status r;
     if ((r = check_heads(h.x, h.x_stride, h.n_heads, rope->head_dim, type)) != TRIA_OK) return r;
     if ((r = check_heads(h.out, h.out_stride, h.n_heads, rope->head_dim, type)) != TRIA_OK) return r;
+    if (h.out == h.x && h.out_stride != h.x_stride && n_tokens > 1) return TRIA_ERR_INVALID_ARG;
     if (h.norm && !aligned(h.norm, 16)) return TRIA_ERR_INVALID_ARG;
     A.part[i] = RopePart{h.x, h.out, h.norm, h.x_stride, h.out_stride, h.n_heads, 0, kPartDirect};
   }
@@ -749,6 +763,7 @@ extern "C" tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_c
     if (a->n_q_heads > 0) {
       if ((r = check_heads(a->q, a->q_stride, a->n_q_heads, hd, a->type)) != TRIA_OK) return r;
       if ((r = check_heads(a->q_out, a->q_out_stride, a->n_q_heads, hd, a->type)) != TRIA_OK) return r;
+      if (a->q_out == a->q && a->q_out_stride != a->q_stride && n_tokens > 1) return TRIA_ERR_INVALID_ARG;
     }
     if ((a->q_norm && !aligned(a->q_norm, 16)) || (a->k_norm && !aligned(a->k_norm, 16))) return TRIA_ERR_INVALID_ARG;
     if ((a->k_held && !aligned(a->k_held, 16)) || (a->v_held && !aligned(a->v_held, 16))) return TRIA_ERR_INVALID_ARG;

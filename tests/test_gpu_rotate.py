@@ -223,3 +223,34 @@ def test_append_qkv_equals_append_of_ready_rows(lib):
         for name, t in c.d.items():
             if t is not None:
                 assert t.cpu().numpy().tobytes() == d.d[name].cpu().numpy().tobytes(), (kt, vt, name)
+
+
+@pytest.mark.parametrize("kt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("at", [0, 15, 16, 31])
+def test_a_nan_reaches_its_block(lib, kt, at):
+    """A quantised block with a NaN reads as NaN in all of its values, in the cache and in what is held; the other
+    blocks are what they are without it."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((3, 2, 64)).astype(np.float32)
+    held = []
+    for bad in (False, True):
+        y = x.copy()
+        if bad:
+            y[1, 1, 32 + at] = np.nan
+        c = R.Cache(lib, np.random.default_rng(0), rows=[2], cap=[8], n_kv=2, hd=64, k_type=kt, v_type=kt)
+        kh, vh = (torch.empty(3, 2, 64, device="cuda") for _ in range(2))
+        pos = torch.tensor([50, 51, 52], device="cuda", dtype=torch.int32)
+        ws = c.ws(lib.workspace_size(c.cache, 0))
+        still = lib.Rope(head_dim=64, nonrot_dim=32, omega=[0.0] * 16)   # (a rotated NaN would reach its pair)
+        lib.append_qkv(still, c.cache, None, R.act(y, "f32"), R.act(y, "f32"), pos, ws=ws, k_held=kh, v_held=vh)
+        assert lib.device_status(ws) == lib.OK
+        cached = []
+        for name in ("k", "v"):
+            rows = np.stack([np.arange(3) + c.row0[0] + g * 8 + 2 for g in range(2)], 1)
+            cached.append(A.values(c.d[name].cpu().numpy()[rows], c.d[name + "_scale"].cpu().numpy()[rows], kt))
+        held.append([R.host(kh), R.host(vh)] + cached)
+    hurt = np.zeros(x.shape, bool)
+    hurt[1, 1, 32:] = True
+    for clean, got in zip(*held):
+        assert np.isnan(got[hurt]).all() and np.array_equal(got[~hurt], clean[~hurt])
+    assert np.array_equal(held[1][0], held[1][2], equal_nan=True) and np.array_equal(held[1][1], held[1][3], equal_nan=True)
