@@ -346,7 +346,10 @@ int sm_count() {
 
 // The kernels of a call run one after the other and share the arrival counters
 // and the space of the partial results. The layout covers every type of
-// queries.
+// queries. The counters, which have to be zero between calls, take the same
+// place for every shape, so that a workspace may serve calls of different
+// shapes: a decode step counts segments (at most kMaxSegments), the others
+// units that are split (fewer than two per SM).
 struct AttendLayout {
   size_t count, span, part, wide_k, wide_v, total;
   int units, split, prompt_split, sms;
@@ -389,7 +392,7 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   L.units = (int)units;
   L.split = plain_split(units * c->n_kv_heads, cap_max);
   L.count = up256(sizeof(Ctrl));
-  L.span = up256(L.count + sizeof(uint32_t) * (size_t)(std::max<int64_t>(units, c->n_seqs) * c->n_kv_heads));
+  L.span = up256(L.count + sizeof(uint32_t) * (size_t)kMaxSegments);
   L.part = up256(L.span + 2 * sizeof(int32_t) * (size_t)c->n_seqs * c->n_kv_heads);
   const size_t plain = L.split > 1 ? (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0;
   // a part a warp (at most 12 a CTA) and two a CTA
@@ -420,7 +423,9 @@ tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const i
   if ((r = check_cache(c)) != TRIA_OK) return r;
   if (!tok0 || n_q_heads < 1) return TRIA_ERR_INVALID_ARG;
   if (n_q_heads % c->n_kv_heads != 0 || n_q_heads / c->n_kv_heads > TRIA_MAX_GROUP) return TRIA_ERR_UNSUPPORTED;
-  return check_tokens(tok0, c->n_seqs);
+  if ((r = check_tokens(tok0, c->n_seqs)) != TRIA_OK) return r;
+  // columns (token x head) are counted in 32 bits
+  return (int64_t)tok0[c->n_seqs] * n_q_heads < ((int64_t)1 << 31) ? TRIA_OK : TRIA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -436,7 +441,7 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   if (!a) return TRIA_ERR_INVALID_ARG;
   if ((r = check_attend_shape(cache, a->n_q_heads, a->tok0)) != TRIA_OK) return r;
   if (!act_ok(a->type)) return TRIA_ERR_UNSUPPORTED;
-  if (a->window < 0 || a->sink < 0 || !(a->scale >= 0.0) || !isfinite(a->scale)) return TRIA_ERR_INVALID_ARG;
+  if (a->window < 0 || a->sink < 0 || !(a->scale >= 0.0) || !isfinite((float)a->scale)) return TRIA_ERR_INVALID_ARG;
   const int hd = cache->head_dim, nq = a->n_q_heads, n_tokens = a->tok0[cache->n_seqs];
   const int size = a->type == TRIA_F32 ? 4 : 2;
   if (n_tokens > 0) {
@@ -494,6 +499,9 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
       cols = std::max(cols, t * G);
     }
   }
+  if (prompt)   // a row of a TMA tile has a signed 32-bit coordinate
+    for (int s = 0; s < cache->n_seqs; ++s)
+      if (cache->seq_row0[s] + (int64_t)cache->n_kv_heads * cache->capacity[s] >= ((int64_t)1 << 31)) return TRIA_ERR_UNSUPPORTED;
   // each kernel sees the sequences it takes, the others without tokens
   auto take = [&](int path) {
     const int per = path == kPathPrompt ? prompt_cols(hd) : kCols;

@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         sl *= __uint_as_float((uint32_t)(127 + ex) << 23);
       }
     }
+    sl = fmaxf(sl, 0x1p-126f);                             // (times -inf stays -inf)
 #pragma unroll 1
     for (int c0q = 0; c0q < HD / 8; c0q += kPart) {
 #pragma unroll
@@ -785,7 +786,8 @@ bool plane_map_f16(CUtensorMap* m, const void* base, int hd, int64_t rows, int b
     return (Encode)fn;
   }();
   if (!encode) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)hd * 2};
+  // (a plane without rows is never read, but a map has one at least)
+  const cuuint64_t dims[2] = {(cuuint64_t)hd, (cuuint64_t)std::max<int64_t>(rows, 1)}, strides[1] = {(cuuint64_t)hd * 2};
   const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, steps[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

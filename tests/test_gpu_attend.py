@@ -253,3 +253,29 @@ def test_two_streams_with_their_own_workspaces(lib):
             lib.attend(c.cache, x, o, pos, ws=w, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(alone, both))
+
+
+def test_one_workspace_for_calls_of_different_shapes(lib):
+    """Calls whose units and parts differ leave a shared workspace fit for the next one."""
+    rng = np.random.default_rng(31)
+    c = R.Cache(lib, rng, rows=[900], cap=[1024], n_kv=8, hd=64, k_type="f16", v_type="f16")
+    ws = c.ws(max(lib.attend_workspace_size(c.cache, 32, t) for t in (1, 2, 50, 400)))
+    for i, (kind, t, window) in enumerate([("f32", 2, 0), ("f32", 50, 0), ("f16", 1, 0), ("f32", 50, 0), ("f16", 1, 300),
+                                           ("f16", 400, 0), ("f16", 2, 0), ("f16", 400, 0), ("f32", 50, 100)]):
+        run(lib, c, 32, kind, [t], window=window, seed=i, ws=ws)
+
+
+@pytest.mark.parametrize("kind,k", [("f16", "f16"), ("bf16", "q4_0"), ("f32", "f32")])
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_planes_without_rows(lib, kind, k, tokens):
+    c = R.Cache(lib, np.random.default_rng(2), rows=[0, 0], cap=[0, 0], n_kv=2, hd=64, k_type=k, v_type=k)
+    out, lse = run(lib, c, 8, kind, [tokens, 0])
+    assert (out[:tokens] == 0).all() and (lse[:tokens] == -np.inf).all()
+
+
+@pytest.mark.parametrize("kind,tokens", [("f16", 1), ("bf16", 1), ("f16", 40), ("bf16", 40), ("f32", 3)])
+@pytest.mark.parametrize("scale", [1e-44, 1e-60])
+def test_logits_near_zero(lib, kind, tokens, scale):
+    """A factor that vanishes in fp32 leaves equal weights; hidden rows stay hidden."""
+    c = R.Cache(lib, np.random.default_rng(3), rows=[70, 300], cap=[80, 300], n_kv=2, hd=128, k_type="f16", v_type="f16")
+    run(lib, c, 8, kind, [tokens, tokens], scale=scale, back=30)

@@ -210,6 +210,33 @@ def test_rotate_and_append_refusals(lib):
     append(tria.OK, tok0=(0, 0, 0), q=0, k=0, v=0, pos=0)
 
 
+def test_refusals_of_sizes_and_of_uneven_strides_in_place(lib):
+    """Counts that pass 31 bits, logit factors outside float's range, rows past a tile's 31-bit coordinate; an output
+    in the place of its input with another stride, whose heads would be overwritten before they are read."""
+    I, S = tria.ERR_INVALID_ARG, tria.ERR_UNSUPPORTED
+    c = cache()
+    t = np.asarray([0, 1 << 29, 1 << 29], np.int32)
+    s = c.c_struct()
+    assert lib.tria_attend_workspace_size(ctypes.byref(s), 4, t.ctypes.data) == 0
+    attention(lib, c, S, tok0=t)
+    attention(lib, c, I, scale=1e39)
+    attention(lib, cache(seq_row0=[0, (1 << 31) - 100]), S, tok0=(0, 9, 9))
+
+    class Handle(ctypes.Structure):
+        _fields_ = [("head_dim", ctypes.c_int32), ("nonrot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                    ("pad", ctypes.c_int32), ("mscale", ctypes.c_double), ("turns", ctypes.c_void_p)]
+    rope = Handle(64, 0, 0, 0, 1.0, None)
+    h = tria._Heads()
+    h.x, h.out, h.norm, h.n_heads, h.x_stride, h.out_stride = 0x1000, 0x1000, None, 2, 128, 256
+    assert lib.tria_rotate(ctypes.byref(rope), 1, ctypes.byref(h), 1, 3, 0x4000, 1e-6, None) == I
+    a = tria._Qkv()
+    a.type, a.n_q_heads, a.q, a.k, a.v, a.q_out = 1, 4, 0x1000, 0x2000, 0x3000, 0x1000
+    a.q_stride, a.k_stride, a.v_stride, a.q_out_stride, a.eps, a.pos = 512, 128, 128, 256, 1e-6, 0x5000
+    two = np.asarray([0, 1, 2], np.int32)
+    a.tok0 = two.ctypes.data
+    assert lib.tria_append_qkv(ctypes.byref(rope), ctypes.byref(s), ctypes.byref(a), 0x100000, 1 << 20, None) == I
+
+
 def test_q4_0_cache_in_the_other_entry_points(lib):
     """The pass's host checks take q4_0 planes, and bf16 is no type of a cache."""
     c = cache(k_type="q4_0", v_type="q4_0", k_scale=0x50000, v_scale=0x60000)
