@@ -36,7 +36,8 @@ namespace tria {
 namespace {
 
 constexpr int kRopeWarps = 16;      // one CTA per SM
-constexpr int kRopeSmem = 226 * 1024, kRopeStageMax = 12288;   // bytes of heads that a warp handles at once
+constexpr int kRopeSmem = 226 * 1024;
+constexpr int rope_stages(bool cache) { return cache ? 1 : 2; }
 constexpr int kPartDirect = 0, kPartKey = 1, kPartValue = 2;
 
 struct RopePart {
@@ -52,7 +53,7 @@ struct RopePart {
 struct RopeArgs {
   RopePart part[3];
   int32_t n_parts, n_tokens, groups;   // groups: of all parts, per token
-  int32_t per_warp, stage;             // groups a warp handles; bytes of its stage
+  int32_t per_warp, stage;             // groups a warp handles at once; bytes of a stage of them
   int32_t hd, rot, layout, lanes;      // lanes: per head, a power of two
   float eps, mscale, inv_hd;
   const unsigned long long* turns;
@@ -329,18 +330,18 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 1) k_rope(const __grid_consta
   const int eb = kInter ? 16 * p + 8 : ea + (rotary ? half : (A.hd - A.rot) / 2);
   const int oa = to_half ? f0 : ea, ob = to_half ? f0 + half : eb;
   const int head_bytes = A.hd * (int)sizeof(T), group_bytes = hpw * head_bytes;
-  uint8_t* stage = smem + warp * A.stage;
-  float* key_buf = reinterpret_cast<float*>(smem + kRopeWarps * A.stage) + (warp * hpw + sub) * (A.hd + 4);
-  const uint32_t units_per_token = (A.groups + A.per_warp - 1) / A.per_warp;   // (their product fits: checked by the host)
-  const uint32_t total = (uint32_t)A.n_tokens * units_per_token, step = gridDim.x * kRopeWarps;
-  const uint32_t first = blockIdx.x * kRopeWarps + warp;
+  constexpr int kStages = rope_stages(kCache);
+  uint8_t* stages = smem + warp * kStages * A.stage;
+  float* key_buf = reinterpret_cast<float*>(smem + kRopeWarps * kStages * A.stage) + (warp * hpw + sub) * (A.hd + 4);
+  // a warp's share of the groups of all tokens (their number fits: checked by the host)
+  const uint32_t total = (uint32_t)A.n_tokens * (uint32_t)A.groups;
+  const uint32_t id = blockIdx.x * kRopeWarps + warp, n_warps = gridDim.x * kRopeWarps;
+  uint32_t at = (uint32_t)((uint64_t)total * id / n_warps);
+  const uint32_t end = (uint32_t)((uint64_t)total * (id + 1) / n_warps);
 
-  // starts the copies of a unit's heads into the stage, group after group
-  auto fetch = [&](uint32_t u) {
-    const int tok = (int)(u / units_per_token), g0 = (int)(u - (uint32_t)tok * units_per_token) * A.per_warp;
-    const int g1 = min(A.groups, g0 + A.per_warp);
+  // starts the copies of groups g0 .. g1 of a token's heads into a stage, group after group
+  auto fetch = [&](uint8_t* dst, int tok, int g0, int g1) {
     int base = 0;
-    uint8_t* dst = stage;
 #pragma unroll 1
     for (int pi = 0; pi < A.n_parts; ++pi) {
       const RopePart& Q = A.part[pi];
@@ -353,150 +354,175 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 1) k_rope(const __grid_consta
       dst += (ge - ga) * group_bytes;
     }
   };
-  for (uint32_t u = first; u < total; u += step) {
-    fetch(u);
+  // the groups at hand (of one token, at most a stage's); the next ones are on their way meanwhile
+  int tok = 0, g0 = 0, g1 = 0, last_tok = -1, position = 0, seq = 0, row = 0, turn = 0;
+  bool row_ok = false;
+  float2 cs[4], sn[4], ns[4];                     // cosines, sines and their negatives of the pairs
+  while (g1 > 0 || at < end) {
+    int n_tok = 0, n_g0 = 0, n_g1 = 0;
+    if (at < end) {
+      n_tok = (int)(at / (uint32_t)A.groups);
+      n_g0 = (int)(at - (uint32_t)n_tok * (uint32_t)A.groups);
+      n_g1 = min(min(A.groups, n_g0 + A.per_warp), n_g0 + (int)(end - at));
+      at += (uint32_t)(n_g1 - n_g0);
+      fetch(stages + turn * A.stage, n_tok, n_g0, n_g1);
+    }
     cp_async_commit();
-    const int tok = (int)(u / units_per_token), g0 = (int)(u - (uint32_t)tok * units_per_token) * A.per_warp;
-    const int g1 = min(A.groups, g0 + A.per_warp);
-    const int position = A.pos[tok];
-    int seq = 0, row = 0;
-    bool row_ok = false;
-    if constexpr (kCache) {
-      int lo = 0, hi = A.n_seqs - 1;              // the last sequence whose first token is <= tok
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (A.tok0[mid] <= tok) lo = mid; else hi = mid - 1;
-      }
-      seq = lo;
-      const int t = A.tok0[seq + 1] - A.tok0[seq];
-      const int n = A.n_before ? A.n_before[seq] : *((volatile const int32_t*)(A.n_live + seq));
-      row_ok = qkv_error(n, t, A.cap[seq]) == 0u;
-      row = n + (tok - A.tok0[seq]);
+    if constexpr (kStages == 1) {
+      tok = n_tok;
+      g0 = n_g0;
+      g1 = n_g1;
+    } else {
+      turn ^= 1;
     }
-    float2 cs[4], sn[4], ns[4];                   // cosines, sines and their negatives of the pairs
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cs[i] = make_float2(1.f, 1.f);
-      sn[i] = make_float2(0.f, 0.f);
-      if (rotary) {
-        const unsigned long long x = (unsigned long long)(long long)position;
-        turn_cos_sin((uint32_t)((x * A.turns[f0 + 2 * i]) >> 32), cs[i].x, sn[i].x);
-        turn_cos_sin((uint32_t)((x * A.turns[f0 + 2 * i + 1]) >> 32), cs[i].y, sn[i].y);
-        cs[i] = make_float2(cs[i].x * A.mscale, cs[i].y * A.mscale);
-        sn[i] = make_float2(sn[i].x * A.mscale, sn[i].y * A.mscale);
-      }
-      ns[i] = make_float2(-sn[i].x, -sn[i].y);
-    }
-    cp_async_wait<0>();
-    __syncwarp();
-    const uint8_t* in = stage + sub * head_bytes;
-    int base = 0;
-#pragma unroll 1
-    for (int pi = 0; pi < A.n_parts; ++pi) {
-      const RopePart& Q = A.part[pi];
-      const int ga = max(g0 - base, 0), ge = min(g1 - base, Q.groups);
-      base += Q.groups;
-      if (ga >= ge) continue;
-      int head = ga * hpw + sub;
-      T* out = reinterpret_cast<T*>(Q.out) + (int64_t)tok * Q.out_stride + (int64_t)head * A.hd;
-      if (kCache && Q.kind == kPartValue) {
-#pragma unroll 1
-        for (int gi = ga; gi < ge; ++gi, head += hpw, in += group_bytes, out += hpw * A.hd) {
-          const bool on = on_dim && head < Q.heads;
-          // (a lane past head_dim holds zeros; a whole head past the last one, junk
-          // that goes nowhere)
-          float a[16] = {};
-          if (on_dim) {
-            load8(reinterpret_cast<const T*>(in) + 16 * p, a);
-            load8(reinterpret_cast<const T*>(in) + 16 * p + 8, a + 8);
+    if (g1 > 0) {
+      if (tok != last_tok) {
+        last_tok = tok;
+        position = A.pos[tok];
+        if constexpr (kCache) {
+          int lo = 0, hi = A.n_seqs - 1;              // the last sequence whose first token is <= tok
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (A.tok0[mid] <= tok) lo = mid; else hi = mid - 1;
           }
-          const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
-          hold16(a, A.v_type, A.v, A.vs, r, A.hd, 16 * p, on && row_ok);
-          if (on && row_ok && Q.out) {
-            store8<T>(out + 16 * p, a);
-            store8<T>(out + 16 * p + 8, a + 8);
-          }
+          seq = lo;
+          const int t = A.tok0[seq + 1] - A.tok0[seq];
+          const int n = A.n_before ? A.n_before[seq] : *((volatile const int32_t*)(A.n_live + seq));
+          row_ok = qkv_error(n, t, A.cap[seq]) == 0u;
+          row = n + (tok - A.tok0[seq]);
         }
-        continue;
-      }
-      Pairs w;
-      if (Q.norm && on_dim) load_pairs<LAYOUT>(Q.norm, ea, eb, w);
-#pragma unroll 1
-      for (int gi = ga; gi < ge; ++gi, head += hpw, in += group_bytes, out += hpw * A.hd) {
-        const bool on = on_dim && head < Q.heads;
-        Pairs a = {};
-        if (on_dim) load_pairs<LAYOUT>(reinterpret_cast<const T*>(in), ea, eb, a);
-        if (Q.norm) {
-          float2 sq = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sq = __ffma2_rn(a.s[i], a.s[i], __ffma2_rn(a.f[i], a.f[i], sq));
-          float ss = sq.x + sq.y;
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1)
-            if (o < A.lanes) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * A.inv_hd + A.eps);
-          const float2 r2 = make_float2(r, r);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a.f[i] = __fmul2_rn(__fmul2_rn(a.f[i], r2), w.f[i]);
-            a.s[i] = __fmul2_rn(__fmul2_rn(a.s[i], r2), w.s[i]);
-          }
-        }
-        if (rotary) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 x = __ffma2_rn(a.f[i], cs[i], __fmul2_rn(a.s[i], ns[i]));
-            a.s[i] = __ffma2_rn(a.f[i], sn[i], __fmul2_rn(a.s[i], cs[i]));
-            a.f[i] = x;
-          }
-        }
-        float b[16];                              // first members, then second ones (or pairs)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (LAYOUT == TRIA_ROPE_INTERLEAVED || (LAYOUT == TRIA_ROPE_INTERLEAVED_TO_HALF && !rotary)) {
-            b[4 * i] = a.f[i].x;
-            b[4 * i + 1] = a.s[i].x;
-            b[4 * i + 2] = a.f[i].y;
-            b[4 * i + 3] = a.s[i].y;
-          } else {
-            b[2 * i] = a.f[i].x;
-            b[2 * i + 1] = a.f[i].y;
-            b[8 + 2 * i] = a.s[i].x;
-            b[8 + 2 * i + 1] = a.s[i].y;
+          cs[i] = make_float2(1.f, 1.f);
+          sn[i] = make_float2(0.f, 0.f);
+          if (rotary) {
+            const unsigned long long x = (unsigned long long)(long long)position;
+            turn_cos_sin((uint32_t)((x * A.turns[f0 + 2 * i]) >> 32), cs[i].x, sn[i].x);
+            turn_cos_sin((uint32_t)((x * A.turns[f0 + 2 * i + 1]) >> 32), cs[i].y, sn[i].y);
+            cs[i] = make_float2(cs[i].x * A.mscale, cs[i].y * A.mscale);
+            sn[i] = make_float2(sn[i].x * A.mscale, sn[i].y * A.mscale);
           }
+          ns[i] = make_float2(-sn[i].x, -sn[i].y);
         }
-        if (!kCache || Q.kind == kPartDirect) {
-          if (on) {
-            store8<T>(out + oa, b);
-            store8<T>(out + ob, b + 8);
+      }
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* in = stages + turn * A.stage + sub * head_bytes;
+      int base = 0;
+#pragma unroll 1
+      for (int pi = 0; pi < A.n_parts; ++pi) {
+        const RopePart& Q = A.part[pi];
+        const int ga = max(g0 - base, 0), ge = min(g1 - base, Q.groups);
+        base += Q.groups;
+        if (ga >= ge) continue;
+        int head = ga * hpw + sub;
+        T* out = reinterpret_cast<T*>(Q.out) + (int64_t)tok * Q.out_stride + (int64_t)head * A.hd;
+        if (kCache && Q.kind == kPartValue) {
+#pragma unroll 1
+          for (int gi = ga; gi < ge; ++gi, head += hpw, in += group_bytes, out += hpw * A.hd) {
+            const bool on = on_dim && head < Q.heads;
+            // (a lane past head_dim holds zeros; a whole head past the last one, junk
+            // that goes nowhere)
+            float a[16] = {};
+            if (on_dim) {
+              load8(reinterpret_cast<const T*>(in) + 16 * p, a);
+              load8(reinterpret_cast<const T*>(in) + 16 * p + 8, a + 8);
+            }
+            const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
+            hold16(a, A.v_type, A.v, A.vs, r, A.hd, 16 * p, on && row_ok);
+            if (on && row_ok && Q.out) {
+              store8<T>(out + 16 * p, a);
+              store8<T>(out + 16 * p + 8, a + 8);
+            }
           }
           continue;
         }
-        if constexpr (kCache) {
-          // a key on its way into the cache: to consecutive dims through shared memory
-          __syncwarp();
-          if (on) {
-            store8<float>(key_buf + oa, b);
-            store8<float>(key_buf + ob, b + 8);
+        Pairs w;
+        if (Q.norm && on_dim) load_pairs<LAYOUT>(Q.norm, ea, eb, w);
+#pragma unroll 1
+        for (int gi = ga; gi < ge; ++gi, head += hpw, in += group_bytes, out += hpw * A.hd) {
+          const bool on = on_dim && head < Q.heads;
+          Pairs a = {};
+          if (on_dim) load_pairs<LAYOUT>(reinterpret_cast<const T*>(in), ea, eb, a);
+          if (Q.norm) {
+            float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sq = __ffma2_rn(a.s[i], a.s[i], __ffma2_rn(a.f[i], a.f[i], sq));
+            float ss = sq.x + sq.y;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1)
+              if (o < A.lanes) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float r = rsqrtf(ss * A.inv_hd + A.eps);
+            const float2 r2 = make_float2(r, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a.f[i] = __fmul2_rn(__fmul2_rn(a.f[i], r2), w.f[i]);
+              a.s[i] = __fmul2_rn(__fmul2_rn(a.s[i], r2), w.s[i]);
+            }
           }
-          __syncwarp();
-          if (on) {
-            load8(key_buf + 16 * p, b);
-            load8(key_buf + 16 * p + 8, b + 8);
+          if (rotary) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = __ffma2_rn(a.f[i], cs[i], __fmul2_rn(a.s[i], ns[i]));
+              a.s[i] = __ffma2_rn(a.f[i], sn[i], __fmul2_rn(a.s[i], cs[i]));
+              a.f[i] = x;
+            }
           }
-          const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
-          hold16(b, A.k_type, A.k, A.ks, r, A.hd, 16 * p, on && row_ok);
-          if (on && row_ok) {
-            if (p == 0) A.cpos[r] = position;
-            if (Q.out) {
-              store8<T>(out + 16 * p, b);
-              store8<T>(out + 16 * p + 8, b + 8);
+          float b[16];                              // first members, then second ones (or pairs)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (LAYOUT == TRIA_ROPE_INTERLEAVED || (LAYOUT == TRIA_ROPE_INTERLEAVED_TO_HALF && !rotary)) {
+              b[4 * i] = a.f[i].x;
+              b[4 * i + 1] = a.s[i].x;
+              b[4 * i + 2] = a.f[i].y;
+              b[4 * i + 3] = a.s[i].y;
+            } else {
+              b[2 * i] = a.f[i].x;
+              b[2 * i + 1] = a.f[i].y;
+              b[8 + 2 * i] = a.s[i].x;
+              b[8 + 2 * i + 1] = a.s[i].y;
+            }
+          }
+          if (!kCache || Q.kind == kPartDirect) {
+            if (on) {
+              store8<T>(out + oa, b);
+              store8<T>(out + ob, b + 8);
+            }
+            continue;
+          }
+          if constexpr (kCache) {
+            // a key on its way into the cache: to consecutive dims through shared memory
+            __syncwarp();
+            if (on) {
+              store8<float>(key_buf + oa, b);
+              store8<float>(key_buf + ob, b + 8);
+            }
+            __syncwarp();
+            if (on) {
+              load8(key_buf + 16 * p, b);
+              load8(key_buf + 16 * p + 8, b + 8);
+            }
+            const int64_t r = A.row0[seq] + (int64_t)head * A.cap[seq] + row;
+            hold16(b, A.k_type, A.k, A.ks, r, A.hd, 16 * p, on && row_ok);
+            if (on && row_ok) {
+              if (p == 0) A.cpos[r] = position;
+              if (Q.out) {
+                store8<T>(out + 16 * p, b);
+                store8<T>(out + 16 * p + 8, b + 8);
+              }
             }
           }
         }
       }
+      __syncwarp();                               // the stage is free
     }
-    __syncwarp();                                 // the stage is free
+    if constexpr (kStages == 1) {
+      g1 = 0;
+    } else {
+      tok = n_tok;
+      g0 = n_g0;
+      g1 = n_g1;
+    }
   }
   if constexpr (kCache) {
     // n_live changes once nothing reads it any more: at once when the rows
@@ -534,10 +560,9 @@ int ceil_pow2(int x) {
 
 template <typename T, bool kCache, int LAYOUT>
 cudaError_t launch_rope_tl(const RopeArgs& A, cudaStream_t st) {
-  const int64_t upt = (A.groups + A.per_warp - 1) / A.per_warp;
-  const int64_t want = ((int64_t)A.n_tokens * upt + kRopeWarps - 1) / kRopeWarps;
+  const int64_t want = ((int64_t)A.n_tokens * A.groups + kRopeWarps - 1) / kRopeWarps;
   const int grid = (int)std::min<int64_t>(std::max<int64_t>(want, 1), 152);
-  const int smem = kRopeWarps * (A.stage + (kCache ? (32 / A.lanes) * (A.hd + 4) * (int)sizeof(float) : 0));
+  const int smem = kRopeWarps * (rope_stages(kCache) * A.stage + (kCache ? (32 / A.lanes) * (A.hd + 4) * (int)sizeof(float) : 0));
   auto kern = k_rope<T, kCache, LAYOUT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -559,11 +584,10 @@ cudaError_t launch_rope(const RopeArgs& A, int type, cudaStream_t st) {
   return launch_rope_t<__nv_bfloat16, kCache>(A, st);
 }
 
-// Work of a warp at once: one group of heads while the groups do not fill the
-// GPU's warps (a single token then takes one short step in as many warps as it
-// has groups), else as many groups of a token as a stage holds, which share
-// the sines and cosines.
-void finish_args(RopeArgs& A, const tria_rope* rope, int type) {
+// Work of a warp at once: as many groups of a token as a stage holds, which
+// share the sines and cosines. (A single token takes one short step in as many
+// warps as it has groups.)
+void finish_args(RopeArgs& A, const tria_rope* rope, int type, bool cache) {
   A.hd = rope->head_dim;
   A.rot = rope->head_dim - rope->nonrot_dim;
   A.layout = rope->layout;
@@ -577,11 +601,9 @@ void finish_args(RopeArgs& A, const tria_rope* rope, int type) {
     A.part[i].groups = (A.part[i].heads + hpw - 1) / hpw;
     A.groups += A.part[i].groups;
   }
-  const int64_t total = (int64_t)A.n_tokens * A.groups;
-  // stages and the keys' buffers of all warps fill shared memory
+  // two stages a warp and the keys' buffers fill shared memory
   const int room = (kRopeSmem / kRopeWarps - hpw * (A.hd + 4) * (int)sizeof(float)) & ~15;
-  const int most = std::min(std::min(room, kRopeStageMax) / group_bytes, A.groups);
-  A.per_warp = (int)std::min<int64_t>(std::max<int64_t>(total / (kRopeWarps * 152), 1), most);
+  A.per_warp = std::min(room / rope_stages(cache) / group_bytes, A.groups);
   A.stage = A.per_warp * group_bytes;
 }
 
@@ -734,7 +756,7 @@ extern "C" tria_status tria_rotate(const tria_rope* rope, tria_dtype type, const
   A.n_tokens = n_tokens;
   A.eps = (float)eps;
   A.pos = pos;
-  finish_args(A, rope, type);
+  finish_args(A, rope, type, false);
   return launch_rope<false>(A, type, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
 
@@ -794,6 +816,6 @@ extern "C" tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_c
     A.cap[s] = cache->capacity[s];
   }
   for (int s = 0; s <= cache->n_seqs; ++s) A.tok0[s] = a->tok0[s];
-  finish_args(A, rope, a->type);
+  finish_args(A, rope, a->type, true);
   return launch_rope<true>(A, a->type, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
