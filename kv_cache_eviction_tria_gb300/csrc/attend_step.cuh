@@ -297,28 +297,19 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
     const int s = unit / A.n_kv, g = unit - s * A.n_kv;
     const AttendSeq& S = A.seq[s];
     const int ncol = S.t * A.G;
-    int pmin = INT32_MAX, pmax = INT32_MIN;
-    for (int i = 0; i < S.t; ++i) {
-      const int p = A.pos[S.tok0 + i];
-      pmin = min(pmin, p);
-      pmax = max(pmax, p);
-    }
-
     // ---- queries: A fragments, columns gid and gid + 8; qf: their exponent
     uint32_t qa[NB * 2][2 * NT];                           // [step][column half * 2 ... k low, k high]
     float qf[NT];
     int pq[NT];
+    uint32_t raw[NT][NB][4];                               // pairs of fp16 or bf16, on their way before the positions
 #pragma unroll
     for (int h = 0; h < NT; ++h) {
       const int col = gid + 8 * h;
       const bool on = col < ncol;
       const int tok = S.tok0 + (on ? col / A.G : 0);
       const int64_t qoff = (int64_t)tok * A.q_stride + (int64_t)(g * A.G + (on ? col % A.G : 0)) * HD;
-      pq[h] = on ? A.pos[tok] : INT32_MIN;
-      float x[NB][8];
-      float am = 0.f;
       const uint16_t* qp = reinterpret_cast<const uint16_t*>(A.q) + qoff;
-      uint32_t raw[NB][4];                                 // pairs of fp16 or bf16
+      pq[h] = on ? A.pos[tok] : INT32_MIN;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         // dims of the thread: fp16 keys 2t, 2t+1, 8+2t, 9+2t (+16); codes 4t .. 4t+3 (+16)
@@ -326,20 +317,32 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint2 v = on ? *reinterpret_cast<const uint2*>(qp + 32 * b + 16 * k + 4 * t4) : make_uint2(0, 0);
-            raw[b][2 * k] = v.x;
-            raw[b][2 * k + 1] = v.y;
+            raw[h][b][2 * k] = v.x;
+            raw[h][b][2 * k + 1] = v.y;
           }
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            raw[b][k] = on ? *reinterpret_cast<const uint32_t*>(qp + 32 * b + 8 * k + 2 * t4) : 0u;
+            raw[h][b][k] = on ? *reinterpret_cast<const uint32_t*>(qp + 32 * b + 8 * k + 2 * t4) : 0u;
         }
       }
+    }
+    int pmin = INT32_MAX, pmax = INT32_MIN;
+    for (int i = 0; i < S.t; ++i) {
+      const int p = A.pos[S.tok0 + i];
+      pmin = min(pmin, p);
+      pmax = max(pmax, p);
+    }
+
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      float x[NB][8];
+      float am = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t w = raw[b][k];
+          const uint32_t w = raw[h][b][k];
           const float2 f = A.type == TRIA_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
                                               : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
           x[b][2 * k] = f.x;
@@ -751,20 +754,37 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
         return (staged >> w) & 1u ? reinterpret_cast<const float*>(smem + w * H::kArea)
                                   : A.part + (int64_t)(blockIdx.x * kWarps + w) * kSlot;
       };
+      // (loads without branches, in the place of a part that is not there one that is:
+      // they are in flight together)
+      float m[kWarps], l[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* x = part((have >> w) & 1u ? w : w0);
+        m[w] = x[col];
+        l[w] = x[kCol + col];
+      }
       float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (!((have >> w) & 1u)) m[w] = -INFINITY;
+        top = fmaxf(top, m[w]);
+      }
+      const float tb = top == -INFINITY ? 0.f : top;
       float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if ((have >> w) & 1u) top = fmaxf(top, part(w)[col]);
-      const float tb = top == -INFINITY ? 0.f : top;
+      for (int w4 = 0; w4 < kWarps; w4 += 4) {
+        float4 v[4];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if ((have >> w) & 1u) {
-          const float* x = part(w);
-          const float f = exp2_approx(x[col] - tb);
-          sum = fmaf(x[kCol + col], f, sum);
-          add(val, f, *reinterpret_cast<const float4*>(x + 2 * kCol + col * HD + d));
-        }
+        for (int k = 0; k < 4; ++k)
+          v[k] = *reinterpret_cast<const float4*>(part((have >> (w4 + k)) & 1u ? w4 + k : w0) + 2 * kCol + col * HD + d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((have >> (w4 + k)) & 1u) {                   // (a NaN in another's part stays there)
+            const float f = exp2_approx(m[w4 + k] - tb);
+            sum = fmaf(l[w4 + k], f, sum);
+            add(val, f, v[k]);
+          }
+      }
       if (inside) {
         write(unit, col, d, val, top, sum);
       } else {
@@ -804,16 +824,15 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
         float4 v8[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          m[k] = -INFINITY;
-          l8[k] = 0.f;
-          v8[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c + k <= c1) {
-            const float* x = cta_parts + ((int64_t)(c + k) * 2 + (c + k > c0 ? 0 : 1)) * kSlot;   // only the first does not start inside
-            m[k] = __ldcg(x + col);
-            l8[k] = __ldcg(x + kCol + col);
-            v8[k] = __ldcg(reinterpret_cast<const float4*>(x + 2 * kCol + col * HD + d));
-          }
+          const int ck = min(c + k, c1);
+          const float* x = cta_parts + ((int64_t)ck * 2 + (ck > c0 ? 0 : 1)) * kSlot;   // only the first does not start inside
+          m[k] = __ldcg(x + col);
+          l8[k] = __ldcg(x + kCol + col);
+          v8[k] = __ldcg(reinterpret_cast<const float4*>(x + 2 * kCol + col * HD + d));
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k > c1) m[k] = -INFINITY;
         float mn = top;
 #pragma unroll
         for (int k = 0; k < 8; ++k) mn = fmaxf(mn, m[k]);
@@ -821,11 +840,12 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
         sum *= f0;
         val = make_float4(val.x * f0, val.y * f0, val.z * f0, val.w * f0);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float f = exp2_approx(m[k] - tb);
-          sum = fmaf(l8[k], f, sum);
-          add(val, f, v8[k]);
-        }
+        for (int k = 0; k < 8; ++k)
+          if (c + k <= c1) {
+            const float f = exp2_approx(m[k] - tb);
+            sum = fmaf(l8[k], f, sum);
+            add(val, f, v8[k]);
+          }
         top = mn;
       }
       write(unit, col, d, val, top, sum);
