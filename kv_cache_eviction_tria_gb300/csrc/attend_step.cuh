@@ -757,11 +757,13 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       // (loads without branches, in the place of a part that is not there one that is:
       // they are in flight together)
       float m[kWarps], l[kWarps];
+      float4 v[kWarps];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* x = part((have >> w) & 1u ? w : w0);
         m[w] = x[col];
         l[w] = x[kCol + col];
+        v[w] = *reinterpret_cast<const float4*>(x + 2 * kCol + col * HD + d);
       }
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -772,19 +774,12 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       const float tb = top == -INFINITY ? 0.f : top;
       float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w4 = 0; w4 < kWarps; w4 += 4) {
-        float4 v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = *reinterpret_cast<const float4*>(part((have >> (w4 + k)) & 1u ? w4 + k : w0) + 2 * kCol + col * HD + d);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((have >> (w4 + k)) & 1u) {                   // (a NaN in another's part stays there)
-            const float f = exp2_approx(m[w4 + k] - tb);
-            sum = fmaf(l[w4 + k], f, sum);
-            add(val, f, v[k]);
-          }
-      }
+      for (int w = 0; w < kWarps; ++w)
+        if ((have >> w) & 1u) {                            // (a NaN in another's part stays there)
+          const float f = exp2_approx(m[w] - tb);
+          sum = fmaf(l[w], f, sum);
+          add(val, f, v[w]);
+        }
       if (inside) {
         write(unit, col, d, val, top, sum);
       } else {
