@@ -630,7 +630,7 @@ typedef struct tria_heads {
 /* Norm and rotation of one or two sets of heads (queries and keys) in one
  * pass. pos: device int32 [n_tokens] absolute positions. type: F32, F16 or
  * BF16, of x and out; computed in fp32, rounded once. n_tokens = 0 does
- * nothing. */
+ * nothing. UNSUPPORTED: type, 2^31 or more tokens x heads. */
 tria_status tria_rotate(const tria_rope* rope, tria_dtype type, const tria_heads* parts, int32_t n_parts,
                         int32_t n_tokens, const int32_t* pos, double eps, void* stream);
 
@@ -662,6 +662,7 @@ typedef struct tria_qkv {
  *   q8_0: d = max |x| / 127, code = x / d rounded half away from zero
  *   q4_0: d = m / -8 with m the first value of largest modulus, code =
  *         min(15, floor(x / d + 8.5)); scales are stored as fp16(d)
+ *   a block with a NaN gets a NaN for its scale
  * The host errors are INVALID_ARG, UNSUPPORTED (type), WORKSPACE (ws: a
  * workspace of this cache, only its control words are used); device errors as
  * tria_append, and a sequence with one is left unchanged (its queries are
@@ -676,9 +677,11 @@ tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_cache* cache
  * with a window, p - pos[r] < window or r < sink:
  *   out = sum_r softmax_r(scale q . K_r) V_r,   lse = ln sum_r exp(scale q . K_r)
  * A token that sees no row gets out = 0 and lse = -inf. Rows that a token
- * does not see never count, whatever they hold (one that sees a row with a
- * non-finite scale has no defined result). Positions must ascend
- * strictly with the rows of a segment (as appends and passes leave them). */
+ * does not see never count, whatever they hold. A token that sees a value row
+ * with an infinity or NaN gets non-finite values, possibly in every dim; one
+ * that sees a row with a non-finite scale has no defined result. Positions
+ * must ascend strictly with the rows of a segment (as appends and passes leave
+ * them); those of the tokens may come in any order. */
 typedef struct tria_attention {
   tria_dtype type;           /* F32, F16 or BF16: q and out */
   int32_t n_q_heads;
@@ -695,16 +698,24 @@ typedef struct tria_attention {
 
 /* Workspace bytes of tria_attend for these shapes (0 on invalid input). The
  * workspace is zeroed once (tria_workspace_init) and not shared with other
- * calls that overlap on the GPU, nor with the pass's workspace. */
+ * calls that overlap on the GPU, nor with the pass's workspace; one that is
+ * large enough for each serves calls of different shapes. Prompts (more than
+ * 16 tokens x query heads per KV head in a sequence) over q8_0 or q4_0 planes
+ * keep an fp16 copy of their sequences' planes in it. */
 size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0);
 
-/* fp32 queries and caches with an fp32 plane are computed in fp32. Otherwise
- * the products run on the tensor cores in fp16 with fp32 sums: queries as
- * fp16 (bf16 ones scaled by a power of two first, which is undone), weights
- * as fp16, statistics in fp32. Host errors: INVALID_ARG, UNSUPPORTED (type,
- * group), WORKSPACE. Device errors (tria_device_status on ws):
- * TRIA_ERR_DEVICE_ARG when n_live is outside [0, capacity]; that sequence's
- * outputs are not written. */
+/* fp32 queries, caches with an fp32 plane and head_dims other than 64, 128 and
+ * 256 are computed in fp32. Otherwise the products run on the tensor cores in
+ * fp16 with fp32 sums: queries as fp16 (bf16 ones scaled by a power of two
+ * first, which is undone), weights as fp16, statistics in fp32. Codes of
+ * quantised planes are exact and their scales fp32 factors, but prompts (as
+ * above) take code x scale rounded to fp16 once, for the output and for lse;
+ * values beyond fp16's range overflow there. Host errors: INVALID_ARG,
+ * UNSUPPORTED (type, group, 2^31 or more tokens x query heads, prompts over
+ * planes of 2^31 or more rows), WORKSPACE. Device errors (tria_device_status
+ * on ws): TRIA_ERR_DEVICE_ARG when n_live is outside [0, capacity]; that
+ * sequence's outputs are not written. TRIA_ERR_TIMEOUT when a bounded wait of
+ * the prompt kernel gave up. */
 tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* attention, void* ws, size_t ws_bytes,
                         void* stream);
 

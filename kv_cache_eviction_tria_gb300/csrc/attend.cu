@@ -8,6 +8,15 @@
 // Positions ascend with the rows, so a token sees a prefix (the sink) and one
 // run of rows; only those are read.
 //
+// A sequence takes one of three kernels. Up to 16 columns (token x query head
+// of a KV head's group), as many as the small products have, are a decode step:
+// a stream over the rows, bound by memory (attend_step.cuh). More are a prompt:
+// products of 128-row tiles on the fifth-generation tensor cores
+// (attend_prompt.cu). 4 tokens x 4 heads take 214 us as a step and 240 us as a
+// prompt over 8 sequences of 32768 fp16 rows, 126 and 518 us over q4_0 rows
+// (which a prompt widens first), 52 and 88 us over one sequence, 25 us either
+// way over 777 rows.
+//
 // The fp32 kernel (k_attend_plain) takes fp32 queries or fp32 planes of the
 // cache, where results are held to fp32 accuracy, and head_dims that the
 // tensor-core kernels are not built for. A CTA handles a unit of up to 8
@@ -28,29 +37,50 @@ namespace tria {
 namespace {
 
 constexpr int kCols = 8;
-constexpr int kPlainWarps = 4;
+constexpr int kPlainWarps = 4, kRows = 4;   // rows of a warp at once: rows x columns = lanes
+static_assert(kRows * kCols == 32, "a logit per lane");
 
-// value e of row `row` of a plane, as fp32
-__device__ __forceinline__ float plane_value(const uint8_t* data, const uint8_t* scale, int type, int64_t row, int hd, int e) {
-  switch (type) {
-    case TRIA_F32: return reinterpret_cast<const float*>(data)[row * hd + e];
-    case TRIA_F16: return __half2float(reinterpret_cast<const __half*>(data)[row * hd + e]);
-    case TRIA_Q8_0:
-      return (float)reinterpret_cast<const int8_t*>(data)[row * hd + e] *
-             __half2float(reinterpret_cast<const __half*>(scale)[row * (hd / 32) + e / 32]);
+// Dim e (of 32-wide block j, this lane's) of rows base + off[r] of a plane, as
+// fp32; the rows' blocks of 32 dims are read by a warp at a time.
+template <int N>
+__device__ __forceinline__ void load_rows(const uint8_t* data, const uint8_t* scale, int type, int64_t base, const int* off, int lane,
+                                          float (*x)[N]) {
+  constexpr int hd = 32 * N;
+  if (type == TRIA_F32) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[r][j] = __ldg(reinterpret_cast<const float*>(data) + (base + off[r]) * hd + 32 * j + lane);
+  } else if (type == TRIA_F16) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        x[r][j] = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(data) + (base + off[r]) * hd + 32 * j + lane)));
+  } else {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float d = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(scale) + (base + off[r]) * N + j)));
+        int c;
+        if (type == TRIA_Q8_0) {
+          c = __ldg(reinterpret_cast<const int8_t*>(data) + (base + off[r]) * hd + 32 * j + lane);
+        } else {
+          const int b = __ldg(data + (base + off[r]) * (hd / 2) + 16 * j + (lane & 15));
+          c = (lane < 16 ? b & 15 : b >> 4) - 8;
+        }
+        x[r][j] = (float)c * d;
+      }
   }
-  const int b = data[row * (hd / 2) + (e / 32) * 16 + (e & 15)];
-  const int c = (e & 16) ? b >> 4 : b & 15;
-  return (float)(c - 8) * __half2float(reinterpret_cast<const __half*>(scale)[row * (hd / 32) + e / 32]);
 }
 
+template <int N>
 __global__ void __launch_bounds__(kPlainWarps * 32) k_attend_plain(const __grid_constant__ AttendArgs A) {
-  extern __shared__ float smem[];
-  const int hd = A.hd, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ts = hd + 1;
-  float* s_q = smem;                                           // [kCols][hd]
-  float* s_p = s_q + kCols * hd + warp * kCols * 32;           // [kCols][32] of this warp
-  float* s_tile = s_q + kCols * hd + kPlainWarps * kCols * 32 + warp * 32 * ts;   // [32][hd + 1]
+  constexpr int hd = 32 * N;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float s_o[kCols * hd];
+  __shared__ __align__(16) float s_w[kPlainWarps][32];
   __shared__ float s_m[kPlainWarps][kCols], s_l[kPlainWarps][kCols];
   __shared__ int s_last;
 
@@ -70,105 +100,117 @@ __global__ void __launch_bounds__(kPlainWarps * 32) k_attend_plain(const __grid_
   }
   const int64_t row0 = S.row0 + (int64_t)g * S.cap;
   const int32_t* rpos = A.cpos + row0;
-  int pcol[kCols];
   int pmin = INT32_MAX, pmax = INT32_MIN;
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    pcol[c] = c < ncol ? A.pos[S.tok0 + (c0 + c) / A.G] : INT32_MIN;
+  for (int c = 0; c < kCols; ++c)
     if (c < ncol) {
-      pmin = min(pmin, pcol[c]);
-      pmax = max(pmax, pcol[c]);
+      const int p = A.pos[S.tok0 + (c0 + c) / A.G];
+      pmin = min(pmin, p);
+      pmax = max(pmax, p);
     }
-  }
   const int hi = rows_upto(rpos, n, pmax);
   const int lo = A.window > 0 ? rows_upto(rpos, hi, (int64_t)pmin - A.window) : 0;
   const int sr = min(A.sink, lo);
   const int R = sr + hi - lo;
   const int v0 = (int)((int64_t)part * R / A.split), v1 = (int)((int64_t)(part + 1) * R / A.split);
 
-  for (int i = threadIdx.x; i < kCols * hd; i += blockDim.x) {
-    const int c = i / hd, e = i - c * hd;
-    float x = 0.f;
-    if (c < ncol) {
-      const int col = c0 + c;
-      x = act_load(A.q, A.type, (int64_t)(S.tok0 + col / A.G) * A.q_stride + (int64_t)(g * A.G + col % A.G) * hd + e) * A.scale;
-    }
-    s_q[i] = x;
-  }
-  __syncthreads();
-
-  float m[kCols], l[kCols], o[kCols][8];
+  float q[kCols][N], o[kCols][N];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) {
-    m[c] = -INFINITY;
-    l[c] = 0.f;
+    const int col = c0 + min(c, ncol - 1);
+    const int64_t at = (int64_t)(S.tok0 + col / A.G) * A.q_stride + (int64_t)(g * A.G + col % A.G) * hd + lane;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[c][j] = 0.f;
+    for (int j = 0; j < N; ++j) {
+      q[c][j] = act_load(A.q, A.type, at + 32 * j) * A.scale;
+      o[c][j] = 0.f;
+    }
   }
-  for (int v = v0 + warp * 32; v < v1; v += kPlainWarps * 32) {
-    const int rows = min(32, v1 - v);
-    auto row_of = [&](int i) { return i < sr ? i : lo + i - sr; };
-    for (int r = 0; r < rows; ++r)
-      for (int e = lane; e < hd; e += 32) s_tile[r * ts + e] = plane_value(A.k, A.ks, A.k_type, row0 + row_of(v + r), hd, e);
-    __syncwarp();
-    float x[kCols];
+  // this lane's logit of a batch: row lane / 8, column lane % 8 (columns past
+  // the last one repeat it, and are not written)
+  const int my_p = A.pos[S.tok0 + (c0 + min(lane & 7, ncol - 1)) / A.G];
+  float M = -INFINITY, l = 0.f;
+  auto row_of = [&](int v) { return v < sr ? v : lo + v - sr; };
+  auto rows_at = [&](int v, int* off) {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) x[c] = 0.f;
-    const float* kr = s_tile + min(lane, rows - 1) * ts;
-    for (int e = 0; e < hd; ++e) {
-      const float kv = kr[e];
+    for (int r = 0; r < kRows; ++r) off[r] = row_of(min(v + r, v1 - 1));
+  };
+  float k[kRows][N];
+  int off[kRows], v = v0 + warp * kRows;
+  if (v < v1) {
+    rows_at(v, off);
+    load_rows<N>(A.k, A.ks, A.k_type, row0, off, lane, k);
+  }
+  for (; v < v1; v += kPlainWarps * kRows) {
+    const int my = row_of(min(v + (lane >> 3), v1 - 1)), p = rpos[my];
+    float x[kRows][N];
+    load_rows<N>(A.v, A.vs, A.v_type, row0, off, lane, x);
+    // products of this lane's dims, then their sums: a lane ends with the one of its number
+    float s[kRows * kCols];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) x[c] = fmaf(s_q[c * hd + e], kv, x[c]);
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        s[r * kCols + c] = q[c][0] * k[r][0];
+#pragma unroll
+        for (int j = 1; j < N; ++j) s[r * kCols + c] = fmaf(q[c][j], k[r][j], s[r * kCols + c]);
+      }
+    if (v + kPlainWarps * kRows < v1) {                    // the next keys are on their way meanwhile
+      rows_at(v + kPlainWarps * kRows, off);
+      load_rows<N>(A.k, A.ks, A.k_type, row0, off, lane, k);
     }
-    const int my = row_of(v + min(lane, rows - 1));
-    const int p = rpos[my];
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      const bool see = lane < rows && p <= pcol[c] && (A.window <= 0 || (int64_t)pcol[c] - p < A.window || my < A.sink);
-      float xc = see ? x[c] : -INFINITY, top = xc;
+    for (int w = 16; w >= 1; w >>= 1) {
+      const bool up = (lane & w) != 0;
 #pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      const float mn = fmaxf(m[c], top);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float a = expf(m[c] - base), w = see ? expf(xc - base) : 0.f;
-      m[c] = mn;
-      float sum = w;
-#pragma unroll
-      for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-      l[c] = l[c] * a + sum;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[c][j] *= a;
-      s_p[c * 32 + lane] = w;
-    }
-    __syncwarp();
-    for (int r = 0; r < rows; ++r)
-      for (int e = lane; e < hd; e += 32) s_tile[r * ts + e] = plane_value(A.v, A.vs, A.v_type, row0 + row_of(v + r), hd, e);
-    __syncwarp();
-    for (int r = 0; r < rows; ++r) {
-      float w[kCols];
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) w[c] = s_p[c * 32 + r];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j * 32 >= hd) break;
-        const float x2 = s_tile[r * ts + j * 32 + lane];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)   // a hidden row's values never count, whatever they are
-          if (w[c] != 0.f) o[c][j] = fmaf(w[c], x2, o[c][j]);
+      for (int i = 0; i < w; ++i) {
+        const float give = up ? s[i] : s[i + w], keep = up ? s[i + w] : s[i];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
       }
     }
+    const bool see = v + (lane >> 3) < v1 && p <= my_p && (A.window <= 0 || (int64_t)my_p - p < A.window || my < A.sink);
+    const float xc = see ? s[0] : -INFINITY;
+    float top = fmaxf(xc, __shfl_xor_sync(0xffffffffu, xc, 8));
+    top = fmaxf(M, fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)));
+    const float base = top == -INFINITY ? 0.f : top;
+    if (__any_sync(0xffffffffu, top > M)) {
+      const float a = expf(M - base);
+      l *= a;
+      M = top;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const float ac = __shfl_sync(0xffffffffu, a, c);
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[c][j] *= ac;
+      }
+    }
+    const float w = see ? expf(xc - base) : 0.f;
+    l += w;
+    s_w[warp][lane] = w;
+    const bool all = __all_sync(0xffffffffu, see);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 w4 = *reinterpret_cast<const float4*>(&s_w[warp][r * kCols + 4 * h]);
+        const float wc[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (all || wc[c] != 0.f) {                       // a hidden row's values never count, whatever they are
+#pragma unroll
+            for (int j = 0; j < N; ++j) o[4 * h + c][j] = fmaf(wc[c], x[r][j], o[4 * h + c][j]);
+          }
+      }
     __syncwarp();
   }
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
   // the warps' results, merged in warp order
-  if (lane == 0) {
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      s_m[warp][c] = m[c];
-      s_l[warp][c] = l[c];
-    }
+  if (lane < kCols) {
+    s_m[warp][lane] = M;
+    s_l[warp][lane] = l;
   }
   __syncthreads();
-  float* s_o = smem + kCols * hd + kPlainWarps * kCols * 32;   // [kCols][hd]
   float mt[kCols], lt[kCols];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) {
@@ -184,13 +226,12 @@ __global__ void __launch_bounds__(kPlainWarps * 32) k_attend_plain(const __grid_
     if (warp == w) {
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const float a = expf(m[c] - (mt[c] == -INFINITY ? 0.f : mt[c]));
+        const float a = expf(s_m[w][c] - (mt[c] == -INFINITY ? 0.f : mt[c]));
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j * 32 < hd) {
-            float* d = s_o + c * hd + j * 32 + lane;
-            *d = (w ? *d : 0.f) + o[c][j] * a;
-          }
+        for (int j = 0; j < N; ++j) {
+          float* d = s_o + c * hd + j * 32 + lane;
+          *d = (w ? *d : 0.f) + o[c][j] * a;
+        }
       }
     }
     __syncthreads();
@@ -291,7 +332,7 @@ __global__ void __launch_bounds__(128) k_attend_span(const __grid_constant__ Att
 // Parts of a unit: enough CTAs for the GPU, none under 128 rows of the
 // capacity.
 int plain_split(int64_t units, int cap_max) {
-  const int64_t want = (2 * 152 + units - 1) / std::max<int64_t>(units, 1);
+  const int64_t want = (3 * 152 + units - 1) / std::max<int64_t>(units, 1);
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)(cap_max + 127) / 128, 64}));
 }
 
@@ -300,10 +341,10 @@ int plain_split(int64_t units, int cap_max) {
 cudaError_t launch_attend_plain(const AttendArgs& A, cudaStream_t st) {
   const int64_t grid = (int64_t)A.units * A.n_kv * A.split;
   if (grid == 0) return cudaSuccess;
-  const int smem = (kCols * A.hd + kPlainWarps * kCols * 32 + kPlainWarps * 32 * (A.hd + 1)) * (int)sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(k_attend_plain, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  k_attend_plain<<<(unsigned)grid, kPlainWarps * 32, smem, st>>>(A);
+  using Fn = void (*)(AttendArgs);
+  static constexpr Fn fn[TRIA_MAX_HEAD_DIM / 32] = {k_attend_plain<1>, k_attend_plain<2>, k_attend_plain<3>, k_attend_plain<4>,
+                                                    k_attend_plain<5>, k_attend_plain<6>, k_attend_plain<7>, k_attend_plain<8>};
+  fn[A.hd / 32 - 1]<<<(unsigned)grid, kPlainWarps * 32, 0, st>>>(A);
   return cudaGetLastError();
 }
 
@@ -349,7 +390,7 @@ int sm_count() {
 // queries. The counters, which have to be zero between calls, take the same
 // place for every shape, so that a workspace may serve calls of different
 // shapes: a decode step counts segments (at most kMaxSegments), the others
-// units that are split (fewer than two per SM).
+// units that are split (fewer than three per SM).
 struct AttendLayout {
   size_t count, span, part, wide_k, wide_v, total;
   int units, split, prompt_split, sms;

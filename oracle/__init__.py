@@ -14,8 +14,9 @@ closed-form computation, an identity the pages rely on, or a value the pages
 print - the pass in ``tests/test_oracle_pins.py``, the decode-loop schedule in
 ``tests/test_lifecycle.py``, the shared-slot combine in
 ``tests/test_shared_oracle.py`` (by its reduction to the per-segment pass and
-the max identity; the combine rule itself is a reading, the pages state none)
-- except the reading of the future-offset set D (the pages do not state D; it
+the max identity; the combine rule itself is a reading, the pages state none),
+rotation, row formats and attention (:mod:`oracle.attend_oracle`) in
+``tests/test_rows_host.py`` - except the reading of the future-offset set D (the pages do not state D; it
 is a load-time parameter and both sides take the same D), which is a
 documented reading rather than a pinned value.
 """
