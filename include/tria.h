@@ -704,9 +704,10 @@ typedef struct tria_attention {
  * keep an fp16 copy of their sequences' planes in it. */
 size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0);
 
-/* fp32 queries, caches with an fp32 plane and head_dims other than 64, 128 and
- * 256 are computed in fp32. Otherwise the products run on the tensor cores in
- * fp16 with fp32 sums: queries as fp16 (bf16 ones scaled by a power of two
+/* fp32 queries, caches with an fp32 plane, head_dim 32 and, for up to 16 tokens
+ * x query heads per KV head in a sequence, head_dims 160, 192 and 224 are
+ * computed in fp32. Otherwise the products run on the tensor cores in fp16
+ * with fp32 sums: queries as fp16 (bf16 ones scaled by a power of two
  * first, which is undone), weights as fp16, statistics in fp32. Codes of
  * quantised planes are exact and their scales fp32 factors, but prompts (as
  * above) take code x scale rounded to fp16 once, for the output and for lse;

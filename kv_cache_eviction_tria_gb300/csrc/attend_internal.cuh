@@ -77,8 +77,9 @@ cudaError_t launch_attend_step_q8_q4(const AttendArgs& A, int cols, int workers,
 cudaError_t launch_attend_step_q4_f16(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 cudaError_t launch_attend_step_q4_q8(const AttendArgs& A, int cols, int workers, cudaStream_t st);
 cudaError_t launch_attend_step_q4_q4(const AttendArgs& A, int cols, int workers, cudaStream_t st);
-// attend_prompt.cu: units of prompt_cols(hd) columns
-inline int prompt_cols(int hd) { return hd == 256 ? 128 : 256; }
+// attend_prompt.cu: tiles of prompt_dims(hd) dims, units of prompt_cols(hd) columns
+inline int prompt_dims(int hd) { return hd <= 64 ? 64 : (hd <= 128 ? 128 : 256); }
+inline int prompt_cols(int hd) { return hd > 128 ? 128 : 256; }
 cudaError_t launch_attend_prompt(const AttendArgs& A, cudaStream_t st);
 
 __device__ __forceinline__ float act_load(const void* p, int type, int64_t i) {

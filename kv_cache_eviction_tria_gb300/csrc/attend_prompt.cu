@@ -12,6 +12,9 @@
 // of key and value tiles filled; one thread that issues the products. What
 // bounds it is the tensor cores' rate together with one exponential per score.
 //
+// Heads of other sizes take the next larger kernel: a tile's dims past the
+// plane's last one arrive as zeros.
+//
 // A thread owns a row of S: maximum and sum need no shuffles. The reference M
 // moves only when a row's maximum has grown by more than 2^8 (kLazy), since
 // until then P stays inside fp16 (it is kept 2^-kShift below its limit) and
@@ -269,14 +272,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
   const int tl = on ? col / A.G : tok_a;
   const int64_t tok = S.tok0 + tl;
   const int head = g * A.G + (on ? col - tl * A.G : 0);
-  const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(A.q) + tok * A.q_stride + (int64_t)head * HD);
+  const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(A.q) + tok * A.q_stride + (int64_t)head * A.hd);
+  auto piece = [&](int c) { return on && 8 * c < A.hd ? src[c] : make_uint4(0, 0, 0, 0); };
   constexpr int kPart = HD / 8 < 16 ? HD / 8 : 16;         // 16-byte pieces held at once
   uint4 v[kPart];
   int pl = INT32_MAX, ph = INT32_MIN, before = 0, after = 0;
   const int h = n - (S.t - 1 - tok_b);
   if (wg < QT) {
 #pragma unroll
-    for (int c = 0; c < kPart; ++c) v[c] = on ? src[c] : make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < kPart; ++c) v[c] = piece(c);
   } else if (wg == 2) {
     if (h > 0) before = rpos[h - 1];
     if (h >= 0 && h < n) after = rpos[h];
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       for (int c0q = 0; c0q < HD / 8; c0q += kPart) {
 #pragma unroll
         for (int c = 0; c < kPart; ++c)
-          if (c0q > 0) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
+          if (c0q > 0) v[c] = piece(c0q + c);
 #pragma unroll
         for (int c = 0; c < kPart; ++c) {
           const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     for (int c0q = 0; c0q < HD / 8; c0q += kPart) {
 #pragma unroll
       for (int c = 0; c < kPart; ++c)
-        if (HD / 8 > kPart) v[c] = on ? src[c0q + c] : make_uint4(0, 0, 0, 0);
+        if (HD / 8 > kPart) v[c] = piece(c0q + c);
 #pragma unroll
       for (int c = 0; c < kPart; ++c) {
         uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       }
       if (!split && on) {
         fence_proxy_async_smem();
-        bulk_s2g(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD, row_out, HD * 2);
+        bulk_s2g(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * A.hd, row_out, A.hd * 2);
         bulk_commit();
         bulk_wait_read_all();
       }
@@ -828,7 +832,7 @@ __global__ void __launch_bounds__(PromptShape<HD>::QT * 128) k_join_parts(const 
     for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(p[(2 + d0 + e) * kCols], f, v[e]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD + d0);
+  uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * A.hd + d0);
 #pragma unroll
   for (int q = 0; q < kJoinDims / 8; ++q) {
     uint32_t w[4];
@@ -939,14 +943,14 @@ cudaError_t launch_prompt_hd(const AttendArgs& A, cudaStream_t st) {
     rows = std::max(rows, A.seq[s].row0 + (int64_t)A.n_kv * A.seq[s].cap);
     wide = std::max(wide, A.seq[s].wide0 + (int64_t)A.n_kv * A.seq[s].cap);
   }
-  if (!plane_map_f16(&mk, A.wide_k ? (const void*)A.wide_k : A.k, HD, A.wide_k ? wide : rows, H::BN) ||
-      !plane_map_f16(&mv, A.wide_v ? (const void*)A.wide_v : A.v, HD, A.wide_v ? wide : rows, H::BN))
+  if (!plane_map_f16(&mk, A.wide_k ? (const void*)A.wide_k : A.k, A.hd, A.wide_k ? wide : rows, H::BN) ||
+      !plane_map_f16(&mv, A.wide_v ? (const void*)A.wide_v : A.v, A.hd, A.wide_v ? wide : rows, H::BN))
     return cudaErrorInvalidValue;
   kern<<<(unsigned)grid, kPromptThreads, H::kSmem, st>>>(A, mk, mv);
   if (A.split > 1) {
     const cudaError_t e3 = cudaGetLastError();
     if (e3 != cudaSuccess) return e3;
-    k_join_parts<HD><<<dim3((unsigned)(A.units * A.n_kv), HD / kJoinDims), H::QT * 128, 0, st>>>(A);
+    k_join_parts<HD><<<dim3((unsigned)(A.units * A.n_kv), A.hd / kJoinDims), H::QT * 128, 0, st>>>(A);
   }
   return cudaGetLastError();
 }
@@ -963,7 +967,7 @@ cudaError_t launch_attend_prompt(const AttendArgs& A, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  switch (A.hd) {
+  switch (prompt_dims(A.hd)) {
     case 64: return launch_prompt_hd<64>(A, st);
     case 128: return launch_prompt_hd<128>(A, st);
     case 256: return launch_prompt_hd<256>(A, st);

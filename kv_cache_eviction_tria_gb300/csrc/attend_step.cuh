@@ -103,6 +103,15 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
 // Block scales of two neighbouring rows (NB halves each, side by side).
 template <int NB>
 __device__ __forceinline__ void load_scales(const uint8_t* p, float* a, float* b) {
+  if constexpr (NB == 3) {                                 // (not a vector's size)
+    const __half* x = reinterpret_cast<const __half*>(p);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      a[i] = __half2float(x[i]);
+      b[i] = __half2float(x[NB + i]);
+    }
+    return;
+  }
   __half2 h[NB];
   if constexpr (NB == 2) {
     *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(p);
@@ -275,7 +284,11 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
     auto copy_scales = [&](uint8_t* dst, const uint8_t* src) {
       if constexpr (H::scRb == 16) cp_async16(dst, src);
       else if constexpr (H::scRb == 8) cp_async8(dst, src);
-      else cp_async4(dst, src);
+      else if constexpr (H::scRb == 4) cp_async4(dst, src);
+      else                                                 // six bytes: no asynchronous copy's size
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          reinterpret_cast<uint16_t*>(dst)[i] = __ldg(reinterpret_cast<const uint16_t*>(src) + i);
     };
     if (lane < rows) {
       if constexpr (H::kKq) copy_scales(d + H::oKs + lane * H::scRb, A.ks + (p_row0 + r + lane) * H::scRb);
@@ -471,20 +484,23 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       if constexpr (H::kVq) {
         float big = 0.f;
         const __half2* vss = reinterpret_cast<const __half2*>(tile_p + H::oVs);
-        // all scales of the tile, spread over the lanes: TR * NB / 2 pairs
+        // all scales of the tile, spread over the lanes: TR * NB / 2 pairs (with an
+        // odd number of blocks, some pairs belong to two rows)
 #pragma unroll
         for (int i = 0; i < (TR * NB / 2 + 31) / 32; ++i) {
           const int x = i * 32 + lane;
-          bool on = x < TR * NB / 2;
+          bool on = x < TR * NB / 2, on2 = on;
           if constexpr (kMasked) {                         // rows that some token sees
-            const int row = 2 * x / NB;
-            on = on && row < rows &&
-                 tp[row] <= pmax && (A.window <= 0 || (int64_t)pmin - tp[row] < A.window || r + row < A.sink);
+            auto some = [&](int row) {
+              return row < rows && tp[row] <= pmax && (A.window <= 0 || (int64_t)pmin - tp[row] < A.window || r + row < A.sink);
+            };
+            on = on && some(2 * x / NB);
+            on2 = NB % 2 == 0 ? on : on2 && some((2 * x + 1) / NB);
           }
-          if (on) {
+          if (on || on2) {
             const float2 f = __half22float2(__habs2(vss[x]));
-            if (f.x <= 65504.f) big = fmaxf(big, f.x);
-            if (f.y <= 65504.f) big = fmaxf(big, f.y);
+            if (on && f.x <= 65504.f) big = fmaxf(big, f.x);
+            if (on2 && f.y <= 65504.f) big = fmaxf(big, f.y);
           }
         }
         // the exponent above the largest one (its bits order like integers)
@@ -865,6 +881,7 @@ cudaError_t launch_attend_step_kv(const AttendArgs& A, int cols, int workers, cu
   const bool one = cols <= 8;
   switch (A.hd) {
     case 64: return one ? launch_attend_step_t<KT, VT, 64, 1>(A, workers, st) : launch_attend_step_t<KT, VT, 64, 2>(A, workers, st);
+    case 96: return one ? launch_attend_step_t<KT, VT, 96, 1>(A, workers, st) : launch_attend_step_t<KT, VT, 96, 2>(A, workers, st);
     case 128: return one ? launch_attend_step_t<KT, VT, 128, 1>(A, workers, st) : launch_attend_step_t<KT, VT, 128, 2>(A, workers, st);
     case 256: return one ? launch_attend_step_t<KT, VT, 256, 1>(A, workers, st) : launch_attend_step_t<KT, VT, 256, 2>(A, workers, st);
   }

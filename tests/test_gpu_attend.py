@@ -279,3 +279,28 @@ def test_logits_near_zero(lib, kind, tokens, scale):
     """A factor that vanishes in fp32 leaves equal weights; hidden rows stay hidden."""
     c = R.Cache(lib, np.random.default_rng(3), rows=[70, 300], cap=[80, 300], n_kv=2, hd=128, k_type="f16", v_type="f16")
     run(lib, c, 8, kind, [tokens, tokens], scale=scale, back=30)
+
+
+@pytest.mark.parametrize("hd", [96, 160, 192, 224])
+@pytest.mark.parametrize("kind,k,v", [("f16", "f16", "f16"), ("bf16", "q8_0", "q4_0"), ("f16", "q4_0", "q8_0")])
+@pytest.mark.parametrize("tokens,rows,window", [([50, 3], [120, 700], 0), ([130, 1], [2100, 40], 0), ([40, 2], [300, 90], 65)])
+def test_head_dims_between_the_kernels(lib, kind, k, v, hd, tokens, rows, window):
+    """Prompts whose heads are padded to the next tile, next to decode steps of the same call."""
+    c = R.Cache(lib, np.random.default_rng(17), rows=rows, cap=[r + 9 for r in rows], n_kv=2, hd=hd, k_type=k, v_type=v)
+    run(lib, c, 8, kind, tokens, window=window, sink=3 if window else 0, seed=hd, back=2)
+
+
+@pytest.mark.parametrize("k,v", [("q8_0", "q8_0"), ("q4_0", "q4_0"), ("f16", "q4_0"), ("q4_0", "f16")])
+@pytest.mark.parametrize("tokens", [1, 4])
+def test_scales_of_three_blocks(lib, k, v, tokens):
+    """head_dim 96: a pair of value scales may belong to two rows, of which a token sees one; hidden scales are huge."""
+    rng = np.random.default_rng(23)
+    c = R.Cache(lib, rng, rows=[77, 16, 1], cap=[80, 16, 4], n_kv=2, hd=96, k_type=k, v_type=v)
+    if c.h["v_scale"] is not None:
+        for s in range(3):                                      # rows that no token sees (back = 5 positions)
+            for g in range(2):
+                r0, n = c.row0[s] + g * c.cap[s], c.rows[s]
+                late = np.flatnonzero(c.h["pos"][r0:r0 + n] > c.last(s) - 5)
+                c.h["v_scale"][r0 + late] = 60000.0
+        c.d["v_scale"].copy_(torch.from_numpy(c.h["v_scale"]))
+    run(lib, c, 8, "f16", [tokens] * 3, back=5)
