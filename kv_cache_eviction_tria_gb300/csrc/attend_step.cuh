@@ -27,6 +27,14 @@
 // warp; parts of a unit go to the workspace and are merged in order, those of
 // a CTA's warps when all have finished, those of several CTAs by the last one
 // to arrive.
+//
+// fp16 rows are bound by memory: 8 sequences, 206246 rows of 8 KV heads x 128
+// dims, 4 query heads each, 150 us (5.6 TB/s); 534879 rows of 4 heads x 256
+// dims 372 us (5.9 TB/s). 4-bit rows are bound by the instructions that turn
+// codes into fragments (about 900 a tile of 32 rows, at 0.6 of the issue
+// slots): 412488 rows 142 us, 3.35 TB/s, 2.9 rows per ns against 1.4 of fp16.
+// Codes used as subnormals, with the offsets in the sums, are fewer
+// instructions but took 185 us: the products wait on one another.
 #pragma once
 
 #include <type_traits>

@@ -15,13 +15,21 @@
 // a head and a warp takes 32 / (lanes per head, rounded up to a power of two)
 // heads at once, so that both members of a pair sit in one lane and the norm
 // is a shuffle reduction. A warp keeps its lanes' sines and cosines over the
-// heads of a token that it handles: they cost about as much as a head. Heads come through shared memory, up to a token's at once: with
-// loads into registers the bytes in flight (16 KB an SM) held the kernel at
-// 2.9 TB/s.
+// heads of a token that it handles: they cost about as much as a group. Heads
+// come through shared memory: with loads into registers the bytes in flight
+// (16 KB an SM) held the kernel at 2.9 TB/s. Warps take equal, contiguous shares
+// of all tokens' groups of heads (whole tokens dealt out in turn left many idle
+// at the end), and while a warp rotates, the next heads are on their way into
+// its second stage: 8191 tokens of 40 heads x 128 bf16 values take 39.4 us (4.3
+// TB/s; 46.8 with one stage and tokens in turn). With the cache's formats behind
+// them, one stage of twice the size is better: 22487 tokens' queries, keys and
+// values (32 + 8 + 8 heads; q8_0 keys, q4_0 values) take 156.5 us (3.8 TB/s), 171
+// with two stages, whose smaller pieces cost more instructions than they hide.
 // Keys on their way into the cache go through shared memory once more, because
 // their quantisation blocks (32 consecutive dims) do not line up with the
-// pairs. The kernels are bound by memory for prompts and by launch latency for
-// single tokens.
+// pairs. Prompts are bound by the instructions of 16 warps a SM (half of the
+// issue slots; with 20 to 24 warps and fewer registers each they were slower),
+// single tokens by latency (4 to 6 us a call).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
