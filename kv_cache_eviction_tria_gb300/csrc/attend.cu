@@ -402,7 +402,7 @@ int sm_count() {
 // shapes: a decode step counts segments (at most kMaxSegments), the others
 // units that are split (fewer than three per SM).
 struct AttendLayout {
-  size_t count, span, part, wide_k, wide_v, total;
+  size_t count, span, part, wide_k, wide_kl, wide_v, total;
   int units, split, prompt_split, sms;
 };
 
@@ -454,7 +454,9 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   L.wide_k = up256(L.part + sizeof(float) * std::max(std::max(plain, step), prompt));
   const size_t plane = up256((size_t)wide * c->head_dim * 2);
   const bool tensor = tensor_types(c, TRIA_F16);
-  L.wide_v = L.wide_k + (tensor && c->k_type != TRIA_F16 ? plane : 0);
+  const size_t keys = tensor && c->k_type != TRIA_F16 ? plane : 0;
+  L.wide_kl = L.wide_k + keys;
+  L.wide_v = L.wide_kl + keys;
   L.total = L.wide_v + (tensor && c->v_type != TRIA_F16 ? plane : 0);
   return L;
 }
@@ -581,7 +583,10 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   if (prompt) {
     take(kPathPrompt);
     A.split = L.prompt_split;
-    if (cache->k_type != TRIA_F16) A.wide_k = (uint16_t*)((uint8_t*)ws + L.wide_k);
+    if (cache->k_type != TRIA_F16) {
+      A.wide_k = (uint16_t*)((uint8_t*)ws + L.wide_k);
+      A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);
+    }
     if (cache->v_type != TRIA_F16) A.wide_v = (uint16_t*)((uint8_t*)ws + L.wide_v);
     if (launch_attend_prompt(A, st) != cudaSuccess) return TRIA_ERR_CUDA;
   }

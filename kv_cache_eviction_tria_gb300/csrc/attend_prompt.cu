@@ -27,8 +27,10 @@
 // rare this way.
 //
 // Tiles come by TMA into 128-byte-swizzled shared memory, so the planes are
-// fp16: 8- and 4-bit rows are rounded to fp16 once (code x scale) into the
-// workspace first (k_widen), 128 rows of them being read again by every 256
+// fp16: 8- and 4-bit rows go into the workspace as fp16 (code x scale) first
+// (k_widen), values rounded once, keys as the rounded value and the remainder,
+// which takes a product of its own (kLow): logits, and the log-sum-exp that is
+// given out in fp32, then carry no rounding of the keys. 128 rows of them being read again by every 256
 // columns. Converting them tile by tile on their way into shared memory, which
 // the products' operands already fill to its rate, held a pair of tiles at 2.3
 // (q4_0) and 3.2 us (q8_0) instead of 1.7.
@@ -222,11 +224,14 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, int rows, uint32_t* ma
   }
 }
 
-template <int HD>
+template <int HD, bool kLow>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __grid_constant__ AttendArgs A,
                                                                      const __grid_constant__ CUtensorMap map_k,
+                                                                     const __grid_constant__ CUtensorMap map_kl,
                                                                      const __grid_constant__ CUtensorMap map_v) {
   using H = PromptShape<HD>;
+  // ring entries of tile i: keys P i, their remainders P i + 1 (kLow), values P i + P - 1
+  constexpr int P = kLow ? 3 : 2;
   constexpr int QT = H::QT, BN = H::BN, NB = H::NB, ST = H::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
@@ -455,13 +460,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t dq = tile_desc(smem_u32(smem + H::oQ), 16), dk = tile_desc(smem_u32(smem + H::oRing), 16),
                      dv = tile_desc(smem_u32(smem + H::oRing), BN * 128);
-      auto scores = [&](int q, int i, int st) {            // address fields count 16 bytes
+      auto scores = [&](int q, int i, int st, int sl) {    // address fields count 16 bytes
         const uint64_t a = dq + (uint64_t)(q * (H::kQ / 16)), b = dk + (uint64_t)(st * (H::kStage / 16));
         const uint32_t d = tm + H::cS(q, i % NB);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
           tc_mma_ss(d, a + (uint64_t)((k >> 2) * (128 * 8) + (k & 3) * 2), b + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2),
                     mma_desc(BN, false), k > 0);
+        if constexpr (kLow) {
+          const uint64_t bl = dk + (uint64_t)(sl * (H::kStage / 16));
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k)
+            tc_mma_ss(d, a + (uint64_t)((k >> 2) * (128 * 8) + (k & 3) * 2), bl + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2),
+                      mma_desc(BN, false), 1);
+        }
         tc_commit(&b_s[NB * q + i % NB]);
       };
       auto sums = [&](int q, int i, int st) {
@@ -471,26 +483,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         for (int k = 0; k < BN / 16; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), i > 0 || k > 0);
         tc_commit(&b_o[q]);
       };
-      bool ok = wait_all(b_q, 0) && wait_all(&b_full[0], 0);
+      bool ok = wait_all(b_q, 0) && wait_all(&b_full[0], 0) && (!kLow || wait_all(&b_full[1], 0));
       tc_fence_after();
       if (ok && elect_one()) {
 #pragma unroll
-        for (int q = 0; q < QT; ++q) scores(q, 0, 0);
+        for (int q = 0; q < QT; ++q) scores(q, 0, 0, 1);
         tc_commit(&b_empty[0]);
+        if (kLow) tc_commit(&b_empty[1]);
       }
       __syncwarp();
-      int sv = 1 % ST, sk = 2 % ST, pv = 0, pk = 2 / ST & 1;   // ring stage and parity of V(i), K(i + 1)
+      int sv = P - 1, sk = P, pv = 0, pk = 0;              // ring stage and parity of V(i), K(i + 1)
+      static_assert(P + 1 < ST, "the first ones lie in the ring's first round");
       for (int i = 0; ok && i < nt; ++i) {
         const bool more = i + 1 < nt;
-        if (more) ok = wait_all(&b_full[sk], pk);
+        const int sl = sk + 1 == ST ? 0 : sk + 1, pl2 = sk + 1 == ST ? pk ^ 1 : pk;   // of the remainders of K(i + 1)
+        if (more) ok = wait_all(&b_full[sk], pk) && (!kLow || wait_all(&b_full[sl], pl2));
         if constexpr (NB == 2) {
           // the other buffer's weights are those of tile i - 1, whose sums were issued before
           if (more) {
             tc_fence_after();
             if (ok && elect_one()) {
 #pragma unroll
-              for (int q = 0; q < QT; ++q) scores(q, i + 1, sk);
+              for (int q = 0; q < QT; ++q) scores(q, i + 1, sk, sl);
               tc_commit(&b_empty[sk]);
+              if (kLow) tc_commit(&b_empty[sl]);
             }
             __syncwarp();
           }
@@ -503,24 +519,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
           if (ok && elect_one()) {
             sums(q, i, sv);
             // products run in the order of their issue: the scores overwrite weights that the sums have used
-            if (NB == 1 && more) scores(q, i + 1, sk);
+            if (NB == 1 && more) scores(q, i + 1, sk, sl);
           }
           __syncwarp();
         }
         if (ok && elect_one()) {
           tc_commit(&b_empty[sv]);
-          if (NB == 1 && more) tc_commit(&b_empty[sk]);
+          if (NB == 1 && more) {
+            tc_commit(&b_empty[sk]);
+            if (kLow) tc_commit(&b_empty[sl]);
+          }
           if (!more)
 #pragma unroll
             for (int q = 0; q < QT; ++q) tc_commit(&b_f[q]);
         }
         __syncwarp();
-        sv += 2;
+        sv += P;
         if (sv >= ST) {
           sv -= ST;
           pv ^= 1;
         }
-        sk += 2;
+        sk += P;
         if (sk >= ST) {
           sk -= ST;
           pk ^= 1;
@@ -532,7 +551,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       }
     }
   } else if (wg >= 2) {
-    // ---- key tiles (ring entries 2i) and value tiles (2i + 1)
+    // ---- key tiles and value tiles
     const int tid = threadIdx.x & 127;
     auto stage = [&](int e) { return smem + H::oRing + (e % ST) * H::kStage; };
     auto free_stage = [&](int e) {
@@ -542,10 +561,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     // threads meet at barriers), start no more copies, and wait, bounded, for
     // those still on their way
     auto go = [&] { return tid == 0 && !*s_abort; };
-    auto drain = [&](int first) {
+    auto drain = [&](bool values) {
       if (!*s_abort || tid != 0) return;
-      for (int e = first; e < 2 * nt; e += 2)
-        for (int it = 0; it < 1024 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
+      for (int e = max(0, P * nt - ST); e < P * nt; ++e)
+        for (int it = 0; it < 1024 && (e % P == P - 1) == values && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
         }
     };
     int rows;
@@ -553,11 +572,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       if (tid == 0) {
         for (int i = 0; i < nt; ++i) {
           // hidden keys, and those past the last row, only reach logits that the mask replaces
-          const int r = tile_row(i, rows), e = 2 * i;
+          const int r = tile_row(i, rows), e = P * i;
           free_stage(e);
           if (go()) copy_tile<HD, BN>(stage(e), &map_k, key0 + r, &b_full[e % ST]);
+          if constexpr (kLow) {
+            free_stage(e + 1);
+            if (go()) copy_tile<HD, BN>(stage(e + 1), &map_kl, key0 + r, &b_full[(e + 1) % ST]);
+          }
         }
-        drain(max(0, 2 * nt - ST) & ~1);
+        drain(false);
       }
     } else {
       constexpr int kPos = (BN + kLoadV - 1) / kLoadV;
@@ -575,7 +598,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       fetch_pos(0);
       int looked = 0;
       for (int i = 0; i < nt; ++i) {
-        const int r = tile_row(i, rows), e = 2 * i + 1;
+        const int r = tile_row(i, rows), e = P * i + P - 1;
         free_stage(e);
         // positions and marks go with the value tile, which stays until the weights are used
         const int32_t* tp = s_pos + (i % H::kPosTiles) * BN;
@@ -596,7 +619,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         asm volatile("bar.sync 3, %0;" ::"n"(kLoadV) : "memory");
         if (tid == 0) mbar_arrive(&b_full[e % ST]);
       }
-      drain(max(1, 2 * nt - ST) | 1);
+      drain(true);
     }
   } else if (wg < QT) {
     // ---- softmax: a thread per row
@@ -621,7 +644,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       int rows;
       const int r = tile_row(i, rows);
       bool masked = rows < BN;
-      const int ev = 2 * i + 1;
+      const int ev = P * i + P - 1;
       if (need_pos || masked) {
         ok = wait(&b_full[ev % ST], (ev / ST) & 1);        // positions and marks are there
         if (!ok) break;
@@ -855,16 +878,17 @@ constexpr int kWidenRows = 64;   // rows of a block
 // Rows of the prompt's sequences as fp16 (code x scale, rounded once), eight
 // values a thread; rows that no token sees are left out. Bound by the fp16
 // rows' way to memory.
-template <int T>
-__device__ __forceinline__ void widen_rows(const uint8_t* data, const uint8_t* scale, uint16_t* out, int64_t src, int64_t dst, int rows,
-                                           int hd) {
+template <int T, bool kLow>
+__device__ __forceinline__ void widen_rows(const uint8_t* data, const uint8_t* scale, uint16_t* out, uint16_t* low, int64_t src,
+                                           int64_t dst, int rows, int hd) {
   const int per = hd / 8;
 #pragma unroll 4
   for (int x = threadIdx.x; x < rows * per; x += blockDim.x) {
     const int r = x / per, c = x - r * per;
     const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(scale) + (src + r) * (hd / 32) + c / 4);
     const uint32_t sc = h | (h << 16);
-    uint32_t o[4];
+    uint32_t o[4], lo[4];
+    const float2 sf = make_float2(__half2float(__ushort_as_half((uint16_t)h)), __half2float(__ushort_as_half((uint16_t)h)));
     uint2 w;
     if constexpr (T == TRIA_Q8_0) {
       w = __ldg(reinterpret_cast<const uint2*>(data + (src + r) * hd + c * 8));
@@ -886,13 +910,21 @@ __device__ __forceinline__ void widen_rows(const uint8_t* data, const uint8_t* s
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(b[k]), "r"(bias));
+      const float2 code = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
       asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(o[k]), "r"(sc));
+      if constexpr (kLow) {
+        // code x scale fits fp32; what fp16 left of it (8 bits at most) fits fp16
+        const float2 x = __fmul2_rn(code, sf), hi = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+        const __half2 l = __floats2half2_rn(x.x - hi.x, x.y - hi.y);
+        lo[k] = *reinterpret_cast<const uint32_t*>(&l);
+      }
     }
+    if constexpr (kLow) *reinterpret_cast<uint4*>(low + (dst + r) * hd + c * 8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     *reinterpret_cast<uint4*>(out + (dst + r) * hd + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
-__global__ void __launch_bounds__(256) k_widen(const __grid_constant__ AttendArgs A, uint16_t* wide_k, uint16_t* wide_v) {
+__global__ void __launch_bounds__(256) k_widen(const __grid_constant__ AttendArgs A) {
   __shared__ int s_min;
   const int g = blockIdx.y;
   // blocks of a sequence follow those of the ones before it
@@ -920,18 +952,18 @@ __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ AttendArg
   }
   const int64_t src = S.row0 + seg0 + r0, dst = S.wide0 + seg0 + r0;
   if (blockIdx.z == 0) {
-    if (A.k_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0>(A.k, A.ks, wide_k, src, dst, rows, A.hd);
-    else if (A.k_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0>(A.k, A.ks, wide_k, src, dst, rows, A.hd);
+    if (A.k_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0, true>(A.k, A.ks, A.wide_k, A.wide_kl, src, dst, rows, A.hd);
+    else if (A.k_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0, true>(A.k, A.ks, A.wide_k, A.wide_kl, src, dst, rows, A.hd);
   } else {
-    if (A.v_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0>(A.v, A.vs, wide_v, src, dst, rows, A.hd);
-    else if (A.v_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0>(A.v, A.vs, wide_v, src, dst, rows, A.hd);
+    if (A.v_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0, false>(A.v, A.vs, A.wide_v, nullptr, src, dst, rows, A.hd);
+    else if (A.v_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0, false>(A.v, A.vs, A.wide_v, nullptr, src, dst, rows, A.hd);
   }
 }
 
-template <int HD>
+template <int HD, bool kLow>
 cudaError_t launch_prompt_hd(const AttendArgs& A, cudaStream_t st) {
   using H = PromptShape<HD>;
-  auto kern = k_attend_prompt<HD>;
+  auto kern = k_attend_prompt<HD, kLow>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, H::kSmem);
   if (e != cudaSuccess) return e;
   // the warpgroups' register shares are cut from what the block starts with
@@ -940,8 +972,9 @@ cudaError_t launch_prompt_hd(const AttendArgs& A, cudaStream_t st) {
   if (e2 != cudaSuccess) return e2;
   if (attr.numRegs != kPromptRegs) return cudaErrorInvalidConfiguration;
   const int64_t grid = (int64_t)A.units * A.n_kv * A.split;
-  CUtensorMap mk, mv;
+  CUtensorMap mk, ml, mv;
   memset(&mk, 0, sizeof(mk));
+  memset(&ml, 0, sizeof(ml));
   memset(&mv, 0, sizeof(mv));
   int64_t rows = 0, wide = 0;
   for (int s = 0; s < A.n_seqs; ++s) {
@@ -951,7 +984,8 @@ cudaError_t launch_prompt_hd(const AttendArgs& A, cudaStream_t st) {
   if (!plane_map_f16(&mk, A.wide_k ? (const void*)A.wide_k : A.k, A.hd, A.wide_k ? wide : rows, H::BN) ||
       !plane_map_f16(&mv, A.wide_v ? (const void*)A.wide_v : A.v, A.hd, A.wide_v ? wide : rows, H::BN))
     return cudaErrorInvalidValue;
-  kern<<<(unsigned)grid, kPromptThreads, H::kSmem, st>>>(A, mk, mv);
+  if (kLow && !plane_map_f16(&ml, A.wide_kl, A.hd, wide, H::BN)) return cudaErrorInvalidValue;
+  kern<<<(unsigned)grid, kPromptThreads, H::kSmem, st>>>(A, mk, ml, mv);
   if (A.split > 1) {
     const cudaError_t e3 = cudaGetLastError();
     if (e3 != cudaSuccess) return e3;
@@ -968,14 +1002,14 @@ cudaError_t launch_attend_prompt(const AttendArgs& A, cudaStream_t st) {
     for (int s = 0; s < A.n_seqs; ++s)
       if (A.seq[s].t > 0) blocks += (A.seq[s].cap + kWidenRows - 1) / kWidenRows;
     const dim3 grid((unsigned)blocks, A.n_kv, 2);
-    if (blocks > 0) k_widen<<<grid, 256, 0, st>>>(A, A.wide_k, A.wide_v);
+    if (blocks > 0) k_widen<<<grid, 256, 0, st>>>(A);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   switch (prompt_dims(A.hd)) {
-    case 64: return launch_prompt_hd<64>(A, st);
-    case 128: return launch_prompt_hd<128>(A, st);
-    case 256: return launch_prompt_hd<256>(A, st);
+    case 64: return A.wide_k ? launch_prompt_hd<64, true>(A, st) : launch_prompt_hd<64, false>(A, st);
+    case 128: return A.wide_k ? launch_prompt_hd<128, true>(A, st) : launch_prompt_hd<128, false>(A, st);
+    case 256: return A.wide_k ? launch_prompt_hd<256, true>(A, st) : launch_prompt_hd<256, false>(A, st);
   }
   return cudaErrorInvalidValue;
 }
