@@ -701,7 +701,7 @@ typedef struct tria_attention {
  * calls that overlap on the GPU, nor with the pass's workspace; one that is
  * large enough for each serves calls of different shapes. Prompts (more than
  * 16 tokens x query heads per KV head in a sequence) over q8_0 or q4_0 planes
- * keep an fp16 copy of their sequences' planes in it. */
+ * keep an fp16 copy of their sequences' planes in it, of keys two. */
 size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0);
 
 /* fp32 queries, caches with an fp32 plane, head_dim 32 and, for up to 16 tokens
@@ -710,8 +710,9 @@ size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_hea
  * with fp32 sums: queries as fp16 (bf16 ones scaled by a power of two
  * first, which is undone), weights as fp16, statistics in fp32. Codes of
  * quantised planes are exact and their scales fp32 factors, but prompts (as
- * above) take code x scale rounded to fp16 once, for the output and for lse;
- * values beyond fp16's range overflow there. Host errors: INVALID_ARG,
+ * above) take code x scale rounded to fp16 once, keys only when lse is NULL
+ * (with lse, logits carry no rounding of the keys); numbers beyond fp16's range
+ * overflow there. Host errors: INVALID_ARG,
  * UNSUPPORTED (type, group, 2^31 or more tokens x query heads, prompts over
  * planes of 2^31 or more rows), WORKSPACE. Device errors (tria_device_status
  * on ws): TRIA_ERR_DEVICE_ARG when n_live is outside [0, capacity]; that

@@ -585,7 +585,7 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
     A.split = L.prompt_split;
     if (cache->k_type != TRIA_F16) {
       A.wide_k = (uint16_t*)((uint8_t*)ws + L.wide_k);
-      A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);
+      if (a->lse) A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);
     }
     if (cache->v_type != TRIA_F16) A.wide_v = (uint16_t*)((uint8_t*)ws + L.wide_v);
     if (launch_attend_prompt(A, st) != cudaSuccess) return TRIA_ERR_CUDA;

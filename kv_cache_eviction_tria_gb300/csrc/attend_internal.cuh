@@ -53,7 +53,7 @@ struct AttendArgs {
   uint32_t* count;     // arrivals per unit, zero between calls
   float* part;         // partial results of split units
   uint16_t* wide_k;    // fp16 copies of quantised planes (prompts; NULL: none)
-  uint16_t* wide_kl;   // what fp16 leaves of the keys
+  uint16_t* wide_kl;   // what fp16 leaves of the keys (NULL: not taken into account)
   uint16_t* wide_v;
   const int32_t* span; // decode steps with a window: [sequence][KV head] {first, past the last} row that a token sees
   int32_t n_seqs, n_kv, G, hd, nq;

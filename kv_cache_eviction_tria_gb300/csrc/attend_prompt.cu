@@ -29,8 +29,10 @@
 // Tiles come by TMA into 128-byte-swizzled shared memory, so the planes are
 // fp16: 8- and 4-bit rows go into the workspace as fp16 (code x scale) first
 // (k_widen), values rounded once, keys as the rounded value and the remainder,
-// which takes a product of its own (kLow): logits, and the log-sum-exp that is
-// given out in fp32, then carry no rounding of the keys. 128 rows of them being read again by every 256
+// which takes a product of its own (kLow) when the log-sum-exp is asked for: it is
+// given out in fp32 and would show the keys' rounding (2e-3 at 230, 1e-5 with the
+// remainders), while the output's own type hides it. 3162 tokens in two chunks
+// over 27081 rows take 975 us with the remainders, 623 us without. 128 rows of them being read again by every 256
 // columns. Converting them tile by tile on their way into shared memory, which
 // the products' operands already fill to its rate, held a pair of tiles at 2.3
 // (q4_0) and 3.2 us (q8_0) instead of 1.7.
@@ -952,8 +954,13 @@ __global__ void __launch_bounds__(256) k_widen(const __grid_constant__ AttendArg
   }
   const int64_t src = S.row0 + seg0 + r0, dst = S.wide0 + seg0 + r0;
   if (blockIdx.z == 0) {
-    if (A.k_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0, true>(A.k, A.ks, A.wide_k, A.wide_kl, src, dst, rows, A.hd);
-    else if (A.k_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0, true>(A.k, A.ks, A.wide_k, A.wide_kl, src, dst, rows, A.hd);
+    if (A.k_type == TRIA_Q8_0) {
+      if (A.wide_kl) widen_rows<TRIA_Q8_0, true>(A.k, A.ks, A.wide_k, A.wide_kl, src, dst, rows, A.hd);
+      else widen_rows<TRIA_Q8_0, false>(A.k, A.ks, A.wide_k, nullptr, src, dst, rows, A.hd);
+    } else if (A.k_type == TRIA_Q4_0) {
+      if (A.wide_kl) widen_rows<TRIA_Q4_0, true>(A.k, A.ks, A.wide_k, A.wide_kl, src, dst, rows, A.hd);
+      else widen_rows<TRIA_Q4_0, false>(A.k, A.ks, A.wide_k, nullptr, src, dst, rows, A.hd);
+    }
   } else {
     if (A.v_type == TRIA_Q8_0) widen_rows<TRIA_Q8_0, false>(A.v, A.vs, A.wide_v, nullptr, src, dst, rows, A.hd);
     else if (A.v_type == TRIA_Q4_0) widen_rows<TRIA_Q4_0, false>(A.v, A.vs, A.wide_v, nullptr, src, dst, rows, A.hd);
@@ -1007,9 +1014,9 @@ cudaError_t launch_attend_prompt(const AttendArgs& A, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   switch (prompt_dims(A.hd)) {
-    case 64: return A.wide_k ? launch_prompt_hd<64, true>(A, st) : launch_prompt_hd<64, false>(A, st);
-    case 128: return A.wide_k ? launch_prompt_hd<128, true>(A, st) : launch_prompt_hd<128, false>(A, st);
-    case 256: return A.wide_k ? launch_prompt_hd<256, true>(A, st) : launch_prompt_hd<256, false>(A, st);
+    case 64: return A.wide_kl ? launch_prompt_hd<64, true>(A, st) : launch_prompt_hd<64, false>(A, st);
+    case 128: return A.wide_kl ? launch_prompt_hd<128, true>(A, st) : launch_prompt_hd<128, false>(A, st);
+    case 256: return A.wide_kl ? launch_prompt_hd<256, true>(A, st) : launch_prompt_hd<256, false>(A, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -304,3 +304,25 @@ def test_scales_of_three_blocks(lib, k, v, tokens):
                 c.h["v_scale"][r0 + late] = 60000.0
         c.d["v_scale"].copy_(torch.from_numpy(c.h["v_scale"]))
     run(lib, c, 8, "f16", [tokens] * 3, back=5)
+
+
+@pytest.mark.parametrize("k,v", [("q8_0", "q4_0"), ("q4_0", "f16")])
+@pytest.mark.parametrize("hd", [64, 128, 192])
+def test_prompts_over_codes_with_and_without_lse(lib, k, v, hd):
+    """With a log-sum-exp asked for, logits over quantised keys are those of exact keys; without one the keys are rounded
+    to fp16 once. Both outputs are within check_attend's bounds of the rounded keys."""
+    c = R.Cache(lib, np.random.default_rng(41), rows=[400, 61], cap=[410, 64], n_kv=2, hd=hd, k_type=k, v_type=v)
+    rng = np.random.default_rng(42)
+    tok0 = np.array([0, 70, 131], np.int32)
+    pos = np.concatenate([c.last(s) - np.arange(t)[::-1] for s, t in enumerate((70, 61))]).astype(np.int32)
+    q = R.act(rng.standard_normal((131, 8, hd)), "f16")
+    ws = c.ws(lib.attend_workspace_size(c.cache, 8, tok0))
+    want = R.attend_expected(c, R.host(q), pos, tok0, 8)
+    for lse in (torch.empty(131, 8, device="cuda"), None):
+        out = torch.empty_like(q)
+        lib.attend(c.cache, q, out, torch.from_numpy(pos).cuda(), tok0=tok0, lse=lse, ws=ws)
+        assert lib.device_status(ws) == lib.OK
+        R.check_attend(R.host(out), None, want, "f16", True, 400, hd, k_exact=False)
+        if lse is not None:                      # (hd + 2) 2^-24 of the moduli and the sum's roundings, none of the keys'
+            tl = (hd + 2) * R.U24 * want[3] + (400 / 32 + 64) * R.U24 + R.U24 * 4 * np.abs(want[1])
+            assert np.all(np.abs(R.host(lse) - want[1]) <= tl)
