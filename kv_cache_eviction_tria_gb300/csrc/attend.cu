@@ -379,12 +379,10 @@ bool tensor_types(const tria_layer_cache* c, int type) {
 // the fp32 kernel.
 bool step_dims(int hd) { return hd == 64 || hd == 96 || hd == 128 || hd == 256; }
 
-constexpr int kStepCols = 16;
-
 int path_of(bool tensor, int hd, int t, int G) {
   if (t == 0) return kPathNone;
   if (!tensor) return kPathPlain;
-  if (t * G > kStepCols) return kPathPrompt;
+  if (prompt_cols_reached(t, G)) return kPathPrompt;
   return step_dims(hd) ? kPathStep : kPathPlain;
 }
 
@@ -427,16 +425,12 @@ int prompt_split(int64_t units, int cap_max, int sms) {
 AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0) {
   AttendLayout L{};
   int64_t units = 0, prompts = 0;
-  int64_t wide = 0;    // rows of the prompts' sequences
   int cap_max = 0, cols = 0;
   for (int s = 0; s < c->n_seqs; ++s) {
     const int64_t x = (int64_t)(tok0[s + 1] - tok0[s]) * G;
     units += (x + kCols - 1) / kCols;
     if (x <= kStepCols) cols = std::max(cols, (int)x);
-    else {
-      prompts += (x + prompt_cols(c->head_dim) - 1) / prompt_cols(c->head_dim);
-      wide += (int64_t)c->n_kv_heads * c->capacity[s];
-    }
+    else prompts += (x + prompt_cols(c->head_dim) - 1) / prompt_cols(c->head_dim);
     cap_max = std::max(cap_max, c->capacity[s]);
   }
   L.sms = sm_count();
@@ -452,6 +446,7 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   const size_t prompt = L.prompt_split > 1
       ? (size_t)(prompts * c->n_kv_heads) * L.prompt_split * prompt_cols(c->head_dim) * (prompt_dims(c->head_dim) + 2) : 0;
   L.wide_k = up256(L.part + sizeof(float) * std::max(std::max(plain, step), prompt));
+  const int64_t wide = widened_rows(c->n_seqs, c->n_kv_heads, G, c->capacity, tok0, nullptr);
   const size_t plane = up256((size_t)wide * c->head_dim * 2);
   const bool tensor = tensor_types(c, TRIA_F16);
   const size_t keys = tensor && c->k_type != TRIA_F16 ? plane : 0;
@@ -558,15 +553,12 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   // each kernel sees the sequences it takes, the others without tokens
   auto take = [&](int path) {
     const int per = path == kPathPrompt ? prompt_cols(hd) : kCols;
-    int64_t wide = 0;
     units = 0;
     for (int s = 0; s < cache->n_seqs; ++s) {
       const int t = a->tok0[s + 1] - a->tok0[s];
       A.seq[s].t = path_of(tensor, hd, t, G) == path ? t : 0;
       A.seq[s].unit0 = units;
-      A.seq[s].wide0 = wide;
       units += (A.seq[s].t * G + per - 1) / per;
-      if (A.seq[s].t > 0) wide += (int64_t)cache->n_kv_heads * cache->capacity[s];
     }
     A.units = units;
   };
@@ -583,6 +575,9 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   if (prompt) {
     take(kPathPrompt);
     A.split = L.prompt_split;
+    int64_t first[kMaxSeqs];
+    A.wide_rows = widened_rows(cache->n_seqs, cache->n_kv_heads, G, cache->capacity, a->tok0, first);
+    for (int s = 0; s < cache->n_seqs; ++s) A.seq[s].wide0 = first[s];
     if (cache->k_type != TRIA_F16) {
       A.wide_k = (uint16_t*)((uint8_t*)ws + L.wide_k);
       if (a->lse) A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);

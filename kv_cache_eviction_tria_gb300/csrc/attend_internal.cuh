@@ -6,6 +6,7 @@
 
 #include <new>
 
+#include "attend_plan.h"
 #include "tria_internal.cuh"
 
 // Opaque rotation handle of the C ABI.
@@ -55,6 +56,7 @@ struct AttendArgs {
   uint16_t* wide_k;    // fp16 copies of quantised planes (prompts; NULL: none)
   uint16_t* wide_kl;   // what fp16 leaves of the keys (NULL: not taken into account)
   uint16_t* wide_v;
+  int64_t wide_rows;   // of each of them (widened_rows)
   const int32_t* span; // decode steps with a window: [sequence][KV head] {first, past the last} row that a token sees
   int32_t n_seqs, n_kv, G, hd, nq;
   int32_t type, k_type, v_type;

@@ -983,15 +983,12 @@ cudaError_t launch_prompt_hd(const AttendArgs& A, cudaStream_t st) {
   memset(&mk, 0, sizeof(mk));
   memset(&ml, 0, sizeof(ml));
   memset(&mv, 0, sizeof(mv));
-  int64_t rows = 0, wide = 0;
-  for (int s = 0; s < A.n_seqs; ++s) {
-    rows = std::max(rows, A.seq[s].row0 + (int64_t)A.n_kv * A.seq[s].cap);
-    wide = std::max(wide, A.seq[s].wide0 + (int64_t)A.n_kv * A.seq[s].cap);
-  }
-  if (!plane_map_f16(&mk, A.wide_k ? (const void*)A.wide_k : A.k, A.hd, A.wide_k ? wide : rows, H::BN) ||
-      !plane_map_f16(&mv, A.wide_v ? (const void*)A.wide_v : A.v, A.hd, A.wide_v ? wide : rows, H::BN))
+  int64_t rows = 0;
+  for (int s = 0; s < A.n_seqs; ++s) rows = std::max(rows, A.seq[s].row0 + (int64_t)A.n_kv * A.seq[s].cap);
+  if (!plane_map_f16(&mk, A.wide_k ? (const void*)A.wide_k : A.k, A.hd, A.wide_k ? A.wide_rows : rows, H::BN) ||
+      !plane_map_f16(&mv, A.wide_v ? (const void*)A.wide_v : A.v, A.hd, A.wide_v ? A.wide_rows : rows, H::BN))
     return cudaErrorInvalidValue;
-  if (kLow && !plane_map_f16(&ml, A.wide_kl, A.hd, wide, H::BN)) return cudaErrorInvalidValue;
+  if (kLow && !plane_map_f16(&ml, A.wide_kl, A.hd, A.wide_rows, H::BN)) return cudaErrorInvalidValue;
   kern<<<(unsigned)grid, kPromptThreads, H::kSmem, st>>>(A, mk, ml, mv);
   if (A.split > 1) {
     const cudaError_t e3 = cudaGetLastError();
