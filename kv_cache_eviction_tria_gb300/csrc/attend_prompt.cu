@@ -91,6 +91,7 @@ constexpr int kSoftRegs = 192, kOtherRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kOtherRegs == 4 * kPromptRegs, "register shares");
 
 constexpr float kLazy = 8.f, kShift = 5.f;
+constexpr int kWaitLimit = 1 << 22;   // polls of a wait before it gives up
 
 // ---- PTX -------------------------------------------------------------------
 
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&X.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -432,15 +434,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     return r;
   };
   const uint32_t tmem = X.tmem;
-  // a bounded wait; after one gave up nobody waits any more
+  // bounded waits; after one gave up nobody waits any more, and the CTA writes no
+  // results. The issuing warp goes on or gives up as one (wait_warp). Threads that
+  // wait for themselves may learn different things near a limit, so none of them
+  // leaves: the softmax and the loading warps run their loops to the end, past waits
+  // that return at once, and a warp's lanes meet at every collective instruction.
+  // (With votes at each of their waits a prompt of 8192 tokens took 530 us, 469 so.)
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    for (int it = 0; it < (1 << 22); ++it) {
-      if (mbar_try_wait(b, parity)) return true;
-      if (*s_abort) return false;
-    }
+    for (int it = 0; it < kWaitLimit; ++it)
+      if (mbar_try_wait(b, parity) || *s_abort) return;
     *s_abort = 1;
-    report(A.ctrl, TRIA_ERR_TIMEOUT, (uint32_t)s);
-    return false;
+  };
+  auto wait_warp = [&](uint64_t* b, uint32_t parity) {
+    const int r = mbar_wait_warp(b, parity, s_abort, kWaitLimit);
+    if (r == 0) *s_abort = 1;
+    return r > 0;
   };
 
   if (wg >= 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -450,15 +458,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       // results of waits and addresses are the same in all lanes and kept in
       // such a form (votes, a broadcast): operands of the products then live in
       // uniform registers, without which issuing them was the bottleneck
-      auto wait_all = [&](uint64_t* b, uint32_t parity) {
-        for (int it = 0; it < (1 << 22); ++it) {
-          if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
-          if (__any_sync(0xffffffffu, *s_abort != 0)) return false;
-        }
-        *s_abort = 1;
-        if (lane == 0) report(A.ctrl, TRIA_ERR_TIMEOUT, (uint32_t)s);
-        return false;
-      };
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t dq = tile_desc(smem_u32(smem + H::oQ), 16), dk = tile_desc(smem_u32(smem + H::oRing), 16),
                      dv = tile_desc(smem_u32(smem + H::oRing), BN * 128);
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         for (int k = 0; k < BN / 16; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), i > 0 || k > 0);
         tc_commit(&b_o[q]);
       };
-      bool ok = wait_all(b_q, 0) && wait_all(&b_full[0], 0) && (!kLow || wait_all(&b_full[1], 0));
+      bool ok = wait_warp(b_q, 0) && wait_warp(&b_full[0], 0) && (!kLow || wait_warp(&b_full[1], 0));
       tc_fence_after();
       if (ok && elect_one()) {
 #pragma unroll
@@ -499,7 +498,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       for (int i = 0; ok && i < nt; ++i) {
         const bool more = i + 1 < nt;
         const int sl = sk + 1 == ST ? 0 : sk + 1, pl2 = sk + 1 == ST ? pk ^ 1 : pk;   // of the remainders of K(i + 1)
-        if (more) ok = wait_all(&b_full[sk], pk) && (!kLow || wait_all(&b_full[sl], pl2));
+        if (more) ok = wait_warp(&b_full[sk], pk) && (!kLow || wait_warp(&b_full[sl], pl2));
         if constexpr (NB == 2) {
           // the other buffer's weights are those of tile i - 1, whose sums were issued before
           if (more) {
@@ -513,10 +512,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
             __syncwarp();
           }
         }
-        ok = ok && wait_all(&b_full[sv], pv);
+        ok = ok && wait_warp(&b_full[sv], pv);
 #pragma unroll
         for (int q = 0; q < QT; ++q) {
-          ok = ok && wait_all(&b_p[NB * q + i % NB], (i / NB) & 1);
+          ok = ok && wait_warp(&b_p[NB * q + i % NB], (i / NB) & 1);
           tc_fence_after();
           if (ok && elect_one()) {
             sums(q, i, sv);
@@ -549,7 +548,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       }
       // nothing may be running when the accumulators are given back
       if (elect_one()) tc_commit(b_x);
-      for (int it = 0; it < (1 << 22) && !mbar_try_wait(b_x, 0); ++it) {
+      for (int it = 0; it < kWaitLimit && !mbar_try_wait(b_x, 0); ++it) {
       }
     }
   } else if (wg >= 2) {
@@ -559,8 +558,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     auto free_stage = [&](int e) {
       if (e >= ST) wait(&b_empty[e % ST], ((e / ST) - 1) & 1);
     };
-    // after a wait gave up the loops run to their end without waiting (their
-    // threads meet at barriers), start no more copies, and wait, bounded, for
+    // after a wait gave up the loops start no more copies, and wait, bounded, for
     // those still on their way
     auto go = [&] { return tid == 0 && !*s_abort; };
     auto drain = [&](bool values) {
@@ -602,6 +600,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       for (int i = 0; i < nt; ++i) {
         const int r = tile_row(i, rows), e = P * i + P - 1;
         free_stage(e);
+        __syncwarp();
         // positions and marks go with the value tile, which stays until the weights are used
         const int32_t* tp = s_pos + (i % H::kPosTiles) * BN;
 #pragma unroll
@@ -615,6 +614,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         if (go()) copy_tile<HD, BN>(stage(e), &map_v, value0 + r, all ? &b_full[e % ST] : b_raw);
         if (all) continue;
         wait(b_raw, looked & 1);
+        __syncwarp();
         ++looked;
         clean_tile<HD, BN>(stage(e), rows, X.junk[e % ST], tid);
         fence_proxy_async_smem();
@@ -633,11 +633,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = lane_base + H::cO + q * HD;
     float M = -INFINITY, l = 0.f;
-    bool poison = false, ok = true;
+    bool poison = false;
     for (int i = 0; i < nt; ++i) {
       const int buf = NB * q + i % NB;
-      ok = wait(&b_s[buf], (i / NB) & 1);
-      if (!ok) break;
+      wait(&b_s[buf], (i / NB) & 1);
+      __syncwarp();
       tc_fence_after();
       const uint32_t ts = lane_base + H::cS(q, i % NB);
       uint32_t x[BN];
@@ -648,8 +648,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       bool masked = rows < BN;
       const int ev = P * i + P - 1;
       if (need_pos || masked) {
-        ok = wait(&b_full[ev % ST], (ev / ST) & 1);        // positions and marks are there
-        if (!ok) break;
+        wait(&b_full[ev % ST], (ev / ST) & 1);       // positions and marks are there
+        __syncwarp();
       }
       const int32_t* tp = s_pos + (i % H::kPosTiles) * BN;
       if (need_pos)
@@ -704,8 +704,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
           l *= a;
         }
         if (i > 0) {
-          ok = wait(&b_o[q], (i - 1) & 1);                 // the sums of the tile before may be running
-          if (!ok) break;
+          wait(&b_o[q], (i - 1) & 1);                // the sums of the tile before may be running
+          __syncwarp();
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < HD; c += 16) {
@@ -742,11 +742,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
       mbar_arrive(&b_p[buf]);
     }
     // ---- results
-    if (ok && nt > 0) {
-      ok = wait(&b_f[q], 0);
+    if (nt > 0) {
+      wait(&b_f[q], 0);
       tc_fence_after();
     }
-    if (ok) {
+    if (__all_sync(0xffffffffu, *s_abort == 0)) {
       const bool split = A.split > 1;
       float* slot = A.part + ((int64_t)y * A.split + part) * (QT * 128) * (HD + 2) + (q * 128 + m);
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -800,7 +800,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
     tc_fence_before();
   }
   __syncthreads();
+  if (threadIdx.x == 0 && *s_abort) report(A.ctrl, TRIA_ERR_TIMEOUT, (uint32_t)s);
   if (warp == kIssueWarp) {
+    __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }

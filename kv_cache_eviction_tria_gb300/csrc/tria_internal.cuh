@@ -284,6 +284,18 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return false;
 }
 
+// The same by a converged warp, with one answer for all of its lanes: 1 when
+// every lane has seen the phase, -1 when *abort is set, 0 when the limit ran
+// out. Near a limit or an abort lanes that decided for themselves could part,
+// and those that went on would meet collective instructions alone.
+__device__ __forceinline__ int mbar_wait_warp(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort, int limit) {
+  for (int it = 0; it < limit; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return 1;
+    if (__any_sync(0xffffffffu, *abort != 0)) return -1;
+  }
+  return 0;
+}
+
 __device__ __forceinline__ uint32_t ld_acquire_u32(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
