@@ -388,6 +388,8 @@ def load_stats(q_mean, q_abs, **kw) -> Stats:
 class LayerCache:
     """One layer's cache (``tria_layer_cache``): device tensors + host layout."""
 
+    _made = None       # (planes' addresses, C struct, reference to it) of the last c_ref()
+
     def __init__(self, *, k, v, pos, n_live, seq_row0, capacity, head_dim: int, n_kv_heads: int,
                  k_type: str = "f16", v_type: str = "f16", k_scale=None, v_scale=None):
         self.k, self.v, self.pos, self.n_live = k, v, pos, n_live
@@ -407,6 +409,10 @@ class LayerCache:
     def __setattr__(self, name, value):
         object.__setattr__(self, "_made", None)
         object.__setattr__(self, name, value)
+
+    def __getstate__(self):
+        """For copy and pickle: all but the C struct, whose addresses belong to this object."""
+        return {name: value for name, value in self.__dict__.items() if name != "_made"}
 
     def c_ref(self):
         """A reference to the C struct, made anew only when a field or a plane's address has changed since the last
