@@ -388,7 +388,7 @@ def load_stats(q_mean, q_abs, **kw) -> Stats:
 class LayerCache:
     """One layer's cache (``tria_layer_cache``): device tensors + host layout."""
 
-    _made = None       # (planes' addresses, C struct, reference to it) of the last c_ref()
+    _made = None       # what c_ref() keeps: how to ask the planes, their addresses, the C struct
 
     def __init__(self, *, k, v, pos, n_live, seq_row0, capacity, head_dim: int, n_kv_heads: int,
                  k_type: str = "f16", v_type: str = "f16", k_scale=None, v_scale=None):
@@ -417,18 +417,20 @@ class LayerCache:
     def c_ref(self):
         """A reference to the C struct, made anew only when a field or a plane's address has changed since the last
         call (a decode step calls this for every layer)."""
-        ks, vs = self.k_scale, self.v_scale
-        at = (self.k if isinstance(self.k, int) else self.k.data_ptr(), self.v if isinstance(self.v, int) else self.v.data_ptr(),
-              self.pos if isinstance(self.pos, int) else self.pos.data_ptr(),
-              self.n_live if isinstance(self.n_live, int) else self.n_live.data_ptr(),
-              0 if ks is None else ks if isinstance(ks, int) else ks.data_ptr(),
-              0 if vs is None else vs if isinstance(vs, int) else vs.data_ptr())
         made = self._made
-        if made is None or made[0] != at:
-            c = self.c_struct()
-            made = (at, c, ctypes.byref(c))
-            object.__setattr__(self, "_made", made)
-        return made[2]
+        if made is not None:
+            address, whole, at, ref, _ = made
+            if [f() for f in address] == at:
+                if False in [f() for f in whole]:            # restrided in place
+                    raise ValueError("device argument must be contiguous")
+                return ref
+        c = self.c_struct()
+        planes = [t for t in (self.k, self.v, self.pos, self.n_live, self.k_scale, self.v_scale)
+                  if t is not None and not isinstance(t, int)]
+        address = [t.data_ptr for t in planes]
+        made = (address, [t.is_contiguous for t in planes], [f() for f in address], ctypes.byref(c), c)
+        object.__setattr__(self, "_made", made)
+        return made[3]
 
 
 class Policy:

@@ -57,3 +57,15 @@ def test_the_struct_follows_fields_and_planes():
     assert fields(c.c_ref()) == {**a, "k": 0x80000, "capacity": [50, 40]}
     c.capacity[0] = 7                                        # in place
     assert fields(c.c_ref())["capacity"] == [7, 40]
+
+
+@pytest.mark.parametrize("name", ["k", "v", "pos", "n_live", "k_scale", "v_scale"])
+def test_a_plane_restrided_in_place_is_refused(name):
+    """At the address that it had, as torch's transpose_ or as_strided_ leave it."""
+    c = cache(Plane)
+    c.c_ref()
+    getattr(c, name).contiguous = False
+    with pytest.raises(ValueError):
+        c.c_ref()
+    getattr(c, name).contiguous = True
+    c.c_ref()
