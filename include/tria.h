@@ -694,6 +694,9 @@ typedef struct tria_attention {
   double scale;              /* 0: 1 / sqrt(head_dim) */
   int32_t window;            /* 0: no window */
   int32_t sink;              /* first rows that stay visible outside the window */
+  int32_t round_keys;        /* 1: prompts over q8_0 / q4_0 keys take code x scale rounded to fp16 once, in out and
+                                in lse (faster); 0: the keys' exact values. No effect elsewhere */
+  int32_t pad;
 } tria_attention;
 
 /* Workspace bytes of tria_attend for these shapes (0 on invalid input). The
@@ -710,8 +713,8 @@ size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_hea
  * with fp32 sums: queries as fp16 (bf16 ones scaled by a power of two
  * first, which is undone), weights as fp16, statistics in fp32. Codes of
  * quantised planes are exact and their scales fp32 factors, but prompts (as
- * above) take code x scale rounded to fp16 once, keys only when lse is NULL
- * (with lse, logits carry no rounding of the keys); numbers beyond fp16's range
+ * above) take values as code x scale rounded to fp16 once, and with round_keys
+ * keys too (without it logits carry no rounding of the keys); numbers beyond fp16's range
  * overflow there. Host errors: INVALID_ARG,
  * UNSUPPORTED (type, group, 2^31 or more tokens x query heads, prompts over
  * planes of 2^31 or more rows), WORKSPACE. Device errors (tria_device_status

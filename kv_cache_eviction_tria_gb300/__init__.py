@@ -136,6 +136,7 @@ class _Attention(ctypes.Structure):
         ("type", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
         ("lse", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("pos", ctypes.c_void_p),
         ("tok0", ctypes.c_void_p), ("scale", ctypes.c_double), ("window", ctypes.c_int32), ("sink", ctypes.c_int32),
+        ("round_keys", ctypes.c_int32), ("pad", ctypes.c_int32),
     ]
 
 
@@ -840,10 +841,11 @@ def attend_workspace_size(cache: LayerCache, n_q_heads: int, tok0) -> int:
 
 
 def attend(cache: LayerCache, q, out, pos, *, ws, tok0=None, lse=None, scale: float = 0.0, window: int = 0, sink: int = 0,
-           stream=None):
+           round_keys: bool = False, stream=None):
     """tria_attend: attention of new tokens over the cache. q / out [tokens][n_q_heads][head_dim], pos int32
     [tokens], tok0 host offsets of the sequences' tokens (None: equally many each), lse float32
-    [tokens][n_q_heads] or None; scale 0: 1 / sqrt(head_dim); window 0: none; sink first rows stay visible."""
+    [tokens][n_q_heads] or None; scale 0: 1 / sqrt(head_dim); window 0: none; sink first rows stay visible;
+    round_keys: prompts over quantised keys take them rounded to fp16 (faster), in out and in lse."""
     n, hd, n_seqs = pos.numel(), cache.head_dim, len(cache.seq_row0)
     a = _Attention()
     a.type, a.n_q_heads = _act_type(q), q.shape[1]
@@ -855,6 +857,7 @@ def attend(cache: LayerCache, q, out, pos, *, ws, tok0=None, lse=None, scale: fl
     a.pos = _pos32(pos, n)
     tok0 = _tokens0(tok0, n_seqs, n)
     a.tok0, a.scale, a.window, a.sink = tok0.ctypes.data, float(scale), int(window), int(sink)
+    a.round_keys = int(round_keys)
     wp, wb = _ws(ws)
     st = load_library().tria_attend(cache.c_ref(), ctypes.byref(a), wp, wb, _stream_handle(stream))
     if st:

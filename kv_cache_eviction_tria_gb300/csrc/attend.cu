@@ -490,6 +490,7 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   if ((r = check_attend_shape(cache, a->n_q_heads, a->tok0)) != TRIA_OK) return r;
   if (!act_ok(a->type)) return TRIA_ERR_UNSUPPORTED;
   if (a->window < 0 || a->sink < 0 || !(a->scale >= 0.0) || !isfinite((float)a->scale)) return TRIA_ERR_INVALID_ARG;
+  if (a->round_keys != 0 && a->round_keys != 1) return TRIA_ERR_INVALID_ARG;
   const int hd = cache->head_dim, nq = a->n_q_heads, n_tokens = a->tok0[cache->n_seqs];
   const int size = a->type == TRIA_F32 ? 4 : 2;
   if (n_tokens > 0) {
@@ -580,7 +581,7 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
     for (int s = 0; s < cache->n_seqs; ++s) A.seq[s].wide0 = first[s];
     if (cache->k_type != TRIA_F16) {
       A.wide_k = (uint16_t*)((uint8_t*)ws + L.wide_k);
-      if (a->lse) A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);
+      if (!a->round_keys) A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);
     }
     if (cache->v_type != TRIA_F16) A.wide_v = (uint16_t*)((uint8_t*)ws + L.wide_v);
     if (launch_attend_prompt(A, st) != cudaSuccess) return TRIA_ERR_CUDA;

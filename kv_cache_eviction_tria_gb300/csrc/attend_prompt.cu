@@ -29,13 +29,15 @@
 // Tiles come by TMA into 128-byte-swizzled shared memory, so the planes are
 // fp16: 8- and 4-bit rows go into the workspace as fp16 (code x scale) first
 // (k_widen), values rounded once, keys as the rounded value and the remainder,
-// which takes a product of its own (kLow) when the log-sum-exp is asked for: it is
-// given out in fp32 and would show the keys' rounding (2e-3 at 230, 1e-5 with the
-// remainders), while the output's own type hides it. 3162 tokens in two chunks
-// over 27081 rows take 975 us with the remainders, 623 us without. 128 rows of them being read again by every 256
-// columns. Converting them tile by tile on their way into shared memory, which
-// the products' operands already fill to its rate, held a pair of tiles at 2.3
-// (q4_0) and 3.2 us (q8_0) instead of 1.7.
+// which takes a product of its own (kLow). The remainders are exact: a scale is a
+// multiple of 2^-24 and a code whole, so what rounding leaves of their product has 8
+// bits at most, all above 2^-24. lse is given out in fp32 and would show the keys'
+// rounding (2e-3 at 230, 1e-5 with the remainders), which the output's own type
+// hides: a caller who takes it (round_keys) saves the remainders. 3162 tokens in two
+// chunks over 27081 rows take 975 us with them, 623 us without. Converting the rows
+// tile by tile on their way into shared memory, which the products' operands
+// already fill to its rate and where each row would be converted again for every
+// 256 columns, held a pair of tiles at 2.3 (q4_0) and 3.2 us (q8_0) instead of 1.7.
 //
 // In tiles that some token does not see whole, value rows past the last one
 // become zeros, and one that holds an infinity or NaN is replaced by zeros
@@ -917,7 +919,7 @@ __device__ __forceinline__ void widen_rows(const uint8_t* data, const uint8_t* s
       const float2 code = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
       asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[k]) : "r"(o[k]), "r"(sc));
       if constexpr (kLow) {
-        // code x scale fits fp32; what fp16 left of it (8 bits at most) fits fp16
+        // code x scale fits fp32, and what fp16 left of it (8 bits at most, all above 2^-24) fits fp16
         const float2 x = __fmul2_rn(code, sf), hi = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
         const __half2 l = __floats2half2_rn(x.x - hi.x, x.y - hi.y);
         lo[k] = *reinterpret_cast<const uint32_t*>(&l);
