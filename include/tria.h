@@ -662,7 +662,7 @@ typedef struct tria_qkv {
  *   q8_0: d = max |x| / 127, code = x / d rounded half away from zero
  *   q4_0: d = m / -8 with m the first value of largest modulus, code =
  *         min(15, floor(x / d + 8.5)); scales are stored as fp16(d)
- *   a block with a NaN gets a NaN for its scale
+ *   a block with an infinity or a NaN gets a NaN for its scale
  * The host errors are INVALID_ARG, UNSUPPORTED (type), WORKSPACE (ws: a
  * workspace of this cache, only its control words are used); device errors as
  * tria_append, and a sequence with one is left unchanged (its queries are

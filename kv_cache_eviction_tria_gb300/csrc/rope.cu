@@ -176,7 +176,7 @@ __device__ __forceinline__ void codes_q4(const float* x, float d, float* m) {
 }
 
 // The larger / smaller value, NaN when either is one (a block that holds a NaN
-// gets a NaN for its scale and reads as NaN, as an unquantised row would).
+// or an infinity gets a NaN for its scale and reads as NaN).
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -238,7 +238,7 @@ __device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_
 #pragma unroll
     for (int i = 0; i < 16; ++i) am = max_nan(am, fabsf(x[i]));
     am = max_nan(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    const float d = __fdiv_rn(am, 127.f);
+    const float d = __fdiv_rn(am, 127.f) + (am - am);   // (an infinity's scale is a NaN too: 0 x inf has no value)
     const __half dh = __float2half_rn(d);
     const float ds = __half2float(dh);
     float m[16];
@@ -271,7 +271,7 @@ __device__ __forceinline__ void hold16(float* x, int type, uint8_t* data, uint8_
   const float other = __shfl_xor_sync(0xffffffffu, big, 1);
   const float first = upper ? other : big, second = upper ? big : other;
   big = fabsf(second) > fabsf(first) || second != second ? second : first;
-  const float d = big * -0.125f;
+  const float d = big * -0.125f + (big - big);          // (an infinity's is a NaN, as in q8_0)
   const __half dh = __float2half_rn(d + 0.f);   // an all-zero block's scale is +0
   const float ds = __half2float(dh);
   float m[16];
