@@ -333,13 +333,6 @@ __global__ void __launch_bounds__(128) k_attend_span(const __grid_constant__ Att
   }
 }
 
-// Parts of a unit: enough CTAs for the GPU, none under 128 rows of the
-// capacity.
-int plain_split(int64_t units, int cap_max) {
-  const int64_t want = (3 * 152 + units - 1) / std::max<int64_t>(units, 1);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)(cap_max + 127) / 128, 64}));
-}
-
 }  // namespace
 
 cudaError_t launch_attend_plain(const AttendArgs& A, cudaStream_t st) {
@@ -386,22 +379,15 @@ int path_of(bool tensor, int hd, int t, int G) {
   return step_dims(hd) ? kPathStep : kPathPlain;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 152;
-  return sms;
-}
-
 // The kernels of a call run one after the other and share the arrival counters
 // and the space of the partial results. The layout covers every type of
 // queries. The counters, which have to be zero between calls, take the same
 // place for every shape, so that a workspace may serve calls of different
-// shapes: a decode step counts segments (at most kMaxSegments), the others
-// units that are split (fewer than three per SM).
+// shapes: a decode step counts segments, the fp32 kernel the units that it
+// splits, at most kMaxSegments both.
 struct AttendLayout {
   size_t count, span, part, wide_k, wide_kl, wide_v, total;
-  int units, split, prompt_split, sms;
+  int split, prompt_split, sms;
 };
 
 // Parts of a unit of a prompt: as many as make the last wave of CTAs (one per
@@ -434,8 +420,7 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
     cap_max = std::max(cap_max, c->capacity[s]);
   }
   L.sms = sm_count();
-  L.units = (int)units;
-  L.split = plain_split(units * c->n_kv_heads, cap_max);
+  L.split = plain_split(units * c->n_kv_heads, cap_max, L.sms, kMaxSegments);
   L.count = up256(sizeof(Ctrl));
   L.span = up256(L.count + sizeof(uint32_t) * (size_t)kMaxSegments);
   L.part = up256(L.span + 2 * sizeof(int32_t) * (size_t)c->n_seqs * c->n_kv_heads);

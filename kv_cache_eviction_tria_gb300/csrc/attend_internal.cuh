@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <new>
 
 #include "attend_plan.h"
@@ -26,6 +27,18 @@ inline tria_status check_tokens(const int32_t* tok0, int n_seqs) {
   for (int s = 0; s < n_seqs; ++s)
     if (tok0[s + 1] < tok0[s]) return TRIA_ERR_INVALID_ARG;
   return TRIA_OK;
+}
+
+// SMs of the current device (without a device, of a whole GB300). Asked once a
+// device: calls that take microseconds need it each time.
+inline int sm_count() {
+  static std::atomic<int> known[16];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+  if (dev < 16 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  if (dev < 16) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 // One attention call, passed by value.

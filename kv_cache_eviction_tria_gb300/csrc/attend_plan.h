@@ -1,11 +1,29 @@
-// Host arithmetic of an attention call that needs no GPU: which sequences are
-// prompts, and the rows of the fp16 copies that prompts over quantised planes
-// read (k_widen). Plain C++, so that it can be checked by itself.
+// Host arithmetic of rotation, append and attention that needs no GPU: grids and
+// splits for a number of SMs, which sequences are prompts, and the rows of the
+// fp16 copies that prompts over quantised planes read (k_widen). Plain C++, so that
+// it can be checked by itself.
 #pragma once
 
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace tria {
+
+// CTAs of k_rope, of which an SM holds one: warps take equal shares of the work
+// (tokens x groups of heads), so no more than one wave.
+inline int rope_grid(int64_t tokens, int64_t groups, int warps, int sms) {
+  return (int)std::min<int64_t>(std::max<int64_t>((tokens * groups + warps - 1) / warps, 1), sms);
+}
+
+// Parts of a unit of the fp32 attention kernel (units: of all KV heads): three CTAs
+// per SM, no part under 128 rows of the capacity. Units that are split count their
+// arrivals: no more of them than there are counters.
+inline int plain_split(int64_t units, int cap_max, int sms, int counters) {
+  if (units > counters) return 1;
+  const int64_t want = (3 * (int64_t)sms + units - 1) / std::max<int64_t>(units, 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, ((int64_t)cap_max + 127) / 128, 64}));
+}
 
 // Columns (token x query head of a KV head's group) that a sequence may have
 // as a decode step.

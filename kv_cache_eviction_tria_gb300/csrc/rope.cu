@@ -75,7 +75,7 @@ struct RopeArgs {
   int32_t* n_live;
   const int32_t* n_before;
   Ctrl* ctrl;
-  int32_t n_seqs, n_kv, k_type, v_type;
+  int32_t n_seqs, k_type, v_type;
   int64_t row0[kMaxSeqs];
   int32_t cap[kMaxSeqs];
   int32_t tok0[kMaxSeqs + 1];
@@ -568,8 +568,7 @@ int ceil_pow2(int x) {
 
 template <typename T, bool kCache, int LAYOUT>
 cudaError_t launch_rope_tl(const RopeArgs& A, cudaStream_t st) {
-  const int64_t want = ((int64_t)A.n_tokens * A.groups + kRopeWarps - 1) / kRopeWarps;
-  const int grid = (int)std::min<int64_t>(std::max<int64_t>(want, 1), 152);
+  const int grid = rope_grid(A.n_tokens, A.groups, kRopeWarps, sm_count());
   const int smem = kRopeWarps * (rope_stages(kCache) * A.stage + (kCache ? (32 / A.lanes) * (A.hd + 4) * (int)sizeof(float) : 0));
   auto kern = k_rope<T, kCache, LAYOUT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -609,7 +608,8 @@ void finish_args(RopeArgs& A, const tria_rope* rope, int type, bool cache) {
     A.part[i].groups = (A.part[i].heads + hpw - 1) / hpw;
     A.groups += A.part[i].groups;
   }
-  // two stages a warp and the keys' buffers fill shared memory
+  // a warp's stages and, behind those of an append, the keys' buffer fill its share of shared
+  // memory (a rotation leaves the buffer's room free)
   const int room = (kRopeSmem / kRopeWarps - hpw * (A.hd + 4) * (int)sizeof(float)) & ~15;
   A.per_warp = std::min(room / rope_stages(cache) / group_bytes, A.groups);
   A.stage = A.per_warp * group_bytes;
@@ -816,7 +816,6 @@ extern "C" tria_status tria_append_qkv(const tria_rope* rope, const tria_layer_c
   A.n_before = n_before;
   A.ctrl = (Ctrl*)ws;
   A.n_seqs = cache->n_seqs;
-  A.n_kv = kv;
   A.k_type = cache->k_type;
   A.v_type = cache->v_type;
   for (int s = 0; s < cache->n_seqs; ++s) {

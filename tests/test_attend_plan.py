@@ -1,5 +1,6 @@
-"""The host arithmetic of an attention call (csrc/attend_plan.h), compiled by
-itself: the rows of the fp16 copies of quantised planes. No GPU."""
+"""The host arithmetic of rotation, append and attention (csrc/attend_plan.h),
+compiled by itself: the rows of the fp16 copies of quantised planes, grids and
+splits for a number of SMs. No GPU."""
 import os
 import shutil
 import subprocess
@@ -16,9 +17,17 @@ PROGRAM = r"""
 #include <vector>
 #include "attend_plan.h"
 // n_seqs n_kv group, capacities, token offsets -> rows, first rows
+// 0 sms units, cap_max, counters, tokens, groups, warps -> parts of a unit, CTAs of a rotation
 int main() {
   int n, kv, g;
   while (std::scanf("%d %d %d", &n, &kv, &g) == 3) {
+    if (n == 0) {
+      int cap_max, counters, groups, warps;
+      long long tokens;
+      if (std::scanf("%d %d %lld %d %d", &cap_max, &counters, &tokens, &groups, &warps) != 5) return 1;
+      std::printf("%d %d\n", tria::plain_split(g, cap_max, kv, counters), tria::rope_grid(tokens, groups, warps, kv));
+      continue;
+    }
     std::vector<int32_t> cap(n), tok0(n + 1);
     std::vector<int64_t> first(n, -1);
     for (int& c : cap) if (std::scanf("%d", &c) != 1) return 1;
@@ -89,3 +98,16 @@ def test_the_workspace_holds_the_widened_rows(plan, kv, group, cap, tokens, k_ty
         from kv_cache_eviction_tria_gb300 import _build
         _build.build()
     assert size(k_type, v_type) - size("f16", "f16") == planes * ((rows * hd * 2 + 255) // 256 * 256)
+
+
+@pytest.mark.parametrize("sms", [1, 38, 76, 152, 400])
+def test_splits_and_grids_follow_the_sms(plan, sms):
+    """Whatever the part of a GPU: units that are split are no more than their counters, the parts of a unit fill three
+    CTAs per SM where the rows allow it, a rotation is one wave."""
+    asked = [(u, cap, tok, g) for u in (0, 1, 7, 455, 456, 1024, 1025, 10 ** 6) for cap in (0, 100, 128, 129, 1 << 20)
+             for tok, g in ((1, 1), (8191, 20), (0, 1))]
+    got = plan("".join(f"0 {sms} {u} {cap} 1024 {tok} {g} 16\n" for u, cap, tok, g in asked))
+    for (u, cap, tok, g), (split, grid) in zip(asked, got):
+        assert 1 <= split <= 64 and (split == 1 or (u <= 1024 and (split - 1) * 128 < cap and u * (split - 1) < 3 * sms))
+        assert split == 64 or u > 1024 or u == 0 or u * split >= 3 * sms or split * 128 >= cap
+        assert 1 <= grid <= sms and (grid == sms or grid * 16 >= tok * g)
