@@ -12,10 +12,11 @@
 // of a KV head's group), as many as the small products have, are a decode step:
 // a stream over the rows, bound by memory (attend_step.cuh). More are a prompt:
 // products of 128-row tiles on the fifth-generation tensor cores
-// (attend_prompt.cu). 4 tokens x 4 heads take 214 us as a step and 240 us as a
-// prompt over 8 sequences of 32768 fp16 rows, 126 and 518 us over q4_0 rows
-// (which a prompt widens first), 52 and 88 us over one sequence, 25 us either
-// way over 777 rows.
+// (attend_prompt.cu). 4 tokens x 4 heads take 216 us as a step and 242 us as a
+// prompt over 8 sequences of 32768 fp16 rows, 54 and 90 us over one of them, 25 and
+// 27 us over 777 rows. Over q4_0 rows, which a prompt widens to fp16 first, they take
+// 126 and 795 us (567 us with round_keys), 42 and 194 us over one sequence: there a
+// step of more columns would win by far, but it is not built.
 //
 // The fp32 kernel (k_attend_plain) takes fp32 queries or fp32 planes of the
 // cache, where results are held to fp32 accuracy, and the head_dims that the
@@ -25,8 +26,8 @@
 // piece, and queries and sums stay in registers; the 32 products of a batch
 // (rows x columns) are summed over the lanes by 31 exchanges that leave each
 // lane with one logit. The next keys are asked for while a batch is computed.
-// About 75 instructions a row bind it: 8 sequences of 32768 fp32 rows (head_dim
-// 128, 4 query heads per KV head) take 502 us, 3.4 TB/s; 1024 tokens over their
+// About 75 instructions a row bind it: 8 sequences, 206246 fp32 rows (head_dim
+// 128, 4 query heads per KV head) take 500 us, 3.4 TB/s; 1024 tokens over their
 // own rows 488 us, 18 TFLOP/s. (With tiles in shared memory and a lane per row,
 // nine reads of shared memory to eight FMAs, they took 6260 and 2707 us.)
 #include <math.h>

@@ -34,7 +34,7 @@
 // bits at most, all above 2^-24. lse is given out in fp32 and would show the keys'
 // rounding (2e-3 at 230, 1e-5 with the remainders), which the output's own type
 // hides: a caller who takes it (round_keys) saves the remainders. 3162 tokens in two
-// chunks over 27081 rows take 975 us with them, 623 us without. Converting the rows
+// chunks over 27081 rows take 975 us with them, 640 us without. Converting the rows
 // tile by tile on their way into shared memory, which the products' operands
 // already fill to its rate and where each row would be converted again for every
 // 256 columns, held a pair of tiles at 2.3 (q4_0) and 3.2 us (q8_0) instead of 1.7.
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
   // wait for themselves may learn different things near a limit, so none of them
   // leaves: the softmax and the loading warps run their loops to the end, past waits
   // that return at once, and a warp's lanes meet at every collective instruction.
-  // (With votes at each of their waits a prompt of 8192 tokens took 530 us, 469 so.)
+  // (With votes at each of their waits a prompt of 8192 tokens took 530 us instead of 463.)
   auto wait = [&](uint64_t* b, uint32_t parity) {
     for (int it = 0; it < kWaitLimit; ++it)
       if (mbar_try_wait(b, parity) || *s_abort) return;
