@@ -724,6 +724,105 @@ size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_hea
 tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* attention, void* ws, size_t ws_bytes,
                         void* stream);
 
+/* ---- Several continuations of one prompt --------------------------------
+ * Sequences that branch from a shared prompt (beam search, several answers to
+ * one question) hold the prompt's rows once, in a cache of their own (the
+ * prefix), and each only the rows behind it:
+ *   tria_append_qkv     the new tokens' rows into each sequence's own cache
+ *   tria_attend_prefix  the new tokens' attention over the prefix, whose rows
+ *                       are read once for all its sequences, and over their own
+ *   tria_beam_select    the best continuations of every group of beams
+ *   tria_reorder        the own rows follow the chosen parents, in every layer
+ * Passes (tria_evict) may run on either cache. Sequences of a prefix or group
+ * are consecutive: those of group i are seq0[i] .. seq0[i + 1] - 1 (host int32
+ * [n_groups + 1], seq0[0] = 0, not descending, ending with the number of
+ * sequences; a group may have none). */
+
+/* Workspace bytes of tria_attend_prefix (0 on invalid input). The notes at
+ * tria_attend_workspace_size hold; one that is large enough for each serves
+ * calls of both. */
+size_t tria_attend_prefix_workspace_size(const tria_layer_cache* prefix, const tria_layer_cache* cache,
+                                         const int32_t* seq0, int32_t n_q_heads, const int32_t* tok0);
+
+/* tria_attend of new tokens over the rows of their sequence's prefix and the
+ * sequence's own rows, as one softmax: a token of a sequence of group i sees
+ * row r of prefix sequence i when r < n_live, pos[r] <= p and, with a window,
+ * p - pos[r] < window or r < sink; and row r of its own sequence when r <
+ * n_live, pos[r] <= p and, with a window, p - pos[r] < window (the sink's rows
+ * are the prefix's). prefix->n_seqs groups; the same n_kv_heads and head_dim in
+ * both caches (INVALID_ARG otherwise), the plane types may differ. Positions
+ * ascend strictly with the rows of a segment of each cache. Everything else,
+ * roundings and errors too, as tria_attend: the two results are joined in fp32
+ * by their log-sum-exps. A token whose prefix or sequence has a bad n_live gets
+ * no outputs. ws is not shared with calls that overlap on the GPU. */
+tria_status tria_attend_prefix(const tria_layer_cache* prefix, const tria_layer_cache* cache, const int32_t* seq0,
+                               const tria_attention* attention, void* ws, size_t ws_bytes, void* stream);
+
+#define TRIA_MAX_BEAMS 32      /* sequences of a group (tria_beam_select, tria_reorder) */
+#define TRIA_MAX_CHOICES 64    /* continuations of a group */
+#define TRIA_MAX_VOCAB 524288
+
+/* One step of beam search over n_groups groups of beams, as seq0 above, with
+ * at most TRIA_MAX_SEQS beams and TRIA_MAX_BEAMS of a group, one at least. */
+typedef struct tria_beams {
+  tria_dtype type;            /* F32, F16 or BF16: logits */
+  int32_t n_groups;
+  const int32_t* seq0;        /* host [n_groups + 1] */
+  int32_t vocab;              /* 1 .. TRIA_MAX_VOCAB */
+  int32_t n_out;              /* continuations of a group: 1 .. min(TRIA_MAX_CHOICES, beams * vocab) */
+  const void* logits;         /* device: beam b's row at logits + b * stride values, aligned to a value */
+  int64_t stride;             /* >= vocab */
+  const float* total;         /* device [beams] running log-probability of each beam */
+  const int32_t* ended;       /* optional device [beams]: not zero where a beam is over */
+  int32_t end_token;          /* its only continuation; -1: no token ends a beam (ended must be NULL) */
+  int32_t in_place;           /* 1: every surviving beam's best continuation takes the beam's own place */
+  float* total_out;           /* device [n_groups][n_out] */
+  int32_t* parent_out;        /* device [n_groups][n_out] */
+  int32_t* token_out;         /* device [n_groups][n_out] */
+  int32_t* ended_out;         /* optional device [n_groups][n_out] */
+} tria_beams;
+
+/* Workspace bytes (0 on invalid input), zeroed once (tria_workspace_init). */
+size_t tria_beam_select_workspace_size(const int32_t* seq0, int32_t n_groups, int32_t vocab, int32_t n_out);
+
+/* The n_out best continuations of every group, in one kernel. Continuation
+ * (b, t) of beam b by token t has
+ *   v(b, t) = total[b] + logits[b][t] - ln sum_u exp(logits[b][u])
+ * or, of a beam that is over, total[b] at t = end_token and -inf elsewhere.
+ * Every continuation of a beam whose total is not finite, or whose logits
+ * hold a NaN or +inf or are all -inf, is worth -inf. They are ordered by v,
+ * compared in 64 bits (exponentials and their sums within 32-bit roundings), equal
+ * ones by beam, then token. total_out: v rounded to fp32; parent_out: b (index
+ * among all beams of the call); token_out: t; ended_out: 1 when t = end_token or
+ * the beam was over. They lie best first or, with in_place (every group then
+ * has n_out beams), so that each parent's best one is in the parent's own place
+ * and the others, best first, in the places left over: tria_reorder then
+ * moves no beam that goes on. total_out may be total, and ended_out ended,
+ * where every group has n_out beams; no other overlaps of outputs with inputs
+ * or with one another. Host errors: INVALID_ARG, UNSUPPORTED (type, vocab,
+ * n_out, beams), WORKSPACE. */
+tria_status tria_beam_select(const tria_beams* beams, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of tria_reorder (0 on invalid input); a workspace of the pass
+ * or of attention serves too. */
+size_t tria_reorder_workspace_size(const tria_layer_cache* caches, int32_t n_layers, const int32_t* seq0, int32_t n_groups);
+
+/* Sequences take the rows of their parents, in place and in every layer:
+ * sequence s gets the live rows (keys, values, scales, positions) and n_live
+ * that sequence parent[s] had before the call. parent: device int32 [n_seqs],
+ * an index among the call's sequences, of the same group (tria_beam_select's
+ * parent_out where every group has n_out beams); any map, one parent for several
+ * sequences and rings too. caches: host array of n_layers (1 .. 128) layers
+ * with the same sequences, n_kv_heads, head_dim and types, each with planes and
+ * n_live of its own (as tria_evict_model; INVALID_ARG when two share one).
+ * Rows at or past the new n_live keep what they held. At most
+ * TRIA_MAX_BEAMS sequences a group (UNSUPPORTED). Device errors
+ * (tria_device_status), of which each leaves the group unchanged in that layer:
+ * DEVICE_ARG (a parent outside the group, a sequence's n_live outside [0,
+ * capacity]), CAPACITY (a parent's rows do not fit). */
+tria_status tria_reorder(const tria_layer_cache* caches, int32_t n_layers, const int32_t* seq0, int32_t n_groups,
+                         const int32_t* parent, void* ws, size_t ws_bytes, void* stream);
+
 const char* tria_status_string(tria_status status);
 int32_t tria_version(void);
 

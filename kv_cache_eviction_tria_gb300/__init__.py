@@ -45,7 +45,8 @@ EXPORTS = (
     "tria_shared_combine", "tria_shared_select",
     "tria_status_string", "tria_version", "tria_workspace_score_offset",
     "tria_rope_frequencies", "tria_load_rope", "tria_free_rope", "tria_rotate", "tria_append_qkv",
-    "tria_attend_workspace_size", "tria_attend",
+    "tria_attend_workspace_size", "tria_attend", "tria_attend_prefix_workspace_size", "tria_attend_prefix",
+    "tria_beam_select_workspace_size", "tria_beam_select", "tria_reorder_workspace_size", "tria_reorder",
 )
 
 
@@ -137,6 +138,15 @@ class _Attention(ctypes.Structure):
         ("lse", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("pos", ctypes.c_void_p),
         ("tok0", ctypes.c_void_p), ("scale", ctypes.c_double), ("window", ctypes.c_int32), ("sink", ctypes.c_int32),
         ("round_keys", ctypes.c_int32), ("pad", ctypes.c_int32),
+    ]
+
+
+class _Beams(ctypes.Structure):
+    _fields_ = [
+        ("type", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("seq0", ctypes.c_void_p), ("vocab", ctypes.c_int32),
+        ("n_out", ctypes.c_int32), ("logits", ctypes.c_void_p), ("stride", ctypes.c_int64), ("total", ctypes.c_void_p),
+        ("ended", ctypes.c_void_p), ("end_token", ctypes.c_int32), ("in_place", ctypes.c_int32), ("total_out", ctypes.c_void_p),
+        ("parent_out", ctypes.c_void_p), ("token_out", ctypes.c_void_p), ("ended_out", ctypes.c_void_p),
     ]
 
 
@@ -239,6 +249,19 @@ def load_library(path: str | None = None):
     lib.tria_attend_workspace_size.restype = sz
     lib.tria_attend.argtypes = [ctypes.POINTER(_LayerCache), ctypes.POINTER(_Attention), vp, sz, vp]
     lib.tria_attend.restype = i32
+    cache_p = ctypes.POINTER(_LayerCache)
+    lib.tria_attend_prefix_workspace_size.argtypes = [cache_p, cache_p, vp, i32, vp]
+    lib.tria_attend_prefix_workspace_size.restype = sz
+    lib.tria_attend_prefix.argtypes = [cache_p, cache_p, vp, ctypes.POINTER(_Attention), vp, sz, vp]
+    lib.tria_attend_prefix.restype = i32
+    lib.tria_beam_select_workspace_size.argtypes = [vp, i32, i32, i32]
+    lib.tria_beam_select_workspace_size.restype = sz
+    lib.tria_beam_select.argtypes = [ctypes.POINTER(_Beams), vp, sz, vp]
+    lib.tria_beam_select.restype = i32
+    lib.tria_reorder_workspace_size.argtypes = [cache_p, i32, vp, i32]
+    lib.tria_reorder_workspace_size.restype = sz
+    lib.tria_reorder.argtypes = [cache_p, i32, vp, i32, vp, vp, sz, vp]
+    lib.tria_reorder.restype = i32
     lib.tria_status_string.argtypes = [i32]
     lib.tria_status_string.restype = ctypes.c_char_p
     lib.tria_workspace_score_offset.argtypes = [ctypes.POINTER(_LayerCache)]
@@ -718,12 +741,16 @@ class Rope:
 _ACT, _INT32 = {}, ()       # torch's types, filled at the first call
 
 
-def _act_type(t) -> int:
+def _fill_types():
     global _INT32
+    import torch
+    _ACT.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    _INT32 = (torch.int32,)
+
+
+def _act_type(t) -> int:
     if not _ACT:
-        import torch
-        _ACT.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
-        _INT32 = (torch.int32,)
+        _fill_types()
     kind = _ACT.get(t.dtype)
     if kind is None:
         raise ValueError("activations must be float32, float16 or bfloat16")
@@ -840,17 +867,13 @@ def attend_workspace_size(cache: LayerCache, n_q_heads: int, tok0) -> int:
     return n
 
 
-def attend(cache: LayerCache, q, out, pos, *, ws, tok0=None, lse=None, scale: float = 0.0, window: int = 0, sink: int = 0,
-           round_keys: bool = False, stream=None):
-    """tria_attend: attention of new tokens over the cache. q / out [tokens][n_q_heads][head_dim], pos int32
-    [tokens], tok0 host offsets of the sequences' tokens (None: equally many each), lse float32
-    [tokens][n_q_heads] or None; scale 0: 1 / sqrt(head_dim); window 0: none; sink first rows stay visible;
-    round_keys: prompts over quantised keys take them rounded to fp16 (faster), in out and in lse."""
-    n, hd, n_seqs = pos.numel(), cache.head_dim, len(cache.seq_row0)
+def _attention(q, out, pos, lse, head_dim: int, n_seqs: int, tok0, scale, window, sink, round_keys):
+    """(tria_attention, what it points to on the host)."""
+    n = pos.numel()
     a = _Attention()
     a.type, a.n_q_heads = _act_type(q), q.shape[1]
-    a.q, a.q_stride = _rows3(q, "q", n, hd)
-    a.out, a.out_stride = _rows3(out, "out", n, hd, q.dtype)
+    a.q, a.q_stride = _rows3(q, "q", n, head_dim)
+    a.out, a.out_stride = _rows3(out, "out", n, head_dim, q.dtype)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     a.lse = _vec32(lse, n * q.shape[1], "lse")
@@ -858,10 +881,135 @@ def attend(cache: LayerCache, q, out, pos, *, ws, tok0=None, lse=None, scale: fl
     tok0 = _tokens0(tok0, n_seqs, n)
     a.tok0, a.scale, a.window, a.sink = tok0.ctypes.data, float(scale), int(window), int(sink)
     a.round_keys = int(round_keys)
+    return a, tok0
+
+
+def attend(cache: LayerCache, q, out, pos, *, ws, tok0=None, lse=None, scale: float = 0.0, window: int = 0, sink: int = 0,
+           round_keys: bool = False, stream=None):
+    """tria_attend: attention of new tokens over the cache. q / out [tokens][n_q_heads][head_dim], pos int32
+    [tokens], tok0 host offsets of the sequences' tokens (None: equally many each), lse float32
+    [tokens][n_q_heads] or None; scale 0: 1 / sqrt(head_dim); window 0: none; sink first rows stay visible;
+    round_keys: prompts over quantised keys take them rounded to fp16 (faster), in out and in lse."""
+    a, _keep = _attention(q, out, pos, lse, cache.head_dim, len(cache.seq_row0), tok0, scale, window, sink, round_keys)
     wp, wb = _ws(ws)
     st = load_library().tria_attend(cache.c_ref(), ctypes.byref(a), wp, wb, _stream_handle(stream))
     if st:
         _check(st, "tria_attend")
+
+
+# --------------------------------------------------------------------------- several continuations of one prompt
+
+def _groups(seq0, n_seqs: int, n_groups: int | None = None):
+    """Host offsets of the groups' sequences; None: one group, or equally many sequences in each of n_groups."""
+    if seq0 is None:
+        g = 1 if n_groups is None else n_groups
+        if g < 1 or n_seqs % g:
+            raise ValueError("seq0 is needed when the groups' sequences differ")
+        return np.arange(g + 1, dtype=np.int32) * (n_seqs // g)
+    if not (isinstance(seq0, np.ndarray) and seq0.dtype == np.int32 and seq0.flags.c_contiguous):
+        seq0 = np.ascontiguousarray(np.asarray(seq0, dtype=np.int32))
+    if seq0.ndim != 1 or len(seq0) < 2 or seq0[-1] != n_seqs or (n_groups is not None and len(seq0) != n_groups + 1):
+        raise ValueError("seq0 must hold the groups' first sequences and, last, the number of sequences")
+    return seq0
+
+
+def attend_prefix_workspace_size(prefix: LayerCache, cache: LayerCache, n_q_heads: int, tok0, seq0=None) -> int:
+    """tria_attend_prefix_workspace_size: tok0 host offsets of the sequences' tokens, or the tokens of every sequence."""
+    n_seqs = len(cache.seq_row0)
+    if np.ndim(tok0) == 0:
+        tok0 = np.arange(n_seqs + 1, dtype=np.int32) * int(tok0)
+    tok0 = _tokens0(tok0, n_seqs, int(tok0[-1]))
+    seq0 = _groups(seq0, n_seqs, len(prefix.seq_row0))
+    n = load_library().tria_attend_prefix_workspace_size(prefix.c_ref(), cache.c_ref(), seq0.ctypes.data, n_q_heads, tok0.ctypes.data)
+    if n == 0:
+        raise TriaError(ERR_INVALID_ARG, "tria_attend_prefix_workspace_size")
+    return n
+
+
+def attend_prefix(prefix: LayerCache, cache: LayerCache, q, out, pos, *, ws, seq0=None, tok0=None, lse=None, scale: float = 0.0,
+                  window: int = 0, sink: int = 0, round_keys: bool = False, stream=None):
+    """tria_attend_prefix: attention of new tokens over the rows of their sequence's prefix, held once for the sequences
+    seq0[i] .. seq0[i + 1] - 1 that continue prefix i (host offsets; None: equally many each), and over the sequence's
+    own rows in cache. The other arguments as attend; sink: first rows of the prefix."""
+    a, _keep = _attention(q, out, pos, lse, cache.head_dim, len(cache.seq_row0), tok0, scale, window, sink, round_keys)
+    seq0 = _groups(seq0, len(cache.seq_row0), len(prefix.seq_row0))
+    wp, wb = _ws(ws)
+    st = load_library().tria_attend_prefix(prefix.c_ref(), cache.c_ref(), seq0.ctypes.data, ctypes.byref(a), wp, wb, _stream_handle(stream))
+    if st:
+        _check(st, "tria_attend_prefix")
+
+
+def beam_select_workspace_size(seq0, vocab: int, n_out: int) -> int:
+    """tria_beam_select_workspace_size: seq0 host offsets of the groups' beams."""
+    seq0 = np.ascontiguousarray(np.asarray(seq0, dtype=np.int32))
+    n = load_library().tria_beam_select_workspace_size(seq0.ctypes.data, len(seq0) - 1, vocab, n_out)
+    if n == 0:
+        raise TriaError(ERR_INVALID_ARG, "tria_beam_select_workspace_size")
+    return n
+
+
+def beam_select(logits, total, total_out, parent, token, *, ws, seq0=None, ended=None, ended_out=None, end_token: int = -1,
+                in_place: bool = False, stream=None):
+    """tria_beam_select: the best continuations of groups of beams. logits [beams][vocab] (float32, float16 or bfloat16,
+    a row's values consecutive), total float32 [beams]; total_out float32, parent and token int32 [groups][n_out];
+    seq0 host offsets of the groups' beams (None: equally many each); ended / ended_out int32 [beams] / [groups][n_out]
+    or None. in_place: every surviving beam's best continuation in the beam's own place."""
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor [beams][vocab], a row's values consecutive")
+    if parent.dim() != 2:
+        raise ValueError("parent must be [groups][n_out]")
+    n, vocab = logits.shape
+    n_groups, n_out = parent.shape
+    b = _Beams()
+    b.type, b.n_groups, b.vocab, b.n_out = _act_type(logits), n_groups, vocab, n_out
+    seq0 = _groups(seq0, n, n_groups)
+    b.seq0 = seq0.ctypes.data
+    b.logits, b.stride = logits.data_ptr(), logits.stride(0) if n > 1 else max(logits.stride(0), vocab)
+    b.total, b.total_out = _vec32(total, n, "total"), _vec32(total_out, n_groups * n_out, "total_out")
+    for name, t, field, count in (("parent", parent, "parent_out", n_groups * n_out), ("token", token, "token_out", n_groups * n_out),
+                                  ("ended", ended, "ended", n), ("ended_out", ended_out, "ended_out", n_groups * n_out)):
+        if t is not None:
+            if t.numel() != count or t.dtype not in _INT32 or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {count} values")
+            setattr(b, field, t.data_ptr())
+    b.end_token, b.in_place = int(end_token), int(in_place)
+    wp, wb = _ws(ws)
+    st = load_library().tria_beam_select(ctypes.byref(b), wp, wb, _stream_handle(stream))
+    if st:
+        _check(st, "tria_beam_select")
+
+
+def _layers(caches):
+    if not caches:
+        raise ValueError("at least one layer")
+    return (_LayerCache * len(caches))(*[c.c_ref()._obj for c in caches])
+
+
+def reorder_workspace_size(caches, seq0=None) -> int:
+    """tria_reorder_workspace_size."""
+    structs = _layers(caches)
+    seq0 = _groups(seq0, len(caches[0].seq_row0))
+    n = load_library().tria_reorder_workspace_size(structs, len(caches), seq0.ctypes.data, len(seq0) - 1)
+    if n == 0:
+        raise TriaError(ERR_INVALID_ARG, "tria_reorder_workspace_size")
+    return n
+
+
+def reorder(caches, parent, *, ws, seq0=None, stream=None):
+    """tria_reorder: in every layer (caches: one LayerCache each), sequence s takes the live rows and n_live of sequence
+    parent[s] (int32 CUDA tensor, one per sequence) of its group; seq0 host offsets of the groups' sequences (None: all
+    sequences are one group)."""
+    structs = _layers(caches)
+    n_seqs = len(caches[0].seq_row0)
+    seq0 = _groups(seq0, n_seqs)
+    if not _ACT:
+        _fill_types()
+    if parent.numel() != n_seqs or parent.dtype not in _INT32 or not parent.is_contiguous() or not parent.is_cuda:
+        raise ValueError(f"parent must be a contiguous int32 CUDA tensor of {n_seqs} sequences")
+    wp, wb = _ws(ws)
+    st = load_library().tria_reorder(structs, len(caches), seq0.ctypes.data, len(seq0) - 1, parent.data_ptr(), wp, wb, _stream_handle(stream))
+    if st:
+        _check(st, "tria_reorder")
 
 
 # --------------------------------------------------------------------------- decode-loop lifecycle

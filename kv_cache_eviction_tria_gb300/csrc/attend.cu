@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kPlainWarps * 32) k_attend_plain(const __grid_
   }
   auto write = [&](int c, int e, float val, float top, float sum) {
     const int col = c0 + c, tok = S.tok0 + col / A.G, head = g * A.G + col % A.G;
-    act_store(A.out, A.type, (int64_t)tok * A.out_stride + (int64_t)head * hd + e, sum > 0.f || sum != sum ? val / sum : 0.f);
+    act_store(A.out, A.out_type, (int64_t)tok * A.out_stride + (int64_t)head * hd + e, sum > 0.f || sum != sum ? val / sum : 0.f);
     if (e == 0 && A.lse) A.lse[(int64_t)tok * A.nq + head] = top + logf(sum);
   };
   if (A.split == 1) {
@@ -351,13 +351,8 @@ cudaError_t launch_attend_span(const AttendArgs& A, int32_t* span, cudaStream_t 
   return cudaGetLastError();
 }
 
-}  // namespace tria
-
-using namespace tria;
-
 namespace {
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Which kernel a sequence of t tokens takes.
@@ -380,17 +375,6 @@ int path_of(bool tensor, int hd, int t, int G) {
   return step_dims(hd) ? kPathStep : kPathPlain;
 }
 
-// The kernels of a call run one after the other and share the arrival counters
-// and the space of the partial results. The layout covers every type of
-// queries. The counters, which have to be zero between calls, take the same
-// place for every shape, so that a workspace may serve calls of different
-// shapes: a decode step counts segments, the fp32 kernel the units that it
-// splits, at most kMaxSegments both.
-struct AttendLayout {
-  size_t count, span, part, wide_k, wide_kl, wide_v, total;
-  int split, prompt_split, sms;
-};
-
 // Parts of a unit of a prompt: as many as make the last wave of CTAs (one per
 // SM) full, each part costing a share of a fixed start and of the merge; none
 // under 512 rows of the capacity.
@@ -408,6 +392,8 @@ int prompt_split(int64_t units, int cap_max, int sms) {
   }
   return best;
 }
+
+}  // namespace
 
 AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0) {
   AttendLayout L{};
@@ -442,6 +428,8 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   return L;
 }
 
+namespace {
+
 cudaError_t launch_step(const AttendArgs& A, int cols, int workers, cudaStream_t st) {
   using Fn = cudaError_t (*)(const AttendArgs&, int, int, cudaStream_t);
   static constexpr Fn fn[3][3] = {
@@ -451,6 +439,8 @@ cudaError_t launch_step(const AttendArgs& A, int cols, int workers, cudaStream_t
   static_assert(TRIA_F16 == 1 && TRIA_Q8_0 == 2 && TRIA_Q4_0 == 3, "table order");
   return fn[A.k_type - 1][A.v_type - 1](A, cols, workers, st);
 }
+
+}  // namespace
 
 tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const int32_t* tok0) {
   tria_status r;
@@ -462,36 +452,33 @@ tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const i
   return (int64_t)tok0[c->n_seqs] * n_q_heads < ((int64_t)1 << 31) ? TRIA_OK : TRIA_ERR_UNSUPPORTED;
 }
 
-}  // namespace
-
-extern "C" size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0) {
-  if (check_attend_shape(cache, n_q_heads, tok0) != TRIA_OK) return 0;
-  return attend_layout(cache, n_q_heads / cache->n_kv_heads, tok0).total;
-}
-
-extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* a, void* ws, size_t ws_bytes,
-                                   void* stream) {
-  tria_status r;
-  if (!a) return TRIA_ERR_INVALID_ARG;
-  if ((r = check_attend_shape(cache, a->n_q_heads, a->tok0)) != TRIA_OK) return r;
+tria_status check_attention(const tria_attention* a, int n_tokens, int hd) {
   if (!act_ok(a->type)) return TRIA_ERR_UNSUPPORTED;
   if (a->window < 0 || a->sink < 0 || !(a->scale >= 0.0) || !isfinite((float)a->scale)) return TRIA_ERR_INVALID_ARG;
   if (a->round_keys != 0 && a->round_keys != 1) return TRIA_ERR_INVALID_ARG;
-  const int hd = cache->head_dim, nq = a->n_q_heads, n_tokens = a->tok0[cache->n_seqs];
-  const int size = a->type == TRIA_F32 ? 4 : 2;
-  if (n_tokens > 0) {
-    if (!a->q || !a->out || !a->pos || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->pos, 4) ||
-        (a->lse && !aligned(a->lse, 4)))
-      return TRIA_ERR_INVALID_ARG;
-    if (a->q_stride < (int64_t)nq * hd || a->out_stride < (int64_t)nq * hd || (a->q_stride * size) % 16 != 0 ||
-        (a->out_stride * size) % 16 != 0)
-      return TRIA_ERR_INVALID_ARG;
-  }
-  const int G = nq / cache->n_kv_heads;
-  const AttendLayout L = attend_layout(cache, G, a->tok0);
-  if (!ws || !aligned(ws, 256) || ws_bytes < L.total) return TRIA_ERR_WORKSPACE;
   if (n_tokens == 0) return TRIA_OK;
-  AttendArgs A;
+  const int size = a->type == TRIA_F32 ? 4 : 2;
+  const int64_t width = (int64_t)a->n_q_heads * hd;
+  auto aligned = [](const void* p, size_t to) { return (uintptr_t)p % to == 0; };
+  if (!a->q || !a->out || !a->pos || !aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->pos, 4) || (a->lse && !aligned(a->lse, 4)))
+    return TRIA_ERR_INVALID_ARG;
+  if (a->q_stride < width || a->out_stride < width || (a->q_stride * size) % 16 != 0 || (a->out_stride * size) % 16 != 0)
+    return TRIA_ERR_INVALID_ARG;
+  return TRIA_OK;
+}
+
+tria_status check_attend_rows(const tria_layer_cache* c, int G, const int32_t* tok0, int type) {
+  // a row of a TMA tile has a signed 32-bit coordinate
+  const bool tensor = tensor_types(c, type);
+  bool prompt = false;
+  for (int s = 0; s < c->n_seqs; ++s) prompt = prompt || path_of(tensor, c->head_dim, tok0[s + 1] - tok0[s], G) == kPathPrompt;
+  if (prompt)
+    for (int s = 0; s < c->n_seqs; ++s)
+      if (c->seq_row0[s] + (int64_t)c->n_kv_heads * c->capacity[s] >= ((int64_t)1 << 31)) return TRIA_ERR_UNSUPPORTED;
+  return TRIA_OK;
+}
+
+void fill_attend(AttendArgs& A, const tria_layer_cache* cache, const tria_attention* a) {
   memset(&A, 0, sizeof(A));
   A.q = a->q;
   A.out = a->out;
@@ -505,28 +492,33 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
   A.vs = (const uint8_t*)cache->v_scale;
   A.cpos = cache->pos;
   A.n_live = cache->n_live;
-  A.ctrl = (Ctrl*)ws;
-  A.count = (uint32_t*)((uint8_t*)ws + L.count);
-  A.part = (float*)((uint8_t*)ws + L.part);
   A.n_seqs = cache->n_seqs;
   A.n_kv = cache->n_kv_heads;
-  A.G = G;
-  A.hd = hd;
-  A.nq = nq;
-  A.type = a->type;
+  A.G = a->n_q_heads / cache->n_kv_heads;
+  A.hd = cache->head_dim;
+  A.nq = a->n_q_heads;
+  A.type = A.out_type = a->type;
   A.k_type = cache->k_type;
   A.v_type = cache->v_type;
   A.window = a->window;
   A.sink = a->sink;
-  A.scale = (float)(a->scale != 0.0 ? a->scale : 1.0 / sqrt((double)hd));
-  const bool tensor = tensor_types(cache, a->type);
-  int units = 0, cols = 0;
+  A.scale = (float)(a->scale != 0.0 ? a->scale : 1.0 / sqrt((double)cache->head_dim));
+}
+
+cudaError_t run_attend(AttendArgs& A, const tria_layer_cache* cache, const int32_t* tok0, bool round_keys, const AttendLayout& L, void* ws,
+                       cudaStream_t st) {
+  const int hd = A.hd, G = A.G;
+  A.ctrl = (Ctrl*)ws;
+  A.count = (uint32_t*)((uint8_t*)ws + L.count);
+  A.part = (float*)((uint8_t*)ws + L.part);
+  const bool tensor = tensor_types(cache, A.type);
+  int cols = 0;
   bool plain = false, step = false, prompt = false;
   for (int s = 0; s < cache->n_seqs; ++s) {
     A.seq[s].row0 = cache->seq_row0[s];
     A.seq[s].cap = cache->capacity[s];
-    A.seq[s].tok0 = a->tok0[s];
-    const int t = a->tok0[s + 1] - a->tok0[s], path = path_of(tensor, hd, t, G);
+    A.seq[s].tok0 = tok0[s];
+    const int t = tok0[s + 1] - tok0[s], path = path_of(tensor, hd, t, G);
     plain = plain || path == kPathPlain;
     prompt = prompt || path == kPathPrompt;
     if (path == kPathStep) {
@@ -534,48 +526,70 @@ extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_att
       cols = std::max(cols, t * G);
     }
   }
-  if (prompt)   // a row of a TMA tile has a signed 32-bit coordinate
-    for (int s = 0; s < cache->n_seqs; ++s)
-      if (cache->seq_row0[s] + (int64_t)cache->n_kv_heads * cache->capacity[s] >= ((int64_t)1 << 31)) return TRIA_ERR_UNSUPPORTED;
   // each kernel sees the sequences it takes, the others without tokens
   auto take = [&](int path) {
     const int per = path == kPathPrompt ? prompt_cols(hd) : kCols;
-    units = 0;
+    int units = 0;
     for (int s = 0; s < cache->n_seqs; ++s) {
-      const int t = a->tok0[s + 1] - a->tok0[s];
+      const int t = tok0[s + 1] - tok0[s];
       A.seq[s].t = path_of(tensor, hd, t, G) == path ? t : 0;
       A.seq[s].unit0 = units;
       units += (A.seq[s].t * G + per - 1) / per;
     }
     A.units = units;
   };
-  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
   if (step) {
     take(kPathStep);
     if (A.window > 0) {
       int32_t* span = (int32_t*)((uint8_t*)ws + L.span);
-      if (launch_attend_span(A, span, st) != cudaSuccess) return TRIA_ERR_CUDA;
+      if ((e = launch_attend_span(A, span, st)) != cudaSuccess) return e;
       A.span = span;
     }
-    if (launch_step(A, cols, L.sms, st) != cudaSuccess) return TRIA_ERR_CUDA;
+    if ((e = launch_step(A, cols, L.sms, st)) != cudaSuccess) return e;
   }
   if (prompt) {
     take(kPathPrompt);
     A.split = L.prompt_split;
     int64_t first[kMaxSeqs];
-    A.wide_rows = widened_rows(cache->n_seqs, cache->n_kv_heads, G, cache->capacity, a->tok0, first);
+    A.wide_rows = widened_rows(cache->n_seqs, cache->n_kv_heads, G, cache->capacity, tok0, first);
     for (int s = 0; s < cache->n_seqs; ++s) A.seq[s].wide0 = first[s];
     if (cache->k_type != TRIA_F16) {
       A.wide_k = (uint16_t*)((uint8_t*)ws + L.wide_k);
-      if (!a->round_keys) A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);
+      if (!round_keys) A.wide_kl = (uint16_t*)((uint8_t*)ws + L.wide_kl);
     }
     if (cache->v_type != TRIA_F16) A.wide_v = (uint16_t*)((uint8_t*)ws + L.wide_v);
-    if (launch_attend_prompt(A, st) != cudaSuccess) return TRIA_ERR_CUDA;
+    if ((e = launch_attend_prompt(A, st)) != cudaSuccess) return e;
   }
   if (plain) {
     take(kPathPlain);
     A.split = L.split;
-    if (launch_attend_plain(A, st) != cudaSuccess) return TRIA_ERR_CUDA;
+    if ((e = launch_attend_plain(A, st)) != cudaSuccess) return e;
   }
-  return TRIA_OK;
+  return cudaSuccess;
+}
+
+}  // namespace tria
+
+using namespace tria;
+
+extern "C" size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0) {
+  if (check_attend_shape(cache, n_q_heads, tok0) != TRIA_OK) return 0;
+  return attend_layout(cache, n_q_heads / cache->n_kv_heads, tok0).total;
+}
+
+extern "C" tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* a, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  tria_status r;
+  if (!a) return TRIA_ERR_INVALID_ARG;
+  if ((r = check_attend_shape(cache, a->n_q_heads, a->tok0)) != TRIA_OK) return r;
+  const int n_tokens = a->tok0[cache->n_seqs], G = a->n_q_heads / cache->n_kv_heads;
+  if ((r = check_attention(a, n_tokens, cache->head_dim)) != TRIA_OK) return r;
+  const AttendLayout L = attend_layout(cache, G, a->tok0);
+  if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < L.total) return TRIA_ERR_WORKSPACE;
+  if (n_tokens == 0) return TRIA_OK;
+  if ((r = check_attend_rows(cache, G, a->tok0, a->type)) != TRIA_OK) return r;
+  AttendArgs A;
+  fill_attend(A, cache, a);
+  return run_attend(A, cache, a->tok0, a->round_keys != 0, L, ws, (cudaStream_t)stream) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }

@@ -73,6 +73,7 @@ struct AttendArgs {
   const int32_t* span; // decode steps with a window: [sequence][KV head] {first, past the last} row that a token sees
   int32_t n_seqs, n_kv, G, hd, nq;
   int32_t type, k_type, v_type;
+  int32_t out_type;    // type, or F32 where results are joined with others
   int32_t window, sink;
   int32_t units;       // units of one KV head over all sequences
   int32_t split;       // parts a unit is cut into
@@ -80,7 +81,25 @@ struct AttendArgs {
   AttendSeq seq[kMaxSeqs];
 };
 
-// attend.cu
+// The kernels of a call run one after the other and share the arrival counters
+// and the space of the partial results. The layout covers every type of
+// queries. The counters, which have to be zero between calls, take the same
+// place for every shape, so that a workspace may serve calls of different
+// shapes: a decode step counts segments, the fp32 kernel the units that it
+// splits, at most kMaxSegments both.
+struct AttendLayout {
+  size_t count, span, part, wide_k, wide_kl, wide_v, total;
+  int split, prompt_split, sms;
+};
+
+// attend.cu: checks of a call, its layout and its kernels over one cache
+tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const int32_t* tok0);
+tria_status check_attention(const tria_attention* a, int n_tokens, int hd);
+tria_status check_attend_rows(const tria_layer_cache* c, int G, const int32_t* tok0, int type);
+AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0);
+void fill_attend(AttendArgs& A, const tria_layer_cache* cache, const tria_attention* a);
+cudaError_t run_attend(AttendArgs& A, const tria_layer_cache* cache, const int32_t* tok0, bool round_keys, const AttendLayout& L, void* ws,
+                       cudaStream_t st);
 cudaError_t launch_attend_plain(const AttendArgs& A, cudaStream_t st);
 cudaError_t launch_attend_span(const AttendArgs& A, int32_t* span, cudaStream_t st);
 // attend_step_*.cu: up to 16 columns (tokens x group) a sequence, one CTA per worker

@@ -775,6 +775,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
         if (split) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) slot[(int64_t)(2 + c + k) * (QT * 128)] = __uint_as_float(o[k]);
+        } else if (A.out_type == TRIA_F32) {               // results that are joined with others
+          if (on && c < A.hd) {
+            float4* to32 = reinterpret_cast<float4*>(reinterpret_cast<float*>(A.out) + tok * A.out_stride + (int64_t)head * A.hd + c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              to32[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv, __uint_as_float(o[4 * k + 2]) * inv,
+                                    __uint_as_float(o[4 * k + 3]) * inv);
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -786,7 +794,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attend_prompt(const __gri
           }
         }
       }
-      if (!split && on) {
+      if (!split && on && A.out_type != TRIA_F32) {
         fence_proxy_async_smem();
         bulk_s2g(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * A.hd, row_out, A.hd * 2);
         bulk_commit();
@@ -866,6 +874,13 @@ __global__ void __launch_bounds__(PromptShape<HD>::QT * 128) k_join_parts(const 
     for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(p[(2 + d0 + e) * kCols], f, v[e]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (d0 == 0 && A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  if (A.out_type == TRIA_F32) {
+    float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(A.out) + tok * A.out_stride + (int64_t)head * A.hd + d0);
+#pragma unroll
+    for (int q = 0; q < kJoinDims / 4; ++q) o[q] = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+    return;
+  }
   uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * A.hd + d0);
 #pragma unroll
   for (int q = 0; q < kJoinDims / 8; ++q) {
@@ -874,7 +889,6 @@ __global__ void __launch_bounds__(PromptShape<HD>::QT * 128) k_join_parts(const 
     for (int e = 0; e < 4; ++e) w[e] = pack_out(A.type, v[8 * q + 2 * e] * inv, v[8 * q + 2 * e + 1] * inv);
     o[q] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (d0 == 0 && A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ---- quantised planes as fp16 ------------------------------------------------

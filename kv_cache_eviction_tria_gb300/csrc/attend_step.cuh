@@ -702,8 +702,8 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
           const int64_t to = (int64_t)(S.tok0 + c2 / A.G) * A.out_stride + (int64_t)(g * A.G + c2 % A.G) * HD;
 #pragma unroll
           for (int i = 0; i < HD / 16; ++i) {
-            act_store(A.out, A.type, to + dim_of(i, 0), o[i][h][e] * f);
-            act_store(A.out, A.type, to + dim_of(i, 2), o[i][h][2 + e] * f);
+            act_store(A.out, A.out_type, to + dim_of(i, 0), o[i][h][e] * f);
+            act_store(A.out, A.out_type, to + dim_of(i, 2), o[i][h][2 + e] * f);
           }
         }
       }
@@ -739,8 +739,14 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
     const int s = unit / A.n_kv, head = (unit - s * A.n_kv) * A.G + col % A.G;
     const int64_t tok = A.seq[s].tok0 + col / A.G;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (d == 0 && A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    if (A.out_type == TRIA_F32) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(A.out) + tok * A.out_stride + (int64_t)head * HD + d) =
+          make_float4(val.x * inv, val.y * inv, val.z * inv, val.w * inv);
+      return;
+    }
     uint32_t w[2];
-    if (A.type == TRIA_F16) {
+    if (A.out_type == TRIA_F16) {
       w[0] = pack_h2(val.x * inv, val.y * inv);
       w[1] = pack_h2(val.z * inv, val.w * inv);
     } else {
@@ -749,7 +755,6 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
       w[1] = *reinterpret_cast<const uint32_t*>(&b);
     }
     *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(A.out) + tok * A.out_stride + (int64_t)head * HD + d) = make_uint2(w[0], w[1]);
-    if (d == 0 && A.lse) A.lse[tok * A.nq + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   };
   int open[2] = {-1, -1};                                  // units that reach into other CTAs: the first, the last
   for (int unit = unit_of(begin); unit < n_units && s_first[unit] < end; ++unit) {

@@ -1,0 +1,459 @@
+// The best continuations of groups of beams (tria_beam_select): one step of
+// beam search, from the logits to the chosen (beam, token) pairs.
+//
+//   v(b, t) = total_b + x_bt - ln sum_u exp(x_bu), the n_out largest of a group
+//
+// One pass over the logits: a CTA holds a piece of a beam's row in registers
+// and takes from it the largest logit, the sum of exponentials relative to it
+// and the piece's n_out best tokens (within a beam v orders like the logits,
+// so they are found before the sum is known). The last CTA of a group to
+// arrive adds the sums up and chooses among the pieces' lists; its CTAs write
+// 16 + 8 n_out bytes each, against 16 to 32 KB read.
+//
+// Choosing k of many: of 32 or 128 runs of threads' values (at least k), the
+// k-th largest of their best values is a bound that k values reach. The few
+// that do (about runs ln(runs / (runs - k)) of random ones) go to a list in
+// shared memory and are ranked by counting. Values are compared with their
+// index (the smaller one first), so that no two are equal: ties cost nothing
+// and the result does not depend on the order of arrival. Where more reach
+// the bound than the list holds (many large values on few threads), the best are
+// taken one after the other instead.
+//
+// Sums: exponentials (of differences from the largest logit, 2 units) and a
+// CTA's sum of 8192 in fp32, the sum of the pieces and v in fp64. A thread has
+// the same tokens of a row whatever its alignment, so equal rows have equal
+// sums, bit by bit, and equal candidates of two beams stay equal.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "attend_internal.cuh"
+
+namespace tria {
+
+namespace {
+
+constexpr int kSelThreads = 256, kHeld = 32;               // logits of a thread
+constexpr int kMaxOut = TRIA_MAX_CHOICES, kMaxBeams = TRIA_MAX_BEAMS;
+constexpr int kList = 1024;                                // candidates ranked by counting
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert((int64_t)kMaxBeams * TRIA_MAX_VOCAB < ((int64_t)1 << 32), "a continuation's index has 32 bits");
+
+struct Piece {
+  float top;            // largest logit
+  float sum;            // of 2^((x - top) log2 e)
+  uint32_t bad, pad;    // a NaN or +inf among them
+};
+
+struct BeamArgs {
+  const void* logits;
+  int64_t stride;
+  const float* total;
+  const int32_t* ended;
+  float* total_out;
+  int32_t* parent_out;
+  int32_t* token_out;
+  int32_t* ended_out;
+  uint32_t* count;      // [groups] arrivals, zero between calls
+  Piece* piece;         // [beams][pieces]
+  uint2* best;          // [beams][pieces][n_out] {ordered logit (0: none), token}, best first
+  int32_t vocab, n_out, n_groups, pieces, held, end_token, in_place, vec;
+  int32_t seq0[kMaxSeqs + 1];
+};
+
+// floats by size, -0 as 0 (no NaN): larger keys are larger floats, none is 0
+__device__ __forceinline__ uint32_t order32(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float from_order32(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
+__device__ __forceinline__ uint64_t order64(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double from_order64(uint64_t k) {
+  return __longlong_as_double((long long)((k >> 63) ? k ^ 0x8000000000000000ull : ~k));
+}
+
+// Candidate: key (0: none) and index; before(a, b): a is the better one.
+struct Cand {
+  uint64_t key;
+  uint32_t at;
+};
+__device__ __forceinline__ bool before(const Cand& a, const Cand& b) { return a.key > b.key || (a.key == b.key && a.at < b.at); }
+__device__ __forceinline__ Cand from_lane(const Cand& x, int o) {      // of the lane whose number differs in bit o
+  return {__shfl_xor_sync(0xffffffffu, x.key, o), __shfl_xor_sync(0xffffffffu, x.at, o)};
+}
+
+struct Choose {
+  Cand run[128];
+  Cand list[kList];
+  Cand out[kMaxOut];
+  Cand warp_best[kSelThreads / 32];
+  int n;
+};
+
+// The best `want` of the candidates that each(f) shows to f, thread by thread
+// and the same ones at every call, into C.out, best first; returns how many
+// there are (fewer when there are no more). `mine`: this thread's best one. All
+// threads of the CTA take part; C.n is 0 at the start.
+template <typename Each>
+__device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int runs = want <= 16 ? 32 : 128, of = kSelThreads / runs;      // of: threads of a run
+  for (int o = 1; o < of; o <<= 1) {
+    const Cand y = from_lane(mine, o);
+    if (before(y, mine)) mine = y;
+  }
+  if (tid % of == 0) C.run[tid / of] = mine;
+  __syncthreads();
+  // the want-th best run: every warp finds it for itself (runs without a candidate rank by their number)
+  Cand bound = {0, 0};
+  for (int i0 = 0; i0 < runs; i0 += 32) {
+    const Cand x = C.run[i0 + lane];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < runs; ++j) {
+      const Cand y = C.run[j];
+      rank += before(y, x) || (y.key == x.key && y.at == x.at && j < i0 + lane);
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, rank == want - 1);
+    if (hit) {
+      bound.key = __shfl_sync(0xffffffffu, x.key, __ffs(hit) - 1);
+      bound.at = __shfl_sync(0xffffffffu, x.at, __ffs(hit) - 1);
+    }
+  }
+  each([&](uint64_t key, uint32_t at) {
+    const Cand x = {key, at};
+    if (key == 0 || before(bound, x)) return;
+    const int i = atomicAdd(&C.n, 1);
+    if (i < kList) C.list[i] = x;
+  });
+  __syncthreads();
+  const int n = C.n;
+  if (n <= kList) {
+    for (int i = tid; i < n; i += kSelThreads) {
+      const Cand x = C.list[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += before(C.list[j], x);
+      if (rank < want) C.out[rank] = x;
+    }
+    __syncthreads();
+    return min(n, want);
+  }
+  Cand last = {~0ull, 0};                                  // every candidate comes after it
+  for (int k = 0; k < want; ++k) {
+    Cand top = {0, 0xFFFFFFFFu};
+    each([&](uint64_t key, uint32_t at) {
+      const Cand x = {key, at};
+      if (key != 0 && before(last, x) && before(x, top)) top = x;
+    });
+    for (int o = 1; o < 32; o <<= 1) {
+      const Cand y = from_lane(top, o);
+      if (before(y, top)) top = y;
+    }
+    if (lane == 0) C.warp_best[tid >> 5] = top;
+    __syncthreads();
+    top = C.warp_best[0];
+    for (int w = 1; w < kSelThreads / 32; ++w)
+      if (before(C.warp_best[w], top)) top = C.warp_best[w];
+    if (tid == 0) C.out[k] = top;
+    __syncthreads();
+    if (top.key == 0) return k;
+    last = top;
+  }
+  return want;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x) {
+  if constexpr (std::is_same_v<T, float>) return x;
+  else if constexpr (std::is_same_v<T, __half>) return __half2float(x);
+  else return __bfloat162float(x);
+}
+
+// kVec: rows start on 16-byte boundaries
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kSelThreads) k_beam_select(const __grid_constant__ BeamArgs A) {
+  constexpr int N = 16 / sizeof(T), V = kHeld / N;         // values of a load, loads of a thread
+  __shared__ Choose C;
+  __shared__ double s_base[kMaxBeams];
+  __shared__ float s_top[kSelThreads / 32];
+  __shared__ float s_sum[kSelThreads / 32];
+  __shared__ int s_bad, s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int beam = blockIdx.x / A.pieces, piece = blockIdx.x - beam * A.pieces;
+  const int first = piece * A.held * kSelThreads;
+  const bool over = A.ended && A.ended[beam] != 0;
+  if (tid == 0) {
+    C.n = 0;
+    s_bad = 0;
+  }
+  // ---- the piece: value e of load j of a thread is token first + (j * 256 + tid) * N + e
+  float x[kHeld];
+  const T* row = reinterpret_cast<const T*>(A.logits) + (int64_t)beam * A.stride;
+  auto token = [&](int i) { return first + ((i / N) * kSelThreads + tid) * N + i % N; };
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int t0 = token(j * N);
+    const bool on = j * N < A.held && !over;
+    if (kVec && on && t0 + N <= A.vocab) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + t0));
+      const T* y = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[j * N + e] = to_float(y[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[j * N + e] = on && t0 + e < A.vocab ? to_float(row[t0 + e]) : -INFINITY;
+    }
+  }
+  if (over) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i < A.held && token(i) == A.end_token) x[i] = 0.f;
+  }
+  // ---- largest logit, sum, the thread's best token (the first of equal ones)
+  bool bad = false;
+  float top = -INFINITY;
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    bad = bad || !(x[i] < INFINITY);
+    if (x[i] > top) {
+      top = x[i];
+      at = i;
+    }
+  }
+  auto candidate = [&](int i, float v) -> uint64_t {       // 0: no token
+    return i < A.held && token(i) < A.vocab ? (uint64_t)order32(v) : 0;
+  };
+  const Cand mine = {candidate(at, top), (uint32_t)token(at)};   // (all -inf: its first token)
+  float wtop = top;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
+  const float base = wtop == -INFINITY ? 0.f : wtop;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) sum += exp2f((x[i] - base) * kLog2e);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) {
+    s_top[warp] = wtop;
+    s_sum[warp] = sum;
+  }
+  __syncthreads();
+  if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
+  const int n = choose(C, A.n_out, mine, [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) f(candidate(i, x[i]), (uint32_t)token(i));
+  });
+  uint2* best = A.best + (int64_t)blockIdx.x * A.n_out;
+  for (int i = tid; i < A.n_out; i += kSelThreads) best[i] = i < n ? make_uint2((uint32_t)C.out[i].key, C.out[i].at) : make_uint2(0, 0);
+  if (warp == 0) {
+    const float t = lane < kSelThreads / 32 ? s_top[lane] : -INFINITY;
+    float all = t;
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+    float s = t > -INFINITY ? s_sum[lane] * exp2f((t - all) * kLog2e) : 0.f;
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) A.piece[blockIdx.x] = {all, s, (uint32_t)s_bad, 0u};
+  }
+  // ---- the last CTA of the group chooses among the pieces' lists
+  int group = 0, hi = A.n_groups - 1;
+  while (group < hi) {
+    const int mid = (group + hi + 1) >> 1;
+    if (A.seq0[mid] <= beam) group = mid; else hi = mid - 1;
+  }
+  const int b0 = A.seq0[group], beams = A.seq0[group + 1] - b0, lists = beams * A.pieces;
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    s_last = atomicAdd(&A.count[group], 1u) == (uint32_t)lists - 1;
+    __threadfence();
+    C.n = 0;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  for (int b = warp; b < beams; b += kSelThreads / 32) {
+    const Piece* p = A.piece + (int64_t)(b0 + b) * A.pieces;
+    float t = -INFINITY;
+    uint32_t junk = 0;
+    for (int i = lane; i < A.pieces; i += 32) {
+      t = fmaxf(t, __ldcg(&p[i].top));
+      junk |= __ldcg(&p[i].bad);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+    junk = __reduce_or_sync(0xffffffffu, junk);
+    double s = 0.0;
+    for (int i = lane; i < A.pieces; i += 32) {
+      const float pt = __ldcg(&p[i].top);
+      if (pt > -INFINITY) s += (double)__ldcg(&p[i].sum) * (double)exp2f((pt - t) * kLog2e);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) {
+      const float tot = A.total[b0 + b];
+      const bool gone = A.ended && A.ended[b0 + b] != 0;
+      // -inf: every continuation is worth that
+      s_base[b] = junk || t == -INFINITY || !(fabsf(tot) < INFINITY) ? -INFINITY
+                  : gone ? (double)tot : (double)tot - ((double)t + log(s));
+    }
+  }
+  __syncthreads();
+  // candidate c: place c / lists of list c % lists, so that the lists' best ones lie on different threads
+  const int n_cand = lists * A.n_out;
+  auto each = [&](auto f) {
+    for (int c = tid; c < n_cand; c += kSelThreads) {
+      const int r = c / lists, l = c - r * lists, b = l / A.pieces;
+      const double base_v = s_base[b];
+      uint2 e = __ldcg(A.best + ((int64_t)b0 * A.pieces + l) * A.n_out + r);
+      double v = -INFINITY;
+      if (base_v == -INFINITY) e = make_uint2(l == b * A.pieces && r < A.vocab, (uint32_t)r);   // its first tokens
+      else v = base_v + (double)from_order32(e.x);
+      f(e.x ? order64(v) : 0ull, (uint32_t)b * (uint32_t)A.vocab + e.y);
+    }
+  };
+  Cand own = {0, 0xFFFFFFFFu};
+  each([&](uint64_t key, uint32_t place) {
+    const Cand y = {key, place};
+    if (before(y, own)) own = y;
+  });
+  const int got = choose(C, A.n_out, own, each);
+  // ---- out: best first, or every parent's best one in the parent's place
+  int to = -1, parent = 0, tok = 0, end = 0;
+  float val = 0.f;
+  if (tid < got) {
+    const Cand y = C.out[tid];
+    parent = (int)(y.at / (uint32_t)A.vocab);
+    tok = (int)(y.at - (uint32_t)parent * (uint32_t)A.vocab);
+    val = (float)from_order64(y.key);
+    to = tid;
+    end = tok == A.end_token || (A.ended && A.ended[b0 + parent] != 0);
+  }
+  if (A.in_place && warp == 0) {                           // (n_out is the group's beams: a lane each)
+    const uint32_t same = __match_any_sync(0xffffffffu, to >= 0 ? parent : -1 - lane);
+    const bool stays = to >= 0 && (same & ((1u << lane) - 1u)) == 0;
+    const uint32_t taken = __reduce_or_sync(0xffffffffu, stays ? 1u << parent : 0u);
+    const uint32_t others = __ballot_sync(0xffffffffu, to >= 0 && !stays);
+    if (stays) to = parent;
+    else if (to >= 0) to = __fns(~taken, 0, __popc(others & ((1u << lane) - 1u)) + 1);
+  }
+  __syncthreads();                                         // total and ended, which may be the outputs, have been read
+  if (to >= 0) {
+    const int64_t o = (int64_t)group * A.n_out + to;
+    A.total_out[o] = val;
+    A.parent_out[o] = b0 + parent;
+    A.token_out[o] = tok;
+    if (A.ended_out) A.ended_out[o] = end;
+  }
+  if (tid == 0) A.count[group] = 0u;
+}
+
+template <typename T>
+void launch_beam_select(const BeamArgs& A, int grid, cudaStream_t st) {
+  if (A.vec) k_beam_select<T, true><<<grid, kSelThreads, 0, st>>>(A);
+  else k_beam_select<T, false><<<grid, kSelThreads, 0, st>>>(A);
+}
+
+// Logits of a thread: the most that still give every SM a CTA, so that a small
+// call is spread over the GPU and a large one has few lists.
+int held_of(int beams, int vocab) {
+  int held = kHeld;
+  while (held > 8 && (int64_t)beams * ((vocab + held * kSelThreads - 1) / (held * kSelThreads)) < sm_count()) held /= 2;
+  return held;
+}
+
+}  // namespace
+
+}  // namespace tria
+
+using namespace tria;
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+tria_status check_beams(const int32_t* seq0, int n_groups, int vocab, int n_out) {
+  if (!seq0 || n_groups < 1 || seq0[0] != 0 || vocab < 1 || n_out < 1) return TRIA_ERR_INVALID_ARG;
+  if (n_groups > kMaxSeqs || vocab > TRIA_MAX_VOCAB || n_out > TRIA_MAX_CHOICES) return TRIA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_groups; ++i) {
+    const int64_t n = (int64_t)seq0[i + 1] - seq0[i];
+    if (n < 1 || n_out > n * vocab) return TRIA_ERR_INVALID_ARG;
+    if (n > TRIA_MAX_BEAMS || seq0[i + 1] > kMaxSeqs) return TRIA_ERR_UNSUPPORTED;
+  }
+  return TRIA_OK;
+}
+
+struct BeamLayout {
+  size_t count, piece, best, total;
+  int held, pieces;
+};
+
+BeamLayout beam_layout(const int32_t* seq0, int n_groups, int vocab, int n_out) {
+  BeamLayout L{};
+  const int beams = seq0[n_groups];
+  L.held = held_of(beams, vocab);
+  L.pieces = (vocab + L.held * kSelThreads - 1) / (L.held * kSelThreads);
+  L.count = up256(sizeof(Ctrl));
+  L.piece = up256(L.count + sizeof(uint32_t) * kMaxSeqs);
+  L.best = up256(L.piece + sizeof(Piece) * (size_t)beams * L.pieces);
+  L.total = up256(L.best + sizeof(uint2) * (size_t)beams * L.pieces * n_out);
+  return L;
+}
+
+}  // namespace
+
+extern "C" size_t tria_beam_select_workspace_size(const int32_t* seq0, int32_t n_groups, int32_t vocab, int32_t n_out) {
+  return check_beams(seq0, n_groups, vocab, n_out) == TRIA_OK ? beam_layout(seq0, n_groups, vocab, n_out).total : 0;
+}
+
+extern "C" tria_status tria_beam_select(const tria_beams* b, void* ws, size_t ws_bytes, void* stream) {
+  tria_status r;
+  if (!b) return TRIA_ERR_INVALID_ARG;
+  if ((r = check_beams(b->seq0, b->n_groups, b->vocab, b->n_out)) != TRIA_OK) return r;
+  if (!act_ok(b->type)) return TRIA_ERR_UNSUPPORTED;
+  const int size = b->type == TRIA_F32 ? 4 : 2;
+  auto off = [](const void* p, int a) { return (uintptr_t)p % a != 0; };
+  if (!b->logits || !b->total || !b->total_out || !b->parent_out || !b->token_out || b->stride < b->vocab || off(b->logits, size) ||
+      off(b->total, 4) || off(b->ended, 4) || off(b->total_out, 4) || off(b->parent_out, 4) || off(b->token_out, 4) || off(b->ended_out, 4))
+    return TRIA_ERR_INVALID_ARG;
+  if (b->end_token < -1 || b->end_token >= b->vocab || (b->ended && b->end_token < 0) || (b->in_place != 0 && b->in_place != 1))
+    return TRIA_ERR_INVALID_ARG;
+  bool square = true;                                      // every group has n_out beams
+  for (int i = 0; i < b->n_groups; ++i) square = square && b->seq0[i + 1] - b->seq0[i] == b->n_out;
+  if (!square && (b->in_place || b->total_out == b->total || (b->ended_out && b->ended_out == b->ended))) return TRIA_ERR_INVALID_ARG;
+  const BeamLayout L = beam_layout(b->seq0, b->n_groups, b->vocab, b->n_out);
+  if (!ws || (uintptr_t)ws % 256 != 0 || ws_bytes < L.total) return TRIA_ERR_WORKSPACE;
+  BeamArgs A;
+  memset(&A, 0, sizeof(A));
+  A.logits = b->logits;
+  A.stride = b->stride;
+  A.total = b->total;
+  A.ended = b->ended;
+  A.total_out = b->total_out;
+  A.parent_out = b->parent_out;
+  A.token_out = b->token_out;
+  A.ended_out = b->ended_out;
+  A.count = (uint32_t*)((uint8_t*)ws + L.count);
+  A.piece = (Piece*)((uint8_t*)ws + L.piece);
+  A.best = (uint2*)((uint8_t*)ws + L.best);
+  A.vocab = b->vocab;
+  A.n_out = b->n_out;
+  A.n_groups = b->n_groups;
+  A.pieces = L.pieces;
+  A.held = L.held;
+  A.end_token = b->end_token;
+  A.in_place = b->in_place;
+  A.vec = (uintptr_t)b->logits % 16 == 0 && (b->stride * size) % 16 == 0;
+  memcpy(A.seq0, b->seq0, sizeof(int32_t) * (b->n_groups + 1));
+  const int grid = b->seq0[b->n_groups] * L.pieces;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (b->type == TRIA_F32) launch_beam_select<float>(A, grid, st);
+  else if (b->type == TRIA_F16) launch_beam_select<__half>(A, grid, st);
+  else launch_beam_select<__nv_bfloat16>(A, grid, st);
+  return cudaGetLastError() == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+}

@@ -49,7 +49,8 @@ struct Ctrl {
   uint32_t ready_count;  // segments whose selection is published (slots of the ready list)
   uint32_t move_cursor;  // first ready slot that may still have unclaimed move blocks
   uint32_t pass_done;    // CTAs of the pass that finished
-  uint32_t pad[49];
+  uint32_t reorder_ticket;  // reorder CTAs that finished (reset by the last one)
+  uint32_t pad[48];
 };
 static_assert(sizeof(Ctrl) == 256, "Ctrl layout");
 
