@@ -46,7 +46,7 @@ def maps(rng, n):
     yield np.arange(n)                                        # nobody moves
     yield np.zeros(n, int)                                    # one parent for all
     yield np.roll(np.arange(n), 1)                            # one ring
-    yield np.arange(n)[::-1]                                  # pairs change places
+    yield np.arange(n)[::-1].copy()                                # pairs change places
     yield np.maximum(np.arange(n) - 1, 0)                     # a chain
     yield rng.permutation(n)
     for _ in range(3):
