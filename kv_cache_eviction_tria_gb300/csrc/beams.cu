@@ -13,16 +13,18 @@
 // Choosing k of many: of 32 or 128 runs of threads' values (at least k), the
 // k-th largest of their best values is a bound that k values reach. The few
 // that do (about runs ln(runs / (runs - k)) of random ones) go to a list in
-// shared memory and are ranked by counting. Values are compared with their
-// index (the smaller one first), so that no two are equal: ties cost nothing
-// and the result does not depend on the order of arrival. Where more reach
-// the bound than the list holds (many large values on few threads), the best are
-// taken one after the other instead.
+// shared memory and are ranked by counting, with their index (the smaller one
+// first), so that no two are equal and the result does not depend on the order
+// of arrival. Where more reach the bound than the list holds, it is taken
+// again with the indices (ties: a masked vocabulary), and where that leaves too
+// many (large values on few threads) the best are taken one after the other.
+// The pieces' lists are sorted, so the last CTA bounds their first entries
+// and reads on in the few lists that reach that.
 //
-// Sums: exponentials (of differences from the largest logit, 2 units) and a
-// CTA's sum of 8192 in fp32, the sum of the pieces and v in fp64. A thread has
-// the same tokens of a row whatever its alignment, so equal rows have equal
-// sums, bit by bit, and equal candidates of two beams stay equal.
+// Sums: exponentials (of differences from the largest logit, 4 units of 2^-24)
+// and their sums in fp32, the logarithm and v in fp64. A thread has the same
+// tokens of a row whatever its alignment, so equal rows have equal sums, bit by
+// bit, and equal candidates of two beams stay equal.
 #include <math.h>
 #include <string.h>
 
@@ -41,12 +43,6 @@ constexpr int kList = 1024;                                // candidates ranked 
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert((int64_t)kMaxBeams * TRIA_MAX_VOCAB < ((int64_t)1 << 32), "a continuation's index has 32 bits");
 
-struct Piece {
-  float top;            // largest logit
-  float sum;            // of 2^((x - top) log2 e)
-  uint32_t bad, pad;    // a NaN or +inf among them
-};
-
 struct BeamArgs {
   const void* logits;
   int64_t stride;
@@ -57,9 +53,10 @@ struct BeamArgs {
   int32_t* token_out;
   int32_t* ended_out;
   uint32_t* count;      // [groups] arrivals, zero between calls
-  Piece* piece;         // [beams][pieces]
+  float2* piece;        // [beams][pieces] {largest logit, sum of 2^((x - it) log2 e): NaN where a logit is NaN or +inf}
   uint2* best;          // [beams][pieces][n_out] {ordered logit (0: none), token}, best first
-  int32_t vocab, n_out, n_groups, pieces, held, end_token, in_place, vec;
+  int32_t vocab, n_out, n_groups, pieces, held, end_token, in_place;
+  int32_t vec;          // rows start on 16-byte boundaries
   int32_t seq0[kMaxSeqs + 1];
 };
 
@@ -77,6 +74,12 @@ __device__ __forceinline__ double from_order64(uint64_t k) {
   return __longlong_as_double((long long)((k >> 63) ? k ^ 0x8000000000000000ull : ~k));
 }
 
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Candidate: key (0: none) and index; before(a, b): a is the better one.
 struct Cand {
   uint64_t key;
@@ -92,39 +95,60 @@ struct Choose {
   Cand list[kList];
   Cand out[kMaxOut];
   Cand warp_best[kSelThreads / 32];
-  int n;
+  float top[128];             // of runs of threads, as values alone
+  uint16_t some[kList];       // lists that reach the bound
+  Cand bound;
+  float least;
+  int n, n_some;
 };
 
-// The best `want` of the candidates that each(f) shows to f, thread by thread
-// and the same ones at every call, into C.out, best first; returns how many
-// there are (fewer when there are no more). `mine`: this thread's best one. All
-// threads of the CTA take part; C.n is 0 at the start.
-template <typename Each>
-__device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int runs = want <= 16 ? 32 : 128, of = kSelThreads / runs;      // of: threads of a run
+// The candidates in C.list, best first, into C.out.
+__device__ __forceinline__ int rank_list(Choose& C, int n, int want) {
+  for (int i = threadIdx.x; i < n; i += kSelThreads) {
+    const Cand x = C.list[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += before(C.list[j], x);
+    if (rank < want) C.out[rank] = x;
+  }
+  __syncthreads();
+  return min(n, want);
+}
+
+// Into C.bound: the want-th best of the runs' best candidates (runs without one
+// rank by their number), `mine` being this thread's.
+__device__ __forceinline__ void find_bound(Choose& C, int want, Cand mine) {
+  const int tid = threadIdx.x, runs = want <= 16 ? 32 : 128, of = kSelThreads / runs;   // of: threads of a run
   for (int o = 1; o < of; o <<= 1) {
     const Cand y = from_lane(mine, o);
     if (before(y, mine)) mine = y;
   }
   if (tid % of == 0) C.run[tid / of] = mine;
   __syncthreads();
-  // the want-th best run: every warp finds it for itself (runs without a candidate rank by their number)
-  Cand bound = {0, 0};
-  for (int i0 = 0; i0 < runs; i0 += 32) {
-    const Cand x = C.run[i0 + lane];
+  if (tid < runs) {
+    const Cand x = C.run[tid];
     int rank = 0;
 #pragma unroll 8
     for (int j = 0; j < runs; ++j) {
       const Cand y = C.run[j];
-      rank += before(y, x) || (y.key == x.key && y.at == x.at && j < i0 + lane);
+      rank += before(y, x) || (y.key == x.key && y.at == x.at && j < tid);
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, rank == want - 1);
-    if (hit) {
-      bound.key = __shfl_sync(0xffffffffu, x.key, __ffs(hit) - 1);
-      bound.at = __shfl_sync(0xffffffffu, x.at, __ffs(hit) - 1);
-    }
+    if (rank == want - 1) C.bound = x;
   }
+  __syncthreads();
+}
+
+// The best `want` of the candidates that each(f) shows to f, thread by thread
+// and the same ones at every call, into C.out, best first; returns how many
+// there are (fewer when there are no more). `mine`: this thread's best one. All
+// threads of the CTA take part; any order, any ties.
+template <typename Each>
+__device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  __syncthreads();
+  if (tid == 0) C.n = 0;
+  find_bound(C, want, mine);
+  const Cand bound = C.bound;
   each([&](uint64_t key, uint32_t at) {
     const Cand x = {key, at};
     if (key == 0 || before(bound, x)) return;
@@ -133,16 +157,7 @@ __device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each)
   });
   __syncthreads();
   const int n = C.n;
-  if (n <= kList) {
-    for (int i = tid; i < n; i += kSelThreads) {
-      const Cand x = C.list[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += before(C.list[j], x);
-      if (rank < want) C.out[rank] = x;
-    }
-    __syncthreads();
-    return min(n, want);
-  }
+  if (n <= kList) return rank_list(C, n, want);
   Cand last = {~0ull, 0};                                  // every candidate comes after it
   for (int k = 0; k < want; ++k) {
     Cand top = {0, 0xFFFFFFFFu};
@@ -174,69 +189,59 @@ __device__ __forceinline__ float to_float(T x) {
   else return __bfloat162float(x);
 }
 
-// kVec: rows start on 16-byte boundaries
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kSelThreads) k_beam_select(const __grid_constant__ BeamArgs A) {
+template <typename T>
+__global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_constant__ BeamArgs A) {
   constexpr int N = 16 / sizeof(T), V = kHeld / N;         // values of a load, loads of a thread
   __shared__ Choose C;
   __shared__ double s_base[kMaxBeams];
   __shared__ float s_top[kSelThreads / 32];
   __shared__ float s_sum[kSelThreads / 32];
-  __shared__ int s_bad, s_last;
+  __shared__ float2 s_beam[kMaxBeams];
+  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int beam = blockIdx.x / A.pieces, piece = blockIdx.x - beam * A.pieces;
   const int first = piece * A.held * kSelThreads;
   const bool over = A.ended && A.ended[beam] != 0;
-  if (tid == 0) {
-    C.n = 0;
-    s_bad = 0;
-  }
+  if (tid == 0) C.n = 0;
   // ---- the piece: value e of load j of a thread is token first + (j * 256 + tid) * N + e
   float x[kHeld];
   const T* row = reinterpret_cast<const T*>(A.logits) + (int64_t)beam * A.stride;
   auto token = [&](int i) { return first + ((i / N) * kSelThreads + tid) * N + i % N; };
+  const int held = A.held;
+  if (A.vec && !over && first + held * kSelThreads <= A.vocab) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int t0 = token(j * N);
-    const bool on = j * N < A.held && !over;
-    if (kVec && on && t0 + N <= A.vocab) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + t0));
+    for (int j = 0; j < V; ++j) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (j * N < held) w = __ldcs(reinterpret_cast<const uint4*>(row + token(j * N)));
       const T* y = reinterpret_cast<const T*>(&w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[j * N + e] = to_float(y[e]);
-    } else {
+      for (int e = 0; e < N; ++e) x[j * N + e] = j * N < held ? to_float(y[e]) : -INFINITY;
+    }
+  } else {                                                 // a row's last piece, or rows that start anywhere
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[j * N + e] = on && t0 + e < A.vocab ? to_float(row[t0 + e]) : -INFINITY;
+    for (int i = 0; i < kHeld; ++i) {
+      x[i] = -INFINITY;
+      if (i < held && token(i) < A.vocab) {
+        if (!over) x[i] = to_float(row[token(i)]);
+        else if (token(i) == A.end_token) x[i] = 0.f;
+      }
     }
   }
-  if (over) {
+  // ---- largest logit and sum (a NaN or +inf makes the sum NaN, nothing else does)
+  float top = x[0];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (i < A.held && token(i) == A.end_token) x[i] = 0.f;
-  }
-  // ---- largest logit, sum, the thread's best token (the first of equal ones)
-  bool bad = false;
-  float top = -INFINITY;
-  int at = 0;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    bad = bad || !(x[i] < INFINITY);
-    if (x[i] > top) {
-      top = x[i];
-      at = i;
-    }
-  }
-  auto candidate = [&](int i, float v) -> uint64_t {       // 0: no token
-    return i < A.held && token(i) < A.vocab ? (uint64_t)order32(v) : 0;
-  };
-  const Cand mine = {candidate(at, top), (uint32_t)token(at)};   // (all -inf: its first token)
+  for (int i = 1; i < kHeld; ++i) top = fmaxf(top, x[i]);
+  const int runs = A.n_out <= 16 ? 32 : 128, of = kSelThreads / runs;
   float wtop = top;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o == of && tid % of == 0) C.top[tid / of] = wtop;  // (of: 2 or 8 threads)
+    wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
+  }
   const float base = wtop == -INFINITY ? 0.f : wtop;
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) sum += exp2f((x[i] - base) * kLog2e);
+  for (int i = 0; i < kHeld; ++i) sum += exp2_ftz((x[i] - base) * kLog2e);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) {
@@ -244,11 +249,44 @@ __global__ void __launch_bounds__(kSelThreads) k_beam_select(const __grid_consta
     s_sum[warp] = sum;
   }
   __syncthreads();
-  if (__any_sync(0xffffffffu, bad) && lane == 0) s_bad = 1;
-  const int n = choose(C, A.n_out, mine, [&](auto f) {
+  // ---- the want-th largest of the runs' values: as many logits reach it
+  if (tid < runs) {
+    const float v = C.top[tid];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < runs; j += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(C.top + j);
+      rank += (y.x > v || (y.x == v && j < tid)) + (y.y > v || (y.y == v && j + 1 < tid)) + (y.z > v || (y.z == v && j + 2 < tid)) +
+              (y.w > v || (y.w == v && j + 3 < tid));
+    }
+    if (rank == A.n_out - 1) C.least = v;
+  }
+  __syncthreads();
+  const float least = C.least;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) f(candidate(i, x[i]), (uint32_t)token(i));
-  });
+  for (int i = 0; i < kHeld; ++i)
+    if (x[i] >= least && i < held && token(i) < A.vocab) {
+      const int place = atomicAdd(&C.n, 1);
+      if (place < kList) C.list[place] = {order32(x[i]), (uint32_t)token(i)};
+    }
+  __syncthreads();
+  int n = C.n;
+  if (n <= kList) {
+    n = rank_list(C, n, A.n_out);
+  } else {                                                 // more ties, or large values on few threads, than the list holds
+    const int end = min(first + held * kSelThreads, A.vocab);
+    auto each = [&](auto f) {
+#pragma unroll 1
+      for (int t = first + tid; t < end; t += kSelThreads)
+        f(order32(over ? (t == A.end_token ? 0.f : -INFINITY) : to_float(row[t])), (uint32_t)t);
+    };
+    Cand mine = {0, 0};
+    each([&](uint64_t key, uint32_t at) {
+      const Cand y = {key, at};
+      if (before(y, mine)) mine = y;
+    });
+    n = choose(C, A.n_out, mine, each);
+  }
   uint2* best = A.best + (int64_t)blockIdx.x * A.n_out;
   for (int i = tid; i < A.n_out; i += kSelThreads) best[i] = i < n ? make_uint2((uint32_t)C.out[i].key, C.out[i].at) : make_uint2(0, 0);
   if (warp == 0) {
@@ -256,10 +294,10 @@ __global__ void __launch_bounds__(kSelThreads) k_beam_select(const __grid_consta
     float all = t;
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-    float s = t > -INFINITY ? s_sum[lane] * exp2f((t - all) * kLog2e) : 0.f;
+    float s = lane >= kSelThreads / 32 ? 0.f : (t > -INFINITY ? s_sum[lane] * exp2_ftz((t - all) * kLog2e) : s_sum[lane]);
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) A.piece[blockIdx.x] = {all, s, (uint32_t)s_bad, 0u};
+    if (lane == 0) A.piece[blockIdx.x] = make_float2(all, s);
   }
   // ---- the last CTA of the group chooses among the pieces' lists
   int group = 0, hi = A.n_groups - 1;
@@ -273,56 +311,93 @@ __global__ void __launch_bounds__(kSelThreads) k_beam_select(const __grid_consta
     __threadfence();
     s_last = atomicAdd(&A.count[group], 1u) == (uint32_t)lists - 1;
     __threadfence();
-    C.n = 0;
+    C.n = C.n_some = 0;
   }
   __syncthreads();
   if (!s_last) return;
   for (int b = warp; b < beams; b += kSelThreads / 32) {
-    const Piece* p = A.piece + (int64_t)(b0 + b) * A.pieces;
-    float t = -INFINITY;
-    uint32_t junk = 0;
+    const float2* p = A.piece + (int64_t)(b0 + b) * A.pieces;
+    float t = -INFINITY, s = 0.f;
     for (int i = lane; i < A.pieces; i += 32) {
-      t = fmaxf(t, __ldcg(&p[i].top));
-      junk |= __ldcg(&p[i].bad);
+      const float2 y = __ldcg(p + i);
+      const float m = fmaxf(t, y.x), mb = m == -INFINITY ? 0.f : m;
+      s = s * exp2_ftz((t - mb) * kLog2e) + y.y * exp2_ftz((y.x - mb) * kLog2e);
+      t = m;
     }
+    float all = t;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-    junk = __reduce_or_sync(0xffffffffu, junk);
-    double s = 0.0;
-    for (int i = lane; i < A.pieces; i += 32) {
-      const float pt = __ldcg(&p[i].top);
-      if (pt > -INFINITY) s += (double)__ldcg(&p[i].sum) * (double)exp2f((pt - t) * kLog2e);
-    }
+    for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+    s *= exp2_ftz((t - (all == -INFINITY ? 0.f : all)) * kLog2e);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-      const float tot = A.total[b0 + b];
-      const bool gone = A.ended && A.ended[b0 + b] != 0;
-      // -inf: every continuation is worth that
-      s_base[b] = junk || t == -INFINITY || !(fabsf(tot) < INFINITY) ? -INFINITY
-                  : gone ? (double)tot : (double)tot - ((double)t + log(s));
-    }
+    if (lane == 0) s_beam[b] = make_float2(all, s);
   }
   __syncthreads();
-  // candidate c: place c / lists of list c % lists, so that the lists' best ones lie on different threads
-  const int n_cand = lists * A.n_out;
-  auto each = [&](auto f) {
-    for (int c = tid; c < n_cand; c += kSelThreads) {
-      const int r = c / lists, l = c - r * lists, b = l / A.pieces;
-      const double base_v = s_base[b];
-      uint2 e = __ldcg(A.best + ((int64_t)b0 * A.pieces + l) * A.n_out + r);
-      double v = -INFINITY;
-      if (base_v == -INFINITY) e = make_uint2(l == b * A.pieces && r < A.vocab, (uint32_t)r);   // its first tokens
-      else v = base_v + (double)from_order32(e.x);
-      f(e.x ? order64(v) : 0ull, (uint32_t)b * (uint32_t)A.vocab + e.y);
-    }
+  if (tid < beams) {
+    const float2 y = s_beam[tid];
+    const float tot = A.total[b0 + tid];
+    const bool gone = A.ended && A.ended[b0 + tid] != 0;
+    // -inf: every continuation is worth that
+    s_base[tid] = y.y != y.y || y.x == -INFINITY || !(fabsf(tot) < INFINITY) ? -INFINITY
+                  : gone ? (double)tot : (double)tot - ((double)y.x + log((double)y.y));
+  }
+  __syncthreads();
+  auto entry = [&](int l, int r) -> Cand {                 // place r of list l
+    const int b = l / A.pieces;
+    const double base_v = s_base[b];
+    uint2 e = __ldcg(A.best + ((int64_t)b0 * A.pieces + l) * A.n_out + r);
+    double v = -INFINITY;
+    if (base_v == -INFINITY) e = make_uint2(l == b * A.pieces && r < A.vocab, (uint32_t)r);   // its first tokens
+    else v = base_v + (double)from_order32(e.x);
+    return {e.x ? order64(v) : 0ull, (uint32_t)b * (uint32_t)A.vocab + e.y};
   };
+  // lists are sorted: those whose first candidate reaches the bound of the first ones, and of these the
+  // candidates that do
+  int step = 1;                                            // few lists lie on threads far from one another
+  while (step * 2 * lists <= kSelThreads) step *= 2;
   Cand own = {0, 0xFFFFFFFFu};
-  each([&](uint64_t key, uint32_t place) {
-    const Cand y = {key, place};
-    if (before(y, own)) own = y;
-  });
-  const int got = choose(C, A.n_out, own, each);
+  if (tid % step == 0)
+    for (int l = tid / step; l < lists; l += kSelThreads / step) {
+      const Cand y = entry(l, 0);
+      if (before(y, own)) own = y;
+    }
+  find_bound(C, A.n_out, own);
+  const Cand bound = C.bound;
+  if (tid % step == 0)
+    for (int l = tid / step; l < lists; l += kSelThreads / step) {
+      const Cand y = entry(l, 0);
+      if (y.key == 0 || before(bound, y)) continue;
+      const int i = atomicAdd(&C.n_some, 1);
+      if (i < kList) C.some[i] = (uint16_t)l;
+    }
+  __syncthreads();
+  const int n_some = C.n_some;
+  if (n_some <= kList)
+    for (int i = warp; i < n_some; i += kSelThreads / 32)
+      for (int r = lane; r < A.n_out; r += 32) {
+        const Cand y = entry(C.some[i], r);
+        if (y.key == 0 || before(bound, y)) break;
+        const int place = atomicAdd(&C.n, 1);
+        if (place < kList) C.list[place] = y;
+      }
+  __syncthreads();
+  int got = C.n;
+  if (n_some <= kList && got <= kList) {
+    got = rank_list(C, got, A.n_out);
+  } else {
+    auto each = [&](auto f) {
+      for (int c = tid; c < lists * A.n_out; c += kSelThreads) {
+        const Cand y = entry(c % lists, c / lists);
+        f(y.key, y.at);
+      }
+    };
+    own = {0, 0xFFFFFFFFu};
+    each([&](uint64_t key, uint32_t place) {
+      const Cand y = {key, place};
+      if (before(y, own)) own = y;
+    });
+    got = choose(C, A.n_out, own, each);
+  }
   // ---- out: best first, or every parent's best one in the parent's place
   int to = -1, parent = 0, tok = 0, end = 0;
   float val = 0.f;
@@ -351,12 +426,6 @@ __global__ void __launch_bounds__(kSelThreads) k_beam_select(const __grid_consta
     if (A.ended_out) A.ended_out[o] = end;
   }
   if (tid == 0) A.count[group] = 0u;
-}
-
-template <typename T>
-void launch_beam_select(const BeamArgs& A, int grid, cudaStream_t st) {
-  if (A.vec) k_beam_select<T, true><<<grid, kSelThreads, 0, st>>>(A);
-  else k_beam_select<T, false><<<grid, kSelThreads, 0, st>>>(A);
 }
 
 // Logits of a thread: the most that still give every SM a CTA, so that a small
@@ -400,7 +469,7 @@ BeamLayout beam_layout(const int32_t* seq0, int n_groups, int vocab, int n_out) 
   L.pieces = (vocab + L.held * kSelThreads - 1) / (L.held * kSelThreads);
   L.count = up256(sizeof(Ctrl));
   L.piece = up256(L.count + sizeof(uint32_t) * kMaxSeqs);
-  L.best = up256(L.piece + sizeof(Piece) * (size_t)beams * L.pieces);
+  L.best = up256(L.piece + sizeof(float2) * (size_t)beams * L.pieces);
   L.total = up256(L.best + sizeof(uint2) * (size_t)beams * L.pieces * n_out);
   return L;
 }
@@ -439,7 +508,7 @@ extern "C" tria_status tria_beam_select(const tria_beams* b, void* ws, size_t ws
   A.token_out = b->token_out;
   A.ended_out = b->ended_out;
   A.count = (uint32_t*)((uint8_t*)ws + L.count);
-  A.piece = (Piece*)((uint8_t*)ws + L.piece);
+  A.piece = (float2*)((uint8_t*)ws + L.piece);
   A.best = (uint2*)((uint8_t*)ws + L.best);
   A.vocab = b->vocab;
   A.n_out = b->n_out;
@@ -452,8 +521,8 @@ extern "C" tria_status tria_beam_select(const tria_beams* b, void* ws, size_t ws
   memcpy(A.seq0, b->seq0, sizeof(int32_t) * (b->n_groups + 1));
   const int grid = b->seq0[b->n_groups] * L.pieces;
   const cudaStream_t st = (cudaStream_t)stream;
-  if (b->type == TRIA_F32) launch_beam_select<float>(A, grid, st);
-  else if (b->type == TRIA_F16) launch_beam_select<__half>(A, grid, st);
-  else launch_beam_select<__nv_bfloat16>(A, grid, st);
+  if (b->type == TRIA_F32) k_beam_select<float><<<grid, kSelThreads, 0, st>>>(A);
+  else if (b->type == TRIA_F16) k_beam_select<__half><<<grid, kSelThreads, 0, st>>>(A);
+  else k_beam_select<__nv_bfloat16><<<grid, kSelThreads, 0, st>>>(A);
   return cudaGetLastError() == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
