@@ -3,12 +3,12 @@
 //
 //   v(b, t) = total_b + x_bt - ln sum_u exp(x_bu), the n_out largest of a group
 //
-// One pass over the logits: a CTA holds a piece of a beam's row in registers
-// and takes from it the largest logit, the sum of exponentials relative to it
-// and the piece's n_out best tokens (within a beam v orders like the logits,
-// so they are found before the sum is known). The last CTA of a group to
-// arrive adds the sums up and chooses among the pieces' lists; its CTAs write
-// 16 + 8 n_out bytes each, against 16 to 32 KB read.
+// One pass over the logits: a CTA takes a part of a beam's row in pieces that
+// its registers hold, and from it the largest logit, the sum of exponentials
+// relative to it and the part's n_out best tokens (within a beam v orders like
+// the logits, so they are found before the sum is known). The last CTA of a
+// group to arrive adds the sums up and chooses among the parts' lists; the CTAs
+// write 8 + 8 n_out bytes each, against 16 KB or more read.
 //
 // Choosing k of many: of 32 or 128 runs of threads' values (at least k), the
 // k-th largest of their best values is a bound that k values reach. The few
@@ -18,8 +18,9 @@
 // of arrival. Where more reach the bound than the list holds, it is taken
 // again with the indices (ties: a masked vocabulary), and where that leaves too
 // many (large values on few threads) the best are taken one after the other.
-// The pieces' lists are sorted, so the last CTA bounds their first entries
-// and reads on in the few lists that reach that.
+// A part's later pieces are held against the first one's bound, without meeting
+// the other threads. The parts' lists are sorted, so the last CTA bounds their first
+// entries and reads on in the few lists that reach that.
 //
 // Sums: exponentials (of differences from the largest logit, 4 units of 2^-24)
 // and their sums in fp32, the logarithm and v in fp64. A thread has the same
@@ -53,9 +54,10 @@ struct BeamArgs {
   int32_t* token_out;
   int32_t* ended_out;
   uint32_t* count;      // [groups] arrivals, zero between calls
-  float2* piece;        // [beams][pieces] {largest logit, sum of 2^((x - it) log2 e): NaN where a logit is NaN or +inf}
-  uint2* best;          // [beams][pieces][n_out] {ordered logit (0: none), token}, best first
-  int32_t vocab, n_out, n_groups, pieces, held, end_token, in_place;
+  float2* part;         // [beams][parts] {largest logit, sum of 2^((x - it) log2 e): NaN where a logit is NaN or +inf}
+  uint2* best;          // [beams][parts][n_out] {ordered logit (0: none), token}, best first
+  int32_t vocab, n_out, n_groups, end_token, in_place;
+  int32_t held, per, parts;   // logits of a thread at a time, how many times, CTAs of a row
   int32_t vec;          // rows start on 16-byte boundaries
   int32_t seq0[kMaxSeqs + 1];
 };
@@ -95,16 +97,70 @@ struct Choose {
   Cand list[kList];
   Cand out[kMaxOut];
   Cand warp_best[kSelThreads / 32];
-  float top[128];             // of runs of threads, as values alone
+  __align__(16) float top[128];       // of runs of threads, as values alone
+  __align__(16) uint32_t least[4];
   uint16_t some[kList];       // lists that reach the bound
   Cand bound;
-  float least;
   int n, n_some;
 };
 
-// The candidates in C.list, best first, into C.out.
-__device__ __forceinline__ int rank_list(Choose& C, int n, int want) {
-  for (int i = threadIdx.x; i < n; i += kSelThreads) {
+// The want-th largest of the runs' largest values (-inf where there are fewer),
+// `top` being this thread's: at least `want` values of the threads reach it.
+__device__ __forceinline__ float find_least(Choose& C, int want, float top) {
+  const int tid = threadIdx.x, lane = tid & 31, runs = want <= 16 ? 32 : 128;
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  if (runs == 32) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+    if ((tid & 7) == 0) C.top[tid >> 3] = top;
+  } else if ((tid & 1) == 0) {
+    C.top[tid >> 1] = top;
+  }
+  __syncthreads();
+  // the smallest value that fewer than `want` others exceed: of 32 runs every warp
+  // finds it for itself, of 128 the first four warps share them
+  if (runs == 32 || tid < runs) {
+    const float v = C.top[runs == 32 ? lane : tid];
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < runs; j += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(C.top + j);
+      above += (y.x > v) + (y.y > v) + (y.z > v) + (y.w > v);
+    }
+    const uint32_t least = __reduce_min_sync(0xffffffffu, above < want ? order32(v) : 0xFFFFFFFFu);
+    if (runs == 32) return from_order32(least);
+    if (lane == 0) C.least[tid >> 5] = least;
+  }
+  __syncthreads();
+  const uint4 y = *reinterpret_cast<const uint4*>(C.least);
+  return from_order32(min(min(y.x, y.y), min(y.z, y.w)));
+}
+
+// The candidates in C.list (n <= kList, the same in all threads), best first,
+// into C.out. Many are first held against a bound of their own: counting takes
+// as long as there are candidates. worth(): values that keep the order.
+template <typename Worth>
+__device__ __forceinline__ int rank_list(Choose& C, int n, int want, Worth worth) {
+  const int tid = threadIdx.x;
+  if (n > 2 * want && n > 64) {
+    Cand mine[kList / kSelThreads];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kList / kSelThreads; ++k)
+      if (k * kSelThreads + tid < n) {
+        mine[k] = C.list[k * kSelThreads + tid];
+        top = fmaxf(top, worth(mine[k]));
+      }
+    const float least = find_least(C, want, top);          // (meets the others: every candidate has been read)
+    if (tid == 0) C.n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kList / kSelThreads; ++k)
+      if (k * kSelThreads + tid < n && worth(mine[k]) >= least) C.list[atomicAdd(&C.n, 1)] = mine[k];
+    __syncthreads();
+    n = C.n;
+  }
+  for (int i = tid; i < n; i += kSelThreads) {
     const Cand x = C.list[i];
     int rank = 0;
 #pragma unroll 4
@@ -142,8 +198,8 @@ __device__ __forceinline__ void find_bound(Choose& C, int want, Cand mine) {
 // and the same ones at every call, into C.out, best first; returns how many
 // there are (fewer when there are no more). `mine`: this thread's best one. All
 // threads of the CTA take part; any order, any ties.
-template <typename Each>
-__device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each) {
+template <typename Each, typename Worth>
+__device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each, Worth worth) {
   const int tid = threadIdx.x, lane = tid & 31;
   __syncthreads();
   if (tid == 0) C.n = 0;
@@ -157,7 +213,7 @@ __device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each)
   });
   __syncthreads();
   const int n = C.n;
-  if (n <= kList) return rank_list(C, n, want);
+  if (n <= kList) return rank_list(C, n, want, worth);
   Cand last = {~0ull, 0};                                  // every candidate comes after it
   for (int k = 0; k < want; ++k) {
     Cand top = {0, 0xFFFFFFFFu};
@@ -194,98 +250,119 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
   constexpr int N = 16 / sizeof(T), V = kHeld / N;         // values of a load, loads of a thread
   __shared__ Choose C;
   __shared__ double s_base[kMaxBeams];
-  __shared__ float s_top[kSelThreads / 32];
-  __shared__ float s_sum[kSelThreads / 32];
-  __shared__ float2 s_beam[kMaxBeams];
+  __shared__ float s_top[kSelThreads / 32], s_sum[kSelThreads / 32];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int beam = blockIdx.x / A.pieces, piece = blockIdx.x - beam * A.pieces;
-  const int first = piece * A.held * kSelThreads;
+  const int beam = blockIdx.x / A.parts, part = blockIdx.x - beam * A.parts;
+  const int held = A.held, piece = held * kSelThreads;     // tokens of a thread and of the CTA at a time
+  const int from = part * A.per * piece, end = min(from + A.per * piece, A.vocab);
   const bool over = A.ended && A.ended[beam] != 0;
-  if (tid == 0) C.n = 0;
-  // ---- the piece: value e of load j of a thread is token first + (j * 256 + tid) * N + e
-  float x[kHeld];
   const T* row = reinterpret_cast<const T*>(A.logits) + (int64_t)beam * A.stride;
-  auto token = [&](int i) { return first + ((i / N) * kSelThreads + tid) * N + i % N; };
-  const int held = A.held;
-  if (A.vec && !over && first + held * kSelThreads <= A.vocab) {
+  const bool ends = over && A.end_token >= from && A.end_token < end;   // its one continuation lies in the part
+  if (tid == 0) {
+    C.n = ends;
+    if (ends) C.list[0] = {order32(0.f), (uint32_t)A.end_token};
+  }
+  // ---- the part, piece by piece: the warps' largest logits, the threads' sums relative to them, and the logits
+  // that reach the first piece's bound
+  float wtop = -INFINITY, sum = 0.f, least = 0.f;
+#pragma unroll 1
+  for (int first = over ? end : from; first < end; first += piece) {
+    // value e of load j of a thread is token first + (j * 256 + tid) * N + e
+    float x[kHeld];
+    auto token = [&](int i) { return first + ((i / N) * kSelThreads + tid) * N + i % N; };
+    if (A.vec && first + piece <= end) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (j * N < held) w = __ldcs(reinterpret_cast<const uint4*>(row + token(j * N)));
-      const T* y = reinterpret_cast<const T*>(&w);
+      for (int j = 0; j < V; ++j) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (j * N < held) w = __ldcs(reinterpret_cast<const uint4*>(row + token(j * N)));
+        const T* y = reinterpret_cast<const T*>(&w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[j * N + e] = j * N < held ? to_float(y[e]) : -INFINITY;
-    }
-  } else {                                                 // a row's last piece, or rows that start anywhere
+        for (int e = 0; e < N; ++e) x[j * N + e] = j * N < held ? to_float(y[e]) : -INFINITY;
+      }
+    } else {                                               // a row's last piece, or rows that start anywhere
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      x[i] = -INFINITY;
-      if (i < held && token(i) < A.vocab) {
-        if (!over) x[i] = to_float(row[token(i)]);
-        else if (token(i) == A.end_token) x[i] = 0.f;
+      for (int i = 0; i < kHeld; ++i) {
+        x[i] = -INFINITY;
+        if (i < held && token(i) < end) x[i] = to_float(row[token(i)]);
       }
     }
+    float most[4];                                         // of eight values each
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      most[k] = x[8 * k];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) most[k] = fmaxf(most[k], x[8 * k + i]);
+    }
+    const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    float now = top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+    if (now > wtop) {
+      sum *= exp2_ftz((wtop - now) * kLog2e);
+      wtop = now;
+    }
+    // (a NaN or +inf makes the sum NaN, nothing else does)
+    const float base = wtop == -INFINITY ? 0.f : wtop;
+    float2 sums = make_float2(sum, 0.f);
+#pragma unroll
+    for (int i = 0; i < kHeld; i += 2) {
+      float2 e = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(-base, -base)), make_float2(kLog2e, kLog2e));
+      e.x = exp2_ftz(e.x);
+      e.y = exp2_ftz(e.y);
+      sums = __fadd2_rn(sums, e);
+    }
+    sum = sums.x + sums.y;
+    if (first == from) least = find_least(C, A.n_out, top);
+    if (top >= least && top > -INFINITY) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (most[k] >= least) {
+#pragma unroll
+          for (int i = 8 * k; i < 8 * k + 8; ++i)
+            if (x[i] >= least && x[i] > -INFINITY) {
+              const int place = atomicAdd(&C.n, 1);
+              if (place < kList) C.list[place] = {order32(x[i]), (uint32_t)token(i)};
+            }
+        }
+    }
   }
-  // ---- largest logit and sum (a NaN or +inf makes the sum NaN, nothing else does)
-  float top = x[0];
-#pragma unroll
-  for (int i = 1; i < kHeld; ++i) top = fmaxf(top, x[i]);
-  const int runs = A.n_out <= 16 ? 32 : 128, of = kSelThreads / runs;
-  float wtop = top;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    if (o == of && tid % of == 0) C.top[tid / of] = wtop;  // (of: 2 or 8 threads)
-    wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, o));
-  }
-  const float base = wtop == -INFINITY ? 0.f : wtop;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) sum += exp2_ftz((x[i] - base) * kLog2e);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) {
-    s_top[warp] = wtop;
-    s_sum[warp] = sum;
+    s_top[warp] = ends ? 0.f : wtop;
+    s_sum[warp] = ends ? 1.f : sum;                        // (of a beam that is over, anything but NaN)
   }
   __syncthreads();
-  // ---- the want-th largest of the runs' values: as many logits reach it
-  if (tid < runs) {
-    const float v = C.top[tid];
-    int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < runs; j += 4) {
-      const float4 y = *reinterpret_cast<const float4*>(C.top + j);
-      rank += (y.x > v || (y.x == v && j < tid)) + (y.y > v || (y.y == v && j + 1 < tid)) + (y.z > v || (y.z == v && j + 2 < tid)) +
-              (y.w > v || (y.w == v && j + 3 < tid));
-    }
-    if (rank == A.n_out - 1) C.least = v;
-  }
-  __syncthreads();
-  const float least = C.least;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (x[i] >= least && i < held && token(i) < A.vocab) {
-      const int place = atomicAdd(&C.n, 1);
-      if (place < kList) C.list[place] = {order32(x[i]), (uint32_t)token(i)};
-    }
-  __syncthreads();
+  const int want = min(A.n_out, end - from);
+  auto logit = [](const Cand& y) { return from_order32((uint32_t)y.key); };
   int n = C.n;
   if (n <= kList) {
-    n = rank_list(C, n, A.n_out);
-  } else {                                                 // more ties, or large values on few threads, than the list holds
-    const int end = min(first + held * kSelThreads, A.vocab);
+    n = rank_list(C, n, A.n_out, logit);
+    if (n < want) {
+      // the others are -inf, the first ones of them: among so many tokens there are enough
+      const int t = from + tid;
+      const bool none = tid < want + n && t < end && (over ? t != A.end_token : to_float(row[t]) == -INFINITY);
+      const uint32_t those = __ballot_sync(0xffffffffu, none);
+      if (lane == 0 && warp < 4) C.least[warp] = __popc(those);   // (want + n < 128)
+      __syncthreads();
+      int place = n + __popc(those & ((1u << lane) - 1u));
+      for (int w = 0; w < min(warp, 3); ++w) place += C.least[w];
+      if (none && place < want) C.out[place] = {order32(-INFINITY), (uint32_t)t};
+      n = want;
+      __syncthreads();
+    }
+  } else {                                                 // ties, or large values on few threads
     auto each = [&](auto f) {
 #pragma unroll 1
-      for (int t = first + tid; t < end; t += kSelThreads)
-        f(order32(over ? (t == A.end_token ? 0.f : -INFINITY) : to_float(row[t])), (uint32_t)t);
+      for (int t = from + tid; t < end; t += kSelThreads) f(order32(to_float(row[t])), (uint32_t)t);
     };
     Cand mine = {0, 0};
     each([&](uint64_t key, uint32_t at) {
       const Cand y = {key, at};
       if (before(y, mine)) mine = y;
     });
-    n = choose(C, A.n_out, mine, each);
+    n = choose(C, A.n_out, mine, each, logit);
   }
   uint2* best = A.best + (int64_t)blockIdx.x * A.n_out;
   for (int i = tid; i < A.n_out; i += kSelThreads) best[i] = i < n ? make_uint2((uint32_t)C.out[i].key, C.out[i].at) : make_uint2(0, 0);
@@ -297,15 +374,15 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
     float s = lane >= kSelThreads / 32 ? 0.f : (t > -INFINITY ? s_sum[lane] * exp2_ftz((t - all) * kLog2e) : s_sum[lane]);
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) A.piece[blockIdx.x] = make_float2(all, s);
+    if (lane == 0) A.part[blockIdx.x] = make_float2(all, s);
   }
-  // ---- the last CTA of the group chooses among the pieces' lists
+  // ---- the last CTA of the group chooses among the parts' lists
   int group = 0, hi = A.n_groups - 1;
   while (group < hi) {
     const int mid = (group + hi + 1) >> 1;
     if (A.seq0[mid] <= beam) group = mid; else hi = mid - 1;
   }
-  const int b0 = A.seq0[group], beams = A.seq0[group + 1] - b0, lists = beams * A.pieces;
+  const int b0 = A.seq0[group], beams = A.seq0[group + 1] - b0, lists = beams * A.parts;
   __syncthreads();
   if (tid == 0) {
     __threadfence();
@@ -315,10 +392,12 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
   }
   __syncthreads();
   if (!s_last) return;
-  for (int b = warp; b < beams; b += kSelThreads / 32) {
-    const float2* p = A.piece + (int64_t)(b0 + b) * A.pieces;
+  {
+    // eight lanes a beam
+    const int b = tid >> 3;
+    const float2* p = A.part + (int64_t)(b0 + min(b, beams - 1)) * A.parts;
     float t = -INFINITY, s = 0.f;
-    for (int i = lane; i < A.pieces; i += 32) {
+    for (int i = tid & 7; i < A.parts; i += 8) {
       const float2 y = __ldcg(p + i);
       const float m = fmaxf(t, y.x), mb = m == -INFINITY ? 0.f : m;
       s = s * exp2_ftz((t - mb) * kLog2e) + y.y * exp2_ftz((y.x - mb) * kLog2e);
@@ -326,64 +405,62 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
     }
     float all = t;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+    for (int o = 4; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
     s *= exp2_ftz((t - (all == -INFINITY ? 0.f : all)) * kLog2e);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) s_beam[b] = make_float2(all, s);
-  }
-  __syncthreads();
-  if (tid < beams) {
-    const float2 y = s_beam[tid];
-    const float tot = A.total[b0 + tid];
-    const bool gone = A.ended && A.ended[b0 + tid] != 0;
-    // -inf: every continuation is worth that
-    s_base[tid] = y.y != y.y || y.x == -INFINITY || !(fabsf(tot) < INFINITY) ? -INFINITY
-                  : gone ? (double)tot : (double)tot - ((double)y.x + log((double)y.y));
+    for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((tid & 7) == 0 && b < beams) {
+      const float tot = A.total[b0 + b];
+      const bool gone = A.ended && A.ended[b0 + b] != 0;
+      // -inf: every continuation is worth that
+      s_base[b] = s != s || all == -INFINITY || !(fabsf(tot) < INFINITY) ? -INFINITY
+                  : gone ? (double)tot : (double)tot - ((double)all + log((double)s));
+    }
   }
   __syncthreads();
   auto entry = [&](int l, int r) -> Cand {                 // place r of list l
-    const int b = l / A.pieces;
+    const int b = l / A.parts;
     const double base_v = s_base[b];
-    uint2 e = __ldcg(A.best + ((int64_t)b0 * A.pieces + l) * A.n_out + r);
+    uint2 e = __ldcg(A.best + ((int64_t)b0 * A.parts + l) * A.n_out + r);
     double v = -INFINITY;
-    if (base_v == -INFINITY) e = make_uint2(l == b * A.pieces && r < A.vocab, (uint32_t)r);   // its first tokens
+    if (base_v == -INFINITY) e = make_uint2(l == b * A.parts && r < A.vocab, (uint32_t)r);   // its first tokens
     else v = base_v + (double)from_order32(e.x);
     return {e.x ? order64(v) : 0ull, (uint32_t)b * (uint32_t)A.vocab + e.y};
   };
   // lists are sorted: those whose first candidate reaches the bound of the first ones, and of these the
-  // candidates that do
+  // candidates that do (values rounded to fp32, which keeps their order)
   int step = 1;                                            // few lists lie on threads far from one another
   while (step * 2 * lists <= kSelThreads) step *= 2;
-  Cand own = {0, 0xFFFFFFFFu};
-  if (tid % step == 0)
+  const bool on = tid % step == 0;
+  auto worth = [](const Cand& y) { return y.key ? (float)from_order64(y.key) : -INFINITY; };
+  float mine = -INFINITY, head = -INFINITY;                // of this thread's lists, and of the first of them
+  if (on)
     for (int l = tid / step; l < lists; l += kSelThreads / step) {
-      const Cand y = entry(l, 0);
-      if (before(y, own)) own = y;
+      const float y = worth(entry(l, 0));
+      if (l == tid / step) head = y;
+      mine = fmaxf(mine, y);
     }
-  find_bound(C, A.n_out, own);
-  const Cand bound = C.bound;
-  if (tid % step == 0)
+  const float reach = find_least(C, A.n_out, mine);
+  if (on && mine >= reach)
     for (int l = tid / step; l < lists; l += kSelThreads / step) {
-      const Cand y = entry(l, 0);
-      if (y.key == 0 || before(bound, y)) continue;
+      if ((l == tid / step ? head : worth(entry(l, 0))) < reach) continue;
       const int i = atomicAdd(&C.n_some, 1);
       if (i < kList) C.some[i] = (uint16_t)l;
     }
   __syncthreads();
   const int n_some = C.n_some;
-  if (n_some <= kList)
-    for (int i = warp; i < n_some; i += kSelThreads / 32)
-      for (int r = lane; r < A.n_out; r += 32) {
+  if (n_some <= kList)                                     // eight threads a list, eight entries at a time
+    for (int i = tid >> 3; i < n_some; i += kSelThreads / 8)
+      for (int r = tid & 7; r < A.n_out; r += 8) {
         const Cand y = entry(C.some[i], r);
-        if (y.key == 0 || before(bound, y)) break;
+        if (y.key == 0 || worth(y) < reach) break;
         const int place = atomicAdd(&C.n, 1);
         if (place < kList) C.list[place] = y;
       }
   __syncthreads();
   int got = C.n;
   if (n_some <= kList && got <= kList) {
-    got = rank_list(C, got, A.n_out);
+    got = rank_list(C, got, A.n_out, worth);
   } else {
     auto each = [&](auto f) {
       for (int c = tid; c < lists * A.n_out; c += kSelThreads) {
@@ -391,15 +468,15 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
         f(y.key, y.at);
       }
     };
-    own = {0, 0xFFFFFFFFu};
+    Cand own = {0, 0xFFFFFFFFu};
     each([&](uint64_t key, uint32_t place) {
       const Cand y = {key, place};
       if (before(y, own)) own = y;
     });
-    got = choose(C, A.n_out, own, each);
+    got = choose(C, A.n_out, own, each, worth);
   }
   // ---- out: best first, or every parent's best one in the parent's place
-  int to = -1, parent = 0, tok = 0, end = 0;
+  int to = -1, parent = 0, tok = 0, done = 0;
   float val = 0.f;
   if (tid < got) {
     const Cand y = C.out[tid];
@@ -407,7 +484,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
     tok = (int)(y.at - (uint32_t)parent * (uint32_t)A.vocab);
     val = (float)from_order64(y.key);
     to = tid;
-    end = tok == A.end_token || (A.ended && A.ended[b0 + parent] != 0);
+    done = tok == A.end_token || (A.ended && A.ended[b0 + parent] != 0);
   }
   if (A.in_place && warp == 0) {                           // (n_out is the group's beams: a lane each)
     const uint32_t same = __match_any_sync(0xffffffffu, to >= 0 ? parent : -1 - lane);
@@ -423,17 +500,9 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
     A.total_out[o] = val;
     A.parent_out[o] = b0 + parent;
     A.token_out[o] = tok;
-    if (A.ended_out) A.ended_out[o] = end;
+    if (A.ended_out) A.ended_out[o] = done;
   }
   if (tid == 0) A.count[group] = 0u;
-}
-
-// Logits of a thread: the most that still give every SM a CTA, so that a small
-// call is spread over the GPU and a large one has few lists.
-int held_of(int beams, int vocab) {
-  int held = kHeld;
-  while (held > 8 && (int64_t)beams * ((vocab + held * kSelThreads - 1) / (held * kSelThreads)) < sm_count()) held /= 2;
-  return held;
 }
 
 }  // namespace
@@ -458,19 +527,24 @@ tria_status check_beams(const int32_t* seq0, int n_groups, int vocab, int n_out)
 }
 
 struct BeamLayout {
-  size_t count, piece, best, total;
-  int held, pieces;
+  size_t count, part, best, total;
+  int held, per, parts;
 };
 
+// Logits of a thread at a time: the most that still give every SM a CTA, so
+// that a small call is spread over the GPU. Pieces of a CTA: as few as keep the
+// CTAs of a large one resident at once (four an SM).
 BeamLayout beam_layout(const int32_t* seq0, int n_groups, int vocab, int n_out) {
   BeamLayout L{};
-  const int beams = seq0[n_groups];
-  L.held = held_of(beams, vocab);
-  L.pieces = (vocab + L.held * kSelThreads - 1) / (L.held * kSelThreads);
+  const int beams = seq0[n_groups], sms = sm_count();
+  auto pieces = [&] { return (vocab + L.held * kSelThreads - 1) / (L.held * kSelThreads); };
+  for (L.held = kHeld; L.held > 8 && (int64_t)beams * pieces() < sms;) L.held /= 2;
+  for (L.per = 1; L.per < pieces() && (int64_t)beams * ((pieces() + L.per - 1) / L.per) > 4 * (int64_t)sms;) ++L.per;
+  L.parts = (pieces() + L.per - 1) / L.per;
   L.count = up256(sizeof(Ctrl));
-  L.piece = up256(L.count + sizeof(uint32_t) * kMaxSeqs);
-  L.best = up256(L.piece + sizeof(float2) * (size_t)beams * L.pieces);
-  L.total = up256(L.best + sizeof(uint2) * (size_t)beams * L.pieces * n_out);
+  L.part = up256(L.count + sizeof(uint32_t) * kMaxSeqs);
+  L.best = up256(L.part + sizeof(float2) * (size_t)beams * L.parts);
+  L.total = up256(L.best + sizeof(uint2) * (size_t)beams * L.parts * n_out);
   return L;
 }
 
@@ -508,18 +582,19 @@ extern "C" tria_status tria_beam_select(const tria_beams* b, void* ws, size_t ws
   A.token_out = b->token_out;
   A.ended_out = b->ended_out;
   A.count = (uint32_t*)((uint8_t*)ws + L.count);
-  A.piece = (float2*)((uint8_t*)ws + L.piece);
+  A.part = (float2*)((uint8_t*)ws + L.part);
   A.best = (uint2*)((uint8_t*)ws + L.best);
   A.vocab = b->vocab;
   A.n_out = b->n_out;
   A.n_groups = b->n_groups;
-  A.pieces = L.pieces;
   A.held = L.held;
+  A.per = L.per;
+  A.parts = L.parts;
   A.end_token = b->end_token;
   A.in_place = b->in_place;
   A.vec = (uintptr_t)b->logits % 16 == 0 && (b->stride * size) % 16 == 0;
   memcpy(A.seq0, b->seq0, sizeof(int32_t) * (b->n_groups + 1));
-  const int grid = b->seq0[b->n_groups] * L.pieces;
+  const int grid = b->seq0[b->n_groups] * L.parts;
   const cudaStream_t st = (cudaStream_t)stream;
   if (b->type == TRIA_F32) k_beam_select<float><<<grid, kSelThreads, 0, st>>>(A);
   else if (b->type == TRIA_F16) k_beam_select<__half><<<grid, kSelThreads, 0, st>>>(A);
