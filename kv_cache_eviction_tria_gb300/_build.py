@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libtria.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "tria")
 
 SOURCES = ["api.cu", "stats.cu", "score.cu", "select.cu", "compact.cu", "noalloc.cu", "calib.cu", "lifecycle.cu",
-           "shared.cu", "pass_f16.cu", "pass_q8.cu", "rope.cu", "attend.cu", "attend_prompt.cu", "attend_prefix.cu",
+           "shared.cu", "pass_f16.cu", "pass_q8.cu", "rope.cu", "attend.cu", "attend_prompt.cu", "attend_group.cu",
+           "attend_prefix.cu",
            "beams.cu", "reorder.cu"] + \
           [f"attend_step_{k}_{v}.cu" for k in ("f16", "q8", "q4") for v in ("f16", "q8", "q4")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

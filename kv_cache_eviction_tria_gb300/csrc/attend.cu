@@ -351,6 +351,11 @@ cudaError_t launch_attend_span(const AttendArgs& A, int32_t* span, cudaStream_t 
   return cudaGetLastError();
 }
 
+bool tensor_types(const tria_layer_cache* c, int type) {
+  return type != TRIA_F32 && c->k_type != TRIA_F32 && c->v_type != TRIA_F32 &&
+         c->head_dim >= 64;
+}
+
 namespace {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -358,10 +363,6 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // Which kernel a sequence of t tokens takes.
 enum { kPathNone, kPathPlain, kPathStep, kPathPrompt };
 
-bool tensor_types(const tria_layer_cache* c, int type) {
-  return type != TRIA_F32 && c->k_type != TRIA_F32 && c->v_type != TRIA_F32 &&
-         c->head_dim >= 64;
-}
 
 // (The prompt kernel's tiles are 64 dims wide at least, narrower planes would
 // be mostly padding.) The decode kernel is built for these head_dims; few tokens of other ones take

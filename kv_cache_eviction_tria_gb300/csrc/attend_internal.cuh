@@ -66,6 +66,7 @@ struct AttendArgs {
   Ctrl* ctrl;
   uint32_t* count;     // arrivals per unit, zero between calls
   float* part;         // partial results of split units
+  int32_t* table;      // first tile of each unit, and the number of tiles (attend_group.cu)
   uint16_t* wide_k;    // fp16 copies of quantised planes (prompts; NULL: none)
   uint16_t* wide_kl;   // what fp16 leaves of the keys (NULL: not taken into account)
   uint16_t* wide_v;
@@ -97,6 +98,7 @@ tria_status check_attend_shape(const tria_layer_cache* c, int n_q_heads, const i
 tria_status check_attention(const tria_attention* a, int n_tokens, int hd);
 tria_status check_attend_rows(const tria_layer_cache* c, int G, const int32_t* tok0, int type);
 AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0);
+bool tensor_types(const tria_layer_cache* c, int type);   // whether the tensor-core kernels take them
 void fill_attend(AttendArgs& A, const tria_layer_cache* cache, const tria_attention* a);
 cudaError_t run_attend(AttendArgs& A, const tria_layer_cache* cache, const int32_t* tok0, bool round_keys, const AttendLayout& L, void* ws,
                        cudaStream_t st);
@@ -116,6 +118,18 @@ cudaError_t launch_attend_step_q4_q4(const AttendArgs& A, int cols, int workers,
 inline int prompt_dims(int hd) { return hd <= 64 ? 64 : (hd <= 128 ? 128 : 256); }
 inline int prompt_cols(int hd) { return hd > 128 ? 128 : 256; }
 cudaError_t launch_attend_prompt(const AttendArgs& A, cudaStream_t st);
+
+// attend_group.cu: units of 128 columns of a prefix and KV head (A.units of all of
+// them), a part of group_part_values(hd) values a unit and CTA; the own rows'
+// sequences for the join
+struct GroupOwn {
+  int32_t n_seqs;
+  int32_t tok0[kMaxSeqs], cap[kMaxSeqs];
+};
+size_t group_part_values(int hd);
+cudaError_t launch_attend_group(const AttendArgs& A, bool round_keys, int grid, cudaStream_t st);
+cudaError_t launch_join_group(const AttendArgs& A, const float* o2, const float* l2, const int32_t* own_live, const GroupOwn& own, int grid,
+                              cudaStream_t st);
 
 __device__ __forceinline__ float act_load(const void* p, int type, int64_t i) {
   if (type == TRIA_F32) return reinterpret_cast<const float*>(p)[i];

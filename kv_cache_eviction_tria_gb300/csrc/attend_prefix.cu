@@ -58,27 +58,48 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_prefix(const __grid_const
   if (d == 0 && A.lse) A.lse[x] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
-struct PrefixLayout {
-  AttendLayout shared, own;
-  size_t o1, l1, o2, l2, total;
-};
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Tokens of each prefix's sequences.
 void prefix_tokens(const int32_t* seq0, int n_prefixes, const int32_t* tok0, int32_t* out) {
   for (int p = 0; p <= n_prefixes; ++p) out[p] = tok0[seq0[p]];
 }
 
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+// Columns (token x query head of a KV head's group) of a prefix up to which its
+// rows are what is cut, by k_attend_group; more take the prompt kernel.
+constexpr int kGroupCols = 1024;
 
+struct PrefixLayout {
+  AttendLayout shared, own;
+  bool group;           // the prefix by k_attend_group
+  int units;            // of it
+  size_t span, table, part, o1, l1, o2, l2, total;
+};
+
+// The layout covers every type of queries, as attend_layout. The two caches'
+// kernels run one after the other and share their space, but for what the join reads.
 PrefixLayout prefix_layout(const tria_layer_cache* prefix, const tria_layer_cache* cache, const int32_t* seq0, int nq, const int32_t* tok0) {
-  PrefixLayout L;
+  PrefixLayout L{};
   int32_t tp[kMaxSeqs + 1];
   prefix_tokens(seq0, prefix->n_seqs, tok0, tp);
-  const int G = nq / cache->n_kv_heads;
-  L.shared = attend_layout(prefix, G, tp);
+  const int G = nq / cache->n_kv_heads, hd = cache->head_dim;
+  int64_t units = 0, most = 0;
+  for (int p = 0; p < prefix->n_seqs; ++p) {
+    const int64_t cols = (int64_t)(tp[p + 1] - tp[p]) * G;
+    most = std::max(most, cols);
+    units += (cols + 127) / 128 * cache->n_kv_heads;
+  }
+  L.group = tensor_types(prefix, TRIA_F16) && most > kStepCols && most <= kGroupCols && units <= kMaxSegments;
+  L.units = (int)units;
   L.own = attend_layout(cache, G, tok0);
-  const size_t rows = (size_t)tok0[cache->n_seqs] * nq, values = up256(rows * cache->head_dim * sizeof(float));
-  L.o1 = up256(std::max(L.shared.total, L.own.total));     // (the two run one after the other)
+  // fp32 queries take the other kernels whatever the columns, with a layout that has no room for fp16 copies
+  L.shared = attend_layout(prefix, G, tp);
+  const size_t shared = L.group ? L.shared.wide_k : L.shared.total;
+  const size_t rows = (size_t)tok0[cache->n_seqs] * nq, values = up256(rows * hd * sizeof(float));
+  L.span = up256(std::max(shared, L.own.total));
+  L.table = up256(L.span + (L.group ? 2 * sizeof(int32_t) * (size_t)prefix->n_seqs * prefix->n_kv_heads : 0));
+  L.part = up256(L.table + (L.group ? sizeof(int32_t) * (size_t)(kMaxSegments + 1) : 0));
+  L.o1 = up256(L.part + (L.group ? sizeof(float) * group_part_values(hd) * (L.units + (size_t)L.own.sms) : 0));
   L.o2 = L.o1 + values;
   L.l1 = L.o2 + values;
   L.l2 = L.l1 + up256(rows * sizeof(float));
@@ -124,23 +145,49 @@ extern "C" tria_status tria_attend_prefix(const tria_layer_cache* prefix, const 
   if ((r = check_attend_rows(prefix, G, tp, a->type)) != TRIA_OK || (r = check_attend_rows(cache, G, a->tok0, a->type)) != TRIA_OK) return r;
   const cudaStream_t st = (cudaStream_t)stream;
   uint8_t* at = (uint8_t*)ws;
+  float *o1 = (float*)(at + L.o1), *l1 = (float*)(at + L.l1), *o2 = (float*)(at + L.o2), *l2 = (float*)(at + L.l2);
   AttendArgs A;
-  for (int own = 0; own < 2; ++own) {
-    const tria_layer_cache* c = own ? cache : prefix;
-    fill_attend(A, c, a);
-    A.out = at + (own ? L.o2 : L.o1);
-    A.lse = (float*)(at + (own ? L.l2 : L.l1));
+  auto into = [&](float* out, float* lse) {                // a part of the result, in fp32
+    A.out = out;
+    A.lse = lse;
     A.out_stride = (int64_t)a->n_q_heads * hd;
     A.out_type = TRIA_F32;
-    if (own) A.sink = 0;
-    if (run_attend(A, c, own ? a->tok0 : tp, a->round_keys != 0, own ? L.own : L.shared, ws, st) != cudaSuccess) return TRIA_ERR_CUDA;
+  };
+  fill_attend(A, cache, a);
+  into(o2, l2);
+  A.sink = 0;
+  if (run_attend(A, cache, a->tok0, a->round_keys != 0, L.own, ws, st) != cudaSuccess) return TRIA_ERR_CUDA;
+  fill_attend(A, prefix, a);
+  if (L.group && tensor_types(prefix, a->type)) {
+    A.ctrl = (Ctrl*)ws;
+    A.table = (int32_t*)(at + L.table);
+    A.part = (float*)(at + L.part);
+    for (int p = 0, unit = 0; p < prefix->n_seqs; ++p) {
+      A.seq[p] = {prefix->seq_row0[p], 0, prefix->capacity[p], tp[p], tp[p + 1] - tp[p], unit};
+      unit += (A.seq[p].t * G + 127) / 128 * A.n_kv;
+    }
+    A.units = L.units;
+    if (A.window > 0) {
+      int32_t* span = (int32_t*)(at + L.span);
+      if (launch_attend_span(A, span, st) != cudaSuccess) return TRIA_ERR_CUDA;
+      A.span = span;
+    }
+    const int grid = L.own.sms;
+    if (launch_attend_group(A, a->round_keys != 0, grid, st) != cudaSuccess) return TRIA_ERR_CUDA;
+    GroupOwn own;
+    own.n_seqs = cache->n_seqs;
+    memcpy(own.tok0, a->tok0, sizeof(int32_t) * cache->n_seqs);
+    memcpy(own.cap, cache->capacity, sizeof(int32_t) * cache->n_seqs);
+    return launch_join_group(A, o2, l2, cache->n_live, own, grid, st) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
   }
+  into(o1, l1);
+  if (run_attend(A, prefix, tp, a->round_keys != 0, L.shared, ws, st) != cudaSuccess) return TRIA_ERR_CUDA;
   JoinArgs J;
   memset(&J, 0, sizeof(J));
-  J.o1 = (const float*)(at + L.o1);
-  J.o2 = (const float*)(at + L.o2);
-  J.l1 = (const float*)(at + L.l1);
-  J.l2 = (const float*)(at + L.l2);
+  J.o1 = o1;
+  J.o2 = o2;
+  J.l1 = l1;
+  J.l2 = l2;
   J.out = a->out;
   J.lse = a->lse;
   J.out_stride = a->out_stride;
