@@ -59,25 +59,30 @@ struct GroupShape {
 constexpr int kGroupBars = 2 * 12 + 2 + 2 + 5 + 2 * 4;
 struct GroupShared {
   uint32_t junk[12][4];                                    // rows of a value tile that held junk, by stage
-  int32_t lo[8], hi[8], c_lo[4], c_hi[4];                  // positions, a warp each
+  int32_t lo[8], hi[8], c_lo[8], c_hi[8];                  // positions, a warp each
   uint32_t tmem, abort;
 };
 static_assert(kGroupBars * 8 + sizeof(GroupShared) <= 1024, "barriers and shared state");
 
-constexpr int kGroupThreads = 512, kGroupIssue = 12, kGroupLoad = 13, kConv = 128;
+// two warpgroups of softmax, two that fill tiles, one whose first warp issues the
+// products and whose second one starts the copies
+constexpr int kGroupThreads = 640, kGroupIssue = 16, kGroupLoad = 17, kConv = 256, kGroupRegs = 96;
+// registers of a thread in each, cut from what the block starts with
+constexpr int kGroupSoft = 120, kGroupConv = 88, kGroupOther = 64;
+static_assert(2 * kGroupSoft + 2 * kGroupConv + kGroupOther == 5 * kGroupRegs, "register shares");
 
 // Eight values of a quantised row: w their codes (q8_0: eight bytes; q4_0: eight
-// bytes of which one half counts), sc their scale twice. hi: code x scale as fp16,
-// lo: what fp16 leaves of it, exactly (see k_widen).
-template <bool kLow>
-__device__ __forceinline__ void widen8(uint2 w, bool q8, uint32_t h, uint32_t* hi, uint32_t* lo) {
-  const uint32_t sc = h | (h << 16), bias = q8 ? 0x64806480u : 0x64086408u;
-  if (q8) {
-    w.x ^= 0x80808080u;
+// bytes of which the low halves count), h their scale. hi: code x scale as fp16,
+// lo: what fp16 leaves of it, which fp16 holds exactly (a scale is a multiple of
+// 2^-24 and a code whole, so 8 bits at most are left, all above 2^-24).
+template <bool kQ8, bool kLow>
+__device__ __forceinline__ void widen8(uint2 w, uint32_t h, uint32_t* hi, uint32_t* lo) {
+  const uint32_t sc = __byte_perm(h, h, 0x1010);
+  constexpr uint32_t bias = kQ8 ? 0x64806480u : 0x64086408u;
+  if (kQ8) {
+    w.x ^= 0x80808080u;                                    // 0x64, code + 128: 1152 + code
     w.y ^= 0x80808080u;
   }
-  const float s = __half2float(__ushort_as_half((uint16_t)h));
-  const float2 sf = make_float2(s, s);
   const uint32_t b[4] = {__byte_perm(w.x, 0x64646464u, 0x4140), __byte_perm(w.x, 0x64646464u, 0x4342),
                          __byte_perm(w.y, 0x64646464u, 0x4140), __byte_perm(w.y, 0x64646464u, 0x4342)};
 #pragma unroll
@@ -85,12 +90,41 @@ __device__ __forceinline__ void widen8(uint2 w, bool q8, uint32_t h, uint32_t* h
     uint32_t c;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(b[k]), "r"(bias));
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(c), "r"(sc));
-    if constexpr (kLow) {
-      const float2 x = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&c)), sf);
-      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-      const __half2 l = __floats2half2_rn(x.x - y.x, x.y - y.y);
-      lo[k] = *reinterpret_cast<const uint32_t*>(&l);
+    if constexpr (kLow) asm("{\n .reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;\n}\n" : "=r"(lo[k]) : "r"(c), "r"(sc), "r"(hi[k]));
+  }
+}
+
+// The rows of a tile of codes (rb bytes each) as fp16 tiles, by kConv threads; a
+// thread has the same eight dims of every kConv / (HD / 8)-th row. Rows from `rows` on
+// are zeros with kClean, which also replaces rows with junk and marks them.
+template <int HD, int BN, bool kQ8, bool kLow, bool kClean>
+__device__ __forceinline__ void widen_tile(const uint8_t* codes, int rb, const uint16_t* scale, uint8_t* hi_t, uint8_t* lo_t, int hd, int rows,
+                                           uint32_t* marks, int tid) {
+  constexpr int per = HD / 8, step = kConv / per, NB = HD / 32;
+  static_assert(step % 8 == 0 && BN % step == 0, "a thread's rows have one place in the swizzle");
+  const int c = tid % per, r0 = tid / per;
+  const uint32_t to = (c >> 3) * (BN * 128) + swz(r0, c & 7);
+  const uint8_t* from = codes + r0 * rb + (kQ8 ? c * 8 : (c / 4) * 16 + (c & 1) * 8);
+  const bool there = 8 * c < hd;
+#pragma unroll
+  for (int i = 0; i < BN / step; ++i) {
+    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+    if (there && (!kClean || r0 + i * step < rows)) {
+      uint2 w = *reinterpret_cast<const uint2*>(from + i * step * rb);
+      if constexpr (!kQ8) {
+        const int up = (c & 2) * 2;
+        w.x = (w.x >> up) & 0x0F0F0F0Fu;
+        w.y = (w.y >> up) & 0x0F0F0F0Fu;
+      }
+      widen8<kQ8, kLow>(w, scale[(r0 + i * step) * NB + c / 4], hi, lo);
+      if (kClean && (junk_h2(hi[0]) || junk_h2(hi[1]) || junk_h2(hi[2]) || junk_h2(hi[3]))) {
+        const int rr = r0 + i * step;
+        hi[0] = hi[1] = hi[2] = hi[3] = 0;
+        atomicOr(&marks[rr >> 5], 1u << (rr & 31));
+      }
     }
+    *reinterpret_cast<uint4*>(hi_t + to + i * step * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (kLow) *reinterpret_cast<uint4*>(lo_t + to + i * step * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -166,9 +200,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       if (blockIdx.x == 0) A.table[A.units] = tot;
     }
   }
+  // The kernel starts while the one before it, over the sequences' own rows,
+  // still runs on other SMs, and needs none of its results; but who waits for
+  // this one to end has to find that one ended.
+  auto leave = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
   if (smem_u32(smem) & 1023u) {                            // the swizzled tiles need it
     if (threadIdx.x == 0) report(A.ctrl, TRIA_ERR_CUDA, 0u);
-    return;
+    return leave();
   }
   if (threadIdx.x == 0) {
     X.abort = 0;
@@ -197,7 +235,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   __syncthreads();
   const int64_t total = s_first[A.units];
   const int64_t workers = min((int64_t)gridDim.x, total);
-  if ((int64_t)blockIdx.x >= workers) return;
+  if ((int64_t)blockIdx.x >= workers) return leave();
   if (warp == kGroupIssue) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&X.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -266,6 +304,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   auto raw = [&](int j) { return smem + H::oRaw + (j % slots) * (2 * raw_v); };
   const int k_rb = A.k_type == TRIA_Q8_0 ? A.hd : A.hd / 2, v_rb = A.v_type == TRIA_Q8_0 ? A.hd : A.hd / 2;
 
+  if (wg >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupOther));
   if (warp == kGroupIssue) {
     // ---- products (results of waits and addresses are the same in all lanes and kept in
     // such a form, see the prompt kernel)
@@ -362,9 +401,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
             }
       }
     }
-  } else if (wg == 2) {
+  } else if (wg >= 2 && wg < 4) {
     // ---- positions; value tiles of fp16 planes; codes into tiles
-    const int tid = threadIdx.x & 127;
+    const int tid = threadIdx.x & 255;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupConv));
     uint16_t* s_scale = reinterpret_cast<uint16_t*>(smem + H::oScale);
     constexpr int NB = HD / 32;
     const int nb = A.hd / 32;
@@ -377,15 +417,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       // the tokens' positions, and whether they hide rows
       const int tok_a = U.c0 / A.G, tok_b = (U.c0 + U.ncol - 1) / A.G;
       int pl = INT32_MAX, ph = INT32_MIN;
-      if (tok_a + tid <= tok_b) pl = ph = A.pos[S.tok0 + tok_a + tid];   // (128 columns at most)
+      if (tok_a + tid <= tok_b) pl = ph = A.pos[S.tok0 + tok_a + tid];
       const int newest = s_hi[u] > 0 ? rpos[s_hi[u] - 1] : INT32_MIN;
       pl = __reduce_min_sync(0xffffffffu, pl);
       ph = __reduce_max_sync(0xffffffffu, ph);
       if (lane == 0) {
-        X.c_lo[warp & 3] = pl;
-        X.c_hi[warp & 3] = ph;
+        X.c_lo[warp & 7] = pl;
+        X.c_hi[warp & 7] = ph;
       }
-      asm volatile("bar.sync 3, 128;" ::: "memory");
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+      // (128 columns at most, so the first four warps hold all of the tokens)
       const int pmin = min(min(X.c_lo[0], X.c_lo[1]), min(X.c_lo[2], X.c_lo[3]));
       const int pmax = max(max(X.c_hi[0], X.c_hi[1]), max(X.c_hi[2], X.c_hi[3]));
       const bool need_pos = A.window > 0 || newest > pmin;
@@ -421,39 +462,18 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         fetch(t + 1);
         if constexpr (kQuant) {
           wait(&b_rf[j % slots], (j / slots) & 1);
-          asm volatile("bar.sync 3, 128;" ::: "memory");   // scales
+          asm volatile("bar.sync 3, 256;" ::: "memory");   // scales
           if (kq) {
             const int e = P * j;
             free_stage(e);
             if (kLow) free_stage(e + 1);
             __syncwarp();
-            uint8_t *hi_t = stage(e), *lo_t = stage(e + 1);
-            const bool q8 = A.k_type == TRIA_Q8_0;
-#pragma unroll 4
-            for (int x = tid; x < BN * (HD / 8); x += kConv) {
-              const int rr = x / (HD / 8), c = x - rr * (HD / 8);
-              uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-              if (8 * c < A.hd) {
-                uint2 w;
-                if (q8) {
-                  w = *reinterpret_cast<const uint2*>(raw(j) + rr * k_rb + c * 8);
-                } else {
-                  w = *reinterpret_cast<const uint2*>(raw(j) + rr * k_rb + (c / 4) * 16 + (c & 1) * 8);
-                  if (c & 2) {
-                    w.x >>= 4;
-                    w.y >>= 4;
-                  }
-                  w.x &= 0x0F0F0F0Fu;
-                  w.y &= 0x0F0F0F0Fu;
-                }
-                widen8<kLow>(w, q8, s_scale[rr * NB + c / 4], hi, lo);
-              }
-              const uint32_t to = (c >> 3) * (BN * 128) + swz(rr, c & 7);
-              *reinterpret_cast<uint4*>(hi_t + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              if constexpr (kLow) *reinterpret_cast<uint4*>(lo_t + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
+            if (A.k_type == TRIA_Q8_0)
+              widen_tile<HD, BN, true, kLow, false>(raw(j), k_rb, s_scale, stage(e), stage(e + 1), A.hd, rows, nullptr, tid);
+            else
+              widen_tile<HD, BN, false, kLow, false>(raw(j), k_rb, s_scale, stage(e), stage(e + 1), A.hd, rows, nullptr, tid);
             fence_proxy_async_smem();
-            asm volatile("bar.sync 3, 128;" ::: "memory");
+            asm volatile("bar.sync 3, 256;" ::: "memory");
             if (tid == 0) {
               mbar_arrive(&b_full[e % ST]);
               if (kLow) mbar_arrive(&b_full[(e + 1) % ST]);
@@ -466,39 +486,21 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         int32_t* tp = s_pos + (j % H::kPosTiles) * BN;
         if (need_pos && tid < BN) tp[tid] = pos_now;
         if (tid < 4) X.junk[ev % ST][tid] = 0;
-        asm volatile("bar.sync 3, 128;" ::: "memory");
+        asm volatile("bar.sync 3, 256;" ::: "memory");
         const bool all = rows == BN && (!need_pos || (tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window ||
                                                                             r + BN <= A.sink)));   // seen whole by every token
         bool filled = false;
         if constexpr (kQuant) {
           if (vq) {
             filled = true;
-            uint8_t* v_t = stage(ev);
-            const bool q8 = A.v_type == TRIA_Q8_0;
-#pragma unroll 4
-            for (int x = tid; x < BN * (HD / 8); x += kConv) {
-              const int rr = x / (HD / 8), c = x - rr * (HD / 8);
-              uint32_t hi[4] = {0, 0, 0, 0};
-              if (8 * c < A.hd && rr < rows) {
-                uint2 w;
-                if (q8) {
-                  w = *reinterpret_cast<const uint2*>(raw(j) + raw_v + rr * v_rb + c * 8);
-                } else {
-                  w = *reinterpret_cast<const uint2*>(raw(j) + raw_v + rr * v_rb + (c / 4) * 16 + (c & 1) * 8);
-                  if (c & 2) {
-                    w.x >>= 4;
-                    w.y >>= 4;
-                  }
-                  w.x &= 0x0F0F0F0Fu;
-                  w.y &= 0x0F0F0F0Fu;
-                }
-                widen8<false>(w, q8, s_scale[(BN + rr) * NB + c / 4], hi, nullptr);
-                if (!all && (junk_h2(hi[0]) || junk_h2(hi[1]) || junk_h2(hi[2]) || junk_h2(hi[3]))) {
-                  hi[0] = hi[1] = hi[2] = hi[3] = 0;
-                  atomicOr(&X.junk[ev % ST][rr >> 5], 1u << (rr & 31));
-                }
-              }
-              *reinterpret_cast<uint4*>(v_t + (c >> 3) * (BN * 128) + swz(rr, c & 7)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            const uint8_t* codes = raw(j) + raw_v;
+            uint32_t* marks = X.junk[ev % ST];
+            if (A.v_type == TRIA_Q8_0) {
+              if (all) widen_tile<HD, BN, true, false, false>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
+              else widen_tile<HD, BN, true, false, true>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
+            } else {
+              if (all) widen_tile<HD, BN, false, false, false>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
+              else widen_tile<HD, BN, false, false, true>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
             }
           }
         }
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         }
         if (filled || kQuant) {
           if (filled) fence_proxy_async_smem();
-          asm volatile("bar.sync 3, 128;" ::: "memory");
+          asm volatile("bar.sync 3, 256;" ::: "memory");
           if (tid == 0) {
             if (filled) mbar_arrive(&b_full[ev % ST]);
             if (kQuant) mbar_arrive(&b_re[j % slots]);
@@ -528,6 +530,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         }
   } else if (wg < 2) {
     // ---- softmax: a thread per row and half of a tile's columns
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupSoft));
     const int m = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     auto meet = [&] { asm volatile("bar.sync 4, 256;" ::: "memory"); };
@@ -743,16 +746,20 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+  leave();
 }
 
-// Joins the parts of a unit, in the order of the CTAs, with its tokens' own rows
-// (o2, l2): a thread per column, kJoinDims dims a block.
-constexpr int kJoinDims = 8;
+// Joins the parts of a unit with its tokens' own rows (o2, l2): a thread per
+// column, a quarter of the parts and kJoinDims dims, whose loads are all in flight; the
+// quarters meet in shared memory, in order. (A thread for all parts waited
+// for memory again and again: 13 to 19 us.)
+constexpr int kJoinDims = 8, kJoinQuarters = 4, kJoinLoads = 5;
 
 template <int HD>
-__global__ void __launch_bounds__(128) k_join_group(const __grid_constant__ AttendArgs A, const float* o2, const float* l2,
-                                                    const int32_t* own_live, const __grid_constant__ GroupOwn own, int grid) {
-  const int u = blockIdx.x, d0 = blockIdx.y * kJoinDims, c = threadIdx.x;
+__global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid_constant__ AttendArgs A, const float* o2, const float* l2,
+                                                                    const int32_t* own_live, const __grid_constant__ GroupOwn own, int grid) {
+  __shared__ float s_m[kJoinQuarters][128], s_l[kJoinQuarters][128], s_v[kJoinQuarters][kJoinDims][128];
+  const int u = blockIdx.x, d0 = blockIdx.y * kJoinDims, c = threadIdx.x & 127, quarter = threadIdx.x >> 7;
   int s = 0, hi_s = A.n_seqs - 1;
   while (s < hi_s) {
     const int mid = (s + hi_s + 1) >> 1;
@@ -760,22 +767,27 @@ __global__ void __launch_bounds__(128) k_join_group(const __grid_constant__ Atte
   }
   const AttendSeq& S = A.seq[s];
   const int ct = (S.t * A.G + 127) / 128, x = u - S.unit0, g = x / ct, col = (x - g * ct) * 128 + c;
-  if (col >= S.t * A.G) return;
-  const int tok = S.tok0 + col / A.G, head = g * A.G + col % A.G;
-  int q = 0, hi_q = own.n_seqs - 1;                        // the token's sequence
-  while (q < hi_q) {
-    const int mid = (q + hi_q + 1) >> 1;
-    if (own.tok0[mid] <= tok) q = mid; else hi_q = mid - 1;
-  }
-  const int n1 = *((volatile const int32_t*)(A.n_live + s)), n2 = *((volatile const int32_t*)(own_live + q));
-  if (n1 < 0 || n1 > S.cap || n2 < 0 || n2 > own.cap[q]) return;
-  const int64_t total = A.table[A.units], t0 = A.table[u], t1 = A.table[u + 1];
+  const bool on = col < S.t * A.G;
+  const int tok = S.tok0 + (on ? col / A.G : 0), head = g * A.G + (on ? col % A.G : 0);
   const int64_t at = (int64_t)tok * A.nq + head;
-  const float4* own_o = reinterpret_cast<const float4*>(o2 + at * A.hd + d0);
-  float4 b[kJoinDims / 4];
+  const int64_t total = A.table[A.units], t0 = A.table[u], t1 = A.table[u + 1];
+  // the sequence's own rows join the first quarter
+  float m = -INFINITY, l = 0.f, v[kJoinDims];
 #pragma unroll
-  for (int e = 0; e < kJoinDims / 4; ++e) b[e] = own_o[e];
-  const float m2 = l2[at] * 1.4426950408889634f;
+  for (int e = 0; e < kJoinDims; ++e) v[e] = 0.f;
+  if (quarter == 0 && on) {
+    const float4* o = reinterpret_cast<const float4*>(o2 + at * A.hd + d0);
+#pragma unroll
+    for (int e = 0; e < kJoinDims / 4; ++e) {
+      const float4 y = o[e];
+      v[4 * e] = y.x;
+      v[4 * e + 1] = y.y;
+      v[4 * e + 2] = y.z;
+      v[4 * e + 3] = y.w;
+    }
+    m = l2[at] * 1.4426950408889634f;
+    l = m == -INFINITY ? 0.f : 1.f;
+  }
   int c0 = 0, parts = 0;
   if (t1 > t0) {
     const int64_t workers = min((int64_t)grid, total);
@@ -784,25 +796,61 @@ __global__ void __launch_bounds__(128) k_join_group(const __grid_constant__ Atte
   }
   constexpr int64_t kSlot = 128 * (HD + 2);
   const float* p = A.part + (int64_t)(u + c0) * kSlot + c;
-  float top = m2;
-#pragma unroll 8
-  for (int k = 0; k < parts; ++k) top = fmaxf(top, p[k * kSlot]);
-  const float tb = top == -INFINITY ? 0.f : top;
-  float sum = exp2f(m2 - tb), v[kJoinDims];
+  if (on)
+    for (int k0 = quarter; k0 < parts; k0 += kJoinQuarters * kJoinLoads) {
+      float pm[kJoinLoads], pl[kJoinLoads], pv[kJoinLoads][kJoinDims];
 #pragma unroll
-  for (int e = 0; e < kJoinDims / 4; ++e) {
-    v[4 * e] = b[e].x * sum;
-    v[4 * e + 1] = b[e].y * sum;
-    v[4 * e + 2] = b[e].z * sum;
-    v[4 * e + 3] = b[e].w * sum;
+      for (int k = 0; k < kJoinLoads; ++k) {
+        const float* y = p + min(k0 + k * kJoinQuarters, parts - 1) * kSlot;   // (in the place of a part that is not there one that is)
+        pm[k] = y[0];
+        pl[k] = y[128];
+#pragma unroll
+        for (int e = 0; e < kJoinDims; ++e) pv[k][e] = y[(2 + d0 + e) * 128];
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kJoinLoads; ++k)
+        if (k0 + k * kJoinQuarters < parts) top = fmaxf(top, pm[k]);
+      const float tb = top == -INFINITY ? 0.f : top, f0 = exp2f(m - tb);
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < kJoinDims; ++e) v[e] *= f0;
+#pragma unroll
+      for (int k = 0; k < kJoinLoads; ++k)
+        if (k0 + k * kJoinQuarters < parts) {
+          const float f = exp2f(pm[k] - tb);
+          l = fmaf(pl[k], f, l);
+#pragma unroll
+          for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(pv[k][e], f, v[e]);
+        }
+      m = top;
+    }
+  s_m[quarter][c] = m;
+  s_l[quarter][c] = l;
+#pragma unroll
+  for (int e = 0; e < kJoinDims; ++e) s_v[quarter][e][c] = v[e];
+  __syncthreads();
+  if (quarter != 0 || !on) return;
+  int q = 0, hi_q = own.n_seqs - 1;                        // the token's sequence
+  while (q < hi_q) {
+    const int mid = (q + hi_q + 1) >> 1;
+    if (own.tok0[mid] <= tok) q = mid; else hi_q = mid - 1;
   }
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
-    const float* y = p + k * kSlot;
-    const float f = exp2f(y[0] - tb);
-    sum = fmaf(y[128], f, sum);
+  const int n1 = *((volatile const int32_t*)(A.n_live + s)), n2 = *((volatile const int32_t*)(own_live + q));
+  if (n1 < 0 || n1 > S.cap || n2 < 0 || n2 > own.cap[q]) return;
+  float top = m;
 #pragma unroll
-    for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(y[(2 + d0 + e) * 128], f, v[e]);
+  for (int k = 1; k < kJoinQuarters; ++k) top = fmaxf(top, s_m[k][c]);
+  const float tb = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < kJoinDims; ++e) v[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinQuarters; ++k) {
+    const float f = exp2f(s_m[k][c] - tb);
+    sum = fmaf(s_l[k][c], f, sum);
+#pragma unroll
+    for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(s_v[k][e][c], f, v[e]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t w[kJoinDims / 2];
@@ -819,6 +867,11 @@ cudaError_t launch_group_t(const AttendArgs& A, int grid, cudaStream_t st) {
   auto kern = k_attend_group<HD, kQuant, kLow>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, H::kSmem);
   if (e != cudaSuccess) return e;
+  // the warpgroups' register shares are cut from what the block starts with
+  cudaFuncAttributes attr;
+  const cudaError_t e2 = cudaFuncGetAttributes(&attr, kern);
+  if (e2 != cudaSuccess) return e2;
+  if (attr.numRegs != kGroupRegs) return cudaErrorInvalidConfiguration;
   CUtensorMap mk, mv;
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));
@@ -826,8 +879,17 @@ cudaError_t launch_group_t(const AttendArgs& A, int grid, cudaStream_t st) {
   for (int s = 0; s < A.n_seqs; ++s) rows = std::max(rows, A.seq[s].row0 + (int64_t)A.n_kv * A.seq[s].cap);
   if (A.k_type == TRIA_F16 && !plane_map_f16(&mk, A.k, A.hd, rows, H::BN)) return cudaErrorInvalidValue;
   if (A.v_type == TRIA_F16 && !plane_map_f16(&mv, A.v, A.hd, rows, H::BN)) return cudaErrorInvalidValue;
-  kern<<<grid, kGroupThreads, H::kSmem, st>>>(A, mk, mv);
-  return cudaGetLastError();
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kGroupThreads);
+  cfg.dynamicSmemBytes = H::kSmem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, A, mk, mv);
 }
 
 template <int HD>
@@ -839,7 +901,7 @@ cudaError_t launch_group_hd(const AttendArgs& A, bool low, int grid, cudaStream_
 template <int HD>
 cudaError_t launch_join_hd(const AttendArgs& A, const float* o2, const float* l2, const int32_t* own_live, const GroupOwn& own, int grid,
                            cudaStream_t st) {
-  k_join_group<HD><<<dim3(A.units, A.hd / kJoinDims), 128, 0, st>>>(A, o2, l2, own_live, own, grid);
+  k_join_group<HD><<<dim3(A.units, A.hd / kJoinDims), 128 * kJoinQuarters, 0, st>>>(A, o2, l2, own_live, own, grid);
   return cudaGetLastError();
 }
 

@@ -147,16 +147,16 @@ extern "C" tria_status tria_attend_prefix(const tria_layer_cache* prefix, const 
   uint8_t* at = (uint8_t*)ws;
   float *o1 = (float*)(at + L.o1), *l1 = (float*)(at + L.l1), *o2 = (float*)(at + L.o2), *l2 = (float*)(at + L.l2);
   AttendArgs A;
-  auto into = [&](float* out, float* lse) {                // a part of the result, in fp32
-    A.out = out;
-    A.lse = lse;
-    A.out_stride = (int64_t)a->n_q_heads * hd;
-    A.out_type = TRIA_F32;
+  auto own_rows = [&] {
+    AttendArgs B;
+    fill_attend(B, cache, a);
+    B.out = o2;
+    B.lse = l2;
+    B.out_stride = (int64_t)a->n_q_heads * hd;
+    B.out_type = TRIA_F32;
+    B.sink = 0;
+    return run_attend(B, cache, a->tok0, a->round_keys != 0, L.own, ws, st) == cudaSuccess;
   };
-  fill_attend(A, cache, a);
-  into(o2, l2);
-  A.sink = 0;
-  if (run_attend(A, cache, a->tok0, a->round_keys != 0, L.own, ws, st) != cudaSuccess) return TRIA_ERR_CUDA;
   fill_attend(A, prefix, a);
   if (L.group && tensor_types(prefix, a->type)) {
     A.ctrl = (Ctrl*)ws;
@@ -173,14 +173,19 @@ extern "C" tria_status tria_attend_prefix(const tria_layer_cache* prefix, const 
       A.span = span;
     }
     const int grid = L.own.sms;
-    if (launch_attend_group(A, a->round_keys != 0, grid, st) != cudaSuccess) return TRIA_ERR_CUDA;
+    // (the own rows' kernel first: the prefix's may start before it has ended, and needs what came before)
+    if (!own_rows() || launch_attend_group(A, a->round_keys != 0, grid, st) != cudaSuccess) return TRIA_ERR_CUDA;
     GroupOwn own;
     own.n_seqs = cache->n_seqs;
     memcpy(own.tok0, a->tok0, sizeof(int32_t) * cache->n_seqs);
     memcpy(own.cap, cache->capacity, sizeof(int32_t) * cache->n_seqs);
     return launch_join_group(A, o2, l2, cache->n_live, own, grid, st) == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
   }
-  into(o1, l1);
+  A.out = o1;
+  A.lse = l1;
+  A.out_stride = (int64_t)a->n_q_heads * hd;
+  A.out_type = TRIA_F32;
+  if (!own_rows()) return TRIA_ERR_CUDA;
   if (run_attend(A, prefix, tp, a->round_keys != 0, L.shared, ws, st) != cudaSuccess) return TRIA_ERR_CUDA;
   JoinArgs J;
   memset(&J, 0, sizeof(J));

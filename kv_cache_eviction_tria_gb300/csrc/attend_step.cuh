@@ -187,6 +187,8 @@ __global__ void __launch_bounds__(StepShape<KT, VT, HD, NT>::kWarps * 32, 1)
   __shared__ int s_scan[40];
   __shared__ int s_flag[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t4 = lane & 3;
+  // (a kernel that does not need this one's results, see k_attend_group, may take SMs as they fall free)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the tile list: every unit has a tile at least (a token without rows
   // still gets its zeros), but those of sequences that take no part
