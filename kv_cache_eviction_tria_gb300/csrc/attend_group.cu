@@ -20,8 +20,9 @@
 // tile on their way into the swizzled ones (each row once for all columns:
 // the prompt kernel, whose units meet every row again and again, widens the planes
 // in memory instead): values rounded once, keys as the rounded value and the
-// remainder, which takes a product of its own (kLow). Two warpgroups share a
-// tile's softmax by columns and agree on its maximum through shared memory.
+// remainder, which takes a product of its own (kLow). Two warpgroups take the
+// tiles' softmax in turn, a thread per row, and hand the reference M on from tile
+// to tile through shared memory.
 //
 // Masks, junk in hidden rows, the lazy reference M and the bounded waits are those of
 // the prompt kernel.
@@ -41,13 +42,13 @@ struct GroupShape {
   static constexpr int kStage = BN * HD * 2;
   static constexpr int kStages = (HD == 64 ? 2 : 1) * (kQuant ? 4 : 6);
   static constexpr int kRaw = BN * HD;                     // bytes of a plane's q8_0 codes
-  static constexpr int kRawArea = kQuant ? 4 * kRaw : 0;   // two tiles of both planes, or four of 4-bit codes
+  static constexpr int kRawArea = kQuant ? 2 * kRaw : 0;   // of a plane: two tiles, or four of 4-bit codes
   static constexpr int kRawSlots = 4;
   static constexpr int kPosTiles = 8;                      // more tiles than the ring holds values of
   static constexpr int kScRow = HD / 16;                   // bytes of a row's block scales
-  static constexpr int oRing = 0, oRaw = kStages * kStage, oPos = oRaw + kRawArea, oScale = oPos + kPosTiles * BN * 4;
-  static constexpr int oTops = oScale + (kQuant ? 2 * BN * kScRow : 0);   // [parity][warpgroup][row]
-  static constexpr int oBar = oTops + 4 * 128 * 4;
+  static constexpr int oRing = 0, oRaw = kStages * kStage, oPos = oRaw + 2 * kRawArea, oScale = oPos + kPosTiles * BN * 4;
+  static constexpr int oRef = oScale + (kQuant ? 2 * BN * kScRow : 0);   // [warpgroup][row], then [parity][warpgroup][row]
+  static constexpr int oBar = oRef + 6 * 128 * 4;
   static constexpr int kSmem = oBar + 1024;
   // TMEM columns: score buffers, outputs, queries
   static constexpr int cS(int buf) { return buf * BN; }
@@ -56,75 +57,75 @@ struct GroupShape {
   static_assert(kSmem + (3 * kMaxSegments + 64) * 4 <= 227 * 1024, "shared memory");
 };
 
-constexpr int kGroupBars = 2 * 12 + 2 + 2 + 5 + 2 * 4;
+constexpr int kGroupBars = 2 * 12 + 2 + 2 + 5 + 4 * 4;
 struct GroupShared {
   uint32_t junk[12][4];                                    // rows of a value tile that held junk, by stage
-  int32_t lo[8], hi[8], c_lo[8], c_hi[8];                  // positions, a warp each
+  int32_t lo[8], hi[8], c_lo[4], c_hi[4];                  // positions, a warp each
   uint32_t tmem, abort;
 };
 static_assert(kGroupBars * 8 + sizeof(GroupShared) <= 1024, "barriers and shared state");
 
-// two warpgroups of softmax, two that fill tiles, one whose first warp issues the
-// products and whose second one starts the copies
-constexpr int kGroupThreads = 640, kGroupIssue = 16, kGroupLoad = 17, kConv = 256, kGroupRegs = 96;
+// two warpgroups of softmax, one that widens keys, one that widens or looks through
+// values, one whose first warp issues the products and whose next ones start copies
+constexpr int kGroupThreads = 640, kGroupIssue = 16, kGroupLoadK = 17, kGroupLoadV = 18, kConv = 128, kGroupRegs = 96;
 // registers of a thread in each, cut from what the block starts with
-constexpr int kGroupSoft = 120, kGroupConv = 88, kGroupOther = 64;
+constexpr int kGroupSoft = 128, kGroupConv = 80, kGroupOther = 64;
 static_assert(2 * kGroupSoft + 2 * kGroupConv + kGroupOther == 5 * kGroupRegs, "register shares");
 
-// Eight values of a quantised row: w their codes (q8_0: eight bytes; q4_0: eight
-// bytes of which the low halves count), h their scale. hi: code x scale as fp16,
-// lo: what fp16 leaves of it, which fp16 holds exactly (a scale is a multiple of
-// 2^-24 and a code whole, so 8 bits at most are left, all above 2^-24).
-template <bool kQ8, bool kLow>
-__device__ __forceinline__ void widen8(uint2 w, uint32_t h, uint32_t* hi, uint32_t* lo) {
-  const uint32_t sc = __byte_perm(h, h, 0x1010);
-  constexpr uint32_t bias = kQ8 ? 0x64806480u : 0x64086408u;
-  if (kQ8) {
-    w.x ^= 0x80808080u;                                    // 0x64, code + 128: 1152 + code
-    w.y ^= 0x80808080u;
-  }
-  const uint32_t b[4] = {__byte_perm(w.x, 0x64646464u, 0x4140), __byte_perm(w.x, 0x64646464u, 0x4342),
-                         __byte_perm(w.y, 0x64646464u, 0x4140), __byte_perm(w.y, 0x64646464u, 0x4342)};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t c;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(b[k]), "r"(bias));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(c), "r"(sc));
-    if constexpr (kLow) asm("{\n .reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;\n}\n" : "=r"(lo[k]) : "r"(c), "r"(sc), "r"(hi[k]));
-  }
-}
-
 // The rows of a tile of codes (rb bytes each) as fp16 tiles, by kConv threads; a
-// thread has the same eight dims of every kConv / (HD / 8)-th row. Rows from `rows` on
-// are zeros with kClean, which also replaces rows with junk and marks them.
-template <int HD, int BN, bool kQ8, bool kLow, bool kClean>
-__device__ __forceinline__ void widen_tile(const uint8_t* codes, int rb, const uint16_t* scale, uint8_t* hi_t, uint8_t* lo_t, int hd, int rows,
-                                           uint32_t* marks, int tid) {
-  constexpr int per = HD / 8, step = kConv / per, NB = HD / 32;
-  static_assert(step % 8 == 0 && BN % step == 0, "a thread's rows have one place in the swizzle");
+// thread has the same eight dims of every kConv / (HD / 8)-th row. hi_t: code x
+// scale, rounded; lo_t (kLow): what fp16 leaves of it, which fp16 holds exactly (a
+// scale is a multiple of 2^-24 and a code whole, so 8 bits at most are left,
+// all above 2^-24). With clean, rows from `rows` on become zeros, and so do pieces with
+// junk, whose rows are marked. (The kernel's roles together have to stay inside
+// the instruction cache: four rows at a time, types told apart in the loop.
+// Unrolled in all variants, 200 KB of code, a tile took twice as long.)
+template <int HD, int BN, bool kLow>
+__device__ __forceinline__ void widen_tile(const uint8_t* codes, int rb, bool q8, const uint16_t* scale, uint8_t* hi_t, uint8_t* lo_t, int hd,
+                                           bool clean, int rows, uint32_t* marks, int tid) {
+  constexpr int per = HD / 8, step = kConv / per, NB = HD / 32, kRows = BN / step < 4 ? BN / step : 4;
+  static_assert((step == 4 || step % 8 == 0) && BN % (step * kRows) == 0, "a thread's rows have one or two places in the swizzle");
   const int c = tid % per, r0 = tid / per;
-  const uint32_t to = (c >> 3) * (BN * 128) + swz(r0, c & 7);
-  const uint8_t* from = codes + r0 * rb + (kQ8 ? c * 8 : (c / 4) * 16 + (c & 1) * 8);
+  const uint32_t block = (c >> 3) * (BN * 128);
+  const uint32_t to[2] = {block + swz(r0, c & 7), step == 4 ? block + swz(r0 + 4, c & 7) - 4 * 128 : block + swz(r0, c & 7)};
   const bool there = 8 * c < hd;
+  const uint8_t* from = codes + r0 * rb + (there ? (q8 ? c * 8 : (c / 4) * 16 + (c & 1) * 8) : 0);
+  const uint16_t* sc_at = scale + r0 * NB + c / 4;
+  const uint32_t flip = q8 ? 0x80808080u : 0u, keep = q8 ? 0xFFFFFFFFu : 0x0F0F0F0Fu, bias = q8 ? 0x64806480u : 0x64086408u;
+  const int up = q8 ? 0 : (c & 2) * 2;
+#pragma unroll 1
+  for (int i0 = 0; i0 < BN / step; i0 += kRows) {
+    uint2 w[kRows];
+    uint32_t sc[kRows];
 #pragma unroll
-  for (int i = 0; i < BN / step; ++i) {
-    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-    if (there && (!kClean || r0 + i * step < rows)) {
-      uint2 w = *reinterpret_cast<const uint2*>(from + i * step * rb);
-      if constexpr (!kQ8) {
-        const int up = (c & 2) * 2;
-        w.x = (w.x >> up) & 0x0F0F0F0Fu;
-        w.y = (w.y >> up) & 0x0F0F0F0Fu;
-      }
-      widen8<kQ8, kLow>(w, scale[(r0 + i * step) * NB + c / 4], hi, lo);
-      if (kClean && (junk_h2(hi[0]) || junk_h2(hi[1]) || junk_h2(hi[2]) || junk_h2(hi[3]))) {
-        const int rr = r0 + i * step;
-        hi[0] = hi[1] = hi[2] = hi[3] = 0;
-        atomicOr(&marks[rr >> 5], 1u << (rr & 31));
-      }
+    for (int i = 0; i < kRows; ++i) {
+      w[i] = *reinterpret_cast<const uint2*>(from + (i0 + i) * step * rb);
+      sc[i] = there ? sc_at[(i0 + i) * step * NB] : 0u;
     }
-    *reinterpret_cast<uint4*>(hi_t + to + i * step * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if constexpr (kLow) *reinterpret_cast<uint4*>(lo_t + to + i * step * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      // 0x64, byte: 1024 + it, exactly; less the bias, the code
+      const uint32_t wx = ((w[i].x >> up) & keep) ^ flip, wy = ((w[i].y >> up) & keep) ^ flip, s2 = __byte_perm(sc[i], sc[i], 0x1010);
+      const uint32_t b[4] = {__byte_perm(wx, 0x64646464u, 0x4140), __byte_perm(wx, 0x64646464u, 0x4342),
+                             __byte_perm(wy, 0x64646464u, 0x4140), __byte_perm(wy, 0x64646464u, 0x4342)};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t v;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(b[k]), "r"(bias));
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(v), "r"(s2));
+        if constexpr (kLow) asm("{\n .reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;\n}\n" : "=r"(lo[k]) : "r"(v), "r"(s2), "r"(hi[k]));
+      }
+      const int rr = r0 + (i0 + i) * step;
+      if (clean) {
+        const bool junk = junk_h2(hi[0]) || junk_h2(hi[1]) || junk_h2(hi[2]) || junk_h2(hi[3]);
+        if (rr >= rows || junk) hi[0] = hi[1] = hi[2] = hi[3] = 0;
+        if (rr < rows && junk) atomicOr(&marks[rr >> 5], 1u << (rr & 31));
+      }
+      const uint32_t at = to[i & 1] + (i0 + i) * step * 128;
+      *reinterpret_cast<uint4*>(hi_t + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (kLow) *reinterpret_cast<uint4*>(lo_t + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
   }
 }
 
@@ -134,18 +135,19 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
                                                                    const __grid_constant__ CUtensorMap map_v) {
   using H = GroupShape<HD, kQuant>;
   // ring entries of tile j: keys P j, their remainders P j + 1 (kLow), values P j + P - 1
-  constexpr int P = kLow ? 3 : 2, BN = H::BN, ST = H::kStages, HALF = BN / 2;
+  constexpr int P = kLow ? 3 : 2, BN = H::BN, ST = H::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_first[kMaxSegments + 1], s_lo[kMaxSegments], s_hi[kMaxSegments];   // of units: first tile, rows
   __shared__ int s_scan[40];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
   // full: a tile is in the ring; empty: its products are done; s: scores; p: weights;
   // o: a tile's sums; f: the unit's last sums; q: queries; x: every product; v: values that are looked
-  // through before their tile is full; rf, re: codes are there, are used
+  // through before their tile is full; rf, re: codes (of keys, of values) are there, are used
   uint64_t *b_full = bar, *b_empty = bar + 12, *b_s = bar + 24, *b_p = b_s + 2, *b_o = b_p + 2, *b_f = b_o + 1, *b_q = b_f + 1,
-           *b_x = b_q + 1, *b_v = b_x + 1, *b_rf = b_v + 1, *b_re = b_rf + H::kRawSlots;
+           *b_x = b_q + 1, *b_v = b_x + 1, *b_rfk = b_v + 1, *b_rek = b_rfk + H::kRawSlots, *b_rfv = b_rek + H::kRawSlots,
+           *b_rev = b_rfv + H::kRawSlots;
   int32_t* s_pos = reinterpret_cast<int32_t*>(smem + H::oPos);
-  float* s_tops = reinterpret_cast<float*>(smem + H::oTops);
+  float* s_ref = reinterpret_cast<float*>(smem + H::oRef);
   GroupShared& X = *reinterpret_cast<GroupShared*>(smem + H::oBar + kGroupBars * 8);
   volatile uint32_t* s_abort = &X.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
@@ -154,6 +156,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   // ---- the tile list
   auto seq_of = [&](int unit) {
     int s = 0, hi_s = A.n_seqs - 1;
+#pragma unroll 1
     while (s < hi_s) {
       const int mid = (s + hi_s + 1) >> 1;
       if (A.seq[mid].unit0 <= unit) s = mid; else hi_s = mid - 1;
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b_s[i], 1);
-      mbar_init(&b_p[i], 256);
+      mbar_init(&b_p[i], 128);
     }
     mbar_init(b_o, 1);
     mbar_init(b_f, 1);
@@ -227,8 +230,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     mbar_init(b_v, 1);
 #pragma unroll
     for (int i = 0; i < H::kRawSlots; ++i) {
-      mbar_init(&b_rf[i], 1);
-      mbar_init(&b_re[i], 1);
+      mbar_init(&b_rfk[i], 1);
+      mbar_init(&b_rek[i], 1);
+      mbar_init(&b_rfv[i], 1);
+      mbar_init(&b_rev[i], 1);
     }
     fence_mbar_init();
   }
@@ -247,6 +252,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   const int begin = (int)(blockIdx.x * total / workers), end = (int)((blockIdx.x + 1) * total / workers);
   auto unit_at = [&](int tile) {                           // the last unit that starts at or before it
     int u = 0, hi_u = A.units - 1;
+#pragma unroll 1
     while (u < hi_u) {
       const int mid = (u + hi_u + 1) >> 1;
       if (s_first[mid] <= tile) u = mid; else hi_u = mid - 1;
@@ -285,23 +291,29 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   // bounded waits, as in the prompt kernel: after one gave up nobody waits any more, no
   // results are written, and every role runs its loops to the end
   auto wait = [&](uint64_t* b, uint32_t parity) {
+#pragma unroll 1
     for (int it = 0; it < kWaitLimit; ++it)
       if (mbar_try_wait(b, parity) || *s_abort) return;
     *s_abort = 1;
   };
-  auto wait_warp = [&](uint64_t* b, uint32_t parity) {
-    const int r = mbar_wait_warp(b, parity, s_abort, kWaitLimit);
-    if (r == 0) *s_abort = 1;
-    return r > 0;
+  auto wait_warp = [&](uint64_t* b, uint32_t parity) {     // one answer for all lanes, see mbar_wait_warp
+#pragma unroll 1
+    for (int it = 0; it < kWaitLimit; ++it) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+      if (__any_sync(0xffffffffu, *s_abort != 0)) return false;
+    }
+    *s_abort = 1;
+    return false;
   };
   auto stage = [&](int e) { return smem + H::oRing + (e % ST) * H::kStage; };
   auto free_stage = [&](int e) {
     if (e >= ST) wait(&b_empty[e % ST], ((e / ST) - 1) & 1);
   };
   const int tiles = end - begin;
-  const int slots = kQuant && (!kq || A.k_type == TRIA_Q4_0) && (!vq || A.v_type == TRIA_Q4_0) ? 4 : 2;
-  const int raw_v = H::kRawArea / slots / 2;               // a slot: codes of keys, then of values
-  auto raw = [&](int j) { return smem + H::oRaw + (j % slots) * (2 * raw_v); };
+  // codes as they lie: two tiles of a plane, or four of 4-bit ones
+  const int slots_k = A.k_type == TRIA_Q4_0 ? 4 : 2, slots_v = A.v_type == TRIA_Q4_0 ? 4 : 2;
+  auto raw_k = [&](int j) { return smem + H::oRaw + (j % slots_k) * (H::kRawArea / slots_k); };
+  auto raw_v = [&](int j) { return smem + H::oRaw + H::kRawArea + (j % slots_v) * (H::kRawArea / slots_v); };
   const int k_rb = A.k_type == TRIA_Q8_0 ? A.hd : A.hd / 2, v_rb = A.v_type == TRIA_Q8_0 ? A.hd : A.hd / 2;
 
   if (wg >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupOther));
@@ -343,6 +355,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       if (ok && elect_one()) scores(t, e % ST, (e + 1) % ST);
       __syncwarp();
     };
+#pragma unroll 1
     for (int u = unit_a; ok && j < tiles; ++u) {
       const int nt = min(end, s_first[u + 1]) - max(begin, s_first[u]);
       if (nt <= 0) continue;
@@ -363,52 +376,106 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     }
     // nothing may be running when the accumulators are given back
     if (elect_one()) tc_commit(b_x);
+#pragma unroll 1
     for (int it = 0; it < kWaitLimit && !mbar_try_wait(b_x, 0); ++it) {
     }
-  } else if (warp == kGroupLoad) {
-    // ---- key tiles of fp16 planes, codes of quantised ones
-    if (lane == 0) {
+  } else if (warp == kGroupLoadK || warp == kGroupLoadV) {
+    // ---- key tiles of fp16 planes, codes of quantised ones (value tiles of fp16 planes are fetched by those who look
+    // through them)
+    const bool keys = warp == kGroupLoadK, codes = keys ? kq : vq;
+    if (lane == 0 && (keys || codes)) {
+      const uint8_t* plane = keys ? A.k : A.v;
+      const int rb = keys ? k_rb : v_rb, slots = keys ? slots_k : slots_v;
+      uint64_t *full = keys ? b_rfk : b_rfv, *empty = keys ? b_rek : b_rev;
       int j = 0;
+#pragma unroll 1
       for (int u = unit_a; j < tiles; ++u) {
         if (min(end, s_first[u + 1]) <= max(begin, s_first[u])) continue;
         const Unit U = unit_of(u);
+#pragma unroll 1
         for (int t = U.t0; t < U.t1; ++t, ++j) {
           int rows;
           const int r = tile_row(u, t, rows);
-          if (!kq) {
+          if (!codes) {
             // hidden keys, and those past the last row, only reach logits that the mask replaces
             const int e = P * j;
             free_stage(e);
             if (!*s_abort) copy_tile<HD, BN>(stage(e), &map_k, U.row0 + r, &b_full[e % ST]);
-          }
-          if constexpr (kQuant) {
+          } else {
             const int x = j % slots;
-            if (j >= slots) wait(&b_re[x], ((j / slots) - 1) & 1);
+            if (j >= slots) wait(&empty[x], ((j / slots) - 1) & 1);
             if (*s_abort) continue;
-            mbar_arrive_expect_tx(&b_rf[x], (kq ? rows * k_rb : 0) + (vq ? rows * v_rb : 0));
-            if (kq) bulk_g2s(raw(j), A.k + (U.row0 + r) * k_rb, rows * k_rb, &b_rf[x]);
-            if (vq) bulk_g2s(raw(j) + raw_v, A.v + (U.row0 + r) * v_rb, rows * v_rb, &b_rf[x]);
+            mbar_arrive_expect_tx(&full[x], rows * rb);
+            bulk_g2s(keys ? raw_k(j) : raw_v(j), plane + (U.row0 + r) * rb, rows * rb, &full[x]);
           }
         }
       }
       if (*s_abort) {                                      // waits, bounded, for copies still on their way
         for (int e = max(0, P * tiles - ST); e < P * tiles; ++e)
-          for (int it = 0; it < 1024 && !kq && e % P == 0 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
+#pragma unroll 1
+          for (int it = 0; it < 1024 && !codes && e % P == 0 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
           }
-        if constexpr (kQuant)
-          for (int i = max(0, tiles - slots); i < tiles; ++i)
-            for (int it = 0; it < 1024 && !mbar_try_wait(&b_rf[i % slots], (i / slots) & 1); ++it) {
-            }
+        for (int i = max(0, tiles - slots); i < tiles; ++i)
+#pragma unroll 1
+          for (int it = 0; it < 1024 && codes && !mbar_try_wait(&full[i % slots], (i / slots) & 1); ++it) {
+          }
       }
     }
-  } else if (wg >= 2 && wg < 4) {
-    // ---- positions; value tiles of fp16 planes; codes into tiles
-    const int tid = threadIdx.x & 255;
+  } else if (wg == 2) {
+    // ---- codes of keys into tiles
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupConv));
-    uint16_t* s_scale = reinterpret_cast<uint16_t*>(smem + H::oScale);
+    const int tid = threadIdx.x & 127;
+    if constexpr (kQuant) {
+      if (kq) {
+        uint16_t* s_scale = reinterpret_cast<uint16_t*>(smem + H::oScale);
+        constexpr int NB = HD / 32;
+        const int nb = A.hd / 32;
+        int j = 0;
+#pragma unroll 1
+        for (int u = unit_a; j < tiles; ++u) {
+          if (min(end, s_first[u + 1]) <= max(begin, s_first[u])) continue;
+          const Unit U = unit_of(u);
+          uint16_t next[NB];                               // scales of this thread's row of the tile to come
+          auto fetch = [&](int t) {
+            int rows = 0;
+            const int r = t < U.t1 ? tile_row(u, t, rows) : 0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              next[b] = tid < rows && b < nb ? __ldg(reinterpret_cast<const uint16_t*>(A.ks) + (U.row0 + r + tid) * nb + b) : (uint16_t)0;
+          };
+          fetch(U.t0);
+#pragma unroll 1
+          for (int t = U.t0; t < U.t1; ++t, ++j) {
+            if (tid < BN)
+#pragma unroll
+              for (int b = 0; b < NB; ++b) s_scale[tid * NB + b] = next[b];
+            fetch(t + 1);
+            const int e = P * j;
+            wait(&b_rfk[j % slots_k], (j / slots_k) & 1);
+            free_stage(e);
+            if (kLow) free_stage(e + 1);
+            asm volatile("bar.sync 3, 128;" ::: "memory");   // scales
+            widen_tile<HD, BN, kLow>(raw_k(j), k_rb, A.k_type == TRIA_Q8_0, s_scale, stage(e), stage(e + 1), A.hd, false, BN, nullptr, tid);
+            fence_proxy_async_smem();
+            asm volatile("bar.sync 3, 128;" ::: "memory");
+            if (tid == 0) {
+              mbar_arrive(&b_full[e % ST]);
+              if (kLow) mbar_arrive(&b_full[(e + 1) % ST]);
+              mbar_arrive(&b_rek[j % slots_k]);
+            }
+          }
+        }
+      }
+    }
+  } else if (wg == 3) {
+    // ---- positions; codes of values into tiles, or value tiles looked through
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupConv));
+    const int tid = threadIdx.x & 127;
     constexpr int NB = HD / 32;
+    uint16_t* s_scale = reinterpret_cast<uint16_t*>(smem + H::oScale) + BN * NB;
     const int nb = A.hd / 32;
     int j = 0, looked = 0;
+#pragma unroll 1
     for (int u = unit_a; j < tiles; ++u) {
       if (min(end, s_first[u + 1]) <= max(begin, s_first[u])) continue;
       const Unit U = unit_of(u);
@@ -417,131 +484,106 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       // the tokens' positions, and whether they hide rows
       const int tok_a = U.c0 / A.G, tok_b = (U.c0 + U.ncol - 1) / A.G;
       int pl = INT32_MAX, ph = INT32_MIN;
-      if (tok_a + tid <= tok_b) pl = ph = A.pos[S.tok0 + tok_a + tid];
+      if (tok_a + tid <= tok_b) pl = ph = A.pos[S.tok0 + tok_a + tid];   // (128 columns at most)
       const int newest = s_hi[u] > 0 ? rpos[s_hi[u] - 1] : INT32_MIN;
-      pl = __reduce_min_sync(0xffffffffu, pl);
-      ph = __reduce_max_sync(0xffffffffu, ph);
-      if (lane == 0) {
-        X.c_lo[warp & 7] = pl;
-        X.c_hi[warp & 7] = ph;
-      }
-      asm volatile("bar.sync 3, 256;" ::: "memory");
-      // (128 columns at most, so the first four warps hold all of the tokens)
-      const int pmin = min(min(X.c_lo[0], X.c_lo[1]), min(X.c_lo[2], X.c_lo[3]));
-      const int pmax = max(max(X.c_hi[0], X.c_hi[1]), max(X.c_hi[2], X.c_hi[3]));
-      const bool need_pos = A.window > 0 || newest > pmin;
-      int next_pos = INT32_MAX;                            // of this thread's row of the tile to come
-      uint16_t next_k[NB], next_v[NB];                     // and its scales
+      uint16_t next[NB];                                   // scales and position of this thread's row of the tile to come
+      int next_pos = INT32_MAX;
+      bool need_pos = true;                                // (until it is known)
       auto fetch = [&](int t) {
         int rows = 0;
         const int r = t < U.t1 ? tile_row(u, t, rows) : 0;
         next_pos = need_pos && tid < rows ? rpos[r + tid] : INT32_MAX;
         if constexpr (kQuant) {
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int64_t at = (U.row0 + r + tid) * nb + b;
-            const bool on = tid < rows && b < nb;
-            next_k[b] = kq && on ? __ldg(reinterpret_cast<const uint16_t*>(A.ks) + at) : (uint16_t)0;
-            next_v[b] = vq && on ? __ldg(reinterpret_cast<const uint16_t*>(A.vs) + at) : (uint16_t)0;
-          }
+          for (int b = 0; b < NB; ++b)
+            next[b] = vq && tid < rows && b < nb ? __ldg(reinterpret_cast<const uint16_t*>(A.vs) + (U.row0 + r + tid) * nb + b) : (uint16_t)0;
         }
       };
       fetch(U.t0);
+      pl = __reduce_min_sync(0xffffffffu, pl);
+      ph = __reduce_max_sync(0xffffffffu, ph);
+      if (lane == 0) {
+        X.c_lo[warp & 3] = pl;
+        X.c_hi[warp & 3] = ph;
+      }
+      asm volatile("bar.sync 6, 128;" ::: "memory");
+      const int pmin = min(min(X.c_lo[0], X.c_lo[1]), min(X.c_lo[2], X.c_lo[3]));
+      const int pmax = max(max(X.c_hi[0], X.c_hi[1]), max(X.c_hi[2], X.c_hi[3]));
+      need_pos = A.window > 0 || newest > pmin;
+#pragma unroll 1
       for (int t = U.t0; t < U.t1; ++t, ++j) {
         int rows;
         const int r = tile_row(u, t, rows), ev = P * j + P - 1;
-        if constexpr (kQuant) {
-          if (tid < BN)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              s_scale[tid * NB + b] = next_k[b];
-              s_scale[(BN + tid) * NB + b] = next_v[b];
-            }
-        }
-        const int pos_now = next_pos;
-        fetch(t + 1);
-        if constexpr (kQuant) {
-          wait(&b_rf[j % slots], (j / slots) & 1);
-          asm volatile("bar.sync 3, 256;" ::: "memory");   // scales
-          if (kq) {
-            const int e = P * j;
-            free_stage(e);
-            if (kLow) free_stage(e + 1);
-            __syncwarp();
-            if (A.k_type == TRIA_Q8_0)
-              widen_tile<HD, BN, true, kLow, false>(raw(j), k_rb, s_scale, stage(e), stage(e + 1), A.hd, rows, nullptr, tid);
-            else
-              widen_tile<HD, BN, false, kLow, false>(raw(j), k_rb, s_scale, stage(e), stage(e + 1), A.hd, rows, nullptr, tid);
-            fence_proxy_async_smem();
-            asm volatile("bar.sync 3, 256;" ::: "memory");
-            if (tid == 0) {
-              mbar_arrive(&b_full[e % ST]);
-              if (kLow) mbar_arrive(&b_full[(e + 1) % ST]);
-            }
-          }
-        }
+        // positions and marks go with the value tile, which stays until the weights are used
         free_stage(ev);
         __syncwarp();
-        // positions and marks go with the value tile, which stays until the weights are used
         int32_t* tp = s_pos + (j % H::kPosTiles) * BN;
-        if (need_pos && tid < BN) tp[tid] = pos_now;
+        if (need_pos && tid < BN) tp[tid] = next_pos;
         if (tid < 4) X.junk[ev % ST][tid] = 0;
-        asm volatile("bar.sync 3, 256;" ::: "memory");
+        if constexpr (kQuant) {
+          if (vq && tid < BN)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) s_scale[tid * NB + b] = next[b];
+        }
+        fetch(t + 1);
+        if (kQuant && vq) wait(&b_rfv[j % slots_v], (j / slots_v) & 1);
+        asm volatile("bar.sync 6, 128;" ::: "memory");
         const bool all = rows == BN && (!need_pos || (tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window ||
                                                                             r + BN <= A.sink)));   // seen whole by every token
-        bool filled = false;
-        if constexpr (kQuant) {
-          if (vq) {
-            filled = true;
-            const uint8_t* codes = raw(j) + raw_v;
-            uint32_t* marks = X.junk[ev % ST];
-            if (A.v_type == TRIA_Q8_0) {
-              if (all) widen_tile<HD, BN, true, false, false>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
-              else widen_tile<HD, BN, true, false, true>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
-            } else {
-              if (all) widen_tile<HD, BN, false, false, false>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
-              else widen_tile<HD, BN, false, false, true>(codes, v_rb, s_scale + BN * NB, stage(ev), nullptr, A.hd, rows, marks, tid);
-            }
-          }
-        }
-        if (!filled) {
+        if (kQuant && vq) {
+          widen_tile<HD, BN, false>(raw_v(j), v_rb, A.v_type == TRIA_Q8_0, s_scale, stage(ev), nullptr, A.hd, !all, rows, X.junk[ev % ST], tid);
+        } else {
           if (tid == 0 && !*s_abort) copy_tile<HD, BN>(stage(ev), &map_v, U.row0 + r, all ? &b_full[ev % ST] : b_v);
-          if (!all) {
-            wait(b_v, looked & 1);
-            __syncwarp();
-            ++looked;
-            clean_tile<HD, BN, kConv>(stage(ev), rows, X.junk[ev % ST], tid);
-            filled = true;
-          }
+          if (all) continue;
+          wait(b_v, looked & 1);
+          __syncwarp();
+          ++looked;
+          clean_tile<HD, BN, kConv>(stage(ev), rows, X.junk[ev % ST], tid);
         }
-        if (filled || kQuant) {
-          if (filled) fence_proxy_async_smem();
-          asm volatile("bar.sync 3, 256;" ::: "memory");
-          if (tid == 0) {
-            if (filled) mbar_arrive(&b_full[ev % ST]);
-            if (kQuant) mbar_arrive(&b_re[j % slots]);
-          }
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 6, 128;" ::: "memory");
+        if (tid == 0) {
+          mbar_arrive(&b_full[ev % ST]);
+          if (kQuant && vq) mbar_arrive(&b_rev[j % slots_v]);
         }
       }
     }
     if (*s_abort && tid == 0 && !vq)                       // value copies still on their way
       for (int e = max(0, P * tiles - ST); e < P * tiles; ++e)
+#pragma unroll 1
         for (int it = 0; it < 1024 && e % P == P - 1 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
         }
   } else if (wg < 2) {
-    // ---- softmax: a thread per row and half of a tile's columns
+    // ---- softmax: a thread per row; the warpgroups take tiles in turn
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupSoft));
     const int m = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    auto meet = [&] { asm volatile("bar.sync 4, 256;" ::: "memory"); };
-    int j = 0, nu = 0, turn = 0;                           // turn: which half of the exchange is next
-    auto swap = [&](float x) {                             // the other half's value of this row
-      float* at = s_tops + (turn & 1) * 256;
+    // Both add to one O, so they have to agree on the reference M: a tile's is
+    // handed on before its weights are made. Barrier 4 + w: warpgroup w has handed
+    // on (and does so again only after the other one has).
+    auto handed = [&] {                                    // waits for the other's
+      __syncwarp();
+      if (wg == 0) asm volatile("bar.sync 5, 256;" ::: "memory");
+      else asm volatile("bar.sync 4, 256;" ::: "memory");
+      return s_ref[(wg ^ 1) * 128 + m];
+    };
+    auto hand = [&](float x) {
+      s_ref[wg * 128 + m] = x;
+      __syncwarp();
+      if (wg == 0) asm volatile("bar.arrive 4, 256;" ::: "memory");
+      else asm volatile("bar.arrive 5, 256;" ::: "memory");
+    };
+    int turn = 0;
+    auto swap = [&](float x) {                             // the other's value of this row
+      float* at = s_ref + 256 + (turn & 1) * 256;
       at[wg * 128 + m] = x;
-      meet();
+      __syncwarp();
+      asm volatile("bar.sync 7, 256;" ::: "memory");
       ++turn;
       return at[(wg ^ 1) * 128 + m];
     };
+    int j = 0, nu = 0;
+#pragma unroll 1
     for (int u = unit_a; j < tiles; ++u) {
       if (min(end, s_first[u + 1]) <= max(begin, s_first[u])) continue;
       const Unit U = unit_of(u);
@@ -593,8 +635,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         }
       }
       sl = fmaxf(sl, 0x1p-126f);                           // (times -inf stays -inf)
-      const int pmin = min(min(X.lo[4 * wg], X.lo[4 * wg + 1]), min(X.lo[4 * wg + 2], X.lo[4 * wg + 3]));
-      const int pmax = max(max(X.hi[4 * wg], X.hi[4 * wg + 1]), max(X.hi[4 * wg + 2], X.hi[4 * wg + 3]));
+      // (of the other warpgroup's warps, which have the same rows: what it wrote before the swap)
+      const int o4 = 4 * (wg ^ 1);
+      const int pmin = min(min(X.lo[o4], X.lo[o4 + 1]), min(X.lo[o4 + 2], X.lo[o4 + 3]));
+      const int pmax = max(max(X.hi[o4], X.hi[o4 + 1]), max(X.hi[o4 + 2], X.hi[o4 + 3]));
       const bool need_pos = A.window > 0 || newest > pmin;
 #pragma unroll
       for (int c = 0; c < kPieces; c += 4) {
@@ -607,17 +651,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       mbar_arrive(b_q);
       // rows at or before it are outside the window
       const int pold = A.window > 0 ? (int)max((int64_t)INT32_MIN, (int64_t)p - A.window) : INT32_MIN;
-      const uint32_t to = lane_base + H::cO + wg * (HD / 2);
+      const uint32_t to = lane_base + H::cO;
       float M = -INFINITY, l = 0.f;
       bool poison = false;
+#pragma unroll 1
       for (int t = U.t0; t < U.t1; ++t, ++j) {
-        wait(&b_s[j & 1], (j >> 1) & 1);
+        if ((j & 1) != wg) continue;
+        wait(&b_s[wg], (j >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        const uint32_t ts = lane_base + H::cS(j & 1);
-        uint32_t x[HALF];
-#pragma unroll
-        for (int c = 0; c < HALF; c += 32) tc_ld32(x + c, ts + wg * HALF + c);
+        const uint32_t ts = lane_base + H::cS(wg);
         int rows;
         const int r = tile_row(u, t, rows);
         bool masked = rows < BN;
@@ -629,15 +672,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         const int32_t* tp = s_pos + (j % H::kPosTiles) * BN;
         if (need_pos)
           masked = masked || tp[BN - 1] > pmin || (A.window > 0 && (int64_t)pmax - tp[0] >= A.window && r + BN > A.sink);
-        tc_wait_ld();
-#pragma unroll
-        for (int c = 0; c < HALF; c += 32) tc_pin(x + c);
+        // the row's token sees columns [cl, ch) and, of the first rows, [0, cf)
+        int cl = 0, ch = BN, cf = 0;
         if (masked) {
-          // the row's token sees columns [cl, ch) and, of the first rows, [0, cf)
-          int cl = 0, ch = rows, cf = 0;
+          ch = rows;
           if (need_pos) {
             auto upto = [&](int pos) {                     // columns with a position <= pos
               int a = 0, b = rows;
+#pragma unroll 1
               while (a < b) {
                 const int mid = (a + b) >> 1;
                 if (tp[mid] <= pos) a = mid + 1; else b = mid;
@@ -650,71 +692,102 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
               cf = min(ch, max(0, A.sink - r));
             }
           }
-#pragma unroll
-          for (int c = 0; c < HALF; ++c) {
-            const int at = wg * HALF + c;
-            if (at >= ch || (at < cl && at >= cf)) x[c] = 0xFF800000u;   // -inf
-          }
           const uint32_t* jm = X.junk[ev % ST];
           if (jm[0] | jm[1] | jm[2] | jm[3])
-            for (int c = wg * HALF; c < min(rows, (wg + 1) * HALF); ++c)
+#pragma unroll 1
+            for (int c = 0; c < rows; ++c)
               if (((jm[c >> 5] >> (c & 31)) & 1u) && c < ch && (c >= cl || c < cf)) poison = true;
         }
-        float tops[4];
+        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };   // bits of columns < n
+        auto hide = [&](uint32_t* x, int c0) {
+          const uint32_t seen = (below(ch - c0) & ~below(cl - c0)) | below(cf - c0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tops[k] = __uint_as_float(x[k]);
-#pragma unroll
-        for (int c = 4; c < HALF; ++c) tops[c & 3] = fmaxf(tops[c & 3], __uint_as_float(x[c]));
-        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        top = fmaxf(top, swap(top));                       // (both halves' scores are in registers: weights may be written)
-        top = top * sl - kShift;
-        const bool move = (top > M + kLazy || M == -INFINITY) && top > -INFINITY;
-        if (__any_sync(0xffffffffu, move)) {
-          float a = 1.f;
-          if (move) {
-            a = exp2_fast(M - top);
-            M = top;
-            l *= a;
-          }
-          if (t > U.t0) {
-            wait(b_o, (j - 1) & 1);                        // the sums of the tile before may be running
-            __syncwarp();
-            tc_fence_after();
+          for (int c = 0; c < 32; ++c)
+            if (!((seen >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
+        };
+        // the largest logit; the scores are loaded once more for the weights, which leaves registers for both
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-            for (int c = 0; c < HD / 2; c += 16) {
-              uint32_t o[16];
-              tc_ld16(o, to + c);
-              tc_wait_ld();
-              tc_pin16(o);
+        for (int c = 0; c < BN; c += 64) {
+          uint32_t x[64];
+          tc_ld32(x, ts + c);
+          tc_ld32(x + 32, ts + c + 32);
+          tc_wait_ld();
+          tc_pin(x);
+          tc_pin(x + 32);
+          if (masked) {
+            hide(x, c);
+            hide(x + 32, c + 32);
+          }
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-              tc_st16(to + c, o);
-            }
+          for (int k = 0; k < 64; k += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tops[i] = fmaxf(fmaxf(tops[i], __uint_as_float(x[k + i])), __uint_as_float(x[k + 4 + i]));
+        }
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        top = top * sl - kShift;
+        const float before = t > U.t0 ? handed() : -INFINITY;   // M after the tile before
+        const bool move = (top > before + kLazy || before == -INFINITY) && top > -INFINITY;
+        const float now = move ? top : before;
+        if (t + 1 < U.t1) hand(now);
+        if (now > M) {                                     // (since this warpgroup's last tile)
+          l *= exp2_fast(M - now);
+          M = now;
+        }
+        if (t > U.t0 && __any_sync(0xffffffffu, move)) {
+          wait(b_o, (j - 1) & 1);                          // the sums of the tile before may be running
+          __syncwarp();
+          tc_fence_after();
+          const float a = move ? exp2_fast(before - now) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 16) {
+            uint32_t o[16];
+            tc_ld16(o, to + c);
+            tc_wait_ld();
+            tc_pin16(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            tc_st16(to + c, o);
           }
         }
         const float mb = M == -INFINITY ? 0.f : M;
         const float2 sl2 = make_float2(sl, sl), mb2 = make_float2(-mb, -mb);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < HALF; c += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), sl2, mb2);
-            e.x = exp2_fast(e.x);
-            e.y = exp2_fast(e.y);
-            ls[k & 1] = __fadd2_rn(ls[k & 1], e);
-            const __half2 h = __floats2half2_rn(e.x, e.y);
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 64) {
+          uint32_t x[64];
+          tc_ld32(x, ts + c);
+          tc_ld32(x + 32, ts + c + 32);
+          tc_wait_ld();
+          tc_pin(x);
+          tc_pin(x + 32);
+          if (masked) {
+            hide(x, c);
+            hide(x + 32, c + 32);
           }
-          tc_st16(ts + (wg * HALF + c) / 2, w);
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(x[h + 2 * k]), __uint_as_float(x[h + 2 * k + 1])), sl2, mb2);
+              e.x = exp2_fast(e.x);
+              e.y = exp2_fast(e.y);
+              ls[k & 1] = __fadd2_rn(ls[k & 1], e);
+              const __half2 y = __floats2half2_rn(e.x, e.y);
+              w[k] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            tc_st16(ts + (c + h) / 2, w);                  // (over scores that have been loaded)
+          }
         }
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&b_p[j & 1]);
+        mbar_arrive(&b_p[wg]);
       }
-      // ---- the unit's part
+      // ---- the unit's part: each warpgroup writes half of the dims
+      const float M2 = swap(M), top = fmaxf(M, M2);        // (the last tile's is the larger one)
+      l = M == -INFINITY ? l : l * exp2_fast(M - top);
       l += swap(l);
       poison = swap(poison ? 1.f : 0.f) != 0.f || poison;
       wait(b_f, nu & 1);
@@ -723,18 +796,18 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       float* slot = A.part + (int64_t)(u + (int)blockIdx.x) * 128 * (HD + 2) + m;
       const bool write = __all_sync(0xffffffffu, *s_abort == 0);
       if (write && wg == 0 && on) {
-        slot[0] = M;
+        slot[0] = top;
         slot[128] = l;
       }
 #pragma unroll 1
-      for (int c = 0; c < HD / 2; c += 32) {
+      for (int c = wg * (HD / 2); c < (wg + 1) * (HD / 2); c += 32) {
         uint32_t o[32];
         tc_ld32(o, to + c);
         tc_wait_ld();
         tc_pin(o);
         if (write && on)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) slot[(int64_t)(2 + wg * (HD / 2) + c + k) * 128] = poison ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[k]);
+          for (int k = 0; k < 32; ++k) slot[(int64_t)(2 + c + k) * 128] = poison ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[k]);
       }
       tc_fence_before();
       ++nu;
@@ -761,6 +834,7 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
   __shared__ float s_m[kJoinQuarters][128], s_l[kJoinQuarters][128], s_v[kJoinQuarters][kJoinDims][128];
   const int u = blockIdx.x, d0 = blockIdx.y * kJoinDims, c = threadIdx.x & 127, quarter = threadIdx.x >> 7;
   int s = 0, hi_s = A.n_seqs - 1;
+#pragma unroll 1
   while (s < hi_s) {
     const int mid = (s + hi_s + 1) >> 1;
     if (A.seq[mid].unit0 <= u) s = mid; else hi_s = mid - 1;
