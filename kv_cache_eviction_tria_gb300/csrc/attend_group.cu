@@ -20,9 +20,14 @@
 // tile on their way into the swizzled ones (each row once for all columns:
 // the prompt kernel, whose units meet every row again and again, widens the planes
 // in memory instead): values rounded once, keys as the rounded value and the
-// remainder, which takes a product of its own (kLow). Two warpgroups take the
-// tiles' softmax in turn, a thread per row, and hand the reference M on from tile
-// to tile through shared memory.
+// remainder, which takes a product of its own (kLow).
+//
+// A tile's scores are two halves by rows, each with a warpgroup of its own (a
+// thread per column of the unit), two score buffers and products of its own, so that a
+// warpgroup's next scores are made while it is in its softmax. Both halves
+// add to one O, so the reference M is handed on from half to half through
+// shared memory, before the weights are made. (Warpgroups that took whole tiles in
+// turn waited for their scores: 2.3 us a tile of q8_0 rows.)
 //
 // Masks, junk in hidden rows, the lazy reference M and the bounded waits are those of
 // the prompt kernel.
@@ -51,13 +56,13 @@ struct GroupShape {
   static constexpr int oBar = oRef + 6 * 128 * 4;
   static constexpr int kSmem = oBar + 1024;
   // TMEM columns: score buffers, outputs, queries
-  static constexpr int cS(int buf) { return buf * BN; }
+  static constexpr int cS(int half, int buf) { return (2 * half + buf) * (BN / 2); }
   static constexpr int cO = 2 * BN, cQ = cO + HD;
   static_assert(cQ + HD / 2 <= 512, "TMEM");
   static_assert(kSmem + (3 * kMaxSegments + 64) * 4 <= 227 * 1024, "shared memory");
 };
 
-constexpr int kGroupBars = 2 * 12 + 2 + 2 + 5 + 4 * 4;
+constexpr int kGroupBars = 2 * 12 + 4 + 4 + 5 + 4 * 4;
 struct GroupShared {
   uint32_t junk[12][4];                                    // rows of a value tile that held junk, by stage
   int32_t lo[8], hi[8], c_lo[4], c_hi[4];                  // positions, a warp each
@@ -140,10 +145,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   __shared__ int s_first[kMaxSegments + 1], s_lo[kMaxSegments], s_hi[kMaxSegments];   // of units: first tile, rows
   __shared__ int s_scan[40];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
-  // full: a tile is in the ring; empty: its products are done; s: scores; p: weights;
-  // o: a tile's sums; f: the unit's last sums; q: queries; x: every product; v: values that are looked
+  // full: a tile is in the ring; empty: its products are done; s: scores; p: weights (of half h
+  // in buffer b: 2 h + b); o: a half's sums; f: the unit's last sums; q: queries; x: every product; v: values that are looked
   // through before their tile is full; rf, re: codes (of keys, of values) are there, are used
-  uint64_t *b_full = bar, *b_empty = bar + 12, *b_s = bar + 24, *b_p = b_s + 2, *b_o = b_p + 2, *b_f = b_o + 1, *b_q = b_f + 1,
+  uint64_t *b_full = bar, *b_empty = bar + 12, *b_s = bar + 24, *b_p = b_s + 4, *b_o = b_p + 4, *b_f = b_o + 1, *b_q = b_f + 1,
            *b_x = b_q + 1, *b_v = b_x + 1, *b_rfk = b_v + 1, *b_rek = b_rfk + H::kRawSlots, *b_rfv = b_rek + H::kRawSlots,
            *b_rev = b_rfv + H::kRawSlots;
   int32_t* s_pos = reinterpret_cast<int32_t*>(smem + H::oPos);
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       mbar_init(&b_empty[i], 1);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&b_s[i], 1);
       mbar_init(&b_p[i], 128);
     }
@@ -322,37 +327,42 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     // such a form, see the prompt kernel)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dk = tile_desc(smem_u32(smem + H::oRing), 16), dv = tile_desc(smem_u32(smem + H::oRing), BN * 128);
-    auto scores = [&](int j, int st, int sl) {
-      const uint64_t b = dk + (uint64_t)(st * (H::kStage / 16));
-      const uint32_t d = tm + H::cS(j & 1), a = tm + H::cQ;
+    // (a half's rows are 8 groups of eight further on in the keys' tile, BN / 32 steps of 16 in the values')
+    auto scores = [&](int h, int buf, int st, int sl) {
+      const uint64_t b = dk + (uint64_t)(st * (H::kStage / 16) + h * (BN / 2) * 8);
+      const uint32_t d = tm + H::cS(h, buf), a = tm + H::cQ;
 #pragma unroll
       for (int k = 0; k < HD / 16; ++k)
-        tc_mma_ts(d, a + k * 8, b + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN, false), k > 0);
+        tc_mma_ts(d, a + k * 8, b + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN / 2, false), k > 0);
       if constexpr (kLow) {
-        const uint64_t bl = dk + (uint64_t)(sl * (H::kStage / 16));
+        const uint64_t bl = dk + (uint64_t)(sl * (H::kStage / 16) + h * (BN / 2) * 8);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
-          tc_mma_ts(d, a + k * 8, bl + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN, false), 1);
+          tc_mma_ts(d, a + k * 8, bl + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN / 2, false), 1);
       }
-      tc_commit(&b_s[j & 1]);
-      tc_commit(&b_empty[st]);
-      if (kLow) tc_commit(&b_empty[sl]);
+      tc_commit(&b_s[2 * h + buf]);
+      if (h == 1) {
+        tc_commit(&b_empty[st]);
+        if (kLow) tc_commit(&b_empty[sl]);
+      }
     };
-    auto sums = [&](int j, int st, bool add) {
-      const uint64_t b = dv + (uint64_t)(st * (H::kStage / 16));
-      const uint32_t d = tm + H::cO, a = tm + H::cS(j & 1);
+    auto sums = [&](int h, int buf, int st, bool add) {
+      const uint64_t b = dv + (uint64_t)(st * (H::kStage / 16) + h * (BN / 32) * 128);
+      const uint32_t d = tm + H::cO, a = tm + H::cS(h, buf);
 #pragma unroll
-      for (int k = 0; k < BN / 16; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), add || k > 0);
+      for (int k = 0; k < BN / 32; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), add || k > 0);
       tc_commit(b_o);
-      tc_commit(&b_empty[st]);
+      if (h == 1) tc_commit(&b_empty[st]);
     };
     bool ok = true;
     int j = 0, nu = 0;
-    auto keys = [&](int t) {                               // scores of tile t
+    auto keys = [&](int t, int h) {                        // scores of half h of tile t
       const int e = P * t;
-      ok = ok && wait_warp(&b_full[e % ST], (e / ST) & 1) && (!kLow || wait_warp(&b_full[(e + 1) % ST], ((e + 1) / ST) & 1));
-      tc_fence_after();
-      if (ok && elect_one()) scores(t, e % ST, (e + 1) % ST);
+      if (h == 0) {
+        ok = ok && wait_warp(&b_full[e % ST], (e / ST) & 1) && (!kLow || wait_warp(&b_full[(e + 1) % ST], ((e + 1) / ST) & 1));
+        tc_fence_after();
+      }
+      if (ok && elect_one()) scores(h, t & 1, e % ST, (e + 1) % ST);
       __syncwarp();
     };
 #pragma unroll 1
@@ -360,17 +370,24 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       const int nt = min(end, s_first[u + 1]) - max(begin, s_first[u]);
       if (nt <= 0) continue;
       ok = wait_warp(b_q, nu & 1);
-      keys(j);
-      for (int i = 0; ok && i < nt; ++i, ++j) {
-        if (i + 1 < nt) keys(j + 1);
-        const int e = P * j + P - 1;
-        ok = ok && wait_warp(&b_full[e % ST], (e / ST) & 1) && wait_warp(&b_p[j & 1], (j >> 1) & 1);
-        tc_fence_after();
-        if (ok && elect_one()) {
-          sums(j, e % ST, i > 0);
-          if (i + 1 == nt) tc_commit(b_f);
+      tc_fence_after();
+#pragma unroll 1
+      for (int i = -1; ok && i < nt; ++i) {                // (round -1 makes the first tile's scores)
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (i + 1 < nt) keys(j + 1 + (i < 0 ? -1 : 0), h);
+          if (i < 0) continue;
+          const int e = P * j + P - 1;
+          if (h == 0) ok = ok && wait_warp(&b_full[e % ST], (e / ST) & 1);
+          ok = ok && wait_warp(&b_p[2 * h + (j & 1)], (j >> 1) & 1);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            sums(h, j & 1, e % ST, i > 0 || h > 0);
+            if (i + 1 == nt && h == 1) tc_commit(b_f);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (i >= 0) ++j;
       }
       ++nu;
     }
@@ -554,13 +571,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         for (int it = 0; it < 1024 && e % P == P - 1 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
         }
   } else if (wg < 2) {
-    // ---- softmax: a thread per row; the warpgroups take tiles in turn
+    // ---- softmax: a thread per row of the unit and half of a tile's rows
+    constexpr int HALF = BN / 2;
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupSoft));
     const int m = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    // Both add to one O, so they have to agree on the reference M: a tile's is
-    // handed on before its weights are made. Barrier 4 + w: warpgroup w has handed
-    // on (and does so again only after the other one has).
+    // Barrier 4 + w: warpgroup w has handed its reference on (and does so again only
+    // after the other one has).
     auto handed = [&] {                                    // waits for the other's
       __syncwarp();
       if (wg == 0) asm volatile("bar.sync 5, 256;" ::: "memory");
@@ -656,11 +673,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       bool poison = false;
 #pragma unroll 1
       for (int t = U.t0; t < U.t1; ++t, ++j) {
-        if ((j & 1) != wg) continue;
-        wait(&b_s[wg], (j >> 1) & 1);
+        wait(&b_s[2 * wg + (j & 1)], (j >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        const uint32_t ts = lane_base + H::cS(wg);
+        const uint32_t ts = lane_base + H::cS(0, 0) + (2 * wg + (j & 1)) * HALF;
+        uint32_t x[HALF];
+#pragma unroll
+        for (int c = 0; c < HALF; c += 32) tc_ld32(x + c, ts + c);
         int rows;
         const int r = tile_row(u, t, rows);
         bool masked = rows < BN;
@@ -672,12 +691,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         const int32_t* tp = s_pos + (j % H::kPosTiles) * BN;
         if (need_pos)
           masked = masked || tp[BN - 1] > pmin || (A.window > 0 && (int64_t)pmax - tp[0] >= A.window && r + BN > A.sink);
-        // the row's token sees columns [cl, ch) and, of the first rows, [0, cf)
-        int cl = 0, ch = BN, cf = 0;
+        tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < HALF; c += 32) tc_pin(x + c);
         if (masked) {
-          ch = rows;
+          // the row's token sees rows [cl, ch) of the tile and, of the first rows, [0, cf)
+          int cl = 0, ch = rows, cf = 0;
           if (need_pos) {
-            auto upto = [&](int pos) {                     // columns with a position <= pos
+            auto upto = [&](int pos) {                     // rows with a position <= pos
               int a = 0, b = rows;
 #pragma unroll 1
               while (a < b) {
@@ -692,50 +713,39 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
               cf = min(ch, max(0, A.sink - r));
             }
           }
-          const uint32_t* jm = X.junk[ev % ST];
-          if (jm[0] | jm[1] | jm[2] | jm[3])
-#pragma unroll 1
-            for (int c = 0; c < rows; ++c)
-              if (((jm[c >> 5] >> (c & 31)) & 1u) && c < ch && (c >= cl || c < cf)) poison = true;
-        }
-        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };   // bits of columns < n
-        auto hide = [&](uint32_t* x, int c0) {
-          const uint32_t seen = (below(ch - c0) & ~below(cl - c0)) | below(cf - c0);
+          auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };   // bits of rows < n
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (!((seen >> c) & 1u)) x[c] = 0xFF800000u;   // -inf
-        };
-        // the largest logit; the scores are loaded once more for the weights, which leaves registers for both
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c = 0; c < BN; c += 64) {
-          uint32_t x[64];
-          tc_ld32(x, ts + c);
-          tc_ld32(x + 32, ts + c + 32);
-          tc_wait_ld();
-          tc_pin(x);
-          tc_pin(x + 32);
-          if (masked) {
-            hide(x, c);
-            hide(x + 32, c + 32);
+          for (int c0 = 0; c0 < HALF; c0 += 32) {
+            const int at = wg * HALF + c0;
+            const uint32_t seen = (below(ch - at) & ~below(cl - at)) | below(cf - at);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((seen >> c) & 1u)) x[c0 + c] = 0xFF800000u;   // -inf
+            if (X.junk[ev % ST][at >> 5] & seen) poison = true;   // (a tile's marks are words of 32 rows)
           }
-#pragma unroll
-          for (int k = 0; k < 64; k += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tops[i] = fmaxf(fmaxf(tops[i], __uint_as_float(x[k + i])), __uint_as_float(x[k + 4 + i]));
         }
+        float tops[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tops[k] = __uint_as_float(x[k]);
+#pragma unroll
+        for (int c = 4; c < HALF - 4; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tops[k] = fmaxf(fmaxf(tops[k], __uint_as_float(x[c + k])), __uint_as_float(x[c + 4 + k]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], __uint_as_float(x[HALF - 4 + k]));
         float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         top = top * sl - kShift;
-        const float before = t > U.t0 ? handed() : -INFINITY;   // M after the tile before
+        const bool first = wg == 0 && t == U.t0;
+        const float before = first ? -INFINITY : handed();   // M after the half before
         const bool move = (top > before + kLazy || before == -INFINITY) && top > -INFINITY;
         const float now = move ? top : before;
-        if (t + 1 < U.t1) hand(now);
-        if (now > M) {                                     // (since this warpgroup's last tile)
+        if (wg == 0 || t + 1 < U.t1) hand(now);
+        if (now > M) {                                     // (since this warpgroup's last half)
           l *= exp2_fast(M - now);
           M = now;
         }
-        if (t > U.t0 && __any_sync(0xffffffffu, move)) {
-          wait(b_o, (j - 1) & 1);                          // the sums of the tile before may be running
+        if (!first && __any_sync(0xffffffffu, move)) {
+          wait(b_o, (2 * j + wg - 1) & 1);                 // the sums of the half before may be running
           __syncwarp();
           tc_fence_after();
           const float a = move ? exp2_fast(before - now) : 1.f;
@@ -753,37 +763,24 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         const float mb = M == -INFINITY ? 0.f : M;
         const float2 sl2 = make_float2(sl, sl), mb2 = make_float2(-mb, -mb);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-        for (int c = 0; c < BN; c += 64) {
-          uint32_t x[64];
-          tc_ld32(x, ts + c);
-          tc_ld32(x + 32, ts + c + 32);
-          tc_wait_ld();
-          tc_pin(x);
-          tc_pin(x + 32);
-          if (masked) {
-            hide(x, c);
-            hide(x + 32, c + 32);
-          }
 #pragma unroll
-          for (int h = 0; h < 64; h += 32) {
-            uint32_t w[16];
+        for (int c = 0; c < HALF; c += 32) {
+          uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float2 e = __ffma2_rn(make_float2(__uint_as_float(x[h + 2 * k]), __uint_as_float(x[h + 2 * k + 1])), sl2, mb2);
-              e.x = exp2_fast(e.x);
-              e.y = exp2_fast(e.y);
-              ls[k & 1] = __fadd2_rn(ls[k & 1], e);
-              const __half2 y = __floats2half2_rn(e.x, e.y);
-              w[k] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            tc_st16(ts + (c + h) / 2, w);                  // (over scores that have been loaded)
+          for (int k = 0; k < 16; ++k) {
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1])), sl2, mb2);
+            e.x = exp2_fast(e.x);
+            e.y = exp2_fast(e.y);
+            ls[k & 1] = __fadd2_rn(ls[k & 1], e);
+            const __half2 y = __floats2half2_rn(e.x, e.y);
+            w[k] = *reinterpret_cast<const uint32_t*>(&y);
           }
+          tc_st16(ts + c / 2, w);
         }
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&b_p[wg]);
+        mbar_arrive(&b_p[2 * wg + (j & 1)]);
       }
       // ---- the unit's part: each warpgroup writes half of the dims
       const float M2 = swap(M), top = fmaxf(M, M2);        // (the last tile's is the larger one)
