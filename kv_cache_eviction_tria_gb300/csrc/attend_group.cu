@@ -22,12 +22,13 @@
 // in memory instead): values rounded once, keys as the rounded value and the
 // remainder, which takes a product of its own (kLow).
 //
-// A tile's scores are two halves by rows, each with a warpgroup of its own (a
-// thread per column of the unit), two score buffers and products of its own, so that a
-// warpgroup's next scores are made while it is in its softmax. Both halves
-// add to one O, so the reference M is handed on from half to half through
-// shared memory, before the weights are made. (Warpgroups that took whole tiles in
-// turn waited for their scores: 2.3 us a tile of q8_0 rows.)
+// Two warpgroups take the tiles' softmax in turn, a thread per column of the
+// unit. Scores are made two or three tiles ahead of the sums, in four buffers, so that
+// neither the warpgroups nor the products wait for a tile that is being widened. Both
+// warpgroups' weights add to one O, so the reference M is handed on from tile
+// to tile through shared memory, before the weights are made. (With tiles of
+// 128 rows the ring held too few of them: a tile's sums waited for the next
+// tile's keys, and those for the sums' place, 2.4 us in turn.)
 //
 // Masks, junk in hidden rows, the lazy reference M and the bounded waits are those of
 // the prompt kernel.
@@ -41,28 +42,29 @@ namespace tria {
 
 namespace {
 
+constexpr int kScSlots = 8, kScAhead = 4;   // tiles whose scales are held, and of these on their way
+
 template <int HD, bool kQuant>
 struct GroupShape {
-  static constexpr int BN = HD == 256 ? 64 : 128;          // rows of a tile
+  static constexpr int BN = HD == 256 ? 32 : 64;           // rows of a tile
   static constexpr int kStage = BN * HD * 2;
-  static constexpr int kStages = (HD == 64 ? 2 : 1) * (kQuant ? 4 : 6);
+  static constexpr int kStages = kQuant ? 8 : 12;
   static constexpr int kRaw = BN * HD;                     // bytes of a plane's q8_0 codes
-  static constexpr int kRawArea = kQuant ? 2 * kRaw : 0;   // of a plane: two tiles, or four of 4-bit codes
-  static constexpr int kRawSlots = 4;
+  static constexpr int kRawSlots = kQuant ? 4 : 0;         // of q8_0 codes; of 4-bit ones twice as many
+  static constexpr int kRawArea = kRawSlots * kRaw;        // of a plane
   static constexpr int kPosTiles = 8;                      // more tiles than the ring holds values of
-  static constexpr int kScRow = HD / 16;                   // bytes of a row's block scales
+  static constexpr int kScTile = BN * HD / 16;             // bytes of a tile's block scales, of a plane
   static constexpr int oRing = 0, oRaw = kStages * kStage, oPos = oRaw + 2 * kRawArea, oScale = oPos + kPosTiles * BN * 4;
-  static constexpr int oRef = oScale + (kQuant ? 2 * BN * kScRow : 0);   // [warpgroup][row], then [parity][warpgroup][row]
+  static constexpr int oRef = oScale + (kQuant ? 2 * kScSlots * kScTile : 0);   // [warpgroup][row], then [parity][warpgroup][row]
   static constexpr int oBar = oRef + 6 * 128 * 4;
   static constexpr int kSmem = oBar + 1024;
   // TMEM columns: score buffers, outputs, queries
-  static constexpr int cS(int half, int buf) { return (2 * half + buf) * (BN / 2); }
-  static constexpr int cO = 2 * BN, cQ = cO + HD;
+  static constexpr int cS = 0, cO = 4 * BN, cQ = cO + HD;
   static_assert(cQ + HD / 2 <= 512, "TMEM");
-  static_assert(kSmem + (3 * kMaxSegments + 64) * 4 <= 227 * 1024, "shared memory");
+  static_assert(kSmem + (3 * kMaxSegments + 256) * 4 <= 227 * 1024, "shared memory");
 };
 
-constexpr int kGroupBars = 2 * 12 + 4 + 4 + 5 + 4 * 4;
+constexpr int kGroupBars = 2 * 12 + 4 + 4 + 5 + 4 * 8;
 struct GroupShared {
   uint32_t junk[12][4];                                    // rows of a value tile that held junk, by stage
   int32_t lo[8], hi[8], c_lo[4], c_hi[4];                  // positions, a warp each
@@ -77,60 +79,95 @@ constexpr int kGroupThreads = 640, kGroupIssue = 16, kGroupLoadK = 17, kGroupLoa
 constexpr int kGroupSoft = 128, kGroupConv = 80, kGroupOther = 64;
 static_assert(2 * kGroupSoft + 2 * kGroupConv + kGroupOther == 5 * kGroupRegs, "register shares");
 
+// Shared memory by its 32-bit addresses (through selected pointers, accesses
+// became generic ones).
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t* v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
 // The rows of a tile of codes (rb bytes each) as fp16 tiles, by kConv threads; a
-// thread has the same eight dims of every kConv / (HD / 8)-th row. hi_t: code x
+// thread has the same 16 dims of every kConv / (HD / 16)-th row. hi_t: code x
 // scale, rounded; lo_t (kLow): what fp16 leaves of it, which fp16 holds exactly (a
 // scale is a multiple of 2^-24 and a code whole, so 8 bits at most are left,
-// all above 2^-24). With clean, rows from `rows` on become zeros, and so do pieces with
-// junk, whose rows are marked. (The kernel's roles together have to stay inside
-// the instruction cache: four rows at a time, types told apart in the loop.
-// Unrolled in all variants, 200 KB of code, a tile took twice as long.)
-template <int HD, int BN, bool kLow>
-__device__ __forceinline__ void widen_tile(const uint8_t* codes, int rb, bool q8, const uint16_t* scale, uint8_t* hi_t, uint8_t* lo_t, int hd,
-                                           bool clean, int rows, uint32_t* marks, int tid) {
-  constexpr int per = HD / 8, step = kConv / per, NB = HD / 32, kRows = BN / step < 4 ? BN / step : 4;
-  static_assert((step == 4 || step % 8 == 0) && BN % (step * kRows) == 0, "a thread's rows have one or two places in the swizzle");
-  const int c = tid % per, r0 = tid / per;
-  const uint32_t block = (c >> 3) * (BN * 128);
-  const uint32_t to[2] = {block + swz(r0, c & 7), step == 4 ? block + swz(r0 + 4, c & 7) - 4 * 128 : block + swz(r0, c & 7)};
-  const bool there = 8 * c < hd;
-  const uint8_t* from = codes + r0 * rb + (there ? (q8 ? c * 8 : (c / 4) * 16 + (c & 1) * 8) : 0);
-  const uint16_t* sc_at = scale + r0 * NB + c / 4;
-  const uint32_t flip = q8 ? 0x80808080u : 0u, keep = q8 ? 0xFFFFFFFFu : 0x0F0F0F0Fu, bias = q8 ? 0x64806480u : 0x64086408u;
-  const int up = q8 ? 0 : (c & 2) * 2;
-#pragma unroll 1
-  for (int i0 = 0; i0 < BN / step; i0 += kRows) {
-    uint2 w[kRows];
-    uint32_t sc[kRows];
+// all above 2^-24). kClean: rows from `rows` on become zeros, and so do pieces with
+// junk, whose rows are marked. No branches, and short enough for four or five
+// roles to stay in the instruction cache side by side: what bounds a warp here is
+// the latency of its instructions (told apart at run time, types and planes
+// cost a third more; 16 rows unrolled, twice as much).
+template <int HD, int BN, bool kQ8, bool kLow, bool kClean>
+__device__ __forceinline__ void widen_tile(uint32_t codes, int rb, uint32_t scale, int nb, uint32_t hi_t, uint32_t lo_t, int hd, int rows,
+                                           uint32_t* marks, int tid) {
+  constexpr int per = HD / 16, step = kConv / per, N = BN / step;   // threads of a row, rows of a thread
+  static_assert(step % 8 == 0 && BN % step == 0, "a thread's rows have one place in the swizzle");
+  // eight lanes store to two rows' four pieces of a 64-dim block: no bank conflicts
+  const int c = (tid & 3) | (((tid >> 3) & (per / 4 - 1)) << 2), r0 = ((tid >> 2) & 1) | ((tid / (2 * per)) << 1);
+  const bool there = 16 * c < hd;
+  // q4_0: the low halves of a block's 16 bytes, or the high ones
+  const uint32_t from = codes + r0 * rb + (there ? (kQ8 ? c * 16 : (c / 2) * 16) : 0);
+  const uint32_t sc_at = scale + (there ? (r0 * nb + c / 2) * 2 : 0), sel = there ? 0x1010u : 0x4444u;
+  const int up = (c & 1) * 4;
+  const uint32_t at0 = (c >> 2) * (BN * 128) + swz(r0, (2 * c) & 7), at1 = at0 ^ 16;   // two neighbouring pieces
+  constexpr uint32_t bias = kQ8 ? 0x64806480u : 0x64086408u;
+  uint4 w[N];
+  uint32_t sc[N];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      w[i] = *reinterpret_cast<const uint2*>(from + (i0 + i) * step * rb);
-      sc[i] = there ? sc_at[(i0 + i) * step * NB] : 0u;
-    }
+  for (int i = 0; i < N; ++i) {
+    w[i] = lds128(from + i * step * rb);
+    sc[i] = lds16(sc_at + i * step * nb * 2);
+  }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < N; ++i) {
+    const uint32_t s2 = __byte_perm(sc[i], 0u, sel);
+    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t v[8], hi[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
       // 0x64, byte: 1024 + it, exactly; less the bias, the code
-      const uint32_t wx = ((w[i].x >> up) & keep) ^ flip, wy = ((w[i].y >> up) & keep) ^ flip, s2 = __byte_perm(sc[i], sc[i], 0x1010);
-      const uint32_t b[4] = {__byte_perm(wx, 0x64646464u, 0x4140), __byte_perm(wx, 0x64646464u, 0x4342),
-                             __byte_perm(wy, 0x64646464u, 0x4140), __byte_perm(wy, 0x64646464u, 0x4342)};
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t v;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(b[k]), "r"(bias));
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(v), "r"(s2));
-        if constexpr (kLow) asm("{\n .reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;\n}\n" : "=r"(lo[k]) : "r"(v), "r"(s2), "r"(hi[k]));
-      }
-      const int rr = r0 + (i0 + i) * step;
-      if (clean) {
-        const bool junk = junk_h2(hi[0]) || junk_h2(hi[1]) || junk_h2(hi[2]) || junk_h2(hi[3]);
-        if (rr >= rows || junk) hi[0] = hi[1] = hi[2] = hi[3] = 0;
-        if (rr < rows && junk) atomicOr(&marks[rr >> 5], 1u << (rr & 31));
-      }
-      const uint32_t at = to[i & 1] + (i0 + i) * step * 128;
-      *reinterpret_cast<uint4*>(hi_t + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if constexpr (kLow) *reinterpret_cast<uint4*>(lo_t + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      const uint32_t y = kQ8 ? x[k / 2] ^ 0x80808080u : (x[k / 2] >> up) & 0x0F0F0F0Fu;
+      const uint32_t b = __byte_perm(y, 0x64646464u, k & 1 ? 0x4342 : 0x4140);
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[k]) : "r"(b), "r"(bias));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(v[k]), "r"(s2));
     }
+    if constexpr (kLow) {
+      uint32_t lo[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) asm("{\n .reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;\n}\n" : "=r"(lo[k]) : "r"(v[k]), "r"(s2), "r"(hi[k]));
+      sts128(lo_t + at0 + i * step * 128, lo);
+      sts128(lo_t + at1 + i * step * 128, lo + 4);
+    }
+    if constexpr (kClean) {
+      const int rr = r0 + i * step;
+      bool junk = false;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) junk = junk || junk_h2(hi[k]);
+      if (rr < rows && junk) atomicOr(&marks[rr >> 5], 1u << (rr & 31));
+      if (rr >= rows || junk)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) hi[k] = 0;
+    }
+    sts128(hi_t + at0 + i * step * 128, hi);
+    sts128(hi_t + at1 + i * step * 128, hi + 4);
+  }
+}
+
+// Starts the copy of a tile's block scales (nb halves a row, consecutive) by
+// kConv threads. With an odd number of blocks a row may begin between two
+// words, which no asynchronous copy takes: they are waited for.
+__device__ __forceinline__ void copy_scales(uint16_t* to, const uint16_t* from, int n, bool words, int tid) {
+  if (words) {
+    if (2 * tid < n) cp_async4(to + 2 * tid, from + 2 * tid);
+  } else {
+    for (int i = tid; i < n; i += kConv) to[i] = __ldg(from + i);
   }
 }
 
@@ -141,16 +178,19 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   using H = GroupShape<HD, kQuant>;
   // ring entries of tile j: keys P j, their remainders P j + 1 (kLow), values P j + P - 1
   constexpr int P = kLow ? 3 : 2, BN = H::BN, ST = H::kStages;
+  // tiles that scores are ahead of sums: less than there are buffers, and the keys' stages must not be those of
+  // values whose sums come after them
+  constexpr int kAhead = kLow ? 2 : 3;
+  static_assert(P * kAhead + P - 2 < ST, "stages");
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_first[kMaxSegments + 1], s_lo[kMaxSegments], s_hi[kMaxSegments];   // of units: first tile, rows
   __shared__ int s_scan[40];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
-  // full: a tile is in the ring; empty: its products are done; s: scores; p: weights (of half h
-  // in buffer b: 2 h + b); o: a half's sums; f: the unit's last sums; q: queries; x: every product; v: values that are looked
+  // full: a tile is in the ring; empty: its products are done; s: scores; p: weights; o: a tile's
+  // sums; f: the unit's last sums; q: queries; x: every product; v: values that are looked
   // through before their tile is full; rf, re: codes (of keys, of values) are there, are used
   uint64_t *b_full = bar, *b_empty = bar + 12, *b_s = bar + 24, *b_p = b_s + 4, *b_o = b_p + 4, *b_f = b_o + 1, *b_q = b_f + 1,
-           *b_x = b_q + 1, *b_v = b_x + 1, *b_rfk = b_v + 1, *b_rek = b_rfk + H::kRawSlots, *b_rfv = b_rek + H::kRawSlots,
-           *b_rev = b_rfv + H::kRawSlots;
+           *b_x = b_q + 1, *b_v = b_x + 1, *b_rfk = b_v + 1, *b_rek = b_rfk + 8, *b_rfv = b_rek + 8, *b_rev = b_rfv + 8;
   int32_t* s_pos = reinterpret_cast<int32_t*>(smem + H::oPos);
   float* s_ref = reinterpret_cast<float*>(smem + H::oRef);
   GroupShared& X = *reinterpret_cast<GroupShared*>(smem + H::oBar + kGroupBars * 8);
@@ -234,7 +274,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     mbar_init(b_x, 1);
     mbar_init(b_v, 1);
 #pragma unroll
-    for (int i = 0; i < H::kRawSlots; ++i) {
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&b_rfk[i], 1);
       mbar_init(&b_rek[i], 1);
       mbar_init(&b_rfv[i], 1);
@@ -243,9 +283,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     fence_mbar_init();
   }
   __syncthreads();
-  const int64_t total = s_first[A.units];
-  const int64_t workers = min((int64_t)gridDim.x, total);
-  if ((int64_t)blockIdx.x >= workers) return leave();
+  const int total = s_first[A.units], workers = min((int)gridDim.x, total);
+  if ((int)blockIdx.x >= workers) return leave();
   if (warp == kGroupIssue) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&X.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -254,7 +293,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = X.tmem;
-  const int begin = (int)(blockIdx.x * total / workers), end = (int)((blockIdx.x + 1) * total / workers);
+  // runs of `each` tiles, the first `more` of one more
+  const int each = total / workers, more = total - each * workers, b = blockIdx.x;
+  const int begin = b * each + min(b, more), end = begin + each + (b < more);
   auto unit_at = [&](int tile) {                           // the last unit that starts at or before it
     int u = 0, hi_u = A.units - 1;
 #pragma unroll 1
@@ -267,6 +308,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   const int unit_a = unit_at(begin);
   struct Unit {
     int s, g, c0, ncol, t0, t1;                            // sequence, KV head, columns, this run's tiles of it
+    int lo, hi, sr, nt_sink;                               // rows besides the sink; the sink's rows and tiles
     int64_t row0;
   };
   auto unit_of = [&](int u) {
@@ -277,20 +319,19 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     U.g = x / ct;
     U.c0 = (x - U.g * ct) * 128;
     U.ncol = min(128, S.t * A.G - U.c0);
-    U.t0 = max(begin, s_first[u]);
-    U.t1 = min(end, s_first[u + 1]);
+    U.lo = s_lo[u];
+    U.hi = s_hi[u];
+    U.sr = min(A.sink, U.lo);
+    U.nt_sink = (U.sr + BN - 1) / BN;
+    U.t0 = max(begin, s_first[u]) - s_first[u];            // (counted from the unit's first one)
+    U.t1 = min(end, s_first[u + 1]) - s_first[u];
     U.row0 = S.row0 + (int64_t)U.g * S.cap;
     return U;
   };
-  auto tile_row = [&](int u, int tile, int& rows) {        // first row in the segment
-    const int j = tile - s_first[u], lo = s_lo[u];
-    const int sr = min(A.sink, lo), nt_sink = (sr + BN - 1) / BN;
-    if (j < nt_sink) {
-      rows = min(BN, sr - j * BN);
-      return j * BN;
-    }
-    const int r = lo + (j - nt_sink) * BN;
-    rows = min(BN, s_hi[u] - r);
+  auto tile_row = [&](const Unit& U, int t, int& rows) {   // first row in the segment
+    const bool sink = t < U.nt_sink;
+    const int r = sink ? t * BN : U.lo + (t - U.nt_sink) * BN;
+    rows = min(BN, (sink ? U.sr : U.hi) - r);
     return r;
   };
   // bounded waits, as in the prompt kernel: after one gave up nobody waits any more, no
@@ -315,10 +356,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     if (e >= ST) wait(&b_empty[e % ST], ((e / ST) - 1) & 1);
   };
   const int tiles = end - begin;
-  // codes as they lie: two tiles of a plane, or four of 4-bit ones
-  const int slots_k = A.k_type == TRIA_Q4_0 ? 4 : 2, slots_v = A.v_type == TRIA_Q4_0 ? 4 : 2;
-  auto raw_k = [&](int j) { return smem + H::oRaw + (j % slots_k) * (H::kRawArea / slots_k); };
-  auto raw_v = [&](int j) { return smem + H::oRaw + H::kRawArea + (j % slots_v) * (H::kRawArea / slots_v); };
+  // codes as they lie: 2^slots tiles
+  const int slots_k = A.k_type == TRIA_Q4_0 ? 3 : 2, slots_v = A.v_type == TRIA_Q4_0 ? 3 : 2;   // (logarithms)
+  auto raw_k = [&](int j) { return smem + H::oRaw + (j & ((1 << slots_k) - 1)) * (H::kRawArea >> slots_k); };
+  auto raw_v = [&](int j) { return smem + H::oRaw + H::kRawArea + (j & ((1 << slots_v) - 1)) * (H::kRawArea >> slots_v); };
   const int k_rb = A.k_type == TRIA_Q8_0 ? A.hd : A.hd / 2, v_rb = A.v_type == TRIA_Q8_0 ? A.hd : A.hd / 2;
 
   if (wg >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupOther));
@@ -327,68 +368,60 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     // such a form, see the prompt kernel)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dk = tile_desc(smem_u32(smem + H::oRing), 16), dv = tile_desc(smem_u32(smem + H::oRing), BN * 128);
-    // (a half's rows are 8 groups of eight further on in the keys' tile, BN / 32 steps of 16 in the values')
-    auto scores = [&](int h, int buf, int st, int sl) {
-      const uint64_t b = dk + (uint64_t)(st * (H::kStage / 16) + h * (BN / 2) * 8);
-      const uint32_t d = tm + H::cS(h, buf), a = tm + H::cQ;
+    auto scores = [&](int buf, int st, int sl) {
+      const uint64_t b = dk + (uint64_t)(st * (H::kStage / 16));
+      const uint32_t d = tm + H::cS + buf * BN, a = tm + H::cQ;
 #pragma unroll
       for (int k = 0; k < HD / 16; ++k)
-        tc_mma_ts(d, a + k * 8, b + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN / 2, false), k > 0);
+        tc_mma_ts(d, a + k * 8, b + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN, false), k > 0);
       if constexpr (kLow) {
-        const uint64_t bl = dk + (uint64_t)(sl * (H::kStage / 16) + h * (BN / 2) * 8);
+        const uint64_t bl = dk + (uint64_t)(sl * (H::kStage / 16));
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
-          tc_mma_ts(d, a + k * 8, bl + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN / 2, false), 1);
+          tc_mma_ts(d, a + k * 8, bl + (uint64_t)((k >> 2) * (BN * 8) + (k & 3) * 2), mma_desc(BN, false), 1);
       }
-      tc_commit(&b_s[2 * h + buf]);
-      if (h == 1) {
-        tc_commit(&b_empty[st]);
-        if (kLow) tc_commit(&b_empty[sl]);
-      }
+      tc_commit(&b_s[buf]);
+      tc_commit(&b_empty[st]);
+      if (kLow) tc_commit(&b_empty[sl]);
     };
-    auto sums = [&](int h, int buf, int st, bool add) {
-      const uint64_t b = dv + (uint64_t)(st * (H::kStage / 16) + h * (BN / 32) * 128);
-      const uint32_t d = tm + H::cO, a = tm + H::cS(h, buf);
+    auto sums = [&](int buf, int st, bool add) {
+      const uint64_t b = dv + (uint64_t)(st * (H::kStage / 16));
+      const uint32_t d = tm + H::cO, a = tm + H::cS + buf * BN;
 #pragma unroll
-      for (int k = 0; k < BN / 32; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), add || k > 0);
+      for (int k = 0; k < BN / 16; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), add || k > 0);
       tc_commit(b_o);
-      if (h == 1) tc_commit(&b_empty[st]);
+      tc_commit(&b_empty[st]);
     };
     bool ok = true;
     int j = 0, nu = 0;
-    auto keys = [&](int t, int h) {                        // scores of half h of tile t
-      const int e = P * t;
-      if (h == 0) {
-        ok = ok && wait_warp(&b_full[e % ST], (e / ST) & 1) && (!kLow || wait_warp(&b_full[(e + 1) % ST], ((e + 1) / ST) & 1));
-        tc_fence_after();
-      }
-      if (ok && elect_one()) scores(h, t & 1, e % ST, (e + 1) % ST);
-      __syncwarp();
-    };
 #pragma unroll 1
     for (int u = unit_a; ok && j < tiles; ++u) {
       const int nt = min(end, s_first[u + 1]) - max(begin, s_first[u]);
       if (nt <= 0) continue;
       ok = wait_warp(b_q, nu & 1);
-      tc_fence_after();
+      // round i: the sums of tile j + i, then the scores of the tile kAhead further on, in the buffer that those of the
+      // tile before have left
 #pragma unroll 1
-      for (int i = -1; ok && i < nt; ++i) {                // (round -1 makes the first tile's scores)
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (i + 1 < nt) keys(j + 1 + (i < 0 ? -1 : 0), h);
-          if (i < 0) continue;
-          const int e = P * j + P - 1;
-          if (h == 0) ok = ok && wait_warp(&b_full[e % ST], (e / ST) & 1);
-          ok = ok && wait_warp(&b_p[2 * h + (j & 1)], (j >> 1) & 1);
+      for (int i = -kAhead; ok && i < nt; ++i) {
+        if (i >= 0) {
+          const int t = j + i, e = P * t + P - 1;
+          ok = wait_warp(&b_full[e % ST], (e / ST) & 1) && wait_warp(&b_p[t & 3], (t >> 2) & 1);
           tc_fence_after();
           if (ok && elect_one()) {
-            sums(h, j & 1, e % ST, i > 0 || h > 0);
-            if (i + 1 == nt && h == 1) tc_commit(b_f);
+            sums(t & 3, e % ST, i > 0);
+            if (i + 1 == nt) tc_commit(b_f);
           }
           __syncwarp();
         }
-        if (i >= 0) ++j;
+        if (i + kAhead < nt) {
+          const int t = j + i + kAhead, e = P * t;
+          ok = ok && wait_warp(&b_full[e % ST], (e / ST) & 1) && (!kLow || wait_warp(&b_full[(e + 1) % ST], ((e + 1) / ST) & 1));
+          tc_fence_after();
+          if (ok && elect_one()) scores(t & 3, e % ST, (e + 1) % ST);
+          __syncwarp();
+        }
       }
+      j += nt;
       ++nu;
     }
     // nothing may be running when the accumulators are given back
@@ -412,15 +445,15 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
 #pragma unroll 1
         for (int t = U.t0; t < U.t1; ++t, ++j) {
           int rows;
-          const int r = tile_row(u, t, rows);
+          const int r = tile_row(U, t, rows);
           if (!codes) {
             // hidden keys, and those past the last row, only reach logits that the mask replaces
             const int e = P * j;
             free_stage(e);
             if (!*s_abort) copy_tile<HD, BN>(stage(e), &map_k, U.row0 + r, &b_full[e % ST]);
           } else {
-            const int x = j % slots;
-            if (j >= slots) wait(&empty[x], ((j / slots) - 1) & 1);
+            const int x = j & ((1 << slots) - 1);
+            if (j >> slots) wait(&empty[x], ((j >> slots) - 1) & 1);
             if (*s_abort) continue;
             mbar_arrive_expect_tx(&full[x], rows * rb);
             bulk_g2s(keys ? raw_k(j) : raw_v(j), plane + (U.row0 + r) * rb, rows * rb, &full[x]);
@@ -432,147 +465,134 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
 #pragma unroll 1
           for (int it = 0; it < 1024 && !codes && e % P == 0 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
           }
-        for (int i = max(0, tiles - slots); i < tiles; ++i)
 #pragma unroll 1
-          for (int it = 0; it < 1024 && codes && !mbar_try_wait(&full[i % slots], (i / slots) & 1); ++it) {
+        for (int i = max(0, tiles - (1 << slots)); i < tiles; ++i)
+#pragma unroll 1
+          for (int it = 0; it < 1024 && codes && !mbar_try_wait(&full[i & ((1 << slots) - 1)], (i >> slots) & 1); ++it) {
           }
       }
     }
-  } else if (wg == 2) {
-    // ---- codes of keys into tiles
+  } else if (wg < 4 && wg >= 2) {
+    // ---- codes into tiles, keys by one warpgroup and values by the other, which also keeps positions and looks through
+    // values that some token does not see
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupConv));
-    const int tid = threadIdx.x & 127;
-    if constexpr (kQuant) {
-      if (kq) {
-        uint16_t* s_scale = reinterpret_cast<uint16_t*>(smem + H::oScale);
-        constexpr int NB = HD / 32;
-        const int nb = A.hd / 32;
-        int j = 0;
-#pragma unroll 1
-        for (int u = unit_a; j < tiles; ++u) {
-          if (min(end, s_first[u + 1]) <= max(begin, s_first[u])) continue;
-          const Unit U = unit_of(u);
-          uint16_t next[NB];                               // scales of this thread's row of the tile to come
-          auto fetch = [&](int t) {
-            int rows = 0;
-            const int r = t < U.t1 ? tile_row(u, t, rows) : 0;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              next[b] = tid < rows && b < nb ? __ldg(reinterpret_cast<const uint16_t*>(A.ks) + (U.row0 + r + tid) * nb + b) : (uint16_t)0;
-          };
-          fetch(U.t0);
-#pragma unroll 1
-          for (int t = U.t0; t < U.t1; ++t, ++j) {
-            if (tid < BN)
-#pragma unroll
-              for (int b = 0; b < NB; ++b) s_scale[tid * NB + b] = next[b];
-            fetch(t + 1);
-            const int e = P * j;
-            wait(&b_rfk[j % slots_k], (j / slots_k) & 1);
-            free_stage(e);
-            if (kLow) free_stage(e + 1);
-            asm volatile("bar.sync 3, 128;" ::: "memory");   // scales
-            widen_tile<HD, BN, kLow>(raw_k(j), k_rb, A.k_type == TRIA_Q8_0, s_scale, stage(e), stage(e + 1), A.hd, false, BN, nullptr, tid);
-            fence_proxy_async_smem();
-            asm volatile("bar.sync 3, 128;" ::: "memory");
-            if (tid == 0) {
-              mbar_arrive(&b_full[e % ST]);
-              if (kLow) mbar_arrive(&b_full[(e + 1) % ST]);
-              mbar_arrive(&b_rek[j % slots_k]);
-            }
-          }
-        }
-      }
-    }
-  } else if (wg == 3) {
-    // ---- positions; codes of values into tiles, or value tiles looked through
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGroupConv));
-    const int tid = threadIdx.x & 127;
-    constexpr int NB = HD / 32;
-    uint16_t* s_scale = reinterpret_cast<uint16_t*>(smem + H::oScale) + BN * NB;
-    const int nb = A.hd / 32;
+    const int tid = threadIdx.x & 127, nb = A.hd / 32;
+    const bool values = wg == 3, codes = values ? vq : kq;
+    const uint16_t* scales = reinterpret_cast<const uint16_t*>(values ? A.vs : A.ks);
+    const int rb = values ? v_rb : k_rb, slots = values ? slots_v : slots_k, entry = values ? P - 1 : 0;
+    const bool q8 = (values ? A.v_type : A.k_type) == TRIA_Q8_0;
+    uint64_t *raw_full = values ? b_rfv : b_rfk, *raw_empty = values ? b_rev : b_rek;
+    auto meet = [&] { asm volatile("bar.sync %0, 128;" ::"r"(values ? 6 : 3) : "memory"); };
+    auto scale = [&](int i) {
+      return reinterpret_cast<uint16_t*>(smem + H::oScale + ((values ? kScSlots : 0) + (i & (kScSlots - 1))) * H::kScTile);
+    };
     int j = 0, looked = 0;
 #pragma unroll 1
-    for (int u = unit_a; j < tiles; ++u) {
+    for (int u = unit_a; j < tiles && (values || codes); ++u) {
       if (min(end, s_first[u + 1]) <= max(begin, s_first[u])) continue;
       const Unit U = unit_of(u);
       const AttendSeq& S = A.seq[U.s];
       const int32_t* rpos = A.cpos + U.row0;
-      // the tokens' positions, and whether they hide rows
-      const int tok_a = U.c0 / A.G, tok_b = (U.c0 + U.ncol - 1) / A.G;
-      int pl = INT32_MAX, ph = INT32_MIN;
-      if (tok_a + tid <= tok_b) pl = ph = A.pos[S.tok0 + tok_a + tid];   // (128 columns at most)
-      const int newest = s_hi[u] > 0 ? rpos[s_hi[u] - 1] : INT32_MIN;
-      uint16_t next[NB];                                   // scales and position of this thread's row of the tile to come
-      int next_pos = INT32_MAX;
-      bool need_pos = true;                                // (until it is known)
-      auto fetch = [&](int t) {
+      const int j0 = j;
+      auto fetch_scales = [&](int t) {
         int rows = 0;
-        const int r = t < U.t1 ? tile_row(u, t, rows) : 0;
-        next_pos = need_pos && tid < rows ? rpos[r + tid] : INT32_MAX;
-        if constexpr (kQuant) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            next[b] = vq && tid < rows && b < nb ? __ldg(reinterpret_cast<const uint16_t*>(A.vs) + (U.row0 + r + tid) * nb + b) : (uint16_t)0;
-        }
+        const int r = t < U.t1 ? tile_row(U, t, rows) : 0;
+        copy_scales(scale(j0 + t - U.t0), scales + (U.row0 + r) * nb, rows * nb, nb % 2 == 0, tid);
+        cp_async_commit();
       };
-      fetch(U.t0);
-      pl = __reduce_min_sync(0xffffffffu, pl);
-      ph = __reduce_max_sync(0xffffffffu, ph);
-      if (lane == 0) {
-        X.c_lo[warp & 3] = pl;
-        X.c_hi[warp & 3] = ph;
+      int next_pos = INT32_MAX, pmin = 0, pmax = 0;        // position of this thread's row of the tile to come
+      bool need_pos = values;                              // (until it is known)
+      auto fetch_pos = [&](int t) {
+        int rows = 0;
+        const int r = t < U.t1 ? tile_row(U, t, rows) : 0;
+        next_pos = need_pos && tid < rows ? rpos[r + tid] : INT32_MAX;
+      };
+      if (codes)
+#pragma unroll 1
+        for (int t = U.t0; t < U.t0 + kScAhead; ++t) fetch_scales(t);
+      if (values) {
+        // the tokens' positions, and whether they hide rows
+        fetch_pos(U.t0);
+        const int tok_a = U.c0 / A.G, tok_b = (U.c0 + U.ncol - 1) / A.G;
+        int pl = INT32_MAX, ph = INT32_MIN;
+        if (tok_a + tid <= tok_b) pl = ph = A.pos[S.tok0 + tok_a + tid];   // (128 columns at most)
+        const int newest = s_hi[u] > 0 ? rpos[s_hi[u] - 1] : INT32_MIN;
+        pl = __reduce_min_sync(0xffffffffu, pl);
+        ph = __reduce_max_sync(0xffffffffu, ph);
+        if (lane == 0) {
+          X.c_lo[warp & 3] = pl;
+          X.c_hi[warp & 3] = ph;
+        }
+        meet();
+        pmin = min(min(X.c_lo[0], X.c_lo[1]), min(X.c_lo[2], X.c_lo[3]));
+        pmax = max(max(X.c_hi[0], X.c_hi[1]), max(X.c_hi[2], X.c_hi[3]));
+        need_pos = A.window > 0 || newest > pmin;
       }
-      asm volatile("bar.sync 6, 128;" ::: "memory");
-      const int pmin = min(min(X.c_lo[0], X.c_lo[1]), min(X.c_lo[2], X.c_lo[3]));
-      const int pmax = max(max(X.c_hi[0], X.c_hi[1]), max(X.c_hi[2], X.c_hi[3]));
-      need_pos = A.window > 0 || newest > pmin;
 #pragma unroll 1
       for (int t = U.t0; t < U.t1; ++t, ++j) {
         int rows;
-        const int r = tile_row(u, t, rows), ev = P * j + P - 1;
-        // positions and marks go with the value tile, which stays until the weights are used
-        free_stage(ev);
-        __syncwarp();
-        int32_t* tp = s_pos + (j % H::kPosTiles) * BN;
-        if (need_pos && tid < BN) tp[tid] = next_pos;
-        if (tid < 4) X.junk[ev % ST][tid] = 0;
-        if constexpr (kQuant) {
-          if (vq && tid < BN)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) s_scale[tid * NB + b] = next[b];
+        const int r = tile_row(U, t, rows), e = P * j + entry;
+        // a warp for each thing to wait for (each costs 200 cycles even when it is there), then they meet
+        const int which = warp & 3;
+        if (which == 0) free_stage(e);
+        else if (kLow && which == 1 && !values) free_stage(e + 1);
+        else if (which == 2 && codes) wait(&raw_full[j & ((1 << slots) - 1)], (j >> slots) & 1);
+        if (codes) {
+          fetch_scales(t + kScAhead);
+          cp_async_wait<kScAhead>();
         }
-        fetch(t + 1);
-        if (kQuant && vq) wait(&b_rfv[j % slots_v], (j / slots_v) & 1);
-        asm volatile("bar.sync 6, 128;" ::: "memory");
-        const bool all = rows == BN && (!need_pos || (tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window ||
-                                                                            r + BN <= A.sink)));   // seen whole by every token
-        if (kQuant && vq) {
-          widen_tile<HD, BN, false>(raw_v(j), v_rb, A.v_type == TRIA_Q8_0, s_scale, stage(ev), nullptr, A.hd, !all, rows, X.junk[ev % ST], tid);
+        int32_t* tp = s_pos + (j % H::kPosTiles) * BN;
+        if (values) {
+          // positions and marks go with the value tile, which stays until the weights are used
+          if (need_pos) {
+            meet();                                        // (their place is free when the tile's is)
+            if (tid < BN) tp[tid] = next_pos;
+            fetch_pos(t + 1);
+          }
+          if (which == 0 && lane < 4) X.junk[e % ST][lane] = 0;
+        }
+        meet();
+        const bool all = !values || (rows == BN && (!need_pos || (tp[BN - 1] <= pmin && (A.window <= 0 || (int64_t)pmax - tp[0] < A.window ||
+                                                                                         r + BN <= A.sink))));   // seen whole by every token
+        if (codes) {
+          const uint32_t hi_t = smem_u32(stage(e)), sc = smem_u32(scale(j));
+          uint32_t* marks = X.junk[e % ST];
+          if (!values) {
+            const uint32_t lo_t = smem_u32(stage(e + 1)), from = smem_u32(raw_k(j));
+            if (q8) widen_tile<HD, BN, true, kLow, false>(from, rb, sc, nb, hi_t, lo_t, A.hd, rows, marks, tid);
+            else widen_tile<HD, BN, false, kLow, false>(from, rb, sc, nb, hi_t, lo_t, A.hd, rows, marks, tid);
+          } else {
+            const uint32_t from = smem_u32(raw_v(j));
+            if (q8 && all) widen_tile<HD, BN, true, false, false>(from, rb, sc, nb, hi_t, 0u, A.hd, rows, marks, tid);
+            else if (q8) widen_tile<HD, BN, true, false, true>(from, rb, sc, nb, hi_t, 0u, A.hd, rows, marks, tid);
+            else if (all) widen_tile<HD, BN, false, false, false>(from, rb, sc, nb, hi_t, 0u, A.hd, rows, marks, tid);
+            else widen_tile<HD, BN, false, false, true>(from, rb, sc, nb, hi_t, 0u, A.hd, rows, marks, tid);
+          }
         } else {
-          if (tid == 0 && !*s_abort) copy_tile<HD, BN>(stage(ev), &map_v, U.row0 + r, all ? &b_full[ev % ST] : b_v);
+          if (tid == 0 && !*s_abort) copy_tile<HD, BN>(stage(e), &map_v, U.row0 + r, all ? &b_full[e % ST] : b_v);
           if (all) continue;
           wait(b_v, looked & 1);
           __syncwarp();
           ++looked;
-          clean_tile<HD, BN, kConv>(stage(ev), rows, X.junk[ev % ST], tid);
+          clean_tile<HD, BN, kConv>(stage(e), rows, X.junk[e % ST], tid);
         }
         fence_proxy_async_smem();
-        asm volatile("bar.sync 6, 128;" ::: "memory");
+        meet();
         if (tid == 0) {
-          mbar_arrive(&b_full[ev % ST]);
-          if (kQuant && vq) mbar_arrive(&b_rev[j % slots_v]);
+          mbar_arrive(&b_full[e % ST]);
+          if (kLow && !values) mbar_arrive(&b_full[(e + 1) % ST]);
+          if (codes) mbar_arrive(&raw_empty[j & ((1 << slots) - 1)]);
         }
       }
     }
-    if (*s_abort && tid == 0 && !vq)                       // value copies still on their way
+    if (*s_abort && tid == 0 && values && !vq)             // value copies still on their way
+#pragma unroll 1
       for (int e = max(0, P * tiles - ST); e < P * tiles; ++e)
 #pragma unroll 1
         for (int it = 0; it < 1024 && e % P == P - 1 && !mbar_try_wait(&b_full[e % ST], (e / ST) & 1); ++it) {
         }
   } else if (wg < 2) {
-    // ---- softmax: a thread per row of the unit and half of a tile's rows
-    constexpr int HALF = BN / 2;
+    // ---- softmax: a thread per column of the unit; the warpgroups take tiles in turn
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupSoft));
     const int m = threadIdx.x & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -673,15 +693,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       bool poison = false;
 #pragma unroll 1
       for (int t = U.t0; t < U.t1; ++t, ++j) {
-        wait(&b_s[2 * wg + (j & 1)], (j >> 1) & 1);
+        if ((j & 1) != wg) continue;
+        wait(&b_s[j & 3], (j >> 2) & 1);
         __syncwarp();
         tc_fence_after();
-        const uint32_t ts = lane_base + H::cS(0, 0) + (2 * wg + (j & 1)) * HALF;
-        uint32_t x[HALF];
+        const uint32_t ts = lane_base + H::cS + (j & 3) * BN;
+        uint32_t x[BN];
 #pragma unroll
-        for (int c = 0; c < HALF; c += 32) tc_ld32(x + c, ts + c);
+        for (int c = 0; c < BN; c += 32) tc_ld32(x + c, ts + c);
         int rows;
-        const int r = tile_row(u, t, rows);
+        const int r = tile_row(U, t, rows);
         bool masked = rows < BN;
         const int ev = P * j + P - 1;
         if (need_pos || masked) {
@@ -693,7 +714,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
           masked = masked || tp[BN - 1] > pmin || (A.window > 0 && (int64_t)pmax - tp[0] >= A.window && r + BN > A.sink);
         tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < HALF; c += 32) tc_pin(x + c);
+        for (int c = 0; c < BN; c += 32) tc_pin(x + c);
         if (masked) {
           // the row's token sees rows [cl, ch) of the tile and, of the first rows, [0, cf)
           int cl = 0, ch = rows, cf = 0;
@@ -715,37 +736,36 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
           }
           auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); };   // bits of rows < n
 #pragma unroll
-          for (int c0 = 0; c0 < HALF; c0 += 32) {
-            const int at = wg * HALF + c0;
-            const uint32_t seen = (below(ch - at) & ~below(cl - at)) | below(cf - at);
+          for (int c0 = 0; c0 < BN; c0 += 32) {
+            const uint32_t seen = (below(ch - c0) & ~below(cl - c0)) | below(cf - c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((seen >> c) & 1u)) x[c0 + c] = 0xFF800000u;   // -inf
-            if (X.junk[ev % ST][at >> 5] & seen) poison = true;   // (a tile's marks are words of 32 rows)
+            if (X.junk[ev % ST][c0 >> 5] & seen) poison = true;   // (a tile's marks are words of 32 rows)
           }
         }
         float tops[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) tops[k] = __uint_as_float(x[k]);
 #pragma unroll
-        for (int c = 4; c < HALF - 4; c += 8)
+        for (int c = 4; c < BN - 4; c += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) tops[k] = fmaxf(fmaxf(tops[k], __uint_as_float(x[c + k])), __uint_as_float(x[c + 4 + k]));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], __uint_as_float(x[HALF - 4 + k]));
+        for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], __uint_as_float(x[BN - 4 + k]));
         float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         top = top * sl - kShift;
-        const bool first = wg == 0 && t == U.t0;
-        const float before = first ? -INFINITY : handed();   // M after the half before
+        const bool first = t == U.t0;
+        const float before = first ? -INFINITY : handed();   // M after the tile before
         const bool move = (top > before + kLazy || before == -INFINITY) && top > -INFINITY;
         const float now = move ? top : before;
-        if (wg == 0 || t + 1 < U.t1) hand(now);
-        if (now > M) {                                     // (since this warpgroup's last half)
+        if (t + 1 < U.t1) hand(now);
+        if (now > M) {                                     // (since this warpgroup's last tile)
           l *= exp2_fast(M - now);
           M = now;
         }
         if (!first && __any_sync(0xffffffffu, move)) {
-          wait(b_o, (2 * j + wg - 1) & 1);                 // the sums of the half before may be running
+          wait(b_o, (j - 1) & 1);                          // the sums of the tile before may be running
           __syncwarp();
           tc_fence_after();
           const float a = move ? exp2_fast(before - now) : 1.f;
@@ -764,7 +784,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         const float2 sl2 = make_float2(sl, sl), mb2 = make_float2(-mb, -mb);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < HALF; c += 32) {
+        for (int c = 0; c < BN; c += 32) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -780,7 +800,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&b_p[2 * wg + (j & 1)]);
+        mbar_arrive(&b_p[j & 3]);
       }
       // ---- the unit's part: each warpgroup writes half of the dims
       const float M2 = swap(M), top = fmaxf(M, M2);        // (the last tile's is the larger one)
@@ -841,7 +861,7 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
   const bool on = col < S.t * A.G;
   const int tok = S.tok0 + (on ? col / A.G : 0), head = g * A.G + (on ? col % A.G : 0);
   const int64_t at = (int64_t)tok * A.nq + head;
-  const int64_t total = A.table[A.units], t0 = A.table[u], t1 = A.table[u + 1];
+  const int total = A.table[A.units], t0 = A.table[u], t1 = A.table[u + 1];
   // the sequence's own rows join the first quarter
   float m = -INFINITY, l = 0.f, v[kJoinDims];
 #pragma unroll
@@ -861,9 +881,10 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
   }
   int c0 = 0, parts = 0;
   if (t1 > t0) {
-    const int64_t workers = min((int64_t)grid, total);
-    c0 = (int)(((t0 + 1) * workers - 1) / total);
-    parts = (int)((t1 * workers - 1) / total) - c0 + 1;
+    const int workers = min(grid, total), each = total / workers, more = total - each * workers;
+    auto cta_of = [&](int tile) { return tile < more * (each + 1) ? tile / (each + 1) : more + (tile - more * (each + 1)) / each; };
+    c0 = cta_of(t0);
+    parts = cta_of(t1 - 1) - c0 + 1;
   }
   constexpr int64_t kSlot = 128 * (HD + 2);
   const float* p = A.part + (int64_t)(u + c0) * kSlot + c;
