@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = X.tmem;
+  asm volatile("griddepcontrol.launch_dependents;");       // (the join waits for this kernel's end; every SM has its CTA)
   // runs of `each` tiles, the first `more` of one more
   const int each = total / workers, more = total - each * workers, b = blockIdx.x;
   const int begin = b * each + min(b, more), end = begin + each + (b < more);
@@ -839,17 +840,20 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   leave();
 }
 
-// Joins the parts of a unit with its tokens' own rows (o2, l2): a thread per
-// column, a quarter of the parts and kJoinDims dims, whose loads are all in flight; the
-// quarters meet in shared memory, in order. (A thread for all parts waited
-// for memory again and again: 13 to 19 us.)
-constexpr int kJoinDims = 8, kJoinQuarters = 4, kJoinLoads = 5;
+// Joins the parts of a unit with its tokens' own rows (o2, l2). A thread takes
+// kJoinDims dims of a column and every Q-th part, whose loads are all in flight; the
+// Q threads of a column meet in shared memory, in order. `wide` is the width in
+// columns of a block's row of threads, a power of two from 32 to 128, no wider than
+// the units need, and Q the most that lets the grid start at once.
+constexpr int kJoinDims = 8, kJoinLoads = 5, kJoinBlocks = 5;   // (blocks of 128 threads per SM, by registers)
 
-template <int HD>
-__global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid_constant__ AttendArgs A, const float* o2, const float* l2,
-                                                                    const int32_t* own_live, const __grid_constant__ GroupOwn own, int grid) {
-  __shared__ float s_m[kJoinQuarters][128], s_l[kJoinQuarters][128], s_v[kJoinQuarters][kJoinDims][128];
-  const int u = blockIdx.x, d0 = blockIdx.y * kJoinDims, c = threadIdx.x & 127, quarter = threadIdx.x >> 7;
+template <int HD, int Q>
+__global__ void __launch_bounds__(128 * Q, kJoinBlocks / Q) k_join_group(const __grid_constant__ AttendArgs A, const float* o2, const float* l2,
+                                                                         const int32_t* own_live, const __grid_constant__ GroupOwn own,
+                                                                         int grid, int wide) {
+  __shared__ float s_m[Q][128], s_l[Q][128], s_v[Q][kJoinDims][128];
+  const int u = blockIdx.x, th = threadIdx.x & 127, part = threadIdx.x >> 7, c = th & (wide - 1);
+  const int d0 = ((int)blockIdx.y * 128 + th) / wide * kJoinDims;
   int s = 0, hi_s = A.n_seqs - 1;
 #pragma unroll 1
   while (s < hi_s) {
@@ -861,12 +865,13 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
   const bool on = col < S.t * A.G;
   const int tok = S.tok0 + (on ? col / A.G : 0), head = g * A.G + (on ? col % A.G : 0);
   const int64_t at = (int64_t)tok * A.nq + head;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // (started while the parts are made)
   const int total = A.table[A.units], t0 = A.table[u], t1 = A.table[u + 1];
-  // the sequence's own rows join the first quarter
+  // the sequence's own rows join the first parts
   float m = -INFINITY, l = 0.f, v[kJoinDims];
 #pragma unroll
   for (int e = 0; e < kJoinDims; ++e) v[e] = 0.f;
-  if (quarter == 0 && on) {
+  if (part == 0 && on) {
     const float4* o = reinterpret_cast<const float4*>(o2 + at * A.hd + d0);
 #pragma unroll
     for (int e = 0; e < kJoinDims / 4; ++e) {
@@ -889,11 +894,11 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
   constexpr int64_t kSlot = 128 * (HD + 2);
   const float* p = A.part + (int64_t)(u + c0) * kSlot + c;
   if (on)
-    for (int k0 = quarter; k0 < parts; k0 += kJoinQuarters * kJoinLoads) {
+    for (int k0 = part; k0 < parts; k0 += Q * kJoinLoads) {
       float pm[kJoinLoads], pl[kJoinLoads], pv[kJoinLoads][kJoinDims];
 #pragma unroll
       for (int k = 0; k < kJoinLoads; ++k) {
-        const float* y = p + min(k0 + k * kJoinQuarters, parts - 1) * kSlot;   // (in the place of a part that is not there one that is)
+        const float* y = p + min(k0 + k * Q, parts - 1) * kSlot;   // (in the place of a part that is not there one that is)
         pm[k] = y[0];
         pl[k] = y[128];
 #pragma unroll
@@ -902,14 +907,14 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
       float top = m;
 #pragma unroll
       for (int k = 0; k < kJoinLoads; ++k)
-        if (k0 + k * kJoinQuarters < parts) top = fmaxf(top, pm[k]);
+        if (k0 + k * Q < parts) top = fmaxf(top, pm[k]);
       const float tb = top == -INFINITY ? 0.f : top, f0 = exp2f(m - tb);
       l *= f0;
 #pragma unroll
       for (int e = 0; e < kJoinDims; ++e) v[e] *= f0;
 #pragma unroll
       for (int k = 0; k < kJoinLoads; ++k)
-        if (k0 + k * kJoinQuarters < parts) {
+        if (k0 + k * Q < parts) {
           const float f = exp2f(pm[k] - tb);
           l = fmaf(pl[k], f, l);
 #pragma unroll
@@ -917,12 +922,12 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
         }
       m = top;
     }
-  s_m[quarter][c] = m;
-  s_l[quarter][c] = l;
+  s_m[part][th] = m;
+  s_l[part][th] = l;
 #pragma unroll
-  for (int e = 0; e < kJoinDims; ++e) s_v[quarter][e][c] = v[e];
+  for (int e = 0; e < kJoinDims; ++e) s_v[part][e][th] = v[e];
   __syncthreads();
-  if (quarter != 0 || !on) return;
+  if (part != 0 || !on) return;
   int q = 0, hi_q = own.n_seqs - 1;                        // the token's sequence
   while (q < hi_q) {
     const int mid = (q + hi_q + 1) >> 1;
@@ -932,17 +937,17 @@ __global__ void __launch_bounds__(128 * kJoinQuarters) k_join_group(const __grid
   if (n1 < 0 || n1 > S.cap || n2 < 0 || n2 > own.cap[q]) return;
   float top = m;
 #pragma unroll
-  for (int k = 1; k < kJoinQuarters; ++k) top = fmaxf(top, s_m[k][c]);
+  for (int k = 1; k < Q; ++k) top = fmaxf(top, s_m[k][th]);
   const float tb = top == -INFINITY ? 0.f : top;
   float sum = 0.f;
 #pragma unroll
   for (int e = 0; e < kJoinDims; ++e) v[e] = 0.f;
 #pragma unroll
-  for (int k = 0; k < kJoinQuarters; ++k) {
-    const float f = exp2f(s_m[k][c] - tb);
-    sum = fmaf(s_l[k][c], f, sum);
+  for (int k = 0; k < Q; ++k) {
+    const float f = exp2f(s_m[k][th] - tb);
+    sum = fmaf(s_l[k][th], f, sum);
 #pragma unroll
-    for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(s_v[k][e][c], f, v[e]);
+    for (int e = 0; e < kJoinDims; ++e) v[e] = fmaf(s_v[k][e][th], f, v[e]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t w[kJoinDims / 2];
@@ -990,11 +995,31 @@ cudaError_t launch_group_hd(const AttendArgs& A, bool low, int grid, cudaStream_
   return low ? launch_group_t<HD, true, true>(A, grid, st) : launch_group_t<HD, true, false>(A, grid, st);
 }
 
+template <int HD, int Q>
+cudaError_t launch_join_t(const AttendArgs& A, const float* o2, const float* l2, const int32_t* own_live, const GroupOwn& own, int grid, int wide,
+                          cudaStream_t st) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(A.units, A.hd / kJoinDims * wide / 128);
+  cfg.blockDim = dim3(128 * Q);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join_group<HD, Q>, A, o2, l2, own_live, own, grid, wide);
+}
+
 template <int HD>
 cudaError_t launch_join_hd(const AttendArgs& A, const float* o2, const float* l2, const int32_t* own_live, const GroupOwn& own, int grid,
                            cudaStream_t st) {
-  k_join_group<HD><<<dim3(A.units, A.hd / kJoinDims), 128 * kJoinQuarters, 0, st>>>(A, o2, l2, own_live, own, grid);
-  return cudaGetLastError();
+  int cols = 0;
+  for (int s = 0; s < A.n_seqs; ++s) cols = std::max(cols, A.seq[s].t * A.G);
+  const int wide = cols <= 32 ? 32 : (cols <= 64 ? 64 : 128);
+  const int64_t blocks = (int64_t)A.units * (A.hd / kJoinDims) * wide / 128, room = (int64_t)kJoinBlocks * grid;
+  if (4 * blocks <= room) return launch_join_t<HD, 4>(A, o2, l2, own_live, own, grid, wide, st);
+  if (2 * blocks <= room) return launch_join_t<HD, 2>(A, o2, l2, own_live, own, grid, wide, st);
+  return launch_join_t<HD, 1>(A, o2, l2, own_live, own, grid, wide, st);
 }
 
 }  // namespace
