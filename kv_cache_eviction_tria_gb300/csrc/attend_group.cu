@@ -1,6 +1,5 @@
 // Attention of many sequences' new tokens over one shared prefix, on the
-// fifth-generation tensor cores: a decode step of 17 columns (token x query
-// head of a KV head's group) or more.
+// fifth-generation tensor cores: a decode step, or a few tokens each.
 //
 //   S = Q K^T (128 x BN, fp32 in TMEM), P = 2^(scale S - M) (fp16, written over
 //   S in TMEM), O += P V (128 x head_dim, fp32 in TMEM), l = sum of P

@@ -65,9 +65,27 @@ void prefix_tokens(const int32_t* seq0, int n_prefixes, const int32_t* tok0, int
   for (int p = 0; p <= n_prefixes; ++p) out[p] = tok0[seq0[p]];
 }
 
-// Columns (token x query head of a KV head's group) of a prefix up to which its
-// rows are what is cut, by k_attend_group; more take the prompt kernel.
-constexpr int kGroupCols = 1024;
+// Whether the prefixes are a matter for k_attend_group, which cuts their rows over
+// the GPU. The others are k_attend's: of up to 16 columns (token x query head of a KV
+// head's group) the step kernel, of more the prompt kernel. `rows` are those that a CTA
+// would get, by the capacities, 128 columns at a time. Measured as whole calls, in us, of 8 KV
+// heads x 128 dims:
+//   up to 16 columns: fp16 planes always (4 columns: 777 rows 19.3 against 27.5 by the step
+//   kernel, 65536 rows 66 against 72; 16 columns 64 against 79). Of quantised ones the step
+//   kernel widens nothing and is faster in the long run (q8_0, 4 columns: 8192 rows 32 against 34,
+//   65536 rows 84 against 62): up to kGroupShort rows.
+//   up to kGroupFew columns (of quantised planes kGroupFewQ) always: 256 columns of 32768
+//   fp16 rows 81 against 104, 512 of q8_0 160 against 213.
+//   up to kGroupCols while a CTA gets kGroupLong rows at most: 512 columns of fp16, 16384
+//   rows 64 against 77, 32768 rows 117 against 107; 1024 of q8_0, 4096 rows 70 against 78.
+constexpr int kGroupFew = 256, kGroupFewQ = 512, kGroupCols = 1024, kGroupShort = 512, kGroupLong = 4096;
+
+bool by_group(const tria_layer_cache* c, int64_t most, int64_t units, int64_t rows) {
+  if (!tensor_types(c, TRIA_F16) || most == 0 || units > kMaxSegments) return false;
+  const bool quantised = c->k_type != TRIA_F16 || c->v_type != TRIA_F16;
+  if (most <= kStepCols) return !quantised || rows <= kGroupShort;
+  return most <= (quantised ? kGroupFewQ : kGroupFew) || (most <= kGroupCols && rows <= kGroupLong);
+}
 
 struct PrefixLayout {
   AttendLayout shared, own;
@@ -83,15 +101,16 @@ PrefixLayout prefix_layout(const tria_layer_cache* prefix, const tria_layer_cach
   int32_t tp[kMaxSeqs + 1];
   prefix_tokens(seq0, prefix->n_seqs, tok0, tp);
   const int G = nq / cache->n_kv_heads, hd = cache->head_dim;
-  int64_t units = 0, most = 0;
+  int64_t units = 0, most = 0, rows_of_units = 0;
   for (int p = 0; p < prefix->n_seqs; ++p) {
     const int64_t cols = (int64_t)(tp[p + 1] - tp[p]) * G;
     most = std::max(most, cols);
     units += (cols + 127) / 128 * cache->n_kv_heads;
+    rows_of_units += (cols + 127) / 128 * cache->n_kv_heads * prefix->capacity[p];
   }
-  L.group = tensor_types(prefix, TRIA_F16) && most > kStepCols && most <= kGroupCols && units <= kMaxSegments;
-  L.units = (int)units;
   L.own = attend_layout(cache, G, tok0);
+  L.group = by_group(prefix, most, units, rows_of_units / L.own.sms);
+  L.units = (int)units;
   // fp32 queries take the other kernels whatever the columns, with a layout that has no room for fp16 copies
   L.shared = attend_layout(prefix, G, tp);
   const size_t shared = L.group ? L.shared.wide_k : L.shared.total;

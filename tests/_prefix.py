@@ -6,12 +6,12 @@ import _rows as R
 from oracle import attend_oracle as A
 
 
-def pair(lib, rng, *, shared, rows, n_kv, hd, types, own_types=None, gaps=True, spare=5, spread=1.0):
+def pair(lib, rng, *, shared, rows, n_kv, hd, types, own_types=None, gaps=True, spare=5, own_spare=None, spread=1.0):
     """(prefix cache of shared[i] rows, cache of rows[s] own rows whose positions follow() moves behind the prefixes')."""
     k, v = types
     ok, ov = own_types or types
     p = R.Cache(lib, rng, rows=shared, cap=[n + spare for n in shared], n_kv=n_kv, hd=hd, k_type=k, v_type=v, gaps=gaps, spread=spread)
-    c = R.Cache(lib, rng, rows=rows, cap=[n + spare for n in rows], n_kv=n_kv, hd=hd, k_type=ok, v_type=ov, gaps=gaps, spread=spread)
+    c = R.Cache(lib, rng, rows=rows, cap=[n + (spare if own_spare is None else own_spare) for n in rows], n_kv=n_kv, hd=hd, k_type=ok, v_type=ov, gaps=gaps, spread=spread)
     return p, c
 
 

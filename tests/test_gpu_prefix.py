@@ -295,3 +295,37 @@ def test_one_workspace_for_calls_of_both_kinds(lib):
         lib.attend(p.cache, q, out, at, ws=ws)
         lib.attend(p.cache, q, once, at, ws=p.ws(lib.attend_workspace_size(p.cache, 16, 2)))
         assert torch.equal(once, out)
+
+
+@pytest.mark.parametrize("kind,k,v", [("f16", "f16", "f16"), ("bf16", "q8_0", "q4_0"), ("f16", "q4_0", "q8_0"), ("f16", "f16", "q8_0")])
+@pytest.mark.parametrize("seqs,tokens,window,sink", [(1, 1, 0, 0), (4, 1, 0, 0), (4, 1, 100, 3), (2, 2, 40, 0), (3, 80, 0, 0), (3, 80, 120, 5),
+                                                     (2, 150, 0, 0)])
+@pytest.mark.parametrize("n_kv,hd", [(2, 64), (1, 256)])
+def test_prefixes_of_large_capacity(lib, kind, k, v, seqs, tokens, window, sink, n_kv, hd):
+    """How a prefix is read depends on its capacity too: few live rows in a place for very many give the same results."""
+    rng = np.random.default_rng(81)
+    for shared, spare in (([400, 0], 90000 // n_kv), ([400, 0], 3)):
+        p, c = P.pair(lib, rng, shared=shared, rows=[tokens + 9] * (seqs + 1), n_kv=n_kv, hd=hd, types=(k, v), spare=spare, own_spare=5, gaps=False)
+        newest = P.follow(p, c, [0, seqs, seqs + 1])
+        run(lib, p, c, [0, seqs, seqs + 1], 4 * n_kv, kind, [tokens] * seqs + [1], newest=newest, window=window, sink=sink)
+
+
+def test_bad_n_live_in_prefixes_of_large_capacity(lib):
+    rng = np.random.default_rng(51)
+    for seqs, tokens in ((4, 1), (2, 150)):
+        p, c = P.pair(lib, rng, shared=[60, 60], rows=[tokens + 40] * seqs, n_kv=1, hd=64, types=("q8_0", "q8_0"), spare=90000, own_spare=0)
+        P.follow(p, c, [0, seqs // 2, seqs])
+        q = R.act(rng.standard_normal((seqs * tokens, 4, 64)), "f16")
+        pos = torch.full((seqs * tokens,), 10 ** 6, device="cuda", dtype=torch.int32)
+        ws = c.ws(lib.attend_prefix_workspace_size(p.cache, c.cache, 4, tokens))
+        half = seqs * tokens // 2
+        for bad in (-1, 90061):
+            keep = p.d["n_live"].clone()
+            p.d["n_live"][0] = bad
+            out = torch.full_like(q, 7.0)
+            lib.attend_prefix(p.cache, c.cache, q, out, pos, ws=ws)
+            assert lib.device_status(ws) == lib.ERR_DEVICE_ARG
+            assert (out[:half] == 7).all() and torch.isfinite(out).all() and (out[half:] != 7).any()
+            p.d["n_live"].copy_(keep)
+            lib.attend_prefix(p.cache, c.cache, q, out, pos, ws=ws)
+            assert lib.device_status(ws) == lib.OK and (out[:half] != 7).any()
