@@ -19,6 +19,12 @@
 // sequence. All layers are one launch, whose CTAs stride over blocks of
 // rows (layer, group, KV head, rows): how many there are is known on the
 // device alone, where n_live is.
+//
+// 36 layers, 4 groups of 8 beams, 401 rows of 8 KV heads x 128 dims: 249 us in fp16,
+// 5.5 TB/s of those bytes; one group of 32 beams, 1003 rows, q8_0 keys and q4_0
+// values 277 us, 4.2 TB/s: five planes with loads of their own, two of them and the
+// positions in pieces of four bytes. One layer of four beams takes 8 us, nearly all of it
+// the start and the end of a kernel.
 #include <string.h>
 
 #include <algorithm>
@@ -32,7 +38,10 @@ namespace {
 constexpr int kReorderThreads = 256, kBatch = 4;
 constexpr int kMaxLayers = 128, kMaxBeams = TRIA_MAX_BEAMS;
 constexpr int kMaxUnits = 2048;       // (layer, group) pairs of a launch
-constexpr int kMaxBlock = 64;         // rows of a block
+// Rows of a block at most: 16 KB of keys, so that a batch of four moves fills the
+// threads' loads twice (128-byte rows, 32 beams x 1003 rows x 36 layers: 276 us with
+// 128 of them, 290 with 64; 256-byte rows: 258 and 249)
+constexpr int kBlockBytes = 16384, kLeastMaxBlock = 64, kMostMaxBlock = 256;
 
 struct ReorderLayer {
   uint8_t *k, *ks, *v, *vs;
@@ -44,6 +53,7 @@ struct ReorderArgs {
   Ctrl* ctrl;
   int32_t n_layers, n_groups, n_seqs, n_kv;
   int32_t k_rb, v_rb, ks_rb, vs_rb;   // bytes of a row of each plane (0: none)
+  int32_t max_block;
   int32_t cap[kMaxSeqs];
   int64_t row0[kMaxSeqs];
   int32_t seq0[kMaxSeqs + 1];
@@ -56,27 +66,30 @@ constexpr uint32_t kKeep = 1u << 16, kTake = 1u << 17;
 __device__ __forceinline__ int dst_of(uint32_t op) { return op & 0xFF; }
 __device__ __forceinline__ int src_of(uint32_t op) { return (op >> 8) & 0xFF; }
 
-// What a batch of moves copies of a block: first rows of the sources and the
-// destinations in a plane, rows.
-struct Batch {
-  int64_t from[kBatch], to[kBatch];
-  int rows[kBatch], most;
+// What a block's moves copy: first rows of the sources and the destinations in
+// a plane, rows (none behind the last move).
+struct Moves {
+  int64_t from[kMaxBeams + kBatch], to[kMaxBeams + kBatch];
+  int rows[kMaxBeams + kBatch];
 };
 
-// The batch's rows of a plane, a piece of T at a time, P pieces of each of M
-// moves in flight, everything of a piece read before anything is written.
+// Rows of a plane by the M moves from `at` on, a piece of T at a time, P pieces of
+// each move in flight, everything of a piece read before anything is written. (A
+// piece is the same thread's in every batch.)
 template <int M, typename T>
-__device__ __forceinline__ void copy_plane(uint8_t* plane, int rb, const Batch& B) {
+__device__ __forceinline__ void copy_plane(uint8_t* plane, int rb, const Moves& B, int at) {
   constexpr int P = 8 / M;
-  const int per = rb / (int)sizeof(T), n = B.most * per;
+  const int per = rb / (int)sizeof(T);
+  int n = 0;
   const T* from[M];
   T* to[M];
   int most[M];
 #pragma unroll
   for (int j = 0; j < M; ++j) {
-    from[j] = reinterpret_cast<const T*>(plane + B.from[j] * rb);
-    to[j] = reinterpret_cast<T*>(plane + B.to[j] * rb);
-    most[j] = B.rows[j] * per;
+    from[j] = reinterpret_cast<const T*>(plane + B.from[at + j] * rb);
+    to[j] = reinterpret_cast<T*>(plane + B.to[at + j] * rb);
+    most[j] = B.rows[at + j] * per;
+    n = max(n, most[j]);
   }
 #pragma unroll 1
   for (int i = threadIdx.x; i < n; i += P * kReorderThreads) {
@@ -96,15 +109,15 @@ __device__ __forceinline__ void copy_plane(uint8_t* plane, int rb, const Batch& 
 
 // A batch's moves of one block, plane by plane.
 template <int M>
-__device__ __forceinline__ void copy_moves(const ReorderArgs& A, const ReorderLayer& L, const Batch& B) {
+__device__ __forceinline__ void copy_moves(const ReorderArgs& A, const ReorderLayer& L, const Moves& B, int at) {
 #pragma unroll 1
   for (int x = 0; x < 2; ++x) {
-    copy_plane<M, uint4>(x ? L.v : L.k, x ? A.v_rb : A.k_rb, B);
+    copy_plane<M, uint4>(x ? L.v : L.k, x ? A.v_rb : A.k_rb, B, at);
     const int rb = x ? A.vs_rb : A.ks_rb;
-    if (rb % 4) copy_plane<M, uint16_t>(x ? L.vs : L.ks, rb, B);
-    else if (rb) copy_plane<M, uint32_t>(x ? L.vs : L.ks, rb, B);
+    if (rb % 4) copy_plane<M, uint16_t>(x ? L.vs : L.ks, rb, B, at);
+    else if (rb) copy_plane<M, uint32_t>(x ? L.vs : L.ks, rb, B, at);
   }
-  copy_plane<M, uint32_t>(reinterpret_cast<uint8_t*>(L.pos), 4, B);
+  copy_plane<M, uint32_t>(reinterpret_cast<uint8_t*>(L.pos), 4, B, at);
 }
 
 // More moves than a batch, rings among them: move by move, piece by piece.
@@ -175,7 +188,7 @@ __global__ void __launch_bounds__(kReorderThreads, 2) k_reorder(const __grid_con
   __shared__ uint8_t s_ring[kMaxSeqs];
   __shared__ int s_first[kMaxUnits + 1], s_rows[kMaxUnits];
   __shared__ int s_scan[40];
-  __shared__ Batch s_batch;
+  __shared__ Moves s_moves[2];                             // of this block and the one before
   __shared__ int s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int group = warp; group < A.n_groups; group += kReorderThreads / 32) {
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kReorderThreads, 2) k_reorder(const __grid_con
   int all;
   block_exclusive_scan(sum, &all, s_scan);
   // blocks small enough that every CTA has some, large enough that a plane's piece is no single load
-  const int block = (int)min((int64_t)kMaxBlock, max((int64_t)8, (int64_t)all * A.n_kv * 2 / (int64_t)gridDim.x & ~(int64_t)7));
+  const int block = (int)min((int64_t)A.max_block, max((int64_t)8, (int64_t)all * A.n_kv * 2 / (int64_t)gridDim.x & ~(int64_t)7));
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int u = (int)threadIdx.x * per + i;
@@ -239,8 +252,14 @@ __global__ void __launch_bounds__(kReorderThreads, 2) k_reorder(const __grid_con
     before += A.n_kv * ((max(s_rows[u], 0) + block - 1) / block);
   }
   if (threadIdx.x == 0) s_first[units] = total;
+  if (threadIdx.x < 2 * kBatch) {
+    Moves& B = s_moves[threadIdx.x / kBatch];
+    B.from[kMaxBeams + threadIdx.x % kBatch] = B.to[kMaxBeams + threadIdx.x % kBatch] = 0;
+    B.rows[kMaxBeams + threadIdx.x % kBatch] = 0;
+  }
   __syncthreads();
 
+  int turn = 0;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     int u = 0, hi = units - 1;                             // the last unit that starts at or before it
     while (u < hi) {
@@ -261,24 +280,19 @@ __global__ void __launch_bounds__(kReorderThreads, 2) k_reorder(const __grid_con
       copy_rings<uint32_t>(A, reinterpret_cast<uint8_t*>(L.pos), 4, L.n_live, ops, n, g, r0, most);
       continue;
     }
+    Moves& B = s_moves[turn ^= 1];
+    if (warp == 0) {
+      const uint32_t op = ops[min(lane, n - 1)];
+      const int s = src_of(op), d = dst_of(op);
+      B.from[lane] = A.row0[s] + (int64_t)g * A.cap[s] + r0;
+      B.to[lane] = A.row0[d] + (int64_t)g * A.cap[d] + r0;
+      B.rows[lane] = lane < n ? max(0, min(block, *((volatile const int32_t*)(L.n_live + s)) - r0)) : 0;
+    }
+    __syncthreads();
+#pragma unroll 1
     for (int at = 0; at < n; at += kBatch) {
-      const int m = min(kBatch, n - at);
-      __syncthreads();                                     // the batch before it is done with
-      if (warp == 0) {
-        const uint32_t op = ops[at + min(lane, m - 1)];
-        const int s = src_of(op), d = dst_of(op);
-        const int rows = lane < m ? max(0, min(block, *((volatile const int32_t*)(L.n_live + s)) - r0)) : 0;
-        if (lane < kBatch) {
-          s_batch.from[lane] = A.row0[s] + (int64_t)g * A.cap[s] + r0;
-          s_batch.to[lane] = A.row0[d] + (int64_t)g * A.cap[d] + r0;
-          s_batch.rows[lane] = rows;
-        }
-        const int most = __reduce_max_sync(0xffffffffu, rows);
-        if (lane == 0) s_batch.most = most;
-      }
-      __syncthreads();
-      if (m <= 2) copy_moves<2>(A, L, s_batch);
-      else copy_moves<4>(A, L, s_batch);
+      if (n - at <= 2) copy_moves<2>(A, L, B, at);
+      else copy_moves<4>(A, L, B, at);
     }
   }
 
@@ -364,6 +378,7 @@ extern "C" tria_status tria_reorder(const tria_layer_cache* caches, int32_t n_la
   A.n_kv = c.n_kv_heads;
   A.k_rb = row_bytes(c.k_type, c.head_dim);
   A.v_rb = row_bytes(c.v_type, c.head_dim);
+  A.max_block = std::min(std::max(kBlockBytes / A.k_rb, kLeastMaxBlock), kMostMaxBlock) & ~7;
   A.ks_rb = c.k_scale ? c.head_dim / 16 : 0;
   A.vs_rb = c.v_scale ? c.head_dim / 16 : 0;
   int64_t rows = 0;
