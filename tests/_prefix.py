@@ -11,7 +11,8 @@ def pair(lib, rng, *, shared, rows, n_kv, hd, types, own_types=None, gaps=True, 
     k, v = types
     ok, ov = own_types or types
     p = R.Cache(lib, rng, rows=shared, cap=[n + spare for n in shared], n_kv=n_kv, hd=hd, k_type=k, v_type=v, gaps=gaps, spread=spread)
-    c = R.Cache(lib, rng, rows=rows, cap=[n + (spare if own_spare is None else own_spare) for n in rows], n_kv=n_kv, hd=hd, k_type=ok, v_type=ov, gaps=gaps, spread=spread)
+    room = spare if own_spare is None else own_spare
+    c = R.Cache(lib, rng, rows=rows, cap=[n + room for n in rows], n_kv=n_kv, hd=hd, k_type=ok, v_type=ov, gaps=gaps, spread=spread)
     return p, c
 
 
