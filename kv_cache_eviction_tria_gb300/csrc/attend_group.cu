@@ -63,7 +63,7 @@ struct GroupShape {
   static_assert(kSmem + (3 * kMaxSegments + 256) * 4 <= 227 * 1024, "shared memory");
 };
 
-constexpr int kGroupBars = 2 * 12 + 4 + 4 + 5 + 4 * 8;
+constexpr int kGroupBars = 2 * 12 + 4 + 4 + 4 + 4 + 4 * 8;
 struct GroupShared {
   uint32_t junk[12][4];                                    // rows of a value tile that held junk, by stage
   int32_t lo[8], hi[8], c_lo[4], c_hi[4];                  // positions, a warp each
@@ -186,9 +186,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
   __shared__ int s_scan[40];
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + H::oBar);
   // full: a tile is in the ring; empty: its products are done; s: scores; p: weights; o: a tile's
-  // sums; f: the unit's last sums; q: queries; x: every product; v: values that are looked
+  // sums (all three by score buffer); f: the unit's last sums; q: queries; x: every product; v: values that are looked
   // through before their tile is full; rf, re: codes (of keys, of values) are there, are used
-  uint64_t *b_full = bar, *b_empty = bar + 12, *b_s = bar + 24, *b_p = b_s + 4, *b_o = b_p + 4, *b_f = b_o + 1, *b_q = b_f + 1,
+  uint64_t *b_full = bar, *b_empty = bar + 12, *b_s = bar + 24, *b_p = b_s + 4, *b_o = b_p + 4, *b_f = b_o + 4, *b_q = b_f + 1,
            *b_x = b_q + 1, *b_v = b_x + 1, *b_rfk = b_v + 1, *b_rek = b_rfk + 8, *b_rfv = b_rek + 8, *b_rev = b_rfv + 8;
   int32_t* s_pos = reinterpret_cast<int32_t*>(smem + H::oPos);
   float* s_ref = reinterpret_cast<float*>(smem + H::oRef);
@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b_s[i], 1);
       mbar_init(&b_p[i], 128);
+      mbar_init(&b_o[i], 1);
     }
-    mbar_init(b_o, 1);
     mbar_init(b_f, 1);
     mbar_init(b_q, 256);
     mbar_init(b_x, 1);
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
       const uint32_t d = tm + H::cO, a = tm + H::cS + buf * BN;
 #pragma unroll
       for (int k = 0; k < BN / 16; ++k) tc_mma_ts(d, a + k * 8, b + (uint64_t)(k * 128), mma_desc(HD, true), add || k > 0);
-      tc_commit(b_o);
+      tc_commit(&b_o[buf]);
       tc_commit(&b_empty[st]);
     };
     bool ok = true;
@@ -765,7 +765,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) k_attend_group(const __grid_
           M = now;
         }
         if (!first && __any_sync(0xffffffffu, move)) {
-          wait(b_o, (j - 1) & 1);                          // the sums of the tile before may be running
+          // the sums of the tile before, and of the one before that, may be running (with one barrier for all
+          // of them, a parity could not tell either from sums done two tiles earlier)
+          wait(&b_o[(j - 1) & 3], ((j - 1) >> 2) & 1);
           __syncwarp();
           tc_fence_after();
           const float a = move ? exp2_fast(before - now) : 1.f;

@@ -6,6 +6,7 @@ import pytest
 
 import _prefix as P
 import _rows as R
+from oracle import attend_oracle as A
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -329,3 +330,40 @@ def test_bad_n_live_in_prefixes_of_large_capacity(lib):
             p.d["n_live"].copy_(keep)
             lib.attend_prefix(p.cache, c.cache, q, out, pos, ws=ws)
             assert lib.device_status(ws) == lib.OK and (out[:half] != 7).any()
+
+
+@pytest.mark.parametrize("kind,k,v,hd", [("f16", "f16", "f16", 128), ("f16", "f16", "f16", 256), ("f16", "f16", "q8_0", 64), ("f16", "q8_0", "q4_0", 128),
+                                         ("f16", "q4_0", "f16", 64)])
+@pytest.mark.parametrize("seqs", [4, 20])
+def test_logits_that_rise_again_and_again(lib, kind, k, v, hd, seqs):
+    """Logits rise by 9.5 powers of two every 64 rows, so that the reference of the softmax moves at every tile, and fall back
+    to their start after 2000 rows; the same call gives the same bits ten times, whatever the workspace held."""
+    n_kv, rows = 8, 24000
+    rng = np.random.default_rng(hd)
+    p, c = P.pair(lib, rng, shared=[rows], rows=[5] * seqs, n_kv=n_kv, hd=hd, types=(k, v), gaps=False, spare=0)
+    sign = rng.choice([-1.0, 1.0], hd)
+    rise = (np.arange(rows) % 2000) * (9.5 / 64 * np.log(2))
+    for g in range(n_kv):
+        r0 = p.row0[0] + g * p.cap[0]
+        data, scale = A.hold((rise[:, None] * sign / np.sqrt(hd) + 0.3 * rng.standard_normal((rows, hd))).astype(np.float32), k)
+        for name, x in (("k", data), ("k_scale", scale)):
+            if x is not None:
+                p.h[name][r0:r0 + rows] = x
+    for name in ("k", "k_scale"):
+        if p.h[name] is not None:
+            p.d[name].copy_(torch.from_numpy(p.h[name]))
+    newest = P.follow(p, c, [0, seqs])
+    q = R.act(sign * (1 + 0.1 * rng.standard_normal((seqs, 4 * n_kv, hd))), kind)
+    pos = torch.tensor(newest, device="cuda", dtype=torch.int32)
+    first = None
+    for i in range(10):
+        out, lse = torch.zeros_like(q), torch.zeros(seqs, 4 * n_kv, device="cuda")
+        ws = torch.full((lib.attend_prefix_workspace_size(p.cache, c.cache, 4 * n_kv, 1),), 255, dtype=torch.uint8, device="cuda")
+        lib.workspace_init(ws)
+        lib.attend_prefix(p.cache, c.cache, q, out, pos, lse=lse, ws=ws)
+        assert lib.device_status(ws) == lib.OK
+        if first is None:
+            first = out, lse
+            want = P.expected(p, c, [0, seqs], R.host(q), pos.cpu().numpy(), np.arange(seqs + 1), 4 * n_kv)
+            P.check(R.host(out), R.host(lse), want, kind, True, rows + 5, hd, k_exact=k == "f16")
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
