@@ -739,8 +739,10 @@ tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* att
  * sequences; a group may have none). */
 
 /* Workspace bytes of tria_attend_prefix (0 on invalid input). The notes at
- * tria_attend_workspace_size hold; one that is large enough for each serves
- * calls of both. */
+ * tria_attend_workspace_size hold, but the fp16 copies of a quantised prefix:
+ * it is widened on the way, without them, for up to 512 tokens x query heads per
+ * KV head of a prefix and, if it is short, 1024. A workspace that is large enough
+ * for each serves calls of both. */
 size_t tria_attend_prefix_workspace_size(const tria_layer_cache* prefix, const tria_layer_cache* cache,
                                          const int32_t* seq0, int32_t n_q_heads, const int32_t* tok0);
 
@@ -752,8 +754,11 @@ size_t tria_attend_prefix_workspace_size(const tria_layer_cache* prefix, const t
  * are the prefix's). prefix->n_seqs groups; the same n_kv_heads and head_dim in
  * both caches (INVALID_ARG otherwise), the plane types may differ. Positions
  * ascend strictly with the rows of a segment of each cache. Everything else,
- * roundings and errors too, as tria_attend: the two results are joined in fp32
- * by their log-sum-exps. A token whose prefix or sequence has a bad n_live gets
+ * errors too, as tria_attend: the two results are joined in fp32 by their
+ * log-sum-exps. On the tensor cores a prefix has the roundings of tria_attend's
+ * prompts, round_keys among them, whatever the number of its tokens, but for
+ * a long quantised one with up to 16 tokens x query heads per KV head (those of
+ * decode steps). A token whose prefix or sequence has a bad n_live gets
  * no outputs. ws is not shared with calls that overlap on the GPU. */
 tria_status tria_attend_prefix(const tria_layer_cache* prefix, const tria_layer_cache* cache, const int32_t* seq0,
                                const tria_attention* attention, void* ws, size_t ws_bytes, void* stream);

@@ -82,6 +82,8 @@ constexpr int kGroupFew = 256, kGroupFewQ = 512, kGroupCols = 1024, kGroupShort 
 
 bool by_group(const tria_layer_cache* c, int64_t most, int64_t units, int64_t rows) {
   if (!tensor_types(c, TRIA_F16) || most == 0 || units > kMaxSegments) return false;
+  for (int p = 0; p < c->n_seqs; ++p)                      // (a row of a TMA tile has a signed 32-bit coordinate)
+    if (c->seq_row0[p] + (int64_t)c->n_kv_heads * c->capacity[p] >= ((int64_t)1 << 31)) return false;
   const bool quantised = c->k_type != TRIA_F16 || c->v_type != TRIA_F16;
   if (most <= kStepCols) return !quantised || rows <= kGroupShort;
   return most <= (quantised ? kGroupFewQ : kGroupFew) || (most <= kGroupCols && rows <= kGroupLong);

@@ -156,3 +156,12 @@ def test_reorder_refusals(lib):
     assert lib.tria_reorder_workspace_size(arr, 2, None, 1) == 0 and lib.tria_reorder_workspace_size(None, 2, s0.ctypes.data, 1) == 0
     twice = (tria._LayerCache * 2)(a, a)
     assert lib.tria_reorder_workspace_size(twice, 2, s0.ctypes.data, 1) == 0
+
+
+def test_rows_past_a_tiles_coordinate_take_no_tiles(lib):
+    """A prefix whose last row's index needs more than 31 bits: up to 16 columns read it without tiles, which shows in the
+    workspace."""
+    t, s0 = np.asarray([0, 1, 2], np.int32), np.asarray([0, 2], np.int32)
+    size = [lib.tria_attend_prefix_workspace_size(ctypes.byref(cache(1, 0x40000, seq_row0=[r])), ctypes.byref(cache()), s0.ctypes.data, 4,
+                                                  t.ctypes.data) for r in (0, (1 << 31) - 201, (1 << 31) - 200)]
+    assert size[0] == size[1] > size[2] > 0
