@@ -5,7 +5,9 @@
 //   out = (o1 e^(l1 - m) + o2 e^(l2 - m)) / (e^(l1 - m) + e^(l2 - m)),
 //   lse = m + ln(e^(l1 - m) + e^(l2 - m)),   m = max(l1, l2)
 //
-// of the two attentions' outputs o and log-sum-exps l, both in fp32.
+// of the two attentions' outputs o and log-sum-exps l, both in fp32. The own rows are
+// tria_attend's; the prefix, too, or k_attend_group's, whose join then takes the own
+// rows in. That join and k_attend_group start while the kernel before them ends.
 #include <math.h>
 #include <string.h>
 
