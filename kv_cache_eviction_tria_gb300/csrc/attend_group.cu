@@ -38,9 +38,13 @@
 // columns take 91 us, bound by the softmax and its hand-overs (1.42 us per 128 rows and
 // 128 columns). 65536 q8_0 rows, 256 columns: 120 us, 1.95 us per 128 rows and 128 columns;
 // q4_0 2.3. There the warpgroup that widens keys sets the pace: 1000 of a tile's 2240
-// cycles are its conversions, the rest waits, fences and meetings, in 0.54 of all
-// issue slots. With a quarter of the keys widened by the values' warpgroup the same rows
-// took 155 us.
+// cycles are its conversions, the rest waits, fences and meetings. Roles at work side by
+// side are bound by the supply of instructions, not by a unit: the SM's instruction cache
+// gives 0.70 of the requests it can, 0.04 of them from further away, for 0.54 of
+// the issue slots, and what lets more roles run at once makes each of them
+// slower. With a quarter of the keys widened by the values' warpgroup the same rows took
+// 155 us, with both warpgroups widening keys and values of tiles in turn 150, and with keys that need not
+// wait for sums (two rings, scores three tiles ahead) 127.
 #include <string.h>
 
 #include <algorithm>
