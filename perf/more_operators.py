@@ -280,8 +280,6 @@ def prepare(case, seed):
         layers, n, kv, hd = case["layers"], case["groups"] * case["beams"], case["kv"], case["hd"]
         rows = [r for r in _beam_rows(case) for _ in range(case["beams"])]
         cap = max(rows) + 36
-        while n * kv * cap * (hd // 16) % 16:              # every layer's scales start where a cache's may
-            cap += 1
         parts = [_planes(gen, case, n, cap) for _ in range(layers)]
         st["planes"] = {k: None if parts[0][k] is None else torch.stack([p[k] for p in parts]) for k in parts[0]}
         del parts
