@@ -787,7 +787,9 @@ typedef struct tria_beams {
   int32_t* ended_out;         /* optional device [n_groups][n_out] */
 } tria_beams;
 
-/* Workspace bytes (0 on invalid input), zeroed once (tria_workspace_init). */
+/* Workspace bytes (0 on invalid input), zeroed once (tria_workspace_init). One
+ * that is large enough for each serves calls of different shapes, of attention
+ * too. */
 size_t tria_beam_select_workspace_size(const int32_t* seq0, int32_t n_groups, int32_t vocab, int32_t n_out);
 
 /* The n_out best continuations of every group, in one kernel. Continuation

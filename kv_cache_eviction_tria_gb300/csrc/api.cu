@@ -65,9 +65,8 @@ Layout make_layout(const tria_layer_cache* c, int G) {
   L.c_max = (cap_max + kChunk - 1) / kChunk;
   size_t off = 0;
   L.ctrl = off;
-  off = up(off + sizeof(Ctrl));
-  L.pass_ctl = off;
-  off = up(off + sizeof(PassCtl));
+  L.pass_ctl = kCountersAt;
+  off = kScratchAt;
   L.seg = off;
   off = up(off + (size_t)L.n_seg * sizeof(SegState));
   L.runs = off;

@@ -409,8 +409,8 @@ AttendLayout attend_layout(const tria_layer_cache* c, int G, const int32_t* tok0
   }
   L.sms = sm_count();
   L.split = plain_split(units * c->n_kv_heads, cap_max, L.sms, kMaxSegments);
-  L.count = up256(sizeof(Ctrl));
-  L.span = up256(L.count + sizeof(uint32_t) * (size_t)kMaxSegments);
+  L.count = kCountersAt;
+  L.span = kScratchAt;
   L.part = up256(L.span + 2 * sizeof(int32_t) * (size_t)c->n_seqs * c->n_kv_heads);
   const size_t plain = L.split > 1 ? (size_t)(units * c->n_kv_heads) * L.split * kCols * (c->head_dim + 2) : 0;
   // a part a warp (at most 12 a CTA) and two a CTA

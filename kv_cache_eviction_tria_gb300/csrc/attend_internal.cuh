@@ -84,10 +84,8 @@ struct AttendArgs {
 
 // The kernels of a call run one after the other and share the arrival counters
 // and the space of the partial results. The layout covers every type of
-// queries. The counters, which have to be zero between calls, take the same
-// place for every shape, so that a workspace may serve calls of different
-// shapes: a decode step counts segments, the fp32 kernel the units that it
-// splits, at most kMaxSegments both.
+// queries. The counters lie at kCountersAt, whatever the shape: a decode step counts
+// segments, the fp32 kernel the units that it splits, at most kMaxSegments both.
 struct AttendLayout {
   size_t count, span, part, wide_k, wide_kl, wide_v, total;
   int split, prompt_split, sms;

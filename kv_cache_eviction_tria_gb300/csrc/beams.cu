@@ -547,8 +547,8 @@ BeamLayout beam_layout(const int32_t* seq0, int n_groups, int vocab, int n_out) 
   for (L.held = kHeld; L.held > 8 && (int64_t)beams * pieces() < sms;) L.held /= 2;
   for (L.per = 1; L.per < pieces() && (int64_t)beams * ((pieces() + L.per - 1) / L.per) > 4 * (int64_t)sms;) ++L.per;
   L.parts = (pieces() + L.per - 1) / L.per;
-  L.count = up256(sizeof(Ctrl));
-  L.part = up256(L.count + sizeof(uint32_t) * kMaxSeqs);
+  L.count = kCountersAt;
+  L.part = kScratchAt;
   L.best = up256(L.part + sizeof(float2) * (size_t)beams * L.parts);
   L.total = up256(L.best + sizeof(uint2) * (size_t)beams * L.parts * n_out);
   return L;

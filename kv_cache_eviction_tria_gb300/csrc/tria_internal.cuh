@@ -193,6 +193,14 @@ struct PassCtl {
   int32_t move_next[kPassCtlSegs];    // next destination block to claim per segment
 };
 
+// Every workspace layout begins alike: the control words, then the words that are
+// zero between calls - the fused pass's state or, in their place, the arrival counters
+// of attention and of beam selection, which put them back to zero too - then
+// whatever a call writes and leaves. So no call finds another's data in its counters.
+constexpr size_t kCountersAt = sizeof(Ctrl), kScratchAt = kCountersAt + sizeof(PassCtl);
+static_assert(kCountersAt % 256 == 0 && kScratchAt % 256 == 0, "workspace parts start on 256 bytes");
+static_assert(sizeof(PassCtl) >= sizeof(uint32_t) * kMaxSegments, "room for a counter of every segment");
+
 __device__ __forceinline__ bool is_protected(int r, int n, int sink, int window) {
   return r < sink || r >= n - window;
 }

@@ -1,0 +1,88 @@
+"""One workspace for all calls of a beam search, one after the other: every
+result has the bits that it has when each call gets a workspace of its own. There are more
+segments (sequences x KV heads) than groups may hold beams, and their rows
+reach across CTAs, so that the calls' counters and parts lie side by side."""
+import numpy as np
+import pytest
+
+import _prefix as P
+import _rows as R
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+class Search:
+    """Beams over shared prompts: append, attention over both caches and over the own rows, choice, reorder."""
+
+    def __init__(self, lib, cfg, steps):
+        self.lib, self.cfg = lib, cfg
+        rng = np.random.default_rng(cfg["beams"])
+        self.groups, self.n_kv, self.hd, self.kind = len(cfg["shared"]), cfg["n_kv"], cfg["hd"], cfg["kind"]
+        self.n = n = self.groups * cfg["beams"]
+        self.nq = self.n_kv * cfg["group"]
+        self.seq0 = [cfg["beams"] * g for g in range(self.groups + 1)]
+        rows = [int(x) for x in rng.integers(cfg["least"], cfg["least"] + 60, n)]
+        self.p, self.c = P.pair(lib, rng, shared=cfg["shared"], rows=rows, n_kv=self.n_kv, hd=self.hd, types=cfg["prefix"],
+                                own_types=cfg["own"], gaps=False, own_spare=steps + 70)
+        newest = P.follow(self.p, self.c, self.seq0)
+        self.rope = lib.Rope(head_dim=self.hd, theta=1e4)
+        qm = rng.standard_normal((1, self.nq, self.hd // 2, 2)).astype(np.float32)
+        self.stats = lib.Stats(qm, np.hypot(qm[..., 0], qm[..., 1]), n_kv_heads=self.n_kv, head_dim=self.hd, rope_theta=1e4)
+        self.heads = self.nq + 2 * self.n_kv
+        self.joint = [R.act(rng.standard_normal((n, self.heads, self.hd)), self.kind) for _ in range(steps)]
+        self.logits = [R.act(3 * rng.standard_normal((n, cfg["vocab"])), "bf16") for _ in range(steps)]
+        self.pos = torch.tensor(np.asarray(newest) + 1, device="cuda", dtype=torch.int32)
+        self.total = torch.zeros(n, device="cuda")
+        self.parent = torch.zeros(self.groups, cfg["beams"], device="cuda", dtype=torch.int32)
+        self.token = torch.zeros_like(self.parent)
+        one = np.arange(n + 1, dtype=np.int32)
+        self.sizes = dict(pass_=lib.workspace_size(self.c.cache, cfg["group"]), attend=lib.attend_workspace_size(self.c.cache, self.nq, one),
+                          prefix=lib.attend_prefix_workspace_size(self.p.cache, self.c.cache, self.nq, 1, self.seq0),
+                          select=lib.beam_select_workspace_size(self.seq0, cfg["vocab"], cfg["beams"]),
+                          reorder=lib.reorder_workspace_size([self.c.cache], self.seq0))
+
+    def run(self, steps, ws_of, evict=()):
+        """The results of every step; ws_of(size) gives a call's workspace."""
+        lib, c, cfg, out = self.lib, self.c, self.cfg, []
+        for i in range(steps):
+            used = [ws_of(self.sizes[k]) for k in ("pass_", "prefix", "attend", "select", "reorder", "pass_")]
+            q, o = (torch.full((self.n, self.nq, self.hd), 7.0, device="cuda", dtype=self.joint[i].dtype) for _ in range(2))
+            own, lse, own_lse = torch.full_like(o, 7.0), *(torch.full((self.n, self.nq), 7.0, device="cuda") for _ in range(2))
+            j, nq, n_kv = self.joint[i], self.nq, self.n_kv
+            lib.append_qkv(self.rope, c.cache, j[:, :nq], j[:, nq:nq + n_kv], j[:, nq + n_kv:], self.pos, q_out=q, ws=used[0])
+            lib.attend_prefix(self.p.cache, c.cache, q, o, self.pos, seq0=self.seq0, lse=lse, ws=used[1])
+            lib.attend(c.cache, q, own, self.pos, lse=own_lse, ws=used[2])
+            lib.beam_select(self.logits[i], self.total, self.total, self.parent, self.token, seq0=self.seq0, in_place=True, ws=used[3])
+            lib.reorder([c.cache], self.parent, seq0=self.seq0, ws=used[4])
+            out += [o, own, lse, own_lse, self.total.clone(), self.parent.clone(), self.token.clone(), c.d["n_live"].clone()]
+            self.pos += 1
+            if i in evict:
+                lib.evict(self.stats, 0, c.cache, lib.Policy(budget_rows=[cfg["least"] // 2] * self.n, window=4, cur_pos=self.pos.tolist()), ws=used[5])
+                out.append(c.d["n_live"].clone())
+            for w in used:
+                assert lib.device_status(w) == lib.OK
+        return out + [t.clone() for t in c.d.values() if t is not None]
+
+
+def once_and_again(lib, cfg, steps, evict=()):
+    x = Search(lib, cfg, steps)
+    shared = x.c.ws(max(x.sizes.values()))
+    got = x.run(steps, lambda size: shared, evict)
+    y = Search(lib, cfg, steps)
+    want = y.run(steps, y.c.ws, evict)
+    bits = lambda t: t.contiguous().view(torch.uint8)
+    bad = [i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(bits(a), bits(b))]
+    assert not bad, f"results {bad} of {len(want)} differ from those with a workspace for each call"
+
+
+LOOPS = [dict(kind="f16", prefix=("f16", "f16"), own=("f16", "f16"), n_kv=8, group=2, hd=64, shared=[300], beams=32, vocab=40000, least=20),
+         dict(kind="bf16", prefix=("q8_0", "q8_0"), own=("q8_0", "q8_0"), n_kv=8, group=4, hd=128, shared=[300, 77], beams=24, vocab=9001, least=30),
+         dict(kind="f16", prefix=("q4_0", "q4_0"), own=("q4_0", "q8_0"), n_kv=8, group=2, hd=64, shared=[700, 9], beams=24, vocab=33000, least=40),
+         dict(kind="f32", prefix=("f16", "f16"), own=("f16", "f16"), n_kv=8, group=2, hd=64, shared=[300], beams=32, vocab=9001, least=1200),
+         dict(kind="f32", prefix=("q8_0", "f32"), own=("q8_0", "f32"), n_kv=8, group=1, hd=64, shared=[90, 300], beams=24, vocab=9001, least=1100)]
+
+
+@pytest.mark.parametrize("cfg", LOOPS)
+def test_attention_choice_and_reorder(lib, cfg):
+    once_and_again(lib, cfg, 4)
