@@ -204,7 +204,10 @@ void tria_free_stats(tria_stats* stats);
 size_t tria_workspace_size(const tria_layer_cache* cache, int32_t group);
 
 /* Zeroes a workspace (required once after allocation and after any device
- * error). Asynchronous. */
+ * error). Asynchronous. One workspace, as large as the largest of the calls' sizes, serves
+ * every call of this library that takes one, one after the other and whatever
+ * their caches and shapes: all keep their counters, which calls leave at zero, in the same
+ * place, and rely on nothing else that a workspace held before the call. */
 tria_status tria_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Step 1 only: writes s(r) to score_out[row] (device float, global row index)
@@ -701,8 +704,7 @@ typedef struct tria_attention {
 
 /* Workspace bytes of tria_attend for these shapes (0 on invalid input). The
  * workspace is zeroed once (tria_workspace_init) and not shared with other
- * calls that overlap on the GPU, nor with the pass's workspace; one that is
- * large enough for each serves calls of different shapes. Prompts (more than
+ * calls that overlap on the GPU. Prompts (more than
  * 16 tokens x query heads per KV head in a sequence) over q8_0 or q4_0 planes
  * keep an fp16 copy of their sequences' planes in it, of keys two. */
 size_t tria_attend_workspace_size(const tria_layer_cache* cache, int32_t n_q_heads, const int32_t* tok0);
@@ -741,8 +743,7 @@ tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* att
 /* Workspace bytes of tria_attend_prefix (0 on invalid input). The notes at
  * tria_attend_workspace_size hold, but the fp16 copies of a quantised prefix:
  * it is widened on the way, without them, for up to 512 tokens x query heads per
- * KV head of a prefix and, if it is short, 1024. A workspace that is large enough
- * for each serves calls of both. */
+ * KV head of a prefix and, if it is short, 1024. */
 size_t tria_attend_prefix_workspace_size(const tria_layer_cache* prefix, const tria_layer_cache* cache,
                                          const int32_t* seq0, int32_t n_q_heads, const int32_t* tok0);
 
@@ -787,9 +788,7 @@ typedef struct tria_beams {
   int32_t* ended_out;         /* optional device [n_groups][n_out] */
 } tria_beams;
 
-/* Workspace bytes (0 on invalid input), zeroed once (tria_workspace_init). One
- * that is large enough for each serves calls of different shapes, of attention
- * too. */
+/* Workspace bytes (0 on invalid input), zeroed once (tria_workspace_init). */
 size_t tria_beam_select_workspace_size(const int32_t* seq0, int32_t n_groups, int32_t vocab, int32_t n_out);
 
 /* The n_out best continuations of every group, in one kernel. Continuation
@@ -810,8 +809,7 @@ size_t tria_beam_select_workspace_size(const int32_t* seq0, int32_t n_groups, in
  * n_out, beams), WORKSPACE. */
 tria_status tria_beam_select(const tria_beams* beams, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of tria_reorder (0 on invalid input); a workspace of the pass
- * or of attention serves too. */
+/* Workspace bytes of tria_reorder (0 on invalid input): its control words alone. */
 size_t tria_reorder_workspace_size(const tria_layer_cache* caches, int32_t n_layers, const int32_t* seq0, int32_t n_groups);
 
 /* Sequences take the rows of their parents, in place and in every layer:

@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads) k_keep_prepass(const __grid_constant
     return;
   }
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  clear_read_flags(P, seg, B, i, gridDim.x * blockDim.x);
   if (i >= B) return;
   const int v = keep[i];
   const int prev = i > 0 ? keep[i - 1] : -1;

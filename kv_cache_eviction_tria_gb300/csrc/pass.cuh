@@ -364,6 +364,8 @@ __device__ __noinline__ void pass_select(const FPass& P, int sg, int nr, uint32_
   }
   int32_t* keep = P.keep + v.wrow0;
   int* pre = P.prefix + (size_t)sg * (P.c_max + 1);
+  // the blocks' read flags, ahead of the segment's publication
+  for (int i = tid; i < (v.B + kChunk - 1) / kChunk; i += blockDim.x) P.flags[(size_t)sg * P.c_max + i] = 0u;
   const uint32_t lt = (1u << lane) - 1u;
   // one chunk: its tie and strict-keep ballots -> its kept rows (the ties by
   // rank), written at the run's position

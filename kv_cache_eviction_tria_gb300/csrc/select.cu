@@ -296,6 +296,14 @@ __global__ void __launch_bounds__(kThreads) k_select(const __grid_constant__ Pas
   const int count_blocks = (P.c_max + kCountChunksPerCta - 1) / kCountChunksPerCta;
   const int count_items = P.n_seg * count_blocks;
 
+  // counters and histograms start at zero whatever the workspace held (they lie in
+  // places that other calls write, and have no fixed one)
+  for (int seg = blockIdx.x; seg < P.n_seg; seg += gridDim.x) {
+    for (int i = threadIdx.x; i < kHistBins; i += blockDim.x) P.hist[(size_t)seg * kHistBins + i] = 0u;
+    if (threadIdx.x == 0) P.seg[seg].cnt = 0;
+  }
+  grid_barrier(P);
+
   // pass 0 (+ z-max score): every active segment
   for (int it = blockIdx.x; it < hist_items; it += gridDim.x) {
     const int seg = it / hist_blocks, blk = it - seg * hist_blocks;
@@ -305,6 +313,7 @@ __global__ void __launch_bounds__(kThreads) k_select(const __grid_constant__ Pas
       continue;
     }
     if (!sv.active || blk * kHistRowsPerCta >= sv.n) continue;
+    clear_read_flags(P, seg, sv.B, blk * kThreads + threadIdx.x, hist_blocks * kThreads);
     hist_block<0, G>(P, seg, blk, sv, sh);
   }
   grid_barrier(P);
@@ -421,6 +430,7 @@ __global__ void __launch_bounds__(kClThreads) k_select_cl(const __grid_constant_
   }
   const int lo = sv.sink, hi = n - P.window;
   const bool none = sv.k <= 0;
+  clear_read_flags(P, seg, sv.B, rank * kClThreads + threadIdx.x, kClusterCtas * kClThreads);
   // the owned totals start at zero; every rank must have cleared its own
   // before any rank adds into them (the barrier completes before the first
   // pass, its latency hidden behind the keys)

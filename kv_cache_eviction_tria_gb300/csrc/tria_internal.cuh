@@ -162,6 +162,13 @@ __device__ __forceinline__ void report(Ctrl* c, uint32_t code, uint32_t detail) 
   if (atomicCAS(&c->status, 0u, code) == 0u) atomicExch(&c->detail, detail);
 }
 
+// Clears the read flags of a segment's destination blocks ahead of its moves (in calls that
+// move), by `threads` threads of which this is number i.
+__device__ __forceinline__ void clear_read_flags(const Pass& P, int seg, int B, int i, int threads) {
+  if (!P.only_active) return;
+  for (; i < (B + kChunk - 1) / kChunk; i += threads) P.flags[(size_t)seg * P.c_max + i] = 0u;
+}
+
 // Order-preserving map float -> uint32: a > b  <=>  key(a) > key(b); -0 and +0
 // share a key; NaN gets the lowest key (evicted first, like a stable sort that
 // puts NaN last in descending order).
@@ -173,9 +180,9 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 }
 
 // Tag of the compaction read-done flags of the call with control epoch e:
-// (e + 1) times an odd constant (mod 2^32), so consecutive calls' tags differ
-// and a tag is unlike the small counts or float bit patterns that other
-// calls may have left in the same workspace bytes; never 0.
+// (e + 1) times an odd constant (mod 2^32), so consecutive calls' tags differ;
+// never 0, which the call's flags are set to before its first move (the workspace may hold
+// anything there, see clear_read_flags).
 __host__ __device__ __forceinline__ uint32_t flag_tag(uint32_t epoch) {
   const uint32_t x = (epoch + 1u) * 0x9E3779B1u;
   return x ? x : 1u;

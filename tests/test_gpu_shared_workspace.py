@@ -86,3 +86,56 @@ LOOPS = [dict(kind="f16", prefix=("f16", "f16"), own=("f16", "f16"), n_kv=8, gro
 @pytest.mark.parametrize("cfg", LOOPS)
 def test_attention_choice_and_reorder(lib, cfg):
     once_and_again(lib, cfg, 4)
+
+
+@pytest.mark.parametrize("cfg", LOOPS)
+def test_with_passes(lib, cfg):
+    """The own rows are evicted twice in between: 256 and 384 segments of fp16 or 8-bit keys take the fused pass."""
+    once_and_again(lib, cfg, 4, evict=(1, 2))
+
+
+TAG, SCRATCH = 0x9E3779B1, 256 + 4 * 4 * 2048       # the first pass's flags; the words that are zero between calls end here
+
+
+@pytest.mark.parametrize("rows,n_kv,seqs,k,v", [(300001, 1, 1, "f16", "f16"), (270000, 2, 1, "q8_0", "q4_0"), (40001, 4, 4, "q4_0", "f16"),
+                                                (9000, 8, 8, "f16", "q8_0"), (3000, 8, 16, "q8_0", "q8_0")])
+def test_a_pass_relies_on_nothing_in_its_scratch(lib, rows, n_kv, seqs, k, v):
+    """Flags that look set, counters and histograms that are not zero: cooperative, cluster and fused selections, moves of
+    many rounds, and a keep list of the caller's."""
+    rng = np.random.default_rng(rows)
+    live = [rows - 37 * s for s in range(seqs)]
+    hd, group = 64, 2
+    qm = rng.standard_normal((1, n_kv * group, hd // 2, 2)).astype(np.float32)
+    stats = lib.Stats(qm, np.hypot(qm[..., 0], qm[..., 1]), n_kv_heads=n_kv, head_dim=hd, rope_theta=1e4)
+    c = R.Cache(lib, rng, rows=live, cap=[rows] * seqs, n_kv=n_kv, hd=hd, k_type=k, v_type=v)
+    first = {name: None if t is None else t.clone() for name, t in c.d.items()}
+    size = lib.workspace_size(c.cache, group)
+    half = [n // 2 for n in live]
+    policies = [lib.Policy(budget_rows=[int(f * n) for n in live], window=16, sink=4, cur_pos=[6 * rows] * seqs) for f in (0.7, 0.3)]
+    keep = torch.zeros(c.row0[-1] + n_kv * rows + 3, device="cuda", dtype=torch.int32)
+    for s in range(seqs):
+        for g in range(n_kv):
+            at = c.row0[s] + g * rows
+            keep[at:at + half[s]] = torch.from_numpy(np.sort(rng.choice(live[s], half[s], replace=False)).astype(np.int32))
+    ends = []
+    for fill in (0, TAG, 1):
+        out = []
+        for call in ("evict", "evict_staged", "compact"):
+            for name, t in first.items():
+                if t is not None:
+                    c.d[name].copy_(t)
+            ws = c.ws(size)
+            words = ws.view(torch.int32)[SCRATCH // 4:]
+            for i, policy in enumerate(policies):                 # the second one's flags carry the second tag
+                tag = (i + 1) * fill % 2 ** 32
+                words.fill_(tag - 2 ** 32 if tag >= 2 ** 31 else tag)
+                if call != "compact":
+                    getattr(lib, call)(stats, 0, c.cache, policy, ws=ws)
+                elif i == 0:
+                    lib.compact(c.cache, lib.Policy(budget_rows=half), keep, ws=ws)
+                assert lib.device_status(ws) == lib.OK
+                out += [t.clone() for t in c.d.values() if t is not None]
+        ends.append(out)
+    for other in ends[1:]:
+        assert all(torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)) for a, b in zip(ends[0], other))
+    stats.close()
