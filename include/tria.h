@@ -798,7 +798,9 @@ size_t tria_beam_select_workspace_size(const int32_t* seq0, int32_t n_groups, in
  * Every continuation of a beam whose total is not finite, or whose logits
  * hold a NaN or +inf or are all -inf, is worth -inf. They are ordered by v,
  * compared in 64 bits (exponentials and their sums within 32-bit roundings), equal
- * ones by beam, then token. total_out: v rounded to fp32; parent_out: b (index
+ * ones by beam, then by logit (those of one beam keep their logits' order where v
+ * does not tell them apart: totals like -1e30, logits that differ by 1e-16; worth
+ * -inf, a continuation has no logit), then by token. total_out: v rounded to fp32; parent_out: b (index
  * among all beams of the call); token_out: t; ended_out: 1 when t = end_token or
  * the beam was over. They lie best first or, with in_place (every group then
  * has n_out beams), so that each parent's best one is in the parent's own place

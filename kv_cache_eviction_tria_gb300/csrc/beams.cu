@@ -5,8 +5,9 @@
 //
 // One pass over the logits: a CTA takes a part of a beam's row in pieces that
 // its registers hold, and from it the largest logit, the sum of exponentials
-// relative to it and the part's n_out best tokens (within a beam v orders like
-// the logits, so they are found before the sum is known). The last CTA of a
+// relative to it and the part's n_out best tokens (within a beam the order is the
+// logits', so they are found before the sum is known; where v in 64 bits does not tell two
+// of a beam's logits apart, they still do). The last CTA of a
 // group to arrive adds the sums up and chooses among the parts' lists; the CTAs
 // write 8 + 8 n_out bytes each, against 16 KB or more read.
 //
@@ -48,7 +49,9 @@ constexpr int kSelThreads = 256, kHeld = 32;               // logits of a thread
 constexpr int kMaxOut = TRIA_MAX_CHOICES, kMaxBeams = TRIA_MAX_BEAMS;
 constexpr int kList = 1024;                                // candidates ranked by counting
 constexpr float kLog2e = 1.4426950408889634f;
-static_assert((int64_t)kMaxBeams * TRIA_MAX_VOCAB < ((int64_t)1 << 32), "a continuation's index has 32 bits");
+// a continuation among equal values: beam, then logit, then token
+constexpr int kTokenBits = 19, kBeamAt = kTokenBits + 32;
+static_assert(TRIA_MAX_VOCAB <= 1 << kTokenBits && kMaxBeams <= 1 << (64 - kBeamAt), "a continuation's place has 64 bits");
 
 struct BeamArgs {
   const void* logits;
@@ -88,10 +91,10 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
-// Candidate: key (0: none) and index; before(a, b): a is the better one.
+// Candidate: key (0: none) and place among equal ones; before(a, b): a is the better one.
 struct Cand {
   uint64_t key;
-  uint32_t at;
+  uint64_t at;
 };
 __device__ __forceinline__ bool before(const Cand& a, const Cand& b) { return a.key > b.key || (a.key == b.key && a.at < b.at); }
 __device__ __forceinline__ Cand from_lane(const Cand& x, int o) {      // of the lane whose number differs in bit o
@@ -211,7 +214,7 @@ __device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each,
   if (tid == 0) C.n = 0;
   find_bound(C, want, mine);
   const Cand bound = C.bound;
-  each([&](uint64_t key, uint32_t at) {
+  each([&](uint64_t key, uint64_t at) {
     const Cand x = {key, at};
     if (key == 0 || before(bound, x)) return;
     const int i = atomicAdd(&C.n, 1);
@@ -222,8 +225,8 @@ __device__ __forceinline__ int choose(Choose& C, int want, Cand mine, Each each,
   if (n <= kList) return rank_list(C, n, want, worth);
   Cand last = {~0ull, 0};                                  // every candidate comes after it
   for (int k = 0; k < want; ++k) {
-    Cand top = {0, 0xFFFFFFFFu};
-    each([&](uint64_t key, uint32_t at) {
+    Cand top = {0, ~0ull};
+    each([&](uint64_t key, uint64_t at) {
       const Cand x = {key, at};
       if (key != 0 && before(last, x) && before(x, top)) top = x;
     });
@@ -364,14 +367,14 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
       for (int t = from + tid; t < end; t += kSelThreads) f(order32(to_float(row[t])), (uint32_t)t);
     };
     Cand mine = {0, 0};
-    each([&](uint64_t key, uint32_t at) {
+    each([&](uint64_t key, uint64_t at) {
       const Cand y = {key, at};
       if (before(y, mine)) mine = y;
     });
     n = choose(C, A.n_out, mine, each, logit);
   }
   uint2* best = A.best + (int64_t)blockIdx.x * A.n_out;
-  for (int i = tid; i < A.n_out; i += kSelThreads) best[i] = i < n ? make_uint2((uint32_t)C.out[i].key, C.out[i].at) : make_uint2(0, 0);
+  for (int i = tid; i < A.n_out; i += kSelThreads) best[i] = i < n ? make_uint2((uint32_t)C.out[i].key, (uint32_t)C.out[i].at) : make_uint2(0, 0);
   if (warp == 0) {
     const float t = lane < kSelThreads / 32 ? s_top[lane] : -INFINITY;
     float all = t;
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
     double v = -INFINITY;
     if (base_v == -INFINITY) e = make_uint2(l == b * A.parts && r < A.vocab, (uint32_t)r);   // its first tokens
     else v = base_v + (double)from_order32(e.x);
-    return {e.x ? order64(v) : 0ull, (uint32_t)b * (uint32_t)A.vocab + e.y};
+    return {e.x ? order64(v) : 0ull, (uint64_t)b << kBeamAt | (uint64_t)~e.x << kTokenBits | e.y};
   };
   // lists are sorted: those whose first candidate reaches the bound of the first ones, and of these the
   // candidates that do (values rounded to fp32, which keeps their order)
@@ -474,8 +477,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
         f(y.key, y.at);
       }
     };
-    Cand own = {0, 0xFFFFFFFFu};
-    each([&](uint64_t key, uint32_t place) {
+    Cand own = {0, ~0ull};
+    each([&](uint64_t key, uint64_t place) {
       const Cand y = {key, place};
       if (before(y, own)) own = y;
     });
@@ -486,8 +489,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) k_beam_select(const __grid_con
   float val = 0.f;
   if (tid < got) {
     const Cand y = C.out[tid];
-    parent = (int)(y.at / (uint32_t)A.vocab);
-    tok = (int)(y.at - (uint32_t)parent * (uint32_t)A.vocab);
+    parent = (int)(y.at >> kBeamAt);
+    tok = (int)(y.at & ((1u << kTokenBits) - 1));
     val = (float)from_order64(y.key);
     to = tid;
     done = tok == A.end_token || (A.ended && A.ended[b0 + parent] != 0);

@@ -25,11 +25,13 @@ def values(logits, total, ended=None, end_token=-1):
     return out
 
 
-def choose(v, first, n_out, in_place=False):
-    """The n_out best of a group's values v [beams][vocab]: (beam index among all, token, value) by place."""
+def choose(v, first, n_out, in_place=False, logits=None):
+    """The n_out best of a group's values v [beams][vocab]: (beam index among all, token, value) by place. logits: of equal
+    values, those of a beam keep their logits' order."""
     beams, vocab = v.shape
     flat = v.reshape(-1)
-    best = [int(i) for i in np.lexsort((np.arange(flat.size), -flat))[:n_out]]
+    x = np.where(v > -np.inf, 0.0 if logits is None else logits, -np.inf).reshape(-1)
+    best = [int(i) for i in np.lexsort((np.arange(flat.size), -x, np.arange(flat.size) // vocab, -flat))[:n_out]]
     if in_place:
         place, rest = {}, []
         for i in best:
