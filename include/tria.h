@@ -820,8 +820,9 @@ size_t tria_reorder_workspace_size(const tria_layer_cache* caches, int32_t n_lay
  * an index among the call's sequences, of the same group (tria_beam_select's
  * parent_out where every group has n_out beams); any map, one parent for several
  * sequences and rings too. caches: host array of n_layers (1 .. 128) layers
- * with the same sequences, n_kv_heads, head_dim and types, each with planes and
- * n_live of its own (as tria_evict_model; INVALID_ARG when two share one).
+ * with the same sequences, n_kv_heads, head_dim and types, each with planes (scales
+ * and positions among them) and n_live of its own; INVALID_ARG where one begins
+ * at another's address.
  * Rows at or past the new n_live keep what they held. At most
  * TRIA_MAX_BEAMS sequences a group (UNSUPPORTED). Device errors
  * (tria_device_status), of which each leaves the group unchanged in that layer:

@@ -339,6 +339,8 @@ tria_status check_reorder(const tria_layer_cache* caches, int n_layers, const in
   if (!caches || n_layers < 1) return TRIA_ERR_INVALID_ARG;
   if (n_layers > kMaxLayers) return TRIA_ERR_UNSUPPORTED;
   const tria_layer_cache& c0 = caches[0];
+  const void* planes[6 * kMaxLayers];
+  int n_planes = 0;
   tria_status r;
   for (int i = 0; i < n_layers; ++i) {
     const tria_layer_cache& c = caches[i];
@@ -348,9 +350,12 @@ tria_status check_reorder(const tria_layer_cache* caches, int n_layers, const in
       return TRIA_ERR_INVALID_ARG;
     for (int s = 0; s < c0.n_seqs; ++s)
       if (c.seq_row0[s] != c0.seq_row0[s] || c.capacity[s] != c0.capacity[s]) return TRIA_ERR_INVALID_ARG;
-    for (int j = 0; j < i; ++j)   // a layer must not be moved twice
-      if (caches[j].k == c.k || caches[j].v == c.v || caches[j].pos == c.pos || caches[j].n_live == c.n_live) return TRIA_ERR_INVALID_ARG;
+    for (const void* x : {(const void*)c.k, (const void*)c.v, (const void*)c.k_scale, (const void*)c.v_scale, (const void*)c.pos,
+                          (const void*)c.n_live})
+      if (x) planes[n_planes++] = x;
   }
+  std::sort(planes, planes + n_planes);                    // no plane may be moved twice
+  if (std::adjacent_find(planes, planes + n_planes) != planes + n_planes) return TRIA_ERR_INVALID_ARG;
   return check_groups(seq0, n_groups, c0.n_seqs);
 }
 
