@@ -146,9 +146,9 @@ typedef struct tria_layer_cache {
   tria_dtype k_type;          /* F32, F16, Q8_0 or Q4_0 */
   tria_dtype v_type;          /* F32, F16, Q8_0 or Q4_0 */
   void* k;                    /* device, 16-byte aligned, rotated keys */
-  void* k_scale;              /* device, q8_0 / q4_0 keys only (else NULL) */
+  void* k_scale;              /* device, 16-byte aligned (tria_reorder: 2), q8_0 / q4_0 keys only (else NULL) */
   void* v;                    /* device, 16-byte aligned */
-  void* v_scale;              /* device, q8_0 / q4_0 values only (else NULL) */
+  void* v_scale;              /* device, aligned as k_scale, q8_0 / q4_0 values only (else NULL) */
   int32_t* pos;               /* device [rows] absolute token positions (moved with the rows) */
   int32_t* n_live;            /* device [n_seqs] live rows per sequence (all its KV heads);
                                  read at the start, set to the budget by compaction */
@@ -822,7 +822,7 @@ size_t tria_reorder_workspace_size(const tria_layer_cache* caches, int32_t n_lay
  * sequences and rings too. caches: host array of n_layers (1 .. 128) layers
  * with the same sequences, n_kv_heads, head_dim and types, each with planes (scales
  * and positions among them) and n_live of its own; INVALID_ARG where one begins
- * at another's address.
+ * at another's address. Scales may start on any value's address here.
  * Rows at or past the new n_live keep what they held. At most
  * TRIA_MAX_BEAMS sequences a group (UNSUPPORTED). Device errors
  * (tria_device_status), of which each leaves the group unchanged in that layer:

@@ -286,7 +286,7 @@ bool fused_preferred(const tria_stats* st, const tria_layer_cache* c, int n_laye
 
 namespace tria {
 
-tria_status check_cache(const tria_layer_cache* c) {
+tria_status check_cache(const tria_layer_cache* c, size_t scale_align) {
   if (!c) return TRIA_ERR_INVALID_ARG;
   if (c->n_seqs < 1 || c->n_seqs > kMaxSeqs || c->n_kv_heads < 1) return TRIA_ERR_INVALID_ARG;
   if (c->n_seqs * c->n_kv_heads > kMaxSegments) return TRIA_ERR_UNSUPPORTED;
@@ -298,8 +298,8 @@ tria_status check_cache(const tria_layer_cache* c) {
     return TRIA_ERR_INVALID_ARG;
   if (has_scales(c->k_type) != (c->k_scale != nullptr)) return TRIA_ERR_INVALID_ARG;
   if (has_scales(c->v_type) != (c->v_scale != nullptr)) return TRIA_ERR_INVALID_ARG;
-  if (c->k_scale && !aligned(c->k_scale, 16)) return TRIA_ERR_INVALID_ARG;
-  if (c->v_scale && !aligned(c->v_scale, 16)) return TRIA_ERR_INVALID_ARG;
+  if (c->k_scale && !aligned(c->k_scale, scale_align)) return TRIA_ERR_INVALID_ARG;
+  if (c->v_scale && !aligned(c->v_scale, scale_align)) return TRIA_ERR_INVALID_ARG;
   // segments of different sequences must not overlap
   std::vector<std::pair<int64_t, int64_t>> spans;
   for (int s = 0; s < c->n_seqs; ++s) {

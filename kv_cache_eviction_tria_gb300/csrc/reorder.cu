@@ -53,6 +53,7 @@ struct ReorderArgs {
   Ctrl* ctrl;
   int32_t n_layers, n_groups, n_seqs, n_kv;
   int32_t k_rb, v_rb, ks_rb, vs_rb;   // bytes of a row of each plane (0: none)
+  int32_t words;                      // every row of the scales starts on 4 bytes, in every layer
   int32_t max_block;
   int32_t cap[kMaxSeqs];
   int64_t row0[kMaxSeqs];
@@ -114,8 +115,8 @@ __device__ __forceinline__ void copy_moves(const ReorderArgs& A, const ReorderLa
   for (int x = 0; x < 2; ++x) {
     copy_plane<M, uint4>(x ? L.v : L.k, x ? A.v_rb : A.k_rb, B, at);
     const int rb = x ? A.vs_rb : A.ks_rb;
-    if (rb % 4) copy_plane<M, uint16_t>(x ? L.vs : L.ks, rb, B, at);
-    else if (rb) copy_plane<M, uint32_t>(x ? L.vs : L.ks, rb, B, at);
+    if (rb && A.words) copy_plane<M, uint32_t>(x ? L.vs : L.ks, rb, B, at);
+    else if (rb) copy_plane<M, uint16_t>(x ? L.vs : L.ks, rb, B, at);
   }
   copy_plane<M, uint32_t>(reinterpret_cast<uint8_t*>(L.pos), 4, B, at);
 }
@@ -344,7 +345,7 @@ tria_status check_reorder(const tria_layer_cache* caches, int n_layers, const in
   tria_status r;
   for (int i = 0; i < n_layers; ++i) {
     const tria_layer_cache& c = caches[i];
-    if ((r = check_cache(&c)) != TRIA_OK) return r;
+    if ((r = check_cache(&c, 2)) != TRIA_OK) return r;     // (bits are moved: scales may start on any value)
     if (c.n_seqs != c0.n_seqs || c.n_kv_heads != c0.n_kv_heads || c.head_dim != c0.head_dim || c.k_type != c0.k_type ||
         c.v_type != c0.v_type)
       return TRIA_ERR_INVALID_ARG;
@@ -386,6 +387,9 @@ extern "C" tria_status tria_reorder(const tria_layer_cache* caches, int32_t n_la
   A.max_block = std::min(std::max(kBlockBytes / A.k_rb, kLeastMaxBlock), kMostMaxBlock) & ~7;
   A.ks_rb = c.k_scale ? c.head_dim / 16 : 0;
   A.vs_rb = c.v_scale ? c.head_dim / 16 : 0;
+  uintptr_t ends = A.ks_rb | A.vs_rb;
+  for (int i = 0; i < n_layers; ++i) ends |= (uintptr_t)caches[i].k_scale | (uintptr_t)caches[i].v_scale;
+  A.words = ends % 4 == 0;
   int64_t rows = 0;
   for (int s = 0; s < c.n_seqs; ++s) {
     A.cap[s] = c.capacity[s];

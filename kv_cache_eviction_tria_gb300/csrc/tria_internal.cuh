@@ -593,7 +593,7 @@ struct StatsDevice;
 // api.cu: the host-side argument checks every entry point on a layer cache
 // shares (layout, pointers and alignment; budget, sink, window and position
 // of every sequence). need_budget = false: scoring only, no budget checked.
-tria_status check_cache(const tria_layer_cache* c);
+tria_status check_cache(const tria_layer_cache* c, size_t scale_align = 16);
 tria_status check_policy(const tria_layer_cache* c, const tria_policy* p, bool need_pos, std::vector<int>& budget,
                          bool need_budget = true);
 

@@ -38,3 +38,16 @@ def test_a_plane_of_two_is_refused(lib, of, to, layers):  # noqa: F811
     c = [layer(i) for i in range(3)]
     setattr(c[layers[1]], to, getattr(c[layers[0]], of))
     assert reorder(lib, c) == (0, tria.ERR_INVALID_ARG)
+
+
+def test_scales_start_on_any_value(lib):  # noqa: F811
+    """Layers side by side in one array, whose rows' scales take no multiple of 16 bytes."""
+    for off in (2, 4, 8, 14):
+        c = [layer(0), layer(1)]
+        c[1].k_scale += off
+        c[0].v_scale += off
+        assert reorder(lib, c) == (256, tria.ERR_WORKSPACE)
+    for name, off in (("k_scale", 1), ("v_scale", 3), ("k", 8), ("v", 8), ("pos", 2), ("n_live", 2)):
+        c = [layer(0), layer(1)]
+        setattr(c[1], name, getattr(c[1], name) + off)
+        assert reorder(lib, c) == (0, tria.ERR_INVALID_ARG)
