@@ -732,7 +732,7 @@ tria_status tria_attend(const tria_layer_cache* cache, const tria_attention* att
  * prefix), and each only the rows behind it:
  *   tria_append_qkv     the new tokens' rows into each sequence's own cache
  *   tria_attend_prefix  the new tokens' attention over the prefix, whose rows
- *                       are read once for all its sequences, and over their own
+ *                       are read for all its sequences together, and over their own
  *   tria_beam_select    the best continuations of every group of beams
  *   tria_reorder        the own rows follow the chosen parents, in every layer
  * Passes (tria_evict) may run on either cache. Sequences of a prefix or group
@@ -751,15 +751,20 @@ size_t tria_attend_prefix_workspace_size(const tria_layer_cache* prefix, const t
  * sequence's own rows, as one softmax: a token of a sequence of group i sees
  * row r of prefix sequence i when r < n_live, pos[r] <= p and, with a window,
  * p - pos[r] < window or r < sink; and row r of its own sequence when r <
- * n_live, pos[r] <= p and, with a window, p - pos[r] < window (the sink's rows
- * are the prefix's). prefix->n_seqs groups; the same n_kv_heads and head_dim in
+ * n_live, pos[r] <= p and, with a window, p - pos[r] < window. The sink's rows
+ * are the prefix's alone: behind a prefix with fewer than `sink` live rows, or none,
+ * a window hides first own rows that tria_attend would show with all the rows in
+ * one cache. prefix->n_seqs groups; the same n_kv_heads and head_dim in
  * both caches (INVALID_ARG otherwise), the plane types may differ. Positions
  * ascend strictly with the rows of a segment of each cache. Everything else,
  * errors too, as tria_attend: the two results are joined in fp32 by their
- * log-sum-exps. On the tensor cores a prefix has the roundings of tria_attend's
- * prompts, round_keys among them, whatever the number of its tokens, but for
- * a long quantised one with up to 16 tokens x query heads per KV head (those of
- * decode steps). A token whose prefix or sequence has a bad n_live gets
+ * log-sum-exps. On the tensor cores the prefixes have the roundings of tria_attend's
+ * prompts, round_keys among them, whatever the number of their tokens. Those of decode
+ * steps (exact codes) have quantised ones in a call whose prefixes all have up to 16
+ * tokens x query heads per KV head and are long: the kernel is chosen for the call,
+ * by the prefix with the most tokens and by all capacities. Rows of a prefix are read once
+ * for 128 tokens x query heads per KV head or more, once for 8 where tria_attend
+ * computes in fp32. A token whose prefix or sequence has a bad n_live gets
  * no outputs. ws is not shared with calls that overlap on the GPU. */
 tria_status tria_attend_prefix(const tria_layer_cache* prefix, const tria_layer_cache* cache, const int32_t* seq0,
                                const tria_attention* attention, void* ws, size_t ws_bytes, void* stream);
@@ -827,7 +832,8 @@ size_t tria_reorder_workspace_size(const tria_layer_cache* caches, int32_t n_lay
  * TRIA_MAX_BEAMS sequences a group (UNSUPPORTED). Device errors
  * (tria_device_status), of which each leaves the group unchanged in that layer:
  * DEVICE_ARG (a parent outside the group, a sequence's n_live outside [0,
- * capacity]), CAPACITY (a parent's rows do not fit). */
+ * capacity] in a group of which some sequence moves), CAPACITY (a parent's rows do
+ * not fit). */
 tria_status tria_reorder(const tria_layer_cache* caches, int32_t n_layers, const int32_t* seq0, int32_t n_groups,
                          const int32_t* parent, void* ws, size_t ws_bytes, void* stream);
 

@@ -930,7 +930,7 @@ def attend_prefix(prefix: LayerCache, cache: LayerCache, q, out, pos, *, ws, seq
                   window: int = 0, sink: int = 0, round_keys: bool = False, stream=None):
     """tria_attend_prefix: attention of new tokens over the rows of their sequence's prefix, held once for the sequences
     seq0[i] .. seq0[i + 1] - 1 that continue prefix i (host offsets; None: equally many each), and over the sequence's
-    own rows in cache. The other arguments as attend; sink: first rows of the prefix."""
+    own rows in cache. The other arguments as attend; sink: first rows of the prefix alone (a shorter prefix has fewer)."""
     a, _keep = _attention(q, out, pos, lse, cache.head_dim, len(cache.seq_row0), tok0, scale, window, sink, round_keys)
     seq0 = _groups(seq0, len(cache.seq_row0), len(prefix.seq_row0))
     wp, wb = _ws(ws)

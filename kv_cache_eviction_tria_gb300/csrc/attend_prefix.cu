@@ -1,6 +1,6 @@
 // Attention of several continuations of one prompt (tria_attend_prefix): new
-// tokens over the rows of a shared prefix, read once for all sequences that
-// continue it, and over each sequence's own rows.
+// tokens over the rows of a shared prefix, read for all sequences that continue it
+// together, and over each sequence's own rows.
 //
 //   out = (o1 e^(l1 - m) + o2 e^(l2 - m)) / (e^(l1 - m) + e^(l2 - m)),
 //   lse = m + ln(e^(l1 - m) + e^(l2 - m)),   m = max(l1, l2)
@@ -80,6 +80,13 @@ void prefix_tokens(const int32_t* seq0, int n_prefixes, const int32_t* tok0, int
 //   fp16 rows 81 against 104, 512 of q8_0 160 against 213.
 //   up to kGroupCols while a CTA gets kGroupLong rows at most: 512 columns of fp16, 16384
 //   rows 64 against 77, 32768 rows 117 against 107; 1024 of q8_0, 4096 rows 70 against 78.
+// Other shapes take the same limits. Of 168 calls (8 KV heads x 64, 128 and 256 dims, 4 x 256;
+// 4 to 1024 columns of 777 to 65536 rows; fp16, q8_0 and q4_0) 152 take the faster side. The worst of
+// the others: 16 columns of 32768 q8_0 rows x 256 dims (4 heads 93 against 57, 8 heads 122 against
+// 85), 1024 columns of 16384 such rows of 8 heads (405 against 296), 512 columns of 32768 fp16
+// rows x 64 dims (104 against 84).
+// One choice for a call: with a prefix of more columns beside it, a long quantised one of few
+// takes k_attend_group's roundings too.
 constexpr int kGroupFew = 256, kGroupFewQ = 512, kGroupCols = 1024, kGroupShort = 512, kGroupLong = 4096;
 
 bool by_group(const tria_layer_cache* c, int64_t most, int64_t units, int64_t rows) {

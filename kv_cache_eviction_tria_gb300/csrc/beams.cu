@@ -28,8 +28,8 @@
 // tokens of a row whatever its alignment, so equal rows have equal sums, bit by
 // bit, and equal candidates of two beams stay equal.
 //
-// 128 beams of 151936 bf16 logits, 8 chosen of 8: 25 us, 39 MB; 128 beams of 50021 fp32
-// logits, 64 chosen of 32: 33 us; 4 beams of 32000 fp16 logits: 10 us. Neither memory
+// 128 beams of 151936 bf16 logits, 8 chosen of 8: 25 us, 39 MB (512 CTAs, five pieces each); 108
+// beams of 50021 fp32 logits, 64 chosen of up to 32: 33 us; 4 beams of 32000 fp16 logits: 10 us. Neither memory
 // (0.17 of its rate) nor instructions (0.4 of the issue slots) are the bound but the steps that
 // wait for one another: a piece's loads, its largest value, the bound, the list, the ranking,
 // then the last CTA's merge; a kernel's start and end are half of the smallest call.

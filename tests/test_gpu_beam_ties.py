@@ -6,7 +6,7 @@ import pytest
 
 import _rows as R
 from oracle import beam_oracle as B
-from test_gpu_beams import LOG_TOL, make, run
+from test_gpu_beams import LOG_TOL, check, make, run
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -40,3 +40,15 @@ def exact(got, logits, total, n_out):
     assert got["parent"][0].tolist() == [b for b, _, _ in want] and got["token"][0].tolist() == [t for _, t, _ in want]
     w = np.asarray([val for _, _, val in want])
     assert np.all(np.abs(got["total_out"][0] - w) <= R.U24 * np.abs(w) + LOG_TOL)
+
+
+@pytest.mark.parametrize("kind", ["f16", "f32"])
+@pytest.mark.parametrize("vocab", [40, 9000, 100001])
+def test_log_probabilities_near_zero(lib, kind, vocab):
+    """Rows with one token that is all but sure, and totals of zero: what is left is the sum's rounding, bounded absolutely."""
+    rng = np.random.default_rng(vocab)
+    for gap in (3.0, 10.0, 17.0, 40.0):
+        logits = make(rng, 4, vocab, kind, 0.5) - gap - np.log(vocab)
+        for b in range(4):
+            logits[b, (b * 977) % vocab] = 5.0
+        check(run(lib, logits, [0.0] * 4, [0, 2, 4], 2), logits, [0.0] * 4, [0, 2, 4], 2)
