@@ -43,9 +43,9 @@ class Search:
                           reorder=lib.reorder_workspace_size([self.c.cache], self.seq0))
 
     def run(self, steps, ws_of, evict=()):
-        """The results of every step; ws_of(size) gives a call's workspace."""
+        """The results of the steps; ws_of(size) gives a call's workspace."""
         lib, c, cfg, out = self.lib, self.c, self.cfg, []
-        for i in range(steps):
+        for i in steps:
             used = [ws_of(self.sizes[k]) for k in ("pass_", "prefix", "attend", "select", "reorder", "pass_")]
             q, o = (torch.full((self.n, self.nq, self.hd), 7.0, device="cuda", dtype=self.joint[i].dtype) for _ in range(2))
             own, lse, own_lse = torch.full_like(o, 7.0), *(torch.full((self.n, self.nq), 7.0, device="cuda") for _ in range(2))
@@ -68,9 +68,12 @@ class Search:
 def once_and_again(lib, cfg, steps, evict=()):
     x = Search(lib, cfg, steps)
     shared = x.c.ws(max(x.sizes.values()))
-    got = x.run(steps, lambda size: shared, evict)
+    got = x.run(range(steps), lambda size: shared, evict)
     y = Search(lib, cfg, steps)
-    want = y.run(steps, y.c.ws, evict)
+    same(got, y.run(range(steps), y.c.ws, evict))
+
+
+def same(got, want):
     bits = lambda t: t.contiguous().view(torch.uint8)
     bad = [i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(bits(a), bits(b))]
     assert not bad, f"results {bad} of {len(want)} differ from those with a workspace for each call"
@@ -91,7 +94,24 @@ def test_attention_choice_and_reorder(lib, cfg):
 @pytest.mark.parametrize("cfg", LOOPS)
 def test_with_passes(lib, cfg):
     """The own rows are evicted twice in between: 256 and 384 segments of fp16 or 8-bit keys take the fused pass."""
+    x = Search(lib, cfg, 1)
+    assert lib.evict_model_fused(x.stats, [0], [x.c.cache]) == (cfg["own"][0] != "q4_0")
     once_and_again(lib, cfg, 4, evict=(1, 2))
+
+
+def test_searches_of_different_shapes_in_turn(lib):
+    """Steps of all of them on one workspace, in a random order."""
+    rng = np.random.default_rng(3)
+    searches = [Search(lib, cfg, 4) for cfg in LOOPS]
+    shared = searches[0].c.ws(max(max(x.sizes.values()) for x in searches))
+    turns = rng.permutation(np.repeat(np.arange(len(LOOPS)), 4))
+    got, at = [[] for _ in LOOPS], [0] * len(LOOPS)
+    for k in turns:
+        got[k] += searches[k].run([at[k]], lambda size: shared, evict=(1, 2))
+        at[k] += 1
+    for cfg, g in zip(LOOPS, got):
+        y = Search(lib, cfg, 4)
+        same(g, [t for i in range(4) for t in y.run([i], y.c.ws, evict=(1, 2))])
 
 
 TAG, SCRATCH = 0x9E3779B1, 256 + 4 * 4 * 2048       # the first pass's flags; the words that are zero between calls end here
